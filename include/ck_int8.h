@@ -254,10 +254,128 @@ int ck_int8_gemm_dequant(const int8_t *q, const float *x_scale, const int8_t *w,
 int ck_int8_gemm_s32(const int8_t *q, const int8_t *w, int32_t *acc, int64_t M, int64_t N, int64_t K,
                      void *workspace, size_t workspace_bytes, void *stream);
 
+/* ------------------------------------------------------------------------------------
+ * Around the linear layers: what a transformer runs between its QKV projection and its
+ * output projection, and its projections with 4-bit weights for few rows.
+ *
+ * Conventions as above (caller-owned device memory, 16-byte aligned pointers -- index
+ * arrays need only their elements' alignment --, work enqueued on `stream`, a status back,
+ * no host synchronisation, CUDA graphs), with
+ *   - dtype: CK_OUT_BF16 or CK_OUT_F16, the 16-bit type of activations;
+ *   - indices that live in device memory (positions, slots, page numbers, lengths,
+ *     sequence bounds) cannot be checked before the launch: the kernels check each before
+ *     they use it, skip the access, write NaN for the outputs that depend on it and set
+ *     bit 7 (value 128) of the device error word, which ck_device_error() reads;
+ *   - all sums, softmax maxima and sums, and norms are fp32. */
+
+/* Element type of a paged cache. */
+typedef enum {
+    CK_KV_BF16 = 0,
+    CK_KV_F16 = 1,
+    CK_KV_INT8 = 2 /* codes and one fp32 scale per row: value = code * scale */
+} ck_kv_dtype_t;
+
+/* A cache of keys and values in pages.  Row (page, head, offset) holds one token's
+ * head_dim values of one head; token t of a sequence whose block table row is T lives at
+ * page T[t / page_size], offset t % page_size.  Slot numbers are page * page_size + offset. */
+typedef struct {
+    void *k, *v;             /* [num_pages, kv_heads, page_size, head_dim] of dtype        */
+    float *k_scale, *v_scale;/* fp32 [num_pages, kv_heads, page_size]; CK_KV_INT8 only      */
+    int64_t num_pages;
+    int64_t page_size;       /* any size >= 1                                             */
+    int64_t kv_heads;
+    int64_t head_dim;
+    int dtype;               /* a ck_kv_dtype_t                                           */
+} ck_kv_cache_t;
+
+/* Norms of queries and keys for each head, with the position rotation, in one pass over a
+ * QKV projection's output, and the way of keys and values into the cache.
+ *   qkv:      [tokens, q_heads + 2 kv_heads, head_dim] of dtype: queries, keys, values;
+ *             `qkv_stride` elements (a multiple of 8) between tokens.
+ *   norm:     1: y = x * rsqrt(mean(x^2) + eps) * weight over each query and key head, in
+ *             fp32; q_weight, k_weight [head_dim] of dtype, NULL meaning ones.  0: y = x.
+ *   rotation: the first rot_dim values of each query and key head (0: none; a multiple of
+ *             16), pairs (a, b) = (i, i + rot_dim/2), or (2i, 2i+1) if interleaved:
+ *             a' = a cos - b sin, b' = b cos + a sin, with row positions[token] (int32) of
+ *             cos_sin, fp32 [max_pos, rot_dim]: rot_dim/2 cosines, then as many sines.
+ *   q_out:    [tokens, q_heads, head_dim] of dtype, written.
+ *   k_out:    [tokens, kv_heads, head_dim] of dtype, or NULL: the rotated keys.
+ *   cache:    or NULL.  Keys (normed, rotated) and values of token t go to slots[t]
+ *             (int64); a negative slot keeps the token out of the cache.  A 16-bit cache has
+ *             the type of dtype.  CK_KV_INT8 rows: scale = max|y| / 127, code =
+ *             clamp(rint(y / scale), -127, 127) from the fp32 y (ck_quantize_int8_rowwise's
+ *             rule).  Two tokens with one slot leave either's row there.
+ * head_dim: a multiple of 8 up to 256.  One launch. */
+int ck_qk_norm_rope(const void *qkv, int64_t qkv_stride, int64_t tokens, int64_t q_heads, int64_t kv_heads,
+                    int64_t head_dim, int dtype, int norm, const void *q_weight, const void *k_weight, float eps,
+                    int64_t rot_dim, int interleaved, const int32_t *positions, const float *cos_sin,
+                    int64_t max_pos, void *q_out, void *k_out, const ck_kv_cache_t *cache, const int64_t *slots,
+                    void *stream);
+
+/* Attention of one new token per sequence over the paged cache.
+ *   out[b,h] = sum_j softmax_j(scale * q[b,h] . k_j) v_j, j over the keys that token
+ *   seq_lens[b] - 1 sees: all of them (window 0), or the last `window` and the first `sinks`.
+ *   q:           [batch, q_heads, head_dim] of dtype, `q_stride` elements between
+ *                sequences (a multiple of 8).  q_heads is a multiple of the cache's kv_heads:
+ *                query heads h * g .. h * g + g - 1 read head h (g = q_heads / kv_heads).
+ *   block_table: int32 [batch, max_blocks]; seq_lens: int32 [batch], the cached tokens,
+ *                0 .. max_blocks * page_size.  An empty sequence gives zeros (lse -inf).
+ *   out:         [batch, q_heads, head_dim] of dtype, written.
+ *   lse:         fp32 [batch, q_heads] or NULL: the natural log of the softmax's sum,
+ *                max included.
+ * head_dim: 64 or 128.  The cache's type is dtype or CK_KV_INT8.  The result does not depend
+ * on what else is in the batch's pages: rows that no sequence sees are never read.
+ * workspace: ck_paged_attention_workspace_size() bytes; its content does not matter. */
+size_t ck_paged_attention_workspace_size(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t head_dim);
+int ck_paged_attention(const void *q, int64_t q_stride, const ck_kv_cache_t *cache, const int32_t *block_table,
+                       int64_t max_blocks, const int32_t *seq_lens, int64_t batch, int64_t q_heads, int dtype,
+                       float scale, int64_t window, int64_t sinks, void *out, float *lse, void *workspace,
+                       size_t workspace_bytes, void *stream);
+
+/* Attention over whole prompts, a ragged batch of them in one call.
+ *   q:       [total_q, q_heads, head_dim] of dtype, q_stride elements between tokens; k, v:
+ *            [total_k, kv_heads, head_dim], k_stride / v_stride elements (multiples of 8;
+ *            views of a fused projection's output qualify).
+ *   cu_q, cu_k: int32 [batch + 1], ascending: sequence b owns rows cu[b] .. cu[b+1] - 1.  A
+ *            token before cu_q[0] or from cu_q[batch] on gets no output.
+ *   causal:  1: query i of a sequence with n queries and m keys sees keys j <= i + m - n (its
+ *            last query sees all), and with window > 0 of those only i + m - n - j < window or
+ *            j < sinks.  0: every key; window must be 0.
+ *   out:     [total_q, q_heads, head_dim] of dtype, written; a query that sees no key gets
+ *            zeros.  lse: fp32 [q_heads, total_q] or NULL (-inf where no key is seen).
+ * head_dim: 64 or 128.  q_heads is a multiple of kv_heads, as in ck_paged_attention.  A key or
+ * value that a query does not see has no part in its row, whatever it holds. */
+int ck_attention(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                 const int32_t *cu_q, const int32_t *cu_k, int64_t batch, int64_t total_q, int64_t total_k,
+                 int64_t q_heads, int64_t kv_heads, int64_t head_dim, int dtype, float scale, int causal,
+                 int64_t window, int64_t sinks, void *out, float *lse, void *stream);
+
+/* A linear layer with 4-bit weights and group scales, for the few rows of a decode step:
+ *   y[m,n] = out( sum_k x[m,k] * (w_scale[n, k / group] * (code[n,k] - 8)) + bias[n]
+ *                 + residual[m,n] ), summed in fp32.
+ *   x:        [M,K] of dtype.  w4: uint32 [N, K/8], eight codes 0..15 to a word: the code of
+ *             k = 8 j + 2 i in bits 4 i .. of word j, that of k = 8 j + 2 i + 1 in bits
+ *             16 + 4 i .. (i = 0..3).  w_scale: bf16 [N, K/group]; group 32, 64, 128 or 256.
+ *   bias:     [N] of dtype or NULL.  residual: [M,N] of out_dtype or NULL (may be y).
+ *   y:        [M,N] of out_dtype (a ck_dtype_t), written.
+ * K a multiple of 128 and of group, N of 8.  Any M; it pays while the weight's bytes, not the
+ * arithmetic, set the time (some tens of rows).
+ *   ck_int4_prepare_weight: fp32 W [N,K] -> w4, w_scale: per group scale = bf16(max|W| / 7),
+ *             code - 8 = clamp(rint(W / scale), -7, 7).
+ *   ck_int4_pack: weights quantized elsewhere, int8 codes [N,K] in [-8, 7] (clamped) -> w4.
+ *   workspace: ck_int4_linear_workspace_size(M, N, K) bytes; its content does not matter. */
+int ck_int4_prepare_weight(const float *W, int64_t N, int64_t K, int64_t group, uint32_t *w4, void *w_scale,
+                           void *stream);
+int ck_int4_pack(const int8_t *codes, int64_t N, int64_t K, uint32_t *w4, void *stream);
+size_t ck_int4_linear_workspace_size(int64_t M, int64_t N, int64_t K);
+int ck_int4_linear(const void *x, const uint32_t *w4, const void *w_scale, const void *bias, const void *residual,
+                   void *y, int64_t M, int64_t N, int64_t K, int64_t group, int dtype, int out_dtype,
+                   void *workspace, size_t workspace_bytes, void *stream);
+
 /* Launch profiling, for benchmarks.  Between ck_profile_begin() and ck_profile_end()
  * the library counts the kernels it enqueues from the calling host thread, by kind
  * (0 = activation quantize, 1 = int8 -> bf16 operand widening, 2 = GEMM with fused
- * epilogue).  With with_events != 0 it also brackets each launch with two CUDA events on
+ * epilogue, 3 = norm and rotation, 4 = attention, 5 = 4-bit linear).  With with_events != 0 it also brackets each launch with two CUDA events on
  * the kernel's own stream (the kernels are unchanged, but the events separate
  * consecutive kernels, so launch overlap between them is lost while timing).
  * ck_profile_end() waits for the events and fills, for each kind k < nkinds,

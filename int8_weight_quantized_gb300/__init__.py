@@ -1,4 +1,4 @@
-"""INT8 quantized linear layer for one NVIDIA GB300 (sm_103a).
+"""INT8 quantized linear layer for one NVIDIA GB300 (sm_103a), and the operators around it.
 
 Thin Python binding of the C ABI in ``include/ck_int8.h`` (library ``lib/libck_int8.so``,
 built by ``build.py``).  The functions have the C names and only marshal arguments:
@@ -68,6 +68,16 @@ def load_library(path=None):
         "ck_device_error": ([I], I),
         "ck_gemm_tile_config": ([I64, I64, I64, P, P, P, P], I),
         "ck_selftest_wait_timeout": ([ctypes.c_uint64, P], I),
+        "ck_qk_norm_rope": ([P, I64, I64, I64, I64, I64, I, I, P, P, ctypes.c_float, I64, I, P, P, I64, P, P, P, P, P],
+                            I),
+        "ck_paged_attention_workspace_size": ([I64, I64, I64, I64], SZ),
+        "ck_paged_attention": ([P, I64, P, P, I64, P, I64, I64, I, ctypes.c_float, I64, I64, P, P, P, SZ, P], I),
+        "ck_attention": ([P, I64, P, I64, P, I64, P, P, I64, I64, I64, I64, I64, I64, I, ctypes.c_float, I, I64, I64, P,
+                          P, P], I),
+        "ck_int4_prepare_weight": ([P, I64, I64, I64, P, P, P], I),
+        "ck_int4_pack": ([P, I64, I64, P, P], I),
+        "ck_int4_linear_workspace_size": ([I64, I64, I64], SZ),
+        "ck_int4_linear": ([P, P, P, P, P, P, I64, I64, I64, I64, I, I, P, SZ, P], I),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -377,7 +387,7 @@ def ck_selftest_wait_timeout(timeout_ns=1_000_000, stream=None):
     return load_library().ck_selftest_wait_timeout(int(timeout_ns), _stream(stream))
 
 
-PROFILE_KINDS = ("quantize", "widen", "gemm")
+PROFILE_KINDS = ("quantize", "widen", "gemm", "norm_rope", "attention", "int4")
 
 
 def ck_profile_begin(with_events=True):
@@ -391,3 +401,7 @@ def ck_profile_end():
     cnt = (ctypes.c_int64 * n)()
     _check(load_library().ck_profile_end(ms, cnt, n))
     return {k: (ms[i], cnt[i]) for i, k in enumerate(PROFILE_KINDS)}
+
+
+from .transformer import (KVCache, ck_attention, ck_int4_linear, ck_int4_pack,  # noqa: E402
+                          ck_int4_prepare_weight, ck_paged_attention, ck_qk_norm_rope, rope_table)

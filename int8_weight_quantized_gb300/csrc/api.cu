@@ -15,6 +15,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "api_common.h"
 #include "ck_int8.h"
 #include "ck_internal.h"
 
@@ -22,6 +23,8 @@ namespace ck {
 namespace {
 
 thread_local std::string g_last_error;
+
+}  // namespace
 
 int fail(int status, const char* fmt, ...)
 {
@@ -39,16 +42,19 @@ int cuda_fail(cudaError_t e, const char* where)
     return fail(CK_ERR_CUDA, "%s: %s (%s)", where, cudaGetErrorString(e), cudaGetErrorName(e));
 }
 
-bool aligned16(const void* p)
+int check_device(DeviceInfo* dev)
 {
-    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
+    cudaError_t e = current_device(dev);
+    if (e != cudaSuccess)
+        return cuda_fail(e, "querying the current device");
+    if (dev->major != 10 || dev->minor != 3)
+        return fail(CK_ERR_UNSUPPORTED_DEVICE,
+                    "this library is built for GB300 (compute capability 10.3); device %d is %d.%d", dev->device,
+                    dev->major, dev->minor);
+    return CK_OK;
 }
 
-constexpr size_t kAlign = 256;
-size_t align_up(size_t v)
-{
-    return (v + kAlign - 1) & ~(kAlign - 1);
-}
+namespace {
 
 constexpr int64_t kMaxDim = 0x7FFFFFFF;  // tensor-copy coordinates are 32-bit
 constexpr int64_t kMaxK = 131072;        // 127*127*K must fit int32
@@ -71,26 +77,6 @@ int check_gemm_shape(int64_t M, int64_t N, int64_t K)
         return fail(CK_ERR_INVALID_ARG, "N must be a multiple of 8 (got %lld)", (long long)N);
     return CK_OK;
 }
-
-int check_device(DeviceInfo* dev)
-{
-    cudaError_t e = current_device(dev);
-    if (e != cudaSuccess)
-        return cuda_fail(e, "querying the current device");
-    if (dev->major != 10 || dev->minor != 3)
-        return fail(CK_ERR_UNSUPPORTED_DEVICE,
-                    "this library is built for GB300 (compute capability 10.3); device %d is %d.%d", dev->device,
-                    dev->major, dev->minor);
-    return CK_OK;
-}
-
-#define CK_REQUIRE_PTR(p)                                                                       \
-    do {                                                                                        \
-        if ((p) == nullptr)                                                                     \
-            return fail(CK_ERR_INVALID_ARG, "%s must not be NULL", #p);                         \
-        if (!aligned16(p))                                                                      \
-            return fail(CK_ERR_INVALID_ARG, "%s must be 16-byte aligned", #p);                  \
-    } while (0)
 
 constexpr int kMaxPartialsForLayout = 1024;  // most blocks that exchange tensorwise maxima
 
@@ -136,10 +122,8 @@ size_t gemm_ws_bytes(int64_t M, int64_t N, int64_t K)
 const int kMaxPartials = kMaxPartialsForLayout;
 
 // ---- launch profiling: events around each kernel launch while enabled -------------
-enum ProfKind { kProfQuantize = 0, kProfWiden = 1, kProfGemm = 2, kProfKinds = 3 };
 struct ProfRec {
     int kind;
-    int launches;
     cudaEvent_t a, b;
 };
 thread_local bool g_prof_on = false;
@@ -161,32 +145,25 @@ cudaEvent_t prof_event()
     return e;
 }
 
-// Brackets the launches made in its lifetime with two events on `s` when profiling is on.
-struct ProfScope {
-    bool active = false;
-    ProfRec r{};
-    cudaStream_t s;
-    ProfScope(int kind, int launches, cudaStream_t st) : s(st)
-    {
-        if (!g_prof_on)
-            return;
-        g_prof_counts[kind] += launches;
-        if (!g_prof_events)
-            return;
-        r.kind = kind;
-        r.launches = launches;
-        r.a = prof_event();
-        r.b = prof_event();
-        active = r.a && r.b && cudaEventRecord(r.a, s) == cudaSuccess;
-    }
-    ~ProfScope()
-    {
-        if (active && cudaEventRecord(r.b, s) == cudaSuccess)
-            g_prof_recs.push_back(r);
-    }
-};
-
 }  // namespace
+
+ProfScope::ProfScope(int kind_, int launches, cudaStream_t st) : kind(kind_), s(st)
+{
+    if (!g_prof_on)
+        return;
+    g_prof_counts[kind] += launches;
+    if (!g_prof_events)
+        return;
+    a = prof_event();
+    b = prof_event();
+    active = a && b && cudaEventRecord(a, s) == cudaSuccess;
+}
+
+ProfScope::~ProfScope()
+{
+    if (active && cudaEventRecord(b, s) == cudaSuccess)
+        g_prof_recs.push_back(ProfRec{kind, a, b});
+}
 
 cudaError_t current_device(DeviceInfo* info)
 {

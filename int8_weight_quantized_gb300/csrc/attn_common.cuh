@@ -1,0 +1,144 @@
+// attn_common.cuh -- device pieces shared by the kernels around the linear layers: the two
+// 16-bit element types, the keys a query sees, and attention of one query row by one warp.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "ck_device.cuh"
+
+namespace ck {
+
+// Further bits of the device error word (see ck_device_error in the C ABI).
+enum : uint32_t {
+    kErrIndex = 1u << 7,       // a position, length, slot, page or sequence bound was out of range
+    kErrWaitAttention = 1u << 8,  // a role of the prompt attention kernel gave up waiting
+};
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// 16-bit element types: conversions to and from fp32 (round to nearest even)
+struct Bf16 {
+    using T = __nv_bfloat16;
+    using T2 = __nv_bfloat162;
+    static __device__ __forceinline__ float2 to2(uint32_t w)
+    {
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    }
+    static __device__ __forceinline__ uint32_t pack2(float lo, float hi)
+    {
+        const T2 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+    static __device__ __forceinline__ float to(T v) { return __bfloat162float(v); }
+    static __device__ __forceinline__ T from(float v) { return __float2bfloat16_rn(v); }
+};
+struct Fp16 {
+    using T = __half;
+    using T2 = __half2;
+    static __device__ __forceinline__ float2 to2(uint32_t w)
+    {
+        return __half22float2(*reinterpret_cast<const __half2*>(&w));
+    }
+    static __device__ __forceinline__ uint32_t pack2(float lo, float hi)
+    {
+        const T2 v = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+    static __device__ __forceinline__ float to(T v) { return __half2float(v); }
+    static __device__ __forceinline__ T from(float v) { return __float2half_rn(v); }
+};
+
+// The keys that one query sees, as two runs: [0, head) and [tail, end).  Numbered through,
+// key number v of `count()` is v (v < head) or v - head + tail.
+struct VisibleKeys {
+    int head, tail, end;
+    __host__ __device__ int count() const { return head + (end - tail); }
+    __host__ __device__ int key(int v) const { return v < head ? v : v - head + tail; }
+};
+
+// end = keys up to and including the query's own position (0: none visible); window <= 0: all
+__host__ __device__ inline VisibleKeys visible_keys(int end, int64_t window, int64_t sinks)
+{
+    VisibleKeys r;
+    r.end = end < 0 ? 0 : end;
+    const int64_t tail = window > 0 && window < r.end ? r.end - window : 0;
+    r.tail = (int)tail;
+    r.head = (int)(sinks < tail ? sinks : tail);
+    return r;
+}
+
+// One query row by one warp: online softmax over `n` keys, 32 at a time.  `qs` holds the
+// query in fp32 (DIM values of shared memory), times the softmax scale and log2 e.  row(v)
+// gives key number v's rows; only visible keys are ever read, so nothing that a mask hides
+// can reach the result.  Lane l leaves with acc[i] = sum_j 2^(s_j - m) v_j[l + 32 i], the
+// maximum m of the scores s (in units of log2) and the sum l of the weights.
+struct KvRow {
+    const void* k;
+    const void* v;
+    float ks, vs;  // int8 codes: the rows' scales
+};
+
+template <class E, bool INT8>
+__device__ __forceinline__ float kv_element(const void* row, int d)
+{
+    if (INT8)
+        return (float)static_cast<const int8_t*>(row)[d];
+    return E::to(static_cast<const typename E::T*>(row)[d]);
+}
+
+template <class E, bool INT8, int DIM, class RowFn>
+__device__ __forceinline__ void attend_row(const float* qs, int n, RowFn row, float (&acc)[(DIM + 31) / 32], float& m,
+                                           float& l)
+{
+    constexpr int PER = (DIM + 31) / 32;
+    const int lane = threadIdx.x & 31;
+    m = -INFINITY;
+    l = 0.0f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        acc[i] = 0.0f;
+    for (int v0 = 0; v0 < n; v0 += 32) {
+        const bool mine = v0 + lane < n;
+        KvRow r{};
+        float s = -INFINITY;
+        if (mine) {
+            r = row(v0 + lane);
+            float dot = 0.0f;
+            for (int d = 0; d < DIM; ++d)
+                dot = fmaf(qs[d], kv_element<E, INT8>(r.k, d), dot);
+            s = INT8 ? dot * r.ks : dot;
+        }
+        float top = s;
+#pragma unroll
+        for (int o = 16; o; o >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float m2 = fmaxf(m, top);
+        const float ref = m2 == -INFINITY ? 0.0f : m2;  // every score so far is -inf: weights 0
+        const float keep = exp2f(m - ref);
+        const float p = mine ? exp2f(s - ref) : 0.0f;
+        l = l * keep + p;
+        m = m2;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            acc[i] *= keep;
+        const int cnt = min(32, n - v0);
+        for (int j = 0; j < cnt; ++j) {
+            const float pj = __shfl_sync(0xffffffffu, p, j);
+            const void* vr = reinterpret_cast<const void*>(
+                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(r.v), j));
+            const float w = INT8 ? pj * __shfl_sync(0xffffffffu, r.vs, j) : pj;
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (lane + 32 * i < DIM)
+                    acc[i] = fmaf(w, kv_element<E, INT8>(vr, lane + 32 * i), acc[i]);
+        }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        l += __shfl_xor_sync(0xffffffffu, l, o);
+}
+
+}  // namespace ck

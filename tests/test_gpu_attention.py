@@ -1,0 +1,203 @@
+"""Attention over whole prompts against the 64-bit definition (the bound's terms are derived in
+transformer_ref.attend; one rounding of the output on top)."""
+import pytest
+import torch
+
+import int8_weight_quantized_gb300 as ck
+import transformer_ref as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def make(q_lens, k_lens, hq, hkv, d, dtype, seed, q_std=1.5):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    tq, tk = sum(q_lens), sum(k_lens)
+    q = (torch.randn((tq, hq, d), generator=g, device=DEV) * q_std).to(dtype)
+    k, v = [torch.randn((tk, hkv, d), generator=g, device=DEV).to(dtype) for _ in range(2)]
+    cu = [torch.tensor([0] + list(x), device=DEV).cumsum(0).to(torch.int32) for x in (q_lens, k_lens)]
+    return q, k, v, cu[0], cu[1]
+
+
+def seen_by(n, m, causal, window, sinks):
+    i = torch.arange(n, device=DEV)[:, None] + (m - n)
+    j = torch.arange(m, device=DEV)[None]
+    if not causal:
+        return torch.ones((n, m), dtype=torch.bool, device=DEV)
+    seen = j <= i
+    if window:
+        seen &= (i - j < window) | (j < sinks)
+    return seen
+
+
+def check(q, k, v, cu_q, cu_k, out, lse, causal=True, window=0, sinks=0, scale=None, heads=None):
+    hq, hkv, d = q.shape[1], k.shape[1], q.shape[2]
+    scale = d ** -0.5 if scale is None else scale
+    cq, ck_ = cu_q.tolist(), cu_k.tolist()
+    for b in range(len(cq) - 1):
+        qs, ks = slice(cq[b], cq[b + 1]), slice(ck_[b], ck_[b + 1])
+        n, m = cq[b + 1] - cq[b], ck_[b + 1] - ck_[b]
+        if n == 0:
+            continue
+        seen = seen_by(n, m, causal, window, sinks)
+        for h in heads or range(hq):
+            want, want_lse, tol, lse_tol = ref.attend(q[qs, h], k[ks, h // (hq // hkv)], v[ks, h // (hq // hkv)], scale,
+                                                      seen, ref.unit(q.dtype), ref.least(q.dtype))
+            tol = tol + (want.abs() + tol) * ref.unit(q.dtype) + ref.least(q.dtype)
+            ref.assert_within(out[qs, h], want, tol, "sequence %d head %d" % (b, h))
+            if lse is not None:
+                none = ~seen.any(-1)
+                assert (lse[h, qs][none] == -float("inf")).all()
+                ref.assert_within(lse[h, qs][~none], want_lse[~none], lse_tol[~none], "lse %d %d" % (b, h))
+
+
+MIXED = [1, 2, 127, 128, 129, 255, 256, 257, 0, 300]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_ragged_batches(d, dtype, causal):
+    q, k, v, cq, cku = make(MIXED, MIXED, 4, 2, d, dtype, seed=d)
+    out, lse = ck.ck_attention(q, k, v, cq, causal=causal, return_lse=True)
+    check(q, k, v, cq, cku, out, lse, causal)
+    assert ck.ck_device_error() == 0
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("hq,hkv,d", [(6, 2, 64), (8, 1, 128), (3, 3, 128), (16, 1, 64)])
+def test_more_keys_than_queries_and_fewer(hq, hkv, d, causal):
+    """Chunks of a prompt against all keys so far; queries before the first key see nothing."""
+    q_lens, k_lens = [1, 5, 130, 64, 200, 33, 7], [500, 5, 700, 0, 90, 300, 1]
+    q, k, v, cq, cku = make(q_lens, k_lens, hq, hkv, d, torch.bfloat16, seed=hq)
+    out, lse = ck.ck_attention(q, k, v, cq, cku, causal=causal, return_lse=True)
+    check(q, k, v, cq, cku, out, lse, causal)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 4), (16, 4), (100, 0), (128, 1), (129, 130), (300, 5), (2000, 4)])
+def test_window_and_first_tokens(window, sinks, d):
+    lens = [1, 700, 129, 385]
+    q, k, v, cq, cku = make(lens, lens, 2, 1, d, torch.bfloat16, seed=window + sinks)
+    out, lse = ck.ck_attention(q, k, v, cq, window=window, sinks=sinks, return_lse=True)
+    check(q, k, v, cq, cku, out, lse, True, window, sinks)
+
+
+def test_window_with_more_keys_than_queries():
+    q, k, v, cq, cku = make([150, 40], [900, 41], 4, 2, 128, torch.float16, seed=3)
+    out, lse = ck.ck_attention(q, k, v, cq, cku, window=70, sinks=4, return_lse=True)
+    check(q, k, v, cq, cku, out, lse, True, 70, 4)
+
+
+def test_long_prompt():
+    q, k, v, cq, cku = make([3001], [3001], 4, 2, 128, torch.bfloat16, seed=4)
+    out, lse = ck.ck_attention(q, k, v, cq, return_lse=True)
+    check(q, k, v, cq, cku, out, lse)
+    again = ck.ck_attention(q, k, v, cq)
+    assert torch.equal(out, again)
+
+
+def test_views_of_a_fused_projection():
+    hq, hkv, d, t = 6, 2, 128, 333
+    g = torch.Generator(device=DEV)
+    g.manual_seed(5)
+    qkv = torch.randn((t, (hq + 2 * hkv) * d), generator=g, device=DEV).to(torch.bfloat16)
+    x = qkv.view(t, hq + 2 * hkv, d)
+    q, k, v = x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:]
+    cu = torch.tensor([0, 100, 333], dtype=torch.int32, device=DEV)
+    out = ck.ck_attention(q, k, v, cu)
+    assert torch.equal(out, ck.ck_attention(q.contiguous(), k.contiguous(), v.contiguous(), cu))
+    check(q, k, v, cu, cu, out, None)
+
+
+def test_sharp_scores_and_rising_maxima():
+    """Scores that grow along the keys: the running maximum rises at every tile."""
+    n, d = 1000, 64
+    q, k, v, cq, cku = make([n], [n], 2, 1, d, torch.bfloat16, seed=6, q_std=1.0)
+    k = (k.float() * 0.1 + torch.linspace(0, 6, n, device=DEV)[:, None, None]).to(torch.bfloat16)
+    q = q.abs()
+    out, lse = ck.ck_attention(q, k, v, cq, causal=False, return_lse=True, scale=0.5)
+    check(q, k, v, cq, cku, out, lse, causal=False, scale=0.5)
+    k2 = k.flip(0).contiguous()
+    out, lse = ck.ck_attention(q, k2, v, cq, causal=False, return_lse=True, scale=0.5)
+    check(q, k2, v, cq, cku, out, lse, causal=False, scale=0.5)
+
+
+def test_negative_and_zero_scale():
+    q, k, v, cq, cku = make([200], [200], 2, 1, 64, torch.float16, seed=11)
+    for scale in (-0.125, 0.0):
+        out, lse = ck.ck_attention(q, k, v, cq, scale=scale, return_lse=True)
+        check(q, k, v, cq, cku, out, lse, scale=scale)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("fill", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("lens,row,window,sinks", [
+    ([300], 299, 0, 0), ([300], 130, 0, 0), ([300], 10, 50, 4), ([40, 300, 5], 339, 0, 0), ([700], 2, 64, 1),
+])
+def test_what_a_query_does_not_see_has_no_part(lens, row, window, sinks, fill, d):
+    """A key and value row of NaN or infinities changes the rows that see it, and no other."""
+    q, k, v, cq, cku = make(lens, lens, 2, 1, d, torch.bfloat16, seed=row)
+    clean, clean_lse = ck.ck_attention(q, k, v, cq, window=window, sinks=sinks, return_lse=True)
+    k, v = k.clone(), v.clone()
+    k[row], v[row] = fill, fill
+    out, lse = ck.ck_attention(q, k, v, cq, window=window, sinks=sinks, return_lse=True)
+    sees = torch.zeros(sum(lens), dtype=torch.bool, device=DEV)
+    lo = 0
+    for n in lens:
+        if lo <= row < lo + n:
+            sees[lo:lo + n] = seen_by(n, n, True, window, sinks)[:, row - lo]
+        lo += n
+    hidden = ~sees
+    assert not out[hidden].isnan().any()
+    # rows that do not see it agree with the clean run to the rounding of their weights
+    ref.assert_within(out[hidden], clean[hidden], 4 * ref.unit(torch.bfloat16) * (clean[hidden].abs().double() + 1), "rows")
+    ref.assert_within(lse[:, hidden], clean_lse[:, hidden], torch.full_like(lse[:, hidden], 1e-4), "lse")
+
+
+def test_value_rows_of_nan_alone():
+    """NaN in the value rows only: their scores are ordinary, their weights are not zero."""
+    q, k, v, cq, cku = make([257], [257], 2, 1, 128, torch.float16, seed=9)
+    v = v.clone()
+    v[200, 0, 5] = float("nan")
+    v[140, 0, 7] = float("inf")
+    out = ck.ck_attention(q, k, v, cq)
+    clean = v.clone()
+    clean[200, 0, 5] = clean[140, 0, 7] = 0
+    assert out[200:, :, 5].isnan().all() and not out[:200, :, 5].isnan().any()
+    assert (out[140:, :, 7] == float("inf")).all() and out[:140, :, 7].isfinite().all()
+    keep = [c for c in range(128) if c not in (5, 7)]
+    check(q[:, :, :], k, clean, cq, cku, torch.where(torch.isfinite(out), out, ck.ck_attention(q, k, clean, cq)), None)
+    assert out[:, :, keep].isfinite().all()
+
+
+def test_bounds_out_of_range_are_reported():
+    """Sequence bounds beyond the tensors: checked in the kernel, NaN for their rows, reported."""
+    assert ck.ck_device_error() == 0
+    q, k, v, cq, cku = make([64, 64], [64, 64], 2, 1, 64, torch.bfloat16, seed=12)
+    bad = cku.clone()
+    bad[2] = 129
+    out = ck.ck_attention(q, k, v, cq, bad)
+    assert out[64:].isnan().all()
+    assert torch.equal(out[:64], ck.ck_attention(q, k, v, cq)[:64])
+    assert ck.ck_device_error(clear=True) == 128
+
+
+def test_other_streams_and_graphs():
+    q, k, v, cq, cku = make([500, 77], [500, 77], 4, 2, 128, torch.bfloat16, seed=13)
+    want = ck.ck_attention(q, k, v, cq)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    outs = [ck.ck_attention(q, k, v, cq, stream=s) for s in streams]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+    out = torch.empty_like(want)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        ck.ck_attention(q, k, v, cq, out=out)
+    q.mul_(0.5)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, ck.ck_attention(q, k, v, cq))

@@ -1,0 +1,194 @@
+"""Attention of one new token over the paged cache, against the 64-bit definition (the bound's
+terms are derived in transformer_ref.attend; one rounding of the output on top)."""
+import pytest
+import torch
+
+import int8_weight_quantized_gb300 as ck
+import transformer_ref as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def make(lens, hq, hkv, d, page, dtype, int8, seed, poison=True, q_std=1.5):
+    """A shuffled pool; every row that no sequence owns is NaN (16-bit) or has a NaN scale."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    need = [-(-n // page) for n in lens]
+    pages = sum(need) + 3
+    pool = torch.randperm(pages, generator=g, device=DEV)
+    width = max(1, max(need)) + 1
+    table = torch.zeros((len(lens), width), dtype=torch.int32, device=DEV)
+    shape = (pages, hkv, page, d)
+    if int8:
+        cache = ck.KVCache.empty(pages, page, hkv, d, dtype=torch.int8)
+        for t, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
+            t.copy_(torch.randint(-127, 128, shape, generator=g, device=DEV, dtype=torch.int8))
+            s.copy_(torch.rand(shape[:3], generator=g, device=DEV) * 0.02 + 0.004)
+    else:
+        cache = ck.KVCache(*[torch.randn(shape, generator=g, device=DEV).to(dtype) for _ in range(2)])
+    owned = torch.zeros((pages, page), dtype=torch.bool, device=DEV)
+    at = 0
+    for b, n in enumerate(lens):
+        mine = pool[at:at + need[b]]
+        at += need[b]
+        table[b, :need[b]] = mine.to(torch.int32)
+        rows = torch.arange(n, device=DEV)
+        if n:
+            owned[mine[rows // page], rows % page] = True
+    if poison:
+        for t in ((cache.k_scale, cache.v_scale) if int8 else (cache.k, cache.v)):
+            hidden = ~owned[:, None, :].expand(pages, hkv, page)
+            t[hidden] = float("nan")
+    q = (torch.randn((len(lens), hq, d), generator=g, device=DEV) * q_std).to(dtype)
+    return q, cache, table, torch.tensor(lens, dtype=torch.int32, device=DEV)
+
+
+def rows_of(cache, table, b, n, page, h):
+    j = torch.arange(n, device=DEV)
+    at, off = table[b].long()[j // page], j % page
+    out = []
+    for t, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
+        x = t[at, h, off].double()
+        out.append(x if s is None else x * s[at, h, off].double()[:, None])
+    return out
+
+
+def check(q, cache, table, lens, out, lse, window=0, sinks=0, scale=None):
+    dtype, d = q.dtype, q.shape[2]
+    hkv, page = cache.k.shape[1], cache.page_size
+    g = q.shape[1] // hkv
+    int8 = cache.k.dtype == torch.int8
+    # weights meet 16-bit values in their own type; int8 codes in fp16
+    p_type = torch.float16 if int8 else dtype
+    scale = d ** -0.5 if scale is None else scale
+    for b, n in enumerate(lens.tolist()):
+        for h in range(hkv):
+            k, v = rows_of(cache, table, b, n, page, h)
+            j = torch.arange(n, device=DEV)
+            seen = torch.ones(n, dtype=torch.bool, device=DEV) if not window else (j >= n - window) | (j < sinks)
+            rows = slice(h * g, (h + 1) * g)
+            want, want_lse, tol, lse_tol = ref.attend(q[b, rows], k, v, scale, seen[None].expand(g, n),
+                                                      ref.unit(p_type), ref.least(p_type))
+            if n:
+                tol = tol + (want.abs() + tol) * ref.unit(dtype) + ref.least(dtype)
+            ref.assert_within(out[b, rows], want, tol, "sequence %d head %d" % (b, h))
+            if lse is not None:
+                if n == 0:
+                    assert (lse[b, rows] == -float("inf")).all()
+                else:
+                    ref.assert_within(lse[b, rows], want_lse, lse_tol, "lse %d" % b)
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("lens,hq,hkv,d,page", [
+    ([1], 8, 2, 128, 16),
+    ([0, 1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65], 4, 1, 64, 16),
+    ([274], 32, 8, 128, 16),
+    ([700, 0, 3, 1025, 129], 12, 2, 128, 7),
+    ([90, 511], 3, 3, 64, 1),
+    ([257], 40, 2, 128, 100),
+    ([5000, 4999], 16, 1, 128, 64),
+])
+def test_against_the_definition(lens, hq, hkv, d, page, dtype, int8):
+    q, cache, table, n = make(lens, hq, hkv, d, page, dtype, int8, seed=len(lens) + d)
+    out, lse = ck.ck_paged_attention(q, cache, table, n, return_lse=True)
+    check(q, cache, table, n, out, lse)
+    assert ck.ck_device_error() == 0
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 3), (16, 4), (100, 0), (130, 5), (4096, 4), (33, 1000)])
+def test_window_and_first_tokens(window, sinks, int8):
+    lens = [0, 1, 4, 100, 133, 135, 136, 999]
+    q, cache, table, n = make(lens, 8, 2, 64, 16, torch.bfloat16, int8, seed=window + sinks)
+    # what the window hides is poisoned too
+    for b, length in enumerate(lens):
+        j = torch.arange(length, device=DEV)
+        hidden = j[(j < length - window) & (j >= sinks)]
+        at, off = table[b].long()[hidden // 16], hidden % 16
+        for t in ((cache.k_scale, cache.v_scale) if int8 else (cache.k, cache.v)):
+            t[at, :, off] = float("inf")
+    out, lse = ck.ck_paged_attention(q, cache, table, n, window=window, sinks=sinks, return_lse=True)
+    for t in (cache.k_scale, cache.v_scale) if int8 else (cache.k, cache.v):
+        t.nan_to_num_(0.0, 0.0, 0.0)
+    check(q, cache, table, n, out, lse, window, sinks)
+
+
+@pytest.mark.parametrize("int8", [False, True])
+def test_many_sequences_and_a_long_one(int8):
+    lens = [(37 * i * i + 11) % 300 for i in range(150)] + [20011]
+    q, cache, table, n = make(lens, 8, 2, 128, 32, torch.bfloat16, int8, seed=77)
+    out, lse = ck.ck_paged_attention(q, cache, table, n, return_lse=True)
+    check(q, cache, table, n, out, lse)
+    again = ck.ck_paged_attention(q, cache, table, n)
+    assert torch.equal(out, again)  # the same split and order of sums every time
+
+
+def test_sharp_scores_and_strides():
+    lens = [300, 41]
+    q, cache, table, n = make(lens, 8, 2, 128, 16, torch.float16, False, seed=5, q_std=12.0)
+    wide = torch.zeros((2, 8 * 128 + 64), dtype=torch.float16, device=DEV)
+    wide[:, :1024] = q.reshape(2, -1)
+    view = wide[:, :1024].view(2, 8, 128)
+    out, lse = ck.ck_paged_attention(view, cache, table, n, return_lse=True, scale=0.3)
+    check(q, cache, table, n, out, lse, scale=0.3)
+
+
+@pytest.mark.parametrize("gain", [1e-30, 1e-6, 1e6, 1e30])
+def test_int8_queries_and_scales_of_any_size(gain):
+    """int8 codes meet bf16 queries and fp32 scales over their whole range."""
+    q, cache, table, n = make([123, 4], 4, 2, 64, 16, torch.bfloat16, True, seed=6)
+    q = (q.float() * gain).to(torch.bfloat16)
+    cache.k_scale.mul_(1.0 / gain)
+    cache.v_scale.mul_(gain)
+    out, lse = ck.ck_paged_attention(q, cache, table, n, return_lse=True)
+    check(q, cache, table, n, out, lse)
+
+
+def test_zero_scale_rows():
+    q, cache, table, n = make([70], 4, 2, 64, 16, torch.bfloat16, True, seed=8)
+    cache.v_scale[table[0].long()[:4]] = 0.0
+    out = ck.ck_paged_attention(q, cache, table, n)
+    check(q, cache, table, n, out, None)
+    cache.v_scale.zero_()
+    assert not ck.ck_paged_attention(q, cache, table, n).any()
+
+
+def test_out_of_range_indices_are_reported():
+    """A length beyond the table and a page beyond the pool: bounds-checked, NaN, reported."""
+    assert ck.ck_device_error() == 0
+    q, cache, table, n = make([50, 50, 50, 50], 4, 2, 64, 16, torch.bfloat16, False, seed=9)
+    good = ck.ck_paged_attention(q, cache, table, n)
+    n[1] = table.shape[1] * 16 + 1
+    table[2, 1] = cache.num_pages
+    out = ck.ck_paged_attention(q, cache, table, n)
+    assert out[1].isnan().all() and out[2].isnan().all()
+    assert torch.equal(out[0], good[0]) and torch.equal(out[3], good[3])
+    assert ck.ck_device_error(clear=True) == 128
+    n[1] = -1
+    assert ck.ck_paged_attention(q, cache, table, n)[1].isnan().all()
+    assert ck.ck_device_error(clear=True) == 128
+
+
+def test_streams_share_nothing_and_graphs_replay():
+    q, cache, table, n = make([900, 20, 3000], 8, 2, 128, 16, torch.bfloat16, False, seed=10)
+    want = ck.ck_paged_attention(q, cache, table, n)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    outs = [[ck.ck_paged_attention(q, cache, table, n, stream=s) for _ in range(5)] for s in streams]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for per in outs for o in per)
+    out = torch.empty_like(want)
+    ws = torch.full((ck.load_library().ck_paged_attention_workspace_size(3, 8, 2, 128),), 255, dtype=torch.uint8,
+                    device=DEV)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        ck.ck_paged_attention(q, cache, table, n, out=out, ws=ws)
+    n[0], n[2] = 10, 2999
+    for _ in range(2):
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, ck.ck_paged_attention(q, cache, table, n))
