@@ -358,7 +358,7 @@ int ck_attention(const void *q, int64_t q_stride, const void *k, int64_t k_strid
  *             16 + 4 i .. (i = 0..3).  w_scale: bf16 [N, K/group]; group 32, 64, 128 or 256.
  *   bias:     [N] of dtype or NULL.  residual: [M,N] of out_dtype or NULL (may be y).
  *   y:        [M,N] of out_dtype (a ck_dtype_t), written.
- * K a multiple of 128 and of group, N of 8.  Any M; it pays while the weight's bytes, not the
+ * K a multiple of 128 and of group, N of 8, M up to 524288; it pays while the weight's bytes, not the
  * arithmetic, set the time (some tens of rows).
  *   ck_int4_prepare_weight: fp32 W [N,K] -> w4, w_scale: per group scale = bf16(max|W| / 7),
  *             code - 8 = clamp(rint(W / scale), -7, 7).

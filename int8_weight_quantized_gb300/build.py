@@ -21,7 +21,8 @@ LIB = os.path.join(LIB_DIR, "libck_int8.so")
 
 SOURCES = ["api.cu", "quantize.cu", "gemm.cu", "api_transformer.cu", "norm_rope.cu", "paged_attention.cu",
            "attention.cu", "int4.cu"]
-HEADERS = ["ck_device.cuh", "ck_internal.h", "gemm_common.cuh", "api_common.h", "transformer.h", "attn_common.cuh"]
+HEADERS = ["ck_device.cuh", "ck_internal.h", "gemm_common.cuh", "api_common.h", "transformer.h", "attn_common.cuh",
+           "warp_mma.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
               "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]

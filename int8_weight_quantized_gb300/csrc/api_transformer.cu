@@ -65,6 +65,8 @@ int check_cache(const ck_kv_cache_t* c, int64_t kv_heads, int64_t head_dim, int 
     if (c->num_pages < 1 || c->page_size < 1 || c->page_size > kMaxCount || c->num_pages > kMaxCount)
         return fail(CK_ERR_INVALID_ARG, "cache num_pages and page_size must be in 1..2^31-1 (got %lld and %lld)",
                     (long long)c->num_pages, (long long)c->page_size);
+    if (c->num_pages * c->page_size > 0xFFFFFFFFll / kv_heads)
+        return fail(CK_ERR_INVALID_ARG, "cache rows (pages * page_size * heads) must be below 2^32");
     if (c->dtype != CK_KV_INT8 && c->dtype != (dtype == CK_OUT_F16 ? CK_KV_F16 : CK_KV_BF16))
         return fail(CK_ERR_INVALID_ARG, "cache dtype %d is neither int8 (2) nor the activations' type (%d)", c->dtype,
                     dtype);
@@ -386,8 +388,8 @@ int ck_int4_linear(const void* x, const uint32_t* w4, const void* w_scale, const
         return fail(CK_ERR_INVALID_ARG, "out_dtype must be 0 (bf16), 1 (fp16) or 2 (fp32), got %d", out_dtype);
     CK_CHECK(check_int4_shape(N, K));
     CK_CHECK(check_group(group, K));
-    if (M < 0 || M > kMaxCount)
-        return fail(CK_ERR_INVALID_ARG, "M must be in 0..2^31-1 (got %lld)", (long long)M);
+    if (M < 0 || M > (1 << 19))
+        return fail(CK_ERR_INVALID_ARG, "M must be in 0..524288 (got %lld)", (long long)M);
     if (M == 0)
         return CK_OK;
     CK_REQUIRE_PTR(x);

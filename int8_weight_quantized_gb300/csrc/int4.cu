@@ -5,11 +5,15 @@
 //   c = code - 8 in [-8, 7], eight codes to a 32-bit word: the code of k = 8 j + 2 i in bits
 //   4 i .. 4 i + 3 of word j, that of k = 8 j + 2 i + 1 in bits 16 + 4 i .. (a pair of
 //   neighbouring k is then one shift and one mask away from two 16-bit halves).
+#include <algorithm>
+#include <type_traits>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "attn_common.cuh"
 #include "transformer.h"
+#include "warp_mma.cuh"
 
 namespace ck {
 namespace {
@@ -19,44 +23,196 @@ __device__ __forceinline__ int code_shift(int e)
     return 4 * (e >> 1) + 16 * (e & 1);
 }
 
+// Bound: HBM, N K / 2 bytes of codes and 2 N K / group of scales, read once.
+//
+// A block takes 16 RT weight rows and its 8 warps share out K in chunks of 128, each warp a
+// contiguous run; a warp streams its run's codes and scales through its own ring of
+// asynchronous copies, with no block-wide barrier until the warps' sums are added, in a fixed
+// order, at the end.  x, which every block reads whole, comes from L2 straight into the
+// registers that the products take, a chunk ahead: in the ring it would take twice the codes'
+// room at 8 rows.  Products run on the 16x8x16 matrix instruction,
+// weight rows as its 16 rows and up to 8 rows of x as its 8 columns: at one row seven columns
+// are idle, which costs nothing while HBM sets the pace, and up to 8 rows cost the same.  The
+// codes are exact in bf16 and fp16 (nibble in the mantissa of 128 or 1024, minus that and 8),
+// the products exact in fp32; a group's sum is scaled once, in fp32.
+constexpr int WARPS = 8;
+constexpr int CHUNK = 128;                 // k of a ring unit
+constexpr int STAGES = 4;
+constexpr int W_LD = 80;                   // bytes of a unit's weight row: 64, padded so that 8 rows spread over the banks
+
 template <class E>
-__global__ void __launch_bounds__(128) int4_row_kernel(const Int4Linear p)
+__device__ __forceinline__ uint32_t codes_of(uint32_t word, int i)
 {
-    griddep_wait();
-    using T = typename E::T;
-    const int lane = threadIdx.x & 31;
-    const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int64_t m = unit / p.N, n = unit - m * p.N;
-    if (m >= p.M)
-        return;
-    const uint32_t* w = p.w4 + n * (p.K / 8);
-    const __nv_bfloat16* sc = static_cast<const __nv_bfloat16*>(p.w_scale) + n * (p.K / p.group);
-    const T* x = static_cast<const T*>(p.x) + m * p.K;
-    float sum = 0.0f;
-    for (int64_t j = lane; j < p.K / 8; j += 32) {
-        const uint32_t word = __ldg(w + j);
-        float part = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            part = fmaf(E::to(x[8 * j + e]), (float)((int)((word >> code_shift(e)) & 15u) - 8), part);
-        sum = fmaf(part, __bfloat162float(sc[8 * j / p.group]), sum);
+    // the pair k = 2 i, 2 i + 1 of the word's eight: code - 8 in two 16-bit floats
+    const uint32_t u = ((word >> (4 * i)) & 0x000F000Fu) | (std::is_same<E, Bf16>::value ? 0x43004300u : 0x64006400u);
+    if (std::is_same<E, Bf16>::value) {
+        const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u), __float2bfloat162_rn(136.0f));
+        return *reinterpret_cast<const uint32_t*>(&v);
     }
+    const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&u), __float2half2_rn(1032.0f));
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+template <int RT>
+constexpr int kUnit = 16 * RT * (W_LD + 8);  // codes, then 8 bytes of scales a row
+
+template <class E, int RT, int MT>
+__global__ void __launch_bounds__(WARPS * 32) int4_kernel(const Int4Linear p)
+{
+    using T = typename E::T;
+    extern __shared__ __align__(128) uint8_t smem[];
+    griddep_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane >> 2, t = lane & 3;
+    const int64_t n0 = (int64_t)blockIdx.x * (16 * RT);
+    const int64_t m0 = (int64_t)blockIdx.y * (8 * MT);
+    const int rows = (int)min((int64_t)(8 * MT), p.M - m0);      // rows of x
+    const int chunks = (int)(p.K / CHUNK);
+    const int c0 = (int)((int64_t)warp * chunks / WARPS), c1 = (int)((int64_t)(warp + 1) * chunks / WARPS);
+    const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * STAGES * kUnit<RT>);
+    const int log_group = 31 - __clz(p.group);  // a power of two
+    const int64_t groups = p.K >> log_group;
+    const int per_chunk = p.group >= CHUNK ? 1 : CHUNK >> log_group;  // scales of a row in a chunk
+
+    auto issue = [&](int c, int stage) {
+        if (c < c1) {
+            const uint32_t w = ring + stage * kUnit<RT>;
+            const uint32_t sc = w + 16 * RT * W_LD;
 #pragma unroll
-    for (int o = 16; o; o >>= 1)
-        sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane != 0)
-        return;
-    if (p.bias != nullptr)
-        sum += E::to(static_cast<const T*>(p.bias)[n]);
-    const int64_t at = m * p.N + n;
-    if (p.out_dtype == CK_OUT_F32)
-        static_cast<float*>(p.y)[at] = sum + (p.residual ? static_cast<const float*>(p.residual)[at] : 0.0f);
-    else if (p.out_dtype == CK_OUT_F16)
-        static_cast<__half*>(p.y)[at] =
-            __float2half_rn(sum + (p.residual ? __half2float(static_cast<const __half*>(p.residual)[at]) : 0.0f));
-    else
-        static_cast<__nv_bfloat16*>(p.y)[at] = __float2bfloat16_rn(
-            sum + (p.residual ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.residual)[at]) : 0.0f));
+            for (int i = 0; i < 2 * RT; ++i) {  // 8 rows of 4 x 16 bytes an instruction
+                const int r = i * 8 + (lane >> 2);
+                const int64_t n = n0 + r;
+                cp_async16(w + r * W_LD + (lane & 3) * 16, p.w4 + (n < p.N ? n : 0) * (p.K / 8) + c * 16 + (lane & 3) * 4,
+                           n < p.N);
+            }
+#pragma unroll
+            for (int i = 0; i < (16 * RT + 31) / 32; ++i) {
+                const int r = i * 32 + lane;
+                const int64_t n = n0 + r;
+                if (r < 16 * RT) {
+                    // the row's scales of this chunk: 8 bytes, 4, or the aligned 4 that hold the one
+                    const int64_t e = (n < p.N ? n : 0) * groups + ((c * (int64_t)CHUNK) >> log_group);
+                    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.w_scale);
+                    if (per_chunk == 4)
+                        cp_async_small<8>(sc + r * 8, src + e, n < p.N);
+                    else
+                        cp_async_small<4>(sc + r * 8, src + (e & ~1ll), n < p.N);
+                }
+            }
+        }
+        cp_async_commit();
+    };
+    // this lane's part of a chunk of x: row g of each tile, k = 32 j + 8 t .. + 7 (rows past M: 0)
+    uint4 ahead[4][MT];
+    const T* xl = static_cast<const T*>(p.x) + (m0 + g) * p.K + t * 8;
+    auto load_x = [&](int c) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+                ahead[j][mt] = 8 * mt + g < rows
+                                   ? __ldg(reinterpret_cast<const uint4*>(xl + 8 * mt * p.K + (int64_t)c * CHUNK + j * 32))
+                                   : make_uint4(0u, 0u, 0u, 0u);
+    };
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s)
+        issue(c0 + s, s);
+    if (c0 < c1)
+        load_x(c0);
+
+    float sum[RT][MT][4] = {};
+    float acc[RT][MT][4] = {};
+    int stage = 0;
+    for (int c = c0; c < c1; ++c) {
+        issue(c + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1);
+        cp_async_wait<STAGES - 1>();
+        __syncwarp();
+        const uint32_t w = ring + stage * kUnit<RT>;
+        const uint32_t sc = w + 16 * RT * W_LD;
+        uint4 b[4][MT];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+                b[j][mt] = ahead[j][mt];
+        if (c + 1 < c1)
+            load_x(c + 1);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {  // 32 k: word 4 j + t of a row is this lane's
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                const uint32_t lo = lds32(w + (16 * rt + g) * W_LD + j * 16 + t * 4);
+                const uint32_t hi = lds32(w + (16 * rt + 8 + g) * W_LD + j * 16 + t * 4);
+                const uint32_t a0[4] = {codes_of<E>(lo, 0), codes_of<E>(hi, 0), codes_of<E>(lo, 1), codes_of<E>(hi, 1)};
+                const uint32_t a1[4] = {codes_of<E>(lo, 2), codes_of<E>(hi, 2), codes_of<E>(lo, 3), codes_of<E>(hi, 3)};
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    mma_16816<E>(acc[rt][mt], a0, b[j][mt].x, b[j][mt].y);
+                    mma_16816<E>(acc[rt][mt], a1, b[j][mt].z, b[j][mt].w);
+                }
+            }
+            // the end of a group: scale its sums
+            if (j == 3 || per_chunk == 4 || (per_chunk == 2 && j == 1)) {
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int r = 16 * rt + 8 * h + g;
+                        int e = per_chunk == 4 ? j : per_chunk == 2 ? j >> 1 : 0;
+                        if (per_chunk == 1)
+                            e = (int)(((n0 + r) * groups + ((c * (int64_t)CHUNK) >> log_group)) & 1);
+                        const uint32_t pair = lds32(sc + r * 8 + (e >> 1) * 4);
+                        const float s = __uint_as_float((e & 1) ? pair & 0xFFFF0000u : pair << 16);
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) {
+                            sum[rt][mt][2 * h] = fmaf(acc[rt][mt][2 * h], s, sum[rt][mt][2 * h]);
+                            sum[rt][mt][2 * h + 1] = fmaf(acc[rt][mt][2 * h + 1], s, sum[rt][mt][2 * h + 1]);
+                            acc[rt][mt][2 * h] = acc[rt][mt][2 * h + 1] = 0.0f;
+                        }
+                    }
+            }
+        }
+        __syncwarp();
+        stage = stage + 1 == STAGES ? 0 : stage + 1;
+    }
+    cp_async_wait<0>();
+    griddep_launch_dependents();
+
+    // add the warps' sums: [warp][m][n] in the ring's memory
+    __syncthreads();
+    float* red = reinterpret_cast<float*>(smem);
+    constexpr int LD = 16 * RT + 1;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int m = 8 * mt + 2 * t + (i & 1);
+                if (m < rows)
+                    red[(warp * rows + m) * LD + 16 * rt + 8 * (i >> 1) + g] = sum[rt][mt][i];
+            }
+    __syncthreads();
+    for (int i = threadIdx.x; i < rows * 16 * RT; i += WARPS * 32) {
+        const int m = i / (16 * RT), r = i - m * (16 * RT);
+        const int64_t n = n0 + r;
+        if (n >= p.N)
+            continue;
+        float v = 0.0f;
+#pragma unroll
+        for (int k = 0; k < WARPS; ++k)
+            v += red[(k * rows + m) * LD + r];
+        if (p.bias != nullptr)
+            v += E::to(static_cast<const T*>(p.bias)[n]);
+        const int64_t at = (m0 + m) * p.N + n;
+        if (p.out_dtype == CK_OUT_F32)
+            static_cast<float*>(p.y)[at] = v + (p.residual ? static_cast<const float*>(p.residual)[at] : 0.0f);
+        else if (p.out_dtype == CK_OUT_F16)
+            static_cast<__half*>(p.y)[at] = Fp16::from(v + (p.residual ? Fp16::to(static_cast<const __half*>(p.residual)[at]) : 0.0f));
+        else
+            static_cast<__nv_bfloat16*>(p.y)[at] =
+                Bf16::from(v + (p.residual ? Bf16::to(static_cast<const __nv_bfloat16*>(p.residual)[at]) : 0.0f));
+    }
 }
 
 // Weight preparation: one thread per word for the codes; the group's scale is found by the
@@ -113,18 +269,49 @@ __global__ void __launch_bounds__(256) int4_pack_kernel(const int8_t* codes, int
 
 }  // namespace
 
+namespace {
+
+template <class E, int RT, int MT>
+cudaError_t launch(const Int4Linear& p, cudaStream_t s)
+{
+    constexpr size_t smem = std::max((size_t)WARPS * STAGES * kUnit<RT>,         // the rings
+                                     (size_t)WARPS * 8 * MT * (16 * RT + 1) * 4);  // then the warps' sums
+    // a kernel attribute belongs to the context it was set in: set once per context
+    static ContextCache<int> cache;
+    int done = 0;
+    cudaError_t e = cache.get(&done, [](int* d) {
+        *d = 1;
+        return cudaFuncSetAttribute(int4_kernel<E, RT, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)smem);
+    });
+    if (e != cudaSuccess)
+        return e;
+    const dim3 grid((unsigned)((p.N + 16 * RT - 1) / (16 * RT)), (unsigned)((p.M + 8 * MT - 1) / (8 * MT)));
+    return launch_pdl(int4_kernel<E, RT, MT>, grid, dim3(WARPS * 32), smem, s, p);
+}
+
+template <class E>
+cudaError_t by_rows(const Int4Linear& p, cudaStream_t s)
+{
+    if (p.M <= 8)
+        return launch<E, 1, 1>(p, s);
+    if (p.M <= 16)
+        return launch<E, 2, 2>(p, s);
+    return launch<E, 2, 4>(p, s);
+}
+
+}  // namespace
+
 size_t int4_linear_workspace(int64_t M, int64_t N, int64_t K)
 {
     (void)M, (void)N, (void)K;
-    return 16;
+    return 0;
 }
 
 cudaError_t launch_int4_linear(const Int4Linear& p, const DeviceInfo& dev, cudaStream_t s)
 {
     (void)dev;
-    const unsigned blocks = (unsigned)((p.M * p.N + 3) / 4);
-    return p.f16 ? launch_pdl(int4_row_kernel<Fp16>, dim3(blocks), dim3(128), 0, s, p)
-                 : launch_pdl(int4_row_kernel<Bf16>, dim3(blocks), dim3(128), 0, s, p);
+    return p.f16 ? by_rows<Fp16>(p, s) : by_rows<Bf16>(p, s);
 }
 
 cudaError_t launch_int4_weight(const float* W, int64_t N, int64_t K, int group, uint32_t* w4, void* w_scale,

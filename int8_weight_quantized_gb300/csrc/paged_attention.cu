@@ -3,93 +3,725 @@
 //   out[b,h] = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale * q[b,h] . k_j - max),  j over the
 //   keys of sequence b that its last token sees (all, or the first `sinks` and the last
 //   `window`); zeros where the sequence is empty.
+//
+// Bound: HBM.  Every visible key and value row is read once per kv head, for the up to 16
+// query heads that share it; nothing else is read more than once.
+//
+// Work.  A segment is one (sequence, kv head, 16 query heads); its visible keys, numbered
+// through without the hidden ones, are cut into tiles of 64.  All segments' tiles in a row are
+// shared out evenly: block c of C takes tiles [c T / C, (c + 1) T / C), whatever the lengths
+// (each block sums the lengths up itself, so nothing depends on the host knowing them and a
+// captured graph may be replayed with new lengths).  A block leaves a segment that it holds
+// whole as the final output, and the at most two that it shares with a neighbour as partial
+// sums (maximum, sum of weights, weighted values); join_kernel adds those up, always in the
+// same order.  Where no segment can hold more than kWholeTiles tiles, one block takes each
+// whole segment and there is no second launch.
+//
+// Inside a block each of the 4 warps takes 16 keys of a tile on its own: its own ring of
+// asynchronous copies (no block-wide barrier while tiles stream), its own running maximum and
+// sum; the four are joined once per segment.  Scores and weighted values run on the 16x8x16
+// matrix instruction with the query heads as its 16 rows; the weights go from the first
+// product's accumulators straight into the second's operand registers.
+//
+// int8 rows: a code is exact in fp16, so both products run in fp16: the query scaled by the
+// power of two that brings its largest value into [1, 2) (undone in the fp32 score), and the
+// row scales folded in as fp32: k's into the score, v's into the weight as
+// 2^(s + log2 v_scale - M) with a running maximum M of its own, so that scales of any size
+// leave the fp16 weight in [0, 1].
+//
+// Rounding to fewer bits: each weight once, to the type of the values' product (bf16 or
+// fp16), which is what the matrix instruction takes; sums, maxima and scores are fp32.
+#include <algorithm>
+#include <type_traits>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "attn_common.cuh"
 #include "transformer.h"
+#include "warp_mma.cuh"
 
 namespace ck {
 namespace {
 
-template <class E, bool INT8, int DIM>
-__global__ void __launch_bounds__(32) paged_row_kernel(const PagedAttention p, unsigned int* err)
+constexpr int WARPS = 4;
+constexpr int KEYS = 16;              // keys of one warp's unit
+constexpr int TILE = WARPS * KEYS;    // keys of a block's tile
+constexpr int HEADS = 16;             // query heads of a segment
+constexpr int kWholeTiles = 8;        // segments of at most this many tiles are not split
+constexpr int kBlocksPerSm = 2;
+
+template <bool INT8, int DIM>
+struct Shape {
+    static constexpr int ROW = DIM * (INT8 ? 1 : 2);        // bytes of a row
+    static constexpr int SCALES = INT8 ? 2 * KEYS * 4 : 0;  // k scales, v scales
+    static constexpr int UNIT = 2 * KEYS * ROW + SCALES;
+    // ring depth: about 24 KB a warp, so that two blocks an SM keep up to ~190 KB in flight
+    static constexpr int STAGES = INT8 ? (DIM == 128 ? 6 : 8) : (DIM == 128 ? 3 : 6);
+    static constexpr int LD = DIM + 4;                       // joined sums: floats per head
+    static constexpr size_t RING = (size_t)WARPS * STAGES * UNIT;
+    static constexpr size_t SMEM = RING + HEADS * LD * 4 + WARPS * HEADS * 8;
+    static constexpr size_t PART = (size_t)HEADS * (DIM + 2);  // floats of one partial
+};
+
+// ---- the division of work, the same in both kernels
+struct Lengths {
+    const int32_t* seq_lens;
+    int64_t max_len, window, sinks;
+    int subs;  // segments of a sequence
+    __device__ int length(int64_t b, bool* bad) const
+    {
+        const int64_t n = __ldg(seq_lens + b);
+        *bad = n < 0 || n > max_len;
+        return *bad ? 0 : (int)n;
+    }
+    __device__ int tiles(int64_t b) const
+    {
+        bool bad;
+        return (visible_keys(length(b, &bad), window, sinks).count() + TILE - 1) / TILE;
+    }
+};
+
+// By a whole warp: tiles of all segments before sequence `upto`.
+__device__ __forceinline__ int64_t tiles_before(const Lengths& L, int64_t upto)
 {
-    griddep_wait();
-    __shared__ float qs[DIM];
-    using T = typename E::T;
-    const int lane = threadIdx.x;
-    const int64_t b = blockIdx.x / p.q_heads;
-    const int h = (int)(blockIdx.x - b * p.q_heads);
-    const int hk = h / (p.q_heads / p.cache.heads);
-    const T* q = static_cast<const T*>(p.q) + b * p.q_stride + (int64_t)h * DIM;
-    for (int d = lane; d < DIM; d += 32)
-        qs[d] = E::to(q[d]) * (p.scale * kLog2e);
-    __syncwarp();
-    const int64_t len = __ldg(p.seq_lens + b);
-    bool bad = len < 0 || len > p.max_blocks * p.cache.page_size;
-    const VisibleKeys keys = visible_keys(bad ? 0 : (int)len, p.window, p.sinks);
-    const int32_t* table = p.block_table + b * p.max_blocks;
-    const size_t row_bytes = (size_t)DIM * (INT8 ? 1 : 2);
-    bool off_table = false;
-    float acc[(DIM + 31) / 32], m, l;
-    attend_row<E, INT8, DIM>(qs, keys.count(), [&](int v) {
-        const int j = keys.key(v);
-        int64_t page = __ldg(table + j / p.cache.page_size);
-        if (page < 0 || page >= p.cache.num_pages) {
-            off_table = true;
-            page = 0;
-        }
-        const int64_t row = (page * p.cache.heads + hk) * p.cache.page_size + j % p.cache.page_size;
-        KvRow r;
-        r.k = static_cast<const uint8_t*>(p.cache.k) + row * row_bytes;
-        r.v = static_cast<const uint8_t*>(p.cache.v) + row * row_bytes;
-        r.ks = INT8 ? __ldg(p.cache.k_scale + row) : 1.0f;
-        r.vs = INT8 ? __ldg(p.cache.v_scale + row) : 1.0f;
-        return r;
-    }, acc, m, l);
-    bad = __any_sync(0xffffffffu, bad || off_table);
-    if (bad && lane == 0)
-        atomicOr(err, kErrIndex);
-    const int64_t at = b * p.q_heads + h;
+    const int lane = threadIdx.x & 31;
+    int64_t sum = 0;
+    for (int64_t b = lane; b < upto; b += 32)
+        sum += (int64_t)L.tiles(b) * L.subs;
 #pragma unroll
-    for (int i = 0; i < (DIM + 31) / 32; ++i)
-        static_cast<T*>(p.out)[at * DIM + lane + 32 * i] =
-            E::from(bad ? NAN : keys.count() == 0 ? 0.0f : acc[i] / l);
-    if (p.lse != nullptr && lane == 0)
-        p.lse[at] = bad ? NAN : (m + log2f(l)) * kLn2;
+    for (int o = 16; o; o >>= 1)
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return sum;
+}
+
+__device__ __forceinline__ int64_t first_tile(int64_t c, int64_t C, int64_t T)
+{
+    return c * T / C;
+}
+
+// By a whole warp: the sequence that holds tile `t` of all tiles, and the tiles before it.
+__device__ __forceinline__ int64_t sequence_at(const Lengths& L, int64_t batch, int64_t t, int64_t* before)
+{
+    const int lane = threadIdx.x & 31;
+    int64_t base = 0;
+    for (int64_t b0 = 0; b0 < batch; b0 += 32) {
+        int64_t mine = b0 + lane < batch ? (int64_t)L.tiles(b0 + lane) * L.subs : 0;
+        int64_t upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o)
+                upto += v;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, base + upto > t);
+        if (past) {
+            const int l = __ffs(past) - 1;
+            *before = base + __shfl_sync(0xffffffffu, upto - mine, l);
+            return b0 + l;
+        }
+        base += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    *before = base;
+    return batch;
+}
+
+// Walks the tiles of a block's range.
+struct Cursor {
+    int64_t b;
+    int sub, tile, tiles;
+    int64_t left;  // tiles of the range from here on
+    VisibleKeys keys;
+    __device__ void open(const Lengths& L)
+    {
+        bool bad;
+        keys = visible_keys(L.length(b, &bad), L.window, L.sinks);
+        tiles = (keys.count() + TILE - 1) / TILE;
+    }
+    __device__ void next(const Lengths& L)
+    {
+        if (--left <= 0 || ++tile < tiles)
+            return;
+        tile = 0;
+        if (++sub < L.subs)
+            return;
+        sub = 0;
+        do {
+            ++b;
+            open(L);
+        } while (tiles == 0);  // left > 0: a later sequence has tiles
+    }
+};
+
+// ---- int8 codes to pairs of fp16, exact: byte ^ 0x80 in the mantissa of 1024, minus 1152
+__device__ __forceinline__ uint32_t half2_of(uint32_t biased_pair_bytes, uint32_t sel)
+{
+    const uint32_t w = __byte_perm(biased_pair_bytes, 0x64646464u, sel);
+    const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&w), __half2half2(__ushort_as_half(0x6480)));
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Byte address of 16-byte chunk c of row r of a ring unit's K or V part, so that the reads
+// below spread over all banks.
+template <bool INT8, int DIM, bool V>
+__device__ __forceinline__ uint32_t chunk_at(int r, int c)
+{
+    constexpr int CHUNKS = Shape<INT8, DIM>::ROW / 16;
+    int p;
+    if (!INT8)
+        p = c ^ (r & 7);  // ldmatrix: one chunk of 8 neighbouring rows
+    else if (CHUNKS == 8)
+        p = V ? c ^ (((r >> 1) & 3) << 1) : c ^ ((r & 1) << 2);
+    else
+        p = V ? c ^ ((r >> 1) & 3) : c;
+    return (uint32_t)(r * Shape<INT8, DIM>::ROW + p * 16);
 }
 
 template <class E, bool INT8, int DIM>
-cudaError_t launch(const PagedAttention& p, unsigned int* err, cudaStream_t s)
+__global__ void __launch_bounds__(WARPS * 32, kBlocksPerSm)
+    paged_kernel(const PagedAttention p, int64_t C, bool split, unsigned int* err)
 {
-    return launch_pdl(paged_row_kernel<E, INT8, DIM>, dim3((unsigned)(p.batch * p.q_heads)), dim3(32), 0, s, p, err);
+    using S = Shape<INT8, DIM>;
+    using T = typename E::T;
+    using M = typename std::conditional<INT8, Fp16, E>::type;  // the products' type
+    extern __shared__ __align__(128) uint8_t smem[];
+    griddep_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane >> 2, t = lane & 3;
+    const int group = p.q_heads / p.cache.heads;  // query heads per kv head
+    const int qtiles = (group + HEADS - 1) / HEADS;
+    const int page_size = p.cache.page_size;
+    Lengths L{p.seq_lens, p.max_blocks * page_size, p.window, p.sinks, p.cache.heads * qtiles};
+
+    // sequences without visible keys have no tiles: zeros, or NaN where the length is out of range
+    for (int64_t b = blockIdx.x; b < p.batch; b += gridDim.x) {
+        bool bad;
+        const int n = L.length(b, &bad);
+        if (n > 0)
+            continue;
+        if (bad && threadIdx.x == 0)
+            atomicOr(err, kErrIndex);
+        for (int i = threadIdx.x; i < p.q_heads * DIM; i += WARPS * 32)
+            static_cast<T*>(p.out)[b * p.q_heads * DIM + i] = E::from(bad ? NAN : 0.0f);
+        if (p.lse != nullptr)
+            for (int i = threadIdx.x; i < p.q_heads; i += WARPS * 32)
+                p.lse[b * p.q_heads + i] = bad ? NAN : -INFINITY;
+    }
+
+    // this block's range of tiles
+    Cursor at;
+    if (split) {
+        const int64_t total = tiles_before(L, p.batch);
+        C = min(C, total);  // no block of those that take part is without tiles
+        if (blockIdx.x >= C)
+            return;
+        const int64_t t0 = first_tile(blockIdx.x, C, total), t1 = first_tile(blockIdx.x + 1, C, total);
+        at.left = t1 - t0;
+        int64_t before;
+        at.b = sequence_at(L, p.batch, t0, &before);
+        at.open(L);
+        at.sub = (int)((t0 - before) / at.tiles);
+        at.tile = (int)((t0 - before) % at.tiles);
+    } else {
+        at.b = blockIdx.x / L.subs;
+        at.sub = (int)(blockIdx.x - at.b * L.subs);
+        at.tile = 0;
+        at.open(L);
+        at.left = at.tiles;
+        if (at.left <= 0)
+            return;
+    }
+
+    const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * S::STAGES * S::UNIT);
+    float* joined = reinterpret_cast<float*>(smem + S::RING);         // [HEADS][LD]
+    float2* maxsum = reinterpret_cast<float2*>(joined + HEADS * S::LD);  // [WARPS][HEADS]
+
+    // ---- copies: lane l looks up the row of key l % 16 of the warp's unit one unit ahead
+    Cursor ahead = at;
+    int32_t page = 0;
+    int in_page = 0;
+    bool have = false;
+    auto look_up = [&]() {
+        const int v = ahead.tile * TILE + warp * KEYS + (lane & 15);
+        have = ahead.left > 0 && v < ahead.keys.count();
+        if (have) {
+            const int j = ahead.keys.key(v);
+            const int blk = j / page_size;
+            in_page = j - blk * page_size;
+            page = __ldg(p.block_table + ahead.b * p.max_blocks + blk);
+        }
+    };
+    uint32_t bad_units = 0;  // bit s: the unit in stage s has a page number out of range
+    auto issue = [&](int stage) {
+        if (ahead.left > 0) {
+            const bool in_pool = page >= 0 && page < p.cache.num_pages;
+            const uint32_t bad = __ballot_sync(0xffffffffu, have && !in_pool);
+            bad_units = (bad_units & ~(1u << stage)) | ((bad ? 1u : 0u) << stage);
+            const bool ok = have && in_pool;
+            const int hk = ahead.sub / qtiles;
+            const uint32_t row = ok ? (uint32_t)(((int64_t)page * p.cache.heads + hk) * page_size + in_page) : 0u;
+            const uint32_t oks = __ballot_sync(0xffffffffu, ok);
+            const uint32_t dst = ring + stage * S::UNIT;
+            constexpr int CH = S::ROW / 16;       // chunks of a row
+            constexpr int RPI = 32 / CH;          // rows of one instruction
+            const int c = lane % CH;
+#pragma unroll
+            for (int i = 0; i < KEYS / RPI; ++i) {
+                const int r = i * RPI + lane / CH;
+                const uint32_t src_row = __shfl_sync(0xffffffffu, row, r);
+                const bool r_ok = (oks >> r) & 1u;
+                const size_t off = (size_t)src_row * S::ROW + c * 16;
+                cp_async16(dst + chunk_at<INT8, DIM, false>(r, c), static_cast<const uint8_t*>(p.cache.k) + off, r_ok);
+                cp_async16(dst + KEYS * S::ROW + chunk_at<INT8, DIM, true>(r, c),
+                           static_cast<const uint8_t*>(p.cache.v) + off, r_ok);
+            }
+            if (INT8)
+                cp_async_small<4>(dst + 2 * KEYS * S::ROW + lane * 4, (lane < 16 ? p.cache.k_scale : p.cache.v_scale) + row,
+                                  ok);
+            ahead.next(L);
+            look_up();
+        }
+        cp_async_commit();
+    };
+    look_up();
+#pragma unroll
+    for (int s = 0; s < S::STAGES - 1; ++s)
+        issue(s);
+
+    uint32_t qa[DIM / 16][4];
+    float o[DIM / 8][4];
+    float m[2], l[2], mv[2];  // rows g and g + 8: maximum and sum of weights; int8: the values' maximum
+    float c_row[2];           // score factor, in units of log2
+    bool bad = false;
+    bool fresh = true;
+    int first_of_segment = 0;  // the block's first tile of the segment
+    int stage = 0;
+    int piece = 0;             // partial slots used
+
+    for (;;) {
+        if (fresh) {  // a new segment: its queries
+            const int hk = at.sub / qtiles, qt = at.sub - hk * qtiles;
+            const int h0 = hk * group + qt * HEADS;
+            const int heads = min(HEADS, group - qt * HEADS);
+            const T* q = static_cast<const T*>(p.q) + at.b * p.q_stride + (int64_t)h0 * DIM;
+            const float c = p.scale * kLog2e;
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int row = g + 8 * r;
+                c_row[r] = c;
+                if (!INT8) {
+#pragma unroll
+                    for (int kk = 0; kk < DIM / 16; ++kk) {
+                        const uint32_t* src = reinterpret_cast<const uint32_t*>(q + (int64_t)row * DIM + 16 * kk + 2 * t);
+                        qa[kk][r] = row < heads ? __ldg(src) : 0u;
+                        qa[kk][2 + r] = row < heads ? __ldg(src + 4) : 0u;
+                    }
+                } else {
+                    // the int8 products' order: k-step kk, lane t <- d = 64 (kk / 4) + 16 t + 4 (kk % 4) ..
+                    float v[DIM / 4];
+                    float top = 0.0f;
+#pragma unroll
+                    for (int kk = 0; kk < DIM / 16; ++kk) {
+                        const uint2 w = row < heads ? __ldg(reinterpret_cast<const uint2*>(
+                                                          q + (int64_t)row * DIM + 64 * (kk / 4) + 16 * t + 4 * (kk % 4)))
+                                                    : make_uint2(0u, 0u);
+                        const float2 a = E::to2(w.x), b = E::to2(w.y);
+                        v[4 * kk] = a.x, v[4 * kk + 1] = a.y, v[4 * kk + 2] = b.x, v[4 * kk + 3] = b.y;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            top = fmaxf(top, fabsf(v[4 * kk + i]));
+                    }
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    const int e = top > 0.0f && top < INFINITY ? ilogbf(top) : 0;
+                    c_row[r] = ldexpf(c, e);
+#pragma unroll
+                    for (int kk = 0; kk < DIM / 16; ++kk) {
+                        qa[kk][r] = Fp16::pack2(ldexpf(v[4 * kk], -e), ldexpf(v[4 * kk + 1], -e));
+                        qa[kk][2 + r] = Fp16::pack2(ldexpf(v[4 * kk + 2], -e), ldexpf(v[4 * kk + 3], -e));
+                    }
+                }
+                m[r] = mv[r] = -INFINITY;
+                l[r] = 0.0f;
+            }
+#pragma unroll
+            for (int e = 0; e < DIM / 8; ++e)
+                o[e][0] = o[e][1] = o[e][2] = o[e][3] = 0.0f;
+            bad = false;
+            fresh = false;
+            first_of_segment = at.tile;
+        }
+
+        issue(stage == 0 ? S::STAGES - 1 : stage - 1);
+        cp_async_wait<S::STAGES - 1>();
+        __syncwarp();
+
+        const int v0 = at.tile * TILE + warp * KEYS;  // the unit's first key number
+        const int n = at.keys.count();
+        if (v0 < n) {  // warp-uniform
+            bad |= (bad_units >> stage) & 1u;
+            const uint32_t ks = ring + stage * S::UNIT;
+            const uint32_t vs = ks + KEYS * S::ROW;
+            float s[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+            float lv[2][2];  // int8: log2 of the values' scales, for this lane's 4 keys
+            if (!INT8) {
+#pragma unroll
+                for (int kk = 0; kk < DIM / 16; ++kk) {
+                    uint32_t kb[4];
+                    ldmatrix_x4(kb, ks + chunk_at<INT8, DIM, false>((lane & 7) + ((lane >> 4) << 3),
+                                                                   2 * kk + ((lane >> 3) & 1)));
+                    mma_16816<M>(s[0], qa[kk], kb[0], kb[1]);
+                    mma_16816<M>(s[1], qa[kk], kb[2], kb[3]);
+                }
+            } else {
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                    for (int hf = 0; hf < DIM / 64; ++hf) {
+                        const uint4 raw = lds128(ks + chunk_at<INT8, DIM, false>(nt * 8 + g, 4 * hf + t));
+                        const uint32_t w[4] = {raw.x ^ 0x80808080u, raw.y ^ 0x80808080u, raw.z ^ 0x80808080u,
+                                               raw.w ^ 0x80808080u};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            mma_16816<M>(s[nt], qa[4 * hf + i], half2_of(w[i], 0x4140), half2_of(w[i], 0x4342));
+                    }
+            }
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+                float2 kscale = make_float2(1.0f, 1.0f);
+                if (INT8) {
+                    const uint32_t sc = vs + KEYS * S::ROW + (nt * 8 + 2 * t) * 4;
+                    const uint2 a = lds64(sc), b = lds64(sc + KEYS * 4);
+                    kscale = make_float2(__uint_as_float(a.x), __uint_as_float(a.y));
+                    lv[nt][0] = fast_log2(__uint_as_float(b.x));
+                    lv[nt][1] = fast_log2(__uint_as_float(b.y));
+                }
+                const int v = v0 + nt * 8 + 2 * t;
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    // scores in units of log2; keys past the end out
+                    const float a = INT8 ? s[nt][2 * r] * kscale.x : s[nt][2 * r];
+                    const float b = INT8 ? s[nt][2 * r + 1] * kscale.y : s[nt][2 * r + 1];
+                    s[nt][2 * r] = v < n ? a * c_row[r] : -INFINITY;
+                    s[nt][2 * r + 1] = v + 1 < n ? b * c_row[r] : -INFINITY;
+                }
+            }
+            float ref[2], refv[2], keep[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                float top = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const float m2 = fmaxf(m[r], top);
+                ref[r] = m2 == -INFINITY ? 0.0f : m2;
+                const float shrink = fast_exp2(m[r] - ref[r]);
+                l[r] *= shrink;
+                m[r] = m2;
+                if (INT8) {
+                    float tv = fmaxf(fmaxf(s[0][2 * r] + lv[0][0], s[0][2 * r + 1] + lv[0][1]),
+                                     fmaxf(s[1][2 * r] + lv[1][0], s[1][2 * r + 1] + lv[1][1]));
+                    tv = fmaxf(tv, __shfl_xor_sync(0xffffffffu, tv, 1));
+                    tv = fmaxf(tv, __shfl_xor_sync(0xffffffffu, tv, 2));
+                    const float mv2 = fmaxf(mv[r], tv);
+                    refv[r] = mv2 == -INFINITY ? 0.0f : mv2;
+                    keep[r] = fast_exp2(mv[r] - refv[r]);
+                    mv[r] = mv2;
+                } else {
+                    keep[r] = shrink;
+                }
+            }
+            uint32_t pa[4];
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float p0 = fast_exp2(s[nt][2 * r] - ref[r]), p1 = fast_exp2(s[nt][2 * r + 1] - ref[r]);
+                    l[r] += p0 + p1;
+                    if (INT8)
+                        pa[2 * nt + r] = Fp16::pack2(fast_exp2(s[nt][2 * r] + lv[nt][0] - refv[r]),
+                                                     fast_exp2(s[nt][2 * r + 1] + lv[nt][1] - refv[r]));
+                    else
+                        pa[2 * nt + r] = M::pack2(p0, p1);
+                }
+            if (__any_sync(0xffffffffu, keep[0] != 1.0f || keep[1] != 1.0f))
+#pragma unroll
+                for (int e = 0; e < DIM / 8; ++e) {
+                    o[e][0] *= keep[0], o[e][1] *= keep[0];
+                    o[e][2] *= keep[1], o[e][3] *= keep[1];
+                }
+            if (!INT8) {
+#pragma unroll
+                for (int ee = 0; ee < DIM / 16; ++ee) {
+                    uint32_t vb[4];
+                    ldmatrix_x4_trans(vb, vs + chunk_at<INT8, DIM, true>((lane & 7) + (((lane >> 3) & 1) << 3),
+                                                                        2 * ee + (lane >> 4)));
+                    mma_16816<M>(o[2 * ee], pa, vb[0], vb[1]);
+                    mma_16816<M>(o[2 * ee + 1], pa, vb[2], vb[3]);
+                }
+            } else {
+                // this lane's 4 keys (2t, 2t+1, 2t+8, 2t+9), values (DIM/8) g .. (DIM/8) (g+1) - 1
+                constexpr int WORDS = DIM / 32;
+                uint32_t w[4][WORDS];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = 2 * t + (i & 1) + 8 * (i >> 1);
+                    if (DIM == 128) {
+                        const uint4 x = lds128(vs + chunk_at<INT8, DIM, true>(r, g));
+                        w[i][0] = x.x, w[i][1] = x.y, w[i][WORDS - 2] = x.z, w[i][WORDS - 1] = x.w;
+                    } else {
+                        const uint2 x = lds64(vs + chunk_at<INT8, DIM, true>(r, g >> 1) + 8 * (g & 1));
+                        w[i][0] = x.x, w[i][1] = x.y;
+                    }
+#pragma unroll
+                    for (int k = 0; k < WORDS; ++k)
+                        w[i][k] ^= 0x80808080u;
+                }
+#pragma unroll
+                for (int k = 0; k < WORDS; ++k) {
+                    const uint32_t lo01 = __byte_perm(w[0][k], w[1][k], 0x5140), hi01 = __byte_perm(w[0][k], w[1][k], 0x7362);
+                    const uint32_t lo23 = __byte_perm(w[2][k], w[3][k], 0x5140), hi23 = __byte_perm(w[2][k], w[3][k], 0x7362);
+                    mma_16816<M>(o[4 * k], pa, half2_of(lo01, 0x4140), half2_of(lo23, 0x4140));
+                    mma_16816<M>(o[4 * k + 1], pa, half2_of(lo01, 0x4342), half2_of(lo23, 0x4342));
+                    mma_16816<M>(o[4 * k + 2], pa, half2_of(hi01, 0x4140), half2_of(hi23, 0x4140));
+                    mma_16816<M>(o[4 * k + 3], pa, half2_of(hi01, 0x4342), half2_of(hi23, 0x4342));
+                }
+            }
+        }
+        __syncwarp();
+        stage = stage + 1 == S::STAGES ? 0 : stage + 1;
+
+        const bool range_end = at.left == 1;
+        const bool segment_end = at.tile + 1 == at.tiles;
+        if (segment_end || range_end) {
+            // ---- join the four warps, then leave the segment's output or this block's part of it
+            const int hk = at.sub / qtiles, qt = at.sub - hk * qtiles;
+            const int h0 = hk * group + qt * HEADS;
+            const int heads = min(HEADS, group - qt * HEADS);
+            if (bad && lane == 0)
+                atomicOr(err, kErrIndex);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+                if (t == 0)
+                    maxsum[warp * HEADS + g + 8 * r] = make_float2(m[r], bad ? NAN : l[r]);
+            }
+            __syncthreads();
+            float f[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                float top = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < WARPS; ++w)
+                    top = fmaxf(top, maxsum[w * HEADS + g + 8 * r].x);
+                const float from = INT8 ? mv[r] : m[r];  // what the sums o are relative to
+                f[r] = from == -INFINITY ? 0.0f : fast_exp2(from - top);
+            }
+            for (int w = 0; w < WARPS; ++w) {
+                if (warp == w)
+#pragma unroll
+                    for (int e = 0; e < DIM / 8; ++e)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int d = INT8 ? DIM / 8 * (2 * t + (i & 1)) + e : 8 * e + 2 * t + (i & 1);
+                            float* dst = joined + (g + 8 * (i >> 1)) * S::LD + d;
+                            const float x = o[e][i] * f[i >> 1];
+                            *dst = w == 0 ? x : *dst + x;
+                        }
+                __syncthreads();
+            }
+            const bool whole = segment_end && first_of_segment == 0;
+            float* part = static_cast<float*>(p.workspace) + (2 * (int64_t)blockIdx.x + piece) * S::PART;
+            for (int i = threadIdx.x; i < heads * (DIM / 4); i += WARPS * 32) {
+                const int row = i / (DIM / 4), d = i % (DIM / 4) * 4;
+                const float4 x = *reinterpret_cast<const float4*>(joined + row * S::LD + d);
+                if (!whole) {
+                    *reinterpret_cast<float4*>(part + row * DIM + d) = x;
+                    continue;
+                }
+                float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+                for (int w = 0; w < WARPS; ++w)
+                    top = fmaxf(top, maxsum[w * HEADS + row].x);
+#pragma unroll
+                for (int w = 0; w < WARPS; ++w) {
+                    const float2 ms = maxsum[w * HEADS + row];
+                    sum += ms.x == -INFINITY ? (ms.y != ms.y ? ms.y : 0.0f) : ms.y * fast_exp2(ms.x - top);
+                }
+                const int64_t at_row = at.b * p.q_heads + h0 + row;
+                *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + at_row * DIM + d) =
+                    make_uint2(E::pack2(x.x / sum, x.y / sum), E::pack2(x.z / sum, x.w / sum));
+                if (d == 0 && p.lse != nullptr)
+                    p.lse[at_row] = (top + log2f(sum)) * kLn2;
+            }
+            if (!whole) {
+                for (int row = threadIdx.x; row < heads; row += WARPS * 32) {
+                    float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+                    for (int w = 0; w < WARPS; ++w)
+                        top = fmaxf(top, maxsum[w * HEADS + row].x);
+#pragma unroll
+                    for (int w = 0; w < WARPS; ++w) {
+                        const float2 ms = maxsum[w * HEADS + row];
+                        sum += ms.x == -INFINITY ? (ms.y != ms.y ? ms.y : 0.0f) : ms.y * fast_exp2(ms.x - top);
+                    }
+                    reinterpret_cast<float2*>(part + HEADS * DIM)[row] = make_float2(top, sum);
+                }
+                ++piece;
+            }
+            if (range_end)
+                break;
+            __syncthreads();  // the join's buffers are free again
+            fresh = true;
+        }
+        at.next(L);
+    }
+    cp_async_wait<0>();
+    griddep_launch_dependents();
+}
+
+// Adds up the partial sums of the segments that blocks share: one block per (sequence, query
+// head), its 4 warps every fourth part each, then the four together.
+template <class E, int DIM>
+__global__ void __launch_bounds__(128) join_kernel(const PagedAttention p, int64_t C)
+{
+    using T = typename E::T;
+    griddep_wait();
+    constexpr size_t PART = (size_t)HEADS * (DIM + 2);
+    __shared__ float4 sums[4][32];
+    __shared__ float2 maxsum[4];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t b = blockIdx.x / p.q_heads;
+    const int h = (int)(blockIdx.x - b * p.q_heads);
+    const int group = p.q_heads / p.cache.heads;
+    const int qtiles = (group + HEADS - 1) / HEADS;
+    Lengths L{p.seq_lens, p.max_blocks * p.cache.page_size, p.window, p.sinks, p.cache.heads * qtiles};
+    const int tiles = L.tiles(b);
+    if (tiles == 0)
+        return;  // the first kernel wrote it
+    const int64_t total = tiles_before(L, p.batch);
+    C = min(C, total);
+    const int in_group = h % group;
+    const int64_t sub = h / group * qtiles + in_group / HEADS;
+    const int row = in_group % HEADS;
+    const int64_t t0 = tiles_before(L, b) + sub * tiles, t1 = t0 + tiles;
+    // block c holds tile t: c = floor(((t + 1) C - 1) / T)
+    const int64_t c0 = ((t0 + 1) * C - 1) / total, c1 = (t1 * C - 1) / total;
+    if (c0 == c1)
+        return;  // one block held the whole segment and wrote the output
+    const float* ws = static_cast<const float*>(p.workspace);
+    float m = -INFINITY, l = 0.0f;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int64_t c = c0 + warp; c <= c1; c += 4) {
+        // Slot 0 holds the first partial that block c left.  That is this segment, unless c = c0
+        // began inside an earlier segment and had to leave that one first.
+        int slot = 0;
+        if (c == c0) {
+            const int64_t begin = first_tile(c, C, total);
+            if (begin < t0) {
+                // an earlier piece was partial exactly if the block began inside its segment
+                int64_t before;
+                const int64_t bb = sequence_at(L, p.batch, begin, &before);
+                const int bt = L.tiles(bb);
+                slot = (begin - before) % bt != 0 ? 1 : 0;
+            }
+        }
+        const float* part = ws + (2 * c + slot) * PART;
+        const float2 ms = __ldcg(reinterpret_cast<const float2*>(part + HEADS * DIM) + row);
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (lane < DIM / 4)
+            x = __ldcg(reinterpret_cast<const float4*>(part + row * DIM) + lane);
+        const float m2 = fmaxf(m, ms.x);
+        const float ref = m2 == -INFINITY ? 0.0f : m2;
+        const float a = fast_exp2(m - ref), f = fast_exp2(ms.x - ref);
+        l = l * a + ms.y * f;
+        acc.x = acc.x * a + x.x * f, acc.y = acc.y * a + x.y * f;
+        acc.z = acc.z * a + x.z * f, acc.w = acc.w * a + x.w * f;
+        m = m2;
+    }
+    sums[warp][lane] = acc;
+    if (lane == 0)
+        maxsum[warp] = make_float2(m, l);
+    __syncthreads();
+    if (warp != 0)
+        return;
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+        top = fmaxf(top, maxsum[w].x);
+    const float ref = top == -INFINITY ? 0.0f : top;
+    float sum = 0.0f;
+    acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const float f = fast_exp2(maxsum[w].x - ref);
+        const float4 x = sums[w][lane];
+        sum += maxsum[w].y * f;
+        acc.x += x.x * f, acc.y += x.y * f, acc.z += x.z * f, acc.w += x.w * f;
+    }
+    const int64_t at_row = b * p.q_heads + h;
+    if (lane < DIM / 4)
+        *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + at_row * DIM + lane * 4) =
+            make_uint2(E::pack2(acc.x / sum, acc.y / sum), E::pack2(acc.z / sum, acc.w / sum));
+    if (lane == 0 && p.lse != nullptr)
+        p.lse[at_row] = (top + log2f(sum)) * kLn2;
+}
+
+constexpr int64_t kMostBlocks = 152 * kBlocksPerSm;  // of any device this library runs on
+
+template <class E, bool INT8, int DIM>
+cudaError_t launch(const PagedAttention& p, const DeviceInfo& dev, unsigned int* err, cudaStream_t s)
+{
+    using S = Shape<INT8, DIM>;
+    // a kernel attribute belongs to the context it was set in: set once per context
+    static ContextCache<int> cache;
+    int done = 0;
+    cudaError_t e = cache.get(&done, [](int* d) {
+        *d = 1;
+        return cudaFuncSetAttribute(paged_kernel<E, INT8, DIM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)S::SMEM);
+    });
+    if (e != cudaSuccess)
+        return e;
+    const int group = p.q_heads / p.cache.heads;
+    const int64_t segments = p.batch * p.cache.heads * ((group + HEADS - 1) / HEADS);
+    int64_t longest = p.max_blocks * p.cache.page_size;
+    if (p.window > 0 && p.sinks < longest)
+        longest = std::min(longest, p.window + p.sinks);
+    const int64_t tiles = (longest + TILE - 1) / TILE;
+    const bool split = tiles > kWholeTiles;
+    const int64_t blocks =
+        split ? std::min<int64_t>({kMostBlocks, (int64_t)dev.sm_count * kBlocksPerSm, segments * tiles}) : segments;
+    e = launch_pdl(paged_kernel<E, INT8, DIM>, dim3((unsigned)blocks), dim3(WARPS * 32), S::SMEM, s, p, blocks, split,
+                   err);
+    if (e == cudaSuccess && split)
+        e = launch_pdl(join_kernel<E, DIM>, dim3((unsigned)(p.batch * p.q_heads)), dim3(128), 0, s, p, blocks);
+    return e;
 }
 
 template <int DIM>
-cudaError_t by_type(const PagedAttention& p, unsigned int* err, cudaStream_t s)
+cudaError_t by_type(const PagedAttention& p, const DeviceInfo& dev, unsigned int* err, cudaStream_t s)
 {
     if (p.cache.dtype == CK_KV_INT8)
-        return p.f16 ? launch<Fp16, true, DIM>(p, err, s) : launch<Bf16, true, DIM>(p, err, s);
-    return p.f16 ? launch<Fp16, false, DIM>(p, err, s) : launch<Bf16, false, DIM>(p, err, s);
+        return p.f16 ? launch<Fp16, true, DIM>(p, dev, err, s) : launch<Bf16, true, DIM>(p, dev, err, s);
+    return p.f16 ? launch<Fp16, false, DIM>(p, dev, err, s) : launch<Bf16, false, DIM>(p, dev, err, s);
 }
 
 }  // namespace
 
 size_t paged_attention_workspace(int64_t batch, int q_heads, int kv_heads, int dim)
 {
-    (void)batch, (void)q_heads, (void)kv_heads, (void)dim;
-    return 16;
+    (void)batch, (void)q_heads, (void)kv_heads;
+    return (size_t)kMostBlocks * 2 * HEADS * (dim + 2) * sizeof(float);
 }
 
 cudaError_t launch_paged_attention(const PagedAttention& p, const DeviceInfo& dev, cudaStream_t s)
 {
-    (void)dev;
     unsigned int* err = nullptr;
     cudaError_t e = device_error_ptr(&err);
     if (e != cudaSuccess)
         return e;
-    return p.cache.dim == 64 ? by_type<64>(p, err, s) : by_type<128>(p, err, s);
+    return p.cache.dim == 64 ? by_type<64>(p, dev, err, s) : by_type<128>(p, dev, err, s);
 }
 
 }  // namespace ck
