@@ -44,19 +44,27 @@ template <class E>
 __device__ __forceinline__ uint32_t codes_of(uint32_t word, int i)
 {
     // the pair k = 2 i, 2 i + 1 of the word's eight: code - 8 in two 16-bit floats
-    const uint32_t u = ((word >> (4 * i)) & 0x000F000Fu) | (std::is_same<E, Bf16>::value ? 0x43004300u : 0x64006400u);
     if (std::is_same<E, Bf16>::value) {
+        const uint32_t u = ((word >> (4 * i)) & 0x000F000Fu) | 0x43004300u;  // 128 + code
         const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u), __float2bfloat162_rn(136.0f));
         return *reinterpret_cast<const uint32_t*>(&v);
     }
-    const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&u), __float2half2_rn(1032.0f));
+    const uint32_t w = i < 2 ? word : word >> 8;
+    if ((i & 1) == 0) {
+        const uint32_t u = (w & 0x000F000Fu) | 0x64006400u;  // 1024 + code
+        const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&u), __float2half2_rn(1032.0f));
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+    const uint32_t u = (w & 0x00F000F0u) | 0x64006400u;  // 1024 + 16 code, exact like the rest
+    const __half2 v = __hfma2(*reinterpret_cast<const __half2*>(&u), __float2half2_rn(0.0625f), __float2half2_rn(-72.0f));
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 template <int RT>
 constexpr int kUnit = 16 * RT * (W_LD + 8);  // codes, then 8 bytes of scales a row
 
-template <class E, int RT, int MT>
+// PER_CHUNK: scales of a row in a chunk (4, 2 or 1 for groups of 32, 64, and 128 or 256)
+template <class E, int RT, int MT, int PER_CHUNK>
 __global__ void __launch_bounds__(WARPS * 32) int4_kernel(const Int4Linear p)
 {
     using T = typename E::T;
@@ -70,55 +78,69 @@ __global__ void __launch_bounds__(WARPS * 32) int4_kernel(const Int4Linear p)
     const int chunks = (int)(p.K / CHUNK);
     const int c0 = (int)((int64_t)warp * chunks / WARPS), c1 = (int)((int64_t)(warp + 1) * chunks / WARPS);
     const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * STAGES * kUnit<RT>);
-    const int log_group = 31 - __clz(p.group);  // a power of two
-    const int64_t groups = p.K >> log_group;
-    const int per_chunk = p.group >= CHUNK ? 1 : CHUNK >> log_group;  // scales of a row in a chunk
+    const int64_t groups = p.K / p.group;
+    const int log_chunks = p.group == 256 ? 1 : 0;  // chunks a group spans, PER_CHUNK == 1
 
+    // where this lane's copies come from: row and 16 bytes of the codes, row of the scales
+    const uint8_t* w_src[2 * RT];
+    bool w_in[2 * RT];
+#pragma unroll
+    for (int i = 0; i < 2 * RT; ++i) {  // 8 rows of 4 x 16 bytes an instruction
+        const int64_t n = n0 + i * 8 + g;
+        w_in[i] = n < p.N;
+        w_src[i] = reinterpret_cast<const uint8_t*>(p.w4) + (w_in[i] ? n : 0) * (p.K / 2) + t * 16;
+    }
+    static_assert(RT <= 2, "one lane per scale row");
+    const int64_t sn = n0 + lane;
+    const bool s_in = lane < 16 * RT && sn < p.N;
+    const int64_t s_first = (s_in ? sn : 0) * groups;  // the row's first scale
+    const __nv_bfloat16* s_src = static_cast<const __nv_bfloat16*>(p.w_scale) + s_first;
+    const int s_odd = (int)(s_first & 1);
     auto issue = [&](int c, int stage) {
         if (c < c1) {
-            const uint32_t w = ring + stage * kUnit<RT>;
-            const uint32_t sc = w + 16 * RT * W_LD;
+            const uint32_t w = ring + stage * kUnit<RT> + g * W_LD + t * 16;
+            const uint32_t sc = ring + stage * kUnit<RT> + 16 * RT * W_LD + lane * 8;
 #pragma unroll
-            for (int i = 0; i < 2 * RT; ++i) {  // 8 rows of 4 x 16 bytes an instruction
-                const int r = i * 8 + (lane >> 2);
-                const int64_t n = n0 + r;
-                cp_async16(w + r * W_LD + (lane & 3) * 16, p.w4 + (n < p.N ? n : 0) * (p.K / 8) + c * 16 + (lane & 3) * 4,
-                           n < p.N);
-            }
-#pragma unroll
-            for (int i = 0; i < (16 * RT + 31) / 32; ++i) {
-                const int r = i * 32 + lane;
-                const int64_t n = n0 + r;
-                if (r < 16 * RT) {
-                    // the row's scales of this chunk: 8 bytes, 4, or the aligned 4 that hold the one
-                    const int64_t e = (n < p.N ? n : 0) * groups + ((c * (int64_t)CHUNK) >> log_group);
-                    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.w_scale);
-                    if (per_chunk == 4)
-                        cp_async_small<8>(sc + r * 8, src + e, n < p.N);
-                    else
-                        cp_async_small<4>(sc + r * 8, src + (e & ~1ll), n < p.N);
-                }
+            for (int i = 0; i < 2 * RT; ++i)
+                cp_async16(w + i * 8 * W_LD, w_src[i] + c * 64, w_in[i]);
+            // the row's scales of this chunk: 8 bytes, 4, or the aligned 4 that hold the one
+            if (lane < 16 * RT) {
+                if (PER_CHUNK == 4)
+                    cp_async_small<8>(sc, s_src + 4 * c, s_in);
+                else if (PER_CHUNK == 2)
+                    cp_async_small<4>(sc, s_src + 2 * c, s_in);
+                else
+                    cp_async_small<4>(sc, s_src + ((s_odd + (c >> log_chunks)) & ~1) - s_odd, s_in);
             }
         }
         cp_async_commit();
     };
-    // this lane's part of a chunk of x: row g of each tile, k = 32 j + 8 t .. + 7 (rows past M: 0)
-    uint4 ahead[4][MT];
+    // this lane's part of 32 k of x: row g of each tile, k = 8 t .. + 7 (rows past M: 0)
+    uint4 b[4][MT];
     const T* xl = static_cast<const T*>(p.x) + (m0 + g) * p.K + t * 8;
-    auto load_x = [&](int c) {
+    auto load_x = [&](int c, int j) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-                ahead[j][mt] = 8 * mt + g < rows
-                                   ? __ldg(reinterpret_cast<const uint4*>(xl + 8 * mt * p.K + (int64_t)c * CHUNK + j * 32))
-                                   : make_uint4(0u, 0u, 0u, 0u);
+        for (int mt = 0; mt < MT; ++mt)
+            if (8 * mt + g < rows)
+                b[j][mt] = __ldg(reinterpret_cast<const uint4*>(xl + 8 * mt * p.K + c * CHUNK + j * 32));
     };
 #pragma unroll
     for (int s = 0; s < STAGES - 1; ++s)
         issue(c0 + s, s);
-    if (c0 < c1)
-        load_x(c0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+            b[j][mt] = make_uint4(0u, 0u, 0u, 0u);
+        if (c0 < c1)
+            load_x(c0, j);
+    }
+    int row_odd[RT][2];  // PER_CHUNK == 1: whether the row's first scale lies in an upper half
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            row_odd[rt][h] = (int)(((n0 + 16 * rt + 8 * h + g) * groups) & 1);
 
     float sum[RT][MT][4] = {};
     float acc[RT][MT][4] = {};
@@ -127,22 +149,14 @@ __global__ void __launch_bounds__(WARPS * 32) int4_kernel(const Int4Linear p)
         issue(c + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1);
         cp_async_wait<STAGES - 1>();
         __syncwarp();
-        const uint32_t w = ring + stage * kUnit<RT>;
-        const uint32_t sc = w + 16 * RT * W_LD;
-        uint4 b[4][MT];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-                b[j][mt] = ahead[j][mt];
-        if (c + 1 < c1)
-            load_x(c + 1);
+        const uint32_t w = ring + stage * kUnit<RT> + g * W_LD + t * 4;
+        const uint32_t sc = ring + stage * kUnit<RT> + 16 * RT * W_LD + g * 8;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {  // 32 k: word 4 j + t of a row is this lane's
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
-                const uint32_t lo = lds32(w + (16 * rt + g) * W_LD + j * 16 + t * 4);
-                const uint32_t hi = lds32(w + (16 * rt + 8 + g) * W_LD + j * 16 + t * 4);
+                const uint32_t lo = lds32(w + 16 * rt * W_LD + j * 16);
+                const uint32_t hi = lds32(w + (16 * rt + 8) * W_LD + j * 16);
                 const uint32_t a0[4] = {codes_of<E>(lo, 0), codes_of<E>(hi, 0), codes_of<E>(lo, 1), codes_of<E>(hi, 1)};
                 const uint32_t a1[4] = {codes_of<E>(lo, 2), codes_of<E>(hi, 2), codes_of<E>(lo, 3), codes_of<E>(hi, 3)};
 #pragma unroll
@@ -151,18 +165,18 @@ __global__ void __launch_bounds__(WARPS * 32) int4_kernel(const Int4Linear p)
                     mma_16816<E>(acc[rt][mt], a1, b[j][mt].z, b[j][mt].w);
                 }
             }
+            if (c + 1 < c1)
+                load_x(c + 1, j);  // the registers are free: the next chunk's
             // the end of a group: scale its sums
-            if (j == 3 || per_chunk == 4 || (per_chunk == 2 && j == 1)) {
+            if ((j + 1) % (4 / PER_CHUNK) == 0) {
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const int r = 16 * rt + 8 * h + g;
-                        int e = per_chunk == 4 ? j : per_chunk == 2 ? j >> 1 : 0;
-                        if (per_chunk == 1)
-                            e = (int)(((n0 + r) * groups + ((c * (int64_t)CHUNK) >> log_group)) & 1);
-                        const uint32_t pair = lds32(sc + r * 8 + (e >> 1) * 4);
-                        const float s = __uint_as_float((e & 1) ? pair & 0xFFFF0000u : pair << 16);
+                        const int e = PER_CHUNK == 4 ? j : PER_CHUNK == 2 ? j >> 1 : 0;
+                        const uint32_t pair = lds32(sc + (16 * rt + 8 * h) * 8 + (e >> 1) * 4);
+                        const bool upper = PER_CHUNK == 1 ? (row_odd[rt][h] + (c >> log_chunks)) & 1 : e & 1;
+                        const float s = __uint_as_float(upper ? pair & 0xFFFF0000u : pair << 16);
 #pragma unroll
                         for (int mt = 0; mt < MT; ++mt) {
                             sum[rt][mt][2 * h] = fmaf(acc[rt][mt][2 * h], s, sum[rt][mt][2 * h]);
@@ -271,7 +285,7 @@ __global__ void __launch_bounds__(256) int4_pack_kernel(const int8_t* codes, int
 
 namespace {
 
-template <class E, int RT, int MT>
+template <class E, int RT, int MT, int PER_CHUNK>
 cudaError_t launch(const Int4Linear& p, cudaStream_t s)
 {
     constexpr size_t smem = std::max((size_t)WARPS * STAGES * kUnit<RT>,         // the rings
@@ -281,23 +295,29 @@ cudaError_t launch(const Int4Linear& p, cudaStream_t s)
     int done = 0;
     cudaError_t e = cache.get(&done, [](int* d) {
         *d = 1;
-        return cudaFuncSetAttribute(int4_kernel<E, RT, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(int4_kernel<E, RT, MT, PER_CHUNK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     (int)smem);
     });
     if (e != cudaSuccess)
         return e;
     const dim3 grid((unsigned)((p.N + 16 * RT - 1) / (16 * RT)), (unsigned)((p.M + 8 * MT - 1) / (8 * MT)));
-    return launch_pdl(int4_kernel<E, RT, MT>, grid, dim3(WARPS * 32), smem, s, p);
+    return launch_pdl(int4_kernel<E, RT, MT, PER_CHUNK>, grid, dim3(WARPS * 32), smem, s, p);
+}
+
+template <class E, int RT, int MT>
+cudaError_t by_group(const Int4Linear& p, cudaStream_t s)
+{
+    return p.group == 32 ? launch<E, RT, MT, 4>(p, s) : p.group == 64 ? launch<E, RT, MT, 2>(p, s) : launch<E, RT, MT, 1>(p, s);
 }
 
 template <class E>
 cudaError_t by_rows(const Int4Linear& p, cudaStream_t s)
 {
     if (p.M <= 8)
-        return launch<E, 1, 1>(p, s);
+        return by_group<E, 1, 1>(p, s);
     if (p.M <= 16)
-        return launch<E, 2, 2>(p, s);
-    return launch<E, 2, 4>(p, s);
+        return by_group<E, 2, 2>(p, s);
+    return by_group<E, 2, 4>(p, s);
 }
 
 }  // namespace

@@ -7,7 +7,7 @@
 // Bound: HBM.  Every visible key and value row is read once per kv head, for the up to 16
 // query heads that share it; nothing else is read more than once.
 //
-// Work.  A segment is one (sequence, kv head, 16 query heads); its visible keys, numbered
+// Work.  A segment is one (sequence, kv head, 8 NT query heads); its visible keys, numbered
 // through without the hidden ones, are cut into tiles of 64.  All segments' tiles in a row are
 // shared out evenly: block c of C takes tiles [c T / C, (c + 1) T / C), whatever the lengths
 // (each block sums the lengths up itself, so nothing depends on the host knowing them and a
@@ -19,9 +19,12 @@
 //
 // Inside a block each of the 4 warps takes 16 keys of a tile on its own: its own ring of
 // asynchronous copies (no block-wide barrier while tiles stream), its own running maximum and
-// sum; the four are joined once per segment.  Scores and weighted values run on the 16x8x16
-// matrix instruction with the query heads as its 16 rows; the weights go from the first
-// product's accumulators straight into the second's operand registers.
+// sum; the four are joined once per segment.  Both products run on the 16x8x16 matrix
+// instruction with keys (then value columns) as its 16 rows and the query heads as its 8
+// columns -- S^T = K Q^T, O^T = V^T P^T --, so that the usual 1 to 8 heads of a group waste
+// little of the softmax arithmetic (heads as rows, 16 of them: 646 instead of about 400
+// instructions per 16 keys on int8 rows, which were bound by that).  Between the two products
+// the weights stay in registers: two 8x8 transposes.
 //
 // int8 rows: a code is exact in fp16, so both products run in fp16: the query scaled by the
 // power of two that brings its largest value into [1, 2) (undone in the fp32 score), and the
@@ -47,17 +50,19 @@ namespace {
 constexpr int WARPS = 4;
 constexpr int KEYS = 16;              // keys of one warp's unit
 constexpr int TILE = WARPS * KEYS;    // keys of a block's tile
-constexpr int HEADS = 16;             // query heads of a segment
 constexpr int kWholeTiles = 8;        // segments of at most this many tiles are not split
-constexpr int kBlocksPerSm = 2;
 
-template <bool INT8, int DIM>
+// NT: tiles of 8 query heads that a segment holds (1, or 2 where a group has more than 8)
+template <bool INT8, int DIM, int NT>
 struct Shape {
+    static constexpr int HEADS = 8 * NT;
     static constexpr int ROW = DIM * (INT8 ? 1 : 2);        // bytes of a row
     static constexpr int SCALES = INT8 ? 2 * KEYS * 4 : 0;  // k scales, v scales
     static constexpr int UNIT = 2 * KEYS * ROW + SCALES;
-    // ring depth: about 24 KB a warp, so that two blocks an SM keep up to ~190 KB in flight
-    static constexpr int STAGES = INT8 ? (DIM == 128 ? 6 : 8) : (DIM == 128 ? 3 : 6);
+    // About 200 KB of rings an SM.  16-bit rows: two blocks; int8 rows, whose arithmetic per
+    // byte is twice that, four (two with 16 heads, which hold twice the sums).
+    static constexpr int BLOCKS = INT8 && NT == 1 ? 4 : 2;
+    static constexpr int STAGES = 24576 * 2 / BLOCKS / UNIT > 8 ? 8 : 24576 * 2 / BLOCKS / (UNIT - SCALES);
     static constexpr int LD = DIM + 4;                       // joined sums: floats per head
     static constexpr size_t RING = (size_t)WARPS * STAGES * UNIT;
     static constexpr size_t SMEM = RING + HEADS * LD * 4 + WARPS * HEADS * 8;
@@ -166,7 +171,7 @@ __device__ __forceinline__ uint32_t half2_of(uint32_t biased_pair_bytes, uint32_
 template <bool INT8, int DIM, bool V>
 __device__ __forceinline__ uint32_t chunk_at(int r, int c)
 {
-    constexpr int CHUNKS = Shape<INT8, DIM>::ROW / 16;
+    constexpr int CHUNKS = Shape<INT8, DIM, 1>::ROW / 16;
     int p;
     if (!INT8)
         p = c ^ (r & 7);  // ldmatrix: one chunk of 8 neighbouring rows
@@ -174,16 +179,17 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c)
         p = V ? c ^ (((r >> 1) & 3) << 1) : c ^ ((r & 1) << 2);
     else
         p = V ? c ^ ((r >> 1) & 3) : c;
-    return (uint32_t)(r * Shape<INT8, DIM>::ROW + p * 16);
+    return (uint32_t)(r * Shape<INT8, DIM, 1>::ROW + p * 16);
 }
 
-template <class E, bool INT8, int DIM>
-__global__ void __launch_bounds__(WARPS * 32, kBlocksPerSm)
+template <class E, bool INT8, int DIM, int NT>
+__global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
     paged_kernel(const PagedAttention p, int64_t C, bool split, unsigned int* err)
 {
-    using S = Shape<INT8, DIM>;
+    using S = Shape<INT8, DIM, NT>;
     using T = typename E::T;
     using M = typename std::conditional<INT8, Fp16, E>::type;  // the products' type
+    constexpr int HEADS = S::HEADS;
     extern __shared__ __align__(128) uint8_t smem[];
     griddep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -288,10 +294,11 @@ __global__ void __launch_bounds__(WARPS * 32, kBlocksPerSm)
     for (int s = 0; s < S::STAGES - 1; ++s)
         issue(s);
 
-    uint32_t qa[DIM / 16][4];
-    float o[DIM / 8][4];
-    float m[2], l[2], mv[2];  // rows g and g + 8: maximum and sum of weights; int8: the values' maximum
-    float c_row[2];           // score factor, in units of log2
+    uint32_t qb[NT][DIM / 16][2];  // queries of head 8 nt + g
+    float o[NT][DIM / 16][4];      // sums of heads 8 nt + 2t, + 1 (columns), two value rows
+    float m[NT][2], l[NT][2];      // of those heads: maximum, sum of weights
+    float mv[NT][2];               // int8: the values' maximum
+    float c_head[NT][2];           // score factor of those heads, in units of log2
     bool bad = false;
     bool fresh = true;
     int first_of_segment = 0;  // the block's first tile of the segment
@@ -306,25 +313,26 @@ __global__ void __launch_bounds__(WARPS * 32, kBlocksPerSm)
             const T* q = static_cast<const T*>(p.q) + at.b * p.q_stride + (int64_t)h0 * DIM;
             const float c = p.scale * kLog2e;
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int row = g + 8 * r;
-                c_row[r] = c;
+            for (int nt = 0; nt < NT; ++nt) {
+                const int head = 8 * nt + g;
+                const T* qh = q + (int64_t)head * DIM;
                 if (!INT8) {
 #pragma unroll
                     for (int kk = 0; kk < DIM / 16; ++kk) {
-                        const uint32_t* src = reinterpret_cast<const uint32_t*>(q + (int64_t)row * DIM + 16 * kk + 2 * t);
-                        qa[kk][r] = row < heads ? __ldg(src) : 0u;
-                        qa[kk][2 + r] = row < heads ? __ldg(src + 4) : 0u;
+                        const uint32_t* src = reinterpret_cast<const uint32_t*>(qh + 16 * kk + 2 * t);
+                        qb[nt][kk][0] = head < heads ? __ldg(src) : 0u;
+                        qb[nt][kk][1] = head < heads ? __ldg(src + 4) : 0u;
                     }
+                    c_head[nt][0] = c_head[nt][1] = c;
                 } else {
                     // the int8 products' order: k-step kk, lane t <- d = 64 (kk / 4) + 16 t + 4 (kk % 4) ..
                     float v[DIM / 4];
                     float top = 0.0f;
 #pragma unroll
                     for (int kk = 0; kk < DIM / 16; ++kk) {
-                        const uint2 w = row < heads ? __ldg(reinterpret_cast<const uint2*>(
-                                                          q + (int64_t)row * DIM + 64 * (kk / 4) + 16 * t + 4 * (kk % 4)))
-                                                    : make_uint2(0u, 0u);
+                        const uint2 w = head < heads
+                                            ? __ldg(reinterpret_cast<const uint2*>(qh + 64 * (kk / 4) + 16 * t + 4 * (kk % 4)))
+                                            : make_uint2(0u, 0u);
                         const float2 a = E::to2(w.x), b = E::to2(w.y);
                         v[4 * kk] = a.x, v[4 * kk + 1] = a.y, v[4 * kk + 2] = b.x, v[4 * kk + 3] = b.y;
 #pragma unroll
@@ -334,19 +342,25 @@ __global__ void __launch_bounds__(WARPS * 32, kBlocksPerSm)
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
                     const int e = top > 0.0f && top < INFINITY ? ilogbf(top) : 0;
-                    c_row[r] = ldexpf(c, e);
 #pragma unroll
                     for (int kk = 0; kk < DIM / 16; ++kk) {
-                        qa[kk][r] = Fp16::pack2(ldexpf(v[4 * kk], -e), ldexpf(v[4 * kk + 1], -e));
-                        qa[kk][2 + r] = Fp16::pack2(ldexpf(v[4 * kk + 2], -e), ldexpf(v[4 * kk + 3], -e));
+                        qb[nt][kk][0] = Fp16::pack2(ldexpf(v[4 * kk], -e), ldexpf(v[4 * kk + 1], -e));
+                        qb[nt][kk][1] = Fp16::pack2(ldexpf(v[4 * kk + 2], -e), ldexpf(v[4 * kk + 3], -e));
                     }
-                }
-                m[r] = mv[r] = -INFINITY;
-                l[r] = 0.0f;
-            }
+                    const float ch = ldexpf(c, e);  // of head g: pass it to the lanes of its column
 #pragma unroll
-            for (int e = 0; e < DIM / 8; ++e)
-                o[e][0] = o[e][1] = o[e][2] = o[e][3] = 0.0f;
+                    for (int j = 0; j < 2; ++j)
+                        c_head[nt][j] = __shfl_sync(0xffffffffu, ch, (2 * t + j) * 4);
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    m[nt][j] = mv[nt][j] = -INFINITY;
+                    l[nt][j] = 0.0f;
+                }
+#pragma unroll
+                for (int e = 0; e < DIM / 16; ++e)
+                    o[nt][e][0] = o[nt][e][1] = o[nt][e][2] = o[nt][e][3] = 0.0f;
+            }
             bad = false;
             fresh = false;
             first_of_segment = at.tile;
@@ -362,104 +376,103 @@ __global__ void __launch_bounds__(WARPS * 32, kBlocksPerSm)
             bad |= (bad_units >> stage) & 1u;
             const uint32_t ks = ring + stage * S::UNIT;
             const uint32_t vs = ks + KEYS * S::ROW;
-            float s[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
-            float lv[2][2];  // int8: log2 of the values' scales, for this lane's 4 keys
+            // S^T: rows keys g, g + 8; columns heads 2t, 2t + 1 of each nt
+            float s[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
             if (!INT8) {
 #pragma unroll
                 for (int kk = 0; kk < DIM / 16; ++kk) {
-                    uint32_t kb[4];
-                    ldmatrix_x4(kb, ks + chunk_at<INT8, DIM, false>((lane & 7) + ((lane >> 4) << 3),
-                                                                   2 * kk + ((lane >> 3) & 1)));
-                    mma_16816<M>(s[0], qa[kk], kb[0], kb[1]);
-                    mma_16816<M>(s[1], qa[kk], kb[2], kb[3]);
+                    uint32_t ka[4];
+                    ldmatrix_x4(ka, ks + chunk_at<INT8, DIM, false>(lane & 15, 2 * kk + (lane >> 4)));
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma_16816<M>(s[nt], ka, qb[nt][kk][0], qb[nt][kk][1]);
                 }
             } else {
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
+                for (int hf = 0; hf < DIM / 64; ++hf) {
+                    const uint4 r0 = lds128(ks + chunk_at<INT8, DIM, false>(g, 4 * hf + t));
+                    const uint4 r1 = lds128(ks + chunk_at<INT8, DIM, false>(g + 8, 4 * hf + t));
+                    const uint32_t w0[4] = {r0.x, r0.y, r0.z, r0.w}, w1[4] = {r1.x, r1.y, r1.z, r1.w};
 #pragma unroll
-                    for (int hf = 0; hf < DIM / 64; ++hf) {
-                        const uint4 raw = lds128(ks + chunk_at<INT8, DIM, false>(nt * 8 + g, 4 * hf + t));
-                        const uint32_t w[4] = {raw.x ^ 0x80808080u, raw.y ^ 0x80808080u, raw.z ^ 0x80808080u,
-                                               raw.w ^ 0x80808080u};
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t u0 = w0[i] ^ 0x80808080u, u1 = w1[i] ^ 0x80808080u;
+                        const uint32_t ka[4] = {half2_of(u0, 0x4140), half2_of(u1, 0x4140), half2_of(u0, 0x4342),
+                                                half2_of(u1, 0x4342)};
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            mma_16816<M>(s[nt], qa[4 * hf + i], half2_of(w[i], 0x4140), half2_of(w[i], 0x4342));
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma_16816<M>(s[nt], ka, qb[nt][4 * hf + i][0], qb[nt][4 * hf + i][1]);
                     }
-            }
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
-                float2 kscale = make_float2(1.0f, 1.0f);
-                if (INT8) {
-                    const uint32_t sc = vs + KEYS * S::ROW + (nt * 8 + 2 * t) * 4;
-                    const uint2 a = lds64(sc), b = lds64(sc + KEYS * 4);
-                    kscale = make_float2(__uint_as_float(a.x), __uint_as_float(a.y));
-                    lv[nt][0] = fast_log2(__uint_as_float(b.x));
-                    lv[nt][1] = fast_log2(__uint_as_float(b.y));
-                }
-                const int v = v0 + nt * 8 + 2 * t;
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    // scores in units of log2; keys past the end out
-                    const float a = INT8 ? s[nt][2 * r] * kscale.x : s[nt][2 * r];
-                    const float b = INT8 ? s[nt][2 * r + 1] * kscale.y : s[nt][2 * r + 1];
-                    s[nt][2 * r] = v < n ? a * c_row[r] : -INFINITY;
-                    s[nt][2 * r + 1] = v + 1 < n ? b * c_row[r] : -INFINITY;
                 }
             }
-            float ref[2], refv[2], keep[2];
+            float kscale[2] = {1.0f, 1.0f}, lv[2] = {0.0f, 0.0f};  // int8: of keys g, g + 8
+            if (INT8) {
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                float top = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const float m2 = fmaxf(m[r], top);
-                ref[r] = m2 == -INFINITY ? 0.0f : m2;
-                const float shrink = fast_exp2(m[r] - ref[r]);
-                l[r] *= shrink;
-                m[r] = m2;
-                if (INT8) {
-                    float tv = fmaxf(fmaxf(s[0][2 * r] + lv[0][0], s[0][2 * r + 1] + lv[0][1]),
-                                     fmaxf(s[1][2 * r] + lv[1][0], s[1][2 * r + 1] + lv[1][1]));
-                    tv = fmaxf(tv, __shfl_xor_sync(0xffffffffu, tv, 1));
-                    tv = fmaxf(tv, __shfl_xor_sync(0xffffffffu, tv, 2));
-                    const float mv2 = fmaxf(mv[r], tv);
-                    refv[r] = mv2 == -INFINITY ? 0.0f : mv2;
-                    keep[r] = fast_exp2(mv[r] - refv[r]);
-                    mv[r] = mv2;
-                } else {
-                    keep[r] = shrink;
+                for (int h = 0; h < 2; ++h) {
+                    kscale[h] = __uint_as_float(lds32(vs + KEYS * S::ROW + (g + 8 * h) * 4));
+                    lv[h] = fast_log2(__uint_as_float(lds32(vs + KEYS * S::ROW + (KEYS + g + 8 * h) * 4)));
                 }
             }
-            uint32_t pa[4];
+            const bool in[2] = {v0 + g < n, v0 + g + 8 < n};
+            uint32_t pb[NT][2];
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
+            for (int nt = 0; nt < NT; ++nt) {
+                float w[4];  // weights for the values' product
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const float p0 = fast_exp2(s[nt][2 * r] - ref[r]), p1 = fast_exp2(s[nt][2 * r + 1] - ref[r]);
-                    l[r] += p0 + p1;
-                    if (INT8)
-                        pa[2 * nt + r] = Fp16::pack2(fast_exp2(s[nt][2 * r] + lv[nt][0] - refv[r]),
-                                                     fast_exp2(s[nt][2 * r + 1] + lv[nt][1] - refv[r]));
-                    else
-                        pa[2 * nt + r] = M::pack2(p0, p1);
+                for (int j = 0; j < 2; ++j) {
+                    float a[2];  // scores in units of log2; keys past the end out
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        a[h] = in[h] ? s[nt][2 * h + j] * (INT8 ? kscale[h] * c_head[nt][j] : c_head[nt][j]) : -INFINITY;
+                    float top = fmaxf(a[0], a[1]);
+                    float topv = INT8 ? fmaxf(a[0] + lv[0], a[1] + lv[1]) : 0.0f;
+#pragma unroll
+                    for (int x = 4; x <= 16; x <<= 1) {
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+                        if (INT8)
+                            topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, x));
+                    }
+                    const float m2 = fmaxf(m[nt][j], top);
+                    const float ref = m2 == -INFINITY ? 0.0f : m2;
+                    float keep = fast_exp2(m[nt][j] - ref);
+                    m[nt][j] = m2;
+                    const float p0 = fast_exp2(a[0] - ref), p1 = fast_exp2(a[1] - ref);
+                    l[nt][j] = l[nt][j] * keep + (p0 + p1);
+                    w[j] = p0;
+                    w[2 + j] = p1;
+                    if (INT8) {
+                        const float mv2 = fmaxf(mv[nt][j], topv);
+                        const float refv = mv2 == -INFINITY ? 0.0f : mv2;
+                        keep = fast_exp2(mv[nt][j] - refv);
+                        mv[nt][j] = mv2;
+                        w[j] = fast_exp2(a[0] + lv[0] - refv);
+                        w[2 + j] = fast_exp2(a[1] + lv[1] - refv);
+                    }
+                    if (__any_sync(0xffffffffu, keep != 1.0f))
+#pragma unroll
+                        for (int e = 0; e < DIM / 16; ++e) {
+                            o[nt][e][j] *= keep;
+                            o[nt][e][2 + j] *= keep;
+                        }
                 }
-            if (__any_sync(0xffffffffu, keep[0] != 1.0f || keep[1] != 1.0f))
-#pragma unroll
-                for (int e = 0; e < DIM / 8; ++e) {
-                    o[e][0] *= keep[0], o[e][1] *= keep[0];
-                    o[e][2] *= keep[1], o[e][3] *= keep[1];
-                }
+                pb[nt][0] = transpose_8x8(M::pack2(w[0], w[1]));
+                pb[nt][1] = transpose_8x8(M::pack2(w[2], w[3]));
+            }
             if (!INT8) {
 #pragma unroll
-                for (int ee = 0; ee < DIM / 16; ++ee) {
-                    uint32_t vb[4];
-                    ldmatrix_x4_trans(vb, vs + chunk_at<INT8, DIM, true>((lane & 7) + (((lane >> 3) & 1) << 3),
-                                                                        2 * ee + (lane >> 4)));
-                    mma_16816<M>(o[2 * ee], pa, vb[0], vb[1]);
-                    mma_16816<M>(o[2 * ee + 1], pa, vb[2], vb[3]);
+                for (int e = 0; e < DIM / 16; ++e) {
+                    uint32_t va[4];
+                    ldmatrix_x4_trans(va, vs + chunk_at<INT8, DIM, true>((lane & 7) + ((lane >> 4) << 3),
+                                                                        2 * e + ((lane >> 3) & 1)));
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma_16816<M>(o[nt][e], va, pb[nt][0], pb[nt][1]);
                 }
             } else {
-                // this lane's 4 keys (2t, 2t+1, 2t+8, 2t+9), values (DIM/8) g .. (DIM/8) (g+1) - 1
+                // this lane's 4 keys (2t, 2t+1, 2t+8, 2t+9), values (DIM/8) g .. (DIM/8) (g+1) - 1:
+                // value 2 e of those is row g of tile e, value 2 e + 1 its row g + 8
                 constexpr int WORDS = DIM / 32;
                 uint32_t w[4][WORDS];
 #pragma unroll
@@ -472,18 +485,20 @@ __global__ void __launch_bounds__(WARPS * 32, kBlocksPerSm)
                         const uint2 x = lds64(vs + chunk_at<INT8, DIM, true>(r, g >> 1) + 8 * (g & 1));
                         w[i][0] = x.x, w[i][1] = x.y;
                     }
-#pragma unroll
-                    for (int k = 0; k < WORDS; ++k)
-                        w[i][k] ^= 0x80808080u;
                 }
 #pragma unroll
                 for (int k = 0; k < WORDS; ++k) {
-                    const uint32_t lo01 = __byte_perm(w[0][k], w[1][k], 0x5140), hi01 = __byte_perm(w[0][k], w[1][k], 0x7362);
-                    const uint32_t lo23 = __byte_perm(w[2][k], w[3][k], 0x5140), hi23 = __byte_perm(w[2][k], w[3][k], 0x7362);
-                    mma_16816<M>(o[4 * k], pa, half2_of(lo01, 0x4140), half2_of(lo23, 0x4140));
-                    mma_16816<M>(o[4 * k + 1], pa, half2_of(lo01, 0x4342), half2_of(lo23, 0x4342));
-                    mma_16816<M>(o[4 * k + 2], pa, half2_of(hi01, 0x4140), half2_of(hi23, 0x4140));
-                    mma_16816<M>(o[4 * k + 3], pa, half2_of(hi01, 0x4342), half2_of(hi23, 0x4342));
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {  // values 4 k + 2 h, + 1: tile 2 k + h
+                        const uint32_t sel = h ? 0x7362 : 0x5140;
+                        const uint32_t k01 = __byte_perm(w[0][k], w[1][k], sel) ^ 0x80808080u;
+                        const uint32_t k23 = __byte_perm(w[2][k], w[3][k], sel) ^ 0x80808080u;
+                        const uint32_t va[4] = {half2_of(k01, 0x4140), half2_of(k01, 0x4342), half2_of(k23, 0x4140),
+                                                half2_of(k23, 0x4342)};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma_16816<M>(o[nt][2 * k + h], va, pb[nt][0], pb[nt][1]);
+                    }
                 }
             }
         }
@@ -500,34 +515,41 @@ __global__ void __launch_bounds__(WARPS * 32, kBlocksPerSm)
             if (bad && lane == 0)
                 atomicOr(err, kErrIndex);
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-                if (t == 0)
-                    maxsum[warp * HEADS + g + 8 * r] = make_float2(m[r], bad ? NAN : l[r]);
-            }
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                    for (int x = 4; x <= 16; x <<= 1)
+                        l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], x);
+                    if (g == 0)
+                        maxsum[warp * HEADS + 8 * nt + 2 * t + j] = make_float2(m[nt][j], bad ? NAN : l[nt][j]);
+                }
             __syncthreads();
-            float f[2];
+            float f[NT][2];
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                float top = -INFINITY;
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int w = 0; w < WARPS; ++w)
-                    top = fmaxf(top, maxsum[w * HEADS + g + 8 * r].x);
-                const float from = INT8 ? mv[r] : m[r];  // what the sums o are relative to
-                f[r] = from == -INFINITY ? 0.0f : fast_exp2(from - top);
-            }
+                for (int j = 0; j < 2; ++j) {
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int w = 0; w < WARPS; ++w)
+                        top = fmaxf(top, maxsum[w * HEADS + 8 * nt + 2 * t + j].x);
+                    const float from = INT8 ? mv[nt][j] : m[nt][j];  // what the sums o are relative to
+                    f[nt][j] = from == -INFINITY ? 0.0f : fast_exp2(from - top);
+                }
             for (int w = 0; w < WARPS; ++w) {
                 if (warp == w)
 #pragma unroll
-                    for (int e = 0; e < DIM / 8; ++e)
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int d = INT8 ? DIM / 8 * (2 * t + (i & 1)) + e : 8 * e + 2 * t + (i & 1);
-                            float* dst = joined + (g + 8 * (i >> 1)) * S::LD + d;
-                            const float x = o[e][i] * f[i >> 1];
-                            *dst = w == 0 ? x : *dst + x;
-                        }
+                        for (int e = 0; e < DIM / 16; ++e)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int d = INT8 ? DIM / 8 * g + 2 * e + (i >> 1) : 16 * e + g + 8 * (i >> 1);
+                                float* dst = joined + (8 * nt + 2 * t + (i & 1)) * S::LD + d;
+                                const float x = o[nt][e][i] * f[nt][i & 1];
+                                *dst = w == 0 ? x : *dst + x;
+                            }
                 __syncthreads();
             }
             const bool whole = segment_end && first_of_segment == 0;
@@ -582,11 +604,12 @@ __global__ void __launch_bounds__(WARPS * 32, kBlocksPerSm)
 
 // Adds up the partial sums of the segments that blocks share: one block per (sequence, query
 // head), its 4 warps every fourth part each, then the four together.
-template <class E, int DIM>
+template <class E, int DIM, int NT>
 __global__ void __launch_bounds__(128) join_kernel(const PagedAttention p, int64_t C)
 {
     using T = typename E::T;
     griddep_wait();
+    constexpr int HEADS = 8 * NT;
     constexpr size_t PART = (size_t)HEADS * (DIM + 2);
     __shared__ float4 sums[4][32];
     __shared__ float2 maxsum[4];
@@ -667,44 +690,51 @@ __global__ void __launch_bounds__(128) join_kernel(const PagedAttention p, int64
         p.lse[at_row] = (top + log2f(sum)) * kLn2;
 }
 
-constexpr int64_t kMostBlocks = 152 * kBlocksPerSm;  // of any device this library runs on
+constexpr int kMostBlocks = 152 * 4;  // of any device this library runs on
 
-template <class E, bool INT8, int DIM>
+template <class E, bool INT8, int DIM, int NT>
 cudaError_t launch(const PagedAttention& p, const DeviceInfo& dev, unsigned int* err, cudaStream_t s)
 {
-    using S = Shape<INT8, DIM>;
+    using S = Shape<INT8, DIM, NT>;
     // a kernel attribute belongs to the context it was set in: set once per context
     static ContextCache<int> cache;
     int done = 0;
     cudaError_t e = cache.get(&done, [](int* d) {
         *d = 1;
-        return cudaFuncSetAttribute(paged_kernel<E, INT8, DIM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(paged_kernel<E, INT8, DIM, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     (int)S::SMEM);
     });
     if (e != cudaSuccess)
         return e;
     const int group = p.q_heads / p.cache.heads;
-    const int64_t segments = p.batch * p.cache.heads * ((group + HEADS - 1) / HEADS);
+    const int64_t segments = p.batch * p.cache.heads * ((group + S::HEADS - 1) / S::HEADS);
     int64_t longest = p.max_blocks * p.cache.page_size;
     if (p.window > 0 && p.sinks < longest)
         longest = std::min(longest, p.window + p.sinks);
     const int64_t tiles = (longest + TILE - 1) / TILE;
     const bool split = tiles > kWholeTiles;
-    const int64_t blocks =
-        split ? std::min<int64_t>({kMostBlocks, (int64_t)dev.sm_count * kBlocksPerSm, segments * tiles}) : segments;
-    e = launch_pdl(paged_kernel<E, INT8, DIM>, dim3((unsigned)blocks), dim3(WARPS * 32), S::SMEM, s, p, blocks, split,
+    const int64_t most = std::min<int64_t>(kMostBlocks, (int64_t)dev.sm_count * S::BLOCKS);
+    const int64_t blocks = split ? std::min(most, segments * tiles) : segments;
+    e = launch_pdl(paged_kernel<E, INT8, DIM, NT>, dim3((unsigned)blocks), dim3(WARPS * 32), S::SMEM, s, p, blocks, split,
                    err);
     if (e == cudaSuccess && split)
-        e = launch_pdl(join_kernel<E, DIM>, dim3((unsigned)(p.batch * p.q_heads)), dim3(128), 0, s, p, blocks);
+        e = launch_pdl(join_kernel<E, DIM, NT>, dim3((unsigned)(p.batch * p.q_heads)), dim3(128), 0, s, p, blocks);
     return e;
+}
+
+template <class E, int DIM, int NT>
+cudaError_t by_cache(const PagedAttention& p, const DeviceInfo& dev, unsigned int* err, cudaStream_t s)
+{
+    return p.cache.dtype == CK_KV_INT8 ? launch<E, true, DIM, NT>(p, dev, err, s)
+                                       : launch<E, false, DIM, NT>(p, dev, err, s);
 }
 
 template <int DIM>
 cudaError_t by_type(const PagedAttention& p, const DeviceInfo& dev, unsigned int* err, cudaStream_t s)
 {
-    if (p.cache.dtype == CK_KV_INT8)
-        return p.f16 ? launch<Fp16, true, DIM>(p, dev, err, s) : launch<Bf16, true, DIM>(p, dev, err, s);
-    return p.f16 ? launch<Fp16, false, DIM>(p, dev, err, s) : launch<Bf16, false, DIM>(p, dev, err, s);
+    if (p.q_heads / p.cache.heads <= 8)
+        return p.f16 ? by_cache<Fp16, DIM, 1>(p, dev, err, s) : by_cache<Bf16, DIM, 1>(p, dev, err, s);
+    return p.f16 ? by_cache<Fp16, DIM, 2>(p, dev, err, s) : by_cache<Bf16, DIM, 2>(p, dev, err, s);
 }
 
 }  // namespace
@@ -712,7 +742,7 @@ cudaError_t by_type(const PagedAttention& p, const DeviceInfo& dev, unsigned int
 size_t paged_attention_workspace(int64_t batch, int q_heads, int kv_heads, int dim)
 {
     (void)batch, (void)q_heads, (void)kv_heads;
-    return (size_t)kMostBlocks * 2 * HEADS * (dim + 2) * sizeof(float);
+    return (size_t)kMostBlocks * 2 * 16 * (dim + 2) * sizeof(float);
 }
 
 cudaError_t launch_paged_attention(const PagedAttention& p, const DeviceInfo& dev, cudaStream_t s)

@@ -76,6 +76,14 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr)
     return v;
 }
 
+// transpose an 8 x 8 matrix of 16-bit values held as fragments (lane 4 g + t: row g, columns 2t, 2t+1)
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v)
+{
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
 // d += a (16 x 16, row major) * b (16 x 8): lane 4 g + t holds rows g, g + 8 and columns
 // 2t, 2t+1 of d; a: {rows g | g+8, k 2t, 2t+1}, {.., k 2t+8, 2t+9}; b: {k 2t, 2t+1 | 2t+8, 2t+9; column g}
 template <class E>
