@@ -3,24 +3,131 @@
 //
 //   out[i,h] = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale * q_i . k_j - max), j over the keys
 //   of query i's sequence that it sees; zeros where it sees none.
+//
+// Bound: the tensor cores, 4 dim flops per visible pair and head (and next to them the
+// exponentials, one per pair and head).
+//
+// A block takes 256 queries of one head as two tiles of 128 and walks the key tiles (128 keys)
+// that any of them sees; a query tile skips those that it sees nothing of.  One block per SM:
+//   warp 0      copies by TMA: the two Q tiles, then K and V tiles through one ring;
+//   warp 1      issues the products, one thread: S_t = Q_t K^T (both operands in shared
+//               memory) and O_t += P_t V (P from tensor memory, V as it lies, keys by columns),
+//               all accumulators in tensor memory;
+//   warps 2-3   look every V tile over before it is used (below);
+//   warps 4-11  softmax, a warpgroup for each query tile, one thread per query row: reads its
+//               row of S, takes the maximum, writes the weights back over S as the 16-bit
+//               operand P of the second product.
+// While the softmax of one tile runs, the products of the other keep the tensor cores busy:
+// the issue order is O_0 += P_0 V_j, S_0 = Q_0 K_{j+1}, O_1 += P_1 V_j, S_1 = Q_1 K_{j+1}.
+//
+// Online softmax without a rescale in most steps: a row keeps the maximum m that its sums are
+// relative to until a new one exceeds it by more than 2^8 (weights reach at most 256, exact
+// powers of two apart from what the newest maximum would give); only then does the row's
+// thread rescale O in tensor memory.  S_{j+1} being complete means that O += P_j V_j is, since
+// it was issued before.
+//
+// What a mask hides has no part in a row: hidden scores are replaced, not multiplied, and V
+// rows beyond the sequence are zeroed in shared memory.  A V row within the sequence that some
+// of the tile's queries see and others do not is multiplied by a weight of zero for the
+// others: harmless unless it holds an infinity or NaN.  So V tiles that need a mask are
+// checked, and a block that met such a value computes its rows again, one at a time, with
+// attend_row, which reads visible keys only.
+//
+// Rounding to fewer bits: each weight once, to the 16-bit type of V, as the tensor core takes
+// it; scores, sums, maxima and O are fp32.
+#include <algorithm>
+#include <cmath>
+#include <mutex>
+#include <type_traits>
+
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <cudaTypedefs.h>
 
 #include "attn_common.cuh"
 #include "transformer.h"
+#include "warp_mma.cuh"
 
 namespace ck {
 namespace {
 
-// The sequence whose queries hold row `row`: the last b with cu[b] <= row (-1: none).
-__device__ __forceinline__ int64_t sequence_of(const int32_t* cu, int64_t batch, int64_t row)
+constexpr int BM = 128;              // query rows of a tile, keys of a key tile
+constexpr int ROWS = 2 * BM;         // query rows of a block
+constexpr int THREADS = 384;
+// registers after the warpgroups re-balance; 384 threads start with 168 each
+constexpr uint32_t REGS_LOAD = 80, REGS_SOFTMAX = 208;
+constexpr uint32_t REGS_NEEDED_PER_BLOCK = 128 * REGS_LOAD + 256 * REGS_SOFTMAX;
+constexpr uint32_t TMEM_COLS = 512;
+constexpr uint64_t TIMEOUT_NS = 2000000000ull;
+constexpr float kLag = 8.0f;         // how far (log2) a row's reference may trail its maximum
+
+template <int DIM>
+struct Cfg {
+    static constexpr int BOXES = DIM / 64;                     // 128-byte wide boxes of a tile
+    static constexpr uint32_t BOX_BYTES = BM * 128;
+    static constexpr uint32_t TILE_BYTES = BOXES * BOX_BYTES;  // a Q, K or V tile
+    static constexpr int SLOTS = DIM == 128 ? 5 : 8;           // K / V ring
+    static constexpr uint32_t Q_BYTES = 2 * TILE_BYTES;
+    static constexpr size_t SMEM = 1024 + Q_BYTES + SLOTS * TILE_BYTES + 512;
+    static_assert(SMEM <= 232448, "shared memory budget");
+};
+
+struct PromptArgs {
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;
+    const int32_t *cu_q, *cu_k;
+    int64_t batch, total_q, total_k;
+    int q_heads, kv_heads;
+    bool causal, negate;
+    float scale, c;  // c = |scale| log2 e
+    int64_t window, sinks;
+    void* out;
+    float* lse;
+    int64_t slots;   // tile slots of a head
+};
+
+// One block's share: which keys its rows see, and the key tiles to walk.
+struct Item {
+    int64_t q_row, k_row;  // first query row of the block, first key row of the sequence
+    int rows;              // queries of the block, at most ROWS
+    int keys;              // keys of the sequence
+    int offset;            // query r of the block stands at key position r + offset
+    bool causal;
+    int window, sinks;     // window 0: none
+    int prefix, first, count;  // key tiles: 0 .. prefix - 1, then first ..; count in all
+
+    __device__ __forceinline__ int key0(int j) const { return BM * (j < prefix ? j : first + (j - prefix)); }
+    __device__ __forceinline__ int hi(int r) const { return causal ? min(r + offset, keys - 1) : keys - 1; }  // last key row r sees
+    __device__ __forceinline__ int lo(int r) const { return window ? max(r + offset - window + 1, 0) : 0; }
+    __device__ __forceinline__ int last_row(int t) const { return min(BM * t + BM, rows) - 1; }
+    __device__ __forceinline__ bool any(int t) const { return BM * t < rows && hi(last_row(t)) >= 0; }
+    // whether any row of query tile t sees a key of the tile at k0
+    __device__ __forceinline__ bool active(int t, int k0) const
+    {
+        return any(t) && hi(last_row(t)) >= k0 && (k0 + BM > lo(BM * t) || k0 < sinks);
+    }
+    // whether some row does not see all of it
+    __device__ __forceinline__ bool partial(int t, int k0) const
+    {
+        return k0 + BM - 1 > hi(BM * t) || (lo(last_row(t)) > k0 && k0 + BM > sinks);
+    }
+    // the last j that is active for tile t, given any(t)
+    __device__ __forceinline__ int last(int t) const
+    {
+        const int kt = hi(last_row(t)) / BM;
+        return kt < prefix ? kt : prefix + kt - first;
+    }
+};
+
+// The sequence with tile slot `s` (slot_of(b) = cu[b] / ROWS + b leaves room for every ragged
+// end, needs no sums over lengths and ascends): the last b with slot_of(b) <= s.
+__device__ __forceinline__ int64_t sequence_of_slot(const int32_t* cu, int64_t batch, int64_t s)
 {
-    int64_t lo = 0, hi = batch;  // cu[lo] <= row < cu[hi], once checked
-    if (__ldg(cu) > row || __ldg(cu + batch) <= row)
-        return -1;
+    int64_t lo = 0, hi = batch;
     while (hi - lo > 1) {
         const int64_t mid = (lo + hi) >> 1;
-        if (__ldg(cu + mid) <= row)
+        if ((int64_t)__ldg(cu + mid) / ROWS + mid <= s)
             lo = mid;
         else
             hi = mid;
@@ -28,71 +135,637 @@ __device__ __forceinline__ int64_t sequence_of(const int32_t* cu, int64_t batch,
     return lo;
 }
 
-template <class E, int DIM>
-__global__ void __launch_bounds__(128) prompt_row_kernel(const PromptAttention p, unsigned int* err)
+// ---- tensor core pieces beyond ck_device.cuh's
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int32_t c0, int32_t c1,
+                                            int32_t c2)
 {
-    griddep_wait();
-    __shared__ float qs_all[4][DIM];
-    using T = typename E::T;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t unit = (int64_t)blockIdx.x * 4 + warp;
-    const int64_t i = unit / p.q_heads;
-    const int h = (int)(unit - i * p.q_heads);
-    if (i >= p.total_q)
-        return;
-    const int64_t b = sequence_of(p.cu_q, p.batch, i);
-    if (b < 0)
-        return;
-    const int64_t q0 = __ldg(p.cu_q + b), q1 = __ldg(p.cu_q + b + 1);
-    const int64_t k0 = __ldg(p.cu_k + b), k1 = __ldg(p.cu_k + b + 1);
-    const bool bad = q0 < 0 || q1 > p.total_q || q1 < q0 || k0 < 0 || k1 < k0 || k1 > p.total_k;
-    float* qs = qs_all[warp];
-    const T* q = static_cast<const T*>(p.q) + i * p.q_stride + (int64_t)h * DIM;
-    for (int d = lane; d < DIM; d += 32)
-        qs[d] = E::to(q[d]) * (p.scale * kLog2e);
-    __syncwarp();
-    const int hk = h / (p.q_heads / p.kv_heads);
-    const int nk = bad ? 0 : (int)(k1 - k0);
-    const VisibleKeys keys = p.causal ? visible_keys((int)(nk - (q1 - 1 - i)), p.window, p.sinks)
-                                      : visible_keys(nk, 0, 0);
-    float acc[(DIM + 31) / 32], m, l;
-    attend_row<E, false, DIM>(qs, bad ? 0 : keys.count(), [&](int v) {
-        const int64_t j = k0 + keys.key(v);
-        KvRow r;
-        r.k = static_cast<const T*>(p.k) + j * p.k_stride + (int64_t)hk * DIM;
-        r.v = static_cast<const T*>(p.v) + j * p.v_stride + (int64_t)hk * DIM;
-        r.ks = r.vs = 1.0f;
-        return r;
-    }, acc, m, l);
-    if (bad && lane == 0)
-        atomicOr(err, kErrIndex);
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_st()
+{
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Descriptor of a [keys][64 values] box with 128-byte swizzling as an operand whose N (the
+// values) is contiguous: 8-key groups 1024 bytes apart (stride offset), 64-value boxes
+// BOX_BYTES apart (leading offset).
+__device__ __forceinline__ uint64_t desc_nmajor_sw128(uint32_t smem_addr, uint32_t box_bytes)
+{
+    uint64_t d = 0;
+    d |= (uint64_t)((smem_addr >> 4) & 0x3FFFu);
+    d |= (uint64_t)(box_bytes >> 4) << 16;
+    d |= (uint64_t)(1024u >> 4) << 32;
+    d |= (uint64_t)1u << 46;
+    d |= (uint64_t)2u << 61;
+    return d;
+}
+
+// Instruction descriptor, fp32 accumulator: 16-bit types at bits 7 and 10 (1 = bf16), negated
+// A at 13, B with N contiguous at 16, N / 8 at 17, M / 16 at 24.
+template <class E>
+__device__ __forceinline__ constexpr uint32_t idesc_of(int n, bool b_nmajor)
+{
+    return (1u << 4) | (std::is_same<E, Bf16>::value ? (1u << 7) | (1u << 10) : 0u) | (b_nmajor ? 1u << 16 : 0u) |
+           ((uint32_t)(n >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+}
+
+// Bounded wait of teardown (raises no abort).
+__device__ __forceinline__ void wait_out(uint64_t* bar, uint32_t parity, unsigned int* err)
+{
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i)
+        if ((i & 255u) == 0 && globaltimer_ns() - t0 > TIMEOUT_NS) {
+            atomicOr(err, kErrWaitAttention);
+            return;
+        }
+}
+
+template <class E>
+__device__ __forceinline__ void store_row(void* out, int64_t at, const float (&v)[32], float f)
+{
+    // 32 values of a row
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<typename E::T*>(out) + at);
 #pragma unroll
-    for (int c = 0; c < (DIM + 31) / 32; ++c)
-        static_cast<T*>(p.out)[(i * p.q_heads + h) * DIM + lane + 32 * c] =
-            E::from(bad ? NAN : keys.count() == 0 ? 0.0f : acc[c] / l);
-    if (p.lse != nullptr && lane == 0)
-        p.lse[(int64_t)h * p.total_q + i] = bad ? NAN : (m + log2f(l)) * kLn2;
+    for (int i = 0; i < 4; ++i)
+        dst[i] = make_uint4(E::pack2(v[8 * i] * f, v[8 * i + 1] * f), E::pack2(v[8 * i + 2] * f, v[8 * i + 3] * f),
+                            E::pack2(v[8 * i + 4] * f, v[8 * i + 5] * f), E::pack2(v[8 * i + 6] * f, v[8 * i + 7] * f));
 }
 
 template <class E, int DIM>
-cudaError_t launch(const PromptAttention& p, unsigned int* err, cudaStream_t s)
+__global__ void __launch_bounds__(THREADS, 1)
+    prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                  const __grid_constant__ CUtensorMap tmV, const PromptArgs p, unsigned int* err)
 {
-    const int64_t units = p.total_q * p.q_heads;
-    return launch_pdl(prompt_row_kernel<E, DIM>, dim3((unsigned)((units + 3) / 4)), dim3(128), 0, s, p, err);
+    using C = Cfg<DIM>;
+    using T = typename E::T;
+    constexpr int SLOTS = C::SLOTS;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* s_q = smem;
+    uint8_t* s_kv = smem + C::Q_BYTES;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(s_kv + (size_t)SLOTS * C::TILE_BYTES);
+    uint64_t* q_full = bars;             // [2]
+    uint64_t* s_full = bars + 2;         // [2] S_t is complete (and every product before it)
+    uint64_t* p_full = bars + 4;         // [2] P_t is written, O_t may be added to
+    uint64_t* o_full = bars + 6;         // [2] O_t is final
+    uint64_t* drain = bars + 8;
+    uint64_t* kv_full = bars + 9;        // [SLOTS] a tile has landed
+    uint64_t* kv_empty = kv_full + SLOTS;  // [SLOTS] its products are done
+    uint64_t* v_ready = kv_empty + SLOTS;  // [SLOTS] looked over
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(v_ready + SLOTS);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile int* dirty = abort_flag + 1;  // a V row holds an infinity or NaN
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp == 0 && lane == 0) {
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&q_full[t], 1);
+            mbar_init(&s_full[t], 1);
+            mbar_init(&p_full[t], 4);
+            mbar_init(&o_full[t], 1);
+        }
+        mbar_init(drain, 1);
+        for (int s = 0; s < SLOTS; ++s) {
+            mbar_init(&kv_full[s], 1);
+            mbar_init(&kv_empty[s], 1);
+            mbar_init(&v_ready[s], 2);
+        }
+        *abort_flag = 0;
+        *dirty = 0;
+        fence_mbar_init();
+        fence_proxy_async_smem();
+        tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, TMEM_COLS);
+        tmem_relinquish();
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    griddep_wait();
+
+    // ---- this block's share; blocks start in order, so the last (for causal prompts the
+    // longest) tiles come first
+    const int64_t slot = p.slots - 1 - (int64_t)blockIdx.x / p.q_heads;
+    const int head = (int)(blockIdx.x % p.q_heads);
+    const int kv_head = head / (p.q_heads / p.kv_heads);
+    Item w;
+    bool bad;
+    {
+        const int64_t b = sequence_of_slot(p.cu_q, p.batch, slot);
+        const int64_t q0 = __ldg(p.cu_q + b), q1 = __ldg(p.cu_q + b + 1);
+        const int64_t k0 = __ldg(p.cu_k + b), k1 = __ldg(p.cu_k + b + 1);
+        const bool bad_q = q0 < 0 || q1 < q0 || q1 > p.total_q;
+        bad = bad_q || k0 < 0 || k1 < k0 || k1 > p.total_k;
+        const int64_t r0 = (slot - (q0 / ROWS + b)) * ROWS;
+        w.q_row = q0 + r0;
+        w.rows = bad_q || r0 < 0 ? 0 : (int)min((int64_t)ROWS, max(q1 - w.q_row, (int64_t)0));
+        w.k_row = k0;
+        w.keys = bad ? 0 : (int)(k1 - k0);
+        w.offset = bad ? 0 : (int)(r0 + (k1 - k0) - (q1 - q0));
+        w.causal = p.causal;
+        w.window = (int)min(p.window, (int64_t)0x3FFFFFFF);
+        w.sinks = w.window ? (int)min(p.sinks, (int64_t)0x3FFFFFFF) : 0;
+        // key tiles: those of the first tokens, then those of the windows' union
+        const int top = w.rows > 0 ? w.hi(w.rows - 1) : -1;
+        w.prefix = w.first = w.count = 0;
+        if (top >= 0) {
+            w.first = w.lo(0) / BM;
+            if (w.sinks > 0 && w.first > 0) {
+                w.prefix = min((min(w.sinks, top + 1) + BM - 1) / BM, w.first);
+                // (first tokens that reach into the windows' union lie in its tiles)
+            }
+            w.count = w.prefix + top / BM - w.first + 1;
+        }
+        if (bad && threadIdx.x == 0)
+            atomicOr(err, kErrIndex);
+    }
+
+    if (warp < 4) {
+        setmaxnreg_dec<REGS_LOAD>();
+        if (warp == 0) {
+            // ---------------------------------------------------------------- copies
+            if (lane == 0 && w.count > 0) {
+                uint32_t issued = 0;
+                bool ok = true;
+                auto load_q = [&](int t) {
+                    if (!w.any(t))
+                        return;
+                    mbar_arrive_expect_tx(&q_full[t], C::TILE_BYTES);
+                    for (int x = 0; x < C::BOXES; ++x)
+                        tma_load_3d(s_q + t * C::TILE_BYTES + x * C::BOX_BYTES, &tmQ, &q_full[t], x * 64, head,
+                                    (int32_t)(w.q_row + BM * t));
+                };
+                load_q(0);
+                int s = 0;
+                uint32_t phase = 0;
+                for (int u = 0; ok && u < 2 * w.count; ++u) {  // K_0, V_0, K_1, V_1, ..
+                    if (!mbar_wait(&kv_empty[s], phase ^ 1u, abort_flag, err, kErrWaitAttention, TIMEOUT_NS)) {
+                        ok = false;
+                        break;
+                    }
+                    const CUtensorMap* map = (u & 1) ? &tmV : &tmK;
+                    mbar_arrive_expect_tx(&kv_full[s], C::TILE_BYTES);
+                    for (int x = 0; x < C::BOXES; ++x)
+                        tma_load_3d(s_kv + (size_t)s * C::TILE_BYTES + x * C::BOX_BYTES, map, &kv_full[s], x * 64, kv_head,
+                                    (int32_t)(w.k_row + w.key0(u >> 1)));
+                    if (u == 0)
+                        load_q(1);
+                    issued = (issued & ~(3u << (2 * s))) | ((2u | phase) << (2 * s));
+                    if (++s == SLOTS) {
+                        s = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) {  // aborting: every issued copy lands before shared memory is released
+                    for (int i = 0; i < SLOTS; ++i)
+                        if ((issued >> (2 * i)) & 2u)
+                            wait_out(&kv_full[i], (issued >> (2 * i)) & 1u, err);
+                    for (int t = 0; t < 2; ++t)
+                        if (w.any(t))
+                            wait_out(&q_full[t], 0, err);
+                }
+            }
+            __syncwarp();
+        } else if (warp == 1) {
+            // -------------------------------------------------------------- products
+            if (lane == 0 && w.count > 0) {
+                const uint32_t idesc_s = idesc_of<E>(BM, false) | (p.negate ? 1u << 13 : 0u);
+                constexpr uint32_t idesc_o = idesc_of<E>(DIM, true);
+                const uint64_t q_desc = desc_kmajor_sw128(smem_u32(s_q));
+                const uint64_t k_desc = desc_kmajor_sw128(smem_u32(s_kv));
+                const uint64_t v_desc = desc_nmajor_sw128(smem_u32(s_kv), C::BOX_BYTES);
+                constexpr uint64_t kTile = C::TILE_BYTES >> 4, kBox = C::BOX_BYTES >> 4;
+                bool q_seen[2] = {false, false}, started[2] = {false, false};
+                uint32_t p_phase[2] = {0, 0};
+                bool ok = true;
+                // ring uses in order: K_j is use 2 j, V_j use 2 j + 1
+                auto slot_of = [](int u) { return u % SLOTS; };
+                auto parity_of = [](int u) { return (uint32_t)(u / SLOTS) & 1u; };
+                // with an odd number of slots each holds K and V tiles by turns
+                auto v_parity_of = [](int u) { return (uint32_t)(u / (SLOTS % 2 ? 2 * SLOTS : SLOTS)) & 1u; };
+                auto wait = [&](uint64_t* bar, uint32_t parity) {
+                    ok = ok && mbar_wait(bar, parity, abort_flag, err, kErrWaitAttention, TIMEOUT_NS);
+                    return ok;
+                };
+                auto scores = [&](int t, int s) {
+                    if (!q_seen[t] && !wait(&q_full[t], 0))
+                        return;
+                    q_seen[t] = true;
+                    tc_fence_after();
+                    const uint64_t a = q_desc + t * kTile, b = k_desc + s * kTile;
+#pragma unroll
+                    for (int k = 0; k < DIM / 16; ++k)
+                        mma_ss(tmem + t * BM, a + (k / 4) * kBox + (k % 4) * 2, b + (k / 4) * kBox + (k % 4) * 2, idesc_s,
+                               k > 0);
+                    mma_commit(&s_full[t]);
+                };
+                const int j0 = 0;
+                if (wait(&kv_full[slot_of(0)], parity_of(0))) {
+                    for (int t = 0; ok && t < 2; ++t)
+                        if (w.active(t, w.key0(j0)))
+                            scores(t, slot_of(0));
+                    mma_commit(&kv_empty[slot_of(0)]);
+                }
+                for (int j = 0; ok && j < w.count; ++j) {
+                    const int k0 = w.key0(j);
+                    const int vu = 2 * j + 1, ku = 2 * j + 2;
+                    const bool more = j + 1 < w.count;
+                    for (int t = 0; ok && t < 2; ++t) {
+                        if (t == 0 && !wait(&v_ready[slot_of(vu)], v_parity_of(vu)))
+                            break;
+                        if (w.active(t, k0)) {
+                            if (!wait(&p_full[t], p_phase[t]))
+                                break;
+                            p_phase[t] ^= 1u;
+                            tc_fence_after();
+                            const uint64_t b = v_desc + slot_of(vu) * kTile;
+#pragma unroll
+                            for (int k = 0; k < BM / 16; ++k)
+                                mma_ts(tmem + 2 * BM + t * DIM, tmem + t * BM + k * 8, b + k * (16 * 128 >> 4), idesc_o,
+                                       started[t] || k > 0);
+                            started[t] = true;
+                            if (j == w.last(t))
+                                mma_commit(&o_full[t]);
+                        }
+                        if (t == 1)
+                            mma_commit(&kv_empty[slot_of(vu)]);
+                        if (more) {
+                            if (t == 0 && !wait(&kv_full[slot_of(ku)], parity_of(ku)))
+                                break;
+                            if (w.active(t, w.key0(j + 1)))
+                                scores(t, slot_of(ku));
+                            if (t == 1)
+                                mma_commit(&kv_empty[slot_of(ku)]);
+                        }
+                    }
+                }
+                // every product must be complete before tensor and shared memory are released
+                mma_commit(drain);
+                wait_out(drain, 0, err);
+            }
+            __syncwarp();
+        } else {
+            // -------------------------------------------------- V tiles, before their use
+            const int tid = threadIdx.x - 64;  // 0..63: rows tid and tid + 64
+            for (int j = 0; j < w.count; ++j) {
+                const int u = 2 * j + 1, s = u % SLOTS;
+                const bool ok = mbar_wait(&kv_full[s], (uint32_t)(u / SLOTS) & 1u, abort_flag, err, kErrWaitAttention,
+                                          TIMEOUT_NS);
+                if (!__all_sync(0xffffffffu, ok))
+                    break;
+                const int k0 = w.key0(j);
+                const bool check = (w.active(0, k0) && w.partial(0, k0)) || (w.active(1, k0) && w.partial(1, k0));
+                if (check) {
+                    uint8_t* tile = s_kv + (size_t)s * C::TILE_BYTES;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int r = tid + 64 * h;
+                        if (k0 + r >= w.keys) {
+                            for (int x = 0; x < C::BOXES; ++x)
+                                for (int c = 0; c < 8; ++c)
+                                    *reinterpret_cast<uint4*>(tile + x * C::BOX_BYTES + r * 128 + ((c ^ r) & 7) * 16) =
+                                        make_uint4(0u, 0u, 0u, 0u);
+                        } else {
+                            // 0 * x is NaN exactly for infinities and NaN; the sum keeps it
+                            typename E::T2 sum = {E::from(0.0f), E::from(0.0f)};
+                            const typename E::T2 zero = sum;
+                            for (int x = 0; x < C::BOXES; ++x)
+#pragma unroll
+                                for (int c = 0; c < 8; ++c) {
+                                    const uint4 v = *reinterpret_cast<const uint4*>(tile + x * C::BOX_BYTES + r * 128 +
+                                                                                    ((c ^ r) & 7) * 16);
+                                    const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i)
+                                        sum = __hfma2(*reinterpret_cast<const typename E::T2*>(&words[i]), zero, sum);
+                                }
+                            const float2 f = E::to2(*reinterpret_cast<const uint32_t*>(&sum));
+                            if (f.x != f.x || f.y != f.y)
+                                *dirty = 1;
+                        }
+                    }
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&v_ready[s]);
+            }
+            __syncwarp();
+        }
+    } else {
+        // ---------------------------------------------------------------------- softmax
+        setmaxnreg_inc<REGS_SOFTMAX>();
+        const int t = (warp - 4) >> 2;
+        const int quarter = warp & 3;  // tensor memory lanes that this warp may access
+        const int row = quarter * 32 + lane;
+        const int r = BM * t + row;    // row of the block
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        const uint32_t s_addr = tmem + lanes + t * BM, o_addr = tmem + lanes + 2 * BM + t * DIM;
+        const int hi = w.hi(r), lo = w.lo(r);
+        const float c = p.c;
+        float m = -INFINITY;  // what the row's sums are relative to, in units of scores
+        float l = 0.0f;
+        uint32_t phase = 0;
+        bool started = false, ok = true;
+        for (int j = 0; j < w.count; ++j) {
+            const int k0 = w.key0(j);
+            if (!w.active(t, k0))
+                continue;
+            ok = mbar_wait(&s_full[t], phase, abort_flag, err, kErrWaitAttention, TIMEOUT_NS);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok)
+                break;
+            phase ^= 1u;
+            tc_fence_after();
+            uint32_t sr[4][32];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                tmem_ld_32x32b_x32(s_addr + 32 * i, sr[i]);
+            tmem_wait_ld();
+            if (w.partial(t, k0)) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    // bit n: key k0 + 32 i + n is seen (k <= hi and (k >= lo or k < sinks))
+                    const int a = k0 + 32 * i;
+                    const int nh = hi - a + 1, nl = lo - a, ns = w.sinks - a;
+                    const uint32_t upto = nh <= 0 ? 0u : nh >= 32 ? 0xffffffffu : (1u << nh) - 1u;
+                    const uint32_t below = nl <= 0 ? 0u : nl >= 32 ? 0xffffffffu : (1u << nl) - 1u;
+                    const uint32_t first = ns <= 0 ? 0u : ns >= 32 ? 0xffffffffu : (1u << ns) - 1u;
+                    const uint32_t seen = upto & (~below | first);
+#pragma unroll
+                    for (int n = 0; n < 32; ++n)
+                        sr[i][n] = (seen >> n) & 1u ? sr[i][n] : 0xff800000u;
+                }
+            }
+            float tops[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                tops[i] = __uint_as_float(sr[i][0]);
+#pragma unroll
+                for (int n = 1; n < 31; n += 2)
+                    tops[i] = fmaxf(tops[i], fmaxf(__uint_as_float(sr[i][n]), __uint_as_float(sr[i][n + 1])));
+                tops[i] = fmaxf(tops[i], __uint_as_float(sr[i][31]));
+            }
+            const float top = fmaxf(m, fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])));
+            const bool raise = (top - m) * c > kLag;
+            if (!started) {
+                m = top;
+            } else if (__any_sync(0xffffffffu, raise)) {
+                // rare: bring the row's sums to the new maximum
+                const float f = raise ? fast_exp2((m - top) * c) : 1.0f;
+                if (raise)
+                    m = top;
+                l *= f;
+#pragma unroll 1
+                for (int i = 0; i < DIM / 16; ++i) {
+                    uint32_t v[16];
+                    tmem_ld_32x32b_x16(o_addr + 16 * i, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int n = 0; n < 16; ++n)
+                        v[n] = __float_as_uint(__uint_as_float(v[n]) * f);
+                    tmem_st_32x32b_x16(o_addr + 16 * i, v);
+                }
+            }
+            started = true;
+            const float mc = m == -INFINITY ? 0.0f : -m * c;  // no key seen yet: weights 0
+            const float2 c2 = make_float2(c, c), mc2 = make_float2(mc, mc);
+            float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t w16[16];
+#pragma unroll
+                for (int n = 0; n < 16; ++n) {
+                    float2 x = f2_fma_rn(make_float2(__uint_as_float(sr[i][2 * n]), __uint_as_float(sr[i][2 * n + 1])), c2,
+                                         mc2);
+                    x.x = fast_exp2(x.x);
+                    x.y = fast_exp2(x.y);
+                    sum = f2_add_rn(sum, x);
+                    w16[n] = E::pack2(x.x, x.y);
+                }
+                tmem_st_32x32b_x16(s_addr + 16 * i, w16);
+            }
+            l += sum.x + sum.y;
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&p_full[t]);
+        }
+        // ---- the rows' outputs
+        const int64_t out_row = w.q_row + r;
+        const int64_t at = (out_row * p.q_heads + head) * DIM;
+        const bool mine = r < w.rows;
+        if (ok && w.count > 0 && w.any(t)) {
+            ok = mbar_wait(&o_full[t], 0, abort_flag, err, kErrWaitAttention, TIMEOUT_NS);
+            ok = __all_sync(0xffffffffu, ok);
+            tc_fence_after();
+            if (ok && *dirty == 0) {
+                const float f = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll 1
+                for (int i = 0; i < DIM / 32; ++i) {
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32(o_addr + 32 * i, v);
+                    tmem_wait_ld();
+                    float x[32];
+#pragma unroll
+                    for (int n = 0; n < 32; ++n)
+                        x[n] = __uint_as_float(v[n]);
+                    if (mine)
+                        store_row<E>(p.out, at + 32 * i, x, f);
+                }
+                if (mine && p.lse != nullptr)
+                    p.lse[(int64_t)head * p.total_q + out_row] = (m * c + log2f(l)) * kLn2;
+            } else if (ok) {
+                // a row at a time, over visible keys only; the tile's Q has been used
+                float* qs = reinterpret_cast<float*>(s_q + t * C::TILE_BYTES) + quarter * DIM;
+                for (int i = 0; i < 32 && BM * t + quarter * 32 + i < w.rows; ++i) {
+                    const int ri = BM * t + quarter * 32 + i;
+                    const T* q = static_cast<const T*>(p.q) + (w.q_row + ri) * p.q_stride + (int64_t)head * DIM;
+                    __syncwarp();
+                    for (int d = lane; d < DIM; d += 32)
+                        qs[d] = E::to(q[d]) * (p.scale * kLog2e);
+                    __syncwarp();
+                    const VisibleKeys keys = p.causal ? visible_keys(ri + w.offset + 1, p.window, p.sinks)
+                                                      : visible_keys(w.keys, 0, 0);
+                    float acc[DIM / 32], rm, rl;
+                    attend_row<E, false, DIM>(qs, keys.count(), [&](int v) {
+                        const int64_t k = w.k_row + keys.key(v);
+                        KvRow kv;
+                        kv.k = static_cast<const T*>(p.k) + k * p.k_stride + (int64_t)kv_head * DIM;
+                        kv.v = static_cast<const T*>(p.v) + k * p.v_stride + (int64_t)kv_head * DIM;
+                        kv.ks = kv.vs = 1.0f;
+                        return kv;
+                    }, acc, rm, rl);
+                    T* dst = static_cast<T*>(p.out) + ((w.q_row + ri) * p.q_heads + head) * DIM;
+#pragma unroll
+                    for (int d = 0; d < DIM / 32; ++d)
+                        dst[lane + 32 * d] = E::from(keys.count() == 0 ? 0.0f : acc[d] / rl);
+                    if (lane == 0 && p.lse != nullptr)
+                        p.lse[(int64_t)head * p.total_q + w.q_row + ri] = (rm + log2f(rl)) * kLn2;
+                }
+            }
+        }
+        if (mine && (!ok || bad || !w.any(t))) {
+            // no keys: zeros; bounds out of range or a wait that gave up: NaN
+            const bool nan = bad || !ok;
+            float x[32];
+#pragma unroll
+            for (int n = 0; n < 32; ++n)
+                x[n] = nan ? NAN : 0.0f;
+#pragma unroll 1
+            for (int i = 0; i < DIM / 32; ++i)
+                store_row<E>(p.out, at + 32 * i, x, 1.0f);
+            if (p.lse != nullptr)
+                p.lse[(int64_t)head * p.total_q + out_row] = nan ? NAN : -INFINITY;
+        }
+    }
+    griddep_launch_dependents();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, TMEM_COLS);
+    }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
+{
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    });
+    return fn;
+}
+
+// [rows, heads, dim] with `stride` elements between rows, copied as boxes of 128 rows x 64
+// values of one head.
+bool make_map(CUtensorMap* map, const void* base, int64_t rows, int heads, int dim, int64_t stride, bool f16,
+              std::string* why)
+{
+    auto fn = encode_fn();
+    if (!fn) {
+        *why = "cuTensorMapEncodeTiled is not available from the driver";
+        return false;
+    }
+    cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)rows};
+    cuuint64_t strides[2] = {(cuuint64_t)dim * 2, (cuuint64_t)stride * 2};
+    cuuint32_t box[3] = {64, 1, BM};
+    cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = fn(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                          const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        *why = "cuTensorMapEncodeTiled failed (" + std::to_string((int)r) + ")";
+    return r == CUDA_SUCCESS;
+}
+
+template <class E, int DIM>
+cudaError_t launch(const PromptAttention& p, unsigned int* err, cudaStream_t s, std::string* why)
+{
+    using C = Cfg<DIM>;
+    // a kernel attribute belongs to the context it was set in: set once per context
+    static ContextCache<int> cache;
+    int done = 0;
+    cudaError_t e = cache.get(&done, [](int* d) {
+        *d = 1;
+        cudaFuncAttributes fa;
+        cudaError_t a = cudaFuncGetAttributes(&fa, prompt_kernel<E, DIM>);
+        if (a != cudaSuccess)
+            return a;
+        // the softmax warps claim what warps 0-3 give back: the launch must provide the sum
+        if ((uint32_t)(fa.numRegs + 7) / 8 * 8 * THREADS < REGS_NEEDED_PER_BLOCK)
+            return cudaErrorLaunchOutOfResources;
+        return cudaFuncSetAttribute(prompt_kernel<E, DIM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+    });
+    if (e != cudaSuccess)
+        return e;
+    CUtensorMap q, k, v;
+    if (!make_map(&q, p.q, p.total_q, p.q_heads, DIM, p.q_stride, p.f16, why))
+        return cudaErrorInvalidValue;
+    k = v = q;  // without keys no block copies any
+    if (p.total_k > 0 && (!make_map(&k, p.k, p.total_k, p.kv_heads, DIM, p.k_stride, p.f16, why) ||
+                          !make_map(&v, p.v, p.total_k, p.kv_heads, DIM, p.v_stride, p.f16, why)))
+        return cudaErrorInvalidValue;
+    PromptArgs a{};
+    a.q = p.q, a.k = p.k, a.v = p.v;
+    a.q_stride = p.q_stride, a.k_stride = p.k_stride, a.v_stride = p.v_stride;
+    a.cu_q = p.cu_q, a.cu_k = p.cu_k;
+    a.batch = p.batch, a.total_q = p.total_q, a.total_k = p.total_k;
+    a.q_heads = p.q_heads, a.kv_heads = p.kv_heads;
+    a.causal = p.causal;
+    // the softmax wants a positive factor: a negative scale negates Q in the first product, and
+    // for 0 the smallest factor that still keeps hidden scores (-inf) hidden stands in
+    a.negate = p.scale < 0.0f;
+    a.scale = p.scale;
+    a.c = std::max(std::fabs(p.scale) * kLog2e, 1e-30f);
+    a.window = p.causal ? p.window : 0;
+    a.sinks = p.sinks;
+    a.out = p.out;
+    a.lse = p.lse;
+    a.slots = p.total_q / ROWS + p.batch;
+    return launch_pdl(prompt_kernel<E, DIM>, dim3((unsigned)(a.slots * p.q_heads)), dim3(THREADS), C::SMEM, s, q, k, v, a,
+                      err);
 }
 
 }  // namespace
 
 cudaError_t launch_attention(const PromptAttention& p, const DeviceInfo& dev, cudaStream_t s, std::string* why)
 {
-    (void)dev, (void)why;
+    (void)dev;
     unsigned int* err = nullptr;
     cudaError_t e = device_error_ptr(&err);
     if (e != cudaSuccess)
         return e;
     if (p.dim == 64)
-        return p.f16 ? launch<Fp16, 64>(p, err, s) : launch<Bf16, 64>(p, err, s);
-    return p.f16 ? launch<Fp16, 128>(p, err, s) : launch<Bf16, 128>(p, err, s);
+        return p.f16 ? launch<Fp16, 64>(p, err, s, why) : launch<Bf16, 64>(p, err, s, why);
+    return p.f16 ? launch<Fp16, 128>(p, err, s, why) : launch<Bf16, 128>(p, err, s, why);
 }
 
 }  // namespace ck
