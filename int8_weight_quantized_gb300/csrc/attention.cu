@@ -20,11 +20,13 @@
 // While the softmax of one tile runs, the products of the other keep the tensor cores busy:
 // the issue order is O_0 += P_0 V_j, S_0 = Q_0 K_{j+1}, O_1 += P_1 V_j, S_1 = Q_1 K_{j+1}.
 //
-// Online softmax without a rescale in most steps: a row keeps the maximum m that its sums are
-// relative to until a new one exceeds it by more than 2^8 (weights reach at most 256, exact
-// powers of two apart from what the newest maximum would give); only then does the row's
-// thread rescale O in tensor memory.  S_{j+1} being complete means that O += P_j V_j is, since
-// it was issued before.
+// Online softmax that seldom waits for its maximum: a row's weights of a tile are taken
+// relative to the reference m that its sums have, while the tile's maximum is found beside
+// them.  A maximum more than 2^8 above m makes the row's thread bring m, the sum and O (in
+// tensor memory) up to it before the next tile; one so far above that a weight would leave its
+// type or the sums (2^64, for fp16 2^15) sends the tile through again at once.  m only scales
+// sums in floating point, so how far it trails costs no precision.  S_{j+1} being complete
+// means that O += P_j V_j is, since it was issued before.
 //
 // What a mask hides has no part in a row: hidden scores are replaced, not multiplied, and V
 // rows beyond the sequence are zeroed in shared memory.  A V row within the sequence that some
@@ -67,9 +69,9 @@ struct Cfg {
     static constexpr int BOXES = DIM / 64;                     // 128-byte wide boxes of a tile
     static constexpr uint32_t BOX_BYTES = BM * 128;
     static constexpr uint32_t TILE_BYTES = BOXES * BOX_BYTES;  // a Q, K or V tile
-    static constexpr int SLOTS = DIM == 128 ? 5 : 8;           // K / V ring
+    static constexpr int STAGES = DIM == 128 ? 2 : 4;          // ring of {V_j, K_{j+1}}; K_0 apart
     static constexpr uint32_t Q_BYTES = 2 * TILE_BYTES;
-    static constexpr size_t SMEM = 1024 + Q_BYTES + SLOTS * TILE_BYTES + 512;
+    static constexpr size_t SMEM = 1024 + Q_BYTES + (1 + 2 * STAGES) * TILE_BYTES + 512;
     static_assert(SMEM <= 232448, "shared memory budget");
 };
 
@@ -102,21 +104,15 @@ struct Item {
     __device__ __forceinline__ int lo(int r) const { return window ? max(r + offset - window + 1, 0) : 0; }
     __device__ __forceinline__ int last_row(int t) const { return min(BM * t + BM, rows) - 1; }
     __device__ __forceinline__ bool any(int t) const { return BM * t < rows && hi(last_row(t)) >= 0; }
-    // whether any row of query tile t sees a key of the tile at k0
-    __device__ __forceinline__ bool active(int t, int k0) const
-    {
-        return any(t) && hi(last_row(t)) >= k0 && (k0 + BM > lo(BM * t) || k0 < sinks);
-    }
+    // key tiles that query tile t has a part in: j < heads() (first tokens) or begin(t) <= j, up
+    // to last(t) (-1: none)
+    __device__ __forceinline__ int heads() const { return prefix + (max(sinks - BM * first, 0) + BM - 1) / BM; }
+    __device__ __forceinline__ int last(int t) const { return any(t) ? prefix + hi(last_row(t)) / BM - first : -1; }
+    __device__ __forceinline__ int begin(int t) const { return prefix + max(lo(BM * t) / BM - first, 0); }
     // whether some row does not see all of it
     __device__ __forceinline__ bool partial(int t, int k0) const
     {
         return k0 + BM - 1 > hi(BM * t) || (lo(last_row(t)) > k0 && k0 + BM > sinks);
-    }
-    // the last j that is active for tile t, given any(t)
-    __device__ __forceinline__ int last(int t) const
-    {
-        const int kt = hi(last_row(t)) / BM;
-        return kt < prefix ? kt : prefix + kt - first;
     }
 };
 
@@ -135,6 +131,12 @@ __device__ __forceinline__ int64_t sequence_of_slot(const int32_t* cu, int64_t b
     return lo;
 }
 
+// The key tiles of one query tile, as the roles test them.
+struct Active {
+    int heads, begin, last;
+    __device__ __forceinline__ bool operator()(int j) const { return j <= last && (j < heads || j >= begin); }
+};
+
 // ---- tensor core pieces beyond ck_device.cuh's
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int32_t c0, int32_t c1,
                                             int32_t c2)
@@ -146,21 +148,29 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
         : "memory");
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t yes;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+    return yes != 0;
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add)
 {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        "l"(a), "l"(b), "r"(idesc), "r"(add)
         : "memory");
 }
 
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add)
 {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        "r"(a), "l"(b), "r"(idesc), "r"(add)
         : "memory");
 }
 
@@ -231,25 +241,27 @@ __global__ void __launch_bounds__(THREADS, 1)
 {
     using C = Cfg<DIM>;
     using T = typename E::T;
-    constexpr int SLOTS = C::SLOTS;
+    constexpr int STAGES = C::STAGES;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* s_q = smem;
-    uint8_t* s_kv = smem + C::Q_BYTES;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(s_kv + (size_t)SLOTS * C::TILE_BYTES);
+    uint8_t* s_k0 = smem + C::Q_BYTES;
+    uint8_t* s_ring = s_k0 + C::TILE_BYTES;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(s_ring + (size_t)2 * STAGES * C::TILE_BYTES);
     uint64_t* q_full = bars;             // [2]
     uint64_t* s_full = bars + 2;         // [2] S_t is complete (and every product before it)
     uint64_t* p_full = bars + 4;         // [2] P_t is written, O_t may be added to
     uint64_t* o_full = bars + 6;         // [2] O_t is final
-    uint64_t* drain = bars + 8;
-    uint64_t* kv_full = bars + 9;        // [SLOTS] a tile has landed
-    uint64_t* kv_empty = kv_full + SLOTS;  // [SLOTS] its products are done
-    uint64_t* v_ready = kv_empty + SLOTS;  // [SLOTS] looked over
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(v_ready + SLOTS);
+    uint64_t* k0_full = bars + 8;
+    uint64_t* drain = bars + 9;
+    uint64_t* full = bars + 10;          // [STAGES] V_j and K_{j+1} have landed
+    uint64_t* ready = full + STAGES;     // [STAGES] and V_j is looked over
+    uint64_t* empty = ready + STAGES;    // [STAGES] their products are done
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(empty + STAGES);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     volatile int* dirty = abort_flag + 1;  // a V row holds an infinity or NaN
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (warp == 0 && lane == 0) {
         for (int t = 0; t < 2; ++t) {
             mbar_init(&q_full[t], 1);
@@ -257,11 +269,12 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(&p_full[t], 4);
             mbar_init(&o_full[t], 1);
         }
+        mbar_init(k0_full, 1);
         mbar_init(drain, 1);
-        for (int s = 0; s < SLOTS; ++s) {
-            mbar_init(&kv_full[s], 1);
-            mbar_init(&kv_empty[s], 1);
-            mbar_init(&v_ready[s], 2);
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&ready[s], 2);
+            mbar_init(&empty[s], 1);
         }
         *abort_flag = 0;
         *dirty = 0;
@@ -279,7 +292,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     griddep_wait();
 
     // ---- this block's share; blocks start in order, so the last (for causal prompts the
@@ -317,6 +330,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         if (bad && threadIdx.x == 0)
             atomicOr(err, kErrIndex);
+        w.rows = __shfl_sync(0xffffffffu, w.rows, 0);
+        w.keys = __shfl_sync(0xffffffffu, w.keys, 0);
+        w.offset = __shfl_sync(0xffffffffu, w.offset, 0);
+        w.prefix = __shfl_sync(0xffffffffu, w.prefix, 0);
+        w.first = __shfl_sync(0xffffffffu, w.first, 0);
+        w.count = __shfl_sync(0xffffffffu, w.count, 0);
     }
 
     if (warp < 4) {
@@ -324,41 +343,40 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (warp == 0) {
             // ---------------------------------------------------------------- copies
             if (lane == 0 && w.count > 0) {
-                uint32_t issued = 0;
-                bool ok = true;
-                auto load_q = [&](int t) {
-                    if (!w.any(t))
-                        return;
-                    mbar_arrive_expect_tx(&q_full[t], C::TILE_BYTES);
+                auto load = [&](const CUtensorMap* map, uint8_t* dst, uint64_t* bar, int h, int64_t row) {
                     for (int x = 0; x < C::BOXES; ++x)
-                        tma_load_3d(s_q + t * C::TILE_BYTES + x * C::BOX_BYTES, &tmQ, &q_full[t], x * 64, head,
-                                    (int32_t)(w.q_row + BM * t));
+                        tma_load_3d(dst + x * C::BOX_BYTES, map, bar, x * 64, h, (int32_t)row);
+                };
+                auto load_q = [&](int t) {
+                    if (w.any(t)) {
+                        mbar_arrive_expect_tx(&q_full[t], C::TILE_BYTES);
+                        load(&tmQ, s_q + t * C::TILE_BYTES, &q_full[t], head, w.q_row + BM * t);
+                    }
                 };
                 load_q(0);
-                int s = 0;
-                uint32_t phase = 0;
-                for (int u = 0; ok && u < 2 * w.count; ++u) {  // K_0, V_0, K_1, V_1, ..
-                    if (!mbar_wait(&kv_empty[s], phase ^ 1u, abort_flag, err, kErrWaitAttention, TIMEOUT_NS)) {
+                mbar_arrive_expect_tx(k0_full, C::TILE_BYTES);
+                load(&tmK, s_k0, k0_full, kv_head, w.k_row + w.key0(0));
+                load_q(1);
+                bool ok = true;
+                int j = 0;
+                for (; j < w.count; ++j) {
+                    const int s = j % STAGES;
+                    if (!mbar_wait(&empty[s], (uint32_t)(j / STAGES + 1) & 1u, abort_flag, err, kErrWaitAttention,
+                                   TIMEOUT_NS)) {
                         ok = false;
                         break;
                     }
-                    const CUtensorMap* map = (u & 1) ? &tmV : &tmK;
-                    mbar_arrive_expect_tx(&kv_full[s], C::TILE_BYTES);
-                    for (int x = 0; x < C::BOXES; ++x)
-                        tma_load_3d(s_kv + (size_t)s * C::TILE_BYTES + x * C::BOX_BYTES, map, &kv_full[s], x * 64, kv_head,
-                                    (int32_t)(w.k_row + w.key0(u >> 1)));
-                    if (u == 0)
-                        load_q(1);
-                    issued = (issued & ~(3u << (2 * s))) | ((2u | phase) << (2 * s));
-                    if (++s == SLOTS) {
-                        s = 0;
-                        phase ^= 1u;
-                    }
+                    const bool more = j + 1 < w.count;
+                    uint8_t* dst = s_ring + (size_t)s * 2 * C::TILE_BYTES;
+                    mbar_arrive_expect_tx(&full[s], more ? 2 * C::TILE_BYTES : C::TILE_BYTES);
+                    load(&tmV, dst, &full[s], kv_head, w.k_row + w.key0(j));
+                    if (more)
+                        load(&tmK, dst + C::TILE_BYTES, &full[s], kv_head, w.k_row + w.key0(j + 1));
                 }
                 if (!ok) {  // aborting: every issued copy lands before shared memory is released
-                    for (int i = 0; i < SLOTS; ++i)
-                        if ((issued >> (2 * i)) & 2u)
-                            wait_out(&kv_full[i], (issued >> (2 * i)) & 1u, err);
+                    for (int i = max(0, j - STAGES); i < j; ++i)
+                        wait_out(&full[i % STAGES], (uint32_t)(i / STAGES) & 1u, err);
+                    wait_out(k0_full, 0, err);
                     for (int t = 0; t < 2; ++t)
                         if (w.any(t))
                             wait_out(&q_full[t], 0, err);
@@ -367,95 +385,118 @@ __global__ void __launch_bounds__(THREADS, 1)
             __syncwarp();
         } else if (warp == 1) {
             // -------------------------------------------------------------- products
-            if (lane == 0 && w.count > 0) {
+            // The whole warp walks the tiles, so that descriptors stay uniform values, and one
+            // elected lane issues; the others wait for it after each issue (left to run ahead into
+            // the next barrier's polling loop they can keep it from being scheduled).
+            if (w.count > 0) {
                 const uint32_t idesc_s = idesc_of<E>(BM, false) | (p.negate ? 1u << 13 : 0u);
                 constexpr uint32_t idesc_o = idesc_of<E>(DIM, true);
                 const uint64_t q_desc = desc_kmajor_sw128(smem_u32(s_q));
-                const uint64_t k_desc = desc_kmajor_sw128(smem_u32(s_kv));
-                const uint64_t v_desc = desc_nmajor_sw128(smem_u32(s_kv), C::BOX_BYTES);
+                const uint64_t k0_desc = desc_kmajor_sw128(smem_u32(s_k0));
+                const uint64_t k_desc = desc_kmajor_sw128(smem_u32(s_ring) + C::TILE_BYTES);
+                const uint64_t v_desc = desc_nmajor_sw128(smem_u32(s_ring), C::BOX_BYTES);
                 constexpr uint64_t kTile = C::TILE_BYTES >> 4, kBox = C::BOX_BYTES >> 4;
-                bool q_seen[2] = {false, false}, started[2] = {false, false};
+                const Active active[2] = {{w.heads(), w.begin(0), w.last(0)}, {w.heads(), w.begin(1), w.last(1)}};
+                bool started[2] = {false, false}, q_seen[2] = {false, false};
                 uint32_t p_phase[2] = {0, 0};
-                bool ok = true;
-                // ring uses in order: K_j is use 2 j, V_j use 2 j + 1
-                auto slot_of = [](int u) { return u % SLOTS; };
-                auto parity_of = [](int u) { return (uint32_t)(u / SLOTS) & 1u; };
-                // with an odd number of slots each holds K and V tiles by turns
-                auto v_parity_of = [](int u) { return (uint32_t)(u / (SLOTS % 2 ? 2 * SLOTS : SLOTS)) & 1u; };
                 auto wait = [&](uint64_t* bar, uint32_t parity) {
-                    ok = ok && mbar_wait(bar, parity, abort_flag, err, kErrWaitAttention, TIMEOUT_NS);
-                    return ok;
+                    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
+                        return true;
+                    const bool ok = mbar_wait(bar, parity, abort_flag, err, kErrWaitAttention, TIMEOUT_NS);
+                    return __all_sync(0xffffffffu, ok) != 0;
                 };
-                auto scores = [&](int t, int s) {
-                    if (!q_seen[t] && !wait(&q_full[t], 0))
-                        return;
-                    q_seen[t] = true;
-                    tc_fence_after();
-                    const uint64_t a = q_desc + t * kTile, b = k_desc + s * kTile;
+                const bool leader = elect_one();
+                auto scores = [&](int t, uint64_t b) {  // S_t = Q_t K^T
+                    const uint64_t a = q_desc + t * kTile;
 #pragma unroll
                     for (int k = 0; k < DIM / 16; ++k)
                         mma_ss(tmem + t * BM, a + (k / 4) * kBox + (k % 4) * 2, b + (k / 4) * kBox + (k % 4) * 2, idesc_s,
                                k > 0);
                     mma_commit(&s_full[t]);
                 };
-                const int j0 = 0;
-                if (wait(&kv_full[slot_of(0)], parity_of(0))) {
-                    for (int t = 0; ok && t < 2; ++t)
-                        if (w.active(t, w.key0(j0)))
-                            scores(t, slot_of(0));
-                    mma_commit(&kv_empty[slot_of(0)]);
-                }
-                for (int j = 0; ok && j < w.count; ++j) {
-                    const int k0 = w.key0(j);
-                    const int vu = 2 * j + 1, ku = 2 * j + 2;
-                    const bool more = j + 1 < w.count;
-                    for (int t = 0; ok && t < 2; ++t) {
-                        if (t == 0 && !wait(&v_ready[slot_of(vu)], v_parity_of(vu)))
-                            break;
-                        if (w.active(t, k0)) {
-                            if (!wait(&p_full[t], p_phase[t]))
-                                break;
-                            p_phase[t] ^= 1u;
-                            tc_fence_after();
-                            const uint64_t b = v_desc + slot_of(vu) * kTile;
+                auto values = [&](int t, uint64_t b) {  // O_t += P_t V
 #pragma unroll
-                            for (int k = 0; k < BM / 16; ++k)
-                                mma_ts(tmem + 2 * BM + t * DIM, tmem + t * BM + k * 8, b + k * (16 * 128 >> 4), idesc_o,
-                                       started[t] || k > 0);
-                            started[t] = true;
-                            if (j == w.last(t))
-                                mma_commit(&o_full[t]);
+                    for (int k = 0; k < BM / 16; ++k)
+                        mma_ts(tmem + 2 * BM + t * DIM, tmem + t * BM + k * 8, b + k * (16 * 128 >> 4), idesc_o,
+                               k > 0 || started[t]);
+                };
+                auto q_here = [&](int t) {
+                    if (!q_seen[t] && !wait(&q_full[t], 0))
+                        return false;
+                    q_seen[t] = true;
+                    return true;
+                };
+                // The tensor core takes a product about as fast as one thread issues it and queues
+                // only a few, and every step of this warp beside the busy softmax warps takes some
+                // 100 cycles: so one wait and one branch stand between two groups of products.
+                auto run = [&]() {
+                    if (!wait(k0_full, 0))
+                        return;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+                        if (active[t](0)) {
+                            if (!q_here(t))
+                                return;
+                            tc_fence_after();
+                            if (leader)
+                                scores(t, k0_desc);
+                            __syncwarp();
                         }
-                        if (t == 1)
-                            mma_commit(&kv_empty[slot_of(vu)]);
-                        if (more) {
-                            if (t == 0 && !wait(&kv_full[slot_of(ku)], parity_of(ku)))
-                                break;
-                            if (w.active(t, w.key0(j + 1)))
-                                scores(t, slot_of(ku));
-                            if (t == 1)
-                                mma_commit(&kv_empty[slot_of(ku)]);
+                    for (int j = 0; j < w.count; ++j) {
+                        const int s = j % STAGES;
+                        const uint64_t v = v_desc + s * 2 * kTile, k = k_desc + s * 2 * kTile;
+                        const bool more = j + 1 < w.count;
+                        if (!wait(&ready[s], (uint32_t)(j / STAGES) & 1u))
+                            return;
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            const bool now = active[t](j), next = more && active[t](j + 1);
+                            if (next && !q_here(t))
+                                return;
+                            if (now) {
+                                if (!wait(&p_full[t], p_phase[t]))
+                                    return;
+                                p_phase[t] ^= 1u;
+                            }
+                            tc_fence_after();
+                            if (leader) {
+                                if (now) {
+                                    values(t, v);
+                                    if (j == active[t].last)
+                                        mma_commit(&o_full[t]);
+                                }
+                                if (next)
+                                    scores(t, k);
+                                if (t == 1)
+                                    mma_commit(&empty[s]);
+                            }
+                            __syncwarp();
+                            started[t] |= now;
                         }
                     }
-                }
+                };
+                run();
                 // every product must be complete before tensor and shared memory are released
-                mma_commit(drain);
-                wait_out(drain, 0, err);
+                if (leader) {
+                    mma_commit(drain);
+                    wait_out(drain, 0, err);
+                }
             }
             __syncwarp();
         } else {
             // -------------------------------------------------- V tiles, before their use
             const int tid = threadIdx.x - 64;  // 0..63: rows tid and tid + 64
+            const Active active0 = {w.heads(), w.begin(0), w.last(0)}, active1 = {w.heads(), w.begin(1), w.last(1)};
             for (int j = 0; j < w.count; ++j) {
-                const int u = 2 * j + 1, s = u % SLOTS;
-                const bool ok = mbar_wait(&kv_full[s], (uint32_t)(u / SLOTS) & 1u, abort_flag, err, kErrWaitAttention,
+                const int s = j % STAGES;
+                const bool ok = mbar_wait(&full[s], (uint32_t)(j / STAGES) & 1u, abort_flag, err, kErrWaitAttention,
                                           TIMEOUT_NS);
                 if (!__all_sync(0xffffffffu, ok))
                     break;
                 const int k0 = w.key0(j);
-                const bool check = (w.active(0, k0) && w.partial(0, k0)) || (w.active(1, k0) && w.partial(1, k0));
+                const bool check = (active0(j) && w.partial(0, k0)) || (active1(j) && w.partial(1, k0));
                 if (check) {
-                    uint8_t* tile = s_kv + (size_t)s * C::TILE_BYTES;
+                    uint8_t* tile = s_ring + (size_t)s * 2 * C::TILE_BYTES;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int r = tid + 64 * h;
@@ -487,7 +528,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(&v_ready[s]);
+                    mbar_arrive(&ready[s]);
+                __syncwarp();  // before the next wait, as for the products
             }
             __syncwarp();
         }
@@ -501,95 +543,117 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         const uint32_t s_addr = tmem + lanes + t * BM, o_addr = tmem + lanes + 2 * BM + t * DIM;
         const int hi = w.hi(r), lo = w.lo(r);
+        const Active active = {w.heads(), w.begin(t), w.last(t)};
         const float c = p.c;
+        // how far (log2) weights may exceed 1 before the tile has to be done again
+        constexpr float kHard = std::is_same<E, Bf16>::value ? 64.0f : 15.0f;
         float m = -INFINITY;  // what the row's sums are relative to, in units of scores
+        float top = -INFINITY;
         float l = 0.0f;
         uint32_t phase = 0;
         bool started = false, ok = true;
+        // bring the row's sums to the maximum `top`, where `raise`
+        auto raise_to_top = [&](bool raise) {
+            const float f = raise ? fast_exp2((m - top) * c) : 1.0f;
+            if (raise)
+                m = top;
+            l *= f;
+            if (!started)
+                return;
+#pragma unroll 1
+            for (int i = 0; i < DIM / 16; ++i) {
+                uint32_t v[16];
+                tmem_ld_32x32b_x16(o_addr + 16 * i, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int n = 0; n < 16; ++n)
+                    v[n] = __float_as_uint(__uint_as_float(v[n]) * f);
+                tmem_st_32x32b_x16(o_addr + 16 * i, v);
+            }
+        };
         for (int j = 0; j < w.count; ++j) {
-            const int k0 = w.key0(j);
-            if (!w.active(t, k0))
+            if (!active(j))
                 continue;
+            const int k0 = w.key0(j);
             ok = mbar_wait(&s_full[t], phase, abort_flag, err, kErrWaitAttention, TIMEOUT_NS);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok)
                 break;
             phase ^= 1u;
             tc_fence_after();
-            uint32_t sr[4][32];
+            const bool raise = (top - m) * c > kLag;  // found in the last tile
+            if (__any_sync(0xffffffffu, raise))
+                raise_to_top(raise);
+            const bool masked = w.partial(t, k0);
+            uint32_t packed[4][16];
+            float2 sum;
+            bool first = !started;
+            for (;;) {
+                uint32_t sr[4][32];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                tmem_ld_32x32b_x32(s_addr + 32 * i, sr[i]);
-            tmem_wait_ld();
-            if (w.partial(t, k0)) {
+                for (int i = 0; i < 4; ++i)
+                    tmem_ld_32x32b_x32(s_addr + 32 * i, sr[i]);
+                tmem_wait_ld();
+                if (masked) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        // bit n: key k0 + 32 i + n is seen (k <= hi and (k >= lo or k < sinks))
+                        const int a = k0 + 32 * i;
+                        const int nh = hi - a + 1, nl = lo - a, ns = w.sinks - a;
+                        const uint32_t upto = nh <= 0 ? 0u : nh >= 32 ? 0xffffffffu : (1u << nh) - 1u;
+                        const uint32_t below = nl <= 0 ? 0u : nl >= 32 ? 0xffffffffu : (1u << nl) - 1u;
+                        const uint32_t head = ns <= 0 ? 0u : ns >= 32 ? 0xffffffffu : (1u << ns) - 1u;
+                        const uint32_t seen = upto & (~below | head);
+#pragma unroll
+                        for (int n = 0; n < 32; ++n)
+                            sr[i][n] = (seen >> n) & 1u ? sr[i][n] : 0xff800000u;
+                    }
+                }
+                if (first) {  // the row's first tile: its own maximum
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int n = 0; n < 32; ++n)
+                            m = fmaxf(m, __uint_as_float(sr[i][n]));
+                    first = false;
+                }
+                const float mc = m == -INFINITY ? 0.0f : -m * c;  // no key seen yet: weights 0
+                const float2 c2 = make_float2(c, c), mc2 = make_float2(mc, mc);
+                sum = make_float2(0.0f, 0.0f);
+                float tops[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    // bit n: key k0 + 32 i + n is seen (k <= hi and (k >= lo or k < sinks))
-                    const int a = k0 + 32 * i;
-                    const int nh = hi - a + 1, nl = lo - a, ns = w.sinks - a;
-                    const uint32_t upto = nh <= 0 ? 0u : nh >= 32 ? 0xffffffffu : (1u << nh) - 1u;
-                    const uint32_t below = nl <= 0 ? 0u : nl >= 32 ? 0xffffffffu : (1u << nl) - 1u;
-                    const uint32_t first = ns <= 0 ? 0u : ns >= 32 ? 0xffffffffu : (1u << ns) - 1u;
-                    const uint32_t seen = upto & (~below | first);
+                    tops[i] = -INFINITY;
 #pragma unroll
-                    for (int n = 0; n < 32; ++n)
-                        sr[i][n] = (seen >> n) & 1u ? sr[i][n] : 0xff800000u;
+                    for (int n = 0; n < 16; ++n) {
+                        const float a = __uint_as_float(sr[i][2 * n]), b = __uint_as_float(sr[i][2 * n + 1]);
+                        float2 x = f2_fma_rn(make_float2(a, b), c2, mc2);
+                        tops[i] = fmaxf(tops[i], fmaxf(a, b));
+                        x.x = fast_exp2(x.x);
+                        x.y = fast_exp2(x.y);
+                        sum = f2_add_rn(sum, x);
+                        packed[i][n] = E::pack2(x.x, x.y);
+                    }
                 }
-            }
-            float tops[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                tops[i] = __uint_as_float(sr[i][0]);
-#pragma unroll
-                for (int n = 1; n < 31; n += 2)
-                    tops[i] = fmaxf(tops[i], fmaxf(__uint_as_float(sr[i][n]), __uint_as_float(sr[i][n + 1])));
-                tops[i] = fmaxf(tops[i], __uint_as_float(sr[i][31]));
-            }
-            const float top = fmaxf(m, fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])));
-            const bool raise = (top - m) * c > kLag;
-            if (!started) {
-                m = top;
-            } else if (__any_sync(0xffffffffu, raise)) {
-                // rare: bring the row's sums to the new maximum
-                const float f = raise ? fast_exp2((m - top) * c) : 1.0f;
-                if (raise)
-                    m = top;
-                l *= f;
-#pragma unroll 1
-                for (int i = 0; i < DIM / 16; ++i) {
-                    uint32_t v[16];
-                    tmem_ld_32x32b_x16(o_addr + 16 * i, v);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int n = 0; n < 16; ++n)
-                        v[n] = __float_as_uint(__uint_as_float(v[n]) * f);
-                    tmem_st_32x32b_x16(o_addr + 16 * i, v);
-                }
-            }
-            started = true;
-            const float mc = m == -INFINITY ? 0.0f : -m * c;  // no key seen yet: weights 0
-            const float2 c2 = make_float2(c, c), mc2 = make_float2(mc, mc);
-            float2 sum = make_float2(0.0f, 0.0f);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t w16[16];
-#pragma unroll
-                for (int n = 0; n < 16; ++n) {
-                    float2 x = f2_fma_rn(make_float2(__uint_as_float(sr[i][2 * n]), __uint_as_float(sr[i][2 * n + 1])), c2,
-                                         mc2);
-                    x.x = fast_exp2(x.x);
-                    x.y = fast_exp2(x.y);
-                    sum = f2_add_rn(sum, x);
-                    w16[n] = E::pack2(x.x, x.y);
-                }
-                tmem_st_32x32b_x16(s_addr + 16 * i, w16);
+                top = fmaxf(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])), m);
+                // S is still there: a weight beyond what its type and the sums hold sends the
+                // tile through again, relative to the maximum just found
+                const bool over = (top - m) * c > kHard;
+                if (!__any_sync(0xffffffffu, over))
+                    break;
+                raise_to_top(over);
             }
             l += sum.x + sum.y;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                tmem_st_32x32b_x16(s_addr + 16 * i, packed[i]);
+            started = true;
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&p_full[t]);
+            __syncwarp();  // before the next wait, as for the products
         }
         // ---- the rows' outputs
         const int64_t out_row = w.q_row + r;
