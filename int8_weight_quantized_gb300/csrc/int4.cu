@@ -25,8 +25,8 @@ __device__ __forceinline__ int code_shift(int e)
 
 // Bound: HBM, N K / 2 bytes of codes and 2 N K / group of scales, read once.
 //
-// A block takes 16 RT weight rows and its 8 warps share out K in chunks of 128, each warp a
-// contiguous run; a warp streams its run's codes and scales through its own ring of
+// A block's 8 warps are 8 / KW row groups of 16 RT weight rows each, and KW warps share out a
+// group's K in chunks of 128, each a contiguous run; a warp streams its run's codes and scales through its own ring of
 // asynchronous copies, with no block-wide barrier until the warps' sums are added, in a fixed
 // order, at the end.  x, which every block reads whole, comes from L2 straight into the
 // registers that the products take, a chunk ahead: in the ring it would take twice the codes'
@@ -64,7 +64,7 @@ template <int RT>
 constexpr int kUnit = 16 * RT * (W_LD + 8);  // codes, then 8 bytes of scales a row
 
 // PER_CHUNK: scales of a row in a chunk (4, 2 or 1 for groups of 32, 64, and 128 or 256)
-template <class E, int RT, int MT, int PER_CHUNK>
+template <class E, int RT, int MT, int PER_CHUNK, int KW>
 __global__ void __launch_bounds__(WARPS * 32) int4_kernel(const Int4Linear p)
 {
     using T = typename E::T;
@@ -72,11 +72,13 @@ __global__ void __launch_bounds__(WARPS * 32) int4_kernel(const Int4Linear p)
     griddep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
-    const int64_t n0 = (int64_t)blockIdx.x * (16 * RT);
+    constexpr int RW = WARPS / KW;             // row groups
+    const int kw = warp % KW, rw = warp / KW;  // this warp's share of K, its row group
+    const int64_t n0 = ((int64_t)blockIdx.x * RW + rw) * (16 * RT);
     const int64_t m0 = (int64_t)blockIdx.y * (8 * MT);
     const int rows = (int)min((int64_t)(8 * MT), p.M - m0);      // rows of x
     const int chunks = (int)(p.K / CHUNK);
-    const int c0 = (int)((int64_t)warp * chunks / WARPS), c1 = (int)((int64_t)(warp + 1) * chunks / WARPS);
+    const int c0 = (int)((int64_t)kw * chunks / KW), c1 = (int)((int64_t)(kw + 1) * chunks / KW);
     const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * STAGES * kUnit<RT>);
     const int64_t groups = p.K / p.group;
     const int log_chunks = p.group == 256 ? 1 : 0;  // chunks a group spans, PER_CHUNK == 1
@@ -207,15 +209,17 @@ __global__ void __launch_bounds__(WARPS * 32) int4_kernel(const Int4Linear p)
                     red[(warp * rows + m) * LD + 16 * rt + 8 * (i >> 1) + g] = sum[rt][mt][i];
             }
     __syncthreads();
-    for (int i = threadIdx.x; i < rows * 16 * RT; i += WARPS * 32) {
-        const int m = i / (16 * RT), r = i - m * (16 * RT);
-        const int64_t n = n0 + r;
+    constexpr int BLOCK_ROWS = 16 * RT * RW;
+    for (int i = threadIdx.x; i < rows * BLOCK_ROWS; i += WARPS * 32) {
+        const int m = i / BLOCK_ROWS, r = i % BLOCK_ROWS;
+        const int64_t n = (int64_t)blockIdx.x * BLOCK_ROWS + r;
         if (n >= p.N)
             continue;
+        const int first = r / (16 * RT) * KW;  // the row group's first warp
         float v = 0.0f;
 #pragma unroll
-        for (int k = 0; k < WARPS; ++k)
-            v += red[(k * rows + m) * LD + r];
+        for (int k = 0; k < KW; ++k)
+            v += red[((first + k) * rows + m) * LD + r % (16 * RT)];
         if (p.bias != nullptr)
             v += E::to(static_cast<const T*>(p.bias)[n]);
         const int64_t at = (m0 + m) * p.N + n;
@@ -285,7 +289,7 @@ __global__ void __launch_bounds__(256) int4_pack_kernel(const int8_t* codes, int
 
 namespace {
 
-template <class E, int RT, int MT, int PER_CHUNK>
+template <class E, int RT, int MT, int PER_CHUNK, int KW>
 cudaError_t launch(const Int4Linear& p, cudaStream_t s)
 {
     constexpr size_t smem = std::max((size_t)WARPS * STAGES * kUnit<RT>,         // the rings
@@ -295,29 +299,46 @@ cudaError_t launch(const Int4Linear& p, cudaStream_t s)
     int done = 0;
     cudaError_t e = cache.get(&done, [](int* d) {
         *d = 1;
-        return cudaFuncSetAttribute(int4_kernel<E, RT, MT, PER_CHUNK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(int4_kernel<E, RT, MT, PER_CHUNK, KW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     (int)smem);
     });
     if (e != cudaSuccess)
         return e;
-    const dim3 grid((unsigned)((p.N + 16 * RT - 1) / (16 * RT)), (unsigned)((p.M + 8 * MT - 1) / (8 * MT)));
-    return launch_pdl(int4_kernel<E, RT, MT, PER_CHUNK>, grid, dim3(WARPS * 32), smem, s, p);
+    constexpr int ROWS = 16 * RT * WARPS / KW;
+    const dim3 grid((unsigned)((p.N + ROWS - 1) / ROWS), (unsigned)((p.M + 8 * MT - 1) / (8 * MT)));
+    return launch_pdl(int4_kernel<E, RT, MT, PER_CHUNK, KW>, grid, dim3(WARPS * 32), smem, s, p);
 }
 
-template <class E, int RT, int MT>
+template <class E, int RT, int MT, int KW>
 cudaError_t by_group(const Int4Linear& p, cudaStream_t s)
 {
-    return p.group == 32 ? launch<E, RT, MT, 4>(p, s) : p.group == 64 ? launch<E, RT, MT, 2>(p, s) : launch<E, RT, MT, 1>(p, s);
+    return p.group == 32   ? launch<E, RT, MT, 4, KW>(p, s)
+           : p.group == 64 ? launch<E, RT, MT, 2, KW>(p, s)
+                           : launch<E, RT, MT, 1, KW>(p, s);
+}
+
+// KW: long runs of K per warp spread its set-up over more work, short ones give a narrow layer
+// enough warps: the fewest warps per row group that still make two blocks per SM.
+template <class E, int RT, int MT>
+cudaError_t by_split(const Int4Linear& p, const DeviceInfo& dev, cudaStream_t s)
+{
+    const int64_t blocks1 = (p.N + 16 * RT * WARPS - 1) / (16 * RT * WARPS);  // at KW = 1
+    const int64_t want = 2 * dev.sm_count;
+    if (blocks1 * 2 >= want)
+        return by_group<E, RT, MT, 2>(p, s);
+    if (blocks1 * 4 >= want)
+        return by_group<E, RT, MT, 4>(p, s);
+    return by_group<E, RT, MT, 8>(p, s);
 }
 
 template <class E>
-cudaError_t by_rows(const Int4Linear& p, cudaStream_t s)
+cudaError_t by_rows(const Int4Linear& p, const DeviceInfo& dev, cudaStream_t s)
 {
     if (p.M <= 8)
-        return by_group<E, 1, 1>(p, s);
+        return by_split<E, 1, 1>(p, dev, s);
     if (p.M <= 16)
-        return by_group<E, 2, 2>(p, s);
-    return by_group<E, 2, 4>(p, s);
+        return by_split<E, 2, 2>(p, dev, s);
+    return by_split<E, 2, 4>(p, dev, s);
 }
 
 }  // namespace
@@ -330,8 +351,7 @@ size_t int4_linear_workspace(int64_t M, int64_t N, int64_t K)
 
 cudaError_t launch_int4_linear(const Int4Linear& p, const DeviceInfo& dev, cudaStream_t s)
 {
-    (void)dev;
-    return p.f16 ? by_rows<Fp16>(p, s) : by_rows<Bf16>(p, s);
+    return p.f16 ? by_rows<Fp16>(p, dev, s) : by_rows<Bf16>(p, dev, s);
 }
 
 cudaError_t launch_int4_weight(const float* W, int64_t N, int64_t K, int group, uint32_t* w4, void* w_scale,

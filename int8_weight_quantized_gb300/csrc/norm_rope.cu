@@ -54,8 +54,8 @@ __global__ void __launch_bounds__(WARPS * 32) norm_rope_kernel(const NormRope p,
     const int group = threadIdx.x / LANES;
     const int heads = p.q_heads + 2 * p.kv_heads;
     const int chunks = (heads + HEADS_PER - 1) / HEADS_PER;
-    const int64_t unit = (int64_t)blockIdx.x * GROUPS + group;
-    const int64_t token = unit / chunks;
+    const uint32_t unit = blockIdx.x * GROUPS + group;  // tokens * heads is below 2^31
+    const int64_t token = unit / (uint32_t)chunks;
     if (token >= p.tokens)
         return;  // whole lane groups leave together; shuffles below name only their group
     const uint32_t mask = LANES == 32 ? 0xffffffffu : ((1u << LANES) - 1u) << ((threadIdx.x & 31) / LANES * LANES);
@@ -64,6 +64,16 @@ __global__ void __launch_bounds__(WARPS * 32) norm_rope_kernel(const NormRope p,
     const bool in = d0 < p.dim;       // dim % 8 == 0: a lane is all in or all out
     const bool rotated = d0 < p.rot;  // rot % 16 == 0, likewise
     const int half = p.rot / 2;
+
+    // the heads' loads first: they are in flight while the position and its angles arrive
+    const T* src = static_cast<const T*>(p.qkv) + token * p.qkv_stride;
+    uint4 raw[HEADS_PER];
+#pragma unroll
+    for (int j = 0; j < HEADS_PER; ++j)
+        if (in && h0 + j < heads)
+            raw[j] = __ldcs(reinterpret_cast<const uint4*>(src + (int64_t)(h0 + j) * p.dim + d0));
+        else
+            raw[j] = make_uint4(0, 0, 0, 0);
 
     // the token's angles for this lane's 8 values, and where it goes in the cache
     float cs[8], sn[8];
@@ -94,9 +104,10 @@ __global__ void __launch_bounds__(WARPS * 32) norm_rope_kernel(const NormRope p,
     if (p.cache.k != nullptr && h0 + HEADS_PER > p.q_heads) {
         const int64_t slot = __ldg(p.slots + token);
         const bool outside = slot >= p.cache.num_pages * p.cache.page_size;
-        if (slot >= 0 && !outside) {
-            page = slot / p.cache.page_size;
-            off = slot - page * p.cache.page_size;
+        if (slot >= 0 && !outside) {  // below 2^32 then: the cache's rows are
+            const uint32_t pg = (uint32_t)slot / (uint32_t)p.cache.page_size;
+            page = pg;
+            off = slot - (int64_t)pg * p.cache.page_size;
         }
         if (outside && lane == 0)
             atomicOr(err, kErrIndex);
@@ -104,14 +115,6 @@ __global__ void __launch_bounds__(WARPS * 32) norm_rope_kernel(const NormRope p,
     if (bad && lane == 0)
         atomicOr(err, kErrIndex);
 
-    const T* src = static_cast<const T*>(p.qkv) + token * p.qkv_stride;
-    uint4 raw[HEADS_PER];
-#pragma unroll
-    for (int j = 0; j < HEADS_PER; ++j)
-        if (in && h0 + j < heads)
-            raw[j] = __ldcs(reinterpret_cast<const uint4*>(src + (int64_t)(h0 + j) * p.dim + d0));
-        else
-            raw[j] = make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int j = 0; j < HEADS_PER; ++j) {
         const int h = h0 + j;
