@@ -239,6 +239,10 @@ int ck_paged_attention(const void* q, int64_t q_stride, const ck_kv_cache_t* cac
     p.scale = scale;
     p.window = window;
     p.sinks = sinks;
+    p.page_shift = -1;
+    if ((p.cache.page_size & (p.cache.page_size - 1)) == 0)
+        for (p.page_shift = 0; (1 << p.page_shift) < p.cache.page_size;)
+            ++p.page_shift;
     p.out = out;
     p.lse = lse;
     p.workspace = workspace;

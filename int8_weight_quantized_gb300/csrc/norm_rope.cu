@@ -10,10 +10,11 @@
 //          fp32 y, which is never rounded to 16 bits on the way
 //
 // Bound: HBM, each value read once and written once (twice where the keys are also kept
-// contiguous).  A head is shared by LANES = 8, 16 or 32 lanes of 8 values (one 16-byte load
-// and store each).  A group of lanes takes up to HEADS_PER heads of ONE token, one after the
-// other, so the token's cosines and sines are read once and kept in registers: read again
-// for each head they would be four times the head's own bytes in L1 traffic.
+// contiguous).  A head is shared by dim / 8 of LANES = 8, 16 or 32 lanes, 8 values each, as two
+// runs of 4 (8-byte loads and stores): for rotation by halves the runs are the two halves of 4
+// pairs, so that no value has to cross lanes (as one run of 8 they took 8 shuffles a head).  A
+// group of lanes takes up to HEADS_PER heads of ONE token, one after the other, so the token's
+// angles and the weights are read once and kept in registers.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -27,21 +28,16 @@ constexpr int WARPS = 4;
 constexpr int HEADS_PER = 4;  // heads a lane group takes, one after the other
 
 template <class E>
-__device__ __forceinline__ void unpack8(const uint4& r, float (&v)[8])
+__device__ __forceinline__ void unpack4(const uint2& r, float* v)
 {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = E::to2(w[i]);
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
-    }
+    const float2 a = E::to2(r.x), b = E::to2(r.y);
+    v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
 }
 
 template <class E>
-__device__ __forceinline__ uint4 pack8(const float (&v)[8])
+__device__ __forceinline__ uint2 pack4(const float* v)
 {
-    return make_uint4(E::pack2(v[0], v[1]), E::pack2(v[2], v[3]), E::pack2(v[4], v[5]), E::pack2(v[6], v[7]));
+    return make_uint2(E::pack2(v[0], v[1]), E::pack2(v[2], v[3]));
 }
 
 template <class E, int LANES>
@@ -60,44 +56,36 @@ __global__ void __launch_bounds__(WARPS * 32) norm_rope_kernel(const NormRope p,
         return;  // whole lane groups leave together; shuffles below name only their group
     const uint32_t mask = LANES == 32 ? 0xffffffffu : ((1u << LANES) - 1u) << ((threadIdx.x & 31) / LANES * LANES);
     const int h0 = (int)(unit - token * chunks) * HEADS_PER;
-    const int d0 = lane * 8;
-    const bool in = d0 < p.dim;       // dim % 8 == 0: a lane is all in or all out
-    const bool rotated = d0 < p.rot;  // rot % 16 == 0, likewise
+    const bool in = lane * 8 < p.dim;       // dim % 8 == 0: a lane is all in or all out
+    const bool rotated = lane * 8 < p.rot;  // rot % 16 == 0, likewise
     const int half = p.rot / 2;
+    // the lane's two runs of 4 values
+    const bool halves = rotated && !p.interleaved;
+    const int d0 = halves ? lane * 4 : lane * 8;
+    const int d1 = halves ? half + lane * 4 : d0 + 4;
 
     // the heads' loads first: they are in flight while the position and its angles arrive
-    const T* src = static_cast<const T*>(p.qkv) + token * p.qkv_stride;
-    uint4 raw[HEADS_PER];
+    const T* src = static_cast<const T*>(p.qkv) + token * p.qkv_stride + (int64_t)h0 * p.dim;
+    uint2 raw[HEADS_PER][2];
 #pragma unroll
-    for (int j = 0; j < HEADS_PER; ++j)
-        if (in && h0 + j < heads)
-            raw[j] = __ldcs(reinterpret_cast<const uint4*>(src + (int64_t)(h0 + j) * p.dim + d0));
-        else
-            raw[j] = make_uint4(0, 0, 0, 0);
+    for (int j = 0; j < HEADS_PER; ++j) {
+        const bool load = in && h0 + j < heads;
+        raw[j][0] = load ? __ldcs(reinterpret_cast<const uint2*>(src + j * p.dim + d0)) : make_uint2(0, 0);
+        raw[j][1] = load ? __ldcs(reinterpret_cast<const uint2*>(src + j * p.dim + d1)) : make_uint2(0, 0);
+    }
 
-    // the token's angles for this lane's 8 values, and where it goes in the cache
-    float cs[8], sn[8];
+    // the token's angles for the lane's 4 pairs, and where it goes in the cache
+    float cs[4], sn[4];
     bool bad = false;
     if (p.rot > 0 && h0 < p.q_heads + p.kv_heads) {
         const int64_t pos = __ldg(p.positions + token);
         bad = pos < 0 || pos >= p.max_pos;
         if (rotated && !bad) {
-            const float* row = p.cos_sin + pos * p.rot;
-            if (p.interleaved) {
-                const float4 c = __ldg(reinterpret_cast<const float4*>(row + d0 / 2));
-                const float4 s = __ldg(reinterpret_cast<const float4*>(row + half + d0 / 2));
-                cs[0] = cs[1] = c.x, cs[2] = cs[3] = c.y, cs[4] = cs[5] = c.z, cs[6] = cs[7] = c.w;
-                sn[0] = sn[1] = s.x, sn[2] = sn[3] = s.y, sn[4] = sn[5] = s.z, sn[6] = sn[7] = s.w;
-            } else {
-                const int i0 = d0 < half ? d0 : d0 - half;
-#pragma unroll
-                for (int i = 0; i < 8; i += 4) {
-                    const float4 c = __ldg(reinterpret_cast<const float4*>(row + i0 + i));
-                    const float4 s = __ldg(reinterpret_cast<const float4*>(row + half + i0 + i));
-                    cs[i] = c.x, cs[i + 1] = c.y, cs[i + 2] = c.z, cs[i + 3] = c.w;
-                    sn[i] = s.x, sn[i + 1] = s.y, sn[i + 2] = s.z, sn[i + 3] = s.w;
-                }
-            }
+            const float* row = p.cos_sin + pos * p.rot + lane * 4;
+            const float4 c = __ldg(reinterpret_cast<const float4*>(row));
+            const float4 s = __ldg(reinterpret_cast<const float4*>(row + half));
+            cs[0] = c.x, cs[1] = c.y, cs[2] = c.z, cs[3] = c.w;
+            sn[0] = s.x, sn[1] = s.y, sn[2] = s.z, sn[3] = s.w;
         }
     }
     int64_t page = -1, off = 0;
@@ -115,6 +103,9 @@ __global__ void __launch_bounds__(WARPS * 32) norm_rope_kernel(const NormRope p,
     if (bad && lane == 0)
         atomicOr(err, kErrIndex);
 
+    float w[8];           // the weights of queries or keys, whichever the last head was
+    int w_of = -1;
+    const float per_dim = 1.0f / (float)p.dim;
 #pragma unroll
     for (int j = 0; j < HEADS_PER; ++j) {
         const int h = h0 + j;
@@ -123,9 +114,22 @@ __global__ void __launch_bounds__(WARPS * 32) norm_rope_kernel(const NormRope p,
         const bool is_v = h >= p.q_heads + p.kv_heads;
         const bool is_q = h < p.q_heads;
         float v[8];
-        unpack8<E>(raw[j], v);
+        unpack4<E>(raw[j][0], v);
+        unpack4<E>(raw[j][1], v + 4);
         if (!is_v) {
             if (p.norm) {
+                if (w_of != (int)is_q) {
+                    w_of = is_q;
+                    const T* weight = static_cast<const T*>(is_q ? p.q_weight : p.k_weight);
+                    if (weight != nullptr && in) {
+                        unpack4<E>(__ldg(reinterpret_cast<const uint2*>(weight + d0)), w);
+                        unpack4<E>(__ldg(reinterpret_cast<const uint2*>(weight + d1)), w + 4);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            w[i] = 1.0f;
+                    }
+                }
                 float sum = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
@@ -133,39 +137,19 @@ __global__ void __launch_bounds__(WARPS * 32) norm_rope_kernel(const NormRope p,
 #pragma unroll
                 for (int o = LANES / 2; o; o >>= 1)
                     sum += __shfl_xor_sync(mask, sum, o);
-                const float inv = 1.0f / sqrtf(sum / (float)p.dim + p.eps);
-                float w[8];
-                const void* weight = is_q ? p.q_weight : p.k_weight;
-                if (weight != nullptr && in)
-                    unpack8<E>(__ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(weight) + d0)), w);
-                else
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        w[i] = 1.0f;
+                const float inv = rsqrtf(fmaf(sum, per_dim, p.eps));  // within 2 units of 2^-24
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     v[i] = v[i] * inv * w[i];
             }
-            if (p.rot > 0) {
-                float other[8];
-                if (p.interleaved) {
+            if (rotated && !bad) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        other[i] = v[i ^ 1];
-                } else {
-                    // the pair's other half lives rot / 16 lanes away (rot % 16 == 0)
-                    const int step = p.rot / 16;
-                    const int from = rotated ? (d0 < half ? lane + step : lane - step) : lane;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        other[i] = __shfl_sync(mask, v[i], from, LANES);
-                }
-                if (rotated && !bad) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const bool first = p.interleaved ? (i & 1) == 0 : d0 < half;
-                        v[i] = first ? v[i] * cs[i] - other[i] * sn[i] : v[i] * cs[i] + other[i] * sn[i];
-                    }
+                for (int i = 0; i < 4; ++i) {
+                    float& a = p.interleaved ? v[2 * i] : v[i];
+                    float& b = p.interleaved ? v[2 * i + 1] : v[4 + i];
+                    const float x = a * cs[i] - b * sn[i];
+                    b = b * cs[i] + a * sn[i];
+                    a = x;
                 }
             }
             if (bad)
@@ -173,14 +157,20 @@ __global__ void __launch_bounds__(WARPS * 32) norm_rope_kernel(const NormRope p,
                 for (int i = 0; i < 8; ++i)
                     v[i] = NAN;
         }
+        // two runs of four values of a row
+        auto store16 = [&](void* base, int64_t row) {
+            T* dst = static_cast<T*>(base) + row * p.dim;
+            *reinterpret_cast<uint2*>(dst + d0) = pack4<E>(v);
+            *reinterpret_cast<uint2*>(dst + d1) = pack4<E>(v + 4);
+        };
         if (is_q) {
             if (in)
-                *reinterpret_cast<uint4*>(static_cast<T*>(p.q_out) + (token * p.q_heads + h) * p.dim + d0) = pack8<E>(v);
+                store16(p.q_out, token * p.q_heads + h);
             continue;
         }
         const int hk = h - p.q_heads - (is_v ? p.kv_heads : 0);
         if (!is_v && p.k_out != nullptr && in)
-            *reinterpret_cast<uint4*>(static_cast<T*>(p.k_out) + (token * p.kv_heads + hk) * p.dim + d0) = pack8<E>(v);
+            store16(p.k_out, token * p.kv_heads + hk);
         if (page < 0)
             continue;
         const int64_t row = (page * p.cache.heads + hk) * p.cache.page_size + off;
@@ -201,12 +191,15 @@ __global__ void __launch_bounds__(WARPS * 32) norm_rope_kernel(const NormRope p,
                 const float t = scale > 0.0f ? fminf(fmaxf(rintf(__fdiv_rn(v[i], scale)), -127.0f), 127.0f) : 0.0f;
                 c[i >> 2] |= (uint32_t)((int)t & 255) << (8 * (i & 3));
             }
-            if (in)
-                *reinterpret_cast<uint2*>(static_cast<int8_t*>(dst) + row * p.dim + d0) = make_uint2(c[0], c[1]);
+            if (in) {
+                int8_t* at = static_cast<int8_t*>(dst) + row * p.dim;
+                *reinterpret_cast<uint32_t*>(at + d0) = c[0];
+                *reinterpret_cast<uint32_t*>(at + d1) = c[1];
+            }
             if (lane == 0)
                 (is_v ? p.cache.v_scale : p.cache.k_scale)[row] = scale;
         } else if (in) {
-            *reinterpret_cast<uint4*>(static_cast<T*>(dst) + row * p.dim + d0) = pack8<E>(v);
+            store16(dst, row);
         }
     }
 }

@@ -8,16 +8,16 @@
 // query heads that share it; nothing else is read more than once.
 //
 // Work.  A segment is one (sequence, kv head, 8 NT query heads); its visible keys, numbered
-// through without the hidden ones, are cut into tiles of 64.  All segments' tiles in a row are
+// through without the hidden ones, are cut into tiles of 64 (int8: 128).  All segments' tiles in a row are
 // shared out evenly: block c of C takes tiles [c T / C, (c + 1) T / C), whatever the lengths
 // (each block sums the lengths up itself, so nothing depends on the host knowing them and a
 // captured graph may be replayed with new lengths).  A block leaves a segment that it holds
 // whole as the final output, and the at most two that it shares with a neighbour as partial
 // sums (maximum, sum of weights, weighted values); join_kernel adds those up, always in the
-// same order.  Where no segment can hold more than kWholeTiles tiles, one block takes each
+// same order.  Where no segment can hold more than kWholeKeys keys, one block takes each
 // whole segment and there is no second launch.
 //
-// Inside a block each of the 4 warps takes 16 keys of a tile on its own: its own ring of
+// Inside a block each of the 4 warps takes 16 (int8: 32) keys of a tile on its own: its own ring of
 // asynchronous copies (no block-wide barrier while tiles stream), its own running maximum and
 // sum; the four are joined once per segment.  Both products run on the 16x8x16 matrix
 // instruction with keys (then value columns) as its 16 rows and the query heads as its 8
@@ -28,9 +28,8 @@
 //
 // int8 rows: a code is exact in fp16, so both products run in fp16: the query scaled by the
 // power of two that brings its largest value into [1, 2) (undone in the fp32 score), and the
-// row scales folded in as fp32: k's into the score, v's into the weight as
-// 2^(s + log2 v_scale - M) with a running maximum M of its own, so that scales of any size
-// leave the fp16 weight in [0, 1].
+// row scales folded in as fp32: k's into the score, v's into the weight, over the largest v
+// scale so far, so that scales of any size leave the fp16 weight in [0, 1].
 //
 // Rounding to fewer bits: each weight once, to the type of the values' product (bf16 or
 // fp16), which is what the matrix instruction takes; sums, maxima and scores are fp32.
@@ -48,21 +47,24 @@ namespace ck {
 namespace {
 
 constexpr int WARPS = 4;
-constexpr int KEYS = 16;              // keys of one warp's unit
-constexpr int TILE = WARPS * KEYS;    // keys of a block's tile
-constexpr int kWholeTiles = 8;        // segments of at most this many tiles are not split
+constexpr int kWholeKeys = 512;       // segments of at most this many keys are not split
 
 // NT: tiles of 8 query heads that a segment holds (1, or 2 where a group has more than 8)
 template <bool INT8, int DIM, int NT>
 struct Shape {
     static constexpr int HEADS = 8 * NT;
+    // Keys of a warp's unit.  int8 rows take twice as many: a unit's fixed cost (look-up, copy
+    // addresses, maximum and sum) is spread over the same bytes as with 16-bit rows.
+    static constexpr int KEYS = INT8 ? 32 : 16;
+    static constexpr int KT = KEYS / 16;                     // tiles of 16 keys
+    static constexpr int TILE = WARPS * KEYS;                // keys of a block's tile
     static constexpr int ROW = DIM * (INT8 ? 1 : 2);        // bytes of a row
-    static constexpr int SCALES = INT8 ? 2 * KEYS * 4 : 0;  // k scales, v scales
+    static constexpr int SCALES = INT8 ? 2 * KEYS * 4 : 0;   // k scales, v scales
     static constexpr int UNIT = 2 * KEYS * ROW + SCALES;
     // About 200 KB of rings an SM.  16-bit rows: two blocks; int8 rows, whose arithmetic per
-    // byte is twice that, four (two with 16 heads, which hold twice the sums).
-    static constexpr int BLOCKS = INT8 && NT == 1 ? 4 : 2;
-    static constexpr int STAGES = 24576 * 2 / BLOCKS / UNIT > 8 ? 8 : 24576 * 2 / BLOCKS / (UNIT - SCALES);
+    // byte is twice that, three (two with 16 heads, which hold twice the sums).
+    static constexpr int BLOCKS = INT8 && NT == 1 ? 3 : 2;
+    static constexpr int STAGES = (BLOCKS == 3 ? 16384 : 24576) / (UNIT - SCALES);
     static constexpr int LD = DIM + 4;                       // joined sums: floats per head
     static constexpr size_t RING = (size_t)WARPS * STAGES * UNIT;
     static constexpr size_t SMEM = RING + HEADS * LD * 4 + WARPS * HEADS * 8;
@@ -74,6 +76,7 @@ struct Lengths {
     const int32_t* seq_lens;
     int64_t max_len, window, sinks;
     int subs;  // segments of a sequence
+    int tile;  // keys of a tile
     __device__ int length(int64_t b, bool* bad) const
     {
         const int64_t n = __ldg(seq_lens + b);
@@ -83,7 +86,7 @@ struct Lengths {
     __device__ int tiles(int64_t b) const
     {
         bool bad;
-        return (visible_keys(length(b, &bad), window, sinks).count() + TILE - 1) / TILE;
+        return (visible_keys(length(b, &bad), window, sinks).count() + tile - 1) / tile;
     }
 };
 
@@ -141,7 +144,7 @@ struct Cursor {
     {
         bool bad;
         keys = visible_keys(L.length(b, &bad), L.window, L.sinks);
-        tiles = (keys.count() + TILE - 1) / TILE;
+        tiles = (keys.count() + L.tile - 1) / L.tile;
     }
     __device__ void next(const Lengths& L)
     {
@@ -189,7 +192,7 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
     using S = Shape<INT8, DIM, NT>;
     using T = typename E::T;
     using M = typename std::conditional<INT8, Fp16, E>::type;  // the products' type
-    constexpr int HEADS = S::HEADS;
+    constexpr int HEADS = S::HEADS, KEYS = S::KEYS, KT = S::KT, TILE = S::TILE;
     extern __shared__ __align__(128) uint8_t smem[];
     griddep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -197,7 +200,7 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
     const int group = p.q_heads / p.cache.heads;  // query heads per kv head
     const int qtiles = (group + HEADS - 1) / HEADS;
     const int page_size = p.cache.page_size;
-    Lengths L{p.seq_lens, p.max_blocks * page_size, p.window, p.sinks, p.cache.heads * qtiles};
+    Lengths L{p.seq_lens, p.max_blocks * page_size, p.window, p.sinks, p.cache.heads * qtiles, TILE};
 
     // sequences without visible keys have no tiles: zeros, or NaN where the length is out of range
     for (int64_t b = blockIdx.x; b < p.batch; b += gridDim.x) {
@@ -242,17 +245,22 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
     float* joined = reinterpret_cast<float*>(smem + S::RING);         // [HEADS][LD]
     float2* maxsum = reinterpret_cast<float2*>(joined + HEADS * S::LD);  // [WARPS][HEADS]
 
-    // ---- copies: lane l looks up the row of key l % 16 of the warp's unit one unit ahead
+    // ---- copies: lane l looks up the row of key l % KEYS of the warp's unit one unit ahead
+    constexpr int CH = S::ROW / 16;       // 16-byte chunks of a row
+    constexpr int RPI = 32 / CH;          // rows of one copy instruction
+    const uint8_t* const k_lane = static_cast<const uint8_t*>(p.cache.k) + lane % CH * 16;
+    const uint8_t* const v_lane = static_cast<const uint8_t*>(p.cache.v) + lane % CH * 16;
     Cursor ahead = at;
     int32_t page = 0;
     int in_page = 0;
     bool have = false;
     auto look_up = [&]() {
-        const int v = ahead.tile * TILE + warp * KEYS + (lane & 15);
+        const int v = ahead.tile * TILE + warp * KEYS + lane % KEYS;
         have = ahead.left > 0 && v < ahead.keys.count();
         if (have) {
             const int j = ahead.keys.key(v);
-            const int blk = j / page_size;
+            // page_shift: the page size is that power of two; -1: it is none
+            const int blk = p.page_shift >= 0 ? j >> p.page_shift : j / page_size;
             in_page = j - blk * page_size;
             page = __ldg(p.block_table + ahead.b * p.max_blocks + blk);
         }
@@ -264,26 +272,25 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
             const uint32_t bad = __ballot_sync(0xffffffffu, have && !in_pool);
             bad_units = (bad_units & ~(1u << stage)) | ((bad ? 1u : 0u) << stage);
             const bool ok = have && in_pool;
-            const int hk = ahead.sub / qtiles;
-            const uint32_t row = ok ? (uint32_t)(((int64_t)page * p.cache.heads + hk) * page_size + in_page) : 0u;
+            const int hk = qtiles == 1 ? ahead.sub : ahead.sub / qtiles;
+            // (the cache's rows are below 2^32)
+            const uint32_t row = ok ? ((uint32_t)page * p.cache.heads + hk) * page_size + in_page : 0u;
             const uint32_t oks = __ballot_sync(0xffffffffu, ok);
             const uint32_t dst = ring + stage * S::UNIT;
-            constexpr int CH = S::ROW / 16;       // chunks of a row
-            constexpr int RPI = 32 / CH;          // rows of one instruction
-            const int c = lane % CH;
 #pragma unroll
             for (int i = 0; i < KEYS / RPI; ++i) {
                 const int r = i * RPI + lane / CH;
-                const uint32_t src_row = __shfl_sync(0xffffffffu, row, r);
+                const uint64_t off = (uint64_t)__shfl_sync(0xffffffffu, row, r) * S::ROW;
                 const bool r_ok = (oks >> r) & 1u;
-                const size_t off = (size_t)src_row * S::ROW + c * 16;
-                cp_async16(dst + chunk_at<INT8, DIM, false>(r, c), static_cast<const uint8_t*>(p.cache.k) + off, r_ok);
-                cp_async16(dst + KEYS * S::ROW + chunk_at<INT8, DIM, true>(r, c),
-                           static_cast<const uint8_t*>(p.cache.v) + off, r_ok);
+                cp_async16(dst + chunk_at<INT8, DIM, false>(r, lane % CH), k_lane + off, r_ok);
+                cp_async16(dst + KEYS * S::ROW + chunk_at<INT8, DIM, true>(r, lane % CH), v_lane + off, r_ok);
             }
-            if (INT8)
-                cp_async_small<4>(dst + 2 * KEYS * S::ROW + lane * 4, (lane < 16 ? p.cache.k_scale : p.cache.v_scale) + row,
-                                  ok);
+            if (INT8) {
+                static_assert(!INT8 || KEYS == 32, "a scale of each kind per lane");
+                const uint32_t sc = dst + 2 * KEYS * S::ROW + lane * 4;
+                cp_async_small<4>(sc, p.cache.k_scale + row, ok);
+                cp_async_small<4>(sc + KEYS * 4, p.cache.v_scale + row, ok);
+            }
             ahead.next(L);
             look_up();
         }
@@ -297,7 +304,7 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
     uint32_t qb[NT][DIM / 16][2];  // queries of head 8 nt + g
     float o[NT][DIM / 16][4];      // sums of heads 8 nt + 2t, + 1 (columns), two value rows
     float m[NT][2], l[NT][2];      // of those heads: maximum, sum of weights
-    float mv[NT][2];               // int8: the values' maximum
+    float vmax = 0.0f;             // int8: what the sums o are relative to besides, the largest value scale
     float c_head[NT][2];           // score factor of those heads, in units of log2
     bool bad = false;
     bool fresh = true;
@@ -354,13 +361,14 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
                 }
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    m[nt][j] = mv[nt][j] = -INFINITY;
+                    m[nt][j] = -INFINITY;
                     l[nt][j] = 0.0f;
                 }
 #pragma unroll
                 for (int e = 0; e < DIM / 16; ++e)
                     o[nt][e][0] = o[nt][e][1] = o[nt][e][2] = o[nt][e][3] = 0.0f;
             }
+            vmax = 0.0f;
             bad = false;
             fresh = false;
             first_of_segment = at.tile;
@@ -376,80 +384,108 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
             bad |= (bad_units >> stage) & 1u;
             const uint32_t ks = ring + stage * S::UNIT;
             const uint32_t vs = ks + KEYS * S::ROW;
-            // S^T: rows keys g, g + 8; columns heads 2t, 2t + 1 of each nt
-            float s[NT][4];
+            // S^T: rows keys 16 kt + g, + 8; columns heads 2t, 2t + 1 of each nt
+            float s[NT][KT][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-                s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
-            if (!INT8) {
 #pragma unroll
-                for (int kk = 0; kk < DIM / 16; ++kk) {
-                    uint32_t ka[4];
-                    ldmatrix_x4(ka, ks + chunk_at<INT8, DIM, false>(lane & 15, 2 * kk + (lane >> 4)));
+                for (int kt = 0; kt < KT; ++kt)
+                    s[nt][kt][0] = s[nt][kt][1] = s[nt][kt][2] = s[nt][kt][3] = 0.0f;
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        mma_16816<M>(s[nt], ka, qb[nt][kk][0], qb[nt][kk][1]);
-                }
-            } else {
+            for (int kt = 0; kt < KT; ++kt) {
+                if (!INT8) {
 #pragma unroll
-                for (int hf = 0; hf < DIM / 64; ++hf) {
-                    const uint4 r0 = lds128(ks + chunk_at<INT8, DIM, false>(g, 4 * hf + t));
-                    const uint4 r1 = lds128(ks + chunk_at<INT8, DIM, false>(g + 8, 4 * hf + t));
-                    const uint32_t w0[4] = {r0.x, r0.y, r0.z, r0.w}, w1[4] = {r1.x, r1.y, r1.z, r1.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t u0 = w0[i] ^ 0x80808080u, u1 = w1[i] ^ 0x80808080u;
-                        const uint32_t ka[4] = {half2_of(u0, 0x4140), half2_of(u1, 0x4140), half2_of(u0, 0x4342),
-                                                half2_of(u1, 0x4342)};
+                    for (int kk = 0; kk < DIM / 16; ++kk) {
+                        uint32_t ka[4];
+                        ldmatrix_x4(ka, ks + chunk_at<INT8, DIM, false>(16 * kt + (lane & 15), 2 * kk + (lane >> 4)));
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
-                            mma_16816<M>(s[nt], ka, qb[nt][4 * hf + i][0], qb[nt][4 * hf + i][1]);
+                            mma_16816<M>(s[nt][kt], ka, qb[nt][kk][0], qb[nt][kk][1]);
+                    }
+                } else {
+#pragma unroll
+                    for (int hf = 0; hf < DIM / 64; ++hf) {
+                        const uint4 r0 = lds128(ks + chunk_at<INT8, DIM, false>(16 * kt + g, 4 * hf + t));
+                        const uint4 r1 = lds128(ks + chunk_at<INT8, DIM, false>(16 * kt + g + 8, 4 * hf + t));
+                        const uint32_t w0[4] = {r0.x, r0.y, r0.z, r0.w}, w1[4] = {r1.x, r1.y, r1.z, r1.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t u0 = w0[i] ^ 0x80808080u, u1 = w1[i] ^ 0x80808080u;
+                            const uint32_t ka[4] = {half2_of(u0, 0x4140), half2_of(u1, 0x4140), half2_of(u0, 0x4342),
+                                                    half2_of(u1, 0x4342)};
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma_16816<M>(s[nt][kt], ka, qb[nt][4 * hf + i][0], qb[nt][4 * hf + i][1]);
+                        }
                     }
                 }
             }
-            float kscale[2] = {1.0f, 1.0f}, lv[2] = {0.0f, 0.0f};  // int8: of keys g, g + 8
+            // int8: of keys 16 kt + g, + 8 the key scales, and the value scales over their maximum
+            float kscale[KT][2], vratio[KT][2];
             if (INT8) {
+                const uint32_t sc = vs + KEYS * S::ROW;
+                float top = vmax;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    kscale[h] = __uint_as_float(lds32(vs + KEYS * S::ROW + (g + 8 * h) * 4));
-                    lv[h] = fast_log2(__uint_as_float(lds32(vs + KEYS * S::ROW + (KEYS + g + 8 * h) * 4)));
+                for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        kscale[kt][h] = __uint_as_float(lds32(sc + (16 * kt + g + 8 * h) * 4));
+                        vratio[kt][h] = __uint_as_float(lds32(sc + (KEYS + 16 * kt + g + 8 * h) * 4));
+                        top = fmaxf(top, vratio[kt][h]);
+                    }
+#pragma unroll
+                for (int x = 4; x <= 16; x <<= 1)
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+                if (top > vmax) {  // warp-uniform
+                    const float f = vmax / top;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < DIM / 16; ++e)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                o[nt][e][i] *= f;
+                    vmax = top;
                 }
-            }
-            const bool in[2] = {v0 + g < n, v0 + g + 8 < n};
-            uint32_t pb[NT][2];
+                const float inv = top > 0.0f ? 1.0f / top : 0.0f;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float w[4];  // weights for the values' product
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    float a[2];  // scores in units of log2; keys past the end out
+                for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
-                        a[h] = in[h] ? s[nt][2 * h + j] * (INT8 ? kscale[h] * c_head[nt][j] : c_head[nt][j]) : -INFINITY;
-                    float top = fmaxf(a[0], a[1]);
-                    float topv = INT8 ? fmaxf(a[0] + lv[0], a[1] + lv[1]) : 0.0f;
+                        vratio[kt][h] *= inv;
+            }
+            uint32_t pb[NT][KT][2];
 #pragma unroll
-                    for (int x = 4; x <= 16; x <<= 1) {
+            for (int nt = 0; nt < NT; ++nt) {
+                float w[KT][4];  // weights for the values' product
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    float a[KT][2];  // scores in units of log2; keys past the end out
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float x = s[nt][kt][2 * h + j] * c_head[nt][j];
+                            a[kt][h] = v0 + 16 * kt + g + 8 * h < n ? (INT8 ? x * kscale[kt][h] : x) : -INFINITY;
+                            top = fmaxf(top, a[kt][h]);
+                        }
+#pragma unroll
+                    for (int x = 4; x <= 16; x <<= 1)
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-                        if (INT8)
-                            topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, x));
-                    }
                     const float m2 = fmaxf(m[nt][j], top);
                     const float ref = m2 == -INFINITY ? 0.0f : m2;
-                    float keep = fast_exp2(m[nt][j] - ref);
+                    const float keep = fast_exp2(m[nt][j] - ref);
                     m[nt][j] = m2;
-                    const float p0 = fast_exp2(a[0] - ref), p1 = fast_exp2(a[1] - ref);
-                    l[nt][j] = l[nt][j] * keep + (p0 + p1);
-                    w[j] = p0;
-                    w[2 + j] = p1;
-                    if (INT8) {
-                        const float mv2 = fmaxf(mv[nt][j], topv);
-                        const float refv = mv2 == -INFINITY ? 0.0f : mv2;
-                        keep = fast_exp2(mv[nt][j] - refv);
-                        mv[nt][j] = mv2;
-                        w[j] = fast_exp2(a[0] + lv[0] - refv);
-                        w[2 + j] = fast_exp2(a[1] + lv[1] - refv);
-                    }
+                    l[nt][j] *= keep;
+#pragma unroll
+                    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float x = fast_exp2(a[kt][h] - ref);
+                            l[nt][j] += x;
+                            w[kt][2 * h + j] = INT8 ? x * vratio[kt][h] : x;
+                        }
                     if (__any_sync(0xffffffffu, keep != 1.0f))
 #pragma unroll
                         for (int e = 0; e < DIM / 16; ++e) {
@@ -457,47 +493,53 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
                             o[nt][e][2 + j] *= keep;
                         }
                 }
-                pb[nt][0] = transpose_8x8(M::pack2(w[0], w[1]));
-                pb[nt][1] = transpose_8x8(M::pack2(w[2], w[3]));
+#pragma unroll
+                for (int kt = 0; kt < KT; ++kt) {
+                    pb[nt][kt][0] = transpose_8x8(M::pack2(w[kt][0], w[kt][1]));
+                    pb[nt][kt][1] = transpose_8x8(M::pack2(w[kt][2], w[kt][3]));
+                }
             }
-            if (!INT8) {
 #pragma unroll
-                for (int e = 0; e < DIM / 16; ++e) {
-                    uint32_t va[4];
-                    ldmatrix_x4_trans(va, vs + chunk_at<INT8, DIM, true>((lane & 7) + ((lane >> 4) << 3),
-                                                                        2 * e + ((lane >> 3) & 1)));
+            for (int kt = 0; kt < KT; ++kt) {
+                if (!INT8) {
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        mma_16816<M>(o[nt][e], va, pb[nt][0], pb[nt][1]);
-                }
-            } else {
-                // this lane's 4 keys (2t, 2t+1, 2t+8, 2t+9), values (DIM/8) g .. (DIM/8) (g+1) - 1:
-                // value 2 e of those is row g of tile e, value 2 e + 1 its row g + 8
-                constexpr int WORDS = DIM / 32;
-                uint32_t w[4][WORDS];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = 2 * t + (i & 1) + 8 * (i >> 1);
-                    if (DIM == 128) {
-                        const uint4 x = lds128(vs + chunk_at<INT8, DIM, true>(r, g));
-                        w[i][0] = x.x, w[i][1] = x.y, w[i][WORDS - 2] = x.z, w[i][WORDS - 1] = x.w;
-                    } else {
-                        const uint2 x = lds64(vs + chunk_at<INT8, DIM, true>(r, g >> 1) + 8 * (g & 1));
-                        w[i][0] = x.x, w[i][1] = x.y;
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < WORDS; ++k) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {  // values 4 k + 2 h, + 1: tile 2 k + h
-                        const uint32_t sel = h ? 0x7362 : 0x5140;
-                        const uint32_t k01 = __byte_perm(w[0][k], w[1][k], sel) ^ 0x80808080u;
-                        const uint32_t k23 = __byte_perm(w[2][k], w[3][k], sel) ^ 0x80808080u;
-                        const uint32_t va[4] = {half2_of(k01, 0x4140), half2_of(k01, 0x4342), half2_of(k23, 0x4140),
-                                                half2_of(k23, 0x4342)};
+                    for (int e = 0; e < DIM / 16; ++e) {
+                        uint32_t va[4];
+                        ldmatrix_x4_trans(va, vs + chunk_at<INT8, DIM, true>(16 * kt + (lane & 7) + ((lane >> 4) << 3),
+                                                                            2 * e + ((lane >> 3) & 1)));
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
-                            mma_16816<M>(o[nt][2 * k + h], va, pb[nt][0], pb[nt][1]);
+                            mma_16816<M>(o[nt][e], va, pb[nt][kt][0], pb[nt][kt][1]);
+                    }
+                } else {
+                    // this lane's 4 keys (16 kt + 2t, 2t+1, 2t+8, 2t+9), values (DIM/8) g .. (DIM/8) (g+1) - 1:
+                    // value 2 e of those is row g of tile e, value 2 e + 1 its row g + 8
+                    constexpr int WORDS = DIM / 32;
+                    uint32_t w[4][WORDS];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = 16 * kt + 2 * t + (i & 1) + 8 * (i >> 1);
+                        if (DIM == 128) {
+                            const uint4 x = lds128(vs + chunk_at<INT8, DIM, true>(r, g));
+                            w[i][0] = x.x, w[i][1] = x.y, w[i][WORDS - 2] = x.z, w[i][WORDS - 1] = x.w;
+                        } else {
+                            const uint2 x = lds64(vs + chunk_at<INT8, DIM, true>(r, g >> 1) + 8 * (g & 1));
+                            w[i][0] = x.x, w[i][1] = x.y;
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < WORDS; ++k) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {  // values 4 k + 2 h, + 1: tile 2 k + h
+                            const uint32_t sel = h ? 0x7362 : 0x5140;
+                            const uint32_t k01 = __byte_perm(w[0][k], w[1][k], sel) ^ 0x80808080u;
+                            const uint32_t k23 = __byte_perm(w[2][k], w[3][k], sel) ^ 0x80808080u;
+                            const uint32_t va[4] = {half2_of(k01, 0x4140), half2_of(k01, 0x4342), half2_of(k23, 0x4140),
+                                                    half2_of(k23, 0x4342)};
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma_16816<M>(o[nt][2 * k + h], va, pb[nt][kt][0], pb[nt][kt][1]);
+                        }
                     }
                 }
             }
@@ -534,8 +576,7 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
 #pragma unroll
                     for (int w = 0; w < WARPS; ++w)
                         top = fmaxf(top, maxsum[w * HEADS + 8 * nt + 2 * t + j].x);
-                    const float from = INT8 ? mv[nt][j] : m[nt][j];  // what the sums o are relative to
-                    f[nt][j] = from == -INFINITY ? 0.0f : fast_exp2(from - top);
+                    f[nt][j] = m[nt][j] == -INFINITY ? 0.0f : fast_exp2(m[nt][j] - top) * (INT8 ? vmax : 1.0f);
                 }
             for (int w = 0; w < WARPS; ++w) {
                 if (warp == w)
@@ -605,7 +646,7 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
 // Adds up the partial sums of the segments that blocks share: one block per (sequence, query
 // head), its 4 warps every fourth part each, then the four together.
 template <class E, int DIM, int NT>
-__global__ void __launch_bounds__(128) join_kernel(const PagedAttention p, int64_t C)
+__global__ void __launch_bounds__(128) join_kernel(const PagedAttention p, int64_t C, int tile)
 {
     using T = typename E::T;
     griddep_wait();
@@ -618,7 +659,7 @@ __global__ void __launch_bounds__(128) join_kernel(const PagedAttention p, int64
     const int h = (int)(blockIdx.x - b * p.q_heads);
     const int group = p.q_heads / p.cache.heads;
     const int qtiles = (group + HEADS - 1) / HEADS;
-    Lengths L{p.seq_lens, p.max_blocks * p.cache.page_size, p.window, p.sinks, p.cache.heads * qtiles};
+    Lengths L{p.seq_lens, p.max_blocks * p.cache.page_size, p.window, p.sinks, p.cache.heads * qtiles, tile};
     const int tiles = L.tiles(b);
     if (tiles == 0)
         return;  // the first kernel wrote it
@@ -711,14 +752,14 @@ cudaError_t launch(const PagedAttention& p, const DeviceInfo& dev, unsigned int*
     int64_t longest = p.max_blocks * p.cache.page_size;
     if (p.window > 0 && p.sinks < longest)
         longest = std::min(longest, p.window + p.sinks);
-    const int64_t tiles = (longest + TILE - 1) / TILE;
-    const bool split = tiles > kWholeTiles;
+    const int64_t tiles = (longest + S::TILE - 1) / S::TILE;
+    const bool split = longest > kWholeKeys;
     const int64_t most = std::min<int64_t>(kMostBlocks, (int64_t)dev.sm_count * S::BLOCKS);
     const int64_t blocks = split ? std::min(most, segments * tiles) : segments;
     e = launch_pdl(paged_kernel<E, INT8, DIM, NT>, dim3((unsigned)blocks), dim3(WARPS * 32), S::SMEM, s, p, blocks, split,
                    err);
     if (e == cudaSuccess && split)
-        e = launch_pdl(join_kernel<E, DIM, NT>, dim3((unsigned)(p.batch * p.q_heads)), dim3(128), 0, s, p, blocks);
+        e = launch_pdl(join_kernel<E, DIM, NT>, dim3((unsigned)(p.batch * p.q_heads)), dim3(128), 0, s, p, blocks, S::TILE);
     return e;
 }
 

@@ -58,6 +58,7 @@ struct PagedAttention {
     bool f16;
     float scale;
     int64_t window, sinks;
+    int page_shift;  // log2 of the page size, -1 if it is no power of two
     void* out;
     float* lse;  // or nullptr
     void* workspace;
