@@ -325,8 +325,11 @@ int ck_qk_norm_rope(const void *qkv, int64_t qkv_stride, int64_t tokens, int64_t
  *                max included.
  * head_dim: 64 or 128.  The cache's type is dtype or CK_KV_INT8.  The result does not depend
  * on what else is in the batch's pages: rows that no sequence sees are never read.
- * workspace: ck_paged_attention_workspace_size() bytes; its content does not matter. */
-size_t ck_paged_attention_workspace_size(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t head_dim);
+ * workspace: ck_paged_attention_workspace_size(batch, q_heads, kv_heads, head_dim, max_blocks *
+ *              page_size) bytes (0 for short tables: it may be NULL then); its content does not
+ *              matter. */
+size_t ck_paged_attention_workspace_size(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                                         int64_t max_len);
 int ck_paged_attention(const void *q, int64_t q_stride, const ck_kv_cache_t *cache, const int32_t *block_table,
                        int64_t max_blocks, const int32_t *seq_lens, int64_t batch, int64_t q_heads, int dtype,
                        float scale, int64_t window, int64_t sinks, void *out, float *lse, void *workspace,
@@ -362,15 +365,12 @@ int ck_attention(const void *q, int64_t q_stride, const void *k, int64_t k_strid
  * arithmetic, set the time (some tens of rows).
  *   ck_int4_prepare_weight: fp32 W [N,K] -> w4, w_scale: per group scale = bf16(max|W| / 7),
  *             code - 8 = clamp(rint(W / scale), -7, 7).
- *   ck_int4_pack: weights quantized elsewhere, int8 codes [N,K] in [-8, 7] (clamped) -> w4.
- *   workspace: ck_int4_linear_workspace_size(M, N, K) bytes; its content does not matter. */
+ *   ck_int4_pack: weights quantized elsewhere, int8 codes [N,K] in [-8, 7] (clamped) -> w4. */
 int ck_int4_prepare_weight(const float *W, int64_t N, int64_t K, int64_t group, uint32_t *w4, void *w_scale,
                            void *stream);
 int ck_int4_pack(const int8_t *codes, int64_t N, int64_t K, uint32_t *w4, void *stream);
-size_t ck_int4_linear_workspace_size(int64_t M, int64_t N, int64_t K);
 int ck_int4_linear(const void *x, const uint32_t *w4, const void *w_scale, const void *bias, const void *residual,
-                   void *y, int64_t M, int64_t N, int64_t K, int64_t group, int dtype, int out_dtype,
-                   void *workspace, size_t workspace_bytes, void *stream);
+                   void *y, int64_t M, int64_t N, int64_t K, int64_t group, int dtype, int out_dtype, void *stream);
 
 /* Launch profiling, for benchmarks.  Between ck_profile_begin() and ck_profile_end()
  * the library counts the kernels it enqueues from the calling host thread, by kind

@@ -70,14 +70,13 @@ def load_library(path=None):
         "ck_selftest_wait_timeout": ([ctypes.c_uint64, P], I),
         "ck_qk_norm_rope": ([P, I64, I64, I64, I64, I64, I, I, P, P, ctypes.c_float, I64, I, P, P, I64, P, P, P, P, P],
                             I),
-        "ck_paged_attention_workspace_size": ([I64, I64, I64, I64], SZ),
+        "ck_paged_attention_workspace_size": ([I64, I64, I64, I64, I64], SZ),
         "ck_paged_attention": ([P, I64, P, P, I64, P, I64, I64, I, ctypes.c_float, I64, I64, P, P, P, SZ, P], I),
         "ck_attention": ([P, I64, P, I64, P, I64, P, P, I64, I64, I64, I64, I64, I64, I, ctypes.c_float, I, I64, I64, P,
                           P, P], I),
         "ck_int4_prepare_weight": ([P, I64, I64, I64, P, P, P], I),
         "ck_int4_pack": ([P, I64, I64, P, P], I),
-        "ck_int4_linear_workspace_size": ([I64, I64, I64], SZ),
-        "ck_int4_linear": ([P, P, P, P, P, P, I64, I64, I64, I64, I, I, P, SZ, P], I),
+        "ck_int4_linear": ([P, P, P, P, P, P, I64, I64, I64, I64, I, I, P], I),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)

@@ -184,12 +184,13 @@ int ck_qk_norm_rope(const void* qkv, int64_t qkv_stride, int64_t tokens, int64_t
     return e == cudaSuccess ? CK_OK : cuda_fail(e, "ck_qk_norm_rope launch");
 }
 
-size_t ck_paged_attention_workspace_size(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t head_dim)
+size_t ck_paged_attention_workspace_size(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                                         int64_t max_len)
 {
-    if (batch < 0 || q_heads < 1 || kv_heads < 1 || head_dim < 1 || q_heads > 65536 || kv_heads > 65536 ||
+    if (batch < 0 || max_len < 0 || q_heads < 1 || kv_heads < 1 || head_dim < 1 || q_heads > 65536 || kv_heads > 65536 ||
         head_dim > 256)
         return 0;
-    return paged_attention_workspace(batch, (int)q_heads, (int)kv_heads, (int)head_dim);
+    return paged_attention_workspace((int)(q_heads / kv_heads), (int)head_dim, max_len);
 }
 
 int ck_paged_attention(const void* q, int64_t q_stride, const ck_kv_cache_t* cache, const int32_t* block_table,
@@ -222,10 +223,13 @@ int ck_paged_attention(const void* q, int64_t q_stride, const ck_kv_cache_t* cac
     CK_REQUIRE_INDEX(seq_lens);
     CK_REQUIRE_PTR(out);
     CK_OPTIONAL_PTR(lse);
-    CK_REQUIRE_PTR(workspace);
-    const size_t need = paged_attention_workspace(batch, (int)q_heads, p.cache.heads, p.cache.dim);
-    if (workspace_bytes < need)
-        return fail(CK_ERR_INVALID_ARG, "workspace too small: %zu bytes given, %zu needed", workspace_bytes, need);
+    const size_t need =
+        paged_attention_workspace((int)q_heads / p.cache.heads, p.cache.dim, max_blocks * p.cache.page_size);
+    if (need > 0) {
+        CK_REQUIRE_PTR(workspace);
+        if (workspace_bytes < need)
+            return fail(CK_ERR_INVALID_ARG, "workspace too small: %zu bytes given, %zu needed", workspace_bytes, need);
+    }
     DeviceInfo dev;
     CK_CHECK(check_device(&dev));
     p.q = q;
@@ -376,16 +380,8 @@ int ck_int4_pack(const int8_t* codes, int64_t N, int64_t K, uint32_t* w4, void* 
     return e == cudaSuccess ? CK_OK : cuda_fail(e, "ck_int4_pack launch");
 }
 
-size_t ck_int4_linear_workspace_size(int64_t M, int64_t N, int64_t K)
-{
-    if (M < 0 || N < 0 || K < 0)
-        return 0;
-    return int4_linear_workspace(M, N, K);
-}
-
 int ck_int4_linear(const void* x, const uint32_t* w4, const void* w_scale, const void* bias, const void* residual,
-                   void* y, int64_t M, int64_t N, int64_t K, int64_t group, int dtype, int out_dtype, void* workspace,
-                   size_t workspace_bytes, void* stream)
+                   void* y, int64_t M, int64_t N, int64_t K, int64_t group, int dtype, int out_dtype, void* stream)
 {
     CK_CHECK(check_dtype(dtype));
     if (out_dtype != CK_OUT_BF16 && out_dtype != CK_OUT_F16 && out_dtype != CK_OUT_F32)
@@ -402,12 +398,6 @@ int ck_int4_linear(const void* x, const uint32_t* w4, const void* w_scale, const
     CK_REQUIRE_PTR(y);
     CK_OPTIONAL_PTR(bias);
     CK_OPTIONAL_PTR(residual);
-    const size_t need = int4_linear_workspace(M, N, K);
-    if (need > 0) {
-        CK_REQUIRE_PTR(workspace);
-        if (workspace_bytes < need)
-            return fail(CK_ERR_INVALID_ARG, "workspace too small: %zu bytes given, %zu needed", workspace_bytes, need);
-    }
     DeviceInfo dev;
     CK_CHECK(check_device(&dev));
     Int4Linear p{};
@@ -423,7 +413,6 @@ int ck_int4_linear(const void* x, const uint32_t* w4, const void* w_scale, const
     p.group = (int)group;
     p.f16 = dtype == CK_OUT_F16;
     p.out_dtype = out_dtype;
-    p.workspace = workspace;
     log_shape("int4_linear", M, N, K, (int)group, "4-bit weights, group scales");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     ProfScope ps(kProfInt4, 1, s);

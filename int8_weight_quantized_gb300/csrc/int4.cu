@@ -343,12 +343,6 @@ cudaError_t by_rows(const Int4Linear& p, const DeviceInfo& dev, cudaStream_t s)
 
 }  // namespace
 
-size_t int4_linear_workspace(int64_t M, int64_t N, int64_t K)
-{
-    (void)M, (void)N, (void)K;
-    return 0;
-}
-
 cudaError_t launch_int4_linear(const Int4Linear& p, const DeviceInfo& dev, cudaStream_t s)
 {
     return p.f16 ? by_rows<Fp16>(p, dev, s) : by_rows<Bf16>(p, dev, s);

@@ -731,7 +731,7 @@ __global__ void __launch_bounds__(128) join_kernel(const PagedAttention p, int64
         p.lse[at_row] = (top + log2f(sum)) * kLn2;
 }
 
-constexpr int kMostBlocks = 152 * 4;  // of any device this library runs on
+constexpr int kMostBlocks = 152 * 3;  // of any device this library runs on
 
 template <class E, bool INT8, int DIM, int NT>
 cudaError_t launch(const PagedAttention& p, const DeviceInfo& dev, unsigned int* err, cudaStream_t s)
@@ -753,6 +753,7 @@ cudaError_t launch(const PagedAttention& p, const DeviceInfo& dev, unsigned int*
     if (p.window > 0 && p.sinks < longest)
         longest = std::min(longest, p.window + p.sinks);
     const int64_t tiles = (longest + S::TILE - 1) / S::TILE;
+    // (the workspace goes by the table alone; a window only shortens)
     const bool split = longest > kWholeKeys;
     const int64_t most = std::min<int64_t>(kMostBlocks, (int64_t)dev.sm_count * S::BLOCKS);
     const int64_t blocks = split ? std::min(most, segments * tiles) : segments;
@@ -780,10 +781,9 @@ cudaError_t by_type(const PagedAttention& p, const DeviceInfo& dev, unsigned int
 
 }  // namespace
 
-size_t paged_attention_workspace(int64_t batch, int q_heads, int kv_heads, int dim)
+size_t paged_attention_workspace(int group, int dim, int64_t max_len)
 {
-    (void)batch, (void)q_heads, (void)kv_heads;
-    return (size_t)kMostBlocks * 2 * 16 * (dim + 2) * sizeof(float);
+    return max_len <= kWholeKeys ? 0 : (size_t)kMostBlocks * 2 * (group <= 8 ? 8 : 16) * (dim + 2) * sizeof(float);
 }
 
 cudaError_t launch_paged_attention(const PagedAttention& p, const DeviceInfo& dev, cudaStream_t s)

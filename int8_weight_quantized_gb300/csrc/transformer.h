@@ -63,7 +63,8 @@ struct PagedAttention {
     float* lse;  // or nullptr
     void* workspace;
 };
-size_t paged_attention_workspace(int64_t batch, int q_heads, int kv_heads, int dim);
+// by query heads per kv head and the most keys a sequence can have
+size_t paged_attention_workspace(int group, int dim, int64_t max_len);
 cudaError_t launch_paged_attention(const PagedAttention& p, const DeviceInfo& dev, cudaStream_t s);
 
 struct PromptAttention {
@@ -91,9 +92,7 @@ struct Int4Linear {
     int group;
     bool f16;
     int out_dtype;
-    void* workspace;
 };
-size_t int4_linear_workspace(int64_t M, int64_t N, int64_t K);
 cudaError_t launch_int4_linear(const Int4Linear& p, const DeviceInfo& dev, cudaStream_t s);
 cudaError_t launch_int4_weight(const float* W, int64_t N, int64_t K, int group, uint32_t* w4, void* w_scale,
                                const DeviceInfo& dev, cudaStream_t s);

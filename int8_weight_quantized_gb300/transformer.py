@@ -6,8 +6,7 @@ As in the rest of the package the functions have the C names and only marshal ar
 Outputs and workspaces that the caller does not give come from torch's allocator on the
 stream that the work is enqueued on, so concurrent streams never share them.
 """
-import contextlib
-import ctypes
+import struct
 
 import torch
 
@@ -19,17 +18,15 @@ _KV = {torch.bfloat16: KV_BF16, torch.float16: KV_F16, torch.int8: KV_INT8}
 _EPS = 1e-6
 
 
-class _CacheStruct(ctypes.Structure):
-    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
-                ("v_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int64),
-                ("kv_heads", ctypes.c_int64), ("head_dim", ctypes.c_int64), ("dtype", ctypes.c_int)]
+# ck_kv_cache_t: k, v, k_scale, v_scale, num_pages, page_size, kv_heads, head_dim, dtype
+_CACHE = struct.Struct("@PPPPqqqqi")
 
 
 class KVCache:
     """Keys and values in pages: k, v [num_pages, kv_heads, page_size, head_dim] of bf16, fp16
     or int8; int8 caches have fp32 k_scale, v_scale [num_pages, kv_heads, page_size]."""
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "_struct")
+    __slots__ = ("k", "v", "k_scale", "v_scale", "page_size", "_struct", "_dim", "_heads")
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         shape, dtype = k.shape, k.dtype
@@ -47,8 +44,9 @@ class KVCache:
         elif k_scale is not None or v_scale is not None:
             raise ValueError("only an int8 cache has scales")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self._struct = _CacheStruct(k.data_ptr(), v.data_ptr(), ck._ptr(k_scale), ck._ptr(v_scale), shape[0], shape[2],
-                                    shape[1], shape[3], _KV[dtype])
+        pages, self._heads, self.page_size, self._dim = shape
+        self._struct = _CACHE.pack(k.data_ptr(), v.data_ptr(), ck._ptr(k_scale) or 0, ck._ptr(v_scale) or 0, pages,
+                                   self.page_size, self._heads, self._dim, _KV[dtype])
 
     @classmethod
     def empty(cls, num_pages, page_size, kv_heads, head_dim, dtype=torch.bfloat16, device="cuda"):
@@ -63,10 +61,6 @@ class KVCache:
     def num_pages(self):
         return self.k.shape[0]
 
-    @property
-    def page_size(self):
-        return self.k.shape[2]
-
 
 def rope_table(max_pos, rot_dim, base=10000.0, device="cuda"):
     """The fp32 cos_sin table [max_pos, rot_dim] of ck_qk_norm_rope for the angles
@@ -76,9 +70,12 @@ def rope_table(max_pos, rot_dim, base=10000.0, device="cuda"):
     return torch.cat([angle.cos(), angle.sin()], 1).float().to(device)
 
 
-def _on(stream):
+def _empty(shape, dtype, device, stream):
     # allocations belong to the stream that uses them
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _act(t, name):
@@ -86,13 +83,6 @@ def _act(t, name):
     if code is None:
         raise TypeError("%s must be torch.bfloat16 or torch.float16, got %s" % (name, t.dtype))
     return code
-
-
-def _index(t, dtype, shape, name):
-    if t.dtype != dtype:
-        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.shape != shape or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError("%s must be a contiguous CUDA tensor of shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
 
 
 def _rows(t, dtype, dim, name):
@@ -118,7 +108,8 @@ def ck_qk_norm_rope(qkv, positions, cos_sin, q_heads, kv_heads, q_weight=None, k
     there is no cache."""
     code = _act(qkv, "qkv")
     dtype = qkv.dtype
-    if qkv.dim() != 2 or not qkv.is_cuda or qkv.stride(1) != 1:
+    stride = qkv.stride()
+    if len(stride) != 2 or stride[1] != 1 or not qkv.is_cuda:
         raise ValueError("qkv must be a CUDA tensor [tokens, (q_heads + 2 kv_heads) * head_dim] with dense rows")
     tokens, width = qkv.shape
     heads = q_heads + 2 * kv_heads
@@ -129,7 +120,7 @@ def ck_qk_norm_rope(qkv, positions, cos_sin, q_heads, kv_heads, q_weight=None, k
     if cos_sin is not None:
         max_pos, rot = cos_sin.shape
         ck._req(cos_sin, torch.float32, (max_pos, rot), "cos_sin")
-        _index(positions, torch.int32, (tokens,), "positions")
+        ck._req(positions, torch.int32, (tokens,), "positions")
     else:
         positions = None
     if q_weight is not None:
@@ -137,21 +128,22 @@ def ck_qk_norm_rope(qkv, positions, cos_sin, q_heads, kv_heads, q_weight=None, k
     if k_weight is not None:
         ck._req(k_weight, dtype, (dim,), "k_weight")
     if cache is not None:
-        _index(slots, torch.int64, (tokens,), "slots")
-    with _on(stream):
-        if q is None:
-            q = torch.empty((tokens, q_heads, dim), dtype=dtype, device=qkv.device)
-        if k is None and (return_k or (return_k is None and cache is None)):
-            k = torch.empty((tokens, kv_heads, dim), dtype=dtype, device=qkv.device)
-    ck._req(q, dtype, (tokens, q_heads, dim), "q")
+        ck._req(slots, torch.int64, (tokens,), "slots")
+    if q is None:
+        q = _empty((tokens, q_heads, dim), dtype, qkv.device, stream)
+    else:
+        ck._req(q, dtype, (tokens, q_heads, dim), "q")
     if k is not None:
         ck._req(k, dtype, (tokens, kv_heads, dim), "k")
-    stride = qkv.stride(0) if tokens > 1 else max(qkv.stride(0), width)
-    ck._check(ck.load_library().ck_qk_norm_rope(
+    elif return_k or (return_k is None and cache is None):
+        k = _empty((tokens, kv_heads, dim), dtype, qkv.device, stream)
+    stride = stride[0] if tokens > 1 else max(stride[0], width)
+    status = (ck._lib or ck.load_library()).ck_qk_norm_rope(
         qkv.data_ptr(), stride, tokens, q_heads, kv_heads, dim, code, 1 if norm else 0, ck._ptr(q_weight),
         ck._ptr(k_weight), eps, rot, 1 if interleaved else 0, ck._ptr(positions), ck._ptr(cos_sin), max_pos,
-        q.data_ptr(), ck._ptr(k), None if cache is None else ctypes.addressof(cache._struct), ck._ptr(slots),
-        ck._stream(stream)))
+        q.data_ptr(), ck._ptr(k), None if cache is None else cache._struct, ck._ptr(slots), ck._stream(stream))
+    if status:
+        ck._check(status)
     return q, k
 
 
@@ -163,27 +155,30 @@ def ck_paged_attention(q, cache, block_table, seq_lens, scale=None, window=0, si
     code = _act(q, "q")
     batch, heads, dim = q.shape
     stride = _rows(q, q.dtype, dim, "q")
-    _index(block_table, torch.int32, (batch, block_table.shape[-1]), "block_table")
-    _index(seq_lens, torch.int32, (batch,), "seq_lens")
-    kv = cache._struct
-    if kv.head_dim != dim:
-        raise ValueError("q has heads of %d values, the cache of %d" % (dim, kv.head_dim))
-    L = ck.load_library()
-    need = L.ck_paged_attention_workspace_size(batch, heads, kv.kv_heads, dim) if ws is None else 0
-    with _on(stream):
-        if out is None:
-            out = torch.empty((batch, heads, dim), dtype=q.dtype, device=q.device)
-        if lse is None and return_lse:
-            lse = torch.empty((batch, heads), dtype=torch.float32, device=q.device)
-        if ws is None:
-            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-    ck._req(out, q.dtype, (batch, heads, dim), "out")
+    max_blocks = block_table.shape[-1]
+    ck._req(block_table, torch.int32, (batch, max_blocks), "block_table")
+    ck._req(seq_lens, torch.int32, (batch,), "seq_lens")
+    if cache._dim != dim:
+        raise ValueError("q has heads of %d values, the cache of %d" % (dim, cache._dim))
+    L = ck._lib or ck.load_library()
+    if out is None:
+        out = _empty((batch, heads, dim), q.dtype, q.device, stream)
+    else:
+        ck._req(out, q.dtype, (batch, heads, dim), "out")
     if lse is not None:
         ck._req(lse, torch.float32, (batch, heads), "lse")
-    ck._check(L.ck_paged_attention(
-        q.data_ptr(), stride, ctypes.addressof(kv), block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(),
-        batch, heads, code, dim ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(), ck._ptr(lse),
-        ws.data_ptr(), ws.numel(), ck._stream(stream)))
+    elif return_lse:
+        lse = _empty((batch, heads), torch.float32, q.device, stream)
+    if ws is None:
+        need = L.ck_paged_attention_workspace_size(batch, heads, cache._heads, dim, max_blocks * cache.page_size)
+        if need:
+            ws = _empty(need, torch.uint8, q.device, stream)
+    status = L.ck_paged_attention(
+        q.data_ptr(), stride, cache._struct, block_table.data_ptr(), max_blocks, seq_lens.data_ptr(), batch, heads, code,
+        dim ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(), ck._ptr(lse), ck._ptr(ws),
+        0 if ws is None else ws.numel(), ck._stream(stream))
+    if status:
+        ck._check(status)
     return (out, lse) if return_lse else out
 
 
@@ -195,27 +190,31 @@ def ck_attention(q, k, v, cu_q, cu_k=None, scale=None, causal=True, window=0, si
     code = _act(q, "q")
     total_q, heads, dim = q.shape
     total_k, kv_heads = k.shape[:2]
-    strides = [_rows(t, q.dtype, dim, n) for t, n in ((q, "q"), (k, "k"), (v, "v"))]
+    dtype = q.dtype
+    strides = _rows(q, dtype, dim, "q"), _rows(k, dtype, dim, "k"), _rows(v, dtype, dim, "v")
     if v.shape != k.shape:
         raise ValueError("k and v must have one shape, got %s and %s" % (tuple(k.shape), tuple(v.shape)))
     cu_k = cu_q if cu_k is None else cu_k
     batch = cu_q.shape[0] - 1
     if batch < 0:
         raise ValueError("cu_q must hold batch + 1 bounds, got none")
-    _index(cu_q, torch.int32, (batch + 1,), "cu_q")
-    _index(cu_k, torch.int32, (batch + 1,), "cu_k")
-    with _on(stream):
-        if out is None:
-            out = torch.empty((total_q, heads, dim), dtype=q.dtype, device=q.device)
-        if lse is None and return_lse:
-            lse = torch.empty((heads, total_q), dtype=torch.float32, device=q.device)
-    ck._req(out, q.dtype, (total_q, heads, dim), "out")
+    ck._req(cu_q, torch.int32, (batch + 1,), "cu_q")
+    if cu_k is not cu_q:
+        ck._req(cu_k, torch.int32, (batch + 1,), "cu_k")
+    if out is None:
+        out = _empty((total_q, heads, dim), q.dtype, q.device, stream)
+    else:
+        ck._req(out, q.dtype, (total_q, heads, dim), "out")
     if lse is not None:
         ck._req(lse, torch.float32, (heads, total_q), "lse")
-    ck._check(ck.load_library().ck_attention(
+    elif return_lse:
+        lse = _empty((heads, total_q), torch.float32, q.device, stream)
+    status = (ck._lib or ck.load_library()).ck_attention(
         q.data_ptr(), strides[0], k.data_ptr(), strides[1], v.data_ptr(), strides[2], cu_q.data_ptr(),
         cu_k.data_ptr(), batch, total_q, total_k, heads, kv_heads, dim, code, dim ** -0.5 if scale is None else scale,
-        1 if causal else 0, window, sinks, out.data_ptr(), ck._ptr(lse), ck._stream(stream)))
+        1 if causal else 0, window, sinks, out.data_ptr(), ck._ptr(lse), ck._stream(stream))
+    if status:
+        ck._check(status)
     return (out, lse) if return_lse else out
 
 
@@ -225,11 +224,8 @@ def ck_int4_prepare_weight(W, group=128, w4=None, w_scale=None, stream=None):
     ck._req(W, torch.float32, (N, K), "W")
     if group < 1 or K % group:
         raise ValueError("K must be a multiple of group (got K=%d group=%d)" % (K, group))
-    with _on(stream):
-        if w4 is None:
-            w4 = torch.empty((N, K // 8), dtype=torch.int32, device=W.device)
-        if w_scale is None:
-            w_scale = torch.empty((N, K // group), dtype=torch.bfloat16, device=W.device)
+    w4 = _empty((N, K // 8), torch.int32, W.device, stream) if w4 is None else w4
+    w_scale = _empty((N, K // group), torch.bfloat16, W.device, stream) if w_scale is None else w_scale
     ck._req(w4, torch.int32, (N, K // 8), "w4")
     ck._req(w_scale, torch.bfloat16, (N, K // group), "w_scale")
     ck._check(ck.load_library().ck_int4_prepare_weight(W.data_ptr(), N, K, group, w4.data_ptr(), w_scale.data_ptr(),
@@ -241,15 +237,13 @@ def ck_int4_pack(codes, w4=None, stream=None):
     """int8 codes [N,K] in [-8, 7] -> w4 int32 [N, K/8]."""
     N, K = codes.shape
     ck._req(codes, torch.int8, (N, K), "codes")
-    with _on(stream):
-        if w4 is None:
-            w4 = torch.empty((N, K // 8), dtype=torch.int32, device=codes.device)
+    w4 = _empty((N, K // 8), torch.int32, codes.device, stream) if w4 is None else w4
     ck._req(w4, torch.int32, (N, K // 8), "w4")
     ck._check(ck.load_library().ck_int4_pack(codes.data_ptr(), N, K, w4.data_ptr(), ck._stream(stream)))
     return w4
 
 
-def ck_int4_linear(x, w4, w_scale, bias=None, residual=None, y=None, ws=None, out_dtype=None, stream=None):
+def ck_int4_linear(x, w4, w_scale, bias=None, residual=None, y=None, out_dtype=None, stream=None):
     """y [M,N] of out_dtype (x's type by default) = x [M,K] (bf16 or fp16) times the 4-bit
     weight w4 int32 [N, K/8] with scales w_scale bf16 [N, K/group] (+ bias) (+ residual);
     residual has y's type and shape and may be y itself."""
@@ -265,16 +259,15 @@ def ck_int4_linear(x, w4, w_scale, bias=None, residual=None, y=None, ws=None, ou
         raise ValueError("K=%d does not divide into %d groups" % (K, groups))
     if bias is not None:
         ck._req(bias, x.dtype, (N,), "bias")
-    L = ck.load_library()
-    need = L.ck_int4_linear_workspace_size(M, N, K) if ws is None else 0
-    with _on(stream):
-        if y is None:
-            y = torch.empty((M, N), dtype=out_dtype, device=x.device)
-        if need:
-            ws = torch.empty(need, dtype=torch.uint8, device=x.device)
-    ck._req(y, out_dtype, (M, N), "y")
-    ck._residual(residual, out_dtype, M, N)
-    ck._check(L.ck_int4_linear(x.data_ptr(), w4.data_ptr(), w_scale.data_ptr(), ck._ptr(bias), ck._ptr(residual),
-                               y.data_ptr(), M, N, K, K // groups, code, out_code, ck._ptr(ws),
-                               0 if ws is None else ws.numel(), ck._stream(stream)))
+    if y is None:
+        y = _empty((M, N), out_dtype, x.device, stream)
+    else:
+        ck._req(y, out_dtype, (M, N), "y")
+    if residual is not None:
+        ck._req(residual, out_dtype, (M, N), "residual")
+    status = (ck._lib or ck.load_library()).ck_int4_linear(
+        x.data_ptr(), w4.data_ptr(), w_scale.data_ptr(), ck._ptr(bias), ck._ptr(residual), y.data_ptr(), M, N, K,
+        K // groups, code, out_code, ck._stream(stream))
+    if status:
+        ck._check(status)
     return y

@@ -181,7 +181,7 @@ def test_streams_share_nothing_and_graphs_replay():
     torch.cuda.synchronize()
     assert all(torch.equal(o, want) for per in outs for o in per)
     out = torch.empty_like(want)
-    ws = torch.full((ck.load_library().ck_paged_attention_workspace_size(3, 8, 2, 128),), 255, dtype=torch.uint8,
+    ws = torch.full((ck.load_library().ck_paged_attention_workspace_size(3, 8, 2, 128, table.shape[1] * 16),), 255, dtype=torch.uint8,
                     device=DEV)
     torch.cuda.synchronize()
     g = torch.cuda.CUDAGraph()

@@ -22,8 +22,8 @@ def lib():
 def cache(**kw):
     f = dict(k=4096, v=4096, k_scale=4096, v_scale=4096, num_pages=4, page_size=16, kv_heads=2, head_dim=64, dtype=0)
     f.update(kw)
-    c = transformer._CacheStruct(*[f[n] for n, _ in transformer._CacheStruct._fields_])
-    return c
+    return transformer._CACHE.pack(*[f[n] for n in ("k", "v", "k_scale", "v_scale", "num_pages", "page_size", "kv_heads",
+                                                    "head_dim", "dtype")])
 
 
 def norm_rope(lib, **kw):
@@ -33,7 +33,7 @@ def norm_rope(lib, **kw):
     c = f["cache"]
     return lib.ck_qk_norm_rope(f["qkv"], f["stride"], f["tokens"], f["hq"], f["hkv"], f["d"], f["dtype"], f["norm"],
                                f["qw"], f["kw"], f["eps"], f["rot"], f["inter"], f["pos"], f["table"], f["max_pos"],
-                               f["q"], f["k"], None if c is None else ctypes.addressof(c), f["slots"], None)
+                               f["q"], f["k"], c, f["slots"], None)
 
 
 @pytest.mark.parametrize("kw,what", [
@@ -54,11 +54,11 @@ def test_norm_rope_refusals(lib, kw, what):
 
 
 def paged(lib, **kw):
-    f = dict(q=P, stride=256, cache=cache(), table=P, blocks=5, lens=P, batch=3, hq=4, dtype=0, scale=0.1, window=0,
+    f = dict(q=P, stride=256, cache=cache(), table=P, blocks=50, lens=P, batch=3, hq=4, dtype=0, scale=0.1, window=0,
              sinks=0, out=P, lse=None, ws=P, nbytes=1 << 40)
     f.update(kw)
     c = f["cache"]
-    return lib.ck_paged_attention(f["q"], f["stride"], None if c is None else ctypes.addressof(c), f["table"],
+    return lib.ck_paged_attention(f["q"], f["stride"], c, f["table"],
                                   f["blocks"], f["lens"], f["batch"], f["hq"], f["dtype"], f["scale"], f["window"],
                                   f["sinks"], f["out"], f["lse"], f["ws"], f["nbytes"], None)
 
@@ -100,10 +100,10 @@ def test_attention_refusals(lib, kw, what):
 
 
 def int4(lib, **kw):
-    f = dict(x=P, w=P, s=P, bias=None, res=None, y=P, M=2, N=16, K=256, group=128, dtype=0, out=0, ws=P, nbytes=1 << 40)
+    f = dict(x=P, w=P, s=P, bias=None, res=None, y=P, M=2, N=16, K=256, group=128, dtype=0, out=0)
     f.update(kw)
     return lib.ck_int4_linear(f["x"], f["w"], f["s"], f["bias"], f["res"], f["y"], f["M"], f["N"], f["K"], f["group"],
-                              f["dtype"], f["out"], f["ws"], f["nbytes"], None)
+                              f["dtype"], f["out"], None)
 
 
 @pytest.mark.parametrize("kw,what", [
@@ -140,9 +140,9 @@ def test_no_device_is_reported_not_faked(lib):
 
 
 def test_workspace_sizes(lib):
-    assert lib.ck_paged_attention_workspace_size(-1, 8, 2, 64) == 0
-    assert lib.ck_paged_attention_workspace_size(1 << 20, 8, 2, 128) < 1 << 34
-    assert lib.ck_int4_linear_workspace_size(-1, 8, 128) == 0
+    assert lib.ck_paged_attention_workspace_size(-1, 8, 2, 64, 4096) == 0
+    assert lib.ck_paged_attention_workspace_size(1, 8, 2, 64, 100) == 0  # short tables need none
+    assert 0 < lib.ck_paged_attention_workspace_size(1 << 20, 8, 2, 128, 1 << 20) < 1 << 28
 
 
 def test_binding_checks():
