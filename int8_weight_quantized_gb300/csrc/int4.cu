@@ -40,22 +40,31 @@ constexpr int CHUNK = 128;                 // k of a ring unit
 constexpr int STAGES = 4;
 constexpr int W_LD = 80;                   // bytes of a unit's weight row: 64, padded so that 8 rows spread over the banks
 
+// (w & MASK) | bits in one instruction (with both as constants the compiler made two of it)
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t bits)
+{
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "n"(MASK), "r"(bits));
+    return r;
+}
+
 template <class E>
 __device__ __forceinline__ uint32_t codes_of(uint32_t word, int i)
 {
     // the pair k = 2 i, 2 i + 1 of the word's eight: code - 8 in two 16-bit floats
     if (std::is_same<E, Bf16>::value) {
-        const uint32_t u = ((word >> (4 * i)) & 0x000F000Fu) | 0x43004300u;  // 128 + code
+        const uint32_t u = and_or<0x000F000Fu>(word >> (4 * i), 0x43004300u);  // 128 + code
         const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u), __float2bfloat162_rn(136.0f));
         return *reinterpret_cast<const uint32_t*>(&v);
     }
     const uint32_t w = i < 2 ? word : word >> 8;
     if ((i & 1) == 0) {
-        const uint32_t u = (w & 0x000F000Fu) | 0x64006400u;  // 1024 + code
+        const uint32_t u = and_or<0x000F000Fu>(w, 0x64006400u);  // 1024 + code
         const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&u), __float2half2_rn(1032.0f));
         return *reinterpret_cast<const uint32_t*>(&v);
     }
-    const uint32_t u = (w & 0x00F000F0u) | 0x64006400u;  // 1024 + 16 code, exact like the rest
+    const uint32_t u = and_or<0x00F000F0u>(w, 0x64006400u);  // 1024 + 16 code, exact like the rest
     const __half2 v = __hfma2(*reinterpret_cast<const __half2*>(&u), __float2half2_rn(0.0625f), __float2half2_rn(-72.0f));
     return *reinterpret_cast<const uint32_t*>(&v);
 }
@@ -92,12 +101,18 @@ __global__ void __launch_bounds__(WARPS * 32) int4_kernel(const Int4Linear p)
         w_in[i] = n < p.N;
         w_src[i] = reinterpret_cast<const uint8_t*>(p.w4) + (w_in[i] ? n : 0) * (p.K / 2) + t * 16;
     }
-    static_assert(RT <= 2, "one lane per scale row");
-    const int64_t sn = n0 + lane;
-    const bool s_in = lane < 16 * RT && sn < p.N;
-    const int64_t s_first = (s_in ? sn : 0) * groups;  // the row's first scale
-    const __nv_bfloat16* s_src = static_cast<const __nv_bfloat16*>(p.w_scale) + s_first;
-    const int s_odd = (int)(s_first & 1);
+    constexpr int SI = (16 * RT + 31) / 32;  // instructions that copy a scale row per lane
+    const __nv_bfloat16* s_src[SI];
+    bool s_in[SI];
+    int s_odd[SI];  // whether the row's first scale lies in an upper half
+#pragma unroll
+    for (int i = 0; i < SI; ++i) {
+        const int64_t n = n0 + i * 32 + lane;
+        s_in[i] = i * 32 + lane < 16 * RT && n < p.N;
+        const int64_t first = (s_in[i] ? n : 0) * groups;
+        s_src[i] = static_cast<const __nv_bfloat16*>(p.w_scale) + first;
+        s_odd[i] = (int)(first & 1);
+    }
     auto issue = [&](int c, int stage) {
         if (c < c1) {
             const uint32_t w = ring + stage * kUnit<RT> + g * W_LD + t * 16;
@@ -106,14 +121,16 @@ __global__ void __launch_bounds__(WARPS * 32) int4_kernel(const Int4Linear p)
             for (int i = 0; i < 2 * RT; ++i)
                 cp_async16(w + i * 8 * W_LD, w_src[i] + c * 64, w_in[i]);
             // the row's scales of this chunk: 8 bytes, 4, or the aligned 4 that hold the one
-            if (lane < 16 * RT) {
-                if (PER_CHUNK == 4)
-                    cp_async_small<8>(sc, s_src + 4 * c, s_in);
-                else if (PER_CHUNK == 2)
-                    cp_async_small<4>(sc, s_src + 2 * c, s_in);
-                else
-                    cp_async_small<4>(sc, s_src + ((s_odd + (c >> log_chunks)) & ~1) - s_odd, s_in);
-            }
+#pragma unroll
+            for (int i = 0; i < SI; ++i)
+                if (i * 32 + lane < 16 * RT) {
+                    if (PER_CHUNK == 4)
+                        cp_async_small<8>(sc + i * 256, s_src[i] + 4 * c, s_in[i]);
+                    else if (PER_CHUNK == 2)
+                        cp_async_small<4>(sc + i * 256, s_src[i] + 2 * c, s_in[i]);
+                    else
+                        cp_async_small<4>(sc + i * 256, s_src[i] + ((s_odd[i] + (c >> log_chunks)) & ~1) - s_odd[i], s_in[i]);
+                }
         }
         cp_async_commit();
     };
@@ -137,12 +154,8 @@ __global__ void __launch_bounds__(WARPS * 32) int4_kernel(const Int4Linear p)
         if (c0 < c1)
             load_x(c0, j);
     }
-    int row_odd[RT][2];  // PER_CHUNK == 1: whether the row's first scale lies in an upper half
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            row_odd[rt][h] = (int)(((n0 + 16 * rt + 8 * h + g) * groups) & 1);
+    // PER_CHUNK == 1: whether the first scale of this lane's rows (8 apart) lies in an upper half
+    const int row_odd = (int)(((n0 + g) * groups) & 1);
 
     float sum[RT][MT][4] = {};
     float acc[RT][MT][4] = {};
@@ -177,7 +190,7 @@ __global__ void __launch_bounds__(WARPS * 32) int4_kernel(const Int4Linear p)
                     for (int h = 0; h < 2; ++h) {
                         const int e = PER_CHUNK == 4 ? j : PER_CHUNK == 2 ? j >> 1 : 0;
                         const uint32_t pair = lds32(sc + (16 * rt + 8 * h) * 8 + (e >> 1) * 4);
-                        const bool upper = PER_CHUNK == 1 ? (row_odd[rt][h] + (c >> log_chunks)) & 1 : e & 1;
+                        const bool upper = PER_CHUNK == 1 ? (row_odd + (c >> log_chunks)) & 1 : e & 1;
                         const float s = __uint_as_float(upper ? pair & 0xFFFF0000u : pair << 16);
 #pragma unroll
                         for (int mt = 0; mt < MT; ++mt) {
