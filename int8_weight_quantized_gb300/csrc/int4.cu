@@ -330,13 +330,15 @@ cudaError_t by_group(const Int4Linear& p, cudaStream_t s)
                            : launch<E, RT, MT, 1, KW>(p, s);
 }
 
-// KW: long runs of K per warp spread its set-up over more work, short ones give a narrow layer
-// enough warps: the fewest warps per row group that still make two blocks per SM.
+// KW: long runs of K per warp spread its set-up over more work and let a block's row groups share
+// their reads of x in L1; short ones give a narrow layer enough warps.  The fewest warps per row
+// group that still make two blocks per SM, or one where there is more than one tile of rows of x
+// (16 rows, 16384 x 4096: 17.9 us with two blocks per SM, 15.1 with one; 8 rows: 14.2 and 15.0).
 template <class E, int RT, int MT>
 cudaError_t by_split(const Int4Linear& p, const DeviceInfo& dev, cudaStream_t s)
 {
     const int64_t blocks1 = (p.N + 16 * RT * WARPS - 1) / (16 * RT * WARPS);  // at KW = 1
-    const int64_t want = 2 * dev.sm_count;
+    const int64_t want = (MT == 1 ? 2 : 1) * dev.sm_count;
     if (blocks1 * 2 >= want)
         return by_group<E, RT, MT, 2>(p, s);
     if (blocks1 * 4 >= want)
