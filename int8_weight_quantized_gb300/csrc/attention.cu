@@ -7,13 +7,15 @@
 // Bound: the tensor cores, 4 dim flops per visible pair and head (and next to them the
 // exponentials, one per pair and head).
 //
-// A block takes 256 queries of one head as two tiles of 128 and walks the key tiles (128 keys)
-// that any of them sees; a query tile skips those that it sees nothing of.  One block per SM:
+// An item is 256 queries of one head, as two tiles of 128; it walks the key tiles (128 keys) that
+// any of them sees, a query tile skipping those that it sees nothing of.  One block per SM takes
+// items by turns (the longest first, every second round backwards), and its roles run on from
+// item to item: the first scores of the next are computed while the last sums of one are stored.
 //   warp 0      copies by TMA: the two Q tiles, then K and V tiles through one ring;
 //   warp 1      issues the products, one thread: S_t = Q_t K^T (both operands in shared
 //               memory) and O_t += P_t V (P from tensor memory, V as it lies, keys by columns),
 //               all accumulators in tensor memory;
-//   warps 2-3   look every V tile over before it is used (below);
+//   warps 2-3   idle (they complete the warpgroup for the register re-balancing);
 //   warps 4-11  softmax, a warpgroup for each query tile, one thread per query row: reads its
 //               row of S, takes the maximum, writes the weights back over S as the 16-bit
 //               operand P of the second product.
@@ -28,12 +30,13 @@
 // sums in floating point, so how far it trails costs no precision.  S_{j+1} being complete
 // means that O += P_j V_j is, since it was issued before.
 //
-// What a mask hides has no part in a row: hidden scores are replaced, not multiplied, and V
-// rows beyond the sequence are zeroed in shared memory.  A V row within the sequence that some
-// of the tile's queries see and others do not is multiplied by a weight of zero for the
-// others: harmless unless it holds an infinity or NaN.  So V tiles that need a mask are
-// checked, and a block that met such a value computes its rows again, one at a time, with
-// attend_row, which reads visible keys only.
+// What a mask hides has no part in a row: hidden scores are replaced, not multiplied.  A V row
+// that some of a tile's queries see and others do not, or that lies beyond the sequence's end,
+// is multiplied by a weight of zero for those: harmless unless it holds an infinity or NaN, and
+// then the sums of the rows it does not belong to become NaN, never a wrong number.  So a warp
+// that finds a sum that is not finite looks through the V rows of its masked tiles, and if one
+// of them holds such a value, its rows are computed again, one at a time, with attend_row, which
+// reads visible keys only.
 //
 // Rounding to fewer bits: each weight once, to the 16-bit type of V, as the tensor core takes
 // it; scores, sums, maxima and O are fp32.
@@ -87,14 +90,17 @@ struct PromptArgs {
     void* out;
     float* lse;
     int64_t slots;   // tile slots of a head
+    int64_t items;   // slots * q_heads
 };
 
-// One block's share: which keys its rows see, and the key tiles to walk.
+// Which keys an item's rows see, and the key tiles to walk.
 struct Item {
-    int64_t q_row, k_row;  // first query row of the block, first key row of the sequence
-    int rows;              // queries of the block, at most ROWS
+    int64_t q_row, k_row;  // first query row of the item, first key row of the sequence
+    int head;
+    bool bad;              // its sequence's bounds are out of range
+    int rows;              // queries of the item, at most ROWS
     int keys;              // keys of the sequence
-    int offset;            // query r of the block stands at key position r + offset
+    int offset;            // query r of the item stands at key position r + offset
     bool causal;
     int window, sinks;     // window 0: none
     int prefix, first, count;  // key tiles: 0 .. prefix - 1, then first ..; count in all
@@ -252,14 +258,14 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint64_t* s_full = bars + 2;         // [2] S_t is complete (and every product before it)
     uint64_t* p_full = bars + 4;         // [2] P_t is written, O_t may be added to
     uint64_t* o_full = bars + 6;         // [2] O_t is final
-    uint64_t* k0_full = bars + 8;
-    uint64_t* drain = bars + 9;
-    uint64_t* full = bars + 10;          // [STAGES] V_j and K_{j+1} have landed
-    uint64_t* ready = full + STAGES;     // [STAGES] and V_j is looked over
-    uint64_t* empty = ready + STAGES;    // [STAGES] their products are done
+    uint64_t* q_empty = bars + 8;        // [2] the item's last scores of tile t are computed
+    uint64_t* k0_full = bars + 10;
+    uint64_t* k0_empty = bars + 11;
+    uint64_t* drain = bars + 12;
+    uint64_t* full = bars + 13;          // [STAGES] V_j and K_{j+1} have landed
+    uint64_t* empty = full + STAGES;     // [STAGES] their products are done
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(empty + STAGES);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    volatile int* dirty = abort_flag + 1;  // a V row holds an infinity or NaN
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (warp == 0 && lane == 0) {
@@ -268,16 +274,16 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(&s_full[t], 1);
             mbar_init(&p_full[t], 4);
             mbar_init(&o_full[t], 1);
+            mbar_init(&q_empty[t], 1);
         }
         mbar_init(k0_full, 1);
+        mbar_init(k0_empty, 1);
         mbar_init(drain, 1);
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&ready[s], 2);
             mbar_init(&empty[s], 1);
         }
         *abort_flag = 0;
-        *dirty = 0;
         fence_mbar_init();
         fence_proxy_async_smem();
         tma_prefetch_desc(&tmQ);
@@ -295,25 +301,23 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     griddep_wait();
 
-    // ---- this block's share; blocks start in order, so the last (for causal prompts the
-    // longest) tiles come first
-    const int64_t slot = p.slots - 1 - (int64_t)blockIdx.x / p.q_heads;
-    const int head = (int)(blockIdx.x % p.q_heads);
-    const int kv_head = head / (p.q_heads / p.kv_heads);
-    Item w;
-    bool bad;
-    {
+    // ---- the block's items.  Item i counts from the last tile slot down: causal prompts' longest
+    // tiles first.
+    auto item_at = [&](int64_t i) {
+        Item w;
+        const int64_t slot = p.slots - 1 - i / p.q_heads;
+        w.head = (int)(i % p.q_heads);
         const int64_t b = sequence_of_slot(p.cu_q, p.batch, slot);
         const int64_t q0 = __ldg(p.cu_q + b), q1 = __ldg(p.cu_q + b + 1);
         const int64_t k0 = __ldg(p.cu_k + b), k1 = __ldg(p.cu_k + b + 1);
         const bool bad_q = q0 < 0 || q1 < q0 || q1 > p.total_q;
-        bad = bad_q || k0 < 0 || k1 < k0 || k1 > p.total_k;
+        w.bad = bad_q || k0 < 0 || k1 < k0 || k1 > p.total_k;
         const int64_t r0 = (slot - (q0 / ROWS + b)) * ROWS;
         w.q_row = q0 + r0;
         w.rows = bad_q || r0 < 0 ? 0 : (int)min((int64_t)ROWS, max(q1 - w.q_row, (int64_t)0));
         w.k_row = k0;
-        w.keys = bad ? 0 : (int)(k1 - k0);
-        w.offset = bad ? 0 : (int)(r0 + (k1 - k0) - (q1 - q0));
+        w.keys = w.bad ? 0 : (int)(k1 - k0);
+        w.offset = w.bad ? 0 : (int)(r0 + (k1 - k0) - (q1 - q0));
         w.causal = p.causal;
         w.window = (int)min(p.window, (int64_t)0x3FFFFFFF);
         w.sinks = w.window ? (int)min(p.sinks, (int64_t)0x3FFFFFFF) : 0;
@@ -328,58 +332,79 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             w.count = w.prefix + top / BM - w.first + 1;
         }
-        if (bad && threadIdx.x == 0)
-            atomicOr(err, kErrIndex);
-        w.rows = __shfl_sync(0xffffffffu, w.rows, 0);
-        w.keys = __shfl_sync(0xffffffffu, w.keys, 0);
-        w.offset = __shfl_sync(0xffffffffu, w.offset, 0);
-        w.prefix = __shfl_sync(0xffffffffu, w.prefix, 0);
-        w.first = __shfl_sync(0xffffffffu, w.first, 0);
-        w.count = __shfl_sync(0xffffffffu, w.count, 0);
-    }
+        return w;
+    };
+    // fn(w) for the block's items in order; stops where fn returns false
+    auto each_item = [&](auto fn) {
+        const int64_t blocks = gridDim.x;
+        for (int64_t round = 0; round * blocks < p.items; ++round) {
+            const int64_t i = round * blocks + ((round & 1) ? blocks - 1 - blockIdx.x : blockIdx.x);
+            if (i < p.items && !fn(item_at(i)))
+                return;
+        }
+    };
+    const int group = p.q_heads / p.kv_heads;
 
     if (warp < 4) {
         setmaxnreg_dec<REGS_LOAD>();
         if (warp == 0) {
             // ---------------------------------------------------------------- copies
-            if (lane == 0 && w.count > 0) {
+            if (lane == 0) {
                 auto load = [&](const CUtensorMap* map, uint8_t* dst, uint64_t* bar, int h, int64_t row) {
                     for (int x = 0; x < C::BOXES; ++x)
                         tma_load_3d(dst + x * C::BOX_BYTES, map, bar, x * 64, h, (int32_t)row);
                 };
-                auto load_q = [&](int t) {
-                    if (w.any(t)) {
-                        mbar_arrive_expect_tx(&q_full[t], C::TILE_BYTES);
-                        load(&tmQ, s_q + t * C::TILE_BYTES, &q_full[t], head, w.q_row + BM * t);
-                    }
+                auto wait = [&](uint64_t* bar, uint32_t parity) {
+                    return mbar_wait(bar, parity, abort_flag, err, kErrWaitAttention, TIMEOUT_NS);
                 };
-                load_q(0);
-                mbar_arrive_expect_tx(k0_full, C::TILE_BYTES);
-                load(&tmK, s_k0, k0_full, kv_head, w.k_row + w.key0(0));
-                load_q(1);
+                uint32_t uses = 0, k0_uses = 0, q_uses[2] = {0, 0};  // loads so far of the ring, K_0, Q_t
                 bool ok = true;
-                int j = 0;
-                for (; j < w.count; ++j) {
-                    const int s = j % STAGES;
-                    if (!mbar_wait(&empty[s], (uint32_t)(j / STAGES + 1) & 1u, abort_flag, err, kErrWaitAttention,
-                                   TIMEOUT_NS)) {
-                        ok = false;
-                        break;
+                each_item([&](const Item& w) {
+                    if (w.bad)
+                        atomicOr(err, kErrIndex);
+                    if (w.count == 0)
+                        return true;
+                    auto load_q = [&](int t) {
+                        if (!w.any(t))
+                            return true;
+                        if (!wait(&q_empty[t], (q_uses[t] + 1) & 1u))
+                            return false;
+                        ++q_uses[t];
+                        mbar_arrive_expect_tx(&q_full[t], C::TILE_BYTES);
+                        load(&tmQ, s_q + t * C::TILE_BYTES, &q_full[t], w.head, w.q_row + BM * t);
+                        return true;
+                    };
+                    const int kv_head = w.head / group;
+                    ok = load_q(0) && wait(k0_empty, (k0_uses + 1) & 1u);
+                    if (!ok)
+                        return false;
+                    ++k0_uses;
+                    mbar_arrive_expect_tx(k0_full, C::TILE_BYTES);
+                    load(&tmK, s_k0, k0_full, kv_head, w.k_row + w.key0(0));
+                    ok = load_q(1);
+                    for (int j = 0; ok && j < w.count; ++j) {
+                        const int s = uses % STAGES;
+                        ok = wait(&empty[s], (uses / STAGES + 1) & 1u);
+                        if (!ok)
+                            break;
+                        ++uses;
+                        const bool more = j + 1 < w.count;
+                        uint8_t* dst = s_ring + (size_t)s * 2 * C::TILE_BYTES;
+                        mbar_arrive_expect_tx(&full[s], more ? 2 * C::TILE_BYTES : C::TILE_BYTES);
+                        load(&tmV, dst, &full[s], kv_head, w.k_row + w.key0(j));
+                        if (more)
+                            load(&tmK, dst + C::TILE_BYTES, &full[s], kv_head, w.k_row + w.key0(j + 1));
                     }
-                    const bool more = j + 1 < w.count;
-                    uint8_t* dst = s_ring + (size_t)s * 2 * C::TILE_BYTES;
-                    mbar_arrive_expect_tx(&full[s], more ? 2 * C::TILE_BYTES : C::TILE_BYTES);
-                    load(&tmV, dst, &full[s], kv_head, w.k_row + w.key0(j));
-                    if (more)
-                        load(&tmK, dst + C::TILE_BYTES, &full[s], kv_head, w.k_row + w.key0(j + 1));
-                }
+                    return ok;
+                });
                 if (!ok) {  // aborting: every issued copy lands before shared memory is released
-                    for (int i = max(0, j - STAGES); i < j; ++i)
-                        wait_out(&full[i % STAGES], (uint32_t)(i / STAGES) & 1u, err);
-                    wait_out(k0_full, 0, err);
+                    for (uint32_t i = uses > STAGES ? uses - STAGES : 0; i < uses; ++i)
+                        wait_out(&full[i % STAGES], (i / STAGES) & 1u, err);
+                    if (k0_uses > 0)
+                        wait_out(k0_full, (k0_uses - 1) & 1u, err);
                     for (int t = 0; t < 2; ++t)
-                        if (w.any(t))
-                            wait_out(&q_full[t], 0, err);
+                        if (q_uses[t] > 0)
+                            wait_out(&q_full[t], (q_uses[t] - 1) & 1u, err);
                 }
             }
             __syncwarp();
@@ -388,7 +413,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             // The whole warp walks the tiles, so that descriptors stay uniform values, and one
             // elected lane issues; the others wait for it after each issue (left to run ahead into
             // the next barrier's polling loop they can keep it from being scheduled).
-            if (w.count > 0) {
+            {
                 const uint32_t idesc_s = idesc_of<E>(BM, false) | (p.negate ? 1u << 13 : 0u);
                 constexpr uint32_t idesc_o = idesc_of<E>(DIM, true);
                 const uint64_t q_desc = desc_kmajor_sw128(smem_u32(s_q));
@@ -396,9 +421,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const uint64_t k_desc = desc_kmajor_sw128(smem_u32(s_ring) + C::TILE_BYTES);
                 const uint64_t v_desc = desc_nmajor_sw128(smem_u32(s_ring), C::BOX_BYTES);
                 constexpr uint64_t kTile = C::TILE_BYTES >> 4, kBox = C::BOX_BYTES >> 4;
-                const Active active[2] = {{w.heads(), w.begin(0), w.last(0)}, {w.heads(), w.begin(1), w.last(1)}};
-                bool started[2] = {false, false}, q_seen[2] = {false, false};
+                uint32_t uses = 0, k0_uses = 0, q_uses[2] = {0, 0};
                 uint32_t p_phase[2] = {0, 0};
+                bool started[2];
                 auto wait = [&](uint64_t* bar, uint32_t parity) {
                     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
                         return true;
@@ -420,42 +445,64 @@ __global__ void __launch_bounds__(THREADS, 1)
                         mma_ts(tmem + 2 * BM + t * DIM, tmem + t * BM + k * 8, b + k * (16 * 128 >> 4), idesc_o,
                                k > 0 || started[t]);
                 };
-                auto q_here = [&](int t) {
-                    if (!q_seen[t] && !wait(&q_full[t], 0))
-                        return false;
-                    q_seen[t] = true;
-                    return true;
-                };
                 // The tensor core takes a product about as fast as one thread issues it and queues
                 // only a few, and every step of this warp beside the busy softmax warps takes some
                 // 100 cycles: so one wait and one branch stand between two groups of products.
-                auto run = [&]() {
-                    if (!wait(k0_full, 0))
-                        return;
+                each_item([&](Item w) {
+                    // the same in every lane; said so, descriptors and bounds stay uniform values
+                    w.rows = __shfl_sync(0xffffffffu, w.rows, 0);
+                    w.keys = __shfl_sync(0xffffffffu, w.keys, 0);
+                    w.offset = __shfl_sync(0xffffffffu, w.offset, 0);
+                    w.prefix = __shfl_sync(0xffffffffu, w.prefix, 0);
+                    w.first = __shfl_sync(0xffffffffu, w.first, 0);
+                    w.count = __shfl_sync(0xffffffffu, w.count, 0);
+                    if (w.count == 0)
+                        return true;
+                    const Active active[2] = {{w.heads(), w.begin(0), w.last(0)}, {w.heads(), w.begin(1), w.last(1)}};
+                    bool q_seen[2] = {false, false};
+                    auto q_here = [&](int t) {
+                        if (!q_seen[t] && !wait(&q_full[t], q_uses[t] & 1u))
+                            return false;
+                        q_uses[t] += q_seen[t] ? 0 : 1;
+                        q_seen[t] = true;
+                        return true;
+                    };
+                    started[0] = started[1] = false;
+                    if (!wait(k0_full, k0_uses & 1u))
+                        return false;
+                    ++k0_uses;
 #pragma unroll
                     for (int t = 0; t < 2; ++t)
                         if (active[t](0)) {
                             if (!q_here(t))
-                                return;
+                                return false;
                             tc_fence_after();
-                            if (leader)
+                            if (leader) {
                                 scores(t, k0_desc);
+                                if (active[t].last == 0)
+                                    mma_commit(&q_empty[t]);
+                            }
                             __syncwarp();
                         }
+                    if (leader)
+                        mma_commit(k0_empty);
+                    __syncwarp();
                     for (int j = 0; j < w.count; ++j) {
-                        const int s = j % STAGES;
+                        const int s = uses % STAGES;
+                        const uint32_t parity = (uses / STAGES) & 1u;
+                        ++uses;
                         const uint64_t v = v_desc + s * 2 * kTile, k = k_desc + s * 2 * kTile;
                         const bool more = j + 1 < w.count;
-                        if (!wait(&ready[s], (uint32_t)(j / STAGES) & 1u))
-                            return;
+                        if (!wait(&full[s], parity))
+                            return false;
 #pragma unroll
                         for (int t = 0; t < 2; ++t) {
                             const bool now = active[t](j), next = more && active[t](j + 1);
                             if (next && !q_here(t))
-                                return;
+                                return false;
                             if (now) {
                                 if (!wait(&p_full[t], p_phase[t]))
-                                    return;
+                                    return false;
                                 p_phase[t] ^= 1u;
                             }
                             tc_fence_after();
@@ -465,8 +512,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                                     if (j == active[t].last)
                                         mma_commit(&o_full[t]);
                                 }
-                                if (next)
+                                if (next) {
                                     scores(t, k);
+                                    if (j + 1 == active[t].last)
+                                        mma_commit(&q_empty[t]);
+                                }
                                 if (t == 1)
                                     mma_commit(&empty[s]);
                             }
@@ -474,62 +524,13 @@ __global__ void __launch_bounds__(THREADS, 1)
                             started[t] |= now;
                         }
                     }
-                };
-                run();
+                    return true;
+                });
                 // every product must be complete before tensor and shared memory are released
                 if (leader) {
                     mma_commit(drain);
                     wait_out(drain, 0, err);
                 }
-            }
-            __syncwarp();
-        } else {
-            // -------------------------------------------------- V tiles, before their use
-            const int tid = threadIdx.x - 64;  // 0..63: rows tid and tid + 64
-            const Active active0 = {w.heads(), w.begin(0), w.last(0)}, active1 = {w.heads(), w.begin(1), w.last(1)};
-            for (int j = 0; j < w.count; ++j) {
-                const int s = j % STAGES;
-                const bool ok = mbar_wait(&full[s], (uint32_t)(j / STAGES) & 1u, abort_flag, err, kErrWaitAttention,
-                                          TIMEOUT_NS);
-                if (!__all_sync(0xffffffffu, ok))
-                    break;
-                const int k0 = w.key0(j);
-                const bool check = (active0(j) && w.partial(0, k0)) || (active1(j) && w.partial(1, k0));
-                if (check) {
-                    uint8_t* tile = s_ring + (size_t)s * 2 * C::TILE_BYTES;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int r = tid + 64 * h;
-                        if (k0 + r >= w.keys) {
-                            for (int x = 0; x < C::BOXES; ++x)
-                                for (int c = 0; c < 8; ++c)
-                                    *reinterpret_cast<uint4*>(tile + x * C::BOX_BYTES + r * 128 + ((c ^ r) & 7) * 16) =
-                                        make_uint4(0u, 0u, 0u, 0u);
-                        } else {
-                            // 0 * x is NaN exactly for infinities and NaN; the sum keeps it
-                            typename E::T2 sum = {E::from(0.0f), E::from(0.0f)};
-                            const typename E::T2 zero = sum;
-                            for (int x = 0; x < C::BOXES; ++x)
-#pragma unroll
-                                for (int c = 0; c < 8; ++c) {
-                                    const uint4 v = *reinterpret_cast<const uint4*>(tile + x * C::BOX_BYTES + r * 128 +
-                                                                                    ((c ^ r) & 7) * 16);
-                                    const uint32_t words[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i)
-                                        sum = __hfma2(*reinterpret_cast<const typename E::T2*>(&words[i]), zero, sum);
-                                }
-                            const float2 f = E::to2(*reinterpret_cast<const uint32_t*>(&sum));
-                            if (f.x != f.x || f.y != f.y)
-                                *dirty = 1;
-                        }
-                    }
-                    fence_proxy_async_smem();
-                }
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&ready[s]);
-                __syncwarp();  // before the next wait, as for the products
             }
             __syncwarp();
         }
@@ -542,16 +543,19 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int r = BM * t + row;    // row of the block
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         const uint32_t s_addr = tmem + lanes + t * BM, o_addr = tmem + lanes + 2 * BM + t * DIM;
-        const int hi = w.hi(r), lo = w.lo(r);
-        const Active active = {w.heads(), w.begin(t), w.last(t)};
         const float c = p.c;
         // how far (log2) weights may exceed 1 before the tile has to be done again
         constexpr float kHard = std::is_same<E, Bf16>::value ? 64.0f : 15.0f;
+        uint32_t phase = 0, o_phase = 0;
+        bool ok = true;  // once a wait has given up, the remaining rows become NaN
+        each_item([&](const Item& w) {
+        const int hi = w.hi(r), lo = w.lo(r);
+        const Active active = {w.heads(), w.begin(t), w.last(t)};
+        const bool any = w.any(t);
         float m = -INFINITY;  // what the row's sums are relative to, in units of scores
         float top = -INFINITY;
         float l = 0.0f;
-        uint32_t phase = 0;
-        bool started = false, ok = true;
+        bool started = false;
         // bring the row's sums to the maximum `top`, where `raise`
         auto raise_to_top = [&](bool raise) {
             const float f = raise ? fast_exp2((m - top) * c) : 1.0f;
@@ -571,7 +575,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tmem_st_32x32b_x16(o_addr + 16 * i, v);
             }
         };
-        for (int j = 0; j < w.count; ++j) {
+        for (int j = 0; ok && j < w.count; ++j) {
             if (!active(j))
                 continue;
             const int k0 = w.key0(j);
@@ -657,14 +661,16 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         // ---- the rows' outputs
         const int64_t out_row = w.q_row + r;
-        const int64_t at = (out_row * p.q_heads + head) * DIM;
+        const int64_t at = (out_row * p.q_heads + w.head) * DIM;
         const bool mine = r < w.rows;
-        if (ok && w.count > 0 && w.any(t)) {
-            ok = mbar_wait(&o_full[t], 0, abort_flag, err, kErrWaitAttention, TIMEOUT_NS);
+        if (ok && any) {
+            ok = mbar_wait(&o_full[t], o_phase, abort_flag, err, kErrWaitAttention, TIMEOUT_NS);
             ok = __all_sync(0xffffffffu, ok);
+            o_phase ^= 1u;
             tc_fence_after();
-            if (ok && *dirty == 0) {
+            if (ok) {
                 const float f = l == 0.0f ? 0.0f : 1.0f / l;
+                float check = 0.0f;  // 0 while all is finite, else NaN
 #pragma unroll 1
                 for (int i = 0; i < DIM / 32; ++i) {
                     uint32_t v[32];
@@ -672,46 +678,52 @@ __global__ void __launch_bounds__(THREADS, 1)
                     tmem_wait_ld();
                     float x[32];
 #pragma unroll
-                    for (int n = 0; n < 32; ++n)
+                    for (int n = 0; n < 32; ++n) {
                         x[n] = __uint_as_float(v[n]);
+                        check = fmaf(x[n], 0.0f, check);
+                    }
                     if (mine)
                         store_row<E>(p.out, at + 32 * i, x, f);
                 }
                 if (mine && p.lse != nullptr)
-                    p.lse[(int64_t)head * p.total_q + out_row] = (m * c + log2f(l)) * kLn2;
-            } else if (ok) {
-                // a row at a time, over visible keys only; the tile's Q has been used
-                float* qs = reinterpret_cast<float*>(s_q + t * C::TILE_BYTES) + quarter * DIM;
-                for (int i = 0; i < 32 && BM * t + quarter * 32 + i < w.rows; ++i) {
-                    const int ri = BM * t + quarter * 32 + i;
-                    const T* q = static_cast<const T*>(p.q) + (w.q_row + ri) * p.q_stride + (int64_t)head * DIM;
-                    __syncwarp();
-                    for (int d = lane; d < DIM; d += 32)
-                        qs[d] = E::to(q[d]) * (p.scale * kLog2e);
-                    __syncwarp();
-                    const VisibleKeys keys = p.causal ? visible_keys(ri + w.offset + 1, p.window, p.sinks)
-                                                      : visible_keys(w.keys, 0, 0);
-                    float acc[DIM / 32], rm, rl;
-                    attend_row<E, false, DIM>(qs, keys.count(), [&](int v) {
-                        const int64_t k = w.k_row + keys.key(v);
-                        KvRow kv;
-                        kv.k = static_cast<const T*>(p.k) + k * p.k_stride + (int64_t)kv_head * DIM;
-                        kv.v = static_cast<const T*>(p.v) + k * p.v_stride + (int64_t)kv_head * DIM;
-                        kv.ks = kv.vs = 1.0f;
-                        return kv;
-                    }, acc, rm, rl);
-                    T* dst = static_cast<T*>(p.out) + ((w.q_row + ri) * p.q_heads + head) * DIM;
+                    p.lse[(int64_t)w.head * p.total_q + out_row] = (m * c + log2f(l)) * kLn2;
+                // (l is NaN or infinite only through scores, which masks replace: not for this)
+                const uint32_t again = __ballot_sync(0xffffffffu, mine && check != check);
+                if (again) {
+                    const int64_t kv_col = (int64_t)(w.head / group) * DIM;
+                    const T* k = static_cast<const T*>(p.k) + w.k_row * p.k_stride + kv_col;
+                    const T* v = static_cast<const T*>(p.v) + w.k_row * p.v_stride + kv_col;
+                    bool found = false;
+                    for (int j = 0; j < w.count; ++j) {
+                        const int k0 = w.key0(j);
+                        if (!active(j) || !w.partial(t, k0))
+                            continue;
+                        for (int key = k0 + lane; key < k0 + BM && w.k_row + key < p.total_k; key += 32)
+                            for (int d = 0; d < DIM; ++d)
+                                found |= !(fabsf(E::to(v[key * p.v_stride + d])) < INFINITY);
+                    }
+                    const uint32_t redo = __any_sync(0xffffffffu, found) ? again : 0u;
+                    __syncwarp();  // the rows' own stores come first
+                    for (int i = 0; i < 32; ++i) {
+                        if (!((redo >> i) & 1u))
+                            continue;
+                        const int64_t qi = w.q_row + BM * t + quarter * 32 + i;
+                        const VisibleKeys keys = p.causal ? visible_keys(BM * t + quarter * 32 + i + w.offset + 1, p.window, p.sinks)
+                                                          : visible_keys(w.keys, 0, 0);
+                        float acc[DIM / 32], rm, rl;
+                        attend_row<E, DIM>(static_cast<const T*>(p.q) + qi * p.q_stride + (int64_t)w.head * DIM,
+                                           p.scale * kLog2e, keys, k, p.k_stride, v, p.v_stride, acc, rm, rl);
+                        T* dst = static_cast<T*>(p.out) + (qi * p.q_heads + w.head) * DIM;
 #pragma unroll
-                    for (int d = 0; d < DIM / 32; ++d)
-                        dst[lane + 32 * d] = E::from(keys.count() == 0 ? 0.0f : acc[d] / rl);
-                    if (lane == 0 && p.lse != nullptr)
-                        p.lse[(int64_t)head * p.total_q + w.q_row + ri] = (rm + log2f(rl)) * kLn2;
+                        for (int d = 0; d < DIM / 32; ++d)
+                            dst[lane + 32 * d] = E::from(keys.count() == 0 ? 0.0f : acc[d] / rl);
+                    }
                 }
             }
         }
-        if (mine && (!ok || bad || !w.any(t))) {
+        if (mine && (!ok || w.bad || !any)) {
             // no keys: zeros; bounds out of range or a wait that gave up: NaN
-            const bool nan = bad || !ok;
+            const bool nan = w.bad || !ok;
             float x[32];
 #pragma unroll
             for (int n = 0; n < 32; ++n)
@@ -720,8 +732,13 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int i = 0; i < DIM / 32; ++i)
                 store_row<E>(p.out, at + 32 * i, x, 1.0f);
             if (p.lse != nullptr)
-                p.lse[(int64_t)head * p.total_q + out_row] = nan ? NAN : -INFINITY;
+                p.lse[(int64_t)w.head * p.total_q + out_row] = nan ? NAN : -INFINITY;
         }
+        // O is read: the item's last hand-over of P was before that, so the next item's first one,
+        // which lets O be written again, says so too
+        tc_fence_before();
+        return true;
+        });
     }
     griddep_launch_dependents();
     tc_fence_before();
@@ -771,7 +788,7 @@ bool make_map(CUtensorMap* map, const void* base, int64_t rows, int heads, int d
 }
 
 template <class E, int DIM>
-cudaError_t launch(const PromptAttention& p, unsigned int* err, cudaStream_t s, std::string* why)
+cudaError_t launch(const PromptAttention& p, const DeviceInfo& dev, unsigned int* err, cudaStream_t s, std::string* why)
 {
     using C = Cfg<DIM>;
     // a kernel attribute belongs to the context it was set in: set once per context
@@ -814,7 +831,9 @@ cudaError_t launch(const PromptAttention& p, unsigned int* err, cudaStream_t s, 
     a.out = p.out;
     a.lse = p.lse;
     a.slots = p.total_q / ROWS + p.batch;
-    return launch_pdl(prompt_kernel<E, DIM>, dim3((unsigned)(a.slots * p.q_heads)), dim3(THREADS), C::SMEM, s, q, k, v, a,
+    a.items = a.slots * p.q_heads;
+    const unsigned blocks = (unsigned)std::min<int64_t>(a.items, dev.sm_count);
+    return launch_pdl(prompt_kernel<E, DIM>, dim3(blocks), dim3(THREADS), C::SMEM, s, q, k, v, a,
                       err);
 }
 
@@ -822,14 +841,13 @@ cudaError_t launch(const PromptAttention& p, unsigned int* err, cudaStream_t s, 
 
 cudaError_t launch_attention(const PromptAttention& p, const DeviceInfo& dev, cudaStream_t s, std::string* why)
 {
-    (void)dev;
     unsigned int* err = nullptr;
     cudaError_t e = device_error_ptr(&err);
     if (e != cudaSuccess)
         return e;
     if (p.dim == 64)
-        return p.f16 ? launch<Fp16, 64>(p, err, s, why) : launch<Bf16, 64>(p, err, s, why);
-    return p.f16 ? launch<Fp16, 128>(p, err, s, why) : launch<Bf16, 128>(p, err, s, why);
+        return p.f16 ? launch<Fp16, 64>(p, dev, err, s, why) : launch<Bf16, 64>(p, dev, err, s, why);
+    return p.f16 ? launch<Fp16, 128>(p, dev, err, s, why) : launch<Bf16, 128>(p, dev, err, s, why);
 }
 
 }  // namespace ck

@@ -70,46 +70,32 @@ __host__ __device__ inline VisibleKeys visible_keys(int end, int64_t window, int
     return r;
 }
 
-// One query row by one warp: online softmax over `n` keys, 32 at a time.  `qs` holds the
-// query in fp32 (DIM values of shared memory), times the softmax scale and log2 e.  row(v)
-// gives key number v's rows; only visible keys are ever read, so nothing that a mask hides
-// can reach the result.  Lane l leaves with acc[i] = sum_j 2^(s_j - m) v_j[l + 32 i], the
+// One query row by one warp: online softmax over its visible keys, 32 at a time.  No other key
+// or value is ever read, so nothing that a mask hides can reach the result.  `factor` is the
+// softmax scale times log2 e.  Lane l leaves with acc[i] = sum_j 2^(s_j - m) v_j[l + 32 i], the
 // maximum m of the scores s (in units of log2) and the sum l of the weights.
-struct KvRow {
-    const void* k;
-    const void* v;
-    float ks, vs;  // int8 codes: the rows' scales
-};
-
-template <class E, bool INT8>
-__device__ __forceinline__ float kv_element(const void* row, int d)
+template <class E, int DIM>
+__device__ __forceinline__ void attend_row(const typename E::T* q, float factor, const VisibleKeys& keys,
+                                           const typename E::T* k, int64_t k_stride, const typename E::T* v,
+                                           int64_t v_stride, float (&acc)[DIM / 32], float& m, float& l)
 {
-    if (INT8)
-        return (float)static_cast<const int8_t*>(row)[d];
-    return E::to(static_cast<const typename E::T*>(row)[d]);
-}
-
-template <class E, bool INT8, int DIM, class RowFn>
-__device__ __forceinline__ void attend_row(const float* qs, int n, RowFn row, float (&acc)[(DIM + 31) / 32], float& m,
-                                           float& l)
-{
-    constexpr int PER = (DIM + 31) / 32;
     const int lane = threadIdx.x & 31;
+    const int n = keys.count();
     m = -INFINITY;
     l = 0.0f;
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
+    for (int i = 0; i < DIM / 32; ++i)
         acc[i] = 0.0f;
     for (int v0 = 0; v0 < n; v0 += 32) {
         const bool mine = v0 + lane < n;
-        KvRow r{};
+        const int64_t key = mine ? keys.key(v0 + lane) : 0;
         float s = -INFINITY;
         if (mine) {
-            r = row(v0 + lane);
             float dot = 0.0f;
+#pragma unroll 4
             for (int d = 0; d < DIM; ++d)
-                dot = fmaf(qs[d], kv_element<E, INT8>(r.k, d), dot);
-            s = INT8 ? dot * r.ks : dot;
+                dot = fmaf(E::to(q[d]), E::to(k[key * k_stride + d]), dot);
+            s = dot * factor;
         }
         float top = s;
 #pragma unroll
@@ -122,18 +108,15 @@ __device__ __forceinline__ void attend_row(const float* qs, int n, RowFn row, fl
         l = l * keep + p;
         m = m2;
 #pragma unroll
-        for (int i = 0; i < PER; ++i)
+        for (int i = 0; i < DIM / 32; ++i)
             acc[i] *= keep;
         const int cnt = min(32, n - v0);
         for (int j = 0; j < cnt; ++j) {
             const float pj = __shfl_sync(0xffffffffu, p, j);
-            const void* vr = reinterpret_cast<const void*>(
-                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(r.v), j));
-            const float w = INT8 ? pj * __shfl_sync(0xffffffffu, r.vs, j) : pj;
+            const typename E::T* row = v + __shfl_sync(0xffffffffu, key, j) * v_stride;
 #pragma unroll
-            for (int i = 0; i < PER; ++i)
-                if (lane + 32 * i < DIM)
-                    acc[i] = fmaf(w, kv_element<E, INT8>(vr, lane + 32 * i), acc[i]);
+            for (int i = 0; i < DIM / 32; ++i)
+                acc[i] = fmaf(pj, E::to(row[lane + 32 * i]), acc[i]);
         }
     }
 #pragma unroll
