@@ -1,9 +1,12 @@
-"""Build the CUDA library libck_int8.so in-tree, for sm_103a only.
+"""Build the CUDA library libck_int8.so in-tree, for sm_103a only, and the compiled part of
+its Python binding.
 
 Each .cu file is compiled by its own nvcc process (in parallel), then the objects are
 linked into one shared library with the CUDA runtime linked statically, so the
 library has no dependency beyond the driver.  The result lives next to this file
-(``lib/libck_int8.so``); the Python binding loads it from there.
+(``lib/libck_int8.so``); the Python binding loads it from there.  ``lib/_ck_binding.so``
+(csrc/binding.cpp, compiled against the installed torch by the host compiler) hands tensors
+to the operators around the linear layers.
 """
 import concurrent.futures as cf
 import os
@@ -18,6 +21,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OBJ_DIR = os.path.join(HERE, "_build")
 LIB_DIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIB_DIR, "libck_int8.so")
+BINDING = os.path.join(LIB_DIR, "_ck_binding.so")
 
 SOURCES = ["api.cu", "quantize.cu", "gemm.cu", "api_transformer.cu", "norm_rope.cu", "paged_attention.cu",
            "attention.cu", "int4.cu"]
@@ -36,7 +40,7 @@ def nvcc():
 
 
 def _inputs_mtime():
-    files = [os.path.join(CSRC, s) for s in SOURCES + HEADERS] + [os.path.join(INCLUDE, "ck_int8.h"), __file__]
+    files = [os.path.join(CSRC, s) for s in SOURCES + HEADERS + ["binding.cpp"]] + [os.path.join(INCLUDE, "ck_int8.h"), __file__]
     return max(os.path.getmtime(f) for f in files)
 
 
@@ -51,14 +55,37 @@ def _compile(src, verbose):
     return obj, r.stderr
 
 
+def _compile_binding():
+    """binding.cpp -> lib/_ck_binding.so, against the torch that will load it."""
+    import sysconfig
+
+    import torch
+    top = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    tmp = BINDING + ".tmp%d" % os.getpid()
+    cmd = [os.environ.get("CXX") or shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI), "-I", INCLUDE,
+           "-isystem", os.path.join(top, "include"), "-isystem", os.path.join(top, "include", "torch", "csrc", "api", "include"),
+           "-isystem", cuda, "-isystem", "/usr/local/cuda/include", "-I", sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L", os.path.join(top, "lib"), "-ltorch_python", "-ltorch",
+           "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath," + os.path.join(top, "lib")]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("%s failed for binding.cpp:\n%s\n%s" % (cmd[0], r.stdout, r.stderr))
+    os.replace(tmp, BINDING)
+
+
 def build(force=False, verbose=False):
     """Compile if any source is newer than the library; return the library path."""
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _inputs_mtime():
+    newest = _inputs_mtime()
+    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= newest for f in (LIB, BINDING)):
         return LIB
     os.makedirs(OBJ_DIR, exist_ok=True)
     os.makedirs(LIB_DIR, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(_compile_binding)
         results = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
+        binding.result()
     if verbose:
         for _, log in results:
             sys.stderr.write(log)

@@ -1,0 +1,79 @@
+"""The compiled binding's checks on CUDA tensors: types, shapes, strides and devices come back as
+Python errors, the library's refusals as CkError, and given outputs are the ones returned."""
+import pytest
+import torch
+
+import int8_weight_quantized_gb300 as ck
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+
+
+def t(*shape, dtype=BF):
+    return torch.zeros(shape, dtype=dtype, device="cuda")
+
+
+def i32(*shape):
+    return t(*shape, dtype=torch.int32)
+
+
+@pytest.mark.parametrize("call,error", [
+    (lambda: ck.ck_attention(t(4, 2, 64), t(4, 1, 64, dtype=torch.float16), t(4, 1, 64), i32(2)), TypeError),
+    (lambda: ck.ck_attention(t(4, 2, 64), t(4, 1, 64), t(5, 1, 64), i32(2)), ValueError),
+    (lambda: ck.ck_attention(t(4, 2, 64), t(4, 1, 64), t(4, 1, 64), i32(2).long()), TypeError),
+    (lambda: ck.ck_attention(t(4, 2, 64), t(4, 1, 64), t(4, 1, 64), i32(2), i32(3)), ValueError),
+    (lambda: ck.ck_attention(t(64, 2, 4).transpose(0, 2), t(4, 1, 64), t(4, 1, 64), i32(2)), ValueError),
+    (lambda: ck.ck_attention(t(4, 2, 64), t(4, 1, 64), t(4, 1, 64), i32(2), out=t(4, 2, 32)), ValueError),
+    (lambda: ck.ck_attention(t(4, 2, 64), t(4, 1, 64), t(4, 1, 64), i32(2), scale="x"), TypeError),
+    (lambda: ck.ck_attention(t(4, 2, 96), t(4, 1, 96), t(4, 1, 96), i32(2)), ck.CkError),
+    (lambda: ck.ck_attention(t(4, 3, 64), t(4, 2, 64), t(4, 2, 64), i32(2)), ck.CkError),
+    (lambda: ck.ck_paged_attention(t(2, 2, 64), ck.KVCache(t(3, 1, 8, 64), t(3, 1, 8, 32)), i32(2, 1), i32(2)), ValueError),
+    (lambda: ck.ck_paged_attention(t(2, 2, 64), ck.KVCache(t(3, 1, 8, 128), t(3, 1, 8, 128)), i32(2, 1), i32(2)), ValueError),
+    (lambda: ck.ck_paged_attention(t(2, 2, 64), ck.KVCache(*[t(3, 1, 8, 64, dtype=torch.int8)] * 2), i32(2, 1), i32(2)),
+     ValueError),
+    (lambda: ck.ck_paged_attention(t(2, 2, 64), ck.KVCache(*[t(3, 1, 8, 64, dtype=torch.float16)] * 2), i32(2, 1), i32(2)),
+     ck.CkError),
+    (lambda: ck.ck_paged_attention(t(2, 2, 64), ck.KVCache(t(3, 1, 8, 64), t(3, 1, 8, 64)), i32(3, 1), i32(2)), ValueError),
+    (lambda: ck.ck_paged_attention(t(2, 2, 64), ck.KVCache(t(3, 1, 8, 64), t(3, 1, 8, 64)), i32(2, 100), i32(2),
+                                   ws=t(16, dtype=torch.uint8)), ck.CkError),
+    (lambda: ck.ck_qk_norm_rope(t(3, 256), None, None, 3, 0), ValueError),
+    (lambda: ck.ck_qk_norm_rope(t(3, 250), None, None, 2, 1), ValueError),
+    (lambda: ck.ck_qk_norm_rope(t(256, 3).t(), None, None, 2, 1), ValueError),
+    (lambda: ck.ck_qk_norm_rope(t(3, 256), i32(2), t(9, 64, dtype=torch.float32), 2, 1), ValueError),
+    (lambda: ck.ck_qk_norm_rope(t(3, 256), i32(3), t(9, 24, dtype=torch.float32), 2, 1), ck.CkError),
+    (lambda: ck.ck_qk_norm_rope(t(3, 256), None, None, 2, 1, q_weight=t(32)), ValueError),
+    (lambda: ck.ck_qk_norm_rope(t(3, 256), None, None, 2, 1, cache=ck.KVCache(t(3, 1, 8, 64), t(3, 1, 8, 64)),
+                                slots=i32(3)), TypeError),
+    (lambda: ck.ck_int4_linear(t(2, 256), i32(16, 31), t(16, 2)), ValueError),
+    (lambda: ck.ck_int4_linear(t(2, 256), i32(16, 32), t(16, 3)), ValueError),
+    (lambda: ck.ck_int4_linear(t(2, 256), i32(12, 32), t(12, 2)), ck.CkError),
+    (lambda: ck.ck_int4_linear(t(2, 256), i32(16, 32), t(16, 2), bias=t(16, dtype=torch.float32)), TypeError),
+    (lambda: ck.ck_int4_linear(t(2, 256), i32(16, 32), t(16, 2), out_dtype=torch.int32), ValueError),
+    (lambda: ck.ck_int4_linear(t(2, 512)[:, ::2], i32(16, 32), t(16, 2)), ValueError),
+])
+def test_refusals(call, error):
+    with pytest.raises(error):
+        call()
+    torch.cuda.synchronize()
+    assert ck.ck_device_error() == 0
+
+
+def test_given_outputs_are_returned():
+    q, k, v, cu = t(4, 2, 64), t(4, 1, 64), t(4, 1, 64), torch.tensor([0, 4], dtype=torch.int32, device="cuda")
+    out, lse = t(4, 2, 64), t(2, 4, dtype=torch.float32)
+    a, b = ck.ck_attention(q, k, v, cu, out=out, lse=lse, return_lse=True)
+    assert a is out and b is lse
+    y = t(2, 16, dtype=torch.float32)
+    assert ck.ck_int4_linear(t(2, 256), i32(16, 32), t(16, 2), y=y, out_dtype=torch.float32) is y
+    qo, ko = t(3, 2, 64), t(3, 1, 64)
+    r = ck.ck_qk_norm_rope(t(3, 256), None, None, 2, 1, q=qo, k=ko)
+    assert r[0] is qo and r[1] is ko
+
+
+def test_empty_batches():
+    assert ck.ck_attention(t(0, 2, 64), t(0, 1, 64), t(0, 1, 64), i32(1)).shape == (0, 2, 64)
+    cache = ck.KVCache(t(3, 1, 8, 64), t(3, 1, 8, 64))
+    assert ck.ck_paged_attention(t(0, 2, 64), cache, i32(0, 1), i32(0)).shape == (0, 2, 64)
+    q, k = ck.ck_qk_norm_rope(t(0, 256), None, None, 2, 1)
+    assert q.shape == (0, 2, 64) and k.shape == (0, 1, 64)
+    assert ck.ck_int4_linear(t(0, 256), i32(16, 32), t(16, 2)).shape == (0, 16)

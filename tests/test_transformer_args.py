@@ -1,12 +1,12 @@
 """The operators around the linear layers reject bad arguments before any device work, through
 the C ABI (with pointers that are never dereferenced) and through the binding."""
 import ctypes
+import struct
 
 import pytest
 import torch
 
 import int8_weight_quantized_gb300 as ck
-from int8_weight_quantized_gb300 import transformer
 
 P = ctypes.c_void_p(4096)
 ODD = ctypes.c_void_p(4097)
@@ -22,7 +22,7 @@ def lib():
 def cache(**kw):
     f = dict(k=4096, v=4096, k_scale=4096, v_scale=4096, num_pages=4, page_size=16, kv_heads=2, head_dim=64, dtype=0)
     f.update(kw)
-    return transformer._CACHE.pack(*[f[n] for n in ("k", "v", "k_scale", "v_scale", "num_pages", "page_size", "kv_heads",
+    return struct.pack("@PPPPqqqqi", *[f[n] for n in ("k", "v", "k_scale", "v_scale", "num_pages", "page_size", "kv_heads",
                                                     "head_dim", "dtype")])
 
 
@@ -145,7 +145,7 @@ def test_workspace_sizes(lib):
     assert 0 < lib.ck_paged_attention_workspace_size(1 << 20, 8, 2, 128, 1 << 20) < 1 << 28
 
 
-def test_binding_checks():
+def test_binding_checks(lib):
     x = torch.zeros((4, 256), dtype=torch.bfloat16)
     with pytest.raises(TypeError):
         ck.ck_qk_norm_rope(x.float(), None, None, 2, 1)
@@ -155,6 +155,9 @@ def test_binding_checks():
         ck.KVCache(torch.zeros((2, 1, 4, 64)), torch.zeros((2, 1, 4, 64)))
     with pytest.raises(ValueError):
         ck.KVCache(torch.zeros((2, 4, 64), dtype=torch.int8), torch.zeros((2, 4, 64), dtype=torch.int8))
+    cache = ck.KVCache(*[torch.zeros((2, 1, 4, 64), dtype=torch.int8)] * 2)
+    with pytest.raises(ValueError):  # not CUDA tensors
+        ck.ck_paged_attention(x.view(4, 4, 64), cache, None, None)
     with pytest.raises(TypeError):
         ck.ck_int4_linear(x.float(), None, None)
     with pytest.raises(TypeError):
