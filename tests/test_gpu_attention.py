@@ -201,3 +201,36 @@ def test_other_streams_and_graphs():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, ck.ck_attention(q, k, v, cq))
+
+
+@pytest.mark.parametrize("hq,hkv", [(3, 1), (4, 1), (10, 2)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (200, 3)])
+def test_many_more_tiles_than_multiprocessors(hq, hkv, d, window, sinks):
+    """Blocks go from item to item, with odd and even numbers of heads to a key head; empty and
+    one-token sequences stand between long ones."""
+    lens = [1500, 0, 1, 2049, 128, 0, 1281, 3, 256, 257] * 2
+    q, k, v, cq, cku = make(lens, lens, hq, hkv, d, torch.bfloat16, seed=hq + d)
+    out, lse = ck.ck_attention(q, k, v, cq, window=window, sinks=sinks, return_lse=True)
+    check(q, k, v, cq, cku, out, lse, True, window, sinks, heads=(0, hq - 1))
+    # the other heads: as the same head computed alone
+    for h in range(1, hq - 1):
+        kv = h // (hq // hkv)
+        one = ck.ck_attention(q[:, h:h + 1], k[:, kv:kv + 1], v[:, kv:kv + 1], cq, window=window, sinks=sinks)
+        ref.assert_within(out[:, h:h + 1], one, 4 * ref.unit(torch.bfloat16) * (one.abs().double() + 1), "head")
+    assert ck.ck_device_error() == 0
+
+
+@pytest.mark.parametrize("hq", [3, 4])
+def test_hidden_infinities_with_shared_heads(hq):
+    """What the last tests ask, with more heads to a key head: each head's rows stand alone."""
+    q, k, v, cq, cku = make([300, 140], [300, 140], hq, 1, 64, torch.bfloat16, seed=hq)
+    want = ck.ck_attention(q, k, v, cq)
+    v = v.clone()
+    v[220] = float("inf")
+    v[300 + 100] = float("nan")
+    out = ck.ck_attention(q, k, v, cq)
+    hidden = torch.ones(440, dtype=torch.bool, device=DEV)
+    hidden[220:300] = hidden[400:440] = False
+    ref.assert_within(out[hidden], want[hidden], 4 * ref.unit(torch.bfloat16) * (want[hidden].abs().double() + 1), "rows")
+    assert not out[~hidden].isfinite().any()
