@@ -35,10 +35,25 @@ __device__ __forceinline__ int code_shift(int e)
 // are idle, which costs nothing while HBM sets the pace, and up to 8 rows cost the same.  The
 // codes are exact in bf16 and fp16 (nibble in the mantissa of 128 or 1024, minus that and 8),
 // the products exact in fp32; a group's sum is scaled once, in fp32.
+//
+// Measured (GB300): one row, 28672 x 5376, groups of 128: 20.8 to 22.9 us, 3.5 to 3.8 TB/s, 52 to
+// 57% of a copy's bandwidth, the ALU (shift and mask of each nibble pair) busy in 57% of the
+// cycles, an instruction issued in 64%; one row, 4096 x 4096: 4.5 us (launch and latency); 16
+// rows, 16384 x 4096, groups of 64: 15.1 us, 2.4 TB/s, waiting on the ring and on x; 32 rows,
+// groups of 128: 23.2 us.
 constexpr int WARPS = 8;
 constexpr int CHUNK = 128;                 // k of a ring unit
 constexpr int STAGES = 4;
 constexpr int W_LD = 80;                   // bytes of a unit's weight row: 64, padded so that 8 rows spread over the banks
+
+// Blocks per SM that the compiler shares the registers out for (0: as it likes, which makes four).
+// 32 rows of x need more than the 128 that two blocks leave (spilled: 32.9 us at 16384 x 4096, 23.3
+// without); 16 rows do not, and two blocks hide more of their waits (18.6 us with one, 15.1 with
+// two); one row at 16384 x 4096 took 13.2 us bound to four and 11.9 to two, 10.8 unbound.
+template <int MT>
+constexpr int kMinBlocks = MT == 4 ? 1 : MT == 2 ? 2 : 0;
+template <int MT>
+constexpr int kResident = MT == 4 ? 1 : MT == 2 ? 2 : 4;
 
 // (w & MASK) | bits in one instruction (with both as constants the compiler made two of it)
 template <uint32_t MASK>
@@ -74,7 +89,7 @@ constexpr int kUnit = 16 * RT * (W_LD + 8);  // codes, then 8 bytes of scales a 
 
 // PER_CHUNK: scales of a row in a chunk (4, 2 or 1 for groups of 32, 64, and 128 or 256)
 template <class E, int RT, int MT, int PER_CHUNK, int KW>
-__global__ void __launch_bounds__(WARPS * 32) int4_kernel(const Int4Linear p)
+__global__ void __launch_bounds__(WARPS * 32, kMinBlocks<MT>) int4_kernel(const Int4Linear p)
 {
     using T = typename E::T;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -331,17 +346,23 @@ cudaError_t by_group(const Int4Linear& p, cudaStream_t s)
 }
 
 // KW: long runs of K per warp spread its set-up over more work and let a block's row groups share
-// their reads of x in L1; short ones give a narrow layer enough warps.  The fewest warps per row
-// group that still make two blocks per SM, or one where there is more than one tile of rows of x
-// (16 rows, 16384 x 4096: 17.9 us with two blocks per SM, 15.1 with one; 8 rows: 14.2 and 15.0).
+// their reads of x in L1; short ones give a narrow layer enough warps and fill the last round of
+// blocks better.  Rounds of blocks times (chunks of a run + 3 for what a block costs besides), at
+// its least: KW = 2, 4, 8 took, in us, for 32 rows at 16384 x 4096 23.3, 24.7, 28.3, at 28672 x 5376
+// 53.6, 45.0, 55.0, at 4096 x 16384 80.8, 40.9, 22.1; for 16 rows at 16384 x 4096 18.5, 15.2, 17.9.
 template <class E, int RT, int MT>
 cudaError_t by_split(const Int4Linear& p, const DeviceInfo& dev, cudaStream_t s)
 {
-    const int64_t blocks1 = (p.N + 16 * RT * WARPS - 1) / (16 * RT * WARPS);  // at KW = 1
-    const int64_t want = (MT == 1 ? 2 : 1) * dev.sm_count;
-    if (blocks1 * 2 >= want)
+    const int64_t chunks = p.K / CHUNK, slots = (int64_t)dev.sm_count * kResident<MT>;
+    auto cost = [&](int kw) {
+        const int64_t rows = 16 * RT * WARPS / kw;
+        const int64_t blocks = (p.N + rows - 1) / rows * ((p.M + 8 * MT - 1) / (8 * MT));
+        return (blocks + slots - 1) / slots * (chunks + 3 * kw) * (8 / kw);
+    };
+    const int64_t c2 = cost(2), c4 = cost(4), c8 = cost(8);
+    if (c2 <= c4 && c2 <= c8)
         return by_group<E, RT, MT, 2>(p, s);
-    if (blocks1 * 4 >= want)
+    if (c4 <= c8)
         return by_group<E, RT, MT, 4>(p, s);
     return by_group<E, RT, MT, 8>(p, s);
 }
