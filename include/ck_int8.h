@@ -280,7 +280,7 @@ typedef enum {
  * page T[t / page_size], offset t % page_size.  Slot numbers are page * page_size + offset. */
 typedef struct {
     void *k, *v;             /* [num_pages, kv_heads, page_size, head_dim] of dtype        */
-    float *k_scale, *v_scale;/* fp32 [num_pages, kv_heads, page_size]; CK_KV_INT8 only      */
+    float *k_scale, *v_scale;/* fp32 [num_pages, kv_heads, page_size], >= 0; CK_KV_INT8 only */
     int64_t num_pages;
     int64_t page_size;       /* any size >= 1                                             */
     int64_t kv_heads;

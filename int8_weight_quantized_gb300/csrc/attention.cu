@@ -26,6 +26,14 @@
 // While the softmax of one tile runs, the products of the other keep the tensor cores busy:
 // the issue order is O_0 += P_0 V_j, S_0 = Q_0 K_{j+1}, O_1 += P_1 V_j, S_1 = Q_1 K_{j+1}.
 //
+// Measured (GB300; 16 query heads on 4 of 128 values, bf16): 16384 causal tokens 715 to 735 us,
+// 1500 to 1540 TFLOP/s, 77% of cuBLAS's measured rate; 8192 not causal 390 us, 1409; window of 1024
+// with 4 first tokens over 16000 (2 key heads) 148 us; heads of 64, 8192 causal 163 us.  A step (a
+// key tile against both query tiles) takes some 3100 cycles, of which the 32 products of the two
+// tiles take 2250: the chain of one tile (score product, softmax 1300, value product, and three
+// hand-overs of 300 to 400) is what it lasts.  Between two items, 6000 to 7000 cycles pass in the
+// output and the next tile's first, masked softmax: a sixth of an item with that window.
+//
 // Online softmax that seldom waits for its maximum: a row's weights of a tile are taken
 // relative to the reference m that its sums have, while the tile's maximum is found beside
 // them.  A maximum more than 2^8 above m makes the row's thread bring m, the sum and O (in
