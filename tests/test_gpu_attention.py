@@ -234,3 +234,27 @@ def test_hidden_infinities_with_shared_heads(hq):
     hidden[220:300] = hidden[400:440] = False
     ref.assert_within(out[hidden], want[hidden], 4 * ref.unit(torch.bfloat16) * (want[hidden].abs().double() + 1), "rows")
     assert not out[~hidden].isfinite().any()
+
+
+@pytest.mark.parametrize("hq", [2, 3])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("sinks", [1, 31, 32, 33, 128, 160])
+def test_numbers_of_first_tokens(sinks, d, hq):
+    """A few first tokens are a narrow key tile, more of them whole tiles."""
+    lens = [700, 33, 520]
+    q, k, v, cq, cku = make(lens, lens, hq, 1, d, torch.float16, seed=sinks)
+    out, lse = ck.ck_attention(q, k, v, cq, window=90, sinks=sinks, return_lse=True)
+    check(q, k, v, cq, cku, out, lse, True, 90, sinks)
+
+
+@pytest.mark.parametrize("row", [0, 3, 4, 31, 32, 127])
+def test_first_tokens_beside_hidden_rows(row):
+    """NaN in a row of the first key tile: only the queries that see it change."""
+    q, k, v, cq, cku = make([600], [600], 2, 1, 64, torch.bfloat16, seed=row)
+    clean = ck.ck_attention(q, k, v, cq, window=100, sinks=4)
+    k, v = k.clone(), v.clone()
+    k[row] = v[row] = float("nan")
+    out = ck.ck_attention(q, k, v, cq, window=100, sinks=4)
+    sees = seen_by(600, 600, True, 100, 4)[:, row]
+    assert out[sees].isnan().all()
+    ref.assert_within(out[~sees], clean[~sees], 4 * ref.unit(torch.bfloat16) * (clean[~sees].abs().double() + 1), "rows")
