@@ -68,7 +68,7 @@ def _compile_binding():
            "-isystem", os.path.join(top, "include"), "-isystem", os.path.join(top, "include", "torch", "csrc", "api", "include"),
            "-isystem", cuda, "-isystem", "/usr/local/cuda/include", "-I", sysconfig.get_paths()["include"],
            os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L", os.path.join(top, "lib"), "-ltorch_python", "-ltorch",
-           "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath," + os.path.join(top, "lib")]
+           "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath," + os.path.join(top, "lib")]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("%s failed for binding.cpp:\n%s\n%s" % (cmd[0], r.stdout, r.stderr))

@@ -8,6 +8,7 @@
 #include <string>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -143,7 +144,8 @@ bool truth(PyObject* o)
 
 at::Tensor empty(c10::IntArrayRef shape, at::ScalarType type, const at::Tensor& like)
 {
-    return at::empty(shape, like.options().dtype(type));
+    // what at::empty comes to for a CUDA tensor, without the dispatcher's way there
+    return at::detail::empty_cuda(shape, type, like.device(), c10::nullopt);
 }
 
 void* ptr(const at::Tensor* t)
