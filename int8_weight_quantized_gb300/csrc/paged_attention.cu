@@ -73,7 +73,12 @@ struct Shape {
     static constexpr int STAGES = (BLOCKS == 3 ? 16384 : 24576) / (UNIT - SCALES);
     static constexpr int LD = DIM + 4;                       // joined sums: floats per head
     static constexpr size_t RING = (size_t)WARPS * STAGES * UNIT;
-    static constexpr size_t SMEM = RING + HEADS * LD * 4 + WARPS * HEADS * 8;
+    // Sums that the warps join theirs in: two, where that leaves room for BLOCKS blocks on an SM.
+    // (One segment of 274 tokens 7.5 us with one and 7.0 with two, 32 of 1025 to 16384 tokens in int8
+    // rows 106.6 and 102.3; 16 heads to an int8 head, whose second block went: 16.5 and 18.6.)
+    static constexpr size_t sums_bytes(int slabs) { return slabs * HEADS * LD * 4 + WARPS * HEADS * 8; }
+    static constexpr int SLABS = RING + sums_bytes(2) <= 233472 / BLOCKS - 1024 ? 2 : 1;
+    static constexpr size_t SMEM = RING + sums_bytes(SLABS);
     static constexpr size_t PART = (size_t)HEADS * (DIM + 2);  // floats of one partial
 };
 
@@ -248,8 +253,8 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
     }
 
     const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * S::STAGES * S::UNIT);
-    float* joined = reinterpret_cast<float*>(smem + S::RING);         // [HEADS][LD]
-    float2* maxsum = reinterpret_cast<float2*>(joined + HEADS * S::LD);  // [WARPS][HEADS]
+    float* joined = reinterpret_cast<float*>(smem + S::RING);             // [SLABS][HEADS][LD]
+    float2* maxsum = reinterpret_cast<float2*>(joined + S::SLABS * HEADS * S::LD);  // [WARPS][HEADS]
 
     // ---- copies: lane l looks up the row of key l % KEYS of the warp's unit one unit ahead
     constexpr int CH = S::ROW / 16;       // 16-byte chunks of a row
@@ -391,7 +396,7 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
             const uint32_t ks = ring + stage * S::UNIT;
             const uint32_t vs = ks + KEYS * S::ROW;
             // S^T: rows keys 16 kt + g, + 8; columns heads 2t, 2t + 1 of each nt
-            float s[NT][KT][4];
+            float s[NT][KT][4], s_odd[NT][4] = {};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -400,14 +405,20 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt) {
                 if (!INT8) {
+                    // two sums: half the wait of a chain of products
 #pragma unroll
                     for (int kk = 0; kk < DIM / 16; ++kk) {
                         uint32_t ka[4];
                         ldmatrix_x4(ka, ks + chunk_at<INT8, DIM, false>(16 * kt + (lane & 15), 2 * kk + (lane >> 4)));
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
-                            mma_16816<M>(s[nt][kt], ka, qb[nt][kk][0], qb[nt][kk][1]);
+                            mma_16816<M>(kk & 1 ? s_odd[nt] : s[nt][kt], ka, qb[nt][kk][0], qb[nt][kk][1]);
                     }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            s[nt][kt][i] += s_odd[nt][i], s_odd[nt][i] = 0.0f;
                 } else {
 #pragma unroll
                     for (int hf = 0; hf < DIM / 64; ++hf) {
@@ -464,41 +475,46 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float w[KT][4];  // weights for the values' product
+                float a[2][KT][2], top[2], keep[2];  // a: scores in units of log2; keys past the end out
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    float a[KT][2];  // scores in units of log2; keys past the end out
-                    float top = -INFINITY;
+                    top[j] = -INFINITY;
 #pragma unroll
                     for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const float x = s[nt][kt][2 * h + j] * c_head[nt][j];
-                            a[kt][h] = v0 + 16 * kt + g + 8 * h < n ? (INT8 ? x * kscale[kt][h] : x) : -INFINITY;
-                            top = fmaxf(top, a[kt][h]);
+                            a[j][kt][h] = v0 + 16 * kt + g + 8 * h < n ? (INT8 ? x * kscale[kt][h] : x) : -INFINITY;
+                            top[j] = fmaxf(top[j], a[j][kt][h]);
                         }
+                }
 #pragma unroll
-                    for (int x = 4; x <= 16; x <<= 1)
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-                    const float m2 = fmaxf(m[nt][j], top);
+                for (int x = 4; x <= 16; x <<= 1) {
+                    const float t0 = __shfl_xor_sync(0xffffffffu, top[0], x), t1 = __shfl_xor_sync(0xffffffffu, top[1], x);
+                    top[0] = fmaxf(top[0], t0), top[1] = fmaxf(top[1], t1);
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float m2 = fmaxf(m[nt][j], top[j]);
                     const float ref = m2 == -INFINITY ? 0.0f : m2;
-                    const float keep = fast_exp2(m[nt][j] - ref);
+                    keep[j] = fast_exp2(m[nt][j] - ref);
                     m[nt][j] = m2;
-                    l[nt][j] *= keep;
+                    l[nt][j] *= keep[j];
 #pragma unroll
                     for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            const float x = fast_exp2(a[kt][h] - ref);
+                            const float x = fast_exp2(a[j][kt][h] - ref);
                             l[nt][j] += x;
                             w[kt][2 * h + j] = INT8 ? x * vratio[kt][h] : x;
                         }
-                    if (__any_sync(0xffffffffu, keep != 1.0f))
-#pragma unroll
-                        for (int e = 0; e < DIM / 16; ++e) {
-                            o[nt][e][j] *= keep;
-                            o[nt][e][2 + j] *= keep;
-                        }
                 }
+                if (__any_sync(0xffffffffu, keep[0] != 1.0f || keep[1] != 1.0f))
+#pragma unroll
+                    for (int e = 0; e < DIM / 16; ++e)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            o[nt][e][i] *= keep[i & 1];
 #pragma unroll
                 for (int kt = 0; kt < KT; ++kt) {
                     pb[nt][kt][0] = transpose_8x8(M::pack2(w[kt][0], w[kt][1]));
@@ -584,8 +600,9 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
                         top = fmaxf(top, maxsum[w * HEADS + 8 * nt + 2 * t + j].x);
                     f[nt][j] = m[nt][j] == -INFINITY ? 0.0f : fast_exp2(m[nt][j] - top) * (INT8 ? vmax : 1.0f);
                 }
-            for (int w = 0; w < WARPS; ++w) {
-                if (warp == w)
+            // SLABS warps at a time, each in sums of its own
+            for (int w = 0; w < WARPS; w += S::SLABS) {
+                if (warp / S::SLABS * S::SLABS == w)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -593,7 +610,7 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 const int d = INT8 ? DIM / 8 * g + 2 * e + (i >> 1) : 16 * e + g + 8 * (i >> 1);
-                                float* dst = joined + (8 * nt + 2 * t + (i & 1)) * S::LD + d;
+                                float* dst = joined + (warp % S::SLABS * HEADS + 8 * nt + 2 * t + (i & 1)) * S::LD + d;
                                 const float x = o[nt][e][i] * f[nt][i & 1];
                                 *dst = w == 0 ? x : *dst + x;
                             }
@@ -603,7 +620,11 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
             float* part = static_cast<float*>(p.workspace) + (2 * (int64_t)blockIdx.x + piece) * S::PART;
             for (int i = threadIdx.x; i < heads * (DIM / 4); i += WARPS * 32) {
                 const int row = i / (DIM / 4), d = i % (DIM / 4) * 4;
-                const float4 x = *reinterpret_cast<const float4*>(joined + row * S::LD + d);
+                float4 x = *reinterpret_cast<const float4*>(joined + row * S::LD + d);
+                if (S::SLABS == 2) {
+                    const float4 y = *reinterpret_cast<const float4*>(joined + (HEADS + row) * S::LD + d);
+                    x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+                }
                 if (!whole) {
                     *reinterpret_cast<float4*>(part + row * DIM + d) = x;
                     continue;
