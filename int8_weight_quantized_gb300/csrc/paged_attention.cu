@@ -33,8 +33,8 @@
 //
 // Measured (GB300; 32 query heads on 8 of 128 values): 64 sequences of 0 to 8192 tokens in 16-bit
 // rows 174 us, 6.2 TB/s, 93% of a copy's bandwidth; one of 131071 tokens 90 us, 90%; 32 sequences
-// of 1025 to 16384 tokens in int8 rows 106 us, 83%; one of 274 tokens 7.1 us (two products, a few
-// tiles per warp: latency).  int8 rows are bound by instructions: each code is widened for the
+// of 1025 to 16384 tokens in int8 rows 101 us, 87%; one of 274 tokens 6.6 us, of 64 tokens 3.6 (two
+// products, a few tiles per warp: latency).  int8 rows are bound by instructions: each code is widened for the
 // matrix instruction, which has no int8 by 16-bit form.
 //
 // Rounding to fewer bits: each weight once, to the type of the values' product (bf16 or
@@ -53,7 +53,9 @@ namespace ck {
 namespace {
 
 constexpr int WARPS = 4;
-constexpr int kWholeKeys = 512;       // segments of at most this many keys are not split
+// Segments of at most this many keys are not split: 64 sequences of 1 to 500 tokens 19.4 us, split
+// 31.5 (a block pays about 1 us for each segment that it takes up, and the sums have to be joined).
+constexpr int kWholeKeys = 512;
 
 // NT: tiles of 8 query heads that a segment holds (1, or 2 where a group has more than 8)
 template <bool INT8, int DIM, int NT>
