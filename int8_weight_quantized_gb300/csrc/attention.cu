@@ -38,13 +38,13 @@
 // hand-overs of 300 to 400) is what it lasts.  Between two items, 6000 to 7000 cycles pass in the
 // output and the next tile's first, masked softmax: a sixth of an item with that window.
 //
-// Online softmax that seldom waits for its maximum: a row's weights of a tile are taken
-// relative to the reference m that its sums have, while the tile's maximum is found beside
-// them.  A maximum more than 2^8 above m makes the row's thread bring m, the sum and O (in
-// tensor memory) up to it before the next tile; one so far above that a weight would leave its
-// type or the sums (2^64, for fp16 2^15) sends the tile through again at once.  m only scales
-// sums in floating point, so how far it trails costs no precision.  S_{j+1} being complete
-// means that O += P_j V_j is, since it was issued before.
+// Online softmax: the load of the scores from tensor memory brings their maximum along
+// (tcgen05.ld.red; found by the row's thread it took a fifth of the softmax: 703 instead of 685 us
+// for 16384 tokens, 153 instead of 133 with heads of 64).  A row's sums stay relative to a reference
+// m that may trail its maximum by up to 2^8; beyond that the thread brings m, the sum and O (in
+// tensor memory) up to it first, which is seldom.  m only scales sums in floating point, so how far
+// it trails costs no precision.  S_{j+1} being complete means that O += P_j V_j is, since it was
+// issued before.
 //
 // What a mask hides has no part in a row: hidden scores are replaced, not multiplied.  A V row
 // that some of a tile's queries see and others do not, or that lies beyond the sequence's end,
@@ -205,6 +205,21 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
         "r"(a), "l"(b), "r"(idesc), "r"(add)
         : "memory");
+}
+
+// 32 columns of the lane's row, and the largest of them (NaN left out).
+__device__ __forceinline__ void tmem_ld_max_32x32b_x32(uint32_t taddr, uint32_t (&r)[32], float& top)
+{
+    asm volatile(
+        "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, %32, [%33];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+          "=f"(top)
+        : "r"(taddr));
 }
 
 __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16])
@@ -654,8 +669,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         const uint32_t s_addr = tmem + lanes + t * BM, o_addr = tmem + lanes + 2 * BM + t * DIM;
         const float c = p.c;
-        // how far (log2) weights may exceed 1 before the tile has to be done again
-        constexpr float kHard = std::is_same<E, Bf16>::value ? 64.0f : 15.0f;
         uint32_t phase = 0, o_phase = 0;
         bool ok = true;  // once a wait has given up, the remaining rows become NaN
         each_item(std::true_type(), std::true_type(), [&](const Item& w) {
@@ -665,11 +678,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         const Active active = {w.heads(), w.begin(t), w.last(t)};
         const bool any = w.any(t);
         float m = -INFINITY;  // what the row's sums are relative to, in units of scores
-        float top = -INFINITY;
         float l = 0.0f;
         bool started = false;
         // bring the row's sums to the maximum `top`, where `raise`
-        auto raise_to_top = [&](bool raise) {
+        auto raise_to = [&](float top, bool raise) {
             const float f = raise ? fast_exp2((m - top) * c) : 1.0f;
             if (raise)
                 m = top;
@@ -696,71 +708,52 @@ __global__ void __launch_bounds__(THREADS, 1)
                 return;
             phase ^= 1u;
             tc_fence_after();
-            const bool raise = (top - m) * c > kLag;  // found in the last tile
-            if (__any_sync(0xffffffffu, raise))
-                raise_to_top(raise);
             const bool masked = w.partial(t, k0);
-            uint32_t packed[CHUNKS][16];
-            float2 sum;
-            bool first = !started;
-            for (;;) {
-                uint32_t sr[CHUNKS][32];
+            uint32_t sr[CHUNKS][32];
+            float tops[CHUNKS];
 #pragma unroll
-                for (int i = 0; i < CHUNKS; ++i)
-                    tmem_ld_32x32b_x32(s_addr + 32 * i, sr[i]);
-                tmem_wait_ld();
-                if (masked) {
-#pragma unroll
-                    for (int i = 0; i < CHUNKS; ++i) {
-                        // bit n: key k0 + 32 i + n is seen (k <= hi and (k >= lo or k < sinks))
-                        const int a = k0 + 32 * i;
-                        const int nh = hi - a + 1, nl = lo - a, ns = w.sinks - a;
-                        const uint32_t upto = nh <= 0 ? 0u : nh >= 32 ? 0xffffffffu : (1u << nh) - 1u;
-                        const uint32_t below = nl <= 0 ? 0u : nl >= 32 ? 0xffffffffu : (1u << nl) - 1u;
-                        const uint32_t head = ns <= 0 ? 0u : ns >= 32 ? 0xffffffffu : (1u << ns) - 1u;
-                        const uint32_t seen = WINDOW ? upto & (~below | head) : upto;
-#pragma unroll
-                        for (int n = 0; n < 32; ++n)
-                            sr[i][n] = (seen >> n) & 1u ? sr[i][n] : 0xff800000u;
-                    }
-                }
-                if (first) {  // the row's first tile: its own maximum
-#pragma unroll
-                    for (int i = 0; i < CHUNKS; ++i)
-#pragma unroll
-                        for (int n = 0; n < 32; ++n)
-                            m = fmaxf(m, __uint_as_float(sr[i][n]));
-                    first = false;
-                }
-                const float mc = m == -INFINITY ? 0.0f : -m * c;  // no key seen yet: weights 0
-                const float2 c2 = make_float2(c, c), mc2 = make_float2(mc, mc);
-                sum = make_float2(0.0f, 0.0f);
-                float tops[CHUNKS];
+            for (int i = 0; i < CHUNKS; ++i)
+                tmem_ld_max_32x32b_x32(s_addr + 32 * i, sr[i], tops[i]);
+            tmem_wait_ld();
+            if (masked) {
 #pragma unroll
                 for (int i = 0; i < CHUNKS; ++i) {
+                    // bit n: key k0 + 32 i + n is seen (k <= hi and (k >= lo or k < sinks))
+                    const int a = k0 + 32 * i;
+                    const int nh = hi - a + 1, nl = lo - a, ns = w.sinks - a;
+                    const uint32_t upto = nh <= 0 ? 0u : nh >= 32 ? 0xffffffffu : (1u << nh) - 1u;
+                    const uint32_t below = nl <= 0 ? 0u : nl >= 32 ? 0xffffffffu : (1u << nl) - 1u;
+                    const uint32_t head = ns <= 0 ? 0u : ns >= 32 ? 0xffffffffu : (1u << ns) - 1u;
+                    const uint32_t seen = WINDOW ? upto & (~below | head) : upto;
                     tops[i] = -INFINITY;
 #pragma unroll
-                    for (int n = 0; n < 16; ++n) {
-                        const float a = __uint_as_float(sr[i][2 * n]), b = __uint_as_float(sr[i][2 * n + 1]);
-                        float2 x = f2_fma_rn(make_float2(a, b), c2, mc2);
-                        tops[i] = fmaxf(tops[i], fmaxf(a, b));
-                        x.x = fast_exp2(x.x);
-                        x.y = fast_exp2(x.y);
-                        sum = f2_add_rn(sum, x);
-                        packed[i][n] = E::pack2(x.x, x.y);
+                    for (int n = 0; n < 32; ++n) {
+                        sr[i][n] = (seen >> n) & 1u ? sr[i][n] : 0xff800000u;
+                        tops[i] = fmaxf(tops[i], __uint_as_float(sr[i][n]));
                     }
                 }
-                if (CHUNKS == 4)
-                    top = fmaxf(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2 % CHUNKS], tops[3 % CHUNKS])), m);
-                else
-                    top = fmaxf(tops[0], m);
-                // S is still there: a weight beyond what its type and the sums hold sends the
-                // tile through again, relative to the maximum just found
-                const bool over = (top - m) * c > kHard;
-                if (!__any_sync(0xffffffffu, over))
-                    break;
-                raise_to_top(over);
             }
+            float top = fmaxf(tops[0], m);
+#pragma unroll
+            for (int i = 1; i < CHUNKS; ++i)
+                top = fmaxf(top, tops[i]);
+            const bool raise = (top - m) * c > kLag;  // (m is -inf before the first key)
+            if (__any_sync(0xffffffffu, raise))
+                raise_to(top, raise);
+            const float mc = m == -INFINITY ? 0.0f : -m * c;  // no key seen yet: weights 0
+            const float2 c2 = make_float2(c, c), mc2 = make_float2(mc, mc);
+            float2 sum = make_float2(0.0f, 0.0f);
+            uint32_t packed[CHUNKS][16];
+#pragma unroll
+            for (int i = 0; i < CHUNKS; ++i)
+#pragma unroll
+                for (int n = 0; n < 16; ++n) {
+                    float2 x = f2_fma_rn(make_float2(__uint_as_float(sr[i][2 * n]), __uint_as_float(sr[i][2 * n + 1])), c2, mc2);
+                    x.x = fast_exp2(x.x);
+                    x.y = fast_exp2(x.y);
+                    sum = f2_add_rn(sum, x);
+                    packed[i][n] = E::pack2(x.x, x.y);
+                }
             l += sum.x + sum.y;
 #pragma unroll
             for (int i = 0; i < CHUNKS; ++i)
