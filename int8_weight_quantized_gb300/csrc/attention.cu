@@ -9,9 +9,10 @@
 //
 // An item is two tiles of 128 queries: the same queries of two heads that share their keys, or,
 // where a group's heads are odd in number, 256 queries of one head.  It walks the key tiles (128
-// keys) that any of them sees, a query tile skipping those that it sees nothing of.  One block per SM takes
-// items by turns (the longest first, every second round backwards), and its roles run on from
-// item to item: the first scores of the next are computed while the last sums of one are stored.
+// keys) that any of them sees, a query tile skipping those that it sees nothing of.  One block per
+// SM takes items by turns (the longest first, every second round backwards), and its roles run on
+// from item to item: the first scores of the next are computed while the last sums of one are
+// stored.
 //   warp 0      copies by TMA: the two Q tiles, then K and V tiles through one ring;
 //   warp 1      issues the products, one lane: S_t = Q_t K^T (both operands in shared
 //               memory) and O_t += P_t V (P from tensor memory, V as it lies, keys by columns),
@@ -21,22 +22,23 @@
 //               its own);
 //   warp 3      idle (it completes the warpgroup for the register re-balancing);
 //   warps 4-11  softmax, a warpgroup for each query tile, one thread per query row: reads its
-//               row of S, takes the maximum, writes the weights back over S as the 16-bit
-//               operand P of the second product.
+//               row of S with its maximum, writes the weights back over S as the 16-bit
+//               operand P of the second product, with heads of 128 in two parts.
 // While the softmax of one tile runs, the products of the other keep the tensor cores busy:
 // the issue order is O_0 += P_0 V_j, S_0 = Q_0 K_{j+1}, O_1 += P_1 V_j, S_1 = Q_1 K_{j+1}.
 //
 // A few first tokens (up to 32 of them, before the windows) are a narrow key tile: 32 scores a row,
-// a quarter of the value product (window of 1024 with 4 first tokens over 16000: 148 us with a
-// whole tile, 140 so; six short prompts 18.7 and 16.8).
+// a quarter of the value product (before the loads brought the maximum: window of 1024 with 4 first
+// tokens over 16000 148 us with a whole tile, 140 so; six short prompts 18.7 and 16.8).
 //
-// Measured (GB300; 16 query heads on 4 of 128 values, bf16): 16384 causal tokens 715 to 735 us,
-// 1500 to 1540 TFLOP/s, 77% of cuBLAS's measured rate; 8192 not causal 391 us, 1406; window of 1024
-// with 4 first tokens over 16000 (2 key heads) 140 us; heads of 64, 8192 causal 154 us.  A step (a
-// key tile against both query tiles) takes some 3100 cycles, of which the 32 products of the two
-// tiles take 2250: the chain of one tile (score product, softmax 1300, value product, and three
-// hand-overs of 300 to 400) is what it lasts.  Between two items, 6000 to 7000 cycles pass in the
-// output and the next tile's first, masked softmax: a sixth of an item with that window.
+// Measured (GB300; 16 query heads on 4 of 128 values, bf16): 16384 causal tokens 672 to 690 us, 1590
+// to 1640 TFLOP/s, 81 to 84% of cuBLAS's measured rate; 8192 not causal 365 us, 1506; window of 1024
+// with 4 first tokens over 16000 (2 key heads) 124 us; heads of 64, 8192 causal 136 us, 1010.  A step
+// (a key tile against both query tiles) takes 1.56 us, some 2900 cycles, of which the 32 products of
+// the two tiles take 2250: what it lasts is the chain of one tile, its score product, its softmax,
+// the rest of its value product, and hand-overs of 300 to 400 cycles between them.  Between two
+// items some 5000 cycles pass in the output and the next tile's first, masked softmax: a sixth of
+// an item with that window.
 //
 // Online softmax: the load of the scores from tensor memory brings their maximum along
 // (tcgen05.ld.red; found by the row's thread it took a fifth of the softmax: 703 instead of 685 us
@@ -82,8 +84,10 @@ constexpr uint32_t TMEM_COLS = 512;
 constexpr int NARROW = 32;           // keys of a key tile of a few first tokens
 // Weights of a tile that are handed over first, so that their value product starts while the others
 // are worked out: 16384 causal tokens 672 us, 693 with all at once, 693 with 32, 673 with 96 (window
-// of 1024 over 16000: 125, 128, 126, 129).
-constexpr int FIRST_KEYS = 64;
+// of 1024 over 16000: 125, 128, 126, 129).  With heads of 64 it changes nothing (8192 causal tokens
+// 135 us) or adds a wait (six short prompts 15.7 us, 15.4 with all at once).
+template <int DIM>
+constexpr int FIRST_KEYS = DIM == 128 ? 64 : 0;
 constexpr int ITEMS = 2;              // items worked out ahead
 constexpr int ITEM_READERS = 10;      // warps 0, 1 and 4-11
 constexpr uint64_t TIMEOUT_NS = 2000000000ull;
@@ -610,14 +614,16 @@ __global__ void __launch_bounds__(THREADS, 1)
                             const bool now = active[t](j), next = more && active[t](j + 1);
                             if (next && !q_here(t))
                                 return false;
-                            constexpr int FIRST = keys.value < FIRST_KEYS ? keys.value : FIRST_KEYS;
+                            constexpr int FIRST = keys.value < FIRST_KEYS<DIM> ? keys.value : FIRST_KEYS<DIM>;
                             if (now) {
-                                if (!wait(&p_half[t], p_phase[t]))
-                                    return false;
-                                tc_fence_after();
-                                if (leader)
-                                    values(t, v, std::integral_constant<int, 0>(), std::integral_constant<int, FIRST>());
-                                __syncwarp();
+                                if constexpr (FIRST > 0) {
+                                    if (!wait(&p_half[t], p_phase[t]))
+                                        return false;
+                                    tc_fence_after();
+                                    if (leader)
+                                        values(t, v, std::integral_constant<int, 0>(), std::integral_constant<int, FIRST>());
+                                    __syncwarp();
+                                }
                                 if (!wait(&p_full[t], p_phase[t]))
                                     return false;
                                 p_phase[t] ^= 1u;
@@ -756,7 +762,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const float mc = m == -INFINITY ? 0.0f : -m * c;  // no key seen yet: weights 0
             const float2 c2 = make_float2(c, c), mc2 = make_float2(mc, mc);
             float2 sum = make_float2(0.0f, 0.0f);
-            constexpr int FIRST = CHUNKS < FIRST_KEYS / 32 ? CHUNKS : FIRST_KEYS / 32;
+            constexpr int FIRST = CHUNKS < FIRST_KEYS<DIM> / 32 ? CHUNKS : FIRST_KEYS<DIM> / 32;
             auto part = [&](auto from, auto to) {
                 uint32_t packed[to.value - from.value][16];
 #pragma unroll
@@ -773,12 +779,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int i = from.value; i < to.value; ++i)
                     tmem_st_32x32b_x16(s_addr + 16 * i, packed[i - from.value]);
             };
-            part(std::integral_constant<int, 0>(), std::integral_constant<int, FIRST>());
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&p_half[t]);
+            if constexpr (FIRST > 0) {
+                part(std::integral_constant<int, 0>(), std::integral_constant<int, FIRST>());
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&p_half[t]);
+            }
             if constexpr (FIRST < CHUNKS)
                 part(std::integral_constant<int, FIRST>(), std::integral_constant<int, CHUNKS>());
             l += sum.x + sum.y;
