@@ -258,3 +258,16 @@ def test_first_tokens_beside_hidden_rows(row):
     sees = seen_by(600, 600, True, 100, 4)[:, row]
     assert out[sees].isnan().all()
     ref.assert_within(out[~sees], clean[~sees], 4 * ref.unit(torch.bfloat16) * (clean[~sees].abs().double() + 1), "rows")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("at", [3, 127, 128, 200, 383, 450])
+def test_one_key_far_above_the_others(at, d, dtype):
+    """A maximum hundreds above all before it, in any part of any tile: sums start anew there."""
+    q, k, v, cq, cku = make([512], [512], 2, 1, d, dtype, seed=at)
+    k = k.clone()
+    k[at] = (30.0 * q[at // 2, 0].float().sign()).to(dtype)
+    for causal in (True, False):
+        out, lse = ck.ck_attention(q, k, v, cq, causal=causal, return_lse=True, scale=1.0)
+        check(q, k, v, cq, cku, out, lse, causal, scale=1.0)
