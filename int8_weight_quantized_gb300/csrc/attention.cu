@@ -821,7 +821,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (ok) {
                 const float f = l == 0.0f ? 0.0f : 1.0f / l;
                 float check = 0.0f;  // 0 while all is finite, else NaN
-#pragma unroll (WINDOW ? 1 : 2)  // (16384 tokens: 744 us with 1 and 725 with 2; six short prompts with a window: 16.6 and 16.9)
+#pragma unroll 1
                 for (int i = 0; i < DIM / 32; ++i) {
                     uint32_t v[32];
                     tmem_ld_32x32b_x32(o_addr + 32 * i, v);
@@ -1001,8 +1001,9 @@ cudaError_t launch_attention(const PromptAttention& p, const DeviceInfo& dev, cu
     cudaError_t e = device_error_ptr(&err);
     if (e != cudaSuccess)
         return e;
-    // A window has its own kernel: with its first tokens' tile in the one for all, 16384 causal tokens
-    // took 730 us instead of 725 and 8192 that are not causal 402 instead of 391.
+    // A window has its own kernel: with its first tokens' tile in one for all, and before the loads
+    // brought the maximum, 16384 causal tokens took 730 us instead of 716, 8192 that are not causal
+    // 402 instead of 388.
     auto by_window = [&](auto type, auto dim) {
         using E = decltype(type);
         constexpr int DIM = decltype(dim)::value;
