@@ -8,7 +8,8 @@
 // exponentials, one per pair and head).
 //
 // An item is two tiles of 128 queries: the same queries of two heads that share their keys, or,
-// where a group's heads are odd in number, 256 queries of one head.  It walks the key tiles (128
+// where a group's heads are odd in number, 256 queries of one head; or one tile alone, where there
+// are few.  It walks the key tiles (128
 // keys) that any of them sees, a query tile skipping those that it sees nothing of.  One block per
 // SM takes items by turns (the longest first, every second round backwards), and its roles run on
 // from item to item: the first scores of the next are computed while the last sums of one are
@@ -33,7 +34,7 @@
 //
 // Measured (GB300; 16 query heads on 4 of 128 values, bf16): 16384 causal tokens 672 to 690 us, 1590
 // to 1640 TFLOP/s, 81 to 84% of cuBLAS's measured rate; 8192 not causal 365 us, 1506; window of 1024
-// with 4 first tokens over 16000 (2 key heads) 124 us; heads of 64, 8192 causal 136 us, 1010.  A step
+// with 4 first tokens over 16000 (2 key heads) 123 to 132 us; heads of 64, 8192 causal 136 us, 1010.  A step
 // (a key tile against both query tiles) takes 1.56 us, some 2900 cycles, of which the 32 products of
 // the two tiles take 2250: what it lasts is the chain of one tile, its score product, its softmax,
 // the rest of its value product, and hand-overs of 300 to 400 cycles between them.  Between two
@@ -983,9 +984,12 @@ cudaError_t launch(const PromptAttention& p, const DeviceInfo& dev, unsigned int
     // both ends of theirs, where one tile then runs alone (16 heads on 4, pairs of heads against
     // 256 queries, when first tokens still took a whole tile: window of 1024 over 16000 tokens 148
     // against 159 us, six short prompts 18.7 against 20.2, 8192 causal tokens of 64 values 163
-    // against 168).
-    a.pair = p.q_heads / p.kv_heads % 2 == 0;
-    a.rows_log2 = a.pair ? 7 : 8;
+    // against 168).  Where there are no more tiles than multiprocessors, each has an item to itself:
+    // its steps are shorter alone (1000 causal tokens of 16 heads: 14.3 us, 16.6 in pairs; 2000 of
+    // 8: 22.6 and 27.0; 100 of 16: 6.3 and 6.7).
+    const bool alone = ((p.total_q >> 7) + p.batch) * p.q_heads <= dev.sm_count;
+    a.pair = !alone && p.q_heads / p.kv_heads % 2 == 0;
+    a.rows_log2 = a.pair || alone ? 7 : 8;
     a.slots = (p.total_q >> a.rows_log2) + p.batch;
     a.items = a.slots * (a.pair ? p.q_heads / 2 : p.q_heads);
     const unsigned blocks = (unsigned)std::min<int64_t>(a.items, dev.sm_count);

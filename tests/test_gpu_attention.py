@@ -271,3 +271,21 @@ def test_one_key_far_above_the_others(at, d, dtype):
     for causal in (True, False):
         out, lse = ck.ck_attention(q, k, v, cq, causal=causal, return_lse=True, scale=1.0)
         check(q, k, v, cq, cku, out, lse, causal, scale=1.0)
+
+
+@pytest.mark.parametrize("hq", [3, 4])
+@pytest.mark.parametrize("d", [64, 128])
+def test_hidden_infinities_among_many_sequences(hq, d):
+    """Infinities and NaN in some sequences' value rows, with more tiles than multiprocessors."""
+    lens = [300, 140] * 24
+    q, k, v, cq, cku = make(lens, lens, hq, 1, d, torch.bfloat16, seed=hq)
+    want = ck.ck_attention(q, k, v, cq)
+    v = v.clone()
+    starts = cq.tolist()
+    sees = torch.zeros(sum(lens), dtype=torch.bool, device=DEV)
+    for s, row, fill in ((0, 220, float("inf")), (7, 100, float("nan")), (30, 0, -float("inf")), (46, 299, float("nan"))):
+        v[starts[s] + row] = fill
+        sees[starts[s] + row:starts[s + 1]] = True
+    out = ck.ck_attention(q, k, v, cq)
+    ref.assert_within(out[~sees], want[~sees], 4 * ref.unit(torch.bfloat16) * (want[~sees].abs().double() + 1), "rows")
+    assert not out[sees].isfinite().any()
