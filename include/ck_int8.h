@@ -280,7 +280,8 @@ typedef enum {
  * page T[t / page_size], offset t % page_size.  Slot numbers are page * page_size + offset. */
 typedef struct {
     void *k, *v;             /* [num_pages, kv_heads, page_size, head_dim] of dtype        */
-    float *k_scale, *v_scale;/* fp32 [num_pages, kv_heads, page_size], >= 0; CK_KV_INT8 only */
+    float *k_scale, *v_scale;/* fp32 [num_pages, kv_heads, page_size], >= 0, or NaN: no numbers
+                                in the row; CK_KV_INT8 only                               */
     int64_t num_pages;
     int64_t page_size;       /* any size >= 1                                             */
     int64_t kv_heads;
@@ -304,7 +305,9 @@ typedef struct {
  *             (int64); a negative slot keeps the token out of the cache.  A 16-bit cache has
  *             the type of dtype.  CK_KV_INT8 rows: scale = max|y| / 127, code =
  *             clamp(rint(y / scale), -127, 127) from the fp32 y (ck_quantize_int8_rowwise's
- *             rule).  Two tokens with one slot leave either's row there.
+ *             rule).  A row of them that holds a NaN or an infinity, as after a position out
+ *             of range, gets the scale NaN: what reads it is NaN, not plausible.  Two tokens
+ *             with one slot leave either's row there.
  * head_dim: a multiple of 8 up to 256.  One launch. */
 int ck_qk_norm_rope(const void *qkv, int64_t qkv_stride, int64_t tokens, int64_t q_heads, int64_t kv_heads,
                     int64_t head_dim, int dtype, int norm, const void *q_weight, const void *k_weight, float eps,

@@ -7,7 +7,8 @@
 //   y_a  = n_a cos - n_b sin,  y_b = n_b cos + n_a sin   for each pair (a, b) of the first
 //          `rot` values: (i, i + rot/2), or (2i, 2i + 1) when interleaved; the rest pass
 //   int8 cache rows: scale = max|y| / 127, code = clamp(rint(y / scale), -127, 127), from the
-//          fp32 y, which is never rounded to 16 bits on the way
+//          fp32 y, which is never rounded to 16 bits on the way; a row that holds a NaN or an
+//          infinity, which codes cannot, gets the scale NaN, so that what reads it is NaN
 //
 // Bound: HBM, each value read once and written once (twice where the keys are also kept
 // contiguous).  A head is shared by dim / 8 of LANES = 8, 16 or 32 lanes, 8 values each, as two
@@ -46,6 +47,14 @@ template <class E>
 __device__ __forceinline__ uint2 pack4(const float* v)
 {
     return make_uint2(E::pack2(v[0], v[1]), E::pack2(v[2], v[3]));
+}
+
+// the larger of two, NaN where either is one (fmaxf drops it)
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
 }
 
 // ROT: 0 no rotation, 1 by halves, 2 interleaved
@@ -222,15 +231,17 @@ __global__ void __launch_bounds__(WARPS * 32, 8) norm_rope_kernel(const NormRope
             float top = 0.0f;
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                top = fmaxf(top, fabsf(v[i]));
+                top = max_nan(top, fabsf(v[i]));
 #pragma unroll
             for (int o = LANES / 2; o; o >>= 1)
-                top = fmaxf(top, __shfl_xor_sync(mask, top, o));
-            const float scale = __fdiv_rn(top, 127.0f);
+                top = max_nan(top, __shfl_xor_sync(mask, top, o));
+            // no numbers in the row (a position out of range, a NaN or infinity of the input): no scale
+            const float scale = top < INFINITY ? __fdiv_rn(top, 127.0f) : NAN;
             uint32_t c[2] = {0, 0};
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                // v / scale is at most 127 (1 + 2^-23) unless the scale is subnormal: clamp
+                // v / scale is at most 127 (1 + 2^-23) unless the scale is subnormal: clamp (codes are 0
+                // where there is no scale)
                 const float q = scale > 0.0f ? fminf(fmaxf(rintf(__fdiv_rn(v[i], scale)), -127.0f), 127.0f) : 0.0f;
                 c[i >> 2] |= (uint32_t)((int)q & 255) << (8 * (i & 3));
             }

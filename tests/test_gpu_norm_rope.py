@@ -164,3 +164,59 @@ def test_on_another_stream_and_in_a_graph():
     q3, k3 = ck.ck_qk_norm_rope(qkv, positions, table, 8, 2, qw, kw)
     torch.cuda.synchronize()
     assert torch.equal(q2, q3) and torch.equal(k2, k3) and not torch.equal(q2, q0)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_int8_rows_that_codes_cannot_hold_have_nan_scales(d, dtype):
+    """A position out of range, a NaN or an infinity leaves no plausible row in an int8 cache: the
+    row's scale is NaN, and what reads it is NaN; every other row is as it was."""
+    assert ck.ck_device_error() == 0
+    tokens, hq, hkv, page = 24, 4, 2, 8
+    qkv, qw, kw, table, positions, _, clean = make(tokens, hq, hkv, d, d, dtype, 11, page=page, cache_dtype=torch.int8)
+    slots = torch.arange(tokens, device=DEV)
+    ck.ck_qk_norm_rope(qkv, positions, table, hq, hkv, qw, kw, cache=clean, slots=slots)
+    qkv, positions = qkv.clone(), positions.clone()
+    x = qkv.view(tokens, hq + 2 * hkv, d)
+    k_bad, v_bad = torch.zeros((2, tokens, hkv), dtype=torch.bool, device=DEV)
+    for token, position in ((4, 4096), (5, -1)):
+        positions[token] = position
+        k_bad[token] = True
+    for token, head, at, fill in ((6, 0, 0, float("nan")), (7, 1, d - 1, float("inf")), (8, 0, 5, -float("inf"))):
+        x[token, hq + head, at] = fill
+        k_bad[token, head] = True
+    for token, head, at, fill in ((9, 1, d // 2, float("nan")), (10, 0, 3, float("inf")), (6, 1, 1, -float("inf"))):
+        x[token, hq + hkv + head, at] = fill
+        v_bad[token, head] = True
+    cache = ck.KVCache.empty(clean.num_pages, page, hkv, d, dtype=torch.int8)
+    ck.ck_qk_norm_rope(qkv, positions, table, hq, hkv, qw, kw, cache=cache, slots=slots)
+    assert ck.ck_device_error(clear=True) == 128
+    at, off = slots // page, slots % page
+    for name, bad in (("k", k_bad), ("v", v_bad)):
+        scale, want = [getattr(c, name + "_scale")[at, :, off] for c in (cache, clean)]
+        assert scale[bad].isnan().all(), name
+        assert torch.equal(scale[~bad], want[~bad])
+        codes, want = [getattr(c, name)[at, :, off] for c in (cache, clean)]
+        assert torch.equal(codes[~bad], want[~bad])
+    if d > 128:
+        return
+    # one sequence to a page: tokens 0..7, 8..15, 16..23; all but the last hold such rows
+    q = torch.randn((3, hq, d), device=DEV).to(dtype)
+    blocks = torch.arange(3, dtype=torch.int32, device=DEV)[:, None]
+    lens = torch.full((3,), page, dtype=torch.int32, device=DEV)
+    out = ck.ck_paged_attention(q, cache, blocks, lens).view(3, hkv, hq // hkv, d)
+    reads = (k_bad | v_bad).view(3, page, hkv).any(1)
+    assert reads[:2].all() and not reads[2].any()
+    assert out[reads].isnan().all()
+    assert torch.equal(out[2], ck.ck_paged_attention(q, clean, blocks, lens).view(3, hkv, hq // hkv, d)[2])
+
+
+@pytest.mark.parametrize("fill", [float("nan"), float("inf")])
+def test_int8_rows_without_norm_or_rotation(fill):
+    qkv, *_, slots, cache = make(9, 2, 1, 64, 0, torch.bfloat16, 12, cache_dtype=torch.int8)
+    qkv = qkv.clone()
+    qkv.view(9, 4, 64)[3, 2, 63] = qkv.view(9, 4, 64)[5, 3, 0] = fill
+    ck.ck_qk_norm_rope(qkv, None, None, 2, 1, norm=False, cache=cache, slots=slots)
+    at, off = slots // 16, slots % 16
+    assert cache.k_scale[at, 0, off].isnan().nonzero().flatten().tolist() == [3]
+    assert cache.v_scale[at, 0, off].isnan().nonzero().flatten().tolist() == [5]
