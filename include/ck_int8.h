@@ -367,7 +367,8 @@ int ck_attention(const void *q, int64_t q_stride, const void *k, int64_t k_strid
  * K a multiple of 128 and of group, N of 8, M up to 524288; it pays while the weight's bytes, not the
  * arithmetic, set the time (some tens of rows).
  *   ck_int4_prepare_weight: fp32 W [N,K] -> w4, w_scale: per group scale = bf16(max|W| / 7),
- *             code - 8 = clamp(rint(W / scale), -7, 7).
+ *             code - 8 = clamp(rint(W / scale), -7, 7); NaN for a group that holds a NaN or an
+ *             infinity.
  *   ck_int4_pack: weights quantized elsewhere, int8 codes [N,K] in [-8, 7] (clamped) -> w4. */
 int ck_int4_prepare_weight(const float *W, int64_t N, int64_t K, int64_t group, uint32_t *w4, void *w_scale,
                            void *stream);

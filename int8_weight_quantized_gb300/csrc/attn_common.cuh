@@ -19,6 +19,14 @@ enum : uint32_t {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// the larger of two, NaN where either is one (fmaxf drops it)
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // 16-bit element types: conversions to and from fp32 (round to nearest even)
 struct Bf16 {
     using T = __nv_bfloat16;

@@ -262,7 +262,8 @@ __global__ void __launch_bounds__(WARPS * 32, kMinBlocks<MT>) int4_kernel(const 
 }
 
 // Weight preparation: one thread per word for the codes; the group's scale is found by the
-// group / 8 threads that share it (group <= 256: within a warp).
+// group / 8 threads that share it (group <= 256: within a warp).  A group that holds a NaN or an
+// infinity, which codes cannot, gets the scale NaN (and codes of zero).
 __global__ void __launch_bounds__(256) int4_weight_kernel(const float* W, int64_t words, int group, uint32_t* w4,
                                                           __nv_bfloat16* w_scale)
 {
@@ -278,13 +279,13 @@ __global__ void __launch_bounds__(256) int4_weight_kernel(const float* W, int64_
         v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            top = fmaxf(top, fabsf(v[e]));
+            top = max_nan(top, fabsf(v[e]));
     }
     for (int o = lanes >> 1; o; o >>= 1)
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
     if (!in)
         return;
-    const __nv_bfloat16 s16 = __float2bfloat16_rn(__fdiv_rn(top, 7.0f));
+    const __nv_bfloat16 s16 = __float2bfloat16_rn(top < INFINITY ? __fdiv_rn(top, 7.0f) : NAN);
     const float s = __bfloat162float(s16);
     uint32_t word = 0;
 #pragma unroll

@@ -49,14 +49,6 @@ __device__ __forceinline__ uint2 pack4(const float* v)
     return make_uint2(E::pack2(v[0], v[1]), E::pack2(v[2], v[3]));
 }
 
-// the larger of two, NaN where either is one (fmaxf drops it)
-__device__ __forceinline__ float max_nan(float a, float b)
-{
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-
 // ROT: 0 no rotation, 1 by halves, 2 interleaved
 template <class E, int LANES, int ROT>
 __global__ void __launch_bounds__(WARPS * 32, 8) norm_rope_kernel(const NormRope p, unsigned int* err)

@@ -114,3 +114,26 @@ def test_other_streams_and_graphs():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(y, -want)
+
+
+@pytest.mark.parametrize("fill", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("group", [32, 64, 128, 256])
+def test_groups_that_codes_cannot_hold_have_nan_scales(group, fill):
+    """A NaN or infinite weight leaves no plausible group: its scale is NaN, and with it its row's
+    outputs; the other groups are as they were."""
+    N, K = 24, 512
+    g = torch.Generator(device=DEV)
+    g.manual_seed(5)
+    W = torch.randn((N, K), generator=g, device=DEV) * 0.02
+    w4, scale = ck.ck_int4_prepare_weight(W, group)
+    bad = torch.zeros(scale.shape, dtype=torch.bool, device=DEV)
+    for n, k in ((0, 0), (3, group - 1), (7, K - 1), (23, group + 9)):
+        W[n, k % K] = fill
+        bad[n, k % K // group] = True
+    got4, got = ck.ck_int4_prepare_weight(W, group)
+    assert torch.equal(got.isnan(), bad)
+    assert torch.equal(got[~bad], scale[~bad])
+    words = bad.repeat_interleave(group // 8, 1)
+    assert torch.equal(got4[~words], w4[~words])
+    y = ck.ck_int4_linear(torch.randn((2, K), generator=g, device=DEV).to(torch.bfloat16), got4, got)
+    assert torch.equal(y.isnan().all(0), bad.any(1)) and torch.equal(y.isnan().any(0), bad.any(1))
