@@ -344,6 +344,10 @@ int ck_paged_attention(const void *q, int64_t q_stride, const ck_kv_cache_t *cac
  *            views of a fused projection's output qualify).
  *   cu_q, cu_k: int32 [batch + 1], ascending: sequence b owns rows cu[b] .. cu[b+1] - 1.  A
  *            token before cu_q[0] or from cu_q[batch] on gets no output.
+ *            Bounds outside the tensors or descending ones set the error word's bit 7; rows of
+ *            the tensor that a sequence of such bounds names get NaN (out and lse).  Where cu_q
+ *            descends, rows that several sequences name get the output of one of them, and rows
+ *            that only a descending sequence leaves out may get none.
  *   causal:  1: query i of a sequence with n queries and m keys sees keys j <= i + m - n (its
  *            last query sees all), and with window > 0 of those only i + m - n - j < window or
  *            j < sinks.  0: every key; window must be 0.

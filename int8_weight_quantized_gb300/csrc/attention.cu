@@ -21,7 +21,8 @@
 //   warp 2      works out the items ahead of the others, which find them in shared memory (a
 //               search and divisions: 2000 to 3000 cycles between two items while every role did
 //               its own);
-//   warp 3      idle (it completes the warpgroup for the register re-balancing);
+//   warp 3      checks the sequences' bounds, then idles (it completes the warpgroup for the register
+//               re-balancing);
 //   warps 4-11  softmax, a warpgroup for each query tile, one thread per query row: reads its
 //               row of S with its maximum, writes the weights back over S as the 16-bit
 //               operand P of the second product, with heads of 128 in two parts.
@@ -157,14 +158,14 @@ struct Item {
     }
 };
 
-// The sequence with slot `s` (slot_of(b) = cu[b] / rows + b leaves room for every ragged
+// The sequence with slot `s` (slot_of(b) = max(cu[b], 0) / rows + b leaves room for every ragged
 // end, needs no sums over lengths and ascends): the last b with slot_of(b) <= s.
 __device__ __forceinline__ int64_t sequence_of_slot(const int32_t* cu, int64_t batch, int rows_log2, int64_t s)
 {
     int64_t lo = 0, hi = batch;
     while (hi - lo > 1) {
         const int64_t mid = (lo + hi) >> 1;
-        if ((int64_t)(__ldg(cu + mid) >> rows_log2) + mid <= s)
+        if ((int64_t)(max(__ldg(cu + mid), 0) >> rows_log2) + mid <= s)
             lo = mid;
         else
             hi = mid;
@@ -404,9 +405,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int64_t k0 = __ldg(p.cu_k + b), k1 = __ldg(p.cu_k + b + 1);
         const bool bad_q = q0 < 0 || q1 < q0 || q1 > p.total_q;
         w.bad = bad_q || k0 < 0 || k1 < k0 || k1 > p.total_k;
-        const int64_t r0 = (slot - ((q0 >> p.rows_log2) + b)) << p.rows_log2;
-        w.q_row = q0 + r0;
-        w.rows = bad_q || r0 < 0 ? 0 : (int)min((int64_t)1 << p.rows_log2, max(q1 - w.q_row, (int64_t)0));
+        const int64_t start = max(q0, (int64_t)0);
+        const int64_t r0 = (slot - ((start >> p.rows_log2) + b)) << p.rows_log2;
+        w.q_row = start + r0;
+        // (of a sequence with bounds out of range the rows inside the tensor)
+        w.rows = r0 < 0 ? 0 : (int)min((int64_t)1 << p.rows_log2, max(min(q1, p.total_q) - w.q_row, (int64_t)0));
         w.k_row = k0;
         w.keys = w.bad ? 0 : (int)(k1 - k0);
         w.offset = w.bad ? 0 : (int)(r0 + (k1 - k0) - (q1 - q0));
@@ -473,8 +476,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                 };
                 uint32_t uses = 0, k0_uses = 0, q_uses[2] = {0, 0};  // loads so far of the ring, K_0, Q_t
                 const bool done = each_item(std::false_type(), std::false_type(), [&](const Item& w) {
-                    if (w.bad)
-                        atomicOr(err, kErrIndex);
                     if (w.count == 0)
                         return true;
                     auto load_q = [&](int t) {
@@ -678,6 +679,18 @@ __global__ void __launch_bounds__(THREADS, 1)
                         break;
                 }
             }
+            __syncwarp();
+        } else {
+            // ---------------------------------------------------------------- bounds
+            // every sequence's, by some block: where they descend there need be no item of it
+            bool bad = false;
+            for (int64_t b = (int64_t)blockIdx.x * 32 + lane; b < p.batch; b += (int64_t)gridDim.x * 32) {
+                const int32_t q0 = __ldg(p.cu_q + b), q1 = __ldg(p.cu_q + b + 1);
+                const int32_t k0 = __ldg(p.cu_k + b), k1 = __ldg(p.cu_k + b + 1);
+                bad |= q0 < 0 || q1 < q0 || q1 > p.total_q || k0 < 0 || k1 < k0 || k1 > p.total_k;
+            }
+            if (bad)
+                atomicOr(err, kErrIndex);
             __syncwarp();
         }
     } else {

@@ -289,3 +289,57 @@ def test_hidden_infinities_among_many_sequences(hq, d):
     out = ck.ck_attention(q, k, v, cq)
     ref.assert_within(out[~sees], want[~sees], 4 * ref.unit(torch.bfloat16) * (want[~sees].abs().double() + 1), "rows")
     assert not out[sees].isfinite().any()
+
+
+def prefilled(q):
+    return torch.full_like(q, 7.0), torch.full((q.shape[1], q.shape[0]), 7.0, device=DEV)
+
+
+@pytest.mark.parametrize("hq", [3, 4])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("bounds", [[0, 64, 700, 1000], [0, 64, 700, 641], [0, 64, 700, 2 ** 31 - 1], [-5, 64, 700, 640],
+                                    [-2 ** 31, 64, 700, 640], [0, 64, 5000, 640]])
+def test_query_bounds_out_of_range_give_nan(bounds, d, hq):
+    """Rows of the tensor that a sequence with bounds outside it names are NaN, with lse; the other
+    sequences' rows are right, and the word is set."""
+    assert ck.ck_device_error() == 0
+    total = 640
+    q, k, v, _, _ = make([total], [total], hq, 1, d, torch.bfloat16, seed=21)
+    cku = torch.tensor([0, 64, 264, 640], dtype=torch.int32, device=DEV)
+    cu = torch.tensor(bounds, dtype=torch.int32, device=DEV)
+    out, lse = prefilled(q)
+    ck.ck_attention(q, k, v, cu, cku, out=out, lse=lse, return_lse=True)
+    assert ck.ck_device_error(clear=True) == 128
+    bad = torch.zeros(total, dtype=torch.bool, device=DEV)
+    for lo, hi in zip(bounds, bounds[1:]):
+        if lo < 0 or hi > total:
+            bad[max(lo, 0):max(min(hi, total), 0)] = True
+        elif lo <= hi:
+            b = bounds.index(lo)
+            ks = slice(cku[b].item(), cku[b + 1].item())
+            one = [torch.tensor([0, n], dtype=torch.int32, device=DEV) for n in (hi - lo, ks.stop - ks.start)]
+            want = ck.ck_attention(q[lo:hi], k[ks], v[ks], *one)
+            ref.assert_within(out[lo:hi], want, 4 * ref.unit(torch.bfloat16) * (want.abs().double() + 1), "rows")
+    assert out[bad].isnan().all() and lse[:, bad].isnan().all()
+    assert ck.ck_device_error() == 0
+
+
+@pytest.mark.parametrize("hq", [3, 4])
+@pytest.mark.parametrize("which", ["q", "k", "both"])
+def test_bounds_that_descend_are_reported(which, hq):
+    """A sequence whose bounds descend has no rows of its own; the word says so even where no other
+    row depends on it.  (Rows that two sequences claim get either's.)"""
+    assert ck.ck_device_error() == 0
+    q, k, v, cu, _ = make([1280], [1280], hq, 1, 64, torch.bfloat16, seed=22)
+    up = torch.tensor([0, 900, 900, 1280], dtype=torch.int32, device=DEV)
+    down = torch.tensor([0, 1000, 50, 1280], dtype=torch.int32, device=DEV)
+    out, lse = prefilled(q)
+    ck.ck_attention(q, k, v, up if which == "k" else down, up if which == "q" else down, out=out, lse=lse, return_lse=True)
+    assert ck.ck_device_error(clear=True) == 128
+    if which == "both":  # rows that one sequence alone claims
+        want = ck.ck_attention(q[:1000], k[:1000], v[:1000], torch.tensor([0, 1000], dtype=torch.int32, device=DEV))
+        ref.assert_within(out[:50], want[:50], 4 * ref.unit(torch.bfloat16) * (want[:50].abs().double() + 1), "first")
+        want = ck.ck_attention(q[50:], k[50:], v[50:], torch.tensor([0, 1230], dtype=torch.int32, device=DEV))
+        ref.assert_within(out[1000:], want[950:], 4 * ref.unit(torch.bfloat16) * (want[950:].abs().double() + 1), "last")
+    if which == "q":
+        assert not (out == 7.0).all(-1).any()
