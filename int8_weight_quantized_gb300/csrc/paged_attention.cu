@@ -466,12 +466,14 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
                                 o[nt][e][i] *= f;
                     vmax = top;
                 }
-                const float inv = top > 0.0f ? 1.0f / top : 0.0f;
+                // (the reciprocal of a subnormal scale would be infinite)
+                const float lift = top < 0x1p-96f ? 0x1p64f : 1.0f;
+                const float inv = top > 0.0f ? 1.0f / (top * lift) : 0.0f;
 #pragma unroll
                 for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
-                        vratio[kt][h] *= inv;
+                        vratio[kt][h] = vratio[kt][h] * lift * inv;
             }
             uint32_t pb[NT][KT][2];
 #pragma unroll

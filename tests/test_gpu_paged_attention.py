@@ -192,3 +192,18 @@ def test_streams_share_nothing_and_graphs_replay():
         g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, ck.ck_paged_attention(q, cache, table, n))
+
+
+@pytest.mark.parametrize("dtype,d", [(torch.bfloat16, 64), (torch.bfloat16, 128), (torch.float16, 64)])
+@pytest.mark.parametrize("scale", [1e-36, 1e-38, 1e-40, 1e-44])
+@pytest.mark.parametrize("lens", [[70], [3, 33, 900]])
+def test_tiny_value_scales_beside_zero_ones(scale, dtype, d, lens):
+    """Scales down to subnormal ones, as rows of tiny values leave them, with zero rows among them."""
+    q, cache, table, n = make(lens, 4, 2, d, 16, dtype, True, seed=31, poison=False)
+    cache.v_scale.fill_(scale)
+    cache.v_scale.view(-1)[::3] = 0.0
+    out, lse = ck.ck_paged_attention(q, cache, table, n, return_lse=True)
+    check(q, cache, table, n, out, lse)
+    cache.k_scale.mul_(scale)
+    out, lse = ck.ck_paged_attention(q, cache, table, n, return_lse=True)
+    check(q, cache, table, n, out, lse)
