@@ -28,8 +28,12 @@
 //
 // int8 rows: a code is exact in fp16, so both products run in fp16: the query scaled by the
 // power of two that brings its largest value into [1, 2) (undone in the fp32 score), and the
-// row scales folded in as fp32: k's into the score, v's into the weight, over the largest v
-// scale so far, so that scales of any size leave the fp16 weight in [0, 1].
+// row scales folded in as fp32: k's into the score, v's, as its base-2 logarithm, into the
+// exponent of the weight.  What is rounded to fp16 is the product of weight and value scale,
+// relative to the largest such product so far (or 2^kLag below it), whatever key that belongs
+// to: relative to the largest scale, a key with nearly all the weight and a small value row lost
+// its bits, or all of it, to a large row that has no weight.  The sum of the weights keeps its
+// own reference, the largest score.
 //
 // Measured (GB300; 32 query heads on 8 of 128 values): 64 sequences of 0 to 8192 tokens in 16-bit
 // rows 174 us, 6.2 TB/s, 93% of a copy's bandwidth; one of 131071 tokens 90 us, 90%; 32 sequences
@@ -56,6 +60,9 @@ constexpr int WARPS = 4;
 // Segments of at most this many keys are not split: 64 sequences of 1 to 500 tokens 19.4 us, split
 // 31.5 (a block pays about 1 us for each segment that it takes up, and the sums have to be joined).
 constexpr int kWholeKeys = 512;
+// int8 rows: how far (log2) the products of weight and value scale may exceed what they are kept
+// relative to (fp16 holds 2^15, its least normal value is 2^-14), before that follows them.
+constexpr float kLag = 8.0f;
 
 // NT: tiles of 8 query heads that a segment holds (1, or 2 where a group has more than 8)
 template <bool INT8, int DIM, int NT>
@@ -317,7 +324,7 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
     uint32_t qb[NT][DIM / 16][2];  // queries of head 8 nt + g
     float o[NT][DIM / 16][4];      // sums of heads 8 nt + 2t, + 1 (columns), two value rows
     float m[NT][2], l[NT][2];      // of those heads: maximum, sum of weights
-    float vmax = 0.0f;             // int8: what the sums o are relative to besides, the largest value scale
+    float mv[NT][2];               // int8: what the sums o are relative to instead of m, see kLag
     float c_head[NT][2];           // score factor of those heads, in units of log2
     bool bad = false;
     bool fresh = true;
@@ -374,14 +381,13 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
                 }
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    m[nt][j] = -INFINITY;
+                    m[nt][j] = mv[nt][j] = -INFINITY;
                     l[nt][j] = 0.0f;
                 }
 #pragma unroll
                 for (int e = 0; e < DIM / 16; ++e)
                     o[nt][e][0] = o[nt][e][1] = o[nt][e][2] = o[nt][e][3] = 0.0f;
             }
-            vmax = 0.0f;
             bad = false;
             fresh = false;
             first_of_segment = at.tile;
@@ -439,41 +445,17 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
                     }
                 }
             }
-            // int8: of keys 16 kt + g, + 8 the key scales, and the value scales over their maximum
-            float kscale[KT][2], vratio[KT][2];
+            // int8: of keys 16 kt + g, + 8 the key scales, and the value scales in units of log2
+            float kscale[KT][2], vlog[KT][2];
             if (INT8) {
                 const uint32_t sc = vs + KEYS * S::ROW;
-                float top = vmax;
 #pragma unroll
                 for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         kscale[kt][h] = __uint_as_float(lds32(sc + (16 * kt + g + 8 * h) * 4));
-                        vratio[kt][h] = __uint_as_float(lds32(sc + (KEYS + 16 * kt + g + 8 * h) * 4));
-                        top = fmaxf(top, vratio[kt][h]);
+                        vlog[kt][h] = fast_log2(__uint_as_float(lds32(sc + (KEYS + 16 * kt + g + 8 * h) * 4)));
                     }
-#pragma unroll
-                for (int x = 4; x <= 16; x <<= 1)
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-                if (top > vmax) {  // warp-uniform
-                    const float f = vmax / top;
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int e = 0; e < DIM / 16; ++e)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                o[nt][e][i] *= f;
-                    vmax = top;
-                }
-                // (the reciprocal of a subnormal scale would be infinite)
-                const float lift = top < 0x1p-96f ? 0x1p64f : 1.0f;
-                const float inv = top > 0.0f ? 1.0f / (top * lift) : 0.0f;
-#pragma unroll
-                for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        vratio[kt][h] = vratio[kt][h] * lift * inv;
             }
             uint32_t pb[NT][KT][2];
 #pragma unroll
@@ -510,8 +492,44 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
                         for (int h = 0; h < 2; ++h) {
                             const float x = fast_exp2(a[j][kt][h] - ref);
                             l[nt][j] += x;
-                            w[kt][2 * h + j] = INT8 ? x * vratio[kt][h] : x;
+                            w[kt][2 * h + j] = x;
                         }
+                }
+                if (INT8) {
+                    // the products of weight and value scale, relative to a reference of their own
+                    float over[2];  // the lane's largest
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        over[j] = -INFINITY;
+#pragma unroll
+                        for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                a[j][kt][h] += vlog[kt][h];
+                                over[j] = fmaxf(over[j], a[j][kt][h]);
+                            }
+                        keep[j] = 1.0f;
+                    }
+                    if (__any_sync(0xffffffffu, over[0] > mv[nt][0] + kLag || over[1] > mv[nt][1] + kLag))
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                            for (int x = 4; x <= 16; x <<= 1)
+                                over[j] = fmaxf(over[j], __shfl_xor_sync(0xffffffffu, over[j], x));
+                            if (over[j] > mv[nt][j]) {
+                                keep[j] = fast_exp2(mv[nt][j] - over[j]);
+                                mv[nt][j] = over[j];
+                            }
+                        }
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float ref = mv[nt][j] == -INFINITY ? 0.0f : mv[nt][j];
+#pragma unroll
+                        for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                w[kt][2 * h + j] = fast_exp2(a[j][kt][h] - ref);
+                    }
                 }
                 if (__any_sync(0xffffffffu, keep[0] != 1.0f || keep[1] != 1.0f))
 #pragma unroll
@@ -602,7 +620,8 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
 #pragma unroll
                     for (int w = 0; w < WARPS; ++w)
                         top = fmaxf(top, maxsum[w * HEADS + 8 * nt + 2 * t + j].x);
-                    f[nt][j] = m[nt][j] == -INFINITY ? 0.0f : fast_exp2(m[nt][j] - top) * (INT8 ? vmax : 1.0f);
+                    // (int8: the square root, twice, since 2^(mv - top) is subnormal for tiny value scales)
+                    f[nt][j] = m[nt][j] == -INFINITY ? 0.0f : fast_exp2(INT8 ? 0.5f * (mv[nt][j] - top) : m[nt][j] - top);
                 }
             // SLABS warps at a time, each in sums of its own
             for (int w = 0; w < WARPS; w += S::SLABS) {
@@ -615,7 +634,9 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
                             for (int i = 0; i < 4; ++i) {
                                 const int d = INT8 ? DIM / 8 * g + 2 * e + (i >> 1) : 16 * e + g + 8 * (i >> 1);
                                 float* dst = joined + (warp % S::SLABS * HEADS + 8 * nt + 2 * t + (i & 1)) * S::LD + d;
-                                const float x = o[nt][e][i] * f[nt][i & 1];
+                                float x = o[nt][e][i] * f[nt][i & 1];
+                                if (INT8)
+                                    x *= f[nt][i & 1];
                                 *dst = w == 0 ? x : *dst + x;
                             }
                 __syncthreads();

@@ -207,3 +207,70 @@ def test_tiny_value_scales_beside_zero_ones(scale, dtype, d, lens):
     cache.k_scale.mul_(scale)
     out, lse = ck.ck_paged_attention(q, cache, table, n, return_lse=True)
     check(q, cache, table, n, out, lse)
+
+
+@pytest.mark.parametrize("hq", [4, 20])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("ratio", [1e-2, 1e-4, 1e-6, 1e-8, 1e-12])
+@pytest.mark.parametrize("lens,at", [([1], [0]), ([100], [0]), ([100], [99]), ([40, 300], [17, 140]), ([2500], [1300])])
+def test_value_scales_that_differ_within_a_sequence(lens, at, ratio, d, hq):
+    """Nearly all the weight on a key whose value row is small beside the others.
+
+    The kernel rounds the product of weight and value scale to fp16 once, relative to at most the
+    largest such product P = max_j w_j s_j: unit(fp16) of each, or least(fp16) of P where it is
+    subnormal, so that codes of at most 127 bring m * least * 127 P.  The rest as in
+    transformer_ref.attend; the scale's base-2 logarithm brings 2^-22 of itself."""
+    hkv, page = 2, 16
+    q, cache, table, n = make(lens, hq, hkv, d, page, torch.bfloat16, True, seed=int(1 / ratio) % 1000, poison=False)
+    g = hq // hkv
+    # scores: some 40 for the chosen key, within 3 of zero for the others
+    q = (torch.ones_like(q).float() * torch.linspace(0.9, 1.1, d, device=DEV)).to(torch.bfloat16)
+    cache.k_scale.fill_(0.01)
+    cache.k.copy_(torch.where(torch.arange(d, device=DEV) % 2 == 0, cache.k, -cache.k.roll(1, -1)))
+    for b, j in enumerate(at):
+        page_at = int(table[b, j // page])
+        cache.k[page_at, :, j % page] = 127
+        cache.k_scale[page_at, :, j % page] = 40.0 / (127 * d ** 0.5)
+        cache.v_scale[page_at, :, j % page] *= ratio
+    out, lse = ck.ck_paged_attention(q, cache, table, n, return_lse=True)
+    fp16, u = torch.float16, ref.U32
+    for b, length in enumerate(lens):
+        for h in range(hkv):
+            rows = slice(h * g, (h + 1) * g)
+            k, v = rows_of(cache, table, b, length, page, h)
+            j = torch.arange(length, device=DEV)
+            s = cache.v_scale[table[b].long()[j // page], h, j % page].double()
+            seen = torch.ones((g, length), dtype=torch.bool, device=DEV)
+            want, want_lse, _, lse_tol = ref.attend(q[b, rows], k, v, d ** -0.5, seen, 0.0, 0.0)
+            score = q[b, rows].double() @ k.t() * d ** -0.5
+            w = torch.exp(score - score.amax(-1, keepdim=True))
+            total = w.sum(-1, keepdim=True)
+            dots = (q[b, rows].double().abs() @ k.abs().t() * d ** -0.5).amax(-1, keepdim=True)
+            span = (score.amax(-1, keepdim=True) - score).amax(-1, keepdim=True)
+            logs = s.log2().abs().amax()
+            eps = (d + 8) * u * dots + 2.0 ** -21 + 4 * u * span + 2.0 ** -22 * logs + ref.unit(fp16)
+            tol = (2 * eps + (length + 8) * u) * (w @ v.abs()) / total
+            tol = tol + length * ref.least(fp16) * 127 * (w * s).amax(-1, keepdim=True) / total
+            tol = tol + (want.abs() + tol) * ref.unit(torch.bfloat16) + ref.least(torch.bfloat16)
+            ref.assert_within(out[b, rows], want, tol, "sequence %d head %d" % (b, h))
+            ref.assert_within(lse[b, rows], want_lse, lse_tol, "lse")
+
+
+def test_a_large_value_row_that_nobody_weighs():
+    """One key of weight e^-60 with a value scale 1e12 times the others' costs these nothing."""
+    q, cache, table, n = make([200, 1500], 8, 2, 64, 16, torch.float16, True, seed=33, poison=False)
+    q = torch.ones_like(q)
+    cache.k_scale.fill_(0.005)
+    want = ck.ck_paged_attention(q, cache, table, n)
+    for b, j in ((0, 60), (1, 700)):
+        page_at = int(table[b, j // 16])
+        cache.k[page_at, :, j % 16] = -127
+        cache.k_scale[page_at, :, j % 16] = 60.0 / (127 * 8.0)
+        cache.v_scale[page_at, :, j % 16] = 0.0
+        clean = ck.ck_paged_attention(q, cache, table, n)
+        cache.v_scale[page_at, :, j % 16] = 1e12
+        out = ck.ck_paged_attention(q, cache, table, n)
+        assert out.isfinite().all()
+        # both round each product of weight and scale once, to a unit of 2^-11 (twice, independently),
+        # and the outputs once; the large row itself brings 1e12 * 127 * e^-60 = 1e-12
+        assert (out.float() - clean.float()).abs().max() <= 4 * 2.0 ** -11 * 127 * 0.024
