@@ -1,5 +1,5 @@
 // attn_common.cuh -- device pieces shared by the kernels around the linear layers: the two
-// 16-bit element types, the keys a query sees, and attention of one query row by one warp.
+// 16-bit element types and the keys a query sees.
 #pragma once
 
 #include <cstdint>
@@ -76,60 +76,6 @@ __host__ __device__ inline VisibleKeys visible_keys(int end, int64_t window, int
     r.tail = (int)tail;
     r.head = (int)(sinks < tail ? sinks : tail);
     return r;
-}
-
-// One query row by one warp: online softmax over its visible keys, 32 at a time.  No other key
-// or value is ever read, so nothing that a mask hides can reach the result.  `factor` is the
-// softmax scale times log2 e.  Lane l leaves with acc[i] = sum_j 2^(s_j - m) v_j[l + 32 i], the
-// maximum m of the scores s (in units of log2) and the sum l of the weights.
-template <class E, int DIM>
-__device__ __forceinline__ void attend_row(const typename E::T* q, float factor, const VisibleKeys& keys,
-                                           const typename E::T* k, int64_t k_stride, const typename E::T* v,
-                                           int64_t v_stride, float (&acc)[DIM / 32], float& m, float& l)
-{
-    const int lane = threadIdx.x & 31;
-    const int n = keys.count();
-    m = -INFINITY;
-    l = 0.0f;
-#pragma unroll
-    for (int i = 0; i < DIM / 32; ++i)
-        acc[i] = 0.0f;
-    for (int v0 = 0; v0 < n; v0 += 32) {
-        const bool mine = v0 + lane < n;
-        const int64_t key = mine ? keys.key(v0 + lane) : 0;
-        float s = -INFINITY;
-        if (mine) {
-            float dot = 0.0f;
-#pragma unroll 4
-            for (int d = 0; d < DIM; ++d)
-                dot = fmaf(E::to(q[d]), E::to(k[key * k_stride + d]), dot);
-            s = dot * factor;
-        }
-        float top = s;
-#pragma unroll
-        for (int o = 16; o; o >>= 1)
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float m2 = fmaxf(m, top);
-        const float ref = m2 == -INFINITY ? 0.0f : m2;  // every score so far is -inf: weights 0
-        const float keep = exp2f(m - ref);
-        const float p = mine ? exp2f(s - ref) : 0.0f;
-        l = l * keep + p;
-        m = m2;
-#pragma unroll
-        for (int i = 0; i < DIM / 32; ++i)
-            acc[i] *= keep;
-        const int cnt = min(32, n - v0);
-        for (int j = 0; j < cnt; ++j) {
-            const float pj = __shfl_sync(0xffffffffu, p, j);
-            const typename E::T* row = v + __shfl_sync(0xffffffffu, key, j) * v_stride;
-#pragma unroll
-            for (int i = 0; i < DIM / 32; ++i)
-                acc[i] = fmaf(pj, E::to(row[lane + 32 * i]), acc[i]);
-        }
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1)
-        l += __shfl_xor_sync(0xffffffffu, l, o);
 }
 
 }  // namespace ck

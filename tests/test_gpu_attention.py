@@ -343,3 +343,76 @@ def test_bounds_that_descend_are_reported(which, hq):
         ref.assert_within(out[1000:], want[950:], 4 * ref.unit(torch.bfloat16) * (want[950:].abs().double() + 1), "last")
     if which == "q":
         assert not (out == 7.0).all(-1).any()
+
+
+def milliseconds(fn):
+    fn()
+    ev = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    ev[0].record()
+    fn()
+    ev[1].record()
+    torch.cuda.synchronize()
+    return ev[0].elapsed_time(ev[1])
+
+
+@pytest.mark.parametrize("n,hq,hkv,d,window,causal", [(2048, 4, 1, 128, 0, True), (4096, 4, 1, 128, 0, True), (4096, 3, 1, 64, 0, True),
+                                                      (2048, 2, 2, 128, 300, True), (2000, 2, 1, 64, 0, False)])
+def test_a_channel_of_infinities(n, hq, hkv, d, window, causal):
+    """One value channel that has overflowed in every token: the other channels are right, and the
+    call does not take the time of a computation row by row."""
+    q, k, v, cq, cku = make([n, 50], [n, 50], hq, hkv, d, torch.float16, seed=n + d)
+    clean = v.clone()
+    clean[..., 3] = 0.0
+    v = v.clone()
+    v[..., 3] = float("inf")
+    sinks = 4 if window else 0
+    call = lambda x: ck.ck_attention(q, k, x, cq, causal=causal, window=window, sinks=sinks, return_lse=True)  # noqa: E731
+    out, lse = call(v)
+    assert (out[..., 3] == float("inf")).all()
+    out[..., 3] = 0.0
+    check(q, k, clean, cq, cku, out, lse, causal, window, sinks)
+    took, plain = milliseconds(lambda: call(v)), milliseconds(lambda: call(clean))
+    print("channel of infinities: %d tokens, heads %d of %d: %.3f ms, %.3f without" % (n, hq, d, took, plain))
+    assert took < 10.0
+    assert ck.ck_device_error() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_hidden_row_at_the_end_of_a_long_prompt(d):
+    n = 6000
+    q, k, v, cq, cku = make([n], [n], 2, 1, d, torch.bfloat16, seed=41)
+    clean, clean_lse = ck.ck_attention(q, k, v, cq, return_lse=True)
+    v = v.clone()
+    v[n - 1] = float("nan")
+    out, lse = ck.ck_attention(q, k, v, cq, return_lse=True)
+    assert out[n - 1].isnan().all()
+    assert torch.equal(lse, clean_lse)
+    ref.assert_within(out[:n - 1], clean[:n - 1], 4 * ref.unit(torch.bfloat16) * (clean[:n - 1].abs().double() + 1), "rows")
+    assert ck.ck_device_error() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (70, 3), (70, 40)])
+def test_every_kind_of_value_among_visible_and_hidden_rows(window, sinks, d):
+    """Infinities of both signs and NaN scattered over values: each output is what its visible keys
+    make it, finite ones to the usual bound."""
+    n = 400
+    q, k, v, cq, cku = make([n], [n], 2, 1, d, torch.bfloat16, seed=window + d)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(7)
+    clean = v.clone()
+    v = v.clone()
+    for fill, often in ((float("inf"), 0.002), (-float("inf"), 0.002), (float("nan"), 0.001)):
+        at = torch.rand(v.shape, generator=g, device=DEV) < often
+        v[at], clean[at] = fill, 0.0
+    out, lse = ck.ck_attention(q, k, v, cq, window=window, sinks=sinks, return_lse=True)
+    seen = seen_by(n, n, True, window, sinks).double()
+    plus, minus, nan = [(seen @ x[:, 0].double()) > 0 for x in (v == float("inf"), v == -float("inf"), v.isnan())]
+    for h in range(2):
+        o = out[:, h]
+        assert torch.equal(o.isnan(), nan | (plus & minus))
+        assert torch.equal(o == float("inf"), plus & ~minus & ~nan)
+        assert torch.equal(o == -float("inf"), minus & ~plus & ~nan)
+    some = (plus | minus | nan)[:, None].expand_as(out)
+    clean_out = ck.ck_attention(q, k, clean, cq, window=window, sinks=sinks)
+    check(q, k, clean, cq, cku, torch.where(some, clean_out, out), lse, True, window, sinks)
