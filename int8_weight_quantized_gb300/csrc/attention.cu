@@ -2,7 +2,8 @@
 // sliding window and first tokens that stay visible.
 //
 //   out[i,h] = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale * q_i . k_j - max), j over the keys
-//   of query i's sequence that it sees; zeros where it sees none.
+//   of query i's sequence that it sees; zeros where it sees none (NaN, 0 / 0, where all scores that
+//   it sees are -inf).
 //
 // Bound: the tensor cores, 4 dim flops per visible pair and head (and next to them the
 // exponentials, one per pair and head).
@@ -1046,7 +1047,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             o_phase ^= 1u;
             tc_fence_after();
             if (ok) {
-                const float f = l == 0.0f ? 0.0f : 1.0f / l;
+                const float f = hi < 0 ? 0.0f : 1.0f / l;  // (scores of -inf alone: 0 / 0, as they should)
                 float check = 0.0f;  // 0 while all is finite, else NaN
 #pragma unroll 1
                 for (int i = 0; i < DIM / 32; ++i) {

@@ -416,3 +416,29 @@ def test_every_kind_of_value_among_visible_and_hidden_rows(window, sinks, d):
     some = (plus | minus | nan)[:, None].expand_as(out)
     clean_out = ck.ck_attention(q, k, clean, cq, window=window, sinks=sinks)
     check(q, k, clean, cq, cku, torch.where(some, clean_out, out), lse, True, window, sinks)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("window", [0, 40])
+def test_rows_whose_scores_are_all_minus_infinity(window, d):
+    """A softmax over scores of minus infinity alone is 0 / 0, as over the cache; a row that sees a
+    finite score beside them, and one that sees no key, are not that."""
+    n = 300
+    q, k, v, _, _ = make([n + 20], [n], 2, 1, d, torch.bfloat16, seed=51)
+    q[..., 0] = q[..., 0].abs() + 0.5
+    k = k.clone()
+    k[:200] = 0.0
+    k[:200, :, 0] = -float("inf")
+    cu_q, cu_k = [torch.tensor([0, x], dtype=torch.int32, device=DEV) for x in (n + 20, n)]
+    out, lse = ck.ck_attention(q, k, v, cu_q, cu_k, window=window, return_lse=True)
+    assert (out[:20] == 0).all() and (lse[:, :20] == -float("inf")).all()
+    assert out[20:220].isnan().all() and (lse[:, 20:220] == -float("inf")).all()
+    assert out[220:].isfinite().all()
+    cache = ck.KVCache(*[x[:, 0].view(n // 10, 1, 10, d).contiguous() for x in (k, v)])
+    table = torch.arange(n // 10, dtype=torch.int32, device=DEV)[None]
+    for length in (1, 100, 200, 300):
+        one, one_lse = ck.ck_paged_attention(q[length + 19:length + 20], cache, table,
+                                             torch.tensor([length], dtype=torch.int32, device=DEV), window=window,
+                                             return_lse=True)
+        assert torch.equal(one.isnan(), out[length + 19:length + 20].isnan())
+        assert torch.equal(one_lse[0].isinf(), lse[:, length + 19].isinf())
