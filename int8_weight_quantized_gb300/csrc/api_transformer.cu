@@ -252,7 +252,7 @@ int ck_paged_attention(const void* q, int64_t q_stride, const ck_kv_cache_t* cac
     p.workspace = workspace;
     log_shape("paged_attention", batch, q_heads, p.cache.dim, p.cache.dtype, "split over the length, joined");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    ProfScope ps(kProfAttention, 1, s);
+    ProfScope ps(kProfAttention, paged_attention_launches(p), s);
     const cudaError_t e = launch_paged_attention(p, dev, s);
     return e == cudaSuccess ? CK_OK : cuda_fail(e, "ck_paged_attention launch");
 }

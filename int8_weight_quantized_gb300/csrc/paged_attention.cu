@@ -785,6 +785,14 @@ __global__ void __launch_bounds__(128) join_kernel(const PagedAttention p, int64
 
 constexpr int kMostBlocks = 152 * 3;  // of any device this library runs on
 
+// The most keys that a sequence can see.  (The workspace goes by the table alone; a window only
+// shortens.)
+int64_t longest_of(const PagedAttention& p)
+{
+    const int64_t longest = p.max_blocks * p.cache.page_size;
+    return p.window > 0 && p.sinks < longest ? std::min(longest, p.window + p.sinks) : longest;
+}
+
 template <class E, bool INT8, int DIM, int NT>
 cudaError_t launch(const PagedAttention& p, const DeviceInfo& dev, unsigned int* err, cudaStream_t s)
 {
@@ -801,11 +809,8 @@ cudaError_t launch(const PagedAttention& p, const DeviceInfo& dev, unsigned int*
         return e;
     const int group = p.q_heads / p.cache.heads;
     const int64_t segments = p.batch * p.cache.heads * ((group + S::HEADS - 1) / S::HEADS);
-    int64_t longest = p.max_blocks * p.cache.page_size;
-    if (p.window > 0 && p.sinks < longest)
-        longest = std::min(longest, p.window + p.sinks);
+    const int64_t longest = longest_of(p);
     const int64_t tiles = (longest + S::TILE - 1) / S::TILE;
-    // (the workspace goes by the table alone; a window only shortens)
     const bool split = longest > kWholeKeys;
     const int64_t most = std::min<int64_t>(kMostBlocks, (int64_t)dev.sm_count * S::BLOCKS);
     const int64_t blocks = split ? std::min(most, segments * tiles) : segments;
@@ -836,6 +841,11 @@ cudaError_t by_type(const PagedAttention& p, const DeviceInfo& dev, unsigned int
 size_t paged_attention_workspace(int group, int dim, int64_t max_len)
 {
     return max_len <= kWholeKeys ? 0 : (size_t)kMostBlocks * 2 * (group <= 8 ? 8 : 16) * (dim + 2) * sizeof(float);
+}
+
+int paged_attention_launches(const PagedAttention& p)
+{
+    return longest_of(p) > kWholeKeys ? 2 : 1;
 }
 
 cudaError_t launch_paged_attention(const PagedAttention& p, const DeviceInfo& dev, cudaStream_t s)

@@ -65,6 +65,7 @@ struct PagedAttention {
 };
 // by query heads per kv head and the most keys a sequence can have
 size_t paged_attention_workspace(int group, int dim, int64_t max_len);
+int paged_attention_launches(const PagedAttention& p);  // kernels that the call enqueues
 cudaError_t launch_paged_attention(const PagedAttention& p, const DeviceInfo& dev, cudaStream_t s);
 
 struct PromptAttention {

@@ -274,3 +274,16 @@ def test_a_large_value_row_that_nobody_weighs():
         # both round each product of weight and scale once, to a unit of 2^-11 (twice, independently),
         # and the outputs once; the large row itself brings 1e12 * 127 * e^-60 = 1e-12
         assert (out.float() - clean.float()).abs().max() <= 4 * 2.0 ** -11 * 127 * 0.024
+
+
+def test_launches_are_counted():
+    """The count of kernels goes by what a call enqueues: a split call joins in a second launch."""
+    for length, launches in ((100, 1), (512, 1), (513, 2), (3000, 2)):
+        q, cache, table, n = make([length], 4, 2, 64, 1, torch.bfloat16, False, seed=41)
+        table = table[:, :length].contiguous()
+        ck.ck_profile_begin(with_events=False)
+        ck.ck_paged_attention(q, cache, table, n)
+        assert ck.ck_profile_end()["attention"][1] == launches
+        ck.ck_profile_begin(with_events=False)
+        ck.ck_paged_attention(q, cache, table, n, window=100, sinks=4)
+        assert ck.ck_profile_end()["attention"][1] == 1
