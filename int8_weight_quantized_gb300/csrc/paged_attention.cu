@@ -790,7 +790,8 @@ constexpr int kMostBlocks = 152 * 3;  // of any device this library runs on
 int64_t longest_of(const PagedAttention& p)
 {
     const int64_t longest = p.max_blocks * p.cache.page_size;
-    return p.window > 0 && p.sinks < longest ? std::min(longest, p.window + p.sinks) : longest;
+    // (by a difference: the sum of a window and first tokens of any size could overflow)
+    return p.window > 0 && p.sinks < longest && p.window < longest - p.sinks ? p.window + p.sinks : longest;
 }
 
 template <class E, bool INT8, int DIM, int NT>

@@ -287,3 +287,14 @@ def test_launches_are_counted():
         ck.ck_profile_begin(with_events=False)
         ck.ck_paged_attention(q, cache, table, n, window=100, sinks=4)
         assert ck.ck_profile_end()["attention"][1] == 1
+
+
+def test_windows_up_to_the_largest_integer():
+    q, cache, table, n = make([3000, 41], 4, 2, 64, 16, torch.bfloat16, False, seed=42)
+    want = ck.ck_paged_attention(q, cache, table, n)
+    most = 2 ** 63 - 1
+    for window, sinks in ((most, 0), (most, 4), (most, most), (most - 3, 4), (5, most)):
+        ck.ck_profile_begin(with_events=False)
+        out = ck.ck_paged_attention(q, cache, table, n, window=window, sinks=sinks)
+        assert ck.ck_profile_end()["attention"][1] == 2  # split, as without a window
+        assert torch.equal(out, want)
