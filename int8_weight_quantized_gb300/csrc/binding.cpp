@@ -100,7 +100,8 @@ int act_type(const at::Tensor& t, const char* name)
     type_error(std::string(name) + " must be torch.bfloat16 or torch.float16, got " + type_name(t.scalar_type()));
 }
 
-// Elements between the tokens of t [tokens, heads, dim], whose rows are dense.
+// Elements between the tokens of t [tokens, heads, dim], whose rows are dense.  (Of one token there is
+// none, whatever the tensor says.)
 int64_t token_stride(const at::Tensor& t, at::ScalarType type, int64_t dim, const char* name)
 {
     require_type(t, type, name);
@@ -109,7 +110,7 @@ int64_t token_stride(const at::Tensor& t, at::ScalarType type, int64_t dim, cons
                     shape_text(t.sizes()));
     if ((t.stride(2) != 1 && dim > 1) || (t.stride(1) != dim && t.size(1) > 1))
         value_error(std::string("the heads of a token must be contiguous in ") + name);
-    return t.size(0) > 1 ? t.stride(0) : std::max(t.stride(0), t.size(1) * dim);
+    return t.size(0) > 1 ? t.stride(0) : t.size(1) * dim;
 }
 
 int64_t integer(PyObject* o, const char* name)
@@ -295,7 +296,7 @@ PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n)
             require(k = tensor(a[16], "k"), type, {tokens, hkv, dim}, "k");
         else if (want_k)
             k = empty({tokens, hkv, dim}, type, qkv);
-        const int64_t stride = tokens > 1 ? qkv.stride(0) : std::max(qkv.stride(0), width);
+        const int64_t stride = tokens > 1 ? qkv.stride(0) : width;
         const int st = p_norm_rope(qkv.data_ptr(), stride, tokens, hq, hkv, dim, dtype, truth(a[8]) ? 1 : 0, ptr(qw), ptr(kw),
                                    (float)number(a[7], "eps"), rot, truth(a[9]) ? 1 : 0,
                                    static_cast<const int32_t*>(ptr(positions)), static_cast<const float*>(ptr(table)), max_pos,

@@ -77,3 +77,19 @@ def test_empty_batches():
     q, k = ck.ck_qk_norm_rope(t(0, 256), None, None, 2, 1)
     assert q.shape == (0, 2, 64) and k.shape == (0, 1, 64)
     assert ck.ck_int4_linear(t(0, 256), i32(16, 32), t(16, 2)).shape == (0, 16)
+
+
+def test_the_stride_of_one_token_does_not_matter():
+    """Views of one row of a wider tensor, whose row length need not be a multiple of anything."""
+    x = torch.randn((3, 4 * 64 + 3), device="cuda").to(BF)
+    q, k, v = x[:, :128].view(3, 2, 64)[:1], x[:, 128:192].view(3, 1, 64)[:1], x[:, 192:256].view(3, 1, 64)[:1]
+    assert q.stride(0) == 259
+    cu = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    assert torch.equal(ck.ck_attention(q, k, v, cu), v.expand(1, 2, 64))
+    got = ck.ck_qk_norm_rope(x[:1, :256], None, None, 2, 1, norm=False)
+    assert torch.equal(got[0], q) and torch.equal(got[1], k)
+    cache = ck.KVCache(k.contiguous().view(1, 1, 1, 64), v.contiguous().view(1, 1, 1, 64))
+    out = ck.ck_paged_attention(q, cache, i32(1, 1), i32(1) + 1)
+    assert torch.equal(out, v.expand(1, 2, 64))
+    with pytest.raises(ck.CkError):  # two tokens have one
+        ck.ck_qk_norm_rope(x[:2, :256], None, None, 2, 1)
