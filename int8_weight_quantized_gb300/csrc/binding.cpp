@@ -227,7 +227,14 @@ PyObject* guarded(const char* name, Py_ssize_t got, Py_ssize_t want, Fn fn)
         return fn();
     } catch (const Raise& r) {
         PyErr_SetString(r.type, r.text.c_str());
-    } catch (const std::exception& e) {  // an allocation that failed
+    } catch (const c10::OutOfMemoryError& e) {  // as torch raises it, for callers that catch it
+        PyObject* torch = PyImport_ImportModule("torch");
+        PyObject* type = torch ? PyObject_GetAttrString(torch, "OutOfMemoryError") : nullptr;
+        if (type)
+            PyErr_SetString(type, e.what_without_backtrace());
+        Py_XDECREF(type);
+        Py_XDECREF(torch);
+    } catch (const std::exception& e) {
         PyErr_SetString(PyExc_RuntimeError, e.what());
     }
     return nullptr;

@@ -93,3 +93,15 @@ def test_the_stride_of_one_token_does_not_matter():
     assert torch.equal(out, v.expand(1, 2, 64))
     with pytest.raises(ck.CkError):  # two tokens have one
         ck.ck_qk_norm_rope(x[:2, :256], None, None, 2, 1)
+
+
+def test_an_output_that_does_not_fit_is_torchs_out_of_memory_error():
+    """2^40 bytes of output for a view of one token repeated: refused by torch's allocator, under a
+    limit that it keeps without asking the device."""
+    torch.cuda.set_per_process_memory_fraction(0.5)
+    try:
+        q = t(1, 2, 64).expand(2 ** 32, 2, 64)
+        with pytest.raises(torch.OutOfMemoryError):
+            ck.ck_attention(q, t(1, 1, 64), t(1, 1, 64), i32(2))
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
