@@ -6,7 +6,8 @@ linked into one shared library with the CUDA runtime linked statically, so the
 library has no dependency beyond the driver.  The result lives next to this file
 (``lib/libck_int8.so``); the Python binding loads it from there.  ``lib/_ck_binding.so``
 (csrc/binding.cpp, compiled against the installed torch by the host compiler) hands tensors
-to the operators around the linear layers.
+to the operators around the linear layers; where it does not compile, the library is built all
+the same, and those operators say that it is missing.
 """
 import concurrent.futures as cf
 import os
@@ -39,9 +40,10 @@ def nvcc():
     return cand
 
 
-def _inputs_mtime():
-    files = [os.path.join(CSRC, s) for s in SOURCES + HEADERS + ["binding.cpp"]] + [os.path.join(INCLUDE, "ck_int8.h"), __file__]
-    return max(os.path.getmtime(f) for f in files)
+def _fresh(target, sources):
+    """Whether target exists and is no older than its sources (of CSRC), the header and this file."""
+    files = [os.path.join(CSRC, s) for s in sources] + [os.path.join(INCLUDE, "ck_int8.h"), __file__]
+    return os.path.exists(target) and os.path.getmtime(target) >= max(os.path.getmtime(f) for f in files)
 
 
 def _compile(src, verbose):
@@ -75,17 +77,9 @@ def _compile_binding():
     os.replace(tmp, BINDING)
 
 
-def build(force=False, verbose=False):
-    """Compile if any source is newer than the library; return the library path."""
-    newest = _inputs_mtime()
-    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= newest for f in (LIB, BINDING)):
-        return LIB
-    os.makedirs(OBJ_DIR, exist_ok=True)
-    os.makedirs(LIB_DIR, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        binding = ex.submit(_compile_binding)
+def _compile_library(verbose):
+    with cf.ThreadPoolExecutor(max_workers=max(1, len(SOURCES))) as ex:
         results = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
-        binding.result()
     if verbose:
         for _, log in results:
             sys.stderr.write(log)
@@ -95,6 +89,26 @@ def build(force=False, verbose=False):
     if r.returncode != 0:
         raise RuntimeError("link failed:\n%s\n%s" % (r.stdout, r.stderr))
     os.replace(tmp, LIB)
+
+
+def build(force=False, verbose=False, require_binding=False):
+    """Compile what is older than its sources; return the library path.  A binding that does not
+    compile is reported on stderr and left out, or with require_binding raised, after the library."""
+    os.makedirs(OBJ_DIR, exist_ok=True)
+    os.makedirs(LIB_DIR, exist_ok=True)
+    failure = None
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        binding = None if not force and _fresh(BINDING, ["binding.cpp"]) else ex.submit(_compile_binding)
+        if force or not _fresh(LIB, SOURCES + HEADERS):
+            _compile_library(verbose)
+        if binding is not None:
+            failure = binding.exception()
+    if failure is not None:
+        if os.path.exists(BINDING):  # of other sources
+            os.remove(BINDING)
+        if require_binding:
+            raise failure
+        sys.stderr.write("the operators around the linear layers are left out: %s\n" % failure)
     return LIB
 
 
