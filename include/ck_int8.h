@@ -326,7 +326,8 @@ int ck_qk_norm_rope(const void *qkv, int64_t qkv_stride, int64_t tokens, int64_t
  *   out:         [batch, q_heads, head_dim] of dtype, written.
  *   lse:         fp32 [batch, q_heads] or NULL: the natural log of the softmax's sum,
  *                max included.
- * head_dim: 64 or 128.  The cache's type is dtype or CK_KV_INT8.  The result does not depend
+ * head_dim: 64 or 128 (a cache that ck_qk_norm_rope fills with heads of another size has no reader
+ * here).  The cache's type is dtype or CK_KV_INT8.  The result does not depend
  * on what else is in the batch's pages: rows that no sequence sees are never read.
  * workspace: ck_paged_attention_workspace_size(batch, q_heads, kv_heads, head_dim, max_blocks *
  *              page_size) bytes (0 for short tables: it may be NULL then); its content does not
@@ -369,11 +370,13 @@ int ck_attention(const void *q, int64_t q_stride, const void *k, int64_t k_strid
  *   bias:     [N] of dtype or NULL.  residual: [M,N] of out_dtype or NULL (may be y).
  *   y:        [M,N] of out_dtype (a ck_dtype_t), written.
  * K a multiple of 128 and of group, N of 8, M up to 524288; it pays while the weight's bytes, not the
- * arithmetic, set the time (some tens of rows).
+ * arithmetic, set the time (some tens of rows; every 32 rows read the whole weight again).
  *   ck_int4_prepare_weight: fp32 W [N,K] -> w4, w_scale: per group scale = bf16(max|W| / 7),
  *             code - 8 = clamp(rint(W / scale), -7, 7); NaN for a group that holds a NaN or an
  *             infinity.
- *   ck_int4_pack: weights quantized elsewhere, int8 codes [N,K] in [-8, 7] (clamped) -> w4. */
+ *   ck_int4_pack: weights quantized elsewhere, int8 codes [N,K] in [-8, 7] (clamped) -> w4.
+ *             Scales are bf16 whatever dtype is, and there is no zero point: fp16 or fp32 scales
+ *             lose up to 2^-9 of each weight on their way to w_scale. */
 int ck_int4_prepare_weight(const float *W, int64_t N, int64_t K, int64_t group, uint32_t *w4, void *w_scale,
                            void *stream);
 int ck_int4_pack(const int8_t *codes, int64_t N, int64_t K, uint32_t *w4, void *stream);

@@ -35,8 +35,9 @@
 // tokens over 16000 148 us with a whole tile, 140 so; six short prompts 18.7 and 16.8).
 //
 // Measured (GB300; 16 query heads on 4 of 128 values, bf16): 16384 causal tokens 672 to 690 us, 1590
-// to 1640 TFLOP/s, 81 to 84% of cuBLAS's measured rate; 8192 not causal 365 us, 1506; window of 1024
-// with 4 first tokens over 16000 (2 key heads) 123 to 132 us; heads of 64, 8192 causal 136 us, 1010.
+// to 1640 TFLOP/s, 81 to 84% of cuBLAS's measured rate; 8192 not causal 358 to 389 us, 1410 to 1540;
+// window of 1024 with 4 first tokens over 16000 (2 key heads) 123 to 132 us; heads of 64, 8192 causal
+// 131 us, 1050.
 // A step (a key tile against both query tiles) takes 1.56 us, some 2900 cycles, of which the 32
 // products of the two tiles take 2250: what it lasts is the chain of one tile, its score product, its softmax,
 // the rest of its value product, and hand-overs of 300 to 400 cycles between them.  Between two

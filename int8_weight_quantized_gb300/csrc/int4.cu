@@ -38,9 +38,11 @@ __device__ __forceinline__ int code_shift(int e)
 //
 // Measured (GB300): one row, 28672 x 5376, groups of 128: 20.8 to 22.9 us, 3.5 to 3.8 TB/s, 52 to
 // 57% of a copy's bandwidth, the ALU (shift and mask of each nibble pair) busy in 57% of the
-// cycles, an instruction issued in 64%; one row, 4096 x 4096: 4.5 us (launch and latency); 16
-// rows, 16384 x 4096, groups of 64: 15.1 us, 2.4 TB/s, waiting on the ring and on x; 32 rows,
-// groups of 128: 23.2 us.
+// cycles, an instruction issued in 64%; in fp16, which takes two shifts less for a word, 21.1: the
+// ALU alone is not what bounds it.  One row, 4096 x 4096: 4.4 us (launch and latency); 16 rows,
+// 16384 x 4096, groups of 64: 15.2 us, 2.4 TB/s, waiting on the ring and on x; 32 rows, groups of
+// 128: 23.0 us, 64 rows 42, 512 rows 267, 8192 rows 4.0 ms (272 TFLOP/s: beyond 32 rows each tile of
+// them reads and widens the whole weight again).
 constexpr int WARPS = 8;
 constexpr int CHUNK = 128;                 // k of a ring unit
 constexpr int STAGES = 4;

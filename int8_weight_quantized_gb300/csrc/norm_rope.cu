@@ -20,10 +20,13 @@
 // three quarters of its 237 instructions per two heads on tests and addresses.
 //
 // Measured (GB300): 8192 tokens of 32 query and 8 key heads of 128, bf16, keys also kept
-// contiguous: 45.9 us, 4.84 TB/s, 73% of a copy's bandwidth; 4096 tokens of 16 and 4 heads of 256:
-// 24 us, 4.3 TB/s; one token 3.0 us (launch).  The arithmetic issues in 73% of the cycles; more
-// warps at 48 registers (10 blocks per SM, 50.8 us) or resident blocks that fetch the next heads
-// while they work on these (49 to 56 us at 4 to 6 blocks per SM) were slower.
+// contiguous: 45.3 to 45.9 us, 4.9 TB/s, 73% of a copy's bandwidth, interleaved 45.7, into int8 rows
+// 62; 4096 tokens of 16 and 4 heads of 256: 23.6 us, 4.4 TB/s; one token 3.0 us (launch).  The
+// arithmetic issues in 73% of the cycles, accesses are of 8 bytes, and at the 64 registers that 8
+// blocks per SM leave the kernels that rotate spill 24 to 48 bytes a thread (the quantization to
+// int8 is a branch of each); which of these sets the time is not settled.  More warps at 48
+// registers (10 blocks per SM, 50.8 us) or resident blocks that fetch the next heads while they
+// work on these (49 to 56 us at 4 to 6 blocks per SM) were slower.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

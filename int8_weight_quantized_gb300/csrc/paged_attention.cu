@@ -36,13 +36,17 @@
 // own reference, the largest score.
 //
 // Measured (GB300; 32 query heads on 8 of 128 values): 64 sequences of 0 to 8192 tokens in 16-bit
-// rows 174 us, 6.2 TB/s, 93% of a copy's bandwidth; one of 131071 tokens 90 us, 90%; 32 sequences
-// of 1025 to 16384 tokens in int8 rows 101 us, 87%; one of 274 tokens 6.6 us, of 64 tokens 3.6 (two
-// products, a few tiles per warp: latency).  int8 rows are bound by instructions: each code is widened for the
-// matrix instruction, which has no int8 by 16-bit form.
+// rows 170 to 174 us, 6.3 TB/s, 94% of a copy's bandwidth; one of 131071 tokens 89 us, 91%; 32
+// sequences of 1025 to 16384 tokens in int8 rows 99 to 101 us, 88%, heads of 64 65.5, 69%; one of 274
+// tokens 6.4 to 6.8 us, of 64 tokens 4 to 5 (two products, a few tiles per warp: latency).  int8 rows are
+// bound by instructions: each code is widened for the matrix instruction, which has no int8 by 16-bit
+// form.
 //
-// Rounding to fewer bits: each weight once, to the type of the values' product (bf16 or
-// fp16), which is what the matrix instruction takes; sums, maxima and scores are fp32.
+// Rounding to fewer bits: each weight once (on int8 rows its product with the value scale), to the
+// type of the values' product (bf16 or fp16), which is what the matrix instruction takes; on int8
+// rows also the query, to fp16 after its scaling, which is exact but for values below 2^-17 (of bf16)
+// or 2^-14 (of fp16) of the head's largest, and those are off by 2^-25 of it at most.  Sums, maxima
+// and scores are fp32.
 #include <algorithm>
 #include <type_traits>
 
