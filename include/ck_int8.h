@@ -339,6 +339,41 @@ int ck_paged_attention(const void *q, int64_t q_stride, const ck_kv_cache_t *cac
                        float scale, int64_t window, int64_t sinks, void *out, float *lse, void *workspace,
                        size_t workspace_bytes, void *stream);
 
+/* The same where groups of sequences stand behind a long prefix that they share (a system prompt, a
+ * document with many questions): its keys and values are stored once, and read for the whole group.
+ *   out[b,h] = sum_j softmax_j(scale * q[b,h] . k_j) v_j, j over the prefix_lens[i] keys of the prefix i
+ *   that sequence b stands behind, then over its own seq_lens[b] keys.
+ *   prefix_table: int32 [num_prefixes, max_prefix_blocks], the pages of each prefix; prefix_lens: int32
+ *                [num_prefixes], 0 .. max_prefix_blocks * page_size.  num_prefixes: 1 to 65536.
+ *   cu_prefix:   int32 [num_prefixes + 1], ascending: sequences cu[i] .. cu[i + 1] - 1 stand behind
+ *                prefix i, those before cu[0] and from cu[num_prefixes] on behind none.  Bounds that
+ *                descend or leave 0 .. batch: every output is NaN.
+ *   block_table, seq_lens: each sequence's own tokens (its new one is the last of them), which need
+ *                not begin on a page of their own length: token t of these is at page T[t / page_size].
+ * The rest as for ck_paged_attention; no window.  A sequence without any key gives zeros (lse -inf).
+ * workspace: ck_prefix_attention_workspace_size(batch, q_heads, kv_heads, head_dim, num_prefixes,
+ *              max_prefix_blocks * page_size, max_blocks * page_size) bytes. */
+size_t ck_prefix_attention_workspace_size(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                                          int64_t num_prefixes, int64_t max_prefix_len, int64_t max_len);
+int ck_prefix_attention(const void *q, int64_t q_stride, const ck_kv_cache_t *cache, const int32_t *prefix_table,
+                        int64_t max_prefix_blocks, const int32_t *prefix_lens, const int32_t *cu_prefix,
+                        int64_t num_prefixes, const int32_t *block_table, int64_t max_blocks, const int32_t *seq_lens,
+                        int64_t batch, int64_t q_heads, int dtype, float scale, void *out, float *lse, void *workspace,
+                        size_t workspace_bytes, void *stream);
+
+/* Rows of the cache back as contiguous keys and values, for ck_attention over tokens that are in
+ * the cache already: a prompt's second chunk, prompts behind a cached prefix (a block table may name
+ * the prefix's pages and then others).
+ *   k_out, v_out: [total, kv_heads, head_dim] of dtype, written: row cu[b] + t is the row of token t of
+ *             sequence b, t < cu[b + 1] - cu[b]; int8 rows are code * scale, rounded once.  Rows
+ *             before cu[0] and from cu[batch] on stay as they are.
+ *   block_table: int32 [batch, max_blocks].  cu: int32 [batch + 1], ascending, cu[batch] <= total.
+ *             Bounds out of range or descending set the error word's bit 7; tokens beyond the table
+ *             or on a page out of range get NaN.
+ * head_dim: a multiple of 8 up to 256.  The cache's type is dtype or CK_KV_INT8.  One launch. */
+int ck_cache_read(const ck_kv_cache_t *cache, const int32_t *block_table, int64_t max_blocks, const int32_t *cu,
+                  int64_t batch, int64_t total, int dtype, void *k_out, void *v_out, void *stream);
+
 /* Attention over whole prompts, a ragged batch of them in one call.
  *   q:       [total_q, q_heads, head_dim] of dtype, q_stride elements between tokens; k, v:
  *            [total_k, kv_heads, head_dim], k_stride / v_stride elements (multiples of 8;
@@ -383,10 +418,43 @@ int ck_int4_pack(const int8_t *codes, int64_t N, int64_t K, uint32_t *w4, void *
 int ck_int4_linear(const void *x, const uint32_t *w4, const void *w_scale, const void *bias, const void *residual,
                    void *y, int64_t M, int64_t N, int64_t K, int64_t group, int dtype, int out_dtype, void *stream);
 
+/* Low-rank adapters of many requests at once, beside a projection that they share:
+ *   y[m] = out( residual[m] + scaling[i] * (x[m] A_i^T) B_i^T ),  i = index[m];  residual[m] where i < 0
+ *   x:        [M,K] of dtype.  a: [num_adapters, rank, K], b: [num_adapters, N, rank] of dtype.
+ *   index:    int32 [M], any order; negative: no adapter.  num_adapters or above: the row is NaN and the
+ *             error word's bit 7 set.
+ *   scaling:  fp32 [num_adapters] or NULL (1).
+ *   residual: [M,N] of out_dtype, the shared projection's output, or NULL (0); may be y.
+ *   y:        [M,N] of out_dtype (a ck_dtype_t), written.
+ * K a multiple of 16, N of 8, rank of 8 up to 128, M up to 16777216.  Sums are fp32.
+ * workspace: ck_adapter_linear_workspace_size(M, N, K, rank) bytes; its content does not matter. */
+size_t ck_adapter_linear_workspace_size(int64_t M, int64_t N, int64_t K, int64_t rank);
+int ck_adapter_linear(const void *x, const void *a, const void *b, const int32_t *index, const float *scaling,
+                      const void *residual, void *y, int64_t M, int64_t N, int64_t K, int64_t rank, int64_t num_adapters,
+                      int dtype, int out_dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Log probabilities of given tokens under rows of logits, with each row's entropy and its likeliest
+ * tokens.  With t_j = scale * (x_j - max x) and s = sum_j exp(t_j):
+ *   logprob[m] = t_token - log s;  entropy[m] = log s - (sum_j t_j exp(t_j)) / s;  lse[m] = scale * max x + log s
+ *   logits:  [rows, vocab] of dtype (a ck_dtype_t, fp32 included), `stride` elements between rows; rows need
+ *            only their elements' alignment.  -inf: a token that cannot be (it adds nothing).  A row
+ *            that holds a NaN or +inf, or only -inf, has NaN log probabilities and entropy.
+ *   tokens:  int32 [rows]; negative: none (logprob 0).  vocab or above: NaN and the error word's bit 7.
+ *   scale:   finite, > 0 (one over the temperature).
+ *   logprob, entropy, lse: fp32 [rows], each NULL where it is not wanted (tokens is read with logprob only).
+ *   top:     0 .. 32, at most vocab: top_logprob fp32, top_index int32 [rows, top], the largest logits in
+ *            descending order, of equal ones the lowest index first, NaN above all others.
+ * workspace: ck_token_logprobs_workspace_size(rows, vocab, top) bytes (it may be NULL where that is 0). */
+size_t ck_token_logprobs_workspace_size(int64_t rows, int64_t vocab, int64_t top);
+int ck_token_logprobs(const void *logits, int64_t stride, const int32_t *tokens, int64_t rows, int64_t vocab, int dtype,
+                      float scale, int64_t top, float *logprob, float *entropy, float *lse, float *top_logprob,
+                      int32_t *top_index, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Launch profiling, for benchmarks.  Between ck_profile_begin() and ck_profile_end()
  * the library counts the kernels it enqueues from the calling host thread, by kind
  * (0 = activation quantize, 1 = int8 -> bf16 operand widening, 2 = GEMM with fused
- * epilogue, 3 = norm and rotation, 4 = attention, 5 = 4-bit linear).  With with_events != 0 it also brackets each launch with two CUDA events on
+ * epilogue, 3 = norm and rotation, 4 = attention, 5 = 4-bit linear, 6 = low-rank
+ * adapters, 7 = log probabilities, 8 = cache rows read back).  With with_events != 0 it also brackets each launch with two CUDA events on
  * the kernel's own stream (the kernels are unchanged, but the events separate
  * consecutive kernels, so launch overlap between them is lost while timing).
  * ck_profile_end() waits for the events and fills, for each kind k < nkinds,

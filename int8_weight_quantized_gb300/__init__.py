@@ -72,6 +72,14 @@ def load_library(path=None):
                             I),
         "ck_paged_attention_workspace_size": ([I64, I64, I64, I64, I64], SZ),
         "ck_paged_attention": ([P, I64, P, P, I64, P, I64, I64, I, ctypes.c_float, I64, I64, P, P, P, SZ, P], I),
+        "ck_prefix_attention_workspace_size": ([I64, I64, I64, I64, I64, I64, I64], SZ),
+        "ck_prefix_attention": ([P, I64, P, P, I64, P, P, I64, P, I64, P, I64, I64, I, ctypes.c_float, P, P, P, SZ, P],
+                                I),
+        "ck_cache_read": ([P, P, I64, P, I64, I64, I, P, P, P], I),
+        "ck_adapter_linear_workspace_size": ([I64, I64, I64, I64], SZ),
+        "ck_adapter_linear": ([P, P, P, P, P, P, P, I64, I64, I64, I64, I64, I, I, P, SZ, P], I),
+        "ck_token_logprobs_workspace_size": ([I64, I64, I64], SZ),
+        "ck_token_logprobs": ([P, I64, P, I64, I64, I, ctypes.c_float, I64, P, P, P, P, P, P, SZ, P], I),
         "ck_attention": ([P, I64, P, I64, P, I64, P, P, I64, I64, I64, I64, I64, I64, I, ctypes.c_float, I, I64, I64, P,
                           P, P], I),
         "ck_int4_prepare_weight": ([P, I64, I64, I64, P, P, P], I),
@@ -386,7 +394,7 @@ def ck_selftest_wait_timeout(timeout_ns=1_000_000, stream=None):
     return load_library().ck_selftest_wait_timeout(int(timeout_ns), _stream(stream))
 
 
-PROFILE_KINDS = ("quantize", "widen", "gemm", "norm_rope", "attention", "int4")
+PROFILE_KINDS = ("quantize", "widen", "gemm", "norm_rope", "attention", "int4", "adapter", "logprobs", "cache_read")
 
 
 def ck_profile_begin(with_events=True):
@@ -402,5 +410,6 @@ def ck_profile_end():
     return {k: (ms[i], cnt[i]) for i, k in enumerate(PROFILE_KINDS)}
 
 
-from .transformer import (KVCache, ck_attention, ck_int4_linear, ck_int4_pack,  # noqa: E402
-                          ck_int4_prepare_weight, ck_paged_attention, ck_qk_norm_rope, rope_table)
+from .transformer import (KVCache, TokenLogprobs, ck_adapter_linear, ck_attention, ck_cache_read,  # noqa: E402
+                          ck_int4_linear, ck_int4_pack, ck_int4_prepare_weight, ck_paged_attention, ck_prefix_attention,
+                          ck_qk_norm_rope, ck_token_logprobs, rope_table)

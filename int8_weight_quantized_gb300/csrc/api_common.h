@@ -47,7 +47,10 @@ enum ProfKind {
     kProfNormRope = 3,
     kProfAttention = 4,
     kProfInt4 = 5,
-    kProfKinds = 6
+    kProfAdapter = 6,
+    kProfLogprobs = 7,
+    kProfCacheRead = 8,
+    kProfKinds = 9
 };
 
 // Counts the launches made in its lifetime and, when event profiling is on, brackets them

@@ -40,6 +40,13 @@ int check_dtype(int dtype)
     return CK_OK;
 }
 
+int check_out_dtype(int out_dtype)
+{
+    if (!valid_16bit(out_dtype) && out_dtype != CK_OUT_F32)
+        return fail(CK_ERR_INVALID_ARG, "out_dtype must be 0 (bf16), 1 (fp16) or 2 (fp32), got %d", out_dtype);
+    return CK_OK;
+}
+
 int check_mask(int64_t window, int64_t sinks)
 {
     if (window < 0 || sinks < 0)
@@ -86,6 +93,17 @@ int check_cache(const ck_kv_cache_t* c, int64_t kv_heads, int64_t head_dim, int 
     out->dim = (int)head_dim;
     out->dtype = c->dtype;
     return CK_OK;
+}
+
+// log2 of the page size, -1 if it is no power of two
+int page_shift_of(int page_size)
+{
+    if ((page_size & (page_size - 1)) != 0)
+        return -1;
+    int shift = 0;
+    while ((1 << shift) < page_size)
+        ++shift;
+    return shift;
 }
 
 #define CK_CHECK(call)            \
@@ -243,10 +261,7 @@ int ck_paged_attention(const void* q, int64_t q_stride, const ck_kv_cache_t* cac
     p.scale = scale;
     p.window = window;
     p.sinks = sinks;
-    p.page_shift = -1;
-    if ((p.cache.page_size & (p.cache.page_size - 1)) == 0)
-        for (p.page_shift = 0; (1 << p.page_shift) < p.cache.page_size;)
-            ++p.page_shift;
+    p.page_shift = page_shift_of(p.cache.page_size);
     p.out = out;
     p.lse = lse;
     p.workspace = workspace;
@@ -255,6 +270,129 @@ int ck_paged_attention(const void* q, int64_t q_stride, const ck_kv_cache_t* cac
     ProfScope ps(kProfAttention, paged_attention_launches(p), s);
     const cudaError_t e = launch_paged_attention(p, dev, s);
     return e == cudaSuccess ? CK_OK : cuda_fail(e, "ck_paged_attention launch");
+}
+
+size_t ck_prefix_attention_workspace_size(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                                          int64_t num_prefixes, int64_t max_prefix_len, int64_t max_len)
+{
+    if (batch < 0 || num_prefixes < 1 || max_prefix_len < 0 || max_len < 0 || q_heads < 1 || kv_heads < 1 || head_dim < 1 ||
+        q_heads > 65536 || kv_heads > 65536 || head_dim > 256 || max_prefix_len > kMaxCount || max_len > kMaxCount)
+        return 0;
+    return paged_attention_workspace((int)(q_heads / kv_heads), (int)head_dim, max_prefix_len + max_len);
+}
+
+int ck_prefix_attention(const void* q, int64_t q_stride, const ck_kv_cache_t* cache, const int32_t* prefix_table,
+                        int64_t max_prefix_blocks, const int32_t* prefix_lens, const int32_t* cu_prefix,
+                        int64_t num_prefixes, const int32_t* block_table, int64_t max_blocks, const int32_t* seq_lens,
+                        int64_t batch, int64_t q_heads, int dtype, float scale, void* out, float* lse, void* workspace,
+                        size_t workspace_bytes, void* stream)
+{
+    CK_CHECK(check_dtype(dtype));
+    if (cache == nullptr)
+        return fail(CK_ERR_INVALID_ARG, "cache must not be NULL");
+    CK_CHECK(check_heads(q_heads, cache->kv_heads));
+    CK_CHECK(check_attention_dim(cache->head_dim));
+    CK_CHECK(check_stride("q_stride", q_stride, q_heads * cache->head_dim));
+    if (!std::isfinite(scale))
+        return fail(CK_ERR_INVALID_ARG, "scale must be finite");
+    if (batch < 0 || batch > kMaxCount / q_heads)
+        return fail(CK_ERR_INVALID_ARG, "batch must be >= 0 and batch * q_heads below 2^31 (got batch=%lld)",
+                    (long long)batch);
+    if (num_prefixes < 1 || num_prefixes > 65536)
+        return fail(CK_ERR_INVALID_ARG, "num_prefixes must be in 1..65536 (got %lld)", (long long)num_prefixes);
+    if (max_blocks < 1 || max_prefix_blocks < 1 || cache->page_size < 1 || cache->page_size > kMaxCount ||
+        max_blocks > kMaxCount / cache->page_size || max_prefix_blocks > kMaxCount / cache->page_size - max_blocks)
+        return fail(CK_ERR_INVALID_ARG,
+                    "max_blocks, max_prefix_blocks and page_size must be >= 1, the keys that both tables name below 2^31 "
+                    "(got %lld, %lld, %lld)",
+                    (long long)max_blocks, (long long)max_prefix_blocks, (long long)cache->page_size);
+    PagedAttention p{};
+    if (batch == 0)
+        return CK_OK;
+    CK_CHECK(check_cache(cache, cache->kv_heads, cache->head_dim, dtype, &p.cache));
+    CK_REQUIRE_PTR(q);
+    CK_REQUIRE_INDEX(prefix_table);
+    CK_REQUIRE_INDEX(prefix_lens);
+    CK_REQUIRE_INDEX(cu_prefix);
+    CK_REQUIRE_INDEX(block_table);
+    CK_REQUIRE_INDEX(seq_lens);
+    CK_REQUIRE_PTR(out);
+    CK_OPTIONAL_PTR(lse);
+    const size_t need = ck_prefix_attention_workspace_size(batch, q_heads, p.cache.heads, p.cache.dim, num_prefixes,
+                                                           max_prefix_blocks * p.cache.page_size,
+                                                           max_blocks * p.cache.page_size);
+    if (need > 0) {
+        CK_REQUIRE_PTR(workspace);
+        if (workspace_bytes < need)
+            return fail(CK_ERR_INVALID_ARG, "workspace too small: %zu bytes given, %zu needed", workspace_bytes, need);
+    }
+    DeviceInfo dev;
+    CK_CHECK(check_device(&dev));
+    p.q = q;
+    p.q_stride = q_stride;
+    p.block_table = block_table;
+    p.max_blocks = max_blocks;
+    p.seq_lens = seq_lens;
+    p.batch = batch;
+    p.q_heads = (int)q_heads;
+    p.f16 = dtype == CK_OUT_F16;
+    p.scale = scale;
+    p.page_shift = page_shift_of(p.cache.page_size);
+    p.out = out;
+    p.lse = lse;
+    p.workspace = workspace;
+    p.shared.table = prefix_table;
+    p.shared.max_blocks = max_prefix_blocks;
+    p.shared.lens = prefix_lens;
+    p.shared.cu = cu_prefix;
+    p.shared.count = num_prefixes;
+    p.shared.max_len = max_prefix_blocks * p.cache.page_size;
+    log_shape("prefix_attention", batch, q_heads, p.cache.dim, p.cache.dtype, "keys of a group's prefix and its own");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    ProfScope ps(kProfAttention, paged_attention_launches(p), s);
+    const cudaError_t e = launch_paged_attention(p, dev, s);
+    return e == cudaSuccess ? CK_OK : cuda_fail(e, "ck_prefix_attention launch");
+}
+
+int ck_cache_read(const ck_kv_cache_t* cache, const int32_t* block_table, int64_t max_blocks, const int32_t* cu,
+                  int64_t batch, int64_t total, int dtype, void* k_out, void* v_out, void* stream)
+{
+    CK_CHECK(check_dtype(dtype));
+    if (cache == nullptr)
+        return fail(CK_ERR_INVALID_ARG, "cache must not be NULL");
+    if (cache->kv_heads < 1 || cache->kv_heads > 65536)
+        return fail(CK_ERR_INVALID_ARG, "kv_heads must be in 1..65536 (got %lld)", (long long)cache->kv_heads);
+    if (cache->head_dim < 8 || cache->head_dim > 256 || cache->head_dim % 8 != 0)
+        return fail(CK_ERR_INVALID_ARG, "head_dim must be a multiple of 8 in 8..256 (got %lld)",
+                    (long long)cache->head_dim);
+    if (batch < 0 || batch > kMaxCount || total < 0 || total > kMaxCount)
+        return fail(CK_ERR_INVALID_ARG, "batch and total must be in 0..2^31-1 (got %lld and %lld)", (long long)batch,
+                    (long long)total);
+    if (max_blocks < 1 || max_blocks > kMaxCount)
+        return fail(CK_ERR_INVALID_ARG, "max_blocks must be in 1..2^31-1 (got %lld)", (long long)max_blocks);
+    if (batch == 0 || total == 0)
+        return CK_OK;
+    CacheRead p{};
+    CK_CHECK(check_cache(cache, cache->kv_heads, cache->head_dim, dtype, &p.cache));
+    CK_REQUIRE_INDEX(block_table);
+    CK_REQUIRE_INDEX(cu);
+    CK_REQUIRE_PTR(k_out);
+    CK_REQUIRE_PTR(v_out);
+    DeviceInfo dev;
+    CK_CHECK(check_device(&dev));
+    p.block_table = block_table;
+    p.max_blocks = max_blocks;
+    p.cu = cu;
+    p.batch = batch;
+    p.total = total;
+    p.f16 = dtype == CK_OUT_F16;
+    p.k_out = k_out;
+    p.v_out = v_out;
+    log_shape("cache_read", total, p.cache.heads, p.cache.dim, p.cache.dtype, "one pass");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    ProfScope ps(kProfCacheRead, 1, s);
+    const cudaError_t e = launch_cache_read(p, dev, s);
+    return e == cudaSuccess ? CK_OK : cuda_fail(e, "ck_cache_read launch");
 }
 
 int ck_attention(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
@@ -328,6 +466,140 @@ int ck_attention(const void* q, int64_t q_stride, const void* k, int64_t k_strid
     return CK_OK;
 }
 
+size_t ck_adapter_linear_workspace_size(int64_t M, int64_t N, int64_t K, int64_t rank)
+{
+    if (M < 0 || N < 1 || K < 1 || rank < 1 || rank > 256 || M > kMaxCount || N > kMaxCount || K > kMaxCount)
+        return 0;
+    return adapter_workspace(M, N, K, (int)rank);
+}
+
+int ck_adapter_linear(const void* x, const void* a, const void* b, const int32_t* index, const float* scaling,
+                      const void* residual, void* y, int64_t M, int64_t N, int64_t K, int64_t rank, int64_t num_adapters,
+                      int dtype, int out_dtype, void* workspace, size_t workspace_bytes, void* stream)
+{
+    CK_CHECK(check_dtype(dtype));
+    CK_CHECK(check_out_dtype(out_dtype));
+    if (N < 1 || K < 1 || N > kMaxCount || K > kMaxCount || N % 8 != 0 || K % 16 != 0)
+        return fail(CK_ERR_INVALID_ARG, "N must be a multiple of 8 and K of 16, both in 1..2^31-1 (got N=%lld K=%lld)",
+                    (long long)N, (long long)K);
+    if (rank < 8 || rank > 128 || rank % 8 != 0)
+        return fail(CK_ERR_INVALID_ARG, "rank must be a multiple of 8 in 8..128 (got %lld)", (long long)rank);
+    if (num_adapters < 0 || num_adapters > kMaxCount)
+        return fail(CK_ERR_INVALID_ARG, "num_adapters must be in 0..2^31-1 (got %lld)", (long long)num_adapters);
+    if (M < 0 || M > (1 << 24))
+        return fail(CK_ERR_INVALID_ARG, "M must be in 0..16777216 (got %lld)", (long long)M);
+    if (M == 0)
+        return CK_OK;
+    CK_REQUIRE_PTR(x);
+    if (num_adapters > 0) {
+        CK_REQUIRE_PTR(a);
+        CK_REQUIRE_PTR(b);
+    }
+    CK_REQUIRE_INDEX(index);
+    if (scaling != nullptr)
+        CK_REQUIRE_INDEX(scaling);
+    CK_OPTIONAL_PTR(residual);
+    CK_REQUIRE_PTR(y);
+    const size_t need = adapter_workspace(M, N, K, (int)rank);
+    if (need > 0) {
+        CK_REQUIRE_PTR(workspace);
+        if (workspace_bytes < need)
+            return fail(CK_ERR_INVALID_ARG, "workspace too small: %zu bytes given, %zu needed", workspace_bytes, need);
+    }
+    DeviceInfo dev;
+    CK_CHECK(check_device(&dev));
+    AdapterLinear p{};
+    p.x = x;
+    p.a = a;
+    p.b = b;
+    p.index = index;
+    p.scaling = scaling;
+    p.residual = residual;
+    p.y = y;
+    p.M = M;
+    p.N = N;
+    p.K = K;
+    p.adapters = num_adapters;
+    p.rank = (int)rank;
+    p.f16 = dtype == CK_OUT_F16;
+    p.out_dtype = out_dtype;
+    p.workspace = workspace;
+    log_shape("adapter_linear", M, N, K, (int)rank, "two low-rank products");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    ProfScope ps(kProfAdapter, 2, s);
+    const cudaError_t e = launch_adapter_linear(p, dev, s);
+    return e == cudaSuccess ? CK_OK : cuda_fail(e, "ck_adapter_linear launch");
+}
+
+size_t ck_token_logprobs_workspace_size(int64_t rows, int64_t vocab, int64_t top)
+{
+    if (rows < 0 || vocab < 1 || top < 0 || top > 32 || rows > kMaxCount || vocab > kMaxCount)
+        return 0;
+    return logprobs_workspace(rows, vocab, (int)top);
+}
+
+int ck_token_logprobs(const void* logits, int64_t stride, const int32_t* tokens, int64_t rows, int64_t vocab, int dtype,
+                      float scale, int64_t top, float* logprob, float* entropy, float* lse, float* top_logprob,
+                      int32_t* top_index, void* workspace, size_t workspace_bytes, void* stream)
+{
+    if (dtype != CK_OUT_BF16 && dtype != CK_OUT_F16 && dtype != CK_OUT_F32)
+        return fail(CK_ERR_INVALID_ARG, "dtype must be 0 (bf16), 1 (fp16) or 2 (fp32), got %d", dtype);
+    if (rows < 0 || rows > kMaxCount || vocab < 1 || vocab > kMaxCount)
+        return fail(CK_ERR_INVALID_ARG, "rows must be in 0..2^31-1 and vocab in 1..2^31-1 (got %lld and %lld)",
+                    (long long)rows, (long long)vocab);
+    if (stride < vocab)
+        return fail(CK_ERR_INVALID_ARG, "stride must be at least vocab (got stride=%lld vocab=%lld)", (long long)stride,
+                    (long long)vocab);
+    if (top < 0 || top > 32 || top > vocab)
+        return fail(CK_ERR_INVALID_ARG, "top must be in 0..32 and at most vocab (got %lld)", (long long)top);
+    if (!(scale > 0.0f && std::isfinite(scale)))
+        return fail(CK_ERR_INVALID_ARG, "scale must be finite and > 0");
+    if (rows == 0)
+        return CK_OK;
+    if (logits == nullptr || reinterpret_cast<uintptr_t>(logits) % (dtype == CK_OUT_F32 ? 4 : 2) != 0)
+        return fail(CK_ERR_INVALID_ARG, "logits must not be NULL, and aligned like its elements");
+    if (logprob != nullptr) {
+        CK_REQUIRE_INDEX(tokens);
+        CK_REQUIRE_INDEX(logprob);
+    }
+    if (entropy != nullptr)
+        CK_REQUIRE_INDEX(entropy);
+    if (lse != nullptr)
+        CK_REQUIRE_INDEX(lse);
+    if (top > 0) {
+        CK_REQUIRE_INDEX(top_logprob);
+        CK_REQUIRE_INDEX(top_index);
+    }
+    const size_t need = logprobs_workspace(rows, vocab, (int)top);
+    if (need > 0) {
+        CK_REQUIRE_PTR(workspace);
+        if (workspace_bytes < need)
+            return fail(CK_ERR_INVALID_ARG, "workspace too small: %zu bytes given, %zu needed", workspace_bytes, need);
+    }
+    DeviceInfo dev;
+    CK_CHECK(check_device(&dev));
+    TokenLogprobs p{};
+    p.logits = logits;
+    p.stride = stride;
+    p.tokens = tokens;
+    p.rows = rows;
+    p.vocab = vocab;
+    p.dtype = dtype;
+    p.scale = scale;
+    p.top = (int)top;
+    p.logprob = logprob;
+    p.entropy = entropy;
+    p.lse = lse;
+    p.top_logprob = top_logprob;
+    p.top_index = top_index;
+    p.workspace = workspace;
+    log_shape("token_logprobs", rows, vocab, top, dtype, "rows of logits");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    ProfScope ps(kProfLogprobs, logprobs_launches(p, dev), s);
+    const cudaError_t e = launch_token_logprobs(p, dev, s);
+    return e == cudaSuccess ? CK_OK : cuda_fail(e, "ck_token_logprobs launch");
+}
+
 static int check_int4_shape(int64_t N, int64_t K)
 {
     if (N < 1 || K < 1 || N > kMaxCount || K > kMaxCount)
@@ -384,8 +656,7 @@ int ck_int4_linear(const void* x, const uint32_t* w4, const void* w_scale, const
                    void* y, int64_t M, int64_t N, int64_t K, int64_t group, int dtype, int out_dtype, void* stream)
 {
     CK_CHECK(check_dtype(dtype));
-    if (out_dtype != CK_OUT_BF16 && out_dtype != CK_OUT_F16 && out_dtype != CK_OUT_F32)
-        return fail(CK_ERR_INVALID_ARG, "out_dtype must be 0 (bf16), 1 (fp16) or 2 (fp32), got %d", out_dtype);
+    CK_CHECK(check_out_dtype(out_dtype));
     CK_CHECK(check_int4_shape(N, K));
     CK_CHECK(check_group(group, K));
     if (M < 0 || M > (1 << 19))

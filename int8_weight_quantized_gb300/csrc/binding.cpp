@@ -22,6 +22,13 @@ decltype(&ck_paged_attention_workspace_size) p_paged_ws = nullptr;
 decltype(&ck_paged_attention) p_paged = nullptr;
 decltype(&ck_attention) p_attention = nullptr;
 decltype(&ck_int4_linear) p_int4 = nullptr;
+decltype(&ck_prefix_attention_workspace_size) p_prefix_ws = nullptr;
+decltype(&ck_prefix_attention) p_prefix = nullptr;
+decltype(&ck_cache_read) p_cache_read = nullptr;
+decltype(&ck_adapter_linear_workspace_size) p_adapter_ws = nullptr;
+decltype(&ck_adapter_linear) p_adapter = nullptr;
+decltype(&ck_token_logprobs_workspace_size) p_logprobs_ws = nullptr;
+decltype(&ck_token_logprobs) p_logprobs = nullptr;
 
 // A Python exception to raise, thrown through the checks.
 struct Raise {
@@ -242,15 +249,22 @@ PyObject* guarded(const char* name, Py_ssize_t got, Py_ssize_t want, Fn fn)
 
 PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
-    return guarded("init", n, 5, [&]() -> PyObject* {
-        void* f[5];
-        for (int i = 0; i < 5; ++i)
+    return guarded("init", n, 12, [&]() -> PyObject* {
+        void* f[12];
+        for (int i = 0; i < 12; ++i)
             f[i] = reinterpret_cast<void*>(static_cast<intptr_t>(integer(a[i], "address")));
         p_norm_rope = reinterpret_cast<decltype(p_norm_rope)>(f[0]);
         p_paged_ws = reinterpret_cast<decltype(p_paged_ws)>(f[1]);
         p_paged = reinterpret_cast<decltype(p_paged)>(f[2]);
         p_attention = reinterpret_cast<decltype(p_attention)>(f[3]);
         p_int4 = reinterpret_cast<decltype(p_int4)>(f[4]);
+        p_prefix_ws = reinterpret_cast<decltype(p_prefix_ws)>(f[5]);
+        p_prefix = reinterpret_cast<decltype(p_prefix)>(f[6]);
+        p_cache_read = reinterpret_cast<decltype(p_cache_read)>(f[7]);
+        p_adapter_ws = reinterpret_cast<decltype(p_adapter_ws)>(f[8]);
+        p_adapter = reinterpret_cast<decltype(p_adapter)>(f[9]);
+        p_logprobs_ws = reinterpret_cast<decltype(p_logprobs_ws)>(f[10]);
+        p_logprobs = reinterpret_cast<decltype(p_logprobs)>(f[11]);
         Py_RETURN_NONE;
     });
 }
@@ -379,6 +393,116 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n)
     });
 }
 
+// A workspace of `bytes` bytes, or the caller's own (whose size the library checks).
+void* workspace_of(PyObject* given, size_t* bytes, const at::Tensor& like, at::Tensor* ws)
+{
+    if (given != Py_None) {
+        *ws = tensor(given, "ws");
+        require(*ws, at::kByte, {ws->numel()}, "ws");
+        *bytes = (size_t)ws->numel();
+    } else if (*bytes > 0) {
+        *ws = empty({(int64_t)*bytes}, at::kByte, like);
+    }
+    return ws->defined() ? ws->data_ptr() : nullptr;
+}
+
+// q, cache k, v, k_scale, v_scale, prefix_table, prefix_lens, cu_prefix, block_table, seq_lens, scale, out,
+// lse, return_lse, ws -> out, or (out, lse)
+PyObject* prefix_attention(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return guarded("prefix_attention", n, 15, [&]() -> PyObject* {
+        const at::Tensor& q = tensor(a[0], "q");
+        const int dtype = act_type(q, "q");
+        const at::ScalarType type = q.scalar_type();
+        const int64_t dim = q.dim() == 3 ? q.size(2) : 0;
+        const int64_t stride = token_stride(q, type, dim, "q");
+        const int64_t batch = q.size(0), heads = q.size(1);
+        const Cache cache = cache_of(a[1], a[2], a[3], a[4]);
+        if (!cache.there)
+            type_error("cache must be a KVCache");
+        if (cache.c.head_dim != dim)
+            value_error("q has heads of " + std::to_string(dim) + " values, the cache of " + std::to_string(cache.c.head_dim));
+        const at::Tensor &ptable = tensor(a[5], "prefix_table"), &plens = tensor(a[6], "prefix_lens"),
+                         &cu = tensor(a[7], "cu_prefix"), &table = tensor(a[8], "block_table"),
+                         &lens = tensor(a[9], "seq_lens");
+        const int64_t prefixes = ptable.dim() == 2 ? ptable.size(0) : 0, pblocks = ptable.dim() == 2 ? ptable.size(1) : 0;
+        const int64_t blocks = table.dim() == 2 ? table.size(1) : 0;
+        require(ptable, at::kInt, {prefixes, pblocks}, "prefix_table");
+        require(plens, at::kInt, {prefixes}, "prefix_lens");
+        require(cu, at::kInt, {prefixes + 1}, "cu_prefix");
+        require(table, at::kInt, {batch, blocks}, "block_table");
+        require(lens, at::kInt, {batch}, "seq_lens");
+        at::Tensor out, lse, ws;
+        if (a[11] == Py_None)
+            out = empty({batch, heads, dim}, type, q);
+        else
+            require(out = tensor(a[11], "out"), type, {batch, heads, dim}, "out");
+        const bool return_lse = truth(a[13]);
+        if (a[12] != Py_None)
+            require(lse = tensor(a[12], "lse"), at::kFloat, {batch, heads}, "lse");
+        else if (return_lse)
+            lse = empty({batch, heads}, at::kFloat, q);
+        const int64_t most = cache.c.page_size > 0 ? (int64_t(1) << 31) / cache.c.page_size : 0;
+        size_t ws_bytes = blocks < most && pblocks < most
+                              ? p_prefix_ws(batch, heads, cache.c.kv_heads, dim, prefixes, pblocks * cache.c.page_size,
+                                            blocks * cache.c.page_size)
+                              : 0;
+        void* ws_ptr = workspace_of(a[14], &ws_bytes, q, &ws);
+        const float scale = a[10] == Py_None ? (float)(1.0 / std::sqrt((double)std::max<int64_t>(dim, 1)))
+                                             : (float)number(a[10], "scale");
+        const int st = p_prefix(q.data_ptr(), stride, &cache.c, ptable.data_ptr<int32_t>(), pblocks,
+                                plens.data_ptr<int32_t>(), cu.data_ptr<int32_t>(), prefixes, table.data_ptr<int32_t>(), blocks,
+                                lens.data_ptr<int32_t>(), batch, heads, dtype, scale, out.data_ptr(),
+                                lse.defined() ? lse.data_ptr<float>() : nullptr, ws_ptr, ws_bytes, current_stream(q));
+        if (st != CK_OK)
+            return PyLong_FromLong(st);
+        PyObject* o = given_or(a[11], out);
+        if (!return_lse)
+            return o;
+        PyObject* l = given_or(a[12], lse);
+        PyObject* r = PyTuple_Pack(2, o, l);
+        Py_DECREF(o);
+        Py_DECREF(l);
+        return r;
+    });
+}
+
+// cache k, v, k_scale, v_scale, block_table, cu, total, dtype, k, v -> (k, v)
+PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return guarded("cache_read", n, 10, [&]() -> PyObject* {
+        const Cache cache = cache_of(a[0], a[1], a[2], a[3]);
+        if (!cache.there)
+            type_error("cache must be a KVCache");
+        const at::Tensor &of = tensor(a[0], "k"), &table = tensor(a[4], "block_table"), &cu = tensor(a[5], "cu");
+        if (table.dim() != 2)
+            value_error("block_table must have shape [batch, max_blocks], got " + shape_text(table.sizes()));
+        const int64_t batch = table.size(0), blocks = table.size(1);
+        require(table, at::kInt, {batch, blocks}, "block_table");
+        require(cu, at::kInt, {batch + 1}, "cu");
+        const int64_t total = integer(a[6], "total");
+        if (total < 0)
+            value_error("total must be >= 0, got " + std::to_string(total));
+        const int dtype = (int)integer(a[7], "dtype");
+        const at::ScalarType type = dtype == CK_OUT_F16 ? at::kHalf : at::kBFloat16;
+        at::Tensor out[2];
+        for (int i = 0; i < 2; ++i)
+            if (a[8 + i] == Py_None)
+                out[i] = empty({total, cache.c.kv_heads, cache.c.head_dim}, type, of);
+            else
+                require(out[i] = tensor(a[8 + i], i ? "v" : "k"), type, {total, cache.c.kv_heads, cache.c.head_dim}, i ? "v" : "k");
+        const int st = p_cache_read(&cache.c, table.data_ptr<int32_t>(), blocks, cu.data_ptr<int32_t>(), batch, total, dtype,
+                                    out[0].data_ptr(), out[1].data_ptr(), current_stream(of));
+        if (st != CK_OK)
+            return PyLong_FromLong(st);
+        PyObject *k = given_or(a[8], out[0]), *v = given_or(a[9], out[1]);
+        PyObject* r = PyTuple_Pack(2, k, v);
+        Py_DECREF(k);
+        Py_DECREF(v);
+        return r;
+    });
+}
+
 // q, k, v, cu_q, cu_k, scale, causal, window, sinks, out, lse, return_lse -> out, or (out, lse)
 PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
@@ -464,6 +588,110 @@ PyObject* int4_linear(PyObject*, PyObject* const* a, Py_ssize_t n)
     });
 }
 
+at::ScalarType type_of(int code)
+{
+    return code == CK_OUT_BF16 ? at::kBFloat16 : code == CK_OUT_F16 ? at::kHalf : at::kFloat;
+}
+
+// a ck_dtype_t, -1 for other types
+int code_of(at::ScalarType t)
+{
+    return t == at::kBFloat16 ? CK_OUT_BF16 : t == at::kHalf ? CK_OUT_F16 : t == at::kFloat ? CK_OUT_F32 : -1;
+}
+
+// x, a, b, index, scaling, residual, y, out_dtype (a ck_dtype_t, or -1: the residual's, else x's), ws -> y
+PyObject* adapter_linear(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return guarded("adapter_linear", n, 9, [&]() -> PyObject* {
+        const at::Tensor &x = tensor(a[0], "x"), &down = tensor(a[1], "a"), &up = tensor(a[2], "b"),
+                         &index = tensor(a[3], "index");
+        const int dtype = act_type(x, "x");
+        const at::ScalarType type = x.scalar_type();
+        if (x.dim() != 2 || down.dim() != 3 || up.dim() != 3)
+            value_error("x must have shape [M, K], a [adapters, rank, K] and b [adapters, N, rank], got " +
+                        shape_text(x.sizes()) + ", " + shape_text(down.sizes()) + " and " + shape_text(up.sizes()));
+        const int64_t M = x.size(0), K = x.size(1), adapters = down.size(0), rank = down.size(1), N = up.size(1);
+        require(x, type, {M, K}, "x");
+        require(down, type, {adapters, rank, K}, "a");
+        require(up, type, {adapters, N, rank}, "b");
+        require(index, at::kInt, {M}, "index");
+        const at::Tensor *scaling = optional_tensor(a[4], "scaling"), *residual = optional_tensor(a[5], "residual");
+        if (scaling)
+            require(*scaling, at::kFloat, {adapters}, "scaling");
+        const int64_t code = integer(a[7], "out_dtype");
+        const int out_code = code >= 0 ? (int)code : residual ? code_of(residual->scalar_type()) : dtype;
+        if (out_code < 0)
+            type_error(std::string("residual must be torch.bfloat16, torch.float16 or torch.float32, got ") +
+                       type_name(residual->scalar_type()));
+        if (residual)
+            require(*residual, type_of(out_code), {M, N}, "residual");
+        at::Tensor y, ws;
+        if (a[6] == Py_None)
+            y = empty({M, N}, type_of(out_code), x);
+        else
+            require(y = tensor(a[6], "y"), type_of(out_code), {M, N}, "y");
+        size_t ws_bytes = p_adapter_ws(M, N, K, rank);
+        void* ws_ptr = workspace_of(a[8], &ws_bytes, x, &ws);
+        const int st = p_adapter(x.data_ptr(), down.data_ptr(), up.data_ptr(), index.data_ptr<int32_t>(),
+                                 static_cast<const float*>(ptr(scaling)), ptr(residual), y.data_ptr(), M, N, K, rank, adapters,
+                                 dtype, out_code, ws_ptr, ws_bytes, current_stream(x));
+        if (st != CK_OK)
+            return PyLong_FromLong(st);
+        return given_or(a[6], y);
+    });
+}
+
+// logits, tokens, top, scale, logprob, entropy, lse, top_logprob, top_index, ws -> the five outputs
+PyObject* token_logprobs(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return guarded("token_logprobs", n, 10, [&]() -> PyObject* {
+        const at::Tensor& x = tensor(a[0], "logits");
+        const int dtype = code_of(x.scalar_type());
+        if (dtype < 0)
+            type_error(std::string("logits must be torch.bfloat16, torch.float16 or torch.float32, got ") +
+                       type_name(x.scalar_type()));
+        if (x.dim() != 2 || !x.is_cuda() || (x.stride(1) != 1 && x.size(1) > 1))
+            value_error("logits must be a CUDA tensor [rows, vocab] with dense rows, got " + shape_text(x.sizes()));
+        const int64_t rows = x.size(0), vocab = x.size(1), top = integer(a[2], "top");
+        const at::Tensor* tokens = optional_tensor(a[1], "tokens");
+        if (tokens)
+            require(*tokens, at::kInt, {rows}, "tokens");
+        const bool wanted[5] = {tokens != nullptr, true, true, top > 0, top > 0};
+        static const char* const names[5] = {"logprob", "entropy", "lse", "top", "index"};
+        bool given = false;
+        for (int i = 0; i < 5; ++i)
+            given |= a[4 + i] != Py_None;
+        at::Tensor out[5], ws;
+        for (int i = 0; i < 5; ++i) {
+            const at::ScalarType type = i == 4 ? at::kInt : at::kFloat;
+            const int64_t shape[2] = {rows, top};
+            const c10::IntArrayRef sizes(shape, i < 3 ? 1 : 2);
+            if (a[4 + i] != Py_None) {
+                if (!wanted[i])
+                    value_error(std::string(names[i]) + " is given, but not asked for");
+                require(out[i] = tensor(a[4 + i], names[i]), type, sizes, names[i]);
+            } else if (wanted[i] && !given && top <= 32) {
+                out[i] = empty(sizes, type, x);
+            } else if (i >= 3 && wanted[i] && given) {
+                value_error("top and index must be given where out is and top > 0");
+            }
+        }
+        size_t ws_bytes = p_logprobs_ws(rows, vocab, top);
+        void* ws_ptr = workspace_of(a[9], &ws_bytes, x, &ws);
+        auto f32 = [&](int i) { return out[i].defined() ? out[i].data_ptr<float>() : nullptr; };
+        const int st = p_logprobs(x.data_ptr(), rows > 1 ? x.stride(0) : vocab, tokens ? tokens->data_ptr<int32_t>() : nullptr,
+                                  rows, vocab, dtype, (float)number(a[3], "scale"), top, f32(0), f32(1), f32(2), f32(3),
+                                  out[4].defined() ? out[4].data_ptr<int32_t>() : nullptr, ws_ptr, ws_bytes,
+                                  current_stream(x));
+        if (st != CK_OK)
+            return PyLong_FromLong(st);
+        PyObject* r = PyTuple_New(5);
+        for (int i = 0; i < 5; ++i)
+            PyTuple_SET_ITEM(r, i, a[4 + i] == Py_None && !out[i].defined() ? Py_NewRef(Py_None) : given_or(a[4 + i], out[i]));
+        return r;
+    });
+}
+
 #define CK_FAST(fn) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(fn))
 
 PyMethodDef methods[] = {{"init", CK_FAST(init), METH_FASTCALL, nullptr},
@@ -471,6 +699,10 @@ PyMethodDef methods[] = {{"init", CK_FAST(init), METH_FASTCALL, nullptr},
                          {"paged_attention", CK_FAST(paged_attention), METH_FASTCALL, nullptr},
                          {"attention", CK_FAST(attention), METH_FASTCALL, nullptr},
                          {"int4_linear", CK_FAST(int4_linear), METH_FASTCALL, nullptr},
+                         {"prefix_attention", CK_FAST(prefix_attention), METH_FASTCALL, nullptr},
+                         {"cache_read", CK_FAST(cache_read), METH_FASTCALL, nullptr},
+                         {"adapter_linear", CK_FAST(adapter_linear), METH_FASTCALL, nullptr},
+                         {"token_logprobs", CK_FAST(token_logprobs), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_ck_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

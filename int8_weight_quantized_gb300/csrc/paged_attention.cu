@@ -96,16 +96,33 @@ struct Shape {
 };
 
 // ---- the division of work, the same in both kernels
+// PREFIX: a sequence's keys are those of the prefix that its group shares, then its own.
+template <bool PREFIX>
 struct Lengths {
     const int32_t* seq_lens;
     int64_t max_len, window, sinks;
     int subs;  // segments of a sequence
     int tile;  // keys of a tile
-    __device__ int length(int64_t b, bool* bad) const
+    SharedPrefixes shared;
+    bool bad_groups;  // the groups' bounds are out of range: no sequence has keys
+    // keys of sequence b; those of its prefix and the prefix's row in the table
+    __device__ int length(int64_t b, bool* bad, int* prefix_keys, int* prefix) const
     {
         const int64_t n = __ldg(seq_lens + b);
         *bad = n < 0 || n > max_len;
+        if constexpr (PREFIX) {
+            *prefix = bad_groups ? -1 : shared.of(b);
+            const int64_t m = *prefix < 0 ? 0 : __ldg(shared.lens + *prefix);
+            *bad |= bad_groups || m < 0 || m > shared.max_len;
+            *prefix_keys = *bad ? 0 : (int)m;
+            return *bad ? 0 : (int)(n + m);
+        }
         return *bad ? 0 : (int)n;
+    }
+    __device__ int length(int64_t b, bool* bad) const
+    {
+        int keys, prefix;
+        return length(b, bad, &keys, &prefix);
     }
     __device__ int tiles(int64_t b) const
     {
@@ -114,8 +131,18 @@ struct Lengths {
     }
 };
 
+template <bool PREFIX>
+__device__ __forceinline__ Lengths<PREFIX> lengths_of(const PagedAttention& p, int subs, int tile)
+{
+    Lengths<PREFIX> L{p.seq_lens, p.max_blocks * p.cache.page_size, p.window, p.sinks, subs, tile, p.shared, false};
+    if constexpr (PREFIX)
+        L.bad_groups = p.shared.bad_groups(p.batch);
+    return L;
+}
+
 // By a whole warp: tiles of all segments before sequence `upto`.
-__device__ __forceinline__ int64_t tiles_before(const Lengths& L, int64_t upto)
+template <class L_>
+__device__ __forceinline__ int64_t tiles_before(const L_& L, int64_t upto)
 {
     const int lane = threadIdx.x & 31;
     int64_t sum = 0;
@@ -133,7 +160,8 @@ __device__ __forceinline__ int64_t first_tile(int64_t c, int64_t C, int64_t T)
 }
 
 // By a whole warp: the sequence that holds tile `t` of all tiles, and the tiles before it.
-__device__ __forceinline__ int64_t sequence_at(const Lengths& L, int64_t batch, int64_t t, int64_t* before)
+template <class L_>
+__device__ __forceinline__ int64_t sequence_at(const L_& L, int64_t batch, int64_t t, int64_t* before)
 {
     const int lane = threadIdx.x & 31;
     int64_t base = 0;
@@ -159,18 +187,20 @@ __device__ __forceinline__ int64_t sequence_at(const Lengths& L, int64_t batch, 
 }
 
 // Walks the tiles of a block's range.
+template <bool PREFIX>
 struct Cursor {
     int64_t b;
     int sub, tile, tiles;
     int64_t left;  // tiles of the range from here on
     VisibleKeys keys;
-    __device__ void open(const Lengths& L)
+    int prefix_keys, prefix;  // PREFIX: keys of the sequence's prefix, its row in the table
+    __device__ void open(const Lengths<PREFIX>& L)
     {
         bool bad;
-        keys = visible_keys(L.length(b, &bad), L.window, L.sinks);
+        keys = visible_keys(L.length(b, &bad, &prefix_keys, &prefix), L.window, L.sinks);
         tiles = (keys.count() + L.tile - 1) / L.tile;
     }
-    __device__ void next(const Lengths& L)
+    __device__ void next(const Lengths<PREFIX>& L)
     {
         if (--left <= 0 || ++tile < tiles)
             return;
@@ -209,7 +239,7 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c)
     return (uint32_t)(r * Shape<INT8, DIM, 1>::ROW + p * 16);
 }
 
-template <class E, bool INT8, int DIM, int NT>
+template <class E, bool INT8, int DIM, int NT, bool PREFIX>
 __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
     paged_kernel(const PagedAttention p, int64_t C, bool split, unsigned int* err)
 {
@@ -224,7 +254,7 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
     const int group = p.q_heads / p.cache.heads;  // query heads per kv head
     const int qtiles = (group + HEADS - 1) / HEADS;
     const int page_size = p.cache.page_size;
-    Lengths L{p.seq_lens, p.max_blocks * page_size, p.window, p.sinks, p.cache.heads * qtiles, TILE};
+    const Lengths<PREFIX> L = lengths_of<PREFIX>(p, p.cache.heads * qtiles, TILE);
 
     // sequences without visible keys have no tiles: zeros, or NaN where the length is out of range
     for (int64_t b = blockIdx.x; b < p.batch; b += gridDim.x) {
@@ -242,7 +272,7 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
     }
 
     // this block's range of tiles
-    Cursor at;
+    Cursor<PREFIX> at;
     if (split) {
         const int64_t total = tiles_before(L, p.batch);
         C = min(C, total);  // no block of those that take part is without tiles
@@ -274,7 +304,7 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
     constexpr int RPI = 32 / CH;          // rows of one copy instruction
     const uint8_t* const k_lane = static_cast<const uint8_t*>(p.cache.k) + lane % CH * 16;
     const uint8_t* const v_lane = static_cast<const uint8_t*>(p.cache.v) + lane % CH * 16;
-    Cursor ahead = at;
+    Cursor<PREFIX> ahead = at;
     int32_t page = 0;
     int in_page = 0;
     bool have = false;
@@ -282,11 +312,18 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
         const int v = ahead.tile * TILE + warp * KEYS + lane % KEYS;
         have = ahead.left > 0 && v < ahead.keys.count();
         if (have) {
-            const int j = ahead.keys.key(v);
+            int j = ahead.keys.key(v);
+            const int32_t* row = p.block_table + ahead.b * p.max_blocks;
+            if constexpr (PREFIX) {
+                if (j < ahead.prefix_keys)
+                    row = p.shared.table + ahead.prefix * p.shared.max_blocks;
+                else
+                    j -= ahead.prefix_keys;
+            }
             // page_shift: the page size is that power of two; -1: it is none
             const int blk = p.page_shift >= 0 ? j >> p.page_shift : j / page_size;
             in_page = j - blk * page_size;
-            page = __ldg(p.block_table + ahead.b * p.max_blocks + blk);
+            page = __ldg(row + blk);
         }
     };
     uint32_t bad_units = 0;  // bit s: the unit in stage s has a page number out of range
@@ -701,7 +738,7 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
 
 // Adds up the partial sums of the segments that blocks share: one block per (sequence, query
 // head), its 4 warps every fourth part each, then the four together.
-template <class E, int DIM, int NT>
+template <class E, int DIM, int NT, bool PREFIX>
 __global__ void __launch_bounds__(128) join_kernel(const PagedAttention p, int64_t C, int tile)
 {
     using T = typename E::T;
@@ -715,7 +752,7 @@ __global__ void __launch_bounds__(128) join_kernel(const PagedAttention p, int64
     const int h = (int)(blockIdx.x - b * p.q_heads);
     const int group = p.q_heads / p.cache.heads;
     const int qtiles = (group + HEADS - 1) / HEADS;
-    Lengths L{p.seq_lens, p.max_blocks * p.cache.page_size, p.window, p.sinks, p.cache.heads * qtiles, tile};
+    const Lengths<PREFIX> L = lengths_of<PREFIX>(p, p.cache.heads * qtiles, tile);
     const int tiles = L.tiles(b);
     if (tiles == 0)
         return;  // the first kernel wrote it
@@ -793,12 +830,12 @@ constexpr int kMostBlocks = 152 * 3;  // of any device this library runs on
 // shortens.)
 int64_t longest_of(const PagedAttention& p)
 {
-    const int64_t longest = p.max_blocks * p.cache.page_size;
+    const int64_t longest = p.max_blocks * p.cache.page_size + p.shared.max_len;
     // (by a difference: the sum of a window and first tokens of any size could overflow)
     return p.window > 0 && p.sinks < longest && p.window < longest - p.sinks ? p.window + p.sinks : longest;
 }
 
-template <class E, bool INT8, int DIM, int NT>
+template <class E, bool INT8, int DIM, int NT, bool PREFIX>
 cudaError_t launch(const PagedAttention& p, const DeviceInfo& dev, unsigned int* err, cudaStream_t s)
 {
     using S = Shape<INT8, DIM, NT>;
@@ -807,7 +844,7 @@ cudaError_t launch(const PagedAttention& p, const DeviceInfo& dev, unsigned int*
     int done = 0;
     cudaError_t e = cache.get(&done, [](int* d) {
         *d = 1;
-        return cudaFuncSetAttribute(paged_kernel<E, INT8, DIM, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(paged_kernel<E, INT8, DIM, NT, PREFIX>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     (int)S::SMEM);
     });
     if (e != cudaSuccess)
@@ -819,18 +856,21 @@ cudaError_t launch(const PagedAttention& p, const DeviceInfo& dev, unsigned int*
     const bool split = longest > kWholeKeys;
     const int64_t most = std::min<int64_t>(kMostBlocks, (int64_t)dev.sm_count * S::BLOCKS);
     const int64_t blocks = split ? std::min(most, segments * tiles) : segments;
-    e = launch_pdl(paged_kernel<E, INT8, DIM, NT>, dim3((unsigned)blocks), dim3(WARPS * 32), S::SMEM, s, p, blocks, split,
-                   err);
+    e = launch_pdl(paged_kernel<E, INT8, DIM, NT, PREFIX>, dim3((unsigned)blocks), dim3(WARPS * 32), S::SMEM, s, p, blocks,
+                   split, err);
     if (e == cudaSuccess && split)
-        e = launch_pdl(join_kernel<E, DIM, NT>, dim3((unsigned)(p.batch * p.q_heads)), dim3(128), 0, s, p, blocks, S::TILE);
+        e = launch_pdl(join_kernel<E, DIM, NT, PREFIX>, dim3((unsigned)(p.batch * p.q_heads)), dim3(128), 0, s, p, blocks, S::TILE);
     return e;
 }
 
 template <class E, int DIM, int NT>
 cudaError_t by_cache(const PagedAttention& p, const DeviceInfo& dev, unsigned int* err, cudaStream_t s)
 {
-    return p.cache.dtype == CK_KV_INT8 ? launch<E, true, DIM, NT>(p, dev, err, s)
-                                       : launch<E, false, DIM, NT>(p, dev, err, s);
+    if (p.shared.count > 0)
+        return p.cache.dtype == CK_KV_INT8 ? launch<E, true, DIM, NT, true>(p, dev, err, s)
+                                           : launch<E, false, DIM, NT, true>(p, dev, err, s);
+    return p.cache.dtype == CK_KV_INT8 ? launch<E, true, DIM, NT, false>(p, dev, err, s)
+                                       : launch<E, false, DIM, NT, false>(p, dev, err, s);
 }
 
 template <int DIM>

@@ -1,6 +1,6 @@
 // transformer.h -- host-side interface between the C ABI (api_transformer.cu) and the kernels
-// of the operators around the linear layers: norm_rope.cu, paged_attention.cu, attention.cu,
-// int4.cu.  The public contract is include/ck_int8.h.
+// of the operators around the linear layers: norm_rope.cu, paged_attention.cu, cache_read.cu,
+// attention.cu, adapter.cu, logprobs.cu, int4.cu.  The public contract is include/ck_int8.h.
 #pragma once
 
 #include <cstddef>
@@ -46,6 +46,42 @@ struct NormRope {
 };
 cudaError_t launch_norm_rope(const NormRope& p, const DeviceInfo& dev, cudaStream_t s);
 
+// Groups of sequences that share the keys of a prefix (count == 0: there are none): sequences
+// cu[i] .. cu[i + 1] - 1 stand behind prefix i.
+struct SharedPrefixes {
+    const int32_t* table;  // [count, max_blocks] pages
+    int64_t max_blocks;
+    const int32_t* lens;   // [count]
+    const int32_t* cu;     // [count + 1]
+    int64_t count;
+    int64_t max_len;       // max_blocks * page_size
+#ifdef __CUDACC__
+    // the prefix of sequence b, -1: none (bounds ascending)
+    __device__ __forceinline__ int of(int64_t b) const
+    {
+        int64_t lo = -1, hi = count;  // the last bound <= b
+        while (lo < hi) {
+            const int64_t mid = (lo + hi + 1) >> 1;
+            if (__ldg(cu + mid) <= b)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        return lo == count ? -1 : (int)lo;
+    }
+    // by a whole warp: whether bounds descend or leave 0 .. batch
+    __device__ __forceinline__ bool bad_groups(int64_t batch) const
+    {
+        bool bad = false;
+        for (int64_t i = threadIdx.x & 31; i <= count; i += 32) {
+            const int64_t c = __ldg(cu + i);
+            bad |= c < 0 || c > batch || (i > 0 && c < __ldg(cu + i - 1));
+        }
+        return __any_sync(0xffffffffu, bad);
+    }
+#endif
+};
+
 struct PagedAttention {
     const void* q;
     int64_t q_stride;  // elements between sequences
@@ -62,11 +98,24 @@ struct PagedAttention {
     void* out;
     float* lse;  // or nullptr
     void* workspace;
+    SharedPrefixes shared;
 };
 // by query heads per kv head and the most keys a sequence can have
 size_t paged_attention_workspace(int group, int dim, int64_t max_len);
 int paged_attention_launches(const PagedAttention& p);  // kernels that the call enqueues
 cudaError_t launch_paged_attention(const PagedAttention& p, const DeviceInfo& dev, cudaStream_t s);
+
+// Rows of the cache back as contiguous 16-bit keys and values.
+struct CacheRead {
+    KvCache cache;
+    const int32_t* block_table;
+    int64_t max_blocks;
+    const int32_t* cu;  // [batch + 1] bounds of the sequences' rows
+    int64_t batch, total;
+    bool f16;
+    void *k_out, *v_out;  // [total, heads, dim]
+};
+cudaError_t launch_cache_read(const CacheRead& p, const DeviceInfo& dev, cudaStream_t s);
 
 struct PromptAttention {
     const void *q, *k, *v;
@@ -81,6 +130,38 @@ struct PromptAttention {
     float* lse;  // or nullptr
 };
 cudaError_t launch_attention(const PromptAttention& p, const DeviceInfo& dev, cudaStream_t s, std::string* why);
+
+struct AdapterLinear {
+    const void *x, *a, *b;   // [M, K], [adapters, rank, K], [adapters, N, rank]
+    const int32_t* index;    // [M], negative: none
+    const float* scaling;    // [adapters] or nullptr
+    const void* residual;    // out type [M, N] or nullptr
+    void* y;
+    int64_t M, N, K, adapters;
+    int rank;
+    bool f16;
+    int out_dtype;
+    void* workspace;
+};
+size_t adapter_workspace(int64_t M, int64_t N, int64_t K, int rank);
+cudaError_t launch_adapter_linear(const AdapterLinear& p, const DeviceInfo& dev, cudaStream_t s);
+
+struct TokenLogprobs {
+    const void* logits;
+    int64_t stride;         // elements between rows
+    const int32_t* tokens;  // [rows] or nullptr
+    int64_t rows, vocab;
+    int dtype;              // ck_dtype_t
+    float scale;
+    int top;
+    float *logprob, *entropy, *lse;  // [rows], each or nullptr
+    float* top_logprob;              // [rows, top]
+    int32_t* top_index;
+    void* workspace;
+};
+size_t logprobs_workspace(int64_t rows, int64_t vocab, int top);
+int logprobs_launches(const TokenLogprobs& p, const DeviceInfo& dev);  // kernels that the call enqueues
+cudaError_t launch_token_logprobs(const TokenLogprobs& p, const DeviceInfo& dev, cudaStream_t s);
 
 struct Int4Linear {
     const void* x;

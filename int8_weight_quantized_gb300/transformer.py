@@ -1,12 +1,14 @@
 """Binding of the operators around the linear layers: norms of queries and keys with the
-position rotation, the paged key-value cache, attention over it and over whole prompts, and
-the linear layer with 4-bit weights.
+position rotation, the paged key-value cache, attention over it (behind shared prefixes too) and
+over whole prompts, its rows read back, the linear layer with 4-bit weights, low-rank adapters, and
+log probabilities of tokens.
 
 As in the rest of the package the functions have the C names and only marshal arguments; the
 checks and allocations run in ``csrc/binding.cpp``.  Outputs and workspaces that the caller
 does not give come from torch's allocator on the stream that the work is enqueued on, so
 concurrent streams never share them.
 """
+import collections
 import ctypes
 import importlib.machinery
 import importlib.util
@@ -34,7 +36,9 @@ def _binding():
         loader.exec_module(module)
         module.init(*[ctypes.cast(getattr(L, n), ctypes.c_void_p).value
                       for n in ("ck_qk_norm_rope", "ck_paged_attention_workspace_size", "ck_paged_attention",
-                                "ck_attention", "ck_int4_linear")])
+                                "ck_attention", "ck_int4_linear", "ck_prefix_attention_workspace_size",
+                                "ck_prefix_attention", "ck_cache_read", "ck_adapter_linear_workspace_size",
+                                "ck_adapter_linear", "ck_token_logprobs_workspace_size", "ck_token_logprobs")])
         _b = module
     return _b
 
@@ -118,6 +122,41 @@ def ck_paged_attention(q, cache, block_table, seq_lens, scale=None, window=0, si
     return r
 
 
+def ck_prefix_attention(q, cache, prefix_table, prefix_lens, cu_prefix, block_table, seq_lens, scale=None, out=None,
+                        lse=None, return_lse=False, ws=None, stream=None):
+    """ck_paged_attention where sequences cu_prefix[i] .. cu_prefix[i + 1] - 1 (int32 [prefixes + 1]) also
+    see the prefix_lens[i] keys of prefix i, whose pages prefix_table int32 [prefixes, max_prefix_blocks]
+    names; block_table and seq_lens are each sequence's own tokens behind it."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return ck_prefix_attention(q, cache, prefix_table, prefix_lens, cu_prefix, block_table, seq_lens, scale, out,
+                                       lse, return_lse, ws)
+    r = (_b or _binding()).prefix_attention(q, cache.k, cache.v, cache.k_scale, cache.v_scale, prefix_table, prefix_lens,
+                                            cu_prefix, block_table, seq_lens, scale, out, lse, return_lse, ws)
+    if r.__class__ is int:
+        ck._check(r)
+    return r
+
+
+def ck_cache_read(cache, block_table, cu, total, dtype=None, k=None, v=None, stream=None):
+    """Cached rows as contiguous (k, v), each [total, kv_heads, head_dim] of dtype (that of `k` or of a
+    16-bit cache by default, else bf16): row cu[b] + t (cu int32 [batch + 1]) is token t of the sequence
+    whose pages block_table int32 [batch, max_blocks] names.  Rows that no sequence has are left as
+    they are (of new outputs: undefined)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return ck_cache_read(cache, block_table, cu, total, dtype, k, v)
+    if dtype is None:
+        dtype = k.dtype if k is not None else torch.bfloat16 if cache.k.dtype == torch.int8 else cache.k.dtype
+    if dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError("dtype must be torch.bfloat16 or torch.float16, got %s" % (dtype,))
+    r = (_b or _binding()).cache_read(cache.k, cache.v, cache.k_scale, cache.v_scale, block_table, cu, total,
+                                      ck.OUT_DTYPES[dtype], k, v)
+    if r.__class__ is int:
+        ck._check(r)
+    return r
+
+
 def ck_attention(q, k, v, cu_q, cu_k=None, scale=None, causal=True, window=0, sinks=0, out=None, lse=None,
                  return_lse=False, stream=None):
     """Attention over whole prompts: q [total_q, q_heads, head_dim], k and v [total_k, kv_heads,
@@ -175,3 +214,36 @@ def ck_int4_linear(x, w4, w_scale, bias=None, residual=None, y=None, out_dtype=N
     if r.__class__ is int:
         ck._check(r)
     return r
+
+
+def ck_adapter_linear(x, a, b, index, scaling=None, residual=None, y=None, out_dtype=None, ws=None, stream=None):
+    """y [M,N] of out_dtype (the residual's type by default, else x's) = residual + scaling[i] * (x[m] @ a[i].T)
+    @ b[i].T with i = index[m] (int32 [M]; negative: none), for x [M,K], a [adapters, rank, K] and
+    b [adapters, N, rank] of one 16-bit type, scaling fp32 [adapters]; residual may be y itself."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return ck_adapter_linear(x, a, b, index, scaling, residual, y, out_dtype, ws)
+    r = (_b or _binding()).adapter_linear(x, a, b, index, scaling, residual, y,
+                                          -1 if out_dtype is None else ck._out_code(out_dtype), ws)
+    if r.__class__ is int:
+        ck._check(r)
+    return r
+
+
+TokenLogprobs = collections.namedtuple("TokenLogprobs", "logprob entropy lse top index")
+TokenLogprobs.__doc__ = """What ck_token_logprobs returns: fp32 logprob (None without tokens), entropy and lse [rows],
+fp32 log probabilities `top` and int32 `index` [rows, top] of the likeliest tokens (None for top=0)."""
+
+
+def ck_token_logprobs(logits, tokens=None, top=0, scale=1.0, out=None, ws=None, stream=None):
+    """Log probabilities of tokens int32 [rows] (negative: none, 0) under softmax(scale * logits), logits
+    [rows, vocab] (bf16, fp16 or fp32; rows may be strided), with each row's entropy, log of the
+    softmax's sum and `top` likeliest tokens.  Returns a TokenLogprobs, `out` itself where it is given."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return ck_token_logprobs(logits, tokens, top, scale, out, ws)
+    given = (None,) * 5 if out is None else out
+    r = (_b or _binding()).token_logprobs(logits, tokens, top, scale, *given, ws)
+    if r.__class__ is int:
+        ck._check(r)
+    return TokenLogprobs(*r) if out is None else out

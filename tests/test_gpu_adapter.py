@@ -1,0 +1,231 @@
+"""Low-rank adapters of many requests at once, against the 64-bit definition.
+
+Bound of row m with adapter i, all sums in fp32: each low-rank value h_r is a K-term sum, off by
+(K + 8) 2^-24 sum_k |x a|, and rounded once to the type of x (relative to the row's largest value where
+that type is fp16, so that nothing overflows: 2^-25 of it at least); the product with B adds
+(rank + 8) 2^-24 of its terms; scaling and residual two more roundings of fp32; then one rounding to
+the output type."""
+import pytest
+import torch
+
+import int8_weight_quantized_gb300 as ck
+import transformer_ref as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+def make(M, N, K, rank, adapters, dtype, seed, order="mixed"):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    x = torch.randn((M, K), generator=g, device=DEV).to(dtype)
+    a = (torch.randn((adapters, rank, K), generator=g, device=DEV) * K ** -0.5).to(dtype)
+    b = (torch.randn((adapters, N, rank), generator=g, device=DEV) * rank ** -0.5).to(dtype)
+    index = torch.randint(-1, adapters, (M,), generator=g, device=DEV, dtype=torch.int32)
+    if order == "runs":
+        index = index.sort().values
+    scaling = torch.rand(adapters, generator=g, device=DEV) + 0.5
+    return x, a, b, index, scaling
+
+
+def expected(x, a, b, index, scaling, residual, out_dtype):
+    M, N, K, rank = x.shape[0], b.shape[1], x.shape[1], a.shape[1]
+    y = torch.zeros((M, N), dtype=torch.float64, device=DEV)
+    tol = torch.zeros_like(y)
+    for i in range(a.shape[0]):
+        rows = (index == i).nonzero()[:, 0]
+        if not rows.numel():
+            continue
+        xs, aa, bb = x[rows].double(), a[i].double(), b[i].double()
+        h = xs @ aa.t()
+        off = (K + 8) * ref.U32 * (xs.abs() @ aa.abs().t())
+        off = off + (h.abs() + off) * ref.unit(x.dtype) + 2.0 ** -25 * (h.abs() + off).amax(1, keepdim=True)
+        s = 1.0 if scaling is None else scaling[i].double()
+        y[rows] = h @ bb.t() * s
+        mag = (h.abs() + off) @ bb.abs().t() * s
+        tol[rows] = off @ bb.abs().t() * s + (rank + 8) * ref.U32 * mag
+    if residual is not None:
+        y = y + residual.double()
+        tol = tol + 2 * ref.U32 * (residual.double().abs() + y.abs())
+    return y, tol + (y.abs() + tol) * ref.unit(out_dtype) + ref.least(out_dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF, F16])
+@pytest.mark.parametrize("M,N,K,rank,adapters,order", [
+    (1, 8, 16, 8, 1, "mixed"), (1, 4096, 4096, 16, 3, "mixed"), (2, 72, 48, 24, 2, "mixed"), (5, 264, 272, 40, 9, "mixed"),
+    (16, 136, 1040, 64, 40, "mixed"), (17, 512, 512, 128, 5, "mixed"), (33, 2056, 5376, 32, 7, "mixed"),
+    (64, 128, 256, 8, 64, "mixed"), (100, 200, 336, 16, 3, "runs"), (257, 72, 144, 56, 300, "mixed"),
+    (300, 520, 1024, 64, 4, "runs"), (1000, 264, 528, 32, 2, "mixed"), (1500, 136, 208, 128, 6, "runs"),
+    (2049, 1032, 1040, 64, 3, "runs"), (129, 8, 16, 8, 2, "runs"),
+])
+def test_against_the_definition(M, N, K, rank, adapters, order, dtype):
+    x, a, b, index, scaling = make(M, N, K, rank, adapters, dtype, M + N, order)
+    if M == 1:
+        index.fill_(adapters - 1)
+    y = torch.full((M, N), float("nan"), dtype=dtype, device=DEV)
+    ck.ck_adapter_linear(x, a, b, index, scaling=scaling, y=y)
+    want, tol = expected(x, a, b, index, scaling, None, dtype)
+    ref.assert_within(y, want, tol, "y")
+    assert (y[index < 0] == 0).all()
+    assert ck.ck_device_error() == 0
+    assert torch.equal(y, ck.ck_adapter_linear(x, a, b, index, scaling=scaling))
+
+
+@pytest.mark.parametrize("out_dtype", [BF, F16, F32])
+@pytest.mark.parametrize("M", [1, 5, 40, 700])
+def test_residual_and_output_types(M, out_dtype):
+    for dtype in (BF, F16):
+        x, a, b, index, scaling = make(M, 272, 768, 16, 4, dtype, M)
+        residual = torch.randn((M, 272), device=DEV).to(out_dtype)
+        want, tol = expected(x, a, b, index, scaling, residual, out_dtype)
+        y = ck.ck_adapter_linear(x, a, b, index, scaling=scaling, residual=residual)
+        assert y.dtype == out_dtype
+        ref.assert_within(y, want, tol, "y")
+        assert torch.equal(y[index < 0], residual[index < 0])  # rows without an adapter, bit for bit
+        z = residual.clone()  # in place
+        assert ck.ck_adapter_linear(x, a, b, index, scaling=scaling, residual=z, y=z) is z
+        assert torch.equal(y, z)
+        want, tol = expected(x, a, b, index, None, None, out_dtype)
+        ref.assert_within(ck.ck_adapter_linear(x, a, b, index, out_dtype=out_dtype), want, tol, "no scaling")
+
+
+@pytest.mark.parametrize("M", [4, 300])
+def test_low_rank_values_beyond_the_types_range(M):
+    """x A^T far above fp16's largest number (and far below its smallest), B and scaling that bring it back."""
+    for gain, back in ((2.0 ** 12, 2.0 ** -14), (2.0 ** -13, 2.0 ** 6)):
+        x, a, b, index, scaling = make(M, 136, 512, 32, 3, F16, 7)
+        x, a = (x.float() * gain).to(F16), (a.float() * gain).to(F16)
+        b, scaling = (b.float() * back).to(F16), scaling * back
+        want, tol = expected(x, a, b, index, scaling, None, F32)
+        y = ck.ck_adapter_linear(x, a, b, index, scaling=scaling, out_dtype=F32)
+        ref.assert_within(y, want, tol, "gain %g" % gain)
+
+
+@pytest.mark.parametrize("M", [6, 500])
+def test_infinities_and_nan_stay_in_their_rows(M):
+    x, a, b, index, scaling = make(M, 136, 512, 16, 4, BF, 8)
+    index[0], index[1], index[2], index[3], index[4] = 0, -1, 1, 2, 3
+    index[5:][index[5:] == 3] = 1
+    want = ck.ck_adapter_linear(x, a, b, index, scaling=scaling)
+    x[0, 7] = float("nan")
+    x[1, 9] = float("inf")  # a row without an adapter does not read x
+    x[2, 500] = float("inf")
+    a[3, 5, 5] = float("nan")  # the adapter of row 4 alone
+    y = ck.ck_adapter_linear(x, a, b, index, scaling=scaling)
+    assert y[0].isnan().all() and y[4].isnan().all() and (y[1] == 0).all()
+    assert not y[2].isfinite().any()
+    keep = torch.ones(M, dtype=torch.bool, device=DEV)
+    keep[[0, 2, 4]] = False
+    assert torch.equal(y[keep], want[keep])
+
+
+@pytest.mark.parametrize("M", [3, 200])
+def test_adapters_out_of_range(M):
+    x, a, b, index, scaling = make(M, 72, 96, 8, 4, BF, 9)
+    want = ck.ck_adapter_linear(x, a, b, index, scaling=scaling)
+    for bad in (4, 2 ** 31 - 1):
+        index[1] = bad
+        y = ck.ck_adapter_linear(x, a, b, index, scaling=scaling)
+        assert ck.ck_device_error() == 128
+        assert y[1].isnan().all()
+        assert torch.equal(y[0], want[0]) and torch.equal(y[2:], want[2:])
+    index.fill_(-2 ** 31)
+    assert (ck.ck_adapter_linear(x, a, b, index, scaling=scaling) == 0).all()
+    assert ck.ck_device_error() == 0
+
+
+def test_no_adapters_at_all():
+    x = torch.randn((5, 32), device=DEV).to(BF)
+    residual = torch.randn((5, 16), device=DEV).to(BF)
+    index = torch.full((5,), -1, dtype=torch.int32, device=DEV)
+    empty = torch.empty((0, 8, 32), dtype=BF, device=DEV), torch.empty((0, 16, 8), dtype=BF, device=DEV)
+    assert torch.equal(ck.ck_adapter_linear(x, *empty, index, residual=residual), residual)
+
+
+def test_beside_the_quantized_projections():
+    """The shared projection's output with the adapters' on top, as the residual of each way round."""
+    x, a, b, index, scaling = make(24, 256, 512, 16, 3, BF, 10)
+    W = torch.randn((256, 512), device=DEV) * 512 ** -0.5
+    w4, scale = ck.ck_int4_prepare_weight(W)
+    base = ck.ck_int4_linear(x, w4, scale)
+    after = ck.ck_adapter_linear(x, a, b, index, scaling=scaling, residual=base)
+    want, tol = expected(x, a, b, index, scaling, base, BF)
+    ref.assert_within(after, want, tol, "after")
+    before = ck.ck_int4_linear(x, w4, scale, residual=ck.ck_adapter_linear(x, a, b, index, scaling=scaling, out_dtype=F32),
+                               out_dtype=F32)
+    # base rounded to bf16 there, nothing here; both adapter sums within their bound
+    assert ((after.double() - before.double()).abs() <= 2 * tol + 2.0 ** -8 * (base.double().abs() + want.abs())).all()
+
+
+@pytest.mark.parametrize("M", [9, 600])
+def test_streams_graphs_and_workspaces(M):
+    x, a, b, index, scaling = make(M, 264, 512, 16, 3, BF, 11)
+    want = ck.ck_adapter_linear(x, a, b, index, scaling=scaling)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    y = ck.ck_adapter_linear(x, a, b, index, scaling=scaling, stream=side)
+    side.synchronize()
+    assert torch.equal(y, want)
+    nbytes = ck.load_library().ck_adapter_linear_workspace_size(M, 264, 512, 16)
+    ws = torch.randint(0, 256, (max(nbytes, 16),), dtype=torch.uint8, device=DEV)
+    other = torch.empty_like(y)
+    graphs = []
+    for out in (y, other):  # two graphs that share a workspace
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            ck.ck_adapter_linear(x, a, b, index, scaling=scaling, y=out, ws=ws)
+        graphs.append(graph)
+    index.copy_(index.flip(0))
+    x.neg_()
+    fresh = ck.ck_adapter_linear(x, a, b, index, scaling=scaling)
+    for _ in range(2):
+        ws.random_(0, 256)
+        graphs[0].replay()
+        graphs[1].replay()
+        assert torch.equal(y, fresh) and torch.equal(other, fresh)
+
+
+def test_more_outputs_than_32_bits_count():
+    """Rows whose outputs lie beyond 2^32 elements."""
+    M, N, K = 2 ** 17, 2 ** 15 + 8, 16
+    x, a, b, _, scaling = make(4, N, K, 8, 2, BF, 12)
+    index = torch.full((M,), -1, dtype=torch.int32, device=DEV)
+    wide = torch.zeros((M, K), dtype=BF, device=DEV)
+    at = torch.tensor([0, M // 2, M - 2, M - 1], device=DEV)
+    wide[at] = x
+    index[at] = torch.tensor([0, 1, 1, 0], dtype=torch.int32, device=DEV)
+    y = torch.zeros((M, N), dtype=BF, device=DEV)
+    ck.ck_adapter_linear(wide, a, b, index, scaling=scaling, residual=y, y=y)
+    want, tol = expected(x, a, b, index[at], scaling, None, BF)
+    ref.assert_within(y[at], want, tol, "y")
+    assert int((y != 0).any(1).sum()) == 4
+
+
+def t(*shape, dtype=BF):
+    return torch.zeros(shape, dtype=dtype, device="cuda")
+
+
+@pytest.mark.parametrize("kw,error", [
+    (lambda: dict(x=t(2, 64, dtype=F32)), TypeError), (lambda: dict(a=t(3, 8, 64, dtype=F16)), TypeError), (lambda: dict(a=t(3, 8, 48)), ValueError),
+    (lambda: dict(b=t(2, 16, 8)), ValueError), (lambda: dict(b=t(3, 16, 16)), ValueError), (lambda: dict(b=t(3, 12, 8)), ck.CkError),
+    (lambda: dict(a=t(3, 136, 64), b=t(3, 16, 136)), ck.CkError), (lambda: dict(a=t(3, 12, 64), b=t(3, 16, 12)), ck.CkError),
+    (lambda: dict(x=t(2, 72), a=t(3, 8, 72)), ck.CkError), (lambda: dict(index=t(2, dtype=torch.int64)), TypeError),
+    (lambda: dict(index=t(3, dtype=torch.int32)), ValueError), (lambda: dict(scaling=t(2, dtype=F32)), ValueError),
+    (lambda: dict(scaling=t(3)), TypeError), (lambda: dict(residual=t(2, 8)), ValueError), (lambda: dict(residual=t(2, 16, dtype=torch.int32)), TypeError),
+    (lambda: dict(residual=t(2, 16), out_dtype=F32), TypeError), (lambda: dict(y=t(2, 16, dtype=F32)), TypeError),
+    (lambda: dict(out_dtype=torch.int32), ValueError), (lambda: dict(x=t(2, 128)[:, ::2]), ValueError),
+])
+def test_refusals(kw, error):
+    f = dict(x=t(2, 64), a=t(3, 8, 64), b=t(3, 16, 8), index=t(2, dtype=torch.int32), scaling=None, residual=None, y=None,
+             out_dtype=None)
+    f.update(kw())
+    with pytest.raises(error):
+        ck.ck_adapter_linear(f["x"], f["a"], f["b"], f["index"], scaling=f["scaling"], residual=f["residual"], y=f["y"],
+                             out_dtype=f["out_dtype"])
+    torch.cuda.synchronize()
+    assert ck.ck_device_error() == 0
+
+
+def test_no_rows():
+    assert ck.ck_adapter_linear(t(0, 64), t(3, 8, 64), t(3, 16, 8), t(0, dtype=torch.int32)).shape == (0, 16)

@@ -1,0 +1,288 @@
+"""Log probabilities of tokens, entropies and top alternatives, against 64 bits.
+
+Bound.  t_j = scale (x_j - max) has two fp32 roundings, 2 u |t_j| (u = 2^-24); its exponential adds the
+rounding of its argument in units of log 2 (2 u |t_j|) and 2^-21 of approximation; sums of positive
+terms in fp32, at most V / 256 + 64 in a row (a block has 256 threads or more): a relative error of
+(V / 256 + 64) u.  So s without the largest's own 1 is off by d = sum_j e_j (4 u |t_j| + 2^-21 +
+(V / 256 + 64) u), and log s by d / s, with 4 u of itself for the function and rounding."""
+import math
+
+import pytest
+import torch
+
+import int8_weight_quantized_gb300 as ck
+import transformer_ref as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+U = ref.U32
+
+
+def expected(x, tokens, top, scale):
+    scale = float(torch.tensor(scale, dtype=F32))
+    x = x.double()
+    V = x.shape[1]
+    high, first = x.max(-1, keepdim=True)
+    t = scale * (x - high)
+    e = t.exp()
+    t0 = torch.where(e > 0, t, 0.0)
+    rest = e.scatter(1, first, 0.0)
+    log_s = torch.log1p(rest.sum(-1))
+    s = 1 + rest.sum(-1)
+    each = 4 * U * t0.abs() + 2.0 ** -21 + (V / 256 + 64) * U
+    d = (rest * each).sum(-1) / s
+    d_log = d + 4 * U * log_s
+    weighted = (e * t0).sum(-1) / s
+    entropy = log_s - weighted
+    d_entropy = d_log + (rest * t0.abs() * (each + 2 * U)).sum(-1) / s + weighted.abs() * (d + 4 * U) + 2 * U * entropy
+    r = dict(entropy=(entropy, d_entropy), lse=(scale * high[:, 0] + log_s, d_log + 2 * U * (scale * high[:, 0] + log_s).abs() +
+                                                2 * U * (scale * high[:, 0]).abs()))
+    if tokens is not None:
+        mine = t.gather(1, tokens.clamp_min(0).long()[:, None])[:, 0]
+        value = torch.where(tokens < 0, 0.0, mine - log_s)
+        r["logprob"] = value, torch.where(mine.isinf(), 0.0, d_log + 4 * U * (mine.abs() + value.abs()))
+    if top:
+        order = torch.sort(x, dim=-1, descending=True, stable=True).indices[:, :top]
+        best = t.gather(1, order)
+        value = best - log_s[:, None]
+        r["top"] = value, torch.where(best.isinf(), 0.0, d_log[:, None] + 4 * U * (best.abs() + value.abs()))
+        r["index"] = order.to(torch.int32)
+    return r
+
+
+def check(x, tokens, got, top, scale=1.0):
+    want = expected(x, tokens, top, scale)
+    for name in ("logprob", "entropy", "lse", "top"):
+        out = getattr(got, name)
+        if name not in want:
+            assert out is None
+            continue
+        value, tol = want[name]
+        assert out.dtype == F32 and out.shape == value.shape
+        inf = value.isinf()
+        assert torch.equal(out.isinf() & (out.double() == value), inf), name
+        ref.assert_within(out[~inf], value[~inf], tol[~inf] + ref.least(F32), name)
+    if top:
+        assert torch.equal(got.index, want["index"])
+    else:
+        assert got.index is None
+
+
+def make(rows, vocab, dtype, seed, masked=0.0, spread=2.5):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    x = torch.randn((rows, vocab), generator=g, device=DEV) * spread
+    if masked:
+        hidden = torch.rand((rows, vocab), generator=g, device=DEV) < masked
+        hidden[:, seed % vocab] = False
+        x.masked_fill_(hidden, -math.inf)
+    tokens = torch.randint(0, vocab, (rows,), generator=g, device=DEV, dtype=torch.int32)
+    if masked:
+        tokens[::2] = seed % vocab
+    return x.to(dtype), tokens
+
+
+@pytest.mark.parametrize("dtype", [BF, F16, F32])
+@pytest.mark.parametrize("rows,vocab,top,masked", [
+    (1, 1, 1, 0), (1, 2, 2, 0), (3, 7, 7, 0), (2, 31, 32 - 1, 0), (2, 32, 32, 0.5), (5, 33, 5, 0), (1, 1000, 20, 0.97),
+    (4, 4097, 32, 0), (1, 32000, 5, 0), (1, 262143, 32, 0), (7, 50001, 20, 0.6), (48, 131071, 20, 0.6), (300, 9999, 1, 0),
+    (2000, 515, 8, 0.3), (70, 64000, 0, 0), (33, 100003, 8, 0.999),
+])
+def test_against_the_definition(rows, vocab, top, masked, dtype):
+    x, tokens = make(rows, vocab, dtype, vocab + rows, masked)
+    got = ck.ck_token_logprobs(x, tokens, top=top)
+    check(x, tokens, got, top)
+    assert ck.ck_device_error() == 0
+    for a, b in zip(got, ck.ck_token_logprobs(x, tokens, top=top)):
+        assert a is b or torch.equal(a, b)
+
+
+@pytest.mark.parametrize("scale", [0.25, 0.7, 1.25, 30.0])
+@pytest.mark.parametrize("rows", [1, 40])
+def test_scale(rows, scale):
+    x, tokens = make(rows, 20011, F32, 3)
+    check(x, tokens, ck.ck_token_logprobs(x, tokens, top=12, scale=scale), 12, scale)
+
+
+@pytest.mark.parametrize("rows", [1, 200])
+def test_sharp_rows_keep_their_small_numbers(rows):
+    """One logit far above the rest: entropy and its log probability are the rest's small sum."""
+    for gap in (12.0, 25.0, 60.0):
+        x, tokens = make(rows, 30011, F32, 4, spread=1.0)
+        x[torch.arange(rows), tokens.long()] = gap
+        check(x, tokens, ck.ck_token_logprobs(x, tokens, top=3), 3)
+        # and with a few halves of that, one after the other in memory, near either end
+        for at in (0, 30005):
+            x[:, at:at + 5] = gap - 0.25 * torch.arange(5, device=DEV)
+            check(x, tokens, ck.ck_token_logprobs(x, tokens, top=7), 7)
+
+
+@pytest.mark.parametrize("order", ["ascending", "descending", "equal", "two values", "blocks"])
+@pytest.mark.parametrize("rows,vocab", [(1, 40000), (3, 4001), (160, 8200)])
+def test_orders_and_ties(rows, vocab, order):
+    j = torch.arange(vocab, device=DEV, dtype=F32)
+    if order == "ascending":
+        x = j / 1000
+    elif order == "descending":
+        x = -j / 1000
+    elif order == "equal":
+        x = torch.full_like(j, -3.5)
+    elif order == "two values":
+        x = torch.where(j % 37 == 11, 1.0, 0.0)
+    else:
+        x = (j // 50) % 9
+    for dtype in (F32, BF):
+        rowsx = x.to(dtype)[None].repeat(rows, 1)
+        tokens = torch.full((rows,), vocab // 2, dtype=torch.int32, device=DEV)
+        check(rowsx, tokens, ck.ck_token_logprobs(rowsx, tokens, top=32), 32)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_rows_anywhere(dtype):
+    """Strided rows that begin at any element."""
+    x, tokens = make(20, 5000, dtype, 6)
+    for start, width in ((0, 4096), (1, 4097), (3, 2999), (7, 8), (5, 1), (13, 4987)):
+        view = x[:, start:start + width]
+        tok = tokens % width
+        check(view, tok, ck.ck_token_logprobs(view, tok, top=min(4, width)), min(4, width))
+    flat = x.view(-1)[1:1 + 19 * 5000 + 4999].as_strided((20, 4999), (5000, 1))
+    tok = tokens % 4999
+    check(flat, tok, ck.ck_token_logprobs(flat, tok, top=4), 4)
+
+
+def test_what_lies_between_rows_is_not_read():
+    x, tokens = make(9, 1100, F32, 7)
+    view = x[:, 5:1000]
+    tok = tokens % 995
+    want = ck.ck_token_logprobs(view, tok, top=6)
+    x[:, :5] = float("nan")
+    x[:, 1000:] = float("inf")
+    for a, b in zip(ck.ck_token_logprobs(view, tok, top=6), want):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [BF, F16, F32])
+@pytest.mark.parametrize("rows,vocab", [(6, 2000), (6, 70000)])
+def test_infinities_and_nan(rows, vocab, dtype):
+    x, tokens = make(rows, vocab, dtype, 8)
+    x[1] = -math.inf
+    x[2, 1234] = math.inf
+    x[3, 77] = math.nan
+    x[3, 55] = math.inf
+    x[3, 1999] = math.nan
+    x[4] = -math.inf
+    x[4, 1500] = -2.0
+    tokens[4] = 3
+    got = ck.ck_token_logprobs(x, tokens, top=4)
+    for i in (1, 2, 3):
+        assert got.logprob[i].isnan() and got.entropy[i].isnan() and got.top[i].isnan().all()
+    assert got.lse[1] == -math.inf and got.lse[2] == math.inf and got.lse[3].isnan()
+    assert got.index[1].tolist() == [0, 1, 2, 3]
+    assert got.index[2, 0] == 1234
+    assert got.index[3, :3].tolist() == [77, 1999, 55]
+    assert got.logprob[4] == -math.inf and got.entropy[4] == 0 and got.lse[4] == -2.0
+    assert got.index[4].tolist() == [1500, 0, 1, 2] and got.top[4].tolist() == [0.0] + [-math.inf] * 3
+    rest = [0, 5]
+    check(x[rest], tokens[rest], type(got)(*[o[rest] for o in got]), 4)
+    assert ck.ck_device_error() == 0
+
+
+def test_extreme_finite_logits():
+    """Differences that overflow fp32, and the largest and smallest numbers."""
+    big = torch.finfo(F32).max
+    x = torch.zeros((4, 600), device=DEV)
+    x[0, 7], x[0, 9] = big, -big
+    x[1] = -big
+    x[2] = big
+    x[3, 5] = 1e-45
+    got = ck.ck_token_logprobs(x, torch.tensor([9, 1, 2, 3], dtype=torch.int32, device=DEV), top=2)
+    n = math.log(600)
+    assert got.logprob[0] == -math.inf and got.entropy[0] == 0 and got.lse[0] == big
+    assert got.index[0].tolist() == [7, 0] and got.index[1].tolist() == [0, 1] and got.index[3].tolist() == [5, 0]
+    for i in (1, 2, 3):
+        assert abs(got.logprob[i].item() + n) < 1e-5 and abs(got.entropy[i].item() - n) < 1e-5
+
+
+@pytest.mark.parametrize("rows,vocab", [(5, 300), (5, 60000)])
+def test_tokens_that_are_none_or_out_of_range(rows, vocab):
+    x, tokens = make(rows, vocab, F32, 9)
+    want = ck.ck_token_logprobs(x, tokens)
+    tokens[1], tokens[3] = -1, -100
+    got = ck.ck_token_logprobs(x, tokens)
+    assert ck.ck_device_error() == 0
+    assert got.logprob[1] == 0 and got.logprob[3] == 0 and torch.equal(got.logprob[::2], want.logprob[::2])
+    for bad in (vocab, 2 ** 31 - 1):
+        tokens[2] = bad
+        got = ck.ck_token_logprobs(x, tokens)
+        assert ck.ck_device_error() == 128
+        assert got.logprob[2].isnan() and torch.equal(got.entropy, want.entropy) and got.logprob[0] == want.logprob[0]
+
+
+def test_without_tokens():
+    x, tokens = make(3, 999, BF, 10)
+    check(x, None, ck.ck_token_logprobs(x, top=2), 2)
+
+
+@pytest.mark.parametrize("rows,vocab", [(2, 70001), (600, 3001)])
+def test_given_outputs_streams_and_graphs(rows, vocab):
+    x, tokens = make(rows, vocab, BF, 11)
+    want = ck.ck_token_logprobs(x, tokens, top=3)
+    out = ck.TokenLogprobs(*[torch.empty_like(o) for o in want])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    assert ck.ck_token_logprobs(x, tokens, top=3, out=out, stream=side) is out
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, want))
+    part = ck.TokenLogprobs(torch.empty_like(want.logprob), None, None, None, None)  # what is not given is not worked out
+    ck.ck_token_logprobs(x, tokens, out=part)
+    assert torch.equal(part.logprob, want.logprob)
+    nbytes = ck.load_library().ck_token_logprobs_workspace_size(rows, vocab, 3)
+    ws = torch.randint(0, 256, (max(nbytes, 16),), dtype=torch.uint8, device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ck.ck_token_logprobs(x, tokens, top=3, out=out, ws=ws)
+    x.neg_()
+    fresh = ck.ck_token_logprobs(x, tokens, top=3)
+    for _ in range(2):
+        ws.random_(0, 256)
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(out, fresh))
+
+
+def test_offsets_beyond_32_bits():
+    rows, vocab = 40000, 65536 * 2 + 8  # 5.2e9 logits
+    x = torch.zeros((rows, vocab), dtype=BF, device=DEV)
+    x[-1], tokens = make(1, vocab, BF, 12)[0][0], torch.full((rows,), vocab - 1, dtype=torch.int32, device=DEV)
+    got = ck.ck_token_logprobs(x, tokens, top=2)
+    check(x[-1:], tokens[-1:], type(got)(*[o[-1:] for o in got]), 2)
+    check(x[20000:20001], tokens[:1], type(got)(*[o[20000:20001] for o in got]), 2)
+
+
+def t(*shape, dtype=F32):
+    return torch.zeros(shape, dtype=dtype, device="cuda")
+
+
+@pytest.mark.parametrize("kw,error", [
+    (lambda: dict(logits=t(2, 50, dtype=torch.float64)), TypeError), (lambda: dict(logits=t(50)), ValueError),
+    (lambda: dict(logits=t(50, 2).t()), ValueError), (lambda: dict(logits=t(2, 50).cpu()), ValueError), (lambda: dict(tokens=t(2)), TypeError),
+    (lambda: dict(tokens=t(3, dtype=torch.int32)), ValueError), (lambda: dict(top=33), ck.CkError), (lambda: dict(top=-1), ck.CkError),
+    (lambda: dict(top="x"), TypeError), (lambda: dict(logits=t(2, 5), top=6), ck.CkError), (lambda: dict(logits=t(2, 0)), ck.CkError),
+    (lambda: dict(scale=0.0), ck.CkError), (lambda: dict(scale=-1.0), ck.CkError), (lambda: dict(scale=float("inf")), ck.CkError),
+    (lambda: dict(scale="x"), TypeError), (lambda: dict(logits=t(1, 50).expand(2, 50)), ck.CkError),
+    (lambda: dict(out=ck.TokenLogprobs(t(2), None, None, t(2, 3), None)), ValueError),
+    (lambda: dict(out=ck.TokenLogprobs(t(3), None, None, None, None)), ValueError),
+    (lambda: dict(out=ck.TokenLogprobs(t(2), None, None, None, None), top=1), ValueError),
+])
+def test_refusals(kw, error):
+    f = dict(logits=t(2, 50), tokens=t(2, dtype=torch.int32), top=0, scale=1.0, out=None)
+    f.update(kw())
+    with pytest.raises(error):
+        ck.ck_token_logprobs(**f)
+    torch.cuda.synchronize()
+    assert ck.ck_device_error() == 0
+
+
+def test_no_rows():
+    got = ck.ck_token_logprobs(t(0, 50), t(0, dtype=torch.int32), top=2)
+    assert got.logprob.shape == (0,) and got.top.shape == (0, 2)

@@ -1,0 +1,296 @@
+"""Attention of one new token behind shared prefixes, against the 64-bit definition over the prefix's
+keys and the sequence's own (transformer_ref.attend derives the bound; values of int8 rows may be
+rounded once to the queries' type before the second product, one more unit of theirs; one rounding
+of the output on top)."""
+import pytest
+import torch
+
+import int8_weight_quantized_gb300 as ck
+import transformer_ref as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF, F16 = torch.bfloat16, torch.float16
+
+
+def make(plens, cu, lens, hq, hkv, d, page, dtype, int8, seed, q_std=1.5, extra=1):
+    """A shuffled pool; every row that nobody owns is NaN (16-bit) or has a NaN scale.  Tables have `extra`
+    pages more than the longest needs, naming a page of NaN rows."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    owners = list(plens) + list(lens)
+    need = [-(-n // page) for n in owners]
+    pages = sum(need) + 3
+    pool = torch.randperm(pages, generator=g, device=DEV)
+    shape = (pages, hkv, page, d)
+    if int8:
+        cache = ck.KVCache.empty(pages, page, hkv, d, dtype=torch.int8)
+        for t, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
+            t.copy_(torch.randint(-127, 128, shape, generator=g, device=DEV, dtype=torch.int8))
+            s.copy_(torch.rand(shape[:3], generator=g, device=DEV) * 0.02 + 0.004)
+    else:
+        cache = ck.KVCache(*[torch.randn(shape, generator=g, device=DEV).to(dtype) for _ in range(2)])
+    spare = int(pool[-1])
+    tables = []
+    owned = torch.zeros((pages, page), dtype=torch.bool, device=DEV)
+    at = 0
+    for part in (list(plens), list(lens)):
+        table = torch.full((len(part), max([1] + [-(-n // page) for n in part]) + extra), spare, dtype=torch.int32, device=DEV)
+        for i, n in enumerate(part):
+            mine = pool[at:at + -(-n // page)]
+            at += len(mine)
+            table[i, :len(mine)] = mine.to(torch.int32)
+            rows = torch.arange(n, device=DEV)
+            if n:
+                owned[mine[rows // page], rows % page] = True
+        tables.append(table)
+    for t in ((cache.k_scale, cache.v_scale) if int8 else (cache.k, cache.v)):
+        t[~owned[:, None, :].expand(pages, hkv, page)] = float("nan")
+    q = (torch.randn((len(lens), hq, d), generator=g, device=DEV) * q_std).to(dtype)
+
+    def i32(x):
+        return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+    return dict(q=q, cache=cache, ptable=tables[0], plens=i32(plens), cu=i32(cu), table=tables[1], lens=i32(lens))
+
+
+def call(s, **kw):
+    return ck.ck_prefix_attention(s["q"], s["cache"], s["ptable"], s["plens"], s["cu"], s["table"], s["lens"], **kw)
+
+
+def rows_of(cache, table, n, h):
+    page = cache.page_size
+    j = torch.arange(n, device=DEV)
+    at, off = table.long()[j // page], j % page
+    out = []
+    for t, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
+        x = t[at, h, off].double()
+        out.append(x if s is None else x * s[at, h, off].double()[:, None])
+    return out
+
+
+def check(s, out, lse, scale=None, only=None):
+    q, cache = s["q"], s["cache"]
+    dtype, d = q.dtype, q.shape[2]
+    hkv = cache.k.shape[1]
+    g = q.shape[1] // hkv
+    int8 = cache.k.dtype == torch.int8
+    scale = d ** -0.5 if scale is None else scale
+    cu, plens = s["cu"].tolist(), s["plens"].tolist()
+    # int8 rows: weights in fp16 (16-bit keys of a short call) or in the queries' type, values rounded once
+    p_unit = ref.unit(dtype) * (2 if int8 else 1)
+    p_least = max(ref.least(dtype), ref.least(F16)) if int8 else ref.least(dtype)
+    for b, n in enumerate(s["lens"].tolist()):
+        if only is not None and b not in only:
+            continue
+        behind = [i for i in range(len(plens)) if cu[i] <= b < cu[i + 1]]
+        for h in range(hkv):
+            k, v = rows_of(cache, s["table"][b], n, h)
+            if behind:
+                pk, pv = rows_of(cache, s["ptable"][behind[0]], plens[behind[0]], h)
+                k, v = torch.cat([pk, k]), torch.cat([pv, v])
+            rows = slice(h * g, (h + 1) * g)
+            seen = torch.ones((g, k.shape[0]), dtype=torch.bool, device=DEV)
+            want, want_lse, tol, lse_tol = ref.attend(q[b, rows], k, v, scale, seen, p_unit, p_least)
+            if k.shape[0]:
+                tol = tol + (want.abs() + tol) * ref.unit(dtype) + ref.least(dtype)
+                ref.assert_within(lse[b, rows], want_lse, lse_tol, "lse %d" % b)
+            else:
+                assert (lse[b, rows] == -float("inf")).all()
+            ref.assert_within(out[b, rows], want, tol, "sequence %d head %d" % (b, h))
+
+
+CASES = [
+    # prefix lengths, groups, own lengths, q heads, kv heads, head_dim, page
+    ([1], [0, 1], [1], 8, 2, 128, 16),
+    ([0], [0, 2], [0, 3], 4, 2, 64, 16),                                # an empty prefix
+    ([127, 128, 129], [0, 2, 3, 6], [0, 1, 5, 130, 17, 0, 40], 4, 1, 64, 16),  # the last one behind none
+    ([300, 5], [1, 1, 4], [9, 8, 7, 600, 2], 12, 2, 128, 7),             # a group of none, the first behind none
+    ([1000], [0, 70], [i % 9 for i in range(70)], 16, 2, 64, 32),       # many rows to a head
+    ([2100], [0, 40], [i * 5 % 64 for i in range(40)], 12, 2, 128, 16),  # groups of 6
+    ([777], [0, 33], [3] * 33, 7, 1, 128, 64),                           # of 7
+    ([1500, 400], [0, 9, 30], [i * 3 for i in range(30)], 40, 2, 64, 100),  # of 20
+    ([4097], [0, 140], [1 + i % 3 for i in range(140)], 8, 8, 128, 128),   # of 1, pages of a tile
+    ([513], [0, 3], [1, 600, 20], 3, 3, 64, 1),                          # pages of one row
+]
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("dtype", [BF, F16])
+@pytest.mark.parametrize("plens,cu,lens,hq,hkv,d,page", CASES)
+def test_against_the_definition(plens, cu, lens, hq, hkv, d, page, dtype, int8):
+    s = make(plens, cu, lens, hq, hkv, d, page, dtype, int8, seed=sum(plens) + d)
+    out, lse = call(s, return_lse=True)
+    check(s, out, lse)
+    assert ck.ck_device_error() == 0
+    assert torch.equal(out, call(s))  # the same split and order of sums every time
+
+
+@pytest.mark.parametrize("int8", [False, True])
+def test_a_long_prefix_and_many_sequences(int8):
+    s = make([20011], [0, 200], [i * 7 % 300 for i in range(200)], 32, 4, 128, 64, BF, int8, seed=3)
+    out, lse = call(s, return_lse=True)
+    check(s, out, lse, only=[0, 1, 63, 64, 127, 128, 198, 199])
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("batch", [3, 40])
+def test_equals_attention_over_one_table(batch, int8):
+    """Behind a prefix of whole pages, a block table that names its pages first says the same."""
+    lens = [1 + i * 11 % 50 for i in range(batch)]
+    s = make([640], [0, batch], lens, 8, 2, 128, 32, BF, int8, seed=batch)
+    both = torch.cat([s["ptable"][:, :20].expand(batch, 20), s["table"]], 1).contiguous()
+    want, want_lse = ck.ck_paged_attention(s["q"], s["cache"], both, s["lens"] + 640, return_lse=True)
+    out, lse = call(s, return_lse=True)
+    # each is within its bound of the definition: weights to 8 bits (values too, int8), the output to 8
+    assert (out.float() - want.float()).abs().max() <= 6 * 2.0 ** -8 * want.float().abs().max()
+    assert (lse - want_lse).abs().max() <= 1e-4 * (1 + want_lse.abs().max())
+
+
+def test_sharp_scores_scale_and_strides():
+    lens = [30, 4, 0] + [5] * 40
+    s = make([900], [0, 43], lens, 8, 2, 128, 16, F16, False, seed=5, q_std=12.0)
+    wide = torch.zeros((43, 8 * 128 + 64), dtype=F16, device=DEV)
+    wide[:, :1024] = s["q"].reshape(43, -1)
+    view = dict(s, q=wide[:, :1024].view(43, 8, 128))
+    for scale in (0.3, -0.2, 0.0):
+        out, lse = call(view, return_lse=True, scale=scale)
+        check(s, out, lse, scale=scale)
+
+
+@pytest.mark.parametrize("batch", [2, 40])
+def test_infinities_and_nan_stay_with_who_sees_them(batch):
+    s = make([300, 400], [0, batch, 2 * batch], [5] * (2 * batch), 4, 2, 64, 16, BF, False, seed=9)
+    want, want_lse = call(s, return_lse=True)
+    s["cache"].v[s["ptable"][1, 3].long(), 0, 2, 5] = float("inf")  # of the second prefix's rows of head 0
+    s["cache"].k[s["table"][0, 0].long(), 1, 1] = float("nan")      # of the first sequence's own keys, head 1
+    out, lse = call(s, return_lse=True)
+    same = torch.ones_like(out, dtype=torch.bool)
+    same[batch:, :2, 5] = False
+    same[0, 2:] = False
+    assert torch.equal(out[same], want[same])
+    assert (out[batch:, :2, 5] == float("inf")).all()
+    assert out[0, 2:].isnan().all() and lse[0, 2:].isnan().all()
+
+
+def test_scores_of_minus_infinity():
+    """A prefix without weight leaves the rest as it is; rows with nothing but such scores are NaN."""
+    s = make([200], [0, 36], [3] * 35 + [0], 4, 2, 64, 16, BF, False, seed=10)
+    s["q"].abs_()
+    clean = ck.ck_paged_attention(s["q"], s["cache"], s["table"], s["lens"])
+    rows = torch.arange(200, device=DEV)
+    s["cache"].k[s["ptable"][0].long()[rows // 16], :, rows % 16] = -float("inf")
+    out, lse = call(s, return_lse=True)
+    assert torch.allclose(out[:35].float(), clean[:35].float(), rtol=2.0 ** -7, atol=2.0 ** -9)
+    assert out[35].isnan().all()
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("batch", [2, 40])
+def test_lengths_bounds_and_pages_out_of_range(batch, int8):
+    lens = [5] * (2 * batch)
+    base = make([300, 200], [0, batch, 2 * batch], lens, 4, 2, 64, 16, BF, int8, seed=11)
+    want = call(base)
+    assert ck.ck_device_error() == 0
+
+    def broken(name, index, value):
+        s = dict(base)
+        s[name] = base[name].clone()
+        s[name][index] = value
+        out, lse = call(s, return_lse=True)
+        assert ck.ck_device_error() == 128
+        bad = out.isnan().flatten(1)
+        assert (bad.all(1) == bad.any(1)).all() and (bad.all(1) == lse.isnan().all(1)).all()
+        good = ~bad.all(1)
+        assert torch.equal(out[good], want[good])
+        return [b for b in range(2 * batch) if not good[b]]
+
+    assert broken("plens", 0, -1) == list(range(batch))
+    assert broken("plens", 1, 16 * base["ptable"].shape[1] + 1) == list(range(batch, 2 * batch))
+    assert broken("lens", 1, -5) == [1]
+    assert broken("lens", 0, 16 * base["table"].shape[1] + 1) == [0]
+    for index, value in ((0, -1), (2, 2 * batch + 1), (1, 2 * batch + 5), (1, -3)):
+        assert broken("cu", index, value) == list(range(2 * batch))
+    assert broken("ptable", (0, 2), 10 ** 6) == list(range(batch))
+    assert broken("ptable", (1, 12), -1) == list(range(batch, 2 * batch))
+    assert broken("table", (1, 0), -2) == [1]
+
+
+def test_given_outputs_streams_and_graphs():
+    s = make([2000], [0, 50], [i % 40 for i in range(50)], 8, 2, 128, 16, BF, False, seed=12)
+    want, want_lse = call(s, return_lse=True)
+    out, lse = torch.empty_like(want), torch.empty_like(want_lse)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    a, b = call(s, out=out, lse=lse, return_lse=True, stream=side)
+    side.synchronize()
+    assert a is out and b is lse and torch.equal(out, want) and torch.equal(lse, want_lse)
+    nbytes = ck.load_library().ck_prefix_attention_workspace_size(50, 8, 2, 128, 1, s["ptable"].shape[1] * 16,
+                                                                  s["table"].shape[1] * 16)
+    ws = torch.randint(0, 256, (max(nbytes, 16),), dtype=torch.uint8, device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(s, out=out, lse=lse, return_lse=True, ws=ws)
+    # replayed with other lengths and queries
+    s["plens"].fill_(1003)
+    s["lens"].copy_(s["lens"].flip(0).clamp(max=int(s["lens"].max())))
+    s["q"].mul_(-1)
+    # (own pages of other lengths: rows that nobody owned may be read now, so give them numbers)
+    for t in (s["cache"].k, s["cache"].v):
+        t.nan_to_num_(0.25)
+    for _ in range(2):
+        out.fill_(float("nan"))
+        ws.random_(0, 256)
+        graph.replay()
+        fresh, fresh_lse = call(s, return_lse=True)
+        assert torch.equal(out, fresh) and torch.equal(lse, fresh_lse)
+
+
+def test_more_rows_than_the_cache_has_bytes_for_in_32_bits():
+    """A cache whose rows lie beyond 2^32 bytes."""
+    pages, page, hkv, d = 2 ** 15 + 8, 64, 8, 128  # 4.3 GB each
+    cache = ck.KVCache(*[torch.empty((pages, hkv, page, d), dtype=BF, device=DEV) for _ in range(2)])
+    at = torch.tensor([pages - 1, 3, pages - 2, 2 ** 15, 1, pages - 3], device=DEV)
+    for t in (cache.k, cache.v):
+        t[at] = torch.randn((6, hkv, page, d), device=DEV).to(BF)
+    s = dict(q=torch.randn((40, 8, d), device=DEV).to(BF), cache=cache, ptable=at[:4][None].to(torch.int32).contiguous(),
+             plens=torch.tensor([250], dtype=torch.int32, device=DEV), cu=torch.tensor([0, 40], dtype=torch.int32, device=DEV),
+             table=at[4:].to(torch.int32).repeat(40, 1).contiguous(), lens=torch.full((40,), 100, dtype=torch.int32, device=DEV))
+    out, lse = call(s, return_lse=True)
+    check(s, out, lse, only=[0, 17, 39])
+
+
+def t(*shape, dtype=BF):
+    return torch.zeros(shape, dtype=dtype, device="cuda")
+
+
+def i32(*shape):
+    return t(*shape, dtype=torch.int32)
+
+
+KV = dict(k=(3, 1, 8, 64), v=(3, 1, 8, 64))
+
+
+@pytest.mark.parametrize("args,error", [
+    ((t, (2, 2, 64), (1, 1), (1,), (2,), (2, 1), (2,), torch.int64), TypeError),
+    ((t, (2, 2, 32), (1, 1), (1,), (2,), (2, 1), (2,), torch.int32), ValueError),
+    ((t, (2, 2, 64), (1, 1), (2,), (2,), (2, 1), (2,), torch.int32), ValueError),
+    ((t, (2, 2, 64), (1, 1), (1,), (3,), (2, 1), (2,), torch.int32), ValueError),
+    ((t, (2, 2, 64), (1, 1), (1,), (2,), (3, 1), (2,), torch.int32), ValueError),
+    ((t, (2, 2, 64), (1, 1), (1,), (2,), (2, 1), (3,), torch.int32), ValueError),
+    ((t, (2, 2, 64), (0, 1), (0,), (1,), (2, 1), (2,), torch.int32), ck.CkError),
+    ((t, (2, 2, 64), (1, 0), (1,), (2,), (2, 1), (2,), torch.int32), ck.CkError),
+    ((t, (2, 2, 64), (1, 1), (1,), (2,), (2, 0), (2,), torch.int32), ck.CkError),
+])
+def test_refusals(args, error):
+    _, q, ptable, plens, cu, table, lens, kind = args
+    cache = ck.KVCache(t(*KV["k"]), t(*KV["v"]))
+    with pytest.raises(error):
+        ck.ck_prefix_attention(t(*q), cache, t(*ptable, dtype=kind), i32(*plens), i32(*cu), i32(*table), i32(*lens))
+    torch.cuda.synchronize()
+    assert ck.ck_device_error() == 0
+
+
+def test_an_empty_batch():
+    cache = ck.KVCache(t(*KV["k"]), t(*KV["v"]))
+    assert ck.ck_prefix_attention(t(0, 2, 64), cache, i32(1, 1), i32(1), i32(2), i32(0, 1), i32(0)).shape == (0, 2, 64)

@@ -1,0 +1,141 @@
+"""The operators for many requests of one model reject bad arguments before any device work, through
+the C ABI (with pointers that are never dereferenced) and through the binding."""
+import ctypes
+
+import pytest
+import torch
+
+import int8_weight_quantized_gb300 as ck
+from test_transformer_args import ODD, P, cache, lib  # noqa: F401
+
+
+def prefix(lib, **kw):  # noqa: F811
+    f = dict(q=P, stride=256, cache=cache(), ptable=P, pblocks=40, plens=P, cu=P, n=2, table=P, blocks=50, lens=P, batch=3,
+             hq=4, dtype=0, scale=0.1, out=P, lse=None, ws=P, nbytes=1 << 40)
+    f.update(kw)
+    return lib.ck_prefix_attention(f["q"], f["stride"], f["cache"], f["ptable"], f["pblocks"], f["plens"], f["cu"], f["n"],
+                                   f["table"], f["blocks"], f["lens"], f["batch"], f["hq"], f["dtype"], f["scale"], f["out"],
+                                   f["lse"], f["ws"], f["nbytes"], None)
+
+
+@pytest.mark.parametrize("kw,what", [
+    (dict(dtype=3), "dtype"), (dict(cache=None), "cache"), (dict(hq=5), "multiple of kv_heads"),
+    (dict(cache=cache(head_dim=96)), "head_dim"), (dict(stride=248), "q_stride"), (dict(scale=float("inf")), "scale"),
+    (dict(batch=-1), "batch"), (dict(n=0), "num_prefixes"), (dict(n=65537), "num_prefixes"), (dict(blocks=0), "max_blocks"),
+    (dict(pblocks=0), "max_prefix_blocks"), (dict(blocks=2 ** 26, pblocks=2 ** 26), "below 2^31"),
+    (dict(pblocks=2 ** 62), "below 2^31"), (dict(cache=cache(page_size=0)), "page_size"), (dict(q=None), "q must"),
+    (dict(ptable=None), "prefix_table"), (dict(plens=ODD), "prefix_lens"), (dict(cu=None), "cu_prefix"),
+    (dict(table=None), "block_table"), (dict(lens=None), "seq_lens"), (dict(out=ODD), "out must be 16-byte"),
+    (dict(lse=ODD), "lse"), (dict(ws=None), "workspace"), (dict(nbytes=0), "workspace too small"),
+    (dict(cache=cache(dtype=1)), "cache dtype"),
+])
+def test_prefix_attention_refusals(lib, kw, what):  # noqa: F811
+    assert prefix(lib, **kw) == ck.CK_ERR_INVALID_ARG
+    assert what in ck.ck_last_error()
+
+
+def read(lib, **kw):  # noqa: F811
+    f = dict(cache=cache(), table=P, blocks=4, cu=P, batch=2, total=30, dtype=0, k=P, v=P)
+    f.update(kw)
+    return lib.ck_cache_read(f["cache"], f["table"], f["blocks"], f["cu"], f["batch"], f["total"], f["dtype"], f["k"], f["v"],
+                             None)
+
+
+@pytest.mark.parametrize("kw,what", [
+    (dict(dtype=2), "dtype"), (dict(cache=None), "cache"), (dict(cache=cache(kv_heads=0)), "kv_heads"),
+    (dict(cache=cache(head_dim=60)), "head_dim"), (dict(cache=cache(head_dim=264)), "head_dim"), (dict(batch=-1), "batch"),
+    (dict(total=2 ** 31), "total"), (dict(blocks=0), "max_blocks"), (dict(cache=cache(dtype=1)), "cache dtype"),
+    (dict(cache=cache(dtype=2, k_scale=0)), "k_scale"), (dict(table=None), "block_table"), (dict(cu=ODD), "cu"),
+    (dict(k=None), "k_out"), (dict(v=ODD), "v_out"),
+])
+def test_cache_read_refusals(lib, kw, what):  # noqa: F811
+    assert read(lib, **kw) == ck.CK_ERR_INVALID_ARG
+    assert what in ck.ck_last_error()
+
+
+def adapter(lib, **kw):  # noqa: F811
+    f = dict(x=P, a=P, b=P, index=P, scaling=None, residual=None, y=P, M=3, N=16, K=32, rank=8, n=4, dtype=0, out=0, ws=P,
+             nbytes=1 << 40)
+    f.update(kw)
+    return lib.ck_adapter_linear(f["x"], f["a"], f["b"], f["index"], f["scaling"], f["residual"], f["y"], f["M"], f["N"],
+                                 f["K"], f["rank"], f["n"], f["dtype"], f["out"], f["ws"], f["nbytes"], None)
+
+
+@pytest.mark.parametrize("kw,what", [
+    (dict(dtype=2), "dtype"), (dict(out=3), "out_dtype"), (dict(N=12), "multiple of 8"), (dict(K=40), "of 16"),
+    (dict(N=2 ** 31), "2^31"), (dict(rank=12), "rank"), (dict(rank=0), "rank"), (dict(rank=136), "rank"),
+    (dict(n=-1), "num_adapters"), (dict(M=-1), "M must"), (dict(M=2 ** 24 + 1), "M must"), (dict(x=None), "x must"),
+    (dict(a=ODD), "a must"), (dict(b=None), "b must"), (dict(index=None), "index"), (dict(index=ODD), "index"),
+    (dict(scaling=ODD), "scaling"), (dict(residual=ODD), "residual"), (dict(y=None), "y must"), (dict(ws=None), "workspace"),
+    (dict(nbytes=0), "workspace too small"),
+])
+def test_adapter_refusals(lib, kw, what):  # noqa: F811
+    assert adapter(lib, **kw) == ck.CK_ERR_INVALID_ARG
+    assert what in ck.ck_last_error()
+
+
+def logprobs(lib, **kw):  # noqa: F811
+    f = dict(logits=P, stride=50000, tokens=P, rows=3, vocab=50000, dtype=0, scale=1.0, top=4, logprob=P, entropy=P, lse=P,
+             best=P, index=P, ws=P, nbytes=1 << 40)
+    f.update(kw)
+    return lib.ck_token_logprobs(f["logits"], f["stride"], f["tokens"], f["rows"], f["vocab"], f["dtype"], f["scale"],
+                                 f["top"], f["logprob"], f["entropy"], f["lse"], f["best"], f["index"], f["ws"], f["nbytes"],
+                                 None)
+
+
+@pytest.mark.parametrize("kw,what", [
+    (dict(dtype=3), "dtype"), (dict(rows=-1), "rows"), (dict(vocab=0), "vocab"), (dict(vocab=2 ** 31), "vocab"),
+    (dict(stride=49999), "stride"), (dict(top=33), "top"), (dict(top=-1), "top"), (dict(vocab=3), "top"),
+    (dict(scale=0.0), "scale"), (dict(scale=float("nan")), "scale"), (dict(logits=None), "logits"),
+    (dict(logits=ODD), "logits"), (dict(dtype=2, logits=ctypes.c_void_p(4098)), "logits"), (dict(tokens=None), "tokens"),
+    (dict(logprob=ODD), "logprob"), (dict(entropy=ODD), "entropy"), (dict(lse=ODD), "lse"), (dict(best=None), "top_logprob"),
+    (dict(index=None), "top_index"),
+])
+def test_logprobs_refusals(lib, kw, what):  # noqa: F811
+    assert logprobs(lib, **kw) == ck.CK_ERR_INVALID_ARG
+    assert what in ck.ck_last_error()
+
+
+def test_nothing_to_do_is_ok(lib):  # noqa: F811
+    assert prefix(lib, batch=0, q=None) == ck.CK_OK
+    assert read(lib, batch=0, k=None) == ck.CK_OK
+    assert read(lib, total=0, k=None) == ck.CK_OK
+    assert adapter(lib, M=0, x=None, y=None) == ck.CK_OK
+    assert logprobs(lib, rows=0, logits=None) == ck.CK_OK
+
+
+def test_no_device_is_reported_not_faked(lib):  # noqa: F811
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+    for st in (prefix(lib), read(lib), adapter(lib), logprobs(lib)):
+        assert st in (ck.CK_ERR_CUDA, ck.CK_ERR_UNSUPPORTED_DEVICE)
+
+
+def test_workspace_sizes(lib):  # noqa: F811
+    assert lib.ck_prefix_attention_workspace_size(-1, 8, 2, 64, 1, 4096, 4096) == 0
+    assert lib.ck_prefix_attention_workspace_size(4, 8, 2, 64, 1, 2 ** 62, 4096) == 0
+    assert 0 < lib.ck_prefix_attention_workspace_size(256, 32, 8, 128, 3, 1 << 17, 1 << 17) < 1 << 30
+    assert lib.ck_adapter_linear_workspace_size(-1, 8, 16, 8) == 0
+    assert lib.ck_adapter_linear_workspace_size(100, 8, 16, 8) >= 100 * 8 * 4
+    assert lib.ck_token_logprobs_workspace_size(1, 0, 4) == 0
+
+
+def test_binding_checks(lib):  # noqa: F811
+    x = torch.zeros((4, 64), dtype=torch.bfloat16)
+    kv = ck.KVCache(*[torch.zeros((2, 1, 4, 64), dtype=torch.bfloat16)] * 2)
+    with pytest.raises(TypeError):
+        ck.ck_prefix_attention(x.view(4, 1, 64).float(), kv, None, None, None, None, None)
+    with pytest.raises(ValueError):  # not a CUDA tensor
+        ck.ck_prefix_attention(x.view(4, 1, 64), kv, None, None, None, None, None)
+    with pytest.raises(ValueError):
+        ck.ck_cache_read(kv, None, None, 4)
+    with pytest.raises(TypeError):
+        ck.ck_cache_read(kv, None, None, 4, dtype=torch.float32)
+    with pytest.raises(TypeError):
+        ck.ck_adapter_linear(x.float(), x, x, None)
+    with pytest.raises(ValueError):
+        ck.ck_adapter_linear(x, x, x, x)
+    with pytest.raises(TypeError):
+        ck.ck_token_logprobs(x.double())
+    with pytest.raises(ValueError):
+        ck.ck_token_logprobs(x)
