@@ -160,7 +160,7 @@ struct TokenLogprobs {
     void* workspace;
 };
 size_t logprobs_workspace(int64_t rows, int64_t vocab, int top);
-int logprobs_launches(const TokenLogprobs& p, const DeviceInfo& dev);  // kernels that the call enqueues
+int logprobs_launches(const TokenLogprobs& p);  // kernels that the call enqueues
 cudaError_t launch_token_logprobs(const TokenLogprobs& p, const DeviceInfo& dev, cudaStream_t s);
 
 struct Int4Linear {
