@@ -440,7 +440,7 @@ int ck_adapter_linear(const void *x, const void *a, const void *b, const int32_t
  *            only their elements' alignment.  -inf: a token that cannot be (it adds nothing).  A row
  *            that holds a NaN or +inf, or only -inf, has NaN log probabilities and entropy.
  *   tokens:  int32 [rows]; negative: none (logprob 0).  vocab or above: NaN and the error word's bit 7.
- *   scale:   one over the temperature, 1e-30 .. 1e30.
+ *   scale:   one over the temperature, 1e-6 .. 1e6.
  *   logprob, entropy, lse: fp32 [rows], each NULL where it is not wanted (tokens is read with logprob only).
  *   top:     0 .. 32, at most vocab: top_logprob fp32, top_index int32 [rows, top], the largest logits in
  *            descending order, of equal ones the lowest index first, NaN above all others.

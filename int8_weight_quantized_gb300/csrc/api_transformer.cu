@@ -552,8 +552,8 @@ int ck_token_logprobs(const void* logits, int64_t stride, const int32_t* tokens,
                     (long long)vocab);
     if (top < 0 || top > 32 || top > vocab)
         return fail(CK_ERR_INVALID_ARG, "top must be in 0..32 and at most vocab (got %lld)", (long long)top);
-    if (!(scale >= 1e-30f && scale <= 1e30f))
-        return fail(CK_ERR_INVALID_ARG, "scale must be in 1e-30..1e30");
+    if (!(scale >= 1e-6f && scale <= 1e6f))
+        return fail(CK_ERR_INVALID_ARG, "scale must be in 1e-6..1e6");
     if (rows == 0)
         return CK_OK;
     if (logits == nullptr || reinterpret_cast<uintptr_t>(logits) % (dtype == CK_OUT_F32 ? 4 : 2) != 0)

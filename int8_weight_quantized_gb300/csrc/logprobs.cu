@@ -7,7 +7,7 @@
 //
 // Bound: HBM, each logit read once.
 //
-// A row is cut into pieces where there are few rows; a block of 8 warps takes a piece, 16 bytes a lane
+// A row is cut into pieces where there are few rows; a block of 4 warps takes a piece, 32 bytes a lane
 // at a time, each warp with a maximum of its own that its sums are relative to.  A warp meets a new
 // maximum seldom (once in the i-th of its steps with probability 1 / i): one vote a step finds it,
 // together with what else is seldom.  Pieces of a row are joined by a second launch, always in the
@@ -19,10 +19,11 @@
 // large itself.
 //
 // Top alternatives.  Each warp keeps its 32 best as (order of the logit, ~index) in one 64-bit number
-// per lane, in descending order.  What exceeds its `top`-th goes to a buffer in shared memory; 32 of
-// these are sorted and merged at a time (bitonic, 15 and 6 exchanges).  The first step's bar is the
-// `top`-th of the lanes' largest, which as many logits reach.  So any order of the logits gives the
-// same result, at most one merge for 32 logits (ascending ones).
+// per lane, in descending order.  What exceeds the bar, its `top`-th, is inserted one by one, or, where a
+// step brings many, by 32 sorted and merged at a time (bitonic, 15 and 6 exchanges).  The warps tell each
+// other which logit their share of `top` reaches: the lowest of these is a bar for all, at first from
+// the largest of each lane's first loads.  Whatever the order of the logits and of the warps, the result is
+// the same; ascending ones cost one merge for 32.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -37,13 +38,18 @@
 namespace ck {
 namespace {
 
-constexpr int WARPS = 8;
+constexpr int WARPS = 4;
 constexpr int THREADS = WARPS * 32;
-constexpr int DEPTH = 4;                 // 16-byte loads of a lane in flight
+constexpr int BLOCKS = 32 / WARPS;       // of an SM
+constexpr int DEPTH = 1;                 // 32-byte loads of a lane ahead of its work
 constexpr int64_t kLeastPiece = 2048;    // logits
 constexpr int64_t kPieces = 152 * 4;     // as many pieces as blocks fit at once
 constexpr uint32_t FULL = 0xffffffffu;
 constexpr float kNone = -160.0f;         // 2^-160 is 0 in fp32
+// Beside a maximum of at most kFew in size, logits below kFloor add nothing (scale is 1e-6 or more): raised
+// to it, -inf times its term of 0 is no NaN.
+constexpr float kFew = 1e29f, kFloor = -1e30f;
+constexpr float kFar = -1e31f;           // in place of -max: nothing is added
 
 // what a piece leaves: its maximum, sums relative to it, the 32 best
 struct Part {
@@ -51,45 +57,97 @@ struct Part {
     float m, a, b, w;  // w: sum of exp(t) t / ln 2
 };
 
+// 32 bytes of logits: a lane's share of a warp's step.  `floored`: raised to kFloor.
+struct alignas(32) Words {
+    uint32_t r[8];
+};
+// (where !there the words stay as they are)
+__device__ __forceinline__ void load_words(Words& w, const Words* p, bool there)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %9, 0;\n\t"
+        "@p ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t}"
+        : "+r"(w.r[0]), "+r"(w.r[1]), "+r"(w.r[2]), "+r"(w.r[3]), "+r"(w.r[4]), "+r"(w.r[5]), "+r"(w.r[6]), "+r"(w.r[7])
+        : "l"(p), "r"((uint32_t)there));
+}
+
 template <int TYPE>
 struct Logit;
 template <>
 struct Logit<CK_OUT_F32> {
     using T = float;
-    static constexpr int VEC = 4;
+    static constexpr int N = 8;
+    static constexpr uint32_t LOW = 0xff800000u;  // -inf in all places
+    Words v;
     static __device__ __forceinline__ float at(const T* p) { return __ldg(p); }
-    static __device__ __forceinline__ void unpack(const uint4& v, float (&x)[VEC])
+    __device__ __forceinline__ void values(float (&x)[N]) const
     {
-        x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y), x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            x[i] = __uint_as_float(v.r[i]);
     }
-    static __device__ __forceinline__ float top(const uint4&, const float (&x)[VEC])
+    __device__ __forceinline__ void floored(float (&x)[N]) const
     {
-        return max_nan(max_nan(x[0], x[1]), max_nan(x[2], x[3]));
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            x[i] = max_nan(__uint_as_float(v.r[i]), kFloor);
+    }
+    __device__ __forceinline__ float largest() const
+    {
+        float x[N];
+        values(x);
+#pragma unroll
+        for (int n = N / 2; n > 0; n /= 2)
+#pragma unroll
+            for (int i = 0; i < n; ++i)
+                x[i] = max_nan(x[i], x[i + n]);
+        return x[0];
     }
 };
 template <class E>
 struct Logit16 {
     using T = typename E::T;
-    static constexpr int VEC = 8;
+    using T2 = typename E::T2;
+    static constexpr int N = 16;
+    static constexpr uint32_t LOW = std::is_same<E, Bf16>::value ? 0xff80ff80u : 0xfc00fc00u;
+    Words v;
     static __device__ __forceinline__ float at(const T* p) { return E::to(__ldg(p)); }
-    static __device__ __forceinline__ void unpack(const uint4& v, float (&x)[VEC])
+    __device__ __forceinline__ T2 pair(int i) const { return *reinterpret_cast<const T2*>(&v.r[i]); }
+    static __device__ __forceinline__ float2 wide(const T2& h) { return E::to2(*reinterpret_cast<const uint32_t*>(&h)); }
+    __device__ __forceinline__ void values(float (&x)[N]) const
     {
-        const uint32_t r[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = E::to2(r[i]);
+        for (int i = 0; i < N / 2; ++i) {
+            const float2 f = wide(pair(i));
             x[2 * i] = f.x, x[2 * i + 1] = f.y;
         }
     }
-    static __device__ __forceinline__ float top(const uint4& v, const float (&)[VEC])
+    __device__ __forceinline__ void floored(float (&x)[N]) const
     {
-        const uint32_t r[4] = {v.x, v.y, v.z, v.w};
-        typename E::T2 h[4];
+        // bf16 as pairs, half the instructions; fp16 has no such number
+        constexpr bool PAIRS = std::is_same<E, Bf16>::value;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            h[i] = *reinterpret_cast<const typename E::T2*>(&r[i]);
-        const typename E::T2 m = __hmax2_nan(__hmax2_nan(h[0], h[1]), __hmax2_nan(h[2], h[3]));
-        const float2 f = E::to2(*reinterpret_cast<const uint32_t*>(&m));
+        for (int i = 0; i < N / 2; ++i) {
+            float2 f;
+            if constexpr (PAIRS)
+                f = wide(__hmax2_nan(pair(i), __float2bfloat162_rn(kFloor)));
+            else
+                f = wide(pair(i)), f = make_float2(max_nan(f.x, kFloor), max_nan(f.y, kFloor));
+            x[2 * i] = f.x, x[2 * i + 1] = f.y;
+        }
+    }
+    __device__ __forceinline__ float largest() const
+    {
+        T2 m[N / 2];
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i)
+            m[i] = pair(i);
+#pragma unroll
+        for (int n = N / 4; n > 0; n /= 2)
+#pragma unroll
+            for (int i = 0; i < n; ++i)
+                m[i] = __hmax2_nan(m[i], m[i + n]);
+        const float2 f = wide(m[0]);
         return max_nan(f.x, f.y);
     }
 };
@@ -97,6 +155,14 @@ template <>
 struct Logit<CK_OUT_BF16> : Logit16<Bf16> {};
 template <>
 struct Logit<CK_OUT_F16> : Logit16<Fp16> {};
+// one logit a lane
+struct OneLogit {
+    static constexpr int N = 1;
+    float v;
+    __device__ __forceinline__ void values(float (&x)[N]) const { x[0] = v; }
+    __device__ __forceinline__ void floored(float (&x)[N]) const { x[0] = max_nan(v, kFloor); }
+    __device__ __forceinline__ float largest() const { return v; }
+};
 
 // Logits as integers in their order: NaN above +inf, -0 and +0 equal; never 0.
 __device__ __forceinline__ uint32_t order_of(float x)
@@ -132,6 +198,20 @@ __device__ __forceinline__ uint64_t exchange(uint64_t k, int m, bool down)
 }
 
 // 32 numbers in descending order over the lanes
+__device__ __forceinline__ uint32_t exchange(uint32_t k, int m, bool down)
+{
+    const uint32_t o = __shfl_xor_sync(FULL, k, m);
+    return ((threadIdx.x & m) == 0) == down ? max(o, k) : min(o, k);
+}
+__device__ __forceinline__ uint32_t sorted(uint32_t k)
+{
+#pragma unroll
+    for (int size = 2; size <= 32; size *= 2)
+#pragma unroll
+        for (int m = size / 2; m > 0; m /= 2)
+            k = exchange(k, m, size == 32 || (threadIdx.x & size) == 0);
+    return k;
+}
 __device__ __forceinline__ uint64_t sorted(uint64_t k)
 {
 #pragma unroll
@@ -172,104 +252,146 @@ __device__ __forceinline__ void rescale(float& a, float& b, float& w, float delt
 }
 
 // A warp's way through its logits.
-template <int TYPE, bool TOP>
+template <bool TOP>
 struct Warp {
-    using L = Logit<TYPE>;
-    static constexpr int VEC = L::VEC;
     float c;         // scale / ln 2
     float near;      // what is above m - near is above 1/4
     float m = -INFINITY, ref = 0.0f;  // the maximum, and it or 0 where there is none yet
-    float a = 0.0f, b = 0.0f, w = 0.0f;
-    int top = 0;
+    float a = 0.0f;
+    float2 b = {0.0f, 0.0f}, w = {0.0f, 0.0f};
+    int top = 0, share = 0;
     uint64_t best = 0;
-    float bar = NAN;      // what is not <= bar goes to the buffer
-    bool fresh = true;
-    uint64_t* buffer = nullptr;  // [64]
-    int waiting = 0;
+    float bar = NAN;      // what is not <= bar may be among the best
+    uint64_t* buffer = nullptr;           // [64]
+    volatile uint32_t* shared = nullptr;  // [WARPS] orders that `share` logits of each warp reach
 
-    __device__ __forceinline__ void set_bar()
+    // Its own `top`-th, or what every warp has its share of `top` at or above: no less than `top` of the row.
+    __device__ __forceinline__ void raise_bar()
     {
-        const uint64_t k = __shfl_sync(FULL, best, top - 1);
-        bar = k == 0 ? NAN : value_of((uint32_t)(k >> 32));
-    }
-    __device__ __forceinline__ void merge_waiting()
-    {
-        __syncwarp();
         const int lane = threadIdx.x & 31;
-        best = absorb(best, lane < waiting ? buffer[lane] : 0);
-        const uint64_t rest = lane + 32 < waiting ? buffer[lane + 32] : 0;
-        __syncwarp();
-        buffer[lane] = rest;
-        waiting = max(waiting - 32, 0);
-        set_bar();
-        __syncwarp();
+        const uint32_t order = (uint32_t)(best >> 32);
+        const uint32_t last = __shfl_sync(FULL, order, top - 1);
+        if (lane == share - 1 && order > shared[threadIdx.x >> 5])
+            shared[threadIdx.x >> 5] = order;
+        const uint32_t all = __reduce_min_sync(FULL, shared[lane & (WARPS - 1)]);
+        float v = all > last ? below(all) : value_of(last);
+        if (last == 0 && all == 0)
+            v = NAN;
+        bar = v <= bar ? bar : v;
     }
-    // logits x[i] with index first + i, of which those in `valid` are there; largest: of these
-    template <int N>
-    __device__ __forceinline__ void take(const float (&x)[N], float largest, uint32_t first, uint32_t valid)
+    __device__ __forceinline__ void insert(uint64_t key)
     {
-        if (TOP) {
-            if (fresh) {
-                fresh = false;
-                const uint64_t k = __shfl_sync(FULL, sorted(valid ? (uint64_t)order_of(largest) << 32 | 1u : 0), top - 1);
-                if (k != 0)
-                    bar = below((uint32_t)(k >> 32));
+        const int lane = threadIdx.x & 31;
+        const int n = __popc(__ballot_sync(FULL, best > key));
+        const uint64_t up = __shfl_up_sync(FULL, best, 1);
+        best = lane < n ? best : lane == n ? key : up;
+    }
+    // the step's candidates: bit i of `found`, x[i], index first + i
+    template <int N>
+    __device__ __forceinline__ void keep(const float (&x)[N], uint32_t first, uint32_t found)
+    {
+        const int lane = threadIdx.x & 31;
+        int waiting = 0;
+        const bool few = __reduce_add_sync(FULL, __popc(found)) <= 6;
+        uint32_t with;
+        while ((with = __ballot_sync(FULL, found != 0)) != 0) {
+            const int i = found ? __ffs(found) - 1 : 0;
+            float v = x[0];
+#pragma unroll
+            for (int n = 1; n < N; ++n)
+                v = n == i ? x[n] : v;
+            const uint64_t key = (uint64_t)order_of(v) << 32 | (FULL - (first + i));
+            if (few) {
+                const int from = __ffs(with) - 1;
+                insert(__shfl_sync(FULL, key, from));
+                if (lane == from)
+                    found &= found - 1;
+                continue;
             }
-            if (__any_sync(FULL, valid && !(largest <= bar))) {
+            if (found)
+                buffer[waiting + __popc(with & ((1u << lane) - 1u))] = key;
+            found &= found - 1;
+            waiting += __popc(with);
+            __syncwarp();
+            if (waiting >= 32) {
+                best = absorb(best, buffer[lane]);
+                const uint64_t rest = buffer[lane + 32];
+                __syncwarp();
+                buffer[lane] = rest;
+                waiting -= 32;
+                __syncwarp();
+            }
+        }
+        if (waiting > 0)
+            best = absorb(best, lane < waiting ? buffer[lane] : 0);
+        __syncwarp();
+        raise_bar();
+    }
+    // a step: logits with index first + i, where `there` (elsewhere numbers that the row has had before)
+    template <class S>
+    __device__ __forceinline__ void take(const S& step, uint32_t first, bool there)
+    {
+        constexpr int N = S::N;
+        const float largest = there ? step.largest() : -INFINITY;
+        float x[N];
+        if (TOP) {
+            if (__any_sync(FULL, there && !(largest <= bar))) {
+                step.values(x);
                 uint32_t found = 0;
 #pragma unroll
                 for (int i = 0; i < N; ++i)
                     found |= !(x[i] <= bar) ? 1u << i : 0u;
-                found &= valid;
-                while (__any_sync(FULL, found != 0)) {
-                    const uint32_t with = __ballot_sync(FULL, found != 0);
-                    if (found) {
-                        const int i = __ffs(found) - 1;
-                        found &= found - 1;
-                        float v = x[0];
-#pragma unroll
-                        for (int n = 1; n < N; ++n)
-                            v = n == i ? x[n] : v;
-                        buffer[waiting + __popc(with & ((1u << (threadIdx.x & 31)) - 1u))] =
-                            (uint64_t)order_of(v) << 32 | (FULL - (first + i));
-                    }
-                    waiting += __popc(with);
-                    if (waiting >= 32)
-                        merge_waiting();
-                }
+                keep(x, first, there ? found : 0u);
             }
         }
-        if (__any_sync(FULL, !(largest <= m - near))) {
+        if (__any_sync(FULL, !(largest <= m)) || !(fabsf(m) <= kFew)) {
             float high = largest;
 #pragma unroll
             for (int o = 16; o; o >>= 1)
                 high = max_nan(high, __shfl_xor_sync(FULL, high, o));
             if (!(high <= m)) {
-                rescale(a, b, w, (m - high) * c);
+                float b1 = b.x + b.y, w1 = w.x + w.y;
+                rescale(a, b1, w1, (m - high) * c);
+                b = make_float2(b1, 0.0f), w = make_float2(w1, 0.0f);
                 m = ref = high;
             }
+            if (!(fabsf(m) <= kFew)) {
+                step.values(x);
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const float t = max_nan(there ? (x[i] - ref) * c : kNone, kNone);
+                    const float e = fast_exp2(t);
+                    a += e > 0.25f ? e : 0.0f;
+                    b.x += e > 0.25f ? 0.0f : e;
+                    w.x = fmaf(e, t, w.x);
+                }
+                return;
+            }
+        }
+        step.floored(x);
+        const float mine = there ? -ref : kFar;
+        const float2 ref2 = make_float2(mine, mine), c2 = make_float2(c, c);
+        const bool big = __any_sync(FULL, !(largest <= m - near));  // the same for the warp
+        float2 b2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            const float2 t = f2_mul_rn(f2_add_rn(make_float2(x[i], i + 1 < N ? x[i + 1] : kFloor), ref2), c2);
+            x[i] = fast_exp2(t.x);
+            float y = fast_exp2(t.y);
+            if (i + 1 < N)
+                x[i + 1] = y;
+            w = f2_fma_rn(make_float2(x[i], y), t, w);
+            if (!big)
+                b2 = f2_add_rn(b2, make_float2(x[i], y));
+        }
+        if (big) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const float t = max_nan((x[i] - ref) * c, kNone);
-                const float e = fast_exp2(t);
-                a += e > 0.25f ? e : 0.0f;
-                b += e > 0.25f ? 0.0f : e;  // (NaN too)
-                w = fmaf(e, t, w);
+                a += x[i] > 0.25f ? x[i] : 0.0f;
+                b2.x += x[i] > 0.25f ? 0.0f : x[i];  // (NaN too)
             }
-        } else {
-            const float2 ref2 = make_float2(-ref, -ref), c2 = make_float2(c, c);
-            float2 b2 = make_float2(b, 0.0f), w2 = make_float2(w, 0.0f);
-#pragma unroll
-            for (int i = 0; i < N; i += 2) {
-                float2 t = f2_mul_rn(f2_add_rn(make_float2(x[i], i + 1 < N ? x[i + 1] : -INFINITY), ref2), c2);
-                t.x = max_nan(t.x, kNone), t.y = max_nan(t.y, kNone);
-                const float2 e = make_float2(fast_exp2(t.x), fast_exp2(t.y));
-                b2 = f2_add_rn(b2, e);
-                w2 = f2_fma_rn(e, t, w2);
-            }
-            b = b2.x + b2.y;
-            w = w2.x + w2.y;
         }
+        b = f2_add_rn(b, b2);
     }
 };
 
@@ -324,72 +446,86 @@ __device__ __forceinline__ void leave(const TokenLogprobs& p, int64_t row, float
 }
 
 template <int TYPE, bool TOP>
-__global__ void __launch_bounds__(THREADS, 4) piece_kernel(const TokenLogprobs p, int pieces, int64_t piece, unsigned int* err)
+__global__ void __launch_bounds__(THREADS, BLOCKS) piece_kernel(const TokenLogprobs p, int pieces, int64_t piece, unsigned int* err)
 {
     using L = Logit<TYPE>;
     using T = typename L::T;
-    constexpr int VEC = L::VEC;
+    constexpr int VEC = L::N;
     griddep_wait();
     __shared__ uint64_t buffers[WARPS][64];
     __shared__ float sums[WARPS][4];
+    __shared__ uint32_t reached[WARPS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t row = blockIdx.x / pieces;
     const int number = (int)(blockIdx.x - row * pieces);
     const int64_t j0 = min(number * piece, p.vocab), j1 = min(j0 + piece, p.vocab);
     const T* x = static_cast<const T*>(p.logits) + row * p.stride;
 
-    Warp<TYPE, TOP> me;
+    Warp<TOP> me;
     me.c = p.scale * kLog2e;
     me.near = 2.0f / me.c;
     me.top = p.top;
+    me.share = (p.top + WARPS - 1) / WARPS;
     me.buffer = buffers[warp];
+    me.shared = reached;
 
-    // whole 16-byte vectors between v0 and v1; up to VEC - 1 logits on either side are warp 0's last step
+    // whole 32-byte vectors between v0 and v1; up to VEC - 1 logits on either side are warp 0's last step
+    static_assert(2 * (VEC - 1) <= 32, "one step for both ends");
     const int skew = (int)((reinterpret_cast<uintptr_t>(x + j0) / sizeof(T)) % VEC);
     const int64_t v0 = min(j0 + (skew ? VEC - skew : 0), j1), vectors = (j1 - v0) / VEC, v1 = v0 + vectors * VEC;
-    const uint4* src = reinterpret_cast<const uint4*>(x + v0);
-    const uint32_t low = (uint32_t)(TYPE == CK_OUT_F32 ? 0xff800000u : TYPE == CK_OUT_F16 ? 0xfc00fc00u : 0xff80ff80u);
-    auto load = [&](int64_t v) {
-        return v < vectors ? __ldcs(src + v) : make_uint4(low, low, low, low);
-    };
-    uint4 ahead[DEPTH];
-    int64_t v = threadIdx.x;
+    const Words* src = reinterpret_cast<const Words*>(x + v0);
+    const int count = (int)vectors;
+    Words ahead[DEPTH];
+    int v = threadIdx.x;
 #pragma unroll
-    for (int d = 0; d < DEPTH; ++d)
-        ahead[d] = load(v + d * THREADS);
-    for (; v - lane < vectors; v += DEPTH * THREADS) {
+    for (int d = 0; d < DEPTH; ++d) {
 #pragma unroll
-        for (int d = 0; d < DEPTH; ++d) {
-            const uint4 now = ahead[d];
-            const int64_t at = v + d * THREADS;
-            ahead[d] = load(at + DEPTH * THREADS);
-            if (at - lane < vectors) {  // the same for the warp
-                float f[VEC];
-                L::unpack(now, f);
-                me.take(f, L::top(now, f), (uint32_t)(v0 + at * VEC), at < vectors ? (1u << VEC) - 1u : 0u);
-            }
-        }
+        for (int i = 0; i < 8; ++i)
+            ahead[d].r[i] = L::LOW;
+        load_words(ahead[d], src + v + d * THREADS, v + d * THREADS < count);
+    }
+    if (TOP) {
+        // the first bar, from the largest that each lane finds in its first loads
+        uint32_t high = 0;
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d)
+            high = max(high, v + d * THREADS < count ? order_of(L{ahead[d]}.largest()) : 0u);
+        high = me.share == 1 ? __reduce_max_sync(FULL, high) : sorted(high);
+        if (lane == me.share - 1)
+            reached[warp] = high;
+        __syncthreads();
+        me.raise_bar();
+    }
+    const uint32_t from = (uint32_t)v0;
+    // (not unrolled: with its seldom taken branches twice or more the loop outgrows the instruction cache)
+#pragma unroll 1
+    for (; v - lane < count; v += THREADS) {
+        const L now{ahead[0]};
+#pragma unroll
+        for (int d = 0; d + 1 < DEPTH; ++d)
+            ahead[d] = ahead[d + 1];
+        load_words(ahead[DEPTH - 1], src + v + DEPTH * THREADS, v + DEPTH * THREADS < count);
+        me.take(now, from + (uint32_t)v * VEC, v < count);
     }
     if (warp == 0 && (v0 > j0 || j1 > v1)) {
         const int64_t j = lane < v0 - j0 ? j0 + lane : v1 + (lane - (v0 - j0));
         const bool there = lane < (v0 - j0) + (j1 - v1);
-        if (TOP && !me.fresh && me.bar == me.bar)  // of equal ones these may come first
+        const OneLogit now{there ? L::at(x + j) : -INFINITY};
+        if (TOP && me.bar == me.bar)  // of equal ones these may come first
             me.bar = below(order_of(me.bar));
-        const float f[1] = {there ? L::at(x + j) : -INFINITY};
-        me.take(f, f[0], (uint32_t)j, there ? 1u : 0u);
+        me.take(now, (uint32_t)j, there);
     }
-    if (TOP && me.waiting > 0)
-        me.merge_waiting();
 
     // ---- the warps' parts as one
+    float part_b = me.b.x + me.b.y, part_w = me.w.x + me.w.y;
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
         me.a += __shfl_xor_sync(FULL, me.a, o);
-        me.b += __shfl_xor_sync(FULL, me.b, o);
-        me.w += __shfl_xor_sync(FULL, me.w, o);
+        part_b += __shfl_xor_sync(FULL, part_b, o);
+        part_w += __shfl_xor_sync(FULL, part_w, o);
     }
     if (lane == 0)
-        sums[warp][0] = me.m, sums[warp][1] = me.a, sums[warp][2] = me.b, sums[warp][3] = me.w;
+        sums[warp][0] = me.m, sums[warp][1] = me.a, sums[warp][2] = part_b, sums[warp][3] = part_w;
     if (TOP)
         buffers[warp][lane] = me.best;
     __syncthreads();
@@ -420,7 +556,7 @@ __global__ void __launch_bounds__(THREADS, 4) piece_kernel(const TokenLogprobs p
     griddep_launch_dependents();
 }
 
-// The pieces of a row as one: each of the block's warps takes every eighth, then the warps together.
+// The pieces of a row as one: each of the block's warps takes every fourth, then the warps together.
 template <int TYPE, bool TOP>
 __global__ void __launch_bounds__(THREADS) join_kernel(const TokenLogprobs p, int pieces, unsigned int* err)
 {
@@ -431,7 +567,7 @@ __global__ void __launch_bounds__(THREADS) join_kernel(const TokenLogprobs p, in
     const int64_t row = blockIdx.x;
     const Part* parts = static_cast<const Part*>(p.workspace) + row * pieces;
     const float c = p.scale * kLog2e;
-    // (a lane takes pieces 32 apart: more than 256 pieces of a row only where it is longer than 2^19)
+    // (a lane takes more than one piece where a row has more than 128)
     float m = -INFINITY, a = 0.0f, b = 0.0f, w = 0.0f;
     for (int i = warp + lane * WARPS; i < pieces; i += 32 * WARPS) {
         const float4 f = __ldcg(reinterpret_cast<const float4*>(&parts[i].m));
