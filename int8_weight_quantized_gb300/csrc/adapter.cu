@@ -28,6 +28,7 @@
 #include <cuda_fp16.h>
 
 #include "attn_common.cuh"
+#include "tensor_core.cuh"
 #include "transformer.h"
 #include "warp_mma.cuh"
 
@@ -173,35 +174,217 @@ __global__ void __launch_bounds__(THREADS) shrink_few_kernel(const AdapterLinear
     }
 }
 
-// ---- many rows: one warp per (row, rank)
-template <class E>
-__global__ void __launch_bounds__(THREADS) shrink_many_kernel(const AdapterLinear p, unsigned int* err)
+// ---- many rows: h of 128 rows over one part of K, for one adapter after the other of those that they have
+//   warp 0       copies 128 x 64 of x and rank x 64 of A by TMA through the ring;
+//   warp 1       issues the products, one lane; the sums of two adapters have room in tensor memory;
+//   warps 2 - 5  leave the rows of a finished adapter.
+// Measured (GB300): see expand_kernel.
+constexpr int MANY_THREADS = 192;
+constexpr uint32_t X_BYTES = TILE * 128;
+constexpr uint32_t RING_BYTES = 96 * 1024;  // of two blocks on an SM
+constexpr int MOST_STAGES = 6;
+
+// columns of an adapter's sums (the instruction wants a multiple of 16; more are other adapters' or zeros)
+__host__ __device__ constexpr int columns_of(int rank)
 {
-    using T = typename E::T;
+    return (rank + 15) / 16 * 16;
+}
+
+template <class E>
+__global__ void __launch_bounds__(MANY_THREADS, 2)
+    shrink_many_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmA, const AdapterLinear p,
+                       int splits, unsigned int* err)
+{
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint32_t key[TILE];
+    __shared__ uint32_t list[TILE];
+    __shared__ uint64_t bars[2 * MOST_STAGES + 5];
+    __shared__ int found[4];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int aborted;
+    uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int columns = columns_of(p.rank);
+    const uint32_t stage_bytes = X_BYTES + columns * 128;
+    const int stages = min((int)(RING_BYTES / stage_bytes), MOST_STAGES);
+    uint64_t *full = bars, *empty = bars + MOST_STAGES, *done = bars + 2 * MOST_STAGES, *taken = done + 2, *drain = taken + 2;
+    volatile int* abort_flag = &aborted;
+    const int warp = __shfl_sync(FULL, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    uint32_t tmem_columns = 32;
+    while (tmem_columns < 2u * columns)
+        tmem_columns *= 2;
+    if (warp == 0 && lane == 0) {
+        for (int i = 0; i < MOST_STAGES; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&done[i], 1);
+            mbar_init(&taken[i], 4);
+        }
+        mbar_init(drain, 1);
+        aborted = 0;
+        fence_mbar_init();
+        fence_proxy_async_smem();
+        tma_prefetch_desc(&tmX);
+        tma_prefetch_desc(&tmA);
+    }
+    if (warp == 1) {
+        tmem_alloc(&tmem_slot, tmem_columns);
+        tmem_relinquish();
+    }
+    __syncwarp();
     griddep_wait();
     griddep_launch_dependents();
-    const int lane = threadIdx.x & 31;
-    const int64_t unit = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int64_t m = unit / p.rank;
-    const int r = (int)(unit - m * p.rank);
-    if (m >= p.M)
-        return;
-    const int i = __ldg(p.index + m);
-    if (i >= p.adapters) {
-        if (lane == 0 && r == 0)
-            atomicOr(err, kErrIndex);
-    } else if (i >= 0) {
-        const T* x = static_cast<const T*>(p.x) + m * p.K;
-        const T* a = static_cast<const T*>(p.a) + ((int64_t)i * p.rank + r) * p.K;
-        float sum = 0.0f;
-        for (int64_t k = lane; k < p.K; k += 32)
-            sum = fmaf(E::to(x[k]), E::to(a[k]), sum);
-#pragma unroll
-        for (int o = 16; o; o >>= 1)
-            sum += __shfl_xor_sync(FULL, sum, o);
-        if (lane == 0)
-            static_cast<float*>(p.workspace)[m * p.rank + r] = sum;
+    // the tile's adapters, in the order of their first rows
+    const int64_t first = blockIdx.x / splits * TILE;
+    const int split = (int)(blockIdx.x % splits);
+    const int m = threadIdx.x;
+    uint32_t mine = (uint32_t)p.adapters;
+    if (m < TILE) {
+        if (first + m < p.M) {
+            const int32_t i = __ldg(p.index + first + m);
+            mine = i < 0 ? (uint32_t)p.adapters : (int64_t)i < p.adapters ? (uint32_t)i : (uint32_t)p.adapters + 1u;
+            if (mine > p.adapters && split == 0)
+                atomicOr(err, kErrIndex);
+        }
+        key[m] = mine;
     }
+    __syncthreads();
+    bool leads = m < TILE && mine < p.adapters;
+    for (int n = 0; leads && n < m; ++n)
+        leads = key[n] != mine;
+    const uint32_t leaders = __ballot_sync(FULL, leads);
+    if (lane == 0 && m < TILE)
+        found[warp] = __popc(leaders);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    int count = 0, before = 0;
+    for (int w = 0; w < 4; ++w) {
+        before += w < warp ? found[w] : 0;
+        count += found[w];
+    }
+    if (leads)
+        list[before + __popc(leaders & ((1u << lane) - 1u))] = mine;
+    __syncthreads();
+    const uint32_t tmem = __shfl_sync(FULL, tmem_slot, 0);
+    const int boxes = (int)((p.K + 63) / 64);
+    const int b0 = (int)((int64_t)split * boxes / splits), b1 = (int)((int64_t)(split + 1) * boxes / splits);
+    const int per = b1 - b0, uses = count * per;  // of the ring
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int issued = 0;
+            for (int n = 0; n < count && issued == n * per; ++n) {
+                const int32_t a_row = (int32_t)(list[n] * (uint32_t)p.rank);
+                for (int i = b0; i < b1; ++i) {
+                    const int s = issued % stages;
+                    if (!mbar_wait(&empty[s], (uint32_t)(issued / stages + 1) & 1u, abort_flag, err, kErrWaitAdapter, TIMEOUT_NS))
+                        break;
+                    uint8_t* dst = ring + s * stage_bytes;
+                    mbar_arrive_expect_tx(&full[s], stage_bytes);
+                    tma_load_2d(dst, &tmX, &full[s], 64 * i, (int32_t)first);
+                    tma_load_2d(dst + X_BYTES, &tmA, &full[s], 64 * i, a_row);
+                    ++issued;
+                }
+            }
+            if (issued < uses)  // aborting: every issued copy lands before shared memory is released
+                for (int i = max(issued - stages, 0); i < issued; ++i)
+                    wait_out(&full[i % stages], (uint32_t)(i / stages) & 1u, err, kErrWaitAdapter, TIMEOUT_NS);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        const uint32_t idesc = idesc_of<E>(columns, false);
+        const uint64_t x_desc = desc_kmajor_sw128(smem_u32(ring)), a_desc = desc_kmajor_sw128(smem_u32(ring) + X_BYTES);
+        const bool leader = elect_one();
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            const bool ok = mbar_wait(bar, parity, abort_flag, err, kErrWaitAdapter, TIMEOUT_NS);
+            return __all_sync(FULL, ok) != 0;
+        };
+        bool ok = true;
+        for (int use = 0; ok && use < uses; ++use) {
+            const int n = use / per, s = use % stages;
+            const bool begins = use == n * per;
+            // the sums of the adapter before the last are out of the way
+            ok = (!begins || n < 2 || wait(&taken[n & 1], (uint32_t)(n / 2 + 1) & 1u)) &&
+                 wait(&full[s], (uint32_t)(use / stages) & 1u);
+            if (!ok)
+                break;
+            tc_fence_after();
+            if (leader) {
+                const uint64_t at = (uint64_t)(s * (stage_bytes >> 4));
+                mma_bf16_kblock<false>(tmem + (n & 1) * columns, x_desc + at, a_desc + at, idesc, !begins);
+                mma_commit(&empty[s]);
+                if (use + 1 == (n + 1) * per)
+                    mma_commit(&done[n & 1]);
+            }
+            __syncwarp();
+        }
+        // every product must be complete before tensor and shared memory are released
+        if (leader) {
+            mma_commit(drain);
+            wait_out(drain, 0, err, kErrWaitAdapter, TIMEOUT_NS);
+        }
+        __syncwarp();
+    } else {
+        const int quarter = warp & 3;  // tensor memory lanes that this warp may access
+        const int row = quarter * 32 + lane;
+        float* out = static_cast<float*>(p.workspace) + ((int64_t)split * p.M + first + row) * p.rank;
+        bool ok = true;
+        for (int n = 0; n < count; ++n) {
+            if (per > 0)
+                ok = ok && mbar_wait(&done[n & 1], (uint32_t)(n / 2) & 1u, abort_flag, err, kErrWaitAdapter, TIMEOUT_NS);
+            ok = __all_sync(FULL, ok);
+            tc_fence_after();
+            const bool store = key[row] == list[n];
+            for (int c = 0; c < p.rank; c += 16) {
+                uint32_t v[16];
+                if (ok && per > 0) {
+                    tmem_ld_32x32b_x16(tmem + ((uint32_t)(quarter * 32) << 16) + (n & 1) * columns + c, v);
+                    tmem_wait_ld();
+                }
+                if (store)
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4)
+                        if (c + i < p.rank)
+                            *reinterpret_cast<uint4*>(out + c + i) =
+                                !ok ? make_uint4(0x7fffffffu, 0x7fffffffu, 0x7fffffffu, 0x7fffffffu)
+                                    : per > 0 ? make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]) : make_uint4(0u, 0u, 0u, 0u);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (ok && lane == 0)
+                mbar_arrive(&taken[n & 1]);
+            __syncwarp();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, tmem_columns);
+    }
+}
+
+// [rows, K] of 16 bits as boxes of `box_rows` x 64.
+bool make_map_2d(CUtensorMap* map, const void* base, int64_t rows, int64_t K, int box_rows, bool f16, std::string* why)
+{
+    auto fn = encode_fn();
+    if (!fn) {
+        *why = "cuTensorMapEncodeTiled is not available from the driver";
+        return false;
+    }
+    cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)K * 2};
+    cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    const CUresult r = fn(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                          const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        *why = "cuTensorMapEncodeTiled failed (" + std::to_string((int)r) + ")";
+    return r == CUDA_SUCCESS;
 }
 
 // ---- 8 neighbouring outputs of a lane
@@ -384,12 +567,23 @@ __global__ void __launch_bounds__(THREADS) expand_kernel(const AdapterLinear p, 
     griddep_launch_dependents();
 }
 
-// Parts of K.
+// Parts of K.  Few rows: enough steps for a block's warps; many: blocks that fill the rounds of two to
+// an SM well, a part at least 4 boxes of 64.
+constexpr int64_t kSlots = 304;
 int splits_of(int64_t M, int64_t K)
 {
-    if (M > kFewRows)
-        return 1;
-    return (int)std::min<int64_t>(8, std::max<int64_t>(1, K / 512));
+    if (M <= kFewRows)
+        return (int)std::min<int64_t>(8, std::max<int64_t>(1, K / 512));
+    const int64_t tiles = (M + TILE - 1) / TILE, boxes = (K + 63) / 64;
+    int best = 1;
+    double least = INFINITY;
+    for (int s = 1; s <= 16 && (s == 1 || boxes / s >= 4); ++s) {
+        // rounds of blocks, each as long as its boxes and a fixed cost of about 6
+        const double cost = (double)((tiles * s + kSlots - 1) / kSlots) * ((double)((boxes + s - 1) / s) + 6.0);
+        if (cost < 0.98 * least)
+            least = cost, best = s;
+    }
+    return best;
 }
 
 }  // namespace
@@ -399,7 +593,7 @@ size_t adapter_workspace(int64_t M, int64_t, int64_t K, int rank)
     return (size_t)splits_of(M, K) * M * rank * sizeof(float);
 }
 
-cudaError_t launch_adapter_linear(const AdapterLinear& p, const DeviceInfo& dev, cudaStream_t s)
+cudaError_t launch_adapter_linear(const AdapterLinear& p, const DeviceInfo& dev, cudaStream_t s, std::string* why)
 {
     unsigned int* err = nullptr;
     const cudaError_t e = device_error_ptr(&err);
@@ -416,8 +610,26 @@ cudaError_t launch_adapter_linear(const AdapterLinear& p, const DeviceInfo& dev,
     const unsigned expand = (unsigned)(tiles * ((p.N + chunk - 1) / chunk));
     auto shrink = [&](auto type) {
         using E = decltype(type);
-        if (!few)
-            return launch_pdl(shrink_many_kernel<E>, dim3((unsigned)((p.M * p.rank + 7) / 8)), dim3(THREADS), 0, s, p, err);
+        if (!few) {
+            // a kernel attribute belongs to the context it was set in: set once per context
+            constexpr int SMEM = RING_BYTES + 1024;
+            static ContextCache<int> cache;
+            int done = 0;
+            const cudaError_t r = cache.get(&done, [](int* d) {
+                *d = 1;
+                return cudaFuncSetAttribute(shrink_many_kernel<E>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+            });
+            if (r != cudaSuccess)
+                return r;
+            CUtensorMap x, a;
+            if (!make_map_2d(&x, p.x, p.M, p.K, TILE, p.f16, why))
+                return cudaErrorInvalidValue;
+            a = x;  // without adapters no block copies any
+            if (p.adapters > 0 && !make_map_2d(&a, p.a, p.adapters * p.rank, p.K, columns_of(p.rank), p.f16, why))
+                return cudaErrorInvalidValue;
+            return launch_pdl(shrink_many_kernel<E>, dim3((unsigned)(tiles * splits)), dim3(MANY_THREADS), (size_t)SMEM, s, x, a,
+                              p, splits, err);
+        }
         auto by_rank = [&](auto rt) {
             return launch_pdl(shrink_few_kernel<E, decltype(rt)::value>, dim3((unsigned)(p.M * splits)), dim3(THREADS), 0, s, p,
                               splits, err);

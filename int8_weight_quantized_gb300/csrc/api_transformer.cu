@@ -484,8 +484,9 @@ int ck_adapter_linear(const void* x, const void* a, const void* b, const int32_t
                     (long long)N, (long long)K);
     if (rank < 8 || rank > 128 || rank % 8 != 0)
         return fail(CK_ERR_INVALID_ARG, "rank must be a multiple of 8 in 8..128 (got %lld)", (long long)rank);
-    if (num_adapters < 0 || num_adapters > kMaxCount)
-        return fail(CK_ERR_INVALID_ARG, "num_adapters must be in 0..2^31-1 (got %lld)", (long long)num_adapters);
+    if (num_adapters < 0 || num_adapters > kMaxCount / rank)
+        return fail(CK_ERR_INVALID_ARG, "num_adapters must be >= 0 and num_adapters * rank below 2^31 (got %lld)",
+                    (long long)num_adapters);
     if (M < 0 || M > (1 << 24))
         return fail(CK_ERR_INVALID_ARG, "M must be in 0..16777216 (got %lld)", (long long)M);
     if (M == 0)
@@ -526,9 +527,15 @@ int ck_adapter_linear(const void* x, const void* a, const void* b, const int32_t
     p.workspace = workspace;
     log_shape("adapter_linear", M, N, K, (int)rank, "two low-rank products");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    ProfScope ps(kProfAdapter, 2, s);
-    const cudaError_t e = launch_adapter_linear(p, dev, s);
-    return e == cudaSuccess ? CK_OK : cuda_fail(e, "ck_adapter_linear launch");
+    std::string why;
+    cudaError_t e;
+    {
+        ProfScope ps(kProfAdapter, 2, s);
+        e = launch_adapter_linear(p, dev, s, &why);
+    }
+    if (e != cudaSuccess)
+        return why.empty() ? cuda_fail(e, "ck_adapter_linear launch") : fail(CK_ERR_CUDA, "%s", why.c_str());
+    return CK_OK;
 }
 
 size_t ck_token_logprobs_workspace_size(int64_t rows, int64_t vocab, int64_t top)

@@ -14,6 +14,8 @@ namespace ck {
 enum : uint32_t {
     kErrIndex = 1u << 7,       // a position, length, slot, page or sequence bound was out of range
     kErrWaitAttention = 1u << 8,  // a role of the prompt attention kernel gave up waiting
+    kErrWaitAdapter = 1u << 9,    // a role of the adapters' first product gave up waiting
+    kErrWaitPrefix = 1u << 10,    // a role of the attention over shared prefixes gave up waiting
 };
 
 constexpr float kLog2e = 1.4426950408889634f;

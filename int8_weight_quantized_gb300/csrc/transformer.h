@@ -144,7 +144,7 @@ struct AdapterLinear {
     void* workspace;
 };
 size_t adapter_workspace(int64_t M, int64_t N, int64_t K, int rank);
-cudaError_t launch_adapter_linear(const AdapterLinear& p, const DeviceInfo& dev, cudaStream_t s);
+cudaError_t launch_adapter_linear(const AdapterLinear& p, const DeviceInfo& dev, cudaStream_t s, std::string* why);
 
 struct TokenLogprobs {
     const void* logits;
