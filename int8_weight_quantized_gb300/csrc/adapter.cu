@@ -439,130 +439,158 @@ struct Eight<CK_OUT_F16> : Eight16<Fp16> {
     static __device__ __forceinline__ Eight load(const void* base, int64_t i) { return {{read(base, i)}}; }
 };
 
-// Items are a tile's (group, 32 columns of the block's); a warp takes a run of them.
+// Items are a tile's (group, 32 columns of the block's); a warp takes a run of them, the residual of the
+// next one on its way while it works on one.  h is added up and rounded once for the block, into shared
+// memory; rows are padded so that 8 of them spread over the banks.
+constexpr int kPad = 8;
+__host__ __device__ constexpr int h_bytes(int tile, int rank)
+{
+    return tile * (rank + kPad) * 2;
+}
+
 template <class E, int OUT, int KT>  // KT: steps of 32 of the rank
-__global__ void __launch_bounds__(THREADS) expand_kernel(const AdapterLinear p, int tile, int chunk, int splits)
+__global__ void __launch_bounds__(THREADS, 2) expand_kernel(const AdapterLinear p, int tile, int chunk, int splits)
 {
     using T = typename E::T;
+    extern __shared__ __align__(16) uint8_t h_smem[];  // [tile][rank + kPad] of T
     __shared__ Groups groups;
+    __shared__ float factors[kFewRows];
     const int64_t chunks = (p.N + chunk - 1) / chunk;
     const int64_t first = blockIdx.x / chunks * tile, n_first = blockIdx.x % chunks * chunk;
     const int rows = (int)min(p.M - first, (int64_t)tile);
+    const int columns = (int)min(p.N - n_first, (int64_t)chunk);
     // (the first kernel lets this one begin when its blocks have seen the work before them complete)
     make_groups(groups, p.index, first, rows, p.adapters);
+    // what the block reads of each adapter's B, into L2 while the first kernel runs
+    for (int i = threadIdx.x; i < groups.count; i += THREADS) {
+        const uint32_t adapter = groups.key[groups.row[groups.begin[i]]];
+        if (adapter < p.adapters && (i == 0 || adapter != groups.key[groups.row[groups.begin[i - 1]]]))
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                             static_cast<const T*>(p.b) + ((int64_t)adapter * p.N + n_first) * p.rank),
+                         "r"((uint32_t)columns * (uint32_t)p.rank * 2u)
+                         : "memory");
+    }
     griddep_wait();
+    const int ld = (p.rank + kPad) * 2;
+    {
+        // 8 values a lane, a row to as many lanes as it takes (a power of two)
+        int lanes = 1;
+        while (lanes * 8 < p.rank)
+            lanes *= 2;
+        const int c = threadIdx.x % lanes * 8;
+        for (int m = threadIdx.x / lanes; m < (rows + 31) / 32 * 32; m += THREADS / lanes) {  // (whole warps)
+            const uint32_t adapter = m < rows ? groups.key[m] : (uint32_t)p.adapters;
+            const bool in = adapter < p.adapters && c < p.rank;
+            float v[8] = {};
+            const float* src = static_cast<const float*>(p.workspace) + (first + m) * p.rank + c;
+            if (in)
+#pragma unroll 4
+                for (int s = 0; s < splits; ++s) {
+                    const float4* part = reinterpret_cast<const float4*>(src + (int64_t)s * p.M * p.rank);
+                    const float4 lo = __ldcg(part), hi = __ldcg(part + 1);
+                    v[0] += lo.x, v[1] += lo.y, v[2] += lo.z, v[3] += lo.w;
+                    v[4] += hi.x, v[5] += hi.y, v[6] += hi.z, v[7] += hi.w;
+                }
+            float down = 1.0f, factor = adapter < p.adapters && p.scaling ? __ldg(p.scaling + adapter) : 1.0f;
+            if (std::is_same<E, Fp16>::value) {
+                float top = 0.0f;
+#pragma unroll
+                for (int n = 0; n < 8; ++n)
+                    top = fmaxf(top, fabsf(v[n]));
+                for (int o = 1; o < lanes; o *= 2)
+                    top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
+                const int e = top > 0.0f && top < INFINITY ? max(ilogbf(top), -126) : 0;
+                down = ldexpf(1.0f, -e);  // (both powers are floats for these e)
+                factor *= ldexpf(1.0f, e);
+            }
+            if (in)
+                *reinterpret_cast<uint4*>(h_smem + m * ld + c * 2) =
+                    make_uint4(E::pack2(v[0] * down, v[1] * down), E::pack2(v[2] * down, v[3] * down),
+                               E::pack2(v[4] * down, v[5] * down), E::pack2(v[6] * down, v[7] * down));
+            if (c == 0 && m < rows)
+                factors[m] = factor;
+        }
+    }
+    __syncthreads();
+
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const int steps = (int)((min(p.N - n_first, (int64_t)chunk) + 31) / 32);
+    const int steps = (columns + 31) / 32;
     const int items = groups.count * steps;
     const int i0 = warp * items / WARPS, i1 = (warp + 1) * items / WARPS;
     const bool in_place = p.residual == p.y;
-    int group = -1;
-    uint32_t adapter = 0;
-    int64_t row[2] = {-1, -1};
-    uint32_t h[KT][2][4];
-    float factor[2] = {0.0f, 0.0f};
-    const T* b = nullptr;
-    for (int i = i0; i < i1; ++i) {
-        if (i / steps != group) {
-            group = i / steps;
-            const int begin = groups.begin[group], count = groups.begin[group + 1] - begin;
-            adapter = groups.key[groups.row[begin]];
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-                row[r] = g + 8 * r < count ? first + groups.row[begin + g + 8 * r] : -1;
-            if (adapter < p.adapters) {
-                const float scaling = p.scaling ? __ldg(p.scaling + adapter) : 1.0f;
-                b = static_cast<const T*>(p.b) + (int64_t)adapter * p.N * p.rank + 8 * t;
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    float v[KT][8];
-                    float top = 0.0f;
-#pragma unroll
-                    for (int k = 0; k < KT; ++k) {
-#pragma unroll
-                        for (int n = 0; n < 8; ++n)
-                            v[k][n] = 0.0f;
-                        if (row[r] >= 0 && 32 * k + 8 * t < p.rank) {
-                            const float* src = static_cast<const float*>(p.workspace) + row[r] * p.rank + 32 * k + 8 * t;
-                            for (int s = 0; s < splits; ++s) {
-                                const float4* part = reinterpret_cast<const float4*>(src + (int64_t)s * p.M * p.rank);
-                                const float4 lo = __ldcg(part), hi = __ldcg(part + 1);
-                                v[k][0] += lo.x, v[k][1] += lo.y, v[k][2] += lo.z, v[k][3] += lo.w;
-                                v[k][4] += hi.x, v[k][5] += hi.y, v[k][6] += hi.z, v[k][7] += hi.w;
-                            }
-                        }
-#pragma unroll
-                        for (int n = 0; n < 8; ++n)
-                            top = fmaxf(top, fabsf(v[k][n]));
-                    }
-                    float down = 1.0f;
-                    factor[r] = scaling;
-                    if (std::is_same<E, Fp16>::value) {
-                        top = fmaxf(top, __shfl_xor_sync(FULL, top, 1));
-                        top = fmaxf(top, __shfl_xor_sync(FULL, top, 2));
-                        // (both powers are floats for these e)
-                        const int e = top > 0.0f && top < INFINITY ? max(ilogbf(top), -126) : 0;
-                        down = ldexpf(1.0f, -e);
-                        factor[r] = scaling * ldexpf(1.0f, e);
-                    }
-#pragma unroll
-                    for (int k = 0; k < KT; ++k)
-#pragma unroll
-                        for (int s = 0; s < 2; ++s) {
-                            h[k][s][r] = E::pack2(v[k][4 * s] * down, v[k][4 * s + 1] * down);
-                            h[k][s][2 + r] = E::pack2(v[k][4 * s + 2] * down, v[k][4 * s + 3] * down);
-                        }
-                }
-            }
-        }
-        const int64_t n0 = n_first + 32 * (i - group * steps), n = n0 + 8 * t;
-        const bool here = n < p.N;
-        if (adapter >= p.adapters) {  // none: the residual, or an index out of range: NaN
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-                if (row[r] >= 0 && here && !(in_place && adapter == p.adapters)) {
-                    Eight<OUT> y{};
-                    if (p.residual)
-                        y = Eight<OUT>::load(p.residual, row[r] * p.N + n);
-                    if (adapter > p.adapters) {
-                        const float nan[8] = {NAN, NAN, NAN, NAN, NAN, NAN, NAN, NAN};
-                        y.add(nan);
-                    }
-                    y.store(p.y, row[r] * p.N + n);
-                }
+    int step = i0 % steps;
+    for (int i = i0, group = i0 / steps; i < i1; ++group, step = 0) {
+        const int last = min(steps, step + (i1 - i));  // of this group's steps
+        i += last - step;
+        const int begin = groups.begin[group], count = groups.begin[group + 1] - begin;
+        const uint32_t adapter = groups.key[groups.row[begin]];
+        if (adapter == p.adapters && in_place)
             continue;
+        const bool none = adapter >= p.adapters;
+        bool there[2];
+        int64_t at[2];  // of the lane's outputs of step 0
+        float factor[2];
+        uint32_t h[KT][2][4];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            there[r] = g + 8 * r < count;
+            const int m = there[r] ? groups.row[begin + g + 8 * r] : 0;
+            at[r] = (first + m) * p.N + n_first + 8 * t;
+            factor[r] = adapter > p.adapters ? NAN : factors[m];
+#pragma unroll
+            for (int k = 0; k < KT; ++k) {
+                uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                if (there[r] && !none && 32 * k + 8 * t < p.rank)
+                    w = *reinterpret_cast<const uint4*>(h_smem + m * ld + (32 * k + 8 * t) * 2);
+                h[k][0][r] = w.x, h[k][0][2 + r] = w.y, h[k][1][r] = w.z, h[k][1][2 + r] = w.w;
+            }
         }
-        Eight<OUT> y[2] = {};
-        if (p.residual)
+        const T* b = static_cast<const T*>(p.b) + (none ? 0 : ((int64_t)adapter * p.N + n_first) * p.rank) + 8 * t;
+        Eight<OUT> next[2] = {};
+        auto fetch = [&](int s) {
 #pragma unroll
             for (int r = 0; r < 2; ++r)
-                if (row[r] >= 0 && here)
-                    y[r] = Eight<OUT>::load(p.residual, row[r] * p.N + n);
-        float acc[4][4] = {};
+                if (there[r] && 32 * s + 8 * t < columns)
+                    next[r] = Eight<OUT>::load(p.residual, at[r] + 32 * s);
+        };
+        if (p.residual)
+            fetch(step);
+        for (; step < last; ++step) {
+            Eight<OUT> y[2] = {next[0], next[1]};
+            if (p.residual && step + 1 < last)
+                fetch(step + 1);
+            float acc[4][4] = {};
+            if (!none) {
 #pragma unroll
-        for (int k = 0; k < KT; ++k) {
-            uint4 bv[4];
+                for (int k = 0; k < KT; ++k) {
+                    uint4 bv[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int64_t col = n0 + 8 * (g >> 1) + 2 * j + (g & 1);
-                bv[j] = col < p.N && 32 * k + 8 * t < p.rank ? __ldg(reinterpret_cast<const uint4*>(b + col * p.rank + 32 * k))
-                                                             : make_uint4(0u, 0u, 0u, 0u);
+                    for (int j = 0; j < 4; ++j) {
+                        const int col = 32 * step + 8 * (g >> 1) + 2 * j + (g & 1);
+                        bv[j] = col < columns && 32 * k + 8 * t < p.rank
+                                    ? __ldg(reinterpret_cast<const uint4*>(b + col * p.rank + 32 * k))
+                                    : make_uint4(0u, 0u, 0u, 0u);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        mma_16816<E>(acc[j], h[k][0], bv[j].x, bv[j].y);
+                        mma_16816<E>(acc[j], h[k][1], bv[j].z, bv[j].w);
+                    }
+                }
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                mma_16816<E>(acc[j], h[k][0], bv[j].x, bv[j].y);
-                mma_16816<E>(acc[j], h[k][1], bv[j].z, bv[j].w);
-            }
+            for (int r = 0; r < 2; ++r)
+                if (there[r] && 32 * step + 8 * t < columns) {
+                    if (adapter != p.adapters) {
+                        const float d[8] = {acc[0][2 * r] * factor[r], acc[0][2 * r + 1] * factor[r], acc[1][2 * r] * factor[r],
+                                            acc[1][2 * r + 1] * factor[r], acc[2][2 * r] * factor[r],
+                                            acc[2][2 * r + 1] * factor[r], acc[3][2 * r] * factor[r],
+                                            acc[3][2 * r + 1] * factor[r]};
+                        y[r].add(d);  // (an index out of range: 0 * NaN)
+                    }
+                    y[r].store(p.y, at[r] + 32 * step);
+                }
         }
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-            if (row[r] >= 0 && here) {
-                const float d[8] = {acc[0][2 * r] * factor[r], acc[0][2 * r + 1] * factor[r], acc[1][2 * r] * factor[r],
-                                    acc[1][2 * r + 1] * factor[r], acc[2][2 * r] * factor[r], acc[2][2 * r + 1] * factor[r],
-                                    acc[3][2 * r] * factor[r], acc[3][2 * r + 1] * factor[r]};
-                y[r].add(d);
-                y[r].store(p.y, row[r] * p.N + n);
-            }
     }
     griddep_launch_dependents();
 }
@@ -601,12 +629,17 @@ cudaError_t launch_adapter_linear(const AdapterLinear& p, const DeviceInfo& dev,
         return e;
     const bool few = p.M <= kFewRows;
     const int splits = splits_of(p.M, p.K);
-    const int tile = few ? kFewRows : TILE;
+    const int tile = few ? (int)p.M : TILE;
     const int64_t tiles = (p.M + tile - 1) / tile;
-    // columns of a block: about four blocks to an SM
+    // columns of a block, by the rounds of two blocks to an SM, each as long as its columns and a fixed cost
     int64_t chunk = 32;
-    while (chunk < 512 && tiles * ((p.N + 2 * chunk - 1) / (2 * chunk)) >= 4 * dev.sm_count)
-        chunk *= 2;
+    double least = INFINITY;
+    for (int64_t c = 32; c <= 512; c += 32) {
+        const int64_t blocks = tiles * ((p.N + c - 1) / c), rounds = (blocks + 2 * dev.sm_count - 1) / (2 * dev.sm_count);
+        const double cost = (double)rounds * ((double)c + 64.0);
+        if (cost < least)
+            least = cost, chunk = c;
+    }
     const unsigned expand = (unsigned)(tiles * ((p.N + chunk - 1) / chunk));
     auto shrink = [&](auto type) {
         using E = decltype(type);
@@ -646,7 +679,17 @@ cudaError_t launch_adapter_linear(const AdapterLinear& p, const DeviceInfo& dev,
         using E = decltype(type);
         constexpr int OUT = decltype(out)::value;
         auto by_rank = [&](auto kt) {
-            return launch_pdl(expand_kernel<E, OUT, decltype(kt)::value>, dim3(expand), dim3(THREADS), 0, s, p, tile, (int)chunk,
+            constexpr auto kernel = expand_kernel<E, OUT, decltype(kt)::value>;
+            static ContextCache<int> cache;
+            int done = 0;
+            const cudaError_t r = cache.get(&done, [&](int* d) {
+                *d = 1;
+                return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            h_bytes(kFewRows, 32 * decltype(kt)::value));
+            });
+            if (r != cudaSuccess)
+                return r;
+            return launch_pdl(kernel, dim3(expand), dim3(THREADS), (size_t)h_bytes(tile, p.rank), s, p, tile, (int)chunk,
                               splits);
         };
         if (p.rank <= 32)
