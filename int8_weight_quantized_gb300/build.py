@@ -25,9 +25,10 @@ LIB = os.path.join(LIB_DIR, "libck_int8.so")
 BINDING = os.path.join(LIB_DIR, "_ck_binding.so")
 
 SOURCES = ["api.cu", "quantize.cu", "gemm.cu", "api_transformer.cu", "norm_rope.cu", "paged_attention.cu",
-           "attention.cu", "int4.cu", "cache_read.cu", "adapter.cu", "logprobs.cu"]
+           "attention.cu", "int4.cu", "cache_read.cu", "adapter.cu", "logprobs.cu", "prefix_attention.cu"]
 HEADERS = ["ck_device.cuh", "ck_internal.h", "gemm_common.cuh", "api_common.h", "transformer.h", "attn_common.cuh",
-           "warp_mma.cuh", "tensor_core.cuh"]
+           "warp_mma.cuh", "tensor_core.cuh",
+           "prefix_common.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
               "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]

@@ -278,7 +278,10 @@ size_t ck_prefix_attention_workspace_size(int64_t batch, int64_t q_heads, int64_
     if (batch < 0 || num_prefixes < 1 || max_prefix_len < 0 || max_len < 0 || q_heads < 1 || kv_heads < 1 || head_dim < 1 ||
         q_heads > 65536 || kv_heads > 65536 || head_dim > 256 || max_prefix_len > kMaxCount || max_len > kMaxCount)
         return 0;
-    return paged_attention_workspace((int)(q_heads / kv_heads), (int)head_dim, max_prefix_len + max_len);
+    if (batch > kMaxCount / q_heads || q_heads % kv_heads != 0)
+        return 0;
+    return prefix_attention_workspace(batch, (int)(q_heads / kv_heads), (int)kv_heads, (int)head_dim, num_prefixes,
+                                      max_prefix_len, max_len);
 }
 
 int ck_prefix_attention(const void* q, int64_t q_stride, const ck_kv_cache_t* cache, const int32_t* prefix_table,
@@ -349,8 +352,8 @@ int ck_prefix_attention(const void* q, int64_t q_stride, const ck_kv_cache_t* ca
     p.shared.max_len = max_prefix_blocks * p.cache.page_size;
     log_shape("prefix_attention", batch, q_heads, p.cache.dim, p.cache.dtype, "keys of a group's prefix and its own");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    ProfScope ps(kProfAttention, paged_attention_launches(p), s);
-    const cudaError_t e = launch_paged_attention(p, dev, s);
+    ProfScope ps(kProfAttention, prefix_attention_launches(p), s);
+    const cudaError_t e = launch_prefix_attention(p, dev, s);
     return e == cudaSuccess ? CK_OK : cuda_fail(e, "ck_prefix_attention launch");
 }
 

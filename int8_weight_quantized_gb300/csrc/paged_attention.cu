@@ -54,6 +54,7 @@
 #include <cuda_fp16.h>
 
 #include "attn_common.cuh"
+#include "prefix_common.cuh"
 #include "transformer.h"
 #include "warp_mma.cuh"
 
@@ -96,8 +97,11 @@ struct Shape {
 };
 
 // ---- the division of work, the same in both kernels
-// PREFIX: a sequence's keys are those of the prefix that its group shares, then its own.
-template <bool PREFIX>
+// What a call is: attention over each sequence's own keys; over those of the prefix that its group
+// shares, then its own; over its own, the last kernel adding the pieces that prefix_attention.cu leaves.
+enum Mode { kOwn, kPrefixThenOwn, kOwnBesidePieces };
+
+template <int MODE>
 struct Lengths {
     const int32_t* seq_lens;
     int64_t max_len, window, sinks;
@@ -110,7 +114,7 @@ struct Lengths {
     {
         const int64_t n = __ldg(seq_lens + b);
         *bad = n < 0 || n > max_len;
-        if constexpr (PREFIX) {
+        if constexpr (MODE == kPrefixThenOwn) {
             *prefix = bad_groups ? -1 : shared.of(b);
             const int64_t m = *prefix < 0 ? 0 : __ldg(shared.lens + *prefix);
             *bad |= bad_groups || m < 0 || m > shared.max_len;
@@ -131,11 +135,11 @@ struct Lengths {
     }
 };
 
-template <bool PREFIX>
-__device__ __forceinline__ Lengths<PREFIX> lengths_of(const PagedAttention& p, int subs, int tile)
+template <int MODE>
+__device__ __forceinline__ Lengths<MODE> lengths_of(const PagedAttention& p, int subs, int tile)
 {
-    Lengths<PREFIX> L{p.seq_lens, p.max_blocks * p.cache.page_size, p.window, p.sinks, subs, tile, p.shared, false};
-    if constexpr (PREFIX)
+    Lengths<MODE> L{p.seq_lens, p.max_blocks * p.cache.page_size, p.window, p.sinks, subs, tile, p.shared, false};
+    if constexpr (MODE == kPrefixThenOwn)
         L.bad_groups = p.shared.bad_groups(p.batch);
     return L;
 }
@@ -187,20 +191,20 @@ __device__ __forceinline__ int64_t sequence_at(const L_& L, int64_t batch, int64
 }
 
 // Walks the tiles of a block's range.
-template <bool PREFIX>
+template <int MODE>
 struct Cursor {
     int64_t b;
     int sub, tile, tiles;
     int64_t left;  // tiles of the range from here on
     VisibleKeys keys;
-    int prefix_keys, prefix;  // PREFIX: keys of the sequence's prefix, its row in the table
-    __device__ void open(const Lengths<PREFIX>& L)
+    int prefix_keys, prefix;  // of kPrefixThenOwn: keys of the sequence's prefix, its row in the table
+    __device__ void open(const Lengths<MODE>& L)
     {
         bool bad;
         keys = visible_keys(L.length(b, &bad, &prefix_keys, &prefix), L.window, L.sinks);
         tiles = (keys.count() + L.tile - 1) / L.tile;
     }
-    __device__ void next(const Lengths<PREFIX>& L)
+    __device__ void next(const Lengths<MODE>& L)
     {
         if (--left <= 0 || ++tile < tiles)
             return;
@@ -239,7 +243,7 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c)
     return (uint32_t)(r * Shape<INT8, DIM, 1>::ROW + p * 16);
 }
 
-template <class E, bool INT8, int DIM, int NT, bool PREFIX>
+template <class E, bool INT8, int DIM, int NT, int MODE>
 __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
     paged_kernel(const PagedAttention p, int64_t C, bool split, unsigned int* err)
 {
@@ -248,13 +252,21 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
     using M = typename std::conditional<INT8, Fp16, E>::type;  // the products' type
     constexpr int HEADS = S::HEADS, KEYS = S::KEYS, KT = S::KT, TILE = S::TILE;
     extern __shared__ __align__(128) uint8_t smem[];
-    griddep_wait();
+    // (Beside pieces: the kernel before this one lets it begin once the work before both is complete, and
+    // nothing of its own is read here: this one only has to end after it.)
+    if constexpr (MODE != kOwnBesidePieces)
+        griddep_wait();
+    auto end = [] {
+        if constexpr (MODE == kOwnBesidePieces)
+            griddep_wait();
+        griddep_launch_dependents();
+    };
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
     const int group = p.q_heads / p.cache.heads;  // query heads per kv head
     const int qtiles = (group + HEADS - 1) / HEADS;
     const int page_size = p.cache.page_size;
-    const Lengths<PREFIX> L = lengths_of<PREFIX>(p, p.cache.heads * qtiles, TILE);
+    const Lengths<MODE> L = lengths_of<MODE>(p, p.cache.heads * qtiles, TILE);
 
     // sequences without visible keys have no tiles: zeros, or NaN where the length is out of range
     for (int64_t b = blockIdx.x; b < p.batch; b += gridDim.x) {
@@ -264,20 +276,24 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
             continue;
         if (bad && threadIdx.x == 0)
             atomicOr(err, kErrIndex);
-        for (int i = threadIdx.x; i < p.q_heads * DIM; i += WARPS * 32)
-            static_cast<T*>(p.out)[b * p.q_heads * DIM + i] = E::from(bad ? NAN : 0.0f);
-        if (p.lse != nullptr)
-            for (int i = threadIdx.x; i < p.q_heads; i += WARPS * 32)
-                p.lse[b * p.q_heads + i] = bad ? NAN : -INFINITY;
+        if constexpr (MODE != kOwnBesidePieces) {  // (there the last kernel writes them)
+            for (int i = threadIdx.x; i < p.q_heads * DIM; i += WARPS * 32)
+                static_cast<T*>(p.out)[b * p.q_heads * DIM + i] = E::from(bad ? NAN : 0.0f);
+            if (p.lse != nullptr)
+                for (int i = threadIdx.x; i < p.q_heads; i += WARPS * 32)
+                    p.lse[b * p.q_heads + i] = bad ? NAN : -INFINITY;
+        }
     }
 
     // this block's range of tiles
-    Cursor<PREFIX> at;
+    Cursor<MODE> at;
     if (split) {
         const int64_t total = tiles_before(L, p.batch);
         C = min(C, total);  // no block of those that take part is without tiles
-        if (blockIdx.x >= C)
+        if (blockIdx.x >= C) {
+            end();
             return;
+        }
         const int64_t t0 = first_tile(blockIdx.x, C, total), t1 = first_tile(blockIdx.x + 1, C, total);
         at.left = t1 - t0;
         int64_t before;
@@ -291,8 +307,10 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
         at.tile = 0;
         at.open(L);
         at.left = at.tiles;
-        if (at.left <= 0)
+        if (at.left <= 0) {
+            end();
             return;
+        }
     }
 
     const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * S::STAGES * S::UNIT);
@@ -304,7 +322,7 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
     constexpr int RPI = 32 / CH;          // rows of one copy instruction
     const uint8_t* const k_lane = static_cast<const uint8_t*>(p.cache.k) + lane % CH * 16;
     const uint8_t* const v_lane = static_cast<const uint8_t*>(p.cache.v) + lane % CH * 16;
-    Cursor<PREFIX> ahead = at;
+    Cursor<MODE> ahead = at;
     int32_t page = 0;
     int in_page = 0;
     bool have = false;
@@ -314,7 +332,7 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
         if (have) {
             int j = ahead.keys.key(v);
             const int32_t* row = p.block_table + ahead.b * p.max_blocks;
-            if constexpr (PREFIX) {
+            if constexpr (MODE == kPrefixThenOwn) {
                 if (j < ahead.prefix_keys)
                     row = p.shared.table + ahead.prefix * p.shared.max_blocks;
                 else
@@ -684,6 +702,13 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
             }
             const bool whole = segment_end && first_of_segment == 0;
             float* part = static_cast<float*>(p.workspace) + (2 * (int64_t)blockIdx.x + piece) * S::PART;
+            float2* part_sums = reinterpret_cast<float2*>(part + HEADS * DIM);
+            constexpr bool JOINED = MODE == kOwnBesidePieces;  // every segment's sums go to the last kernel
+            if (JOINED && whole) {
+                const int64_t at_row = at.b * p.q_heads + h0;
+                part = p.own_sums + at_row * DIM;
+                part_sums = reinterpret_cast<float2*>(p.own_sums + p.batch * p.q_heads * DIM) + at_row;
+            }
             for (int i = threadIdx.x; i < heads * (DIM / 4); i += WARPS * 32) {
                 const int row = i / (DIM / 4), d = i % (DIM / 4) * 4;
                 float4 x = *reinterpret_cast<const float4*>(joined + row * S::LD + d);
@@ -691,7 +716,7 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
                     const float4 y = *reinterpret_cast<const float4*>(joined + (HEADS + row) * S::LD + d);
                     x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
                 }
-                if (!whole) {
+                if (JOINED || !whole) {
                     *reinterpret_cast<float4*>(part + row * DIM + d) = x;
                     continue;
                 }
@@ -710,7 +735,7 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
                 if (d == 0 && p.lse != nullptr)
                     p.lse[at_row] = (top + log2f(sum)) * kLn2;
             }
-            if (!whole) {
+            if (JOINED || !whole) {
                 for (int row = threadIdx.x; row < heads; row += WARPS * 32) {
                     float top = -INFINITY, sum = 0.0f;
 #pragma unroll
@@ -721,9 +746,9 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
                         const float2 ms = maxsum[w * HEADS + row];
                         sum += ms.x == -INFINITY ? (ms.y != ms.y ? ms.y : 0.0f) : ms.y * fast_exp2(ms.x - top);
                     }
-                    reinterpret_cast<float2*>(part + HEADS * DIM)[row] = make_float2(top, sum);
+                    part_sums[row] = make_float2(top, sum);
                 }
-                ++piece;
+                piece += whole ? 0 : 1;
             }
             if (range_end)
                 break;
@@ -733,12 +758,12 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
         at.next(L);
     }
     cp_async_wait<0>();
-    griddep_launch_dependents();
+    end();
 }
 
 // Adds up the partial sums of the segments that blocks share: one block per (sequence, query
 // head), its 4 warps every fourth part each, then the four together.
-template <class E, int DIM, int NT, bool PREFIX>
+template <class E, int DIM, int NT, int MODE>
 __global__ void __launch_bounds__(128) join_kernel(const PagedAttention p, int64_t C, int tile)
 {
     using T = typename E::T;
@@ -752,42 +777,99 @@ __global__ void __launch_bounds__(128) join_kernel(const PagedAttention p, int64
     const int h = (int)(blockIdx.x - b * p.q_heads);
     const int group = p.q_heads / p.cache.heads;
     const int qtiles = (group + HEADS - 1) / HEADS;
-    const Lengths<PREFIX> L = lengths_of<PREFIX>(p, p.cache.heads * qtiles, tile);
+    const Lengths<MODE> L = lengths_of<MODE>(p, p.cache.heads * qtiles, tile);
+    constexpr bool BESIDE = MODE == kOwnBesidePieces;
     const int tiles = L.tiles(b);
-    if (tiles == 0)
+    if (!BESIDE && tiles == 0)
         return;  // the first kernel wrote it
-    const int64_t total = tiles_before(L, p.batch);
-    C = min(C, total);
+    const int64_t at_row = b * p.q_heads + h;
     const int in_group = h % group;
+    // the prefix's pieces
+    int64_t pieces = 0, piece0 = 0;
+    int piece_row = 0;
+    if constexpr (BESIDE) {
+        bool bad;
+        L.length(b, &bad);
+        bad |= p.shared.bad_groups(p.batch);
+        const int prefix = bad ? -1 : p.shared.of(b);
+        if (prefix >= 0) {
+            const int64_t n = __ldg(p.shared.lens + prefix);
+            bad |= n < 0 || n > p.shared.max_len;
+            const PrefixWork work{p.shared, p.cache.heads, 128 / group};
+            const PrefixWork::Of of = work.of(prefix);
+            if (of.tiles > 0) {
+                int64_t total, units, before, units_before;
+                work.before(p.shared.count, &total, &units);
+                work.before(prefix, &before, &units_before);
+                const int64_t blocks = min((int64_t)p.piece_blocks, total);
+                const int seq = (int)(b - __ldg(p.shared.cu + prefix)), pair = seq / (2 * work.per_tile);
+                const int in_pair = seq - pair * 2 * work.per_tile, t = in_pair / work.per_tile;
+                piece_row = t * kPrefixKeys + (in_pair - t * work.per_tile) * group + in_group;
+                const int64_t unit = (int64_t)(h / group) * of.pairs + pair;
+                const int64_t t0 = before + unit * of.tiles, t1 = t0 + of.tiles;
+                const int64_t c0 = ((t0 + 1) * blocks - 1) / total, c1 = (t1 * blocks - 1) / total;
+                pieces = c1 - c0 + 1;
+                piece0 = c0 + units_before + unit;
+            }
+        }
+        if (bad || (pieces == 0 && tiles == 0)) {
+            for (int d = threadIdx.x; d < DIM; d += 128)
+                static_cast<T*>(p.out)[at_row * DIM + d] = E::from(bad ? NAN : 0.0f);
+            if (threadIdx.x == 0 && p.lse != nullptr)
+                p.lse[at_row] = bad ? NAN : -INFINITY;
+            return;
+        }
+    }
+    const int64_t total = tiles > 0 ? tiles_before(L, p.batch) : 1;
+    C = min(C, total);
     const int64_t sub = h / group * qtiles + in_group / HEADS;
     const int row = in_group % HEADS;
-    const int64_t t0 = tiles_before(L, b) + sub * tiles, t1 = t0 + tiles;
+    const int64_t t0 = tiles > 0 ? tiles_before(L, b) + sub * tiles : 0, t1 = t0 + tiles;
     // block c holds tile t: c = floor(((t + 1) C - 1) / T)
-    const int64_t c0 = ((t0 + 1) * C - 1) / total, c1 = (t1 * C - 1) / total;
-    if (c0 == c1)
+    int64_t c0 = 0, c1 = -1;
+    if (tiles > 0 && (!BESIDE || p.own_split))
+        c0 = ((t0 + 1) * C - 1) / total, c1 = (t1 * C - 1) / total;
+    const bool whole = tiles > 0 && (BESIDE && !p.own_split ? true : c0 == c1);
+    if (!BESIDE && whole)
         return;  // one block held the whole segment and wrote the output
     const float* ws = static_cast<const float*>(p.workspace);
     float m = -INFINITY, l = 0.0f;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int64_t c = c0 + warp; c <= c1; c += 4) {
-        // Slot 0 holds the first partial that block c left.  That is this segment, unless c = c0
-        // began inside an earlier segment and had to leave that one first.
-        int slot = 0;
-        if (c == c0) {
-            const int64_t begin = first_tile(c, C, total);
-            if (begin < t0) {
-                // an earlier piece was partial exactly if the block began inside its segment
-                int64_t before;
-                const int64_t bb = sequence_at(L, p.batch, begin, &before);
-                const int bt = L.tiles(bb);
-                slot = (begin - before) % bt != 0 ? 1 : 0;
+    const int64_t own = tiles == 0 ? 0 : whole ? 1 : c1 - c0 + 1;
+    for (int64_t i = warp; i < pieces + own; i += 4) {
+        const float* part;
+        const float2* part_sum;
+        int part_row = row;
+        const int64_t c = c0 + (i - pieces);
+        if (BESIDE && i < pieces) {
+            part = p.pieces + (piece0 + i) * prefix_piece(DIM);
+            part_sum = reinterpret_cast<const float2*>(part + (int64_t)kPrefixRows * DIM) + piece_row;
+            part_row = piece_row;
+        } else if (BESIDE && whole) {
+            part = p.own_sums + at_row * DIM;
+            part_sum = reinterpret_cast<const float2*>(p.own_sums + p.batch * p.q_heads * DIM) + at_row;
+            part_row = 0;
+        } else {
+            // Slot 0 holds the first partial that block c left.  That is this segment, unless c = c0
+            // began inside an earlier segment and had to leave that one first.
+            int slot = 0;
+            if (c == c0) {
+                const int64_t begin = first_tile(c, C, total);
+                if (begin < t0) {
+                    // an earlier piece was partial exactly if the block began inside its segment
+                    int64_t before;
+                    const int64_t bb = sequence_at(L, p.batch, begin, &before);
+                    const int bt = L.tiles(bb);
+                    slot = (begin - before) % bt != 0 ? 1 : 0;
+                }
             }
+            part = ws + (2 * c + slot) * PART;
+            part_sum = reinterpret_cast<const float2*>(part + HEADS * DIM) + row;
         }
-        const float* part = ws + (2 * c + slot) * PART;
-        const float2 ms = __ldcg(reinterpret_cast<const float2*>(part + HEADS * DIM) + row);
+        const float2 ms = __ldcg(part_sum);
         float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (lane < DIM / 4)
-            x = __ldcg(reinterpret_cast<const float4*>(part + row * DIM) + lane);
+            x = __ldcg(reinterpret_cast<const float4*>(part + (int64_t)part_row * DIM) + lane);
         const float m2 = fmaxf(m, ms.x);
         const float ref = m2 == -INFINITY ? 0.0f : m2;
         const float a = fast_exp2(m - ref), f = fast_exp2(ms.x - ref);
@@ -816,7 +898,6 @@ __global__ void __launch_bounds__(128) join_kernel(const PagedAttention p, int64
         sum += maxsum[w].y * f;
         acc.x += x.x * f, acc.y += x.y * f, acc.z += x.z * f, acc.w += x.w * f;
     }
-    const int64_t at_row = b * p.q_heads + h;
     if (lane < DIM / 4)
         *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + at_row * DIM + lane * 4) =
             make_uint2(E::pack2(acc.x / sum, acc.y / sum), E::pack2(acc.z / sum, acc.w / sum));
@@ -835,8 +916,8 @@ int64_t longest_of(const PagedAttention& p)
     return p.window > 0 && p.sinks < longest && p.window < longest - p.sinks ? p.window + p.sinks : longest;
 }
 
-template <class E, bool INT8, int DIM, int NT, bool PREFIX>
-cudaError_t launch(const PagedAttention& p, const DeviceInfo& dev, unsigned int* err, cudaStream_t s)
+template <class E, bool INT8, int DIM, int NT, int MODE>
+cudaError_t launch(PagedAttention p, const DeviceInfo& dev, unsigned int* err, cudaStream_t s)
 {
     using S = Shape<INT8, DIM, NT>;
     // a kernel attribute belongs to the context it was set in: set once per context
@@ -844,33 +925,36 @@ cudaError_t launch(const PagedAttention& p, const DeviceInfo& dev, unsigned int*
     int done = 0;
     cudaError_t e = cache.get(&done, [](int* d) {
         *d = 1;
-        return cudaFuncSetAttribute(paged_kernel<E, INT8, DIM, NT, PREFIX>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(paged_kernel<E, INT8, DIM, NT, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     (int)S::SMEM);
     });
     if (e != cudaSuccess)
         return e;
     const int group = p.q_heads / p.cache.heads;
     const int64_t segments = p.batch * p.cache.heads * ((group + S::HEADS - 1) / S::HEADS);
-    const int64_t longest = longest_of(p);
+    const int64_t longest = MODE == kOwnBesidePieces ? p.max_blocks * p.cache.page_size : longest_of(p);
     const int64_t tiles = (longest + S::TILE - 1) / S::TILE;
     const bool split = longest > kWholeKeys;
     const int64_t most = std::min<int64_t>(kMostBlocks, (int64_t)dev.sm_count * S::BLOCKS);
     const int64_t blocks = split ? std::min(most, segments * tiles) : segments;
-    e = launch_pdl(paged_kernel<E, INT8, DIM, NT, PREFIX>, dim3((unsigned)blocks), dim3(WARPS * 32), S::SMEM, s, p, blocks,
+    e = launch_pdl(paged_kernel<E, INT8, DIM, NT, MODE>, dim3((unsigned)blocks), dim3(WARPS * 32), S::SMEM, s, p, blocks,
                    split, err);
-    if (e == cudaSuccess && split)
-        e = launch_pdl(join_kernel<E, DIM, NT, PREFIX>, dim3((unsigned)(p.batch * p.q_heads)), dim3(128), 0, s, p, blocks, S::TILE);
+    p.own_split = split;
+    if (e == cudaSuccess && (split || MODE == kOwnBesidePieces))
+        e = launch_pdl(join_kernel<E, DIM, NT, MODE>, dim3((unsigned)(p.batch * p.q_heads)), dim3(128), 0, s, p, blocks, S::TILE);
     return e;
 }
 
 template <class E, int DIM, int NT>
 cudaError_t by_cache(const PagedAttention& p, const DeviceInfo& dev, unsigned int* err, cudaStream_t s)
 {
-    if (p.shared.count > 0)
-        return p.cache.dtype == CK_KV_INT8 ? launch<E, true, DIM, NT, true>(p, dev, err, s)
-                                           : launch<E, false, DIM, NT, true>(p, dev, err, s);
-    return p.cache.dtype == CK_KV_INT8 ? launch<E, true, DIM, NT, false>(p, dev, err, s)
-                                       : launch<E, false, DIM, NT, false>(p, dev, err, s);
+    auto by_mode = [&](auto int8) {
+        constexpr bool INT8 = decltype(int8)::value;
+        return p.shared.count == 0 ? launch<E, INT8, DIM, NT, kOwn>(p, dev, err, s)
+               : p.pieces == nullptr ? launch<E, INT8, DIM, NT, kPrefixThenOwn>(p, dev, err, s)
+                                     : launch<E, INT8, DIM, NT, kOwnBesidePieces>(p, dev, err, s);
+    };
+    return p.cache.dtype == CK_KV_INT8 ? by_mode(std::true_type()) : by_mode(std::false_type());
 }
 
 template <int DIM>
@@ -900,6 +984,58 @@ cudaError_t launch_paged_attention(const PagedAttention& p, const DeviceInfo& de
     if (e != cudaSuccess)
         return e;
     return p.cache.dim == 64 ? by_type<64>(p, dev, err, s) : by_type<128>(p, dev, err, s);
+}
+
+// ---- behind shared prefixes
+namespace {
+
+constexpr size_t align256(size_t n)
+{
+    return (n + 255) / 256 * 256;
+}
+
+// Whether the shared part is computed for whole groups: where there are rows enough to a prefix.
+bool in_pieces(int64_t batch, int group, int64_t prefixes, int64_t max_prefix_len)
+{
+    return group <= 128 && batch * group >= 16 * prefixes && max_prefix_len >= 256;
+}
+
+size_t pieces_bytes(int64_t batch, int group, int kv_heads, int dim, int64_t prefixes)
+{
+    const int64_t units = kv_heads * (batch / (2 * (128 / group)) + std::min(prefixes, batch));
+    return align256((size_t)(kPrefixBlocks + units) * prefix_piece(dim) * sizeof(float));
+}
+
+}  // namespace
+
+size_t prefix_attention_workspace(int64_t batch, int group, int kv_heads, int dim, int64_t prefixes, int64_t max_prefix_len,
+                                  int64_t max_len)
+{
+    if (!in_pieces(batch, group, prefixes, max_prefix_len))
+        return paged_attention_workspace(group, dim, max_prefix_len + max_len);
+    return pieces_bytes(batch, group, kv_heads, dim, prefixes) + align256(paged_attention_workspace(group, dim, max_len)) +
+           (size_t)batch * group * kv_heads * (dim + 2) * sizeof(float);
+}
+
+int prefix_attention_launches(const PagedAttention& p)
+{
+    return in_pieces(p.batch, p.q_heads / p.cache.heads, p.shared.count, p.shared.max_len) ? 3 : paged_attention_launches(p);
+}
+
+cudaError_t launch_prefix_attention(PagedAttention p, const DeviceInfo& dev, cudaStream_t s)
+{
+    const int group = p.q_heads / p.cache.heads;
+    if (!in_pieces(p.batch, group, p.shared.count, p.shared.max_len))
+        return launch_paged_attention(p, dev, s);
+    char* ws = static_cast<char*>(p.workspace);
+    p.pieces = reinterpret_cast<float*>(ws);
+    p.piece_blocks = std::min(dev.sm_count, kPrefixBlocks);
+    ws += pieces_bytes(p.batch, group, p.cache.heads, p.cache.dim, p.shared.count);
+    p.workspace = ws;
+    ws += align256(paged_attention_workspace(group, p.cache.dim, p.max_blocks * p.cache.page_size));
+    p.own_sums = reinterpret_cast<float*>(ws);
+    const cudaError_t e = launch_prefix_pieces(p, p.pieces, dev, s);
+    return e == cudaSuccess ? launch_paged_attention(p, dev, s) : e;
 }
 
 }  // namespace ck

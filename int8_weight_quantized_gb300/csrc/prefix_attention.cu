@@ -1,0 +1,842 @@
+// prefix_attention.cu -- the shared part of attention behind prefixes: the queries of all sequences of a
+// group against the keys that they share, as a product of whole tiles.
+//
+//   O_r = sum_j w_j v_j, l_r = sum_j w_j, w_j = exp(scale * q_r . k_j - m_r), j over a run of the prefix's
+//   keys; the pieces, and each sequence's own keys, are joined by paged_attention.cu's last kernel.
+//
+// Bound: at few rows HBM, each key and value row once per kv head and 256 query rows; at many the tensor
+// cores, 4 dim flops per query head and key.
+//
+// The rows of a tile are the query heads of one kv head of floor(128 / group) sequences.  One block per SM;
+// its roles run on from piece to piece:
+//   warp 0      issues the products, one lane: S_t = Q_t K^T, O_t += P_t V, sums in tensor memory, in
+//               the order O_0 += P_0 V_j, S_0 = Q_0 K_{j+1}, O_1 += P_1 V_j, S_1 = Q_1 K_{j+1};
+//   warps 1-3   copies: rows of the pages, whatever their size, by 16-byte asynchronous copies into the
+//               swizzled layout that the products read; int8 rows through a small ring of raw codes,
+//               each thread widening what it copied itself;
+//   warps 4-11  softmax, a warpgroup for each query tile, one thread per row, as in attention.cu: the
+//               weights go back over S as the 16-bit operand P of the second product, the row's
+//               reference trails its maximum by up to 2^8.
+// int8 rows: codes are exact in bf16 and fp16; k's scale multiplies the fp32 score, v's the code, rounded
+// once to the queries' type.
+//
+// Rounding to fewer bits: each weight once, to the queries' type (and the values of int8 rows); scores,
+// sums, maxima and O are fp32.
+#include <algorithm>
+#include <cmath>
+#include <type_traits>
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "attn_common.cuh"
+#include "prefix_common.cuh"
+#include "tensor_core.cuh"
+#include "transformer.h"
+#include "warp_mma.cuh"
+
+namespace ck {
+namespace {
+
+constexpr int BM = 128;              // query rows of a tile, keys of a key tile
+constexpr int THREADS = 384;
+constexpr int LOADERS = 3;           // warps
+// registers after the warpgroups re-balance; 384 threads start with 168 each
+constexpr uint32_t REGS_LOAD = 88, REGS_SOFTMAX = 208;
+constexpr uint32_t REGS_NEEDED_PER_BLOCK = 128 * REGS_LOAD + 256 * REGS_SOFTMAX;
+constexpr uint32_t TMEM_COLS = 512;
+constexpr uint32_t FULL = 0xffffffffu;
+constexpr uint64_t TIMEOUT_NS = 2000000000ull;
+constexpr float kLag = 8.0f;         // how far (log2) a row's reference may trail its maximum
+// weights of a tile that are handed over first (see attention.cu)
+template <int DIM>
+constexpr int FIRST_KEYS = DIM == 128 ? 64 : 0;
+
+template <int DIM, bool INT8>
+struct Cfg {
+    static constexpr uint32_t BOX_BYTES = BM * 128;             // 128 rows of 64 values
+    static constexpr uint32_t TILE_BYTES = DIM / 64 * BOX_BYTES;  // a Q, K or V tile
+    static constexpr int UNITS = (DIM == 128 ? 5 : 10) - (INT8 ? 1 : 0);  // ring of K_0, V_0, K_1, V_1, ..
+    static constexpr int RAW_ROWS = 64;                         // int8 codes on their way: half a tile
+    static constexpr int RAWS = INT8 ? 3 : 0;
+    static constexpr uint32_t RAW_BYTES = RAW_ROWS * DIM;
+    // Key tiles whose scales are kept: while a softmax warp reads those of tile j, V_j is in the ring, so that K's
+    // of up to UNITS / 2 further tiles are.
+    static constexpr int SCALES = UNITS / 2 + 2;
+    static constexpr size_t SCALE_BYTES = INT8 ? SCALES * BM * 4 + RAWS * RAW_ROWS * 4 : 0;
+    static constexpr size_t STATE = 512;
+    static constexpr size_t SMEM = 1024 + (2 + UNITS) * (size_t)TILE_BYTES + RAWS * RAW_BYTES + SCALE_BYTES + STATE;
+    static_assert(SMEM <= 232448, "shared memory budget");
+};
+
+struct Args {
+    PagedAttention p;
+    PrefixWork work;
+    int group;
+    bool negate;
+    float c;  // |scale| log2 e
+};
+
+// A block's way through its key tiles, piece by piece.
+struct Walk {
+    int64_t prefix, unit, left;  // left: tiles from here on
+    PrefixWork::Of of;
+    int64_t seq0;                // first sequence of the prefix
+    int head, pair, tile;
+    __device__ __forceinline__ void open(const PrefixWork& w)
+    {
+        of = w.of(prefix);
+        seq0 = __ldg(w.shared.cu + prefix);
+    }
+    // the piece here: tiles tile .. tile + count - 1 of the unit
+    __device__ __forceinline__ int count() const { return (int)min((int64_t)(of.tiles - tile), left); }
+    __device__ __forceinline__ void next(const PrefixWork& w)
+    {
+        left -= count();
+        tile = 0;
+        if (left <= 0)
+            return;
+        ++unit;
+        if (++pair < of.pairs)
+            return;
+        pair = 0;
+        if (++head < w.heads)
+            return;
+        head = 0;
+        do {
+            ++prefix;
+            open(w);
+        } while (of.tiles == 0);  // left > 0: a later prefix has tiles
+    }
+};
+
+// 32 values of each lane's row, to dst + lane * stride, for the first `rows` lanes: four lanes trade
+// their 16-byte pieces, so that a store writes 64 bytes of each of 8 rows.
+__device__ __forceinline__ void store_sums(float* dst, int64_t stride, int lane, int rows, uint32_t (&v)[32])
+{
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        uint32_t* r = v + 16 * half;
+#pragma unroll
+        for (int m = 1; m <= 2; m *= 2)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (!(i & m))
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        const bool up = lane & m;
+                        const uint32_t got = __shfl_xor_sync(FULL, up ? r[4 * i + n] : r[4 * (i | m) + n], m);
+                        r[4 * i + n] = up ? got : r[4 * i + n];
+                        r[4 * (i | m) + n] = up ? r[4 * (i | m) + n] : got;
+                    }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = (lane & ~3) + i;
+            if (row < rows)
+                *reinterpret_cast<uint4*>(dst + row * stride + 16 * half + (lane & 3) * 4) =
+                    make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+        }
+    }
+}
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint4 v)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// byte i of four codes with their signs flipped, as the number that it stands for
+__device__ __forceinline__ float code_value(uint32_t flipped, int i)
+{
+    return __uint_as_float(__byte_perm(flipped, 0x4B000000u, 0x7440 | i)) - 8388736.0f;  // 2^23 + 128
+}
+
+template <class E, int DIM, bool INT8>
+__global__ void __launch_bounds__(THREADS, 1) prefix_kernel(const Args a, float* parts, unsigned int* err)
+{
+    using C = Cfg<DIM, INT8>;
+    using T = typename E::T;
+    constexpr int UNITS = C::UNITS;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* s_q = smem;
+    uint8_t* s_ring = s_q + 2 * C::TILE_BYTES;
+    uint8_t* s_raw = s_ring + UNITS * C::TILE_BYTES;
+    float* s_kscale = reinterpret_cast<float*>(s_raw + C::RAWS * C::RAW_BYTES);     // [SCALES][BM]
+    float* s_rscale = s_kscale + (INT8 ? C::SCALES * BM : 0);                        // [RAWS][RAW_ROWS]
+    uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(s_kscale) + C::SCALE_BYTES);
+    uint64_t* q_full = bars;             // [2]
+    uint64_t* q_empty = bars + 2;        // [2] the piece's last scores of tile t are computed
+    uint64_t* s_full = bars + 4;         // [2] S_t is complete (and every product before it)
+    uint64_t* p_half = bars + 6;         // [2] P_t is for its first keys, O_t may be added to
+    uint64_t* p_full = bars + 8;         // [2] P_t is written
+    uint64_t* o_full = bars + 10;        // [2] O_t is final
+    uint64_t* drain = bars + 12;
+    uint64_t* full = bars + 13;          // [UNITS]
+    uint64_t* empty = full + UNITS;      // [UNITS]
+    int64_t* s_start = reinterpret_cast<int64_t*>(empty + UNITS);  // where the block begins
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_start + 5);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    static_assert((13 + 2 * UNITS + 5) * 8 + 8 <= C::STATE, "barriers");
+
+    const int warp = __shfl_sync(FULL, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    if (warp == 0 && lane == 0) {
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&q_full[t], LOADERS);
+            mbar_init(&q_empty[t], 1);
+            mbar_init(&s_full[t], 1);
+            mbar_init(&p_half[t], 4);
+            mbar_init(&p_full[t], 4);
+            mbar_init(&o_full[t], 1);
+        }
+        mbar_init(drain, 1);
+        for (int s = 0; s < UNITS; ++s) {
+            mbar_init(&full[s], LOADERS);
+            mbar_init(&empty[s], 1);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+        fence_proxy_async_smem();
+    }
+    if (warp == 0) {
+        __syncwarp();
+        tmem_alloc(tmem_slot, TMEM_COLS);
+        tmem_relinquish();
+    }
+    __syncwarp();
+    griddep_wait();
+    griddep_launch_dependents();
+    const PrefixWork& work = a.work;
+    if (warp == 1) {
+        // this block's range of tiles
+        const bool bad = work.shared.bad_groups(a.p.batch);
+        int64_t total = 0, units = 0, t_before = 0, u_before = 0, prefix = 0, t0 = 0, left = 0;
+        if (!bad) {
+            work.before(work.shared.count, &total, &units);
+            const int64_t blocks = min((int64_t)gridDim.x, total);
+            if (blockIdx.x < blocks) {
+                t0 = blockIdx.x * total / blocks;
+                left = (blockIdx.x + 1) * total / blocks - t0;
+                prefix = work.holds(t0, &t_before, &u_before);
+            }
+        }
+        if (lane == 0) {
+            s_start[0] = left, s_start[1] = prefix, s_start[2] = t0 - t_before, s_start[3] = u_before;
+            if (bad)
+                atomicOr(err, kErrIndex);
+        }
+    } else if (warp == 2 && blockIdx.x == 0) {
+        // lengths out of range (the last kernel gives NaN for them)
+        bool bad = false;
+        for (int64_t i = lane; i < work.shared.count; i += 32) {
+            const int64_t n = __ldg(work.shared.lens + i);
+            bad |= n < 0 || n > work.shared.max_len;
+        }
+        if (bad)
+            atomicOr(err, kErrIndex);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = __shfl_sync(FULL, *tmem_slot, 0);
+    Walk at;
+    at.left = s_start[0];
+    const bool any = at.left > 0;
+    if (any) {
+        at.prefix = s_start[1];
+        at.open(work);
+        const int64_t in_prefix = s_start[2], unit = in_prefix / at.of.tiles;
+        at.tile = (int)(in_prefix - unit * at.of.tiles);
+        at.unit = s_start[3] + unit;
+        at.head = (int)(unit / at.of.pairs);
+        at.pair = (int)(unit - (int64_t)at.head * at.of.pairs);
+    }
+    const int per_tile = work.per_tile, group = a.group;
+    // sequences of query tile t of the piece
+    auto seqs = [&](int t) { return max(0, min(per_tile, at.of.seqs - (2 * at.pair + t) * per_tile)); };
+    const KvCache& cache = a.p.cache;
+
+    if (!any) {
+        // nothing to do (fewer tiles than blocks)
+    } else if (warp < 4) {
+        setmaxnreg_dec<REGS_LOAD>();
+        auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+            if (__all_sync(FULL, mbar_try_wait(bar, parity)))
+                return true;
+            const bool ok = mbar_wait(bar, parity, abort_flag, err, kErrWaitPrefix, TIMEOUT_NS);
+            return __all_sync(FULL, ok) != 0;
+        };
+        if (warp == 0) {
+            // -------------------------------------------------------------- products
+            const uint32_t idesc_s = idesc_of<E>(BM, false) | (a.negate ? 1u << 13 : 0u);
+            constexpr uint32_t idesc_o = idesc_of<E>(DIM, true);
+            const uint64_t q_desc = desc_kmajor_sw128(smem_u32(s_q));
+            const uint64_t k_desc = desc_kmajor_sw128(smem_u32(s_ring));
+            const uint64_t v_desc = desc_nmajor_sw128(smem_u32(s_ring), C::BOX_BYTES);
+            constexpr uint64_t kTile = C::TILE_BYTES >> 4, kBox = C::BOX_BYTES >> 4;
+            uint32_t uses = 0, q_uses[2] = {0, 0}, p_phase[2] = {0, 0};
+            const bool leader = elect_one();
+            auto scores = [&](int t, int slot) {  // S_t = Q_t K^T
+                const uint64_t x = q_desc + t * kTile, y = k_desc + slot * kTile;
+#pragma unroll
+                for (int k = 0; k < DIM / 16; ++k)
+                    mma_ss(tmem + t * BM, x + (k / 4) * kBox + (k % 4) * 2, y + (k / 4) * kBox + (k % 4) * 2, idesc_s, k > 0);
+                mma_commit(&s_full[t]);
+            };
+            auto values = [&](int t, int slot, auto from, auto keys, bool started) {  // O_t += P_t V
+                const uint64_t y = v_desc + slot * kTile;
+#pragma unroll
+                for (int k = from.value / 16; k < keys.value / 16; ++k)
+                    mma_ts(tmem + 2 * BM + t * DIM, tmem + t * BM + k * 8, y + k * (16 * 128 >> 4), idesc_o, k > 0 || started);
+            };
+            auto piece = [&]() {
+                const int count = __shfl_sync(FULL, at.count(), 0);
+                const int tiles = __shfl_sync(FULL, seqs(1) > 0 ? 2 : 1, 0);
+                int slot = uses % UNITS;
+                if (!wait_all(&full[slot], (uses / UNITS) & 1u))
+                    return false;
+                ++uses;
+                for (int t = 0; t < tiles; ++t) {
+                    if (!wait_all(&q_full[t], q_uses[t]++ & 1u))
+                        return false;
+                    tc_fence_after();
+                    if (leader) {
+                        scores(t, slot);
+                        if (count == 1)
+                            mma_commit(&q_empty[t]);
+                    }
+                    __syncwarp();
+                }
+                if (leader)
+                    mma_commit(&empty[slot]);
+                __syncwarp();
+                for (int j = 0; j < count; ++j) {
+                    const bool more = j + 1 < count;
+                    const int v_slot = uses % UNITS;
+                    if (!wait_all(&full[v_slot], (uses / UNITS) & 1u))
+                        return false;
+                    ++uses;
+                    const int k_slot = uses % UNITS;
+                    if (more) {
+                        if (!wait_all(&full[k_slot], (uses / UNITS) & 1u))
+                            return false;
+                        ++uses;
+                    }
+                    for (int t = 0; t < tiles; ++t) {
+                        constexpr int FIRST = FIRST_KEYS<DIM>;
+                        if constexpr (FIRST > 0) {
+                            if (!wait_all(&p_half[t], p_phase[t]))
+                                return false;
+                            tc_fence_after();
+                            if (leader)
+                                values(t, v_slot, std::integral_constant<int, 0>(), std::integral_constant<int, FIRST>(), j > 0);
+                            __syncwarp();
+                        }
+                        if (!wait_all(&p_full[t], p_phase[t]))
+                            return false;
+                        p_phase[t] ^= 1u;
+                        tc_fence_after();
+                        if (leader) {
+                            values(t, v_slot, std::integral_constant<int, FIRST>(), std::integral_constant<int, BM>(), j > 0);
+                            if (!more)
+                                mma_commit(&o_full[t]);
+                            if (more) {
+                                scores(t, k_slot);
+                                if (j + 2 == count)
+                                    mma_commit(&q_empty[t]);
+                            }
+                            if (t + 1 == tiles) {
+                                mma_commit(&empty[v_slot]);
+                                if (more)
+                                    mma_commit(&empty[k_slot]);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                }
+                return true;
+            };
+            for (; at.left > 0; at.next(work))
+                if (!piece())
+                    break;
+            // every product must be complete before tensor and shared memory are released
+            if (leader) {
+                mma_commit(drain);
+                wait_out(drain, 0, err, kErrWaitPrefix, TIMEOUT_NS);
+            }
+            __syncwarp();
+        } else {
+            // ---------------------------------------------------------------- copies
+            const int w = warp - 1;
+            // groups of copies in flight, and the barriers that wait for them (the oldest first)
+            constexpr int FLIGHT = 2;
+            uint64_t* pending[FLIGHT + 1] = {};
+            int in_flight = 0;
+            auto landed = [&](uint64_t* bar) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bar);
+            };
+            auto all_landed = [&]() {
+                cp_async_wait<0>();
+#pragma unroll
+                for (int i = 0; i < FLIGHT; ++i)
+                    if (i < in_flight)
+                        landed(pending[i]);
+                in_flight = 0;
+            };
+            auto sent = [&](uint64_t* bar) {
+                cp_async_commit();
+#pragma unroll
+                for (int i = 0; i <= FLIGHT; ++i)
+                    pending[i] = i == in_flight ? bar : pending[i];
+                if (++in_flight > FLIGHT) {
+                    cp_async_wait<FLIGHT>();
+                    landed(pending[0]);
+#pragma unroll
+                    for (int i = 0; i < FLIGHT; ++i)
+                        pending[i] = pending[i + 1];
+                    --in_flight;
+                }
+            };
+            // (what has been sent must not wait for what is to come)
+            auto wait = [&](uint64_t* bar, uint32_t parity) {
+                if (__all_sync(FULL, mbar_try_wait(bar, parity)))
+                    return true;
+                if (!INT8)
+                    all_landed();
+                return wait_all(bar, parity);
+            };
+            uint32_t uses = 0, q_uses[2] = {0, 0};
+            // byte address of 16-byte chunk c of row r of a tile
+            auto chunk_at = [&](int r, int c) {
+                return (uint32_t)((c >> 3) * C::BOX_BYTES + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+            };
+            auto load_q = [&](int t) {
+                if (!wait(&q_empty[t], (q_uses[t] + 1) & 1u))
+                    return false;
+                ++q_uses[t];
+                const int rows = seqs(t) * group;
+                const T* q = static_cast<const T*>(a.p.q) +
+                             (at.seq0 + (2 * at.pair + t) * per_tile) * a.p.q_stride + (int64_t)at.head * group * DIM;
+                const uint32_t dst = smem_u32(s_q) + t * C::TILE_BYTES;
+                constexpr int CH = DIM / 8;
+                for (int i = w * 32 + lane; i < BM * CH; i += LOADERS * 32) {
+                    const int r = i / CH, c = i % CH, s = r / group;
+                    const bool ok = r < rows;
+                    cp_async16(dst + chunk_at(r, c), ok ? q + s * a.p.q_stride + (r - s * group) * DIM + c * 8 : q, ok);
+                }
+                sent(&q_full[t]);
+                if (INT8)
+                    all_landed();
+                return true;
+            };
+            // where key `j` of the prefix lies: its row in the cache; ok: there is one, bad: on a page out of range
+            auto row_of = [&](int j, bool* ok, bool* bad) {
+                *ok = *bad = false;
+                if (j >= at.of.keys)
+                    return 0u;
+                const int blk = a.p.page_shift >= 0 ? j >> a.p.page_shift : j / cache.page_size;
+                const int32_t page = __ldg(work.shared.table + at.prefix * work.shared.max_blocks + blk);
+                *ok = page >= 0 && page < cache.num_pages;
+                *bad = !*ok;
+                return *ok ? ((uint32_t)page * cache.heads + at.head) * cache.page_size + (j - blk * cache.page_size) : 0u;
+            };
+            if constexpr (!INT8) {
+                // a copy instruction takes RPI rows, the warps by turns; number n of a warp's rows is row
+                // (n / RPI * LOADERS + w) * RPI + n % RPI, and its lane n % 32 looks it up
+                constexpr int CH = DIM / 8, RPI = 32 / CH, TURNS = (BM / RPI + LOADERS - 1) / LOADERS;
+                static_assert(TURNS * RPI <= 64, "two rows a lane");
+                uint32_t rows[2], oks[2], bads[2];
+                auto look_up = [&](int tile) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int n = 32 * h + lane, r = (n / RPI * LOADERS + w) * RPI + n % RPI;
+                        bool ok = false, bad = false;
+                        rows[h] = 0;
+                        if (n < TURNS * RPI && r < BM)
+                            rows[h] = row_of(tile * BM + r, &ok, &bad);
+                        oks[h] = __ballot_sync(FULL, ok), bads[h] = __ballot_sync(FULL, bad);
+                    }
+                    if ((bads[0] | bads[1]) && lane == 0)
+                        atomicOr(err, kErrIndex);
+                };
+                auto load_unit = [&](bool is_k) {
+                    const int slot = uses % UNITS;
+                    if (!wait(&empty[slot], (uses / UNITS + 1) & 1u))
+                        return false;
+                    ++uses;
+                    const uint8_t* base = static_cast<const uint8_t*>(is_k ? cache.k : cache.v) + lane % CH * 16;
+                    const uint32_t dst = smem_u32(s_ring) + slot * C::TILE_BYTES;
+#pragma unroll
+                    for (int i = 0; i < TURNS; ++i) {
+                        const int r = (i * LOADERS + w) * RPI + lane / CH, n = i * RPI + lane / CH;
+                        const uint32_t row = __shfl_sync(FULL, rows[i * RPI / 32], n % 32);
+                        if (r < BM) {
+                            const bool ok = (oks[i * RPI / 32] >> (n % 32)) & 1u;
+                            const uint32_t to = dst + chunk_at(r, lane % CH);
+                            if (is_k && ((bads[i * RPI / 32] >> (n % 32)) & 1u))
+                                sts128(to, make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu));  // NaN
+                            else
+                                cp_async16(to, base + (uint64_t)row * (DIM * 2), ok);
+                        }
+                    }
+                    sent(&full[slot]);
+                    return true;
+                };
+                bool ok = true;
+                for (; ok && at.left > 0; at.next(work)) {
+                    const int count = at.count();
+                    ok = load_q(0);
+                    look_up(at.tile);
+                    ok = ok && load_unit(true);
+                    if (ok && seqs(1) > 0)
+                        ok = load_q(1);
+                    for (int j = 0; ok && j < count; ++j) {
+                        ok = load_unit(false);
+                        if (ok && j + 1 < count) {
+                            look_up(at.tile + j + 1);
+                            ok = load_unit(true);
+                        }
+                    }
+                }
+                all_landed();
+            } else {
+                // half tiles of raw codes through a ring, each widened by the thread that copied it
+                constexpr int CH = DIM / 16, RPI = 32 / CH, ROWS = C::RAW_ROWS;
+                constexpr int TURNS = (ROWS / RPI + LOADERS - 1) / LOADERS;
+                static_assert(TURNS * RPI <= 32, "a row a lane");
+                // copies run ahead of the widening by up to RAWS - 1 halves, over the pieces' ends too
+                Walk ahead = at;
+                int ahead_half = 0;  // of the piece: 4 j + (0, 1: K; 2, 3: V)
+                uint32_t copies = 0, widened = 0, k_tiles_ahead = 0;
+                uint32_t bads[C::RAWS] = {};
+                auto copy = [&]() {
+                    if (ahead.left > 0) {
+                        const int raw = copies % C::RAWS;
+                        const bool is_k = (ahead_half & 2) == 0;
+                        const int first = (ahead.tile + ahead_half / 4) * BM + (ahead_half & 1) * ROWS;
+                        const int n = lane, r = (n / RPI * LOADERS + w) * RPI + n % RPI;
+                        bool ok = false, bad = false;
+                        uint32_t row = 0;
+                        if (n < TURNS * RPI && r < ROWS && first + r < ahead.of.keys) {
+                            const int j = first + r;
+                            const int blk = a.p.page_shift >= 0 ? j >> a.p.page_shift : j / cache.page_size;
+                            const int32_t page = __ldg(work.shared.table + ahead.prefix * work.shared.max_blocks + blk);
+                            ok = page >= 0 && page < cache.num_pages;
+                            bad = !ok;
+                            row = ok ? ((uint32_t)page * cache.heads + ahead.head) * cache.page_size + (j - blk * cache.page_size)
+                                     : 0u;
+                        }
+                        const uint32_t oks = __ballot_sync(FULL, ok), bad_rows = __ballot_sync(FULL, bad);
+#pragma unroll
+                        for (int i = 0; i < C::RAWS; ++i)
+                            bads[i] = i == raw ? bad_rows : bads[i];
+                        if (bad_rows && lane == 0)
+                            atomicOr(err, kErrIndex);
+                        const uint8_t* base = static_cast<const uint8_t*>(is_k ? cache.k : cache.v) + lane % CH * 16;
+                        const float* scales = is_k ? cache.k_scale : cache.v_scale;
+                        const uint32_t dst = smem_u32(s_raw) + raw * C::RAW_BYTES;
+#pragma unroll
+                        for (int i = 0; i < TURNS; ++i) {
+                            const int rr = (i * LOADERS + w) * RPI + lane / CH, nn = i * RPI + lane / CH;
+                            const uint32_t from = __shfl_sync(FULL, row, nn);
+                            if (rr < ROWS)
+                                cp_async16(dst + rr * DIM + lane % CH * 16, base + (uint64_t)from * DIM, (oks >> nn) & 1u);
+                        }
+                        if (n < TURNS * RPI && r < ROWS)
+                            cp_async_small<4>(smem_u32(s_rscale + raw * ROWS + r), scales + row, ok);
+                        ++copies;
+                        ahead_half++;
+                        if (ahead_half == 4 * ahead.count()) {
+                            ahead_half = 0;
+                            ahead.next(work);
+                        }
+                    }
+                    cp_async_commit();
+                };
+                // the next half, into rows half * ROWS .. of the tile at dst
+                auto widen = [&](uint32_t dst, int half, bool is_k, float* kscale) {
+                    cp_async_wait<C::RAWS - 2>();
+                    __syncwarp();  // scales come from other lanes' copies
+                    const int raw = widened % C::RAWS;
+                    uint32_t bad_rows = 0;
+#pragma unroll
+                    for (int i = 0; i < C::RAWS; ++i)
+                        bad_rows = i == raw ? bads[i] : bad_rows;
+                    ++widened;
+#pragma unroll 1
+                    for (int i = 0; i < TURNS; ++i) {
+                        const int r = (i * LOADERS + w) * RPI + lane / CH, c = lane % CH;
+                        if (r >= ROWS)
+                            break;
+                        const bool bad = (bad_rows >> (i * RPI + lane / CH)) & 1u;
+                        const uint4 codes = lds128(smem_u32(s_raw) + raw * C::RAW_BYTES + r * DIM + c * 16);
+                        const float scale = s_rscale[raw * ROWS + r];
+                        const uint32_t word[4] = {codes.x ^ 0x80808080u, codes.y ^ 0x80808080u, codes.z ^ 0x80808080u,
+                                                  codes.w ^ 0x80808080u};
+                        uint32_t out[8];
+                        const float f = is_k ? 1.0f : scale;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            out[k] = E::pack2(code_value(word[k / 2], 2 * (k & 1)) * f, code_value(word[k / 2], 2 * (k & 1) + 1) * f);
+                        const int row = half * ROWS + r;
+                        sts128(dst + chunk_at(row, 2 * c), make_uint4(out[0], out[1], out[2], out[3]));
+                        sts128(dst + chunk_at(row, 2 * c + 1), make_uint4(out[4], out[5], out[6], out[7]));
+                        if (is_k && c == 0)
+                            kscale[row] = bad ? NAN : scale;
+                    }
+                    __syncwarp();
+                    copy();
+                };
+                auto load_unit = [&](bool is_k) {
+                    const int slot = uses % UNITS;
+                    if (!wait(&empty[slot], (uses / UNITS + 1) & 1u))
+                        return false;
+                    ++uses;
+                    const uint32_t dst = smem_u32(s_ring) + slot * C::TILE_BYTES;
+                    float* kscale = s_kscale + k_tiles_ahead % C::SCALES * BM;
+                    k_tiles_ahead += is_k ? 1 : 0;
+                    widen(dst, 0, is_k, kscale);
+                    widen(dst, 1, is_k, kscale);
+                    landed(&full[slot]);
+                    return true;
+                };
+                bool ok = load_q(0);
+                bool first_q = true;
+#pragma unroll
+                for (int i = 0; i < C::RAWS - 1; ++i)
+                    copy();
+                for (; ok && at.left > 0; at.next(work)) {
+                    const int count = at.count();
+                    if (!first_q)
+                        ok = load_q(0);
+                    first_q = false;
+                    ok = ok && load_unit(true);
+                    if (ok && seqs(1) > 0)
+                        ok = load_q(1);
+                    for (int j = 0; ok && j < count; ++j) {
+                        ok = load_unit(false);
+                        if (ok && j + 1 < count)
+                            ok = load_unit(true);
+                    }
+                }
+                cp_async_wait<0>();
+            }
+            __syncwarp();
+        }
+    } else {
+        // ---------------------------------------------------------------------- softmax
+        setmaxnreg_inc<REGS_SOFTMAX>();
+        const int t = (warp - 4) >> 2;
+        const int quarter = warp & 3;  // tensor memory lanes that this warp may access
+        const int row = quarter * 32 + lane;
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        const uint32_t s_addr = tmem + lanes + t * BM, o_addr = tmem + lanes + 2 * BM + t * DIM;
+        const float c = a.c;
+        uint32_t phase = 0, o_phase = 0, k_tiles = 0;
+        bool ok = true;  // once a wait has given up, the remaining rows become NaN
+        for (; at.left > 0; at.next(work)) {
+            const int count = at.count();
+            const int rows = seqs(t) * group;
+            if (rows == 0) {
+                k_tiles += count;
+                continue;
+            }
+            float m = -INFINITY;  // what the row's sums are relative to, in units of scores
+            float l = 0.0f;
+            for (int j = 0; ok && j < count; ++j, ++k_tiles) {
+                ok = mbar_wait(&s_full[t], phase, abort_flag, err, kErrWaitPrefix, TIMEOUT_NS);
+                ok = __all_sync(FULL, ok);
+                if (!ok)
+                    break;
+                phase ^= 1u;
+                tc_fence_after();
+                const int keys = at.of.keys - (at.tile + j) * BM;  // of this tile and after it
+                uint32_t sr[4][32];
+                float tops[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    tmem_ld_max_32x32b_x32(s_addr + 32 * i, sr[i], tops[i]);
+                tmem_wait_ld();
+                if constexpr (INT8) {
+                    const uint32_t scales = smem_u32(s_kscale + k_tiles % C::SCALES * BM);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        tops[i] = -INFINITY;
+#pragma unroll
+                        for (int n = 0; n < 32; n += 4) {
+                            const uint4 f = lds128(scales + (32 * i + n) * 4);
+                            const float2 x = f2_mul_rn(make_float2(__uint_as_float(sr[i][n]), __uint_as_float(sr[i][n + 1])),
+                                                       make_float2(__uint_as_float(f.x), __uint_as_float(f.y)));
+                            const float2 y = f2_mul_rn(make_float2(__uint_as_float(sr[i][n + 2]), __uint_as_float(sr[i][n + 3])),
+                                                       make_float2(__uint_as_float(f.z), __uint_as_float(f.w)));
+                            sr[i][n] = __float_as_uint(x.x), sr[i][n + 1] = __float_as_uint(x.y);
+                            sr[i][n + 2] = __float_as_uint(y.x), sr[i][n + 3] = __float_as_uint(y.y);
+                            tops[i] = fmaxf(fmaxf(tops[i], fmaxf(x.x, x.y)), fmaxf(y.x, y.y));
+                        }
+                    }
+                }
+                if (keys < BM) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int nh = keys - 32 * i;
+                        const uint32_t seen = nh <= 0 ? 0u : nh >= 32 ? FULL : (1u << nh) - 1u;
+                        tops[i] = -INFINITY;
+#pragma unroll
+                        for (int n = 0; n < 32; ++n) {
+                            sr[i][n] = (seen >> n) & 1u ? sr[i][n] : 0xff800000u;
+                            tops[i] = fmaxf(tops[i], __uint_as_float(sr[i][n]));
+                        }
+                    }
+                }
+                float top = m;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    top = fmaxf(top, tops[i]);
+                const bool raise = (top - m) * c > kLag;  // (m is -inf before the first key)
+                if (__any_sync(FULL, raise)) {
+                    // bring the row's sums to the maximum
+                    const float f = raise ? fast_exp2((m - top) * c) : 1.0f;
+                    if (raise)
+                        m = top;
+                    l *= f;
+                    if (j > 0) {
+#pragma unroll 1
+                        for (int i = 0; i < DIM / 16; ++i) {
+                            uint32_t v[16];
+                            tmem_ld_32x32b_x16(o_addr + 16 * i, v);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int n = 0; n < 16; ++n)
+                                v[n] = __float_as_uint(__uint_as_float(v[n]) * f);
+                            tmem_st_32x32b_x16(o_addr + 16 * i, v);
+                        }
+                    }
+                }
+                const float mc = m == -INFINITY ? 0.0f : -m * c;  // no key with a score yet: weights 0
+                const float2 c2 = make_float2(c, c), mc2 = make_float2(mc, mc);
+                float2 sum = make_float2(0.0f, 0.0f);
+                constexpr int FIRST = FIRST_KEYS<DIM> / 32;
+                auto part = [&](auto from, auto to) {
+                    uint32_t packed[to.value - from.value][16];
+#pragma unroll
+                    for (int i = from.value; i < to.value; ++i)
+#pragma unroll
+                        for (int n = 0; n < 16; ++n) {
+                            float2 x = f2_fma_rn(make_float2(__uint_as_float(sr[i][2 * n]), __uint_as_float(sr[i][2 * n + 1])), c2,
+                                                 mc2);
+                            x.x = fast_exp2(x.x);
+                            x.y = fast_exp2(x.y);
+                            sum = f2_add_rn(sum, x);
+                            packed[i - from.value][n] = E::pack2(x.x, x.y);
+                        }
+#pragma unroll
+                    for (int i = from.value; i < to.value; ++i)
+                        tmem_st_32x32b_x16(s_addr + 16 * i, packed[i - from.value]);
+                };
+                if constexpr (FIRST > 0) {
+                    part(std::integral_constant<int, 0>(), std::integral_constant<int, FIRST>());
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&p_half[t]);
+                }
+                part(std::integral_constant<int, FIRST>(), std::integral_constant<int, 4>());
+                l += sum.x + sum.y;
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&p_full[t]);
+                __syncwarp();
+            }
+            // ---- the piece
+            if (ok) {
+                ok = mbar_wait(&o_full[t], o_phase, abort_flag, err, kErrWaitPrefix, TIMEOUT_NS);
+                ok = __all_sync(FULL, ok);
+                o_phase ^= 1u;
+                tc_fence_after();
+            }
+            float* part = parts + (blockIdx.x + at.unit) * prefix_piece(DIM);
+            if (ok) {
+#pragma unroll 1
+                for (int i = 0; i < DIM / 32; ++i) {
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32(o_addr + 32 * i, v);
+                    tmem_wait_ld();
+                    store_sums(part + (int64_t)(t * BM + quarter * 32) * DIM + 32 * i, DIM, lane, rows - quarter * 32, v);
+                }
+            }
+            if (row < rows)
+                reinterpret_cast<float2*>(part + (int64_t)kPrefixRows * DIM)[t * BM + row] =
+                    make_float2(ok ? m * c : 0.0f, ok ? l : NAN);
+            // O is read: the piece's last hand-over of P was before that, so the next one's first, which lets O be
+            // written again, says so too
+            tc_fence_before();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, TMEM_COLS);
+    }
+}
+
+template <class E, int DIM, bool INT8>
+cudaError_t launch(const PagedAttention& p, float* parts, const DeviceInfo& dev, unsigned int* err, cudaStream_t s)
+{
+    using C = Cfg<DIM, INT8>;
+    // a kernel attribute belongs to the context it was set in: set once per context
+    static ContextCache<int> cache;
+    int done = 0;
+    const cudaError_t e = cache.get(&done, [](int* d) {
+        *d = 1;
+        cudaFuncAttributes fa;
+        const cudaError_t r = cudaFuncGetAttributes(&fa, prefix_kernel<E, DIM, INT8>);
+        if (r != cudaSuccess)
+            return r;
+        // the softmax warps claim what warps 0-3 give back: the launch must provide the sum
+        if ((uint32_t)(fa.numRegs + 7) / 8 * 8 * THREADS < REGS_NEEDED_PER_BLOCK)
+            return cudaErrorLaunchOutOfResources;
+        return cudaFuncSetAttribute(prefix_kernel<E, DIM, INT8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+    });
+    if (e != cudaSuccess)
+        return e;
+    Args a{};
+    a.p = p;
+    a.group = p.q_heads / p.cache.heads;
+    a.work.shared = p.shared;
+    a.work.heads = p.cache.heads;
+    a.work.per_tile = BM / a.group;
+    // the softmax wants a positive factor: a negative scale negates Q in the first product, and for 0 the
+    // smallest factor that still keeps scores of -inf apart stands in
+    a.negate = p.scale < 0.0f;
+    a.c = std::max(std::fabs(p.scale) * kLog2e, 1e-30f);
+    return launch_pdl(prefix_kernel<E, DIM, INT8>, dim3((unsigned)std::min(dev.sm_count, kPrefixBlocks)), dim3(THREADS),
+                      C::SMEM, s, a, parts, err);
+}
+
+}  // namespace
+
+cudaError_t launch_prefix_pieces(const PagedAttention& p, float* parts, const DeviceInfo& dev, cudaStream_t s)
+{
+    unsigned int* err = nullptr;
+    const cudaError_t e = device_error_ptr(&err);
+    if (e != cudaSuccess)
+        return e;
+    auto by_cache = [&](auto type, auto dim) {
+        using E = decltype(type);
+        constexpr int DIM = decltype(dim)::value;
+        return p.cache.dtype == CK_KV_INT8 ? launch<E, DIM, true>(p, parts, dev, err, s)
+                                           : launch<E, DIM, false>(p, parts, dev, err, s);
+    };
+    if (p.cache.dim == 64)
+        return p.f16 ? by_cache(Fp16(), std::integral_constant<int, 64>()) : by_cache(Bf16(), std::integral_constant<int, 64>());
+    return p.f16 ? by_cache(Fp16(), std::integral_constant<int, 128>()) : by_cache(Bf16(), std::integral_constant<int, 128>());
+}
+
+}  // namespace ck

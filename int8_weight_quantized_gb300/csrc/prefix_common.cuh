@@ -1,0 +1,95 @@
+// prefix_common.cuh -- how the shared part of attention behind prefixes is divided into pieces, for the
+// kernel that computes them and the one that joins them.
+//
+// A unit is (prefix, kv head, up to 256 query rows: two tiles of floor(128 / group) sequences with all
+// query heads of the group); its keys are tiles of 128.  All units' key tiles in a row are cut evenly
+// over the blocks: block c of C takes tiles [c T / C, (c + 1) T / C), and leaves a piece of every unit
+// that it meets.  Piece (c, unit number u) lies at place c + u: going on either raises c or u.
+#pragma once
+
+#include <cstdint>
+
+#include "attn_common.cuh"
+#include "transformer.h"
+
+namespace ck {
+
+constexpr int kPrefixKeys = 128;                    // of a tile
+constexpr int kPrefixRows = 256;                    // of a unit
+constexpr int kPrefixBlocks = 152;                  // of any device this library runs on
+
+struct PrefixWork {
+    SharedPrefixes shared;
+    int heads;    // kv heads
+    int per_tile; // sequences of a query tile
+    struct Of {
+        int seqs, keys, pairs, tiles;  // tiles: 0 where there is nothing to do
+    };
+    // of prefix i (bounds ascending and inside the batch)
+    __device__ __forceinline__ Of of(int64_t i) const
+    {
+        Of w;
+        w.seqs = __ldg(shared.cu + i + 1) - __ldg(shared.cu + i);
+        const int64_t n = __ldg(shared.lens + i);
+        w.keys = n < 0 || n > shared.max_len ? 0 : (int)n;
+        w.pairs = (w.seqs + 2 * per_tile - 1) / (2 * per_tile);
+        w.tiles = w.seqs > 0 ? (w.keys + kPrefixKeys - 1) / kPrefixKeys : 0;
+        return w;
+    }
+    __device__ __forceinline__ int64_t units(const Of& w) const { return w.tiles > 0 ? (int64_t)heads * w.pairs : 0; }
+    // by a whole warp: key tiles and units of the prefixes before `upto`
+    __device__ __forceinline__ void before(int64_t upto, int64_t* tiles, int64_t* units_) const
+    {
+        int64_t t = 0, u = 0;
+        for (int64_t i = threadIdx.x & 31; i < upto; i += 32) {
+            const Of w = of(i);
+            const int64_t n = units(w);
+            u += n, t += n * w.tiles;
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            t += __shfl_xor_sync(0xffffffffu, t, o);
+            u += __shfl_xor_sync(0xffffffffu, u, o);
+        }
+        *tiles = t, *units_ = u;
+    }
+    // by a whole warp: the prefix that holds key tile `t` of all, and the tiles and units before it
+    __device__ __forceinline__ int64_t holds(int64_t t, int64_t* tiles, int64_t* units_) const
+    {
+        const int lane = threadIdx.x & 31;
+        int64_t base_t = 0, base_u = 0;
+        for (int64_t i0 = 0; i0 < shared.count; i0 += 32) {
+            int64_t u = 0, n = 0;
+            if (i0 + lane < shared.count) {
+                const Of w = of(i0 + lane);
+                u = units(w), n = u * w.tiles;
+            }
+            int64_t upto_t = n, upto_u = u;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t vt = __shfl_up_sync(0xffffffffu, upto_t, o), vu = __shfl_up_sync(0xffffffffu, upto_u, o);
+                if (lane >= o)
+                    upto_t += vt, upto_u += vu;
+            }
+            const uint32_t past = __ballot_sync(0xffffffffu, base_t + upto_t > t);
+            if (past) {
+                const int l = __ffs(past) - 1;
+                *tiles = base_t + __shfl_sync(0xffffffffu, upto_t - n, l);
+                *units_ = base_u + __shfl_sync(0xffffffffu, upto_u - u, l);
+                return i0 + l;
+            }
+            base_t += __shfl_sync(0xffffffffu, upto_t, 31);
+            base_u += __shfl_sync(0xffffffffu, upto_u, 31);
+        }
+        *tiles = base_t, *units_ = base_u;
+        return shared.count;
+    }
+};
+
+// floats of a piece: sums of its rows, then (maximum in units of log 2, sum of weights) of each
+__host__ __device__ constexpr int64_t prefix_piece(int dim)
+{
+    return (int64_t)kPrefixRows * (dim + 2);
+}
+
+}  // namespace ck

@@ -1,6 +1,6 @@
 // transformer.h -- host-side interface between the C ABI (api_transformer.cu) and the kernels
-// of the operators around the linear layers: norm_rope.cu, paged_attention.cu, cache_read.cu,
-// attention.cu, adapter.cu, logprobs.cu, int4.cu.  The public contract is include/ck_int8.h.
+// of the operators around the linear layers: norm_rope.cu, paged_attention.cu, prefix_attention.cu,
+// cache_read.cu, attention.cu, adapter.cu, logprobs.cu, int4.cu.  The public contract is include/ck_int8.h.
 #pragma once
 
 #include <cstddef>
@@ -99,11 +99,24 @@ struct PagedAttention {
     float* lse;  // or nullptr
     void* workspace;
     SharedPrefixes shared;
+    // behind prefixes, the shared part in pieces: theirs (nullptr: not so), the blocks that compute them,
+    // room for the sums over own keys, whether blocks share segments of these
+    float* pieces;
+    int piece_blocks;
+    float* own_sums;
+    bool own_split;
 };
 // by query heads per kv head and the most keys a sequence can have
 size_t paged_attention_workspace(int group, int dim, int64_t max_len);
 int paged_attention_launches(const PagedAttention& p);  // kernels that the call enqueues
 cudaError_t launch_paged_attention(const PagedAttention& p, const DeviceInfo& dev, cudaStream_t s);
+
+// Attention behind shared prefixes (p.shared.count >= 1).
+size_t prefix_attention_workspace(int64_t batch, int group, int kv_heads, int dim, int64_t prefixes, int64_t max_prefix_len,
+                                  int64_t max_len);
+int prefix_attention_launches(const PagedAttention& p);
+cudaError_t launch_prefix_attention(PagedAttention p, const DeviceInfo& dev, cudaStream_t s);
+cudaError_t launch_prefix_pieces(const PagedAttention& p, float* parts, const DeviceInfo& dev, cudaStream_t s);
 
 // Rows of the cache back as contiguous 16-bit keys and values.
 struct CacheRead {
