@@ -369,22 +369,10 @@ __global__ void __launch_bounds__(MANY_THREADS, 2)
 // [rows, K] of 16 bits as boxes of `box_rows` x 64.
 bool make_map_2d(CUtensorMap* map, const void* base, int64_t rows, int64_t K, int box_rows, bool f16, std::string* why)
 {
-    auto fn = encode_fn();
-    if (!fn) {
-        *why = "cuTensorMapEncodeTiled is not available from the driver";
-        return false;
-    }
-    cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)K * 2};
-    cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
-    cuuint32_t estr[2] = {1, 1};
-    const CUresult r = fn(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-                          const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS)
-        *why = "cuTensorMapEncodeTiled failed (" + std::to_string((int)r) + ")";
-    return r == CUDA_SUCCESS;
+    const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)K * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+    return make_box_map(map, base, 2, dims, strides, box, f16, why);
 }
 
 // ---- 8 neighbouring outputs of a lane

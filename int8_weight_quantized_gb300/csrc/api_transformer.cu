@@ -352,9 +352,15 @@ int ck_prefix_attention(const void* q, int64_t q_stride, const ck_kv_cache_t* ca
     p.shared.max_len = max_prefix_blocks * p.cache.page_size;
     log_shape("prefix_attention", batch, q_heads, p.cache.dim, p.cache.dtype, "keys of a group's prefix and its own");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    ProfScope ps(kProfAttention, prefix_attention_launches(p), s);
-    const cudaError_t e = launch_prefix_attention(p, dev, s);
-    return e == cudaSuccess ? CK_OK : cuda_fail(e, "ck_prefix_attention launch");
+    std::string why;
+    cudaError_t e;
+    {
+        ProfScope ps(kProfAttention, prefix_attention_launches(p), s);
+        e = launch_prefix_attention(p, dev, s, &why);
+    }
+    if (e != cudaSuccess)
+        return why.empty() ? cuda_fail(e, "ck_prefix_attention launch") : fail(CK_ERR_CUDA, "%s", why.c_str());
+    return CK_OK;
 }
 
 int ck_cache_read(const ck_kv_cache_t* cache, const int32_t* block_table, int64_t max_blocks, const int32_t* cu,

@@ -980,22 +980,10 @@ __global__ void __launch_bounds__(THREADS, 1)
 bool make_map(CUtensorMap* map, const void* base, int64_t rows, int heads, int dim, int64_t stride, bool f16,
               std::string* why)
 {
-    auto fn = encode_fn();
-    if (!fn) {
-        *why = "cuTensorMapEncodeTiled is not available from the driver";
-        return false;
-    }
-    cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)rows};
-    cuuint64_t strides[2] = {(cuuint64_t)dim * 2, (cuuint64_t)stride * 2};
-    cuuint32_t box[3] = {64, 1, BM};
-    cuuint32_t estr[3] = {1, 1, 1};
-    const CUresult r = fn(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-                          const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS)
-        *why = "cuTensorMapEncodeTiled failed (" + std::to_string((int)r) + ")";
-    return r == CUDA_SUCCESS;
+    const cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)rows};
+    const cuuint64_t strides[2] = {(cuuint64_t)dim * 2, (cuuint64_t)stride * 2};
+    const cuuint32_t box[3] = {64, 1, BM};
+    return make_box_map(map, base, 3, dims, strides, box, f16, why);
 }
 
 template <class E, int DIM, bool WINDOW>

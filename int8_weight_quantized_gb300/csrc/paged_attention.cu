@@ -1022,7 +1022,7 @@ int prefix_attention_launches(const PagedAttention& p)
     return in_pieces(p.batch, p.q_heads / p.cache.heads, p.shared.count, p.shared.max_len) ? 3 : paged_attention_launches(p);
 }
 
-cudaError_t launch_prefix_attention(PagedAttention p, const DeviceInfo& dev, cudaStream_t s)
+cudaError_t launch_prefix_attention(PagedAttention p, const DeviceInfo& dev, cudaStream_t s, std::string* why)
 {
     const int group = p.q_heads / p.cache.heads;
     if (!in_pieces(p.batch, group, p.shared.count, p.shared.max_len))
@@ -1034,7 +1034,7 @@ cudaError_t launch_prefix_attention(PagedAttention p, const DeviceInfo& dev, cud
     p.workspace = ws;
     ws += align256(paged_attention_workspace(group, p.cache.dim, p.max_blocks * p.cache.page_size));
     p.own_sums = reinterpret_cast<float*>(ws);
-    const cudaError_t e = launch_prefix_pieces(p, p.pieces, dev, s);
+    const cudaError_t e = launch_prefix_pieces(p, p.pieces, dev, s, why);
     return e == cudaSuccess ? launch_paged_attention(p, dev, s) : e;
 }
 

@@ -11,9 +11,9 @@
 // its roles run on from piece to piece:
 //   warp 0      issues the products, one lane: S_t = Q_t K^T, O_t += P_t V, sums in tensor memory, in
 //               the order O_0 += P_0 V_j, S_0 = Q_0 K_{j+1}, O_1 += P_1 V_j, S_1 = Q_1 K_{j+1};
-//   warps 1-3   copies: rows of the pages, whatever their size, by 16-byte asynchronous copies into the
-//               swizzled layout that the products read; int8 rows through a small ring of raw codes,
-//               each thread widening what it copied itself;
+//   warps 1-3   copies: queries, and rows of pages of a multiple of 8, by TMA; rows of other pages, and those
+//               of a prefix's last tile, by 16-byte asynchronous copies into the same swizzled layout; int8
+//               rows through a small ring of raw codes, each thread widening what it copied itself;
 //   warps 4-11  softmax, a warpgroup for each query tile, one thread per row, as in attention.cu: the
 //               weights go back over S as the 16-bit operand P of the second product, the row's
 //               reference trails its maximum by up to 2^8.
@@ -76,6 +76,7 @@ struct Args {
     int group;
     bool negate;
     float c;  // |scale| log2 e
+    int box;  // rows of a page that one copy by TMA takes, 0: none do
 };
 
 // A block's way through its key tiles, piece by piece.
@@ -152,7 +153,9 @@ __device__ __forceinline__ float code_value(uint32_t flipped, int i)
 }
 
 template <class E, int DIM, bool INT8>
-__global__ void __launch_bounds__(THREADS, 1) prefix_kernel(const Args a, float* parts, unsigned int* err)
+__global__ void __launch_bounds__(THREADS, 1)
+    prefix_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                  const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Args a, float* parts, unsigned int* err)
 {
     using C = Cfg<DIM, INT8>;
     using T = typename E::T;
@@ -197,6 +200,9 @@ __global__ void __launch_bounds__(THREADS, 1) prefix_kernel(const Args a, float*
         *abort_flag = 0;
         fence_mbar_init();
         fence_proxy_async_smem();
+        tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
     }
     if (warp == 0) {
         __syncwarp();
@@ -413,91 +419,166 @@ __global__ void __launch_bounds__(THREADS, 1) prefix_kernel(const Args a, float*
             auto chunk_at = [&](int r, int c) {
                 return (uint32_t)((c >> 3) * C::BOX_BYTES + r * 128 + (((c & 7) ^ (r & 7)) << 4));
             };
+            // Every warp arrives at each tile's barrier: the first of them, with the bytes that it has asked for, where
+            // a tile comes by TMA.
             auto load_q = [&](int t) {
                 if (!wait(&q_empty[t], (q_uses[t] + 1) & 1u))
                     return false;
                 ++q_uses[t];
-                const int rows = seqs(t) * group;
-                const T* q = static_cast<const T*>(a.p.q) +
-                             (at.seq0 + (2 * at.pair + t) * per_tile) * a.p.q_stride + (int64_t)at.head * group * DIM;
-                const uint32_t dst = smem_u32(s_q) + t * C::TILE_BYTES;
-                constexpr int CH = DIM / 8;
-                for (int i = w * 32 + lane; i < BM * CH; i += LOADERS * 32) {
-                    const int r = i / CH, c = i % CH, s = r / group;
-                    const bool ok = r < rows;
-                    cp_async16(dst + chunk_at(r, c), ok ? q + s * a.p.q_stride + (r - s * group) * DIM + c * 8 : q, ok);
+                if (lane == 0) {
+                    if (w == 0) {
+                        mbar_arrive_expect_tx(&q_full[t], (uint32_t)(DIM / 64 * per_tile * group * 128));
+                        for (int x = 0; x < DIM / 64; ++x)
+                            tma_load_3d(s_q + t * C::TILE_BYTES + x * C::BOX_BYTES, &tmQ, &q_full[t], x * 64, at.head * group,
+                                        (int32_t)(at.seq0 + (2 * at.pair + t) * per_tile));
+                    } else {
+                        mbar_arrive(&q_full[t]);
+                    }
                 }
-                sent(&q_full[t]);
-                if (INT8)
-                    all_landed();
+                __syncwarp();
                 return true;
             };
-            // where key `j` of the prefix lies: its row in the cache; ok: there is one, bad: on a page out of range
-            auto row_of = [&](int j, bool* ok, bool* bad) {
-                *ok = *bad = false;
-                if (j >= at.of.keys)
-                    return 0u;
+            // the page of key `j` of a walk's prefix, -1 past its end; and the key's row in the cache
+            auto page_of = [&](const Walk& of, int j) {
+                if (j >= of.of.keys)
+                    return -1;
                 const int blk = a.p.page_shift >= 0 ? j >> a.p.page_shift : j / cache.page_size;
-                const int32_t page = __ldg(work.shared.table + at.prefix * work.shared.max_blocks + blk);
-                *ok = page >= 0 && page < cache.num_pages;
-                *bad = !*ok;
-                return *ok ? ((uint32_t)page * cache.heads + at.head) * cache.page_size + (j - blk * cache.page_size) : 0u;
+                return (int)__ldg(work.shared.table + of.prefix * work.shared.max_blocks + blk);
             };
+            auto row_of = [&](const Walk& of, int j, int page, bool* ok, bool* bad) {
+                const bool there = j < of.of.keys;
+                *ok = there && page >= 0 && page < cache.num_pages;
+                *bad = there && !*ok;
+                const int in_page = a.p.page_shift >= 0 ? j & (cache.page_size - 1) : j % cache.page_size;
+                return *ok ? ((uint32_t)page * cache.heads + of.head) * cache.page_size + in_page : 0u;
+            };
+            bool ok = true;
             if constexpr (!INT8) {
                 // a copy instruction takes RPI rows, the warps by turns; number n of a warp's rows is row
                 // (n / RPI * LOADERS + w) * RPI + n % RPI, and its lane n % 32 looks it up
                 constexpr int CH = DIM / 8, RPI = 32 / CH, TURNS = (BM / RPI + LOADERS - 1) / LOADERS;
                 static_assert(TURNS * RPI <= 64, "two rows a lane");
-                uint32_t rows[2], oks[2], bads[2];
-                auto look_up = [&](int tile) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int n = 32 * h + lane, r = (n / RPI * LOADERS + w) * RPI + n % RPI;
-                        bool ok = false, bad = false;
-                        rows[h] = 0;
-                        if (n < TURNS * RPI && r < BM)
-                            rows[h] = row_of(tile * BM + r, &ok, &bad);
-                        oks[h] = __ballot_sync(FULL, ok), bads[h] = __ballot_sync(FULL, bad);
-                    }
-                    if ((bads[0] | bads[1]) && lane == 0)
-                        atomicOr(err, kErrIndex);
+                uint32_t rows[2] = {}, oks[2] = {}, bads[2] = {};
+                // pages are asked for a tile ahead
+                Walk ahead = at;
+                int ahead_tile = 0;  // of the piece
+                int pages[2] = {};
+                auto row_in_tile = [&](int h) {
+                    const int n = 32 * h + lane, r = (n / RPI * LOADERS + w) * RPI + n % RPI;
+                    return n < TURNS * RPI && r < BM ? r : -1;
                 };
-                auto load_unit = [&](bool is_k) {
-                    const int slot = uses % UNITS;
-                    if (!wait(&empty[slot], (uses / UNITS + 1) & 1u))
-                        return false;
-                    ++uses;
+                auto by_tma = [&](const Walk& of, int tile) { return a.box > 0 && of.of.keys - tile * BM >= BM; };
+                int box_page = 0, box_asked = 0;
+                auto ask = [&]() {
+                    if (ahead.left <= 0)
+                        return;
+                    const int tile = ahead.tile + ahead_tile;
+                    if (by_tma(ahead, tile)) {
+                        box_asked = page_of(ahead, tile * BM + lane % (BM / a.box) * a.box);
+                        return;
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (row_in_tile(h) >= 0)
+                            pages[h] = page_of(ahead, tile * BM + row_in_tile(h));
+                };
+                auto look_up = [&](int tile) {
+                    box_page = box_asked;
+                    if (!by_tma(at, tile)) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            bool ok = false, bad = false;
+                            rows[h] = 0;
+                            if (row_in_tile(h) >= 0)
+                                rows[h] = row_of(at, tile * BM + row_in_tile(h), pages[h], &ok, &bad);
+                            oks[h] = __ballot_sync(FULL, ok), bads[h] = __ballot_sync(FULL, bad);
+                        }
+                        if ((bads[0] | bads[1]) && lane == 0)
+                            atomicOr(err, kErrIndex);
+                    }
+                    if (++ahead_tile == ahead.count()) {
+                        ahead_tile = 0;
+                        ahead.next(work);
+                    }
+                    ask();
+                };
+                ask();
+                // A tile whose keys are all there comes by TMA, a lane of the first warp for each box of rows of one page
+                // and 64 values; one on a page out of range gets NaN for K and zeros for V.
+                const int box = a.box, boxes = box > 0 ? BM / box * (DIM / 64) : 0;
+                auto load_boxes = [&](bool is_k, int slot, int tile) {
+                    uint8_t* dst = s_ring + slot * C::TILE_BYTES;
+                    if (w != 0) {
+                        if (lane == 0)
+                            mbar_arrive(&full[slot]);
+                        __syncwarp();
+                        return;
+                    }
+                    // (boxes <= 32: one turn)
+                    const int r = lane % (BM / box) * box, x = lane / (BM / box);
+                    bool ok = false, bad = false;
+                    uint32_t row = 0;
+                    if (lane < boxes)
+                        row = row_of(at, tile * BM + r, box_page, &ok, &bad);
+                    if (bad) {
+                        const uint32_t fill = is_k ? 0x7fff7fffu : 0u;
+                        for (int i = 0; i < box * 8; ++i)
+                            sts128(smem_u32(dst + x * C::BOX_BYTES + r * 128 + i * 16), make_uint4(fill, fill, fill, fill));
+                        fence_proxy_async_smem();
+                        atomicOr(err, kErrIndex);
+                    }
+                    const uint32_t oks = __ballot_sync(FULL, ok);
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(&full[slot], (uint32_t)(__popc(oks) * box * 128));
+                    __syncwarp();
+                    if (ok)
+                        tma_load_2d(dst + x * C::BOX_BYTES + r * 128, is_k ? &tmK : &tmV, &full[slot], x * 64, (int32_t)row);
+                    __syncwarp();
+                };
+                auto load_rows = [&](bool is_k, int slot) {
                     const uint8_t* base = static_cast<const uint8_t*>(is_k ? cache.k : cache.v) + lane % CH * 16;
                     const uint32_t dst = smem_u32(s_ring) + slot * C::TILE_BYTES;
-#pragma unroll
+#pragma unroll 2
                     for (int i = 0; i < TURNS; ++i) {
-                        const int r = (i * LOADERS + w) * RPI + lane / CH, n = i * RPI + lane / CH;
-                        const uint32_t row = __shfl_sync(FULL, rows[i * RPI / 32], n % 32);
+                        const int r = (i * LOADERS + w) * RPI + lane / CH, n = i * RPI + lane / CH, h = i * RPI / 32;
+                        const uint32_t row = __shfl_sync(FULL, h ? rows[1] : rows[0], n % 32);
                         if (r < BM) {
-                            const bool ok = (oks[i * RPI / 32] >> (n % 32)) & 1u;
+                            const bool ok = ((h ? oks[1] : oks[0]) >> (n % 32)) & 1u;
                             const uint32_t to = dst + chunk_at(r, lane % CH);
-                            if (is_k && ((bads[i * RPI / 32] >> (n % 32)) & 1u))
+                            if (is_k && (((h ? bads[1] : bads[0]) >> (n % 32)) & 1u))
                                 sts128(to, make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu));  // NaN
                             else
                                 cp_async16(to, base + (uint64_t)row * (DIM * 2), ok);
                         }
                     }
                     sent(&full[slot]);
+                };
+                auto load_unit = [&](bool is_k, int tile) {
+                    const int slot = uses % UNITS;
+                    if (!wait(&empty[slot], (uses / UNITS + 1) & 1u))
+                        return false;
+                    ++uses;
+                    if (by_tma(at, tile)) {
+                        if (in_flight > 0)
+                            all_landed();
+                        load_boxes(is_k, slot, tile);
+                    } else {
+                        load_rows(is_k, slot);
+                    }
                     return true;
                 };
-                bool ok = true;
                 for (; ok && at.left > 0; at.next(work)) {
                     const int count = at.count();
                     ok = load_q(0);
                     look_up(at.tile);
-                    ok = ok && load_unit(true);
+                    ok = ok && load_unit(true, at.tile);
                     if (ok && seqs(1) > 0)
                         ok = load_q(1);
                     for (int j = 0; ok && j < count; ++j) {
-                        ok = load_unit(false);
+                        ok = load_unit(false, at.tile + j);
                         if (ok && j + 1 < count) {
                             look_up(at.tile + j + 1);
-                            ok = load_unit(true);
+                            ok = load_unit(true, at.tile + j + 1);
                         }
                     }
                 }
@@ -520,15 +601,8 @@ __global__ void __launch_bounds__(THREADS, 1) prefix_kernel(const Args a, float*
                         const int n = lane, r = (n / RPI * LOADERS + w) * RPI + n % RPI;
                         bool ok = false, bad = false;
                         uint32_t row = 0;
-                        if (n < TURNS * RPI && r < ROWS && first + r < ahead.of.keys) {
-                            const int j = first + r;
-                            const int blk = a.p.page_shift >= 0 ? j >> a.p.page_shift : j / cache.page_size;
-                            const int32_t page = __ldg(work.shared.table + ahead.prefix * work.shared.max_blocks + blk);
-                            ok = page >= 0 && page < cache.num_pages;
-                            bad = !ok;
-                            row = ok ? ((uint32_t)page * cache.heads + ahead.head) * cache.page_size + (j - blk * cache.page_size)
-                                     : 0u;
-                        }
+                        if (n < TURNS * RPI && r < ROWS)
+                            row = row_of(ahead, first + r, page_of(ahead, first + r), &ok, &bad);
                         const uint32_t oks = __ballot_sync(FULL, ok), bad_rows = __ballot_sync(FULL, bad);
 #pragma unroll
                         for (int i = 0; i < C::RAWS; ++i)
@@ -603,7 +677,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefix_kernel(const Args a, float*
                     landed(&full[slot]);
                     return true;
                 };
-                bool ok = load_q(0);
+                ok = load_q(0);
                 bool first_q = true;
 #pragma unroll
                 for (int i = 0; i < C::RAWS - 1; ++i)
@@ -623,6 +697,13 @@ __global__ void __launch_bounds__(THREADS, 1) prefix_kernel(const Args a, float*
                     }
                 }
                 cp_async_wait<0>();
+            }
+            if (!ok && w == 0 && lane == 0) {  // aborting: every issued copy lands before shared memory is released
+                for (int t = 0; t < 2; ++t)
+                    if (q_uses[t] > 0)
+                        wait_out(&q_full[t], (q_uses[t] - 1) & 1u, err, kErrWaitPrefix, TIMEOUT_NS);
+                for (uint32_t i = INT8 ? uses : uses > UNITS ? uses - UNITS : 0; i < uses; ++i)
+                    wait_out(&full[i % UNITS], (i / UNITS) & 1u, err, kErrWaitPrefix, TIMEOUT_NS);
             }
             __syncwarp();
         }
@@ -787,7 +868,8 @@ __global__ void __launch_bounds__(THREADS, 1) prefix_kernel(const Args a, float*
 }
 
 template <class E, int DIM, bool INT8>
-cudaError_t launch(const PagedAttention& p, float* parts, const DeviceInfo& dev, unsigned int* err, cudaStream_t s)
+cudaError_t launch(const PagedAttention& p, float* parts, const DeviceInfo& dev, unsigned int* err, cudaStream_t s,
+                   std::string* why)
 {
     using C = Cfg<DIM, INT8>;
     // a kernel attribute belongs to the context it was set in: set once per context
@@ -816,13 +898,34 @@ cudaError_t launch(const PagedAttention& p, float* parts, const DeviceInfo& dev,
     // smallest factor that still keeps scores of -inf apart stands in
     a.negate = p.scale < 0.0f;
     a.c = std::max(std::fabs(p.scale) * kLog2e, 1e-30f);
+    // Whole rows of one page at a time by TMA, where pages have 8 rows (the swizzle's period) or a multiple, a
+    // tile takes no more boxes than a warp has lanes, and coordinates suffice; row by row otherwise.
+    int box = 1;
+    while (box < BM && p.cache.page_size % (2 * box) == 0)
+        box *= 2;
+    const int64_t rows = p.cache.num_pages * p.cache.heads * p.cache.page_size;
+    a.box = !INT8 && box >= 8 && BM / box * (DIM / 64) <= 32 && rows <= 0x7FFFFFFF ? box : 0;
+    const cuuint64_t q_dims[3] = {DIM, (cuuint64_t)p.q_heads, (cuuint64_t)p.batch};
+    const cuuint64_t q_strides[2] = {DIM * 2, (cuuint64_t)p.q_stride * 2};
+    const cuuint32_t q_box[3] = {64, (cuuint32_t)a.group, (cuuint32_t)a.work.per_tile};
+    const cuuint64_t dims[2] = {DIM, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {DIM * 2};
+    const cuuint32_t kv_box[2] = {64, (cuuint32_t)std::max(a.box, 1)};
+    CUtensorMap q, k, v;
+    if (!make_box_map(&q, p.q, 3, q_dims, q_strides, q_box, p.f16, why))
+        return cudaErrorInvalidValue;
+    k = v = q;
+    if (a.box > 0 && (!make_box_map(&k, p.cache.k, 2, dims, strides, kv_box, p.f16, why) ||
+                      !make_box_map(&v, p.cache.v, 2, dims, strides, kv_box, p.f16, why)))
+        return cudaErrorInvalidValue;
     return launch_pdl(prefix_kernel<E, DIM, INT8>, dim3((unsigned)std::min(dev.sm_count, kPrefixBlocks)), dim3(THREADS),
-                      C::SMEM, s, a, parts, err);
+                      C::SMEM, s, q, k, v, a, parts, err);
 }
 
 }  // namespace
 
-cudaError_t launch_prefix_pieces(const PagedAttention& p, float* parts, const DeviceInfo& dev, cudaStream_t s)
+cudaError_t launch_prefix_pieces(const PagedAttention& p, float* parts, const DeviceInfo& dev, cudaStream_t s,
+                                 std::string* why)
 {
     unsigned int* err = nullptr;
     const cudaError_t e = device_error_ptr(&err);
@@ -831,8 +934,8 @@ cudaError_t launch_prefix_pieces(const PagedAttention& p, float* parts, const De
     auto by_cache = [&](auto type, auto dim) {
         using E = decltype(type);
         constexpr int DIM = decltype(dim)::value;
-        return p.cache.dtype == CK_KV_INT8 ? launch<E, DIM, true>(p, parts, dev, err, s)
-                                           : launch<E, DIM, false>(p, parts, dev, err, s);
+        return p.cache.dtype == CK_KV_INT8 ? launch<E, DIM, true>(p, parts, dev, err, s, why)
+                                           : launch<E, DIM, false>(p, parts, dev, err, s, why);
     };
     if (p.cache.dim == 64)
         return p.f16 ? by_cache(Fp16(), std::integral_constant<int, 64>()) : by_cache(Bf16(), std::integral_constant<int, 64>());

@@ -115,8 +115,9 @@ cudaError_t launch_paged_attention(const PagedAttention& p, const DeviceInfo& de
 size_t prefix_attention_workspace(int64_t batch, int group, int kv_heads, int dim, int64_t prefixes, int64_t max_prefix_len,
                                   int64_t max_len);
 int prefix_attention_launches(const PagedAttention& p);
-cudaError_t launch_prefix_attention(PagedAttention p, const DeviceInfo& dev, cudaStream_t s);
-cudaError_t launch_prefix_pieces(const PagedAttention& p, float* parts, const DeviceInfo& dev, cudaStream_t s);
+cudaError_t launch_prefix_attention(PagedAttention p, const DeviceInfo& dev, cudaStream_t s, std::string* why);
+cudaError_t launch_prefix_pieces(const PagedAttention& p, float* parts, const DeviceInfo& dev, cudaStream_t s,
+                                 std::string* why);
 
 // Rows of the cache back as contiguous 16-bit keys and values.
 struct CacheRead {
