@@ -256,10 +256,13 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
     // nothing of its own is read here: this one only has to end after it.)
     if constexpr (MODE != kOwnBesidePieces)
         griddep_wait();
+    else
+        griddep_launch_dependents();
     auto end = [] {
         if constexpr (MODE == kOwnBesidePieces)
             griddep_wait();
-        griddep_launch_dependents();
+        else
+            griddep_launch_dependents();
     };
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
@@ -704,6 +707,10 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<INT8, DIM, NT>::BLOCKS)
             float* part = static_cast<float*>(p.workspace) + (2 * (int64_t)blockIdx.x + piece) * S::PART;
             float2* part_sums = reinterpret_cast<float2*>(part + HEADS * DIM);
             constexpr bool JOINED = MODE == kOwnBesidePieces;  // every segment's sums go to the last kernel
+            if (JOINED) {
+                part = static_cast<float*>(p.workspace) + (2 * (int64_t)blockIdx.x + (first_of_segment == 0 ? 1 : 0)) * S::PART;
+                part_sums = reinterpret_cast<float2*>(part + HEADS * DIM);
+            }
             if (JOINED && whole) {
                 const int64_t at_row = at.b * p.q_heads + h0;
                 part = p.own_sums + at_row * DIM;
@@ -778,98 +785,41 @@ __global__ void __launch_bounds__(128) join_kernel(const PagedAttention p, int64
     const int group = p.q_heads / p.cache.heads;
     const int qtiles = (group + HEADS - 1) / HEADS;
     const Lengths<MODE> L = lengths_of<MODE>(p, p.cache.heads * qtiles, tile);
-    constexpr bool BESIDE = MODE == kOwnBesidePieces;
     const int tiles = L.tiles(b);
-    if (!BESIDE && tiles == 0)
+    if (tiles == 0)
         return;  // the first kernel wrote it
-    const int64_t at_row = b * p.q_heads + h;
-    const int in_group = h % group;
-    // the prefix's pieces
-    int64_t pieces = 0, piece0 = 0;
-    int piece_row = 0;
-    if constexpr (BESIDE) {
-        bool bad;
-        L.length(b, &bad);
-        bad |= p.shared.bad_groups(p.batch);
-        const int prefix = bad ? -1 : p.shared.of(b);
-        if (prefix >= 0) {
-            const int64_t n = __ldg(p.shared.lens + prefix);
-            bad |= n < 0 || n > p.shared.max_len;
-            const PrefixWork work{p.shared, p.cache.heads, 128 / group};
-            const PrefixWork::Of of = work.of(prefix);
-            if (of.tiles > 0) {
-                int64_t total, units, before, units_before;
-                work.before(p.shared.count, &total, &units);
-                work.before(prefix, &before, &units_before);
-                const int64_t blocks = min((int64_t)p.piece_blocks, total);
-                const int seq = (int)(b - __ldg(p.shared.cu + prefix)), pair = seq / (2 * work.per_tile);
-                const int in_pair = seq - pair * 2 * work.per_tile, t = in_pair / work.per_tile;
-                piece_row = t * kPrefixKeys + (in_pair - t * work.per_tile) * group + in_group;
-                const int64_t unit = (int64_t)(h / group) * of.pairs + pair;
-                const int64_t t0 = before + unit * of.tiles, t1 = t0 + of.tiles;
-                const int64_t c0 = ((t0 + 1) * blocks - 1) / total, c1 = (t1 * blocks - 1) / total;
-                pieces = c1 - c0 + 1;
-                piece0 = c0 + units_before + unit;
-            }
-        }
-        if (bad || (pieces == 0 && tiles == 0)) {
-            for (int d = threadIdx.x; d < DIM; d += 128)
-                static_cast<T*>(p.out)[at_row * DIM + d] = E::from(bad ? NAN : 0.0f);
-            if (threadIdx.x == 0 && p.lse != nullptr)
-                p.lse[at_row] = bad ? NAN : -INFINITY;
-            return;
-        }
-    }
-    const int64_t total = tiles > 0 ? tiles_before(L, p.batch) : 1;
+    const int64_t total = tiles_before(L, p.batch);
     C = min(C, total);
+    const int in_group = h % group;
     const int64_t sub = h / group * qtiles + in_group / HEADS;
     const int row = in_group % HEADS;
-    const int64_t t0 = tiles > 0 ? tiles_before(L, b) + sub * tiles : 0, t1 = t0 + tiles;
+    const int64_t t0 = tiles_before(L, b) + sub * tiles, t1 = t0 + tiles;
     // block c holds tile t: c = floor(((t + 1) C - 1) / T)
-    int64_t c0 = 0, c1 = -1;
-    if (tiles > 0 && (!BESIDE || p.own_split))
-        c0 = ((t0 + 1) * C - 1) / total, c1 = (t1 * C - 1) / total;
-    const bool whole = tiles > 0 && (BESIDE && !p.own_split ? true : c0 == c1);
-    if (!BESIDE && whole)
+    const int64_t c0 = ((t0 + 1) * C - 1) / total, c1 = (t1 * C - 1) / total;
+    if (c0 == c1)
         return;  // one block held the whole segment and wrote the output
     const float* ws = static_cast<const float*>(p.workspace);
     float m = -INFINITY, l = 0.0f;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    const int64_t own = tiles == 0 ? 0 : whole ? 1 : c1 - c0 + 1;
-    for (int64_t i = warp; i < pieces + own; i += 4) {
-        const float* part;
-        const float2* part_sum;
-        int part_row = row;
-        const int64_t c = c0 + (i - pieces);
-        if (BESIDE && i < pieces) {
-            part = p.pieces + (piece0 + i) * prefix_piece(DIM);
-            part_sum = reinterpret_cast<const float2*>(part + (int64_t)kPrefixRows * DIM) + piece_row;
-            part_row = piece_row;
-        } else if (BESIDE && whole) {
-            part = p.own_sums + at_row * DIM;
-            part_sum = reinterpret_cast<const float2*>(p.own_sums + p.batch * p.q_heads * DIM) + at_row;
-            part_row = 0;
-        } else {
-            // Slot 0 holds the first partial that block c left.  That is this segment, unless c = c0
-            // began inside an earlier segment and had to leave that one first.
-            int slot = 0;
-            if (c == c0) {
-                const int64_t begin = first_tile(c, C, total);
-                if (begin < t0) {
-                    // an earlier piece was partial exactly if the block began inside its segment
-                    int64_t before;
-                    const int64_t bb = sequence_at(L, p.batch, begin, &before);
-                    const int bt = L.tiles(bb);
-                    slot = (begin - before) % bt != 0 ? 1 : 0;
-                }
+    for (int64_t c = c0 + warp; c <= c1; c += 4) {
+        // Slot 0 holds the first partial that block c left.  That is this segment, unless c = c0
+        // began inside an earlier segment and had to leave that one first.
+        int slot = 0;
+        if (c == c0) {
+            const int64_t begin = first_tile(c, C, total);
+            if (begin < t0) {
+                // an earlier piece was partial exactly if the block began inside its segment
+                int64_t before;
+                const int64_t bb = sequence_at(L, p.batch, begin, &before);
+                const int bt = L.tiles(bb);
+                slot = (begin - before) % bt != 0 ? 1 : 0;
             }
-            part = ws + (2 * c + slot) * PART;
-            part_sum = reinterpret_cast<const float2*>(part + HEADS * DIM) + row;
         }
-        const float2 ms = __ldcg(part_sum);
+        const float* part = ws + (2 * c + slot) * PART;
+        const float2 ms = __ldcg(reinterpret_cast<const float2*>(part + HEADS * DIM) + row);
         float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (lane < DIM / 4)
-            x = __ldcg(reinterpret_cast<const float4*>(part + (int64_t)part_row * DIM) + lane);
+            x = __ldcg(reinterpret_cast<const float4*>(part + row * DIM) + lane);
         const float m2 = fmaxf(m, ms.x);
         const float ref = m2 == -INFINITY ? 0.0f : m2;
         const float a = fast_exp2(m - ref), f = fast_exp2(ms.x - ref);
@@ -898,11 +848,169 @@ __global__ void __launch_bounds__(128) join_kernel(const PagedAttention p, int64
         sum += maxsum[w].y * f;
         acc.x += x.x * f, acc.y += x.y * f, acc.z += x.z * f, acc.w += x.w * f;
     }
+    const int64_t at_row = b * p.q_heads + h;
     if (lane < DIM / 4)
         *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + at_row * DIM + lane * 4) =
             make_uint2(E::pack2(acc.x / sum, acc.y / sum), E::pack2(acc.z / sum, acc.w / sum));
     if (lane == 0 && p.lse != nullptr)
         p.lse[at_row] = (top + log2f(sum)) * kLn2;
+}
+
+// Beside pieces: adds up, for each query head, the pieces of its sequence's prefix and the sums over the
+// sequence's own keys, a warp to a head.  What the lengths say is worked out before the other kernels have
+// ended.
+template <class E, int DIM, int NT>
+__global__ void __launch_bounds__(256) join_pieces_kernel(const PagedAttention p, int64_t C, int tile)
+{
+    using T = typename E::T;
+    constexpr int HEADS = 8 * NT, VEC = DIM / 32;
+    constexpr size_t PART = (size_t)HEADS * (DIM + 2);
+    __shared__ int64_t s_own[2], s_shared[4];
+    __shared__ PrefixWork::Of s_of;
+    __shared__ int s_bad[2];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int per = (p.q_heads + 7) / 8;  // blocks of a sequence
+    const int64_t b = blockIdx.x / per;
+    const int h = (int)(blockIdx.x - b * per) * 8 + warp;
+    const int group = p.q_heads / p.cache.heads;
+    const int qtiles = (group + HEADS - 1) / HEADS;
+    const Lengths<kOwnBesidePieces> L = lengths_of<kOwnBesidePieces>(p, p.cache.heads * qtiles, tile);
+    const PrefixWork work{p.shared, p.cache.heads, kPrefixKeys / group};
+    if (warp == 0) {
+        bool bad;
+        L.length(b, &bad);
+        const int64_t total = p.own_split ? tiles_before(L, p.batch) : 0, before = p.own_split ? tiles_before(L, b) : 0;
+        if (lane == 0)
+            s_own[0] = total, s_own[1] = before, s_bad[0] = bad;
+    } else if (warp == 1) {
+        bool bad = p.shared.bad_groups(p.batch);
+        const int prefix = bad ? -1 : p.shared.of(b);
+        PrefixWork::Of of{};
+        int64_t total = 0, units = 0, before = 0, units_before = 0, first = 0;
+        if (prefix >= 0) {
+            const int64_t n = __ldg(p.shared.lens + prefix);
+            bad = n < 0 || n > p.shared.max_len;
+            of = work.of(prefix);
+            first = __ldg(p.shared.cu + prefix);
+            work.before(p.shared.count, &total, &units);
+            work.before(prefix, &before, &units_before);
+        }
+        if (lane == 0) {
+            s_shared[0] = total, s_shared[1] = before, s_shared[2] = units_before, s_shared[3] = first;
+            s_of = of, s_bad[1] = bad;
+        }
+    }
+    __syncthreads();
+    if (h >= p.q_heads) {
+        griddep_wait();
+        return;
+    }
+    const int in_group = h % group, head = h / group;
+    const int64_t at_row = b * p.q_heads + h;
+    const bool bad = s_bad[0] || s_bad[1];
+    // the prefix's pieces: places piece0 .., their row
+    int pieces = 0, piece_row = 0;
+    int64_t piece0 = 0;
+    const PrefixWork::Of of = s_of;
+    if (of.tiles > 0) {
+        const int64_t total = s_shared[0], blocks = min((int64_t)p.piece_blocks, total);
+        const int seq = (int)(b - s_shared[3]), pair = seq / (2 * work.per_tile);
+        const int in_pair = seq - pair * 2 * work.per_tile, t = in_pair / work.per_tile;
+        piece_row = t * kPrefixKeys + (in_pair - t * work.per_tile) * group + in_group;
+        const int64_t unit = (int64_t)head * of.pairs + pair;
+        const int64_t t0 = s_shared[1] + unit * of.tiles, t1 = t0 + of.tiles;
+        // block c holds tile t: c = floor(((t + 1) C - 1) / T)
+        const int64_t c0 = ((t0 + 1) * blocks - 1) / total, c1 = (t1 * blocks - 1) / total;
+        pieces = (int)(c1 - c0) + 1;
+        piece0 = c0 + s_shared[2] + unit;
+    }
+    // the sums over own keys: a row of own_sums where one block held the segment, else one of each block: in
+    // its slot 1 where it began the segment, 0 where it went on with it
+    const int tiles = L.tiles(b);
+    int own = tiles > 0 ? 1 : 0;
+    bool whole = true;
+    int64_t own0 = 0;
+    const int row = in_group % HEADS;
+    if (tiles > 0 && p.own_split) {
+        const int64_t total = s_own[0], blocks = min(C, total);
+        const int64_t t0 = s_own[1] + (int64_t)(head * qtiles + in_group / HEADS) * tiles, t1 = t0 + tiles;
+        const int64_t c0 = ((t0 + 1) * blocks - 1) / total, c1 = (t1 * blocks - 1) / total;
+        whole = c0 == c1;
+        own = (int)(c1 - c0) + 1;
+        own0 = c0;
+    }
+    const float2* own_pairs = reinterpret_cast<const float2*>(p.own_sums + p.batch * p.q_heads * DIM);
+    auto part_of = [&](int i, const float2** pair) {
+        if (i < pieces) {
+            const float* part = p.pieces + (piece0 + i) * prefix_piece(DIM);
+            *pair = reinterpret_cast<const float2*>(part + (int64_t)kPrefixRows * DIM) + piece_row;
+            return part + piece_row * DIM;
+        }
+        if (whole) {
+            *pair = own_pairs + at_row;
+            return static_cast<const float*>(p.own_sums) + at_row * DIM;
+        }
+        const int64_t n = i - pieces;
+        const float* part = static_cast<const float*>(p.workspace) + (2 * (own0 + n) + (n == 0 ? 1 : 0)) * PART;
+        *pair = reinterpret_cast<const float2*>(part + HEADS * DIM) + row;
+        return part + row * DIM;
+    };
+    griddep_wait();
+    float m = -INFINITY, l = 0.0f, acc[VEC] = {};
+    constexpr int AHEAD = 4;
+    for (int i0 = 0; i0 < pieces + own; i0 += AHEAD) {
+        float2 ms[AHEAD];
+        float x[AHEAD][VEC];
+#pragma unroll
+        for (int n = 0; n < AHEAD; ++n) {
+            ms[n] = make_float2(-INFINITY, 0.0f);
+#pragma unroll
+            for (int v = 0; v < VEC; ++v)
+                x[n][v] = 0.0f;
+            if (i0 + n < pieces + own) {
+                const float2* pair;
+                const float* part = part_of(i0 + n, &pair);
+                ms[n] = __ldcg(pair);
+                if constexpr (VEC == 4) {
+                    const float4 f = __ldcg(reinterpret_cast<const float4*>(part) + lane);
+                    x[n][0] = f.x, x[n][1] = f.y, x[n][2] = f.z, x[n][3] = f.w;
+                } else {
+                    const float2 f = __ldcg(reinterpret_cast<const float2*>(part) + lane);
+                    x[n][0] = f.x, x[n][1] = f.y;
+                }
+            }
+        }
+        float top = m;
+#pragma unroll
+        for (int n = 0; n < AHEAD; ++n)
+            top = fmaxf(top, ms[n].x);
+        const float ref = top == -INFINITY ? 0.0f : top;
+        const float keep = fast_exp2(m - ref);
+        l *= keep;
+#pragma unroll
+        for (int v = 0; v < VEC; ++v)
+            acc[v] *= keep;
+#pragma unroll
+        for (int n = 0; n < AHEAD; ++n) {
+            const float f = fast_exp2(ms[n].x - ref);
+            l += ms[n].y * f;
+#pragma unroll
+            for (int v = 0; v < VEC; ++v)
+                acc[v] += x[n][v] * f;
+        }
+        m = top;
+    }
+    const bool none = pieces + own == 0;
+#pragma unroll
+    for (int v = 0; v < VEC; ++v)
+        acc[v] = bad ? NAN : none ? 0.0f : acc[v] / l;
+    T* out = static_cast<T*>(p.out) + at_row * DIM + lane * VEC;
+    if constexpr (VEC == 4)
+        *reinterpret_cast<uint2*>(out) = make_uint2(E::pack2(acc[0], acc[1]), E::pack2(acc[2], acc[3]));
+    else
+        *reinterpret_cast<uint32_t*>(out) = E::pack2(acc[0], acc[1]);
+    if (lane == 0 && p.lse != nullptr)
+        p.lse[at_row] = bad ? NAN : none ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 constexpr int kMostBlocks = 152 * 3;  // of any device this library runs on
@@ -940,8 +1048,15 @@ cudaError_t launch(PagedAttention p, const DeviceInfo& dev, unsigned int* err, c
     e = launch_pdl(paged_kernel<E, INT8, DIM, NT, MODE>, dim3((unsigned)blocks), dim3(WARPS * 32), S::SMEM, s, p, blocks,
                    split, err);
     p.own_split = split;
-    if (e == cudaSuccess && (split || MODE == kOwnBesidePieces))
-        e = launch_pdl(join_kernel<E, DIM, NT, MODE>, dim3((unsigned)(p.batch * p.q_heads)), dim3(128), 0, s, p, blocks, S::TILE);
+    if constexpr (MODE == kOwnBesidePieces) {
+        if (e == cudaSuccess)
+            e = launch_pdl(join_pieces_kernel<E, DIM, NT>, dim3((unsigned)(p.batch * ((p.q_heads + 7) / 8))), dim3(256), 0, s, p,
+                           blocks, S::TILE);
+    } else {
+        if (e == cudaSuccess && split)
+            e = launch_pdl(join_kernel<E, DIM, NT, MODE>, dim3((unsigned)(p.batch * p.q_heads)), dim3(128), 0, s, p, blocks,
+                           S::TILE);
+    }
     return e;
 }
 
