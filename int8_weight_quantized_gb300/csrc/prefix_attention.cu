@@ -9,11 +9,11 @@
 //
 // The rows of a tile are the query heads of one kv head of floor(128 / group) sequences.  One block per SM;
 // its roles run on from piece to piece:
-//   warp 0      issues the products, one lane: S_t = Q_t K^T, O_t += P_t V, sums in tensor memory, in
+//   warp 0      copies the queries by TMA and issues the products, one lane: S_t = Q_t K^T, O_t += P_t V, sums in tensor memory, in
 //               the order O_0 += P_0 V_j, S_0 = Q_0 K_{j+1}, O_1 += P_1 V_j, S_1 = Q_1 K_{j+1};
-//   warps 1-3   copies: queries, and rows of pages of a multiple of 8, by TMA; rows of other pages, and those
-//               of a prefix's last tile, by 16-byte asynchronous copies into the same swizzled layout; int8
-//               rows through a small ring of raw codes, each thread widening what it copied itself;
+//   warps 1-3   copies: rows of pages of a multiple of 8 by TMA; rows of other pages, and those of a prefix's
+//               last tile, by 16-byte asynchronous copies into the same swizzled layout; int8 rows as raw
+//               codes into their place in the ring, from where they are widened in place;
 //   warps 4-11  softmax, a warpgroup for each query tile, one thread per row, as in attention.cu: the
 //               weights go back over S as the 16-bit operand P of the second product, the row's
 //               reference trails its maximum by up to 2^8.
@@ -57,16 +57,13 @@ template <int DIM, bool INT8>
 struct Cfg {
     static constexpr uint32_t BOX_BYTES = BM * 128;             // 128 rows of 64 values
     static constexpr uint32_t TILE_BYTES = DIM / 64 * BOX_BYTES;  // a Q, K or V tile
-    static constexpr int UNITS = (DIM == 128 ? 5 : 10) - (INT8 ? 1 : 0);  // ring of K_0, V_0, K_1, V_1, ..
-    static constexpr int RAW_ROWS = 64;                         // int8 codes on their way: half a tile
-    static constexpr int RAWS = INT8 ? 3 : 0;
-    static constexpr uint32_t RAW_BYTES = RAW_ROWS * DIM;
-    // Key tiles whose scales are kept: while a softmax warp reads those of tile j, V_j is in the ring, so that K's
-    // of up to UNITS / 2 further tiles are.
-    static constexpr int SCALES = UNITS / 2 + 2;
-    static constexpr size_t SCALE_BYTES = INT8 ? SCALES * BM * 4 + RAWS * RAW_ROWS * 4 : 0;
+    static constexpr int UNITS = DIM == 128 ? 5 : 10;             // ring of K_0, V_0, K_1, V_1, ..
+    // Key tiles whose scales are kept: while a softmax warp reads those of tile j, V_j is in the ring, so that
+    // K's of up to UNITS / 2 further tiles are.
+    static constexpr int SCALES = UNITS / 2 + 1;
+    static constexpr size_t SCALE_BYTES = INT8 ? SCALES * BM * 4 : 0;
     static constexpr size_t STATE = 512;
-    static constexpr size_t SMEM = 1024 + (2 + UNITS) * (size_t)TILE_BYTES + RAWS * RAW_BYTES + SCALE_BYTES + STATE;
+    static constexpr size_t SMEM = 1024 + (2 + UNITS) * (size_t)TILE_BYTES + SCALE_BYTES + STATE;
     static_assert(SMEM <= 232448, "shared memory budget");
 };
 
@@ -146,10 +143,22 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint4 v)
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
-// byte i of four codes with their signs flipped, as the number that it stands for
-__device__ __forceinline__ float code_value(uint32_t flipped, int i)
+// Codes 2 i and 2 i + 1 of four (i = 0, 1) as a pair of 16-bit numbers, exact.  bf16: 128 + (code & 127)
+// minus 128 or, with the sign bit, 256; fp16: the code with its sign flipped in the mantissa of 1024, minus
+// 1152.
+template <class E>
+__device__ __forceinline__ uint32_t code_pair(uint32_t codes, int i)
 {
-    return __uint_as_float(__byte_perm(flipped, 0x4B000000u, 0x7440 | i)) - 8388736.0f;  // 2^23 + 128
+    if constexpr (std::is_same<E, Bf16>::value) {
+        const uint32_t x = __byte_perm(codes, 0x43434343u, i ? 0x4342 : 0x4140);
+        const uint32_t a = x & 0xff7fff7fu, b = x & 0xff80ff80u;
+        const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+        return *reinterpret_cast<const uint32_t*>(&v);
+    } else {
+        const uint32_t x = __byte_perm(codes ^ 0x80808080u, 0x64646464u, i ? 0x4342 : 0x4140);
+        const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&x), __half2half2(__ushort_as_half(0x6480)));
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
 }
 
 template <class E, int DIM, bool INT8>
@@ -164,12 +173,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* s_q = smem;
     uint8_t* s_ring = s_q + 2 * C::TILE_BYTES;
-    uint8_t* s_raw = s_ring + UNITS * C::TILE_BYTES;
-    float* s_kscale = reinterpret_cast<float*>(s_raw + C::RAWS * C::RAW_BYTES);     // [SCALES][BM]
-    float* s_rscale = s_kscale + (INT8 ? C::SCALES * BM : 0);                        // [RAWS][RAW_ROWS]
+    float* s_kscale = reinterpret_cast<float*>(s_ring + UNITS * C::TILE_BYTES);  // int8: [SCALES][BM]
     uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(s_kscale) + C::SCALE_BYTES);
     uint64_t* q_full = bars;             // [2]
-    uint64_t* q_empty = bars + 2;        // [2] the piece's last scores of tile t are computed
+    uint64_t* raw_read = bars + 2;       // int8: the raw codes of a tile are in registers
     uint64_t* s_full = bars + 4;         // [2] S_t is complete (and every product before it)
     uint64_t* p_half = bars + 6;         // [2] P_t is for its first keys, O_t may be added to
     uint64_t* p_full = bars + 8;         // [2] P_t is written
@@ -185,13 +192,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int warp = __shfl_sync(FULL, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (warp == 0 && lane == 0) {
         for (int t = 0; t < 2; ++t) {
-            mbar_init(&q_full[t], LOADERS);
-            mbar_init(&q_empty[t], 1);
+            mbar_init(&q_full[t], 1);
             mbar_init(&s_full[t], 1);
             mbar_init(&p_half[t], 4);
             mbar_init(&p_full[t], 4);
             mbar_init(&o_full[t], 1);
         }
+        mbar_init(raw_read, LOADERS);
         mbar_init(drain, 1);
         for (int s = 0; s < UNITS; ++s) {
             mbar_init(&full[s], LOADERS);
@@ -258,8 +265,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         at.pair = (int)(unit - (int64_t)at.head * at.of.pairs);
     }
     const int per_tile = work.per_tile, group = a.group;
-    // sequences of query tile t of the piece
-    auto seqs = [&](int t) { return max(0, min(per_tile, at.of.seqs - (2 * at.pair + t) * per_tile)); };
+    // sequences of query tile t of a walk's piece
+    auto seqs_of = [&](const Walk& of, int t) { return max(0, min(per_tile, of.of.seqs - (2 * of.pair + t) * per_tile)); };
+    auto seqs = [&](int t) { return seqs_of(at, t); };
     const KvCache& cache = a.p.cache;
 
     if (!any) {
@@ -295,9 +303,26 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int k = from.value / 16; k < keys.value / 16; ++k)
                     mma_ts(tmem + 2 * BM + t * DIM, tmem + t * BM + k * 8, y + k * (16 * 128 >> 4), idesc_o, k > 0 || started);
             };
+            // Q_t of a walk's piece, once the scores from the one before are computed
+            auto load_q = [&](const Walk& of, int t) {
+                if (leader && seqs_of(of, t) > 0) {
+                    mbar_arrive_expect_tx(&q_full[t], (uint32_t)(DIM / 64 * per_tile * group * 128));
+                    for (int x = 0; x < DIM / 64; ++x)
+                        tma_load_3d(s_q + t * C::TILE_BYTES + x * C::BOX_BYTES, &tmQ, &q_full[t], x * 64, of.head * group,
+                                    (int32_t)(of.seq0 + (2 * of.pair + t) * per_tile));
+                }
+                __syncwarp();
+            };
+            uint32_t q_loads[2] = {0, 0};
+            Walk then = at;
+            for (int t = 0; t < 2; ++t) {
+                load_q(at, t);
+                q_loads[t] += seqs(t) > 0 ? 1 : 0;
+            }
             auto piece = [&]() {
                 const int count = __shfl_sync(FULL, at.count(), 0);
                 const int tiles = __shfl_sync(FULL, seqs(1) > 0 ? 2 : 1, 0);
+                then.next(work);
                 int slot = uses % UNITS;
                 if (!wait_all(&full[slot], (uses / UNITS) & 1u))
                     return false;
@@ -306,11 +331,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (!wait_all(&q_full[t], q_uses[t]++ & 1u))
                         return false;
                     tc_fence_after();
-                    if (leader) {
+                    if (leader)
                         scores(t, slot);
-                        if (count == 1)
-                            mma_commit(&q_empty[t]);
-                    }
                     __syncwarp();
                 }
                 if (leader)
@@ -342,15 +364,20 @@ __global__ void __launch_bounds__(THREADS, 1)
                             return false;
                         p_phase[t] ^= 1u;
                         tc_fence_after();
+                        if (!more && then.left > 0) {  // (its weights: so the scores are computed)
+                            load_q(then, t);
+                            q_loads[t] += seqs_of(then, t) > 0 ? 1 : 0;
+                            if (tiles == 1) {
+                                load_q(then, 1);
+                                q_loads[1] += seqs_of(then, 1) > 0 ? 1 : 0;
+                            }
+                        }
                         if (leader) {
                             values(t, v_slot, std::integral_constant<int, FIRST>(), std::integral_constant<int, BM>(), j > 0);
                             if (!more)
                                 mma_commit(&o_full[t]);
-                            if (more) {
+                            if (more)
                                 scores(t, k_slot);
-                                if (j + 2 == count)
-                                    mma_commit(&q_empty[t]);
-                            }
                             if (t + 1 == tiles) {
                                 mma_commit(&empty[v_slot]);
                                 if (more)
@@ -365,8 +392,11 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (; at.left > 0; at.next(work))
                 if (!piece())
                     break;
-            // every product must be complete before tensor and shared memory are released
+            // every copy and product must be complete before tensor and shared memory are released
             if (leader) {
+                for (int t = 0; t < 2; ++t)
+                    if (q_loads[t] > 0)
+                        wait_out(&q_full[t], (q_loads[t] - 1) & 1u, err, kErrWaitPrefix, TIMEOUT_NS);
                 mma_commit(drain);
                 wait_out(drain, 0, err, kErrWaitPrefix, TIMEOUT_NS);
             }
@@ -374,69 +404,16 @@ __global__ void __launch_bounds__(THREADS, 1)
         } else {
             // ---------------------------------------------------------------- copies
             const int w = warp - 1;
-            // groups of copies in flight, and the barriers that wait for them (the oldest first)
-            constexpr int FLIGHT = 2;
-            uint64_t* pending[FLIGHT + 1] = {};
-            int in_flight = 0;
+            uint32_t uses = 0;
+            // byte address of 16-byte chunk c of row r of a tile
+            auto chunk_at = [&](int r, int c) {
+                return (uint32_t)((c >> 3) * C::BOX_BYTES + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+            };
             auto landed = [&](uint64_t* bar) {
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(bar);
-            };
-            auto all_landed = [&]() {
-                cp_async_wait<0>();
-#pragma unroll
-                for (int i = 0; i < FLIGHT; ++i)
-                    if (i < in_flight)
-                        landed(pending[i]);
-                in_flight = 0;
-            };
-            auto sent = [&](uint64_t* bar) {
-                cp_async_commit();
-#pragma unroll
-                for (int i = 0; i <= FLIGHT; ++i)
-                    pending[i] = i == in_flight ? bar : pending[i];
-                if (++in_flight > FLIGHT) {
-                    cp_async_wait<FLIGHT>();
-                    landed(pending[0]);
-#pragma unroll
-                    for (int i = 0; i < FLIGHT; ++i)
-                        pending[i] = pending[i + 1];
-                    --in_flight;
-                }
-            };
-            // (what has been sent must not wait for what is to come)
-            auto wait = [&](uint64_t* bar, uint32_t parity) {
-                if (__all_sync(FULL, mbar_try_wait(bar, parity)))
-                    return true;
-                if (!INT8)
-                    all_landed();
-                return wait_all(bar, parity);
-            };
-            uint32_t uses = 0, q_uses[2] = {0, 0};
-            // byte address of 16-byte chunk c of row r of a tile
-            auto chunk_at = [&](int r, int c) {
-                return (uint32_t)((c >> 3) * C::BOX_BYTES + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-            };
-            // Every warp arrives at each tile's barrier: the first of them, with the bytes that it has asked for, where
-            // a tile comes by TMA.
-            auto load_q = [&](int t) {
-                if (!wait(&q_empty[t], (q_uses[t] + 1) & 1u))
-                    return false;
-                ++q_uses[t];
-                if (lane == 0) {
-                    if (w == 0) {
-                        mbar_arrive_expect_tx(&q_full[t], (uint32_t)(DIM / 64 * per_tile * group * 128));
-                        for (int x = 0; x < DIM / 64; ++x)
-                            tma_load_3d(s_q + t * C::TILE_BYTES + x * C::BOX_BYTES, &tmQ, &q_full[t], x * 64, at.head * group,
-                                        (int32_t)(at.seq0 + (2 * at.pair + t) * per_tile));
-                    } else {
-                        mbar_arrive(&q_full[t]);
-                    }
-                }
-                __syncwarp();
-                return true;
             };
             // the page of key `j` of a walk's prefix, -1 past its end; and the key's row in the cache
             auto page_of = [&](const Walk& of, int j) {
@@ -453,56 +430,87 @@ __global__ void __launch_bounds__(THREADS, 1)
                 return *ok ? ((uint32_t)page * cache.heads + of.head) * cache.page_size + in_page : 0u;
             };
             bool ok = true;
-            if constexpr (!INT8) {
-                // a copy instruction takes RPI rows, the warps by turns; number n of a warp's rows is row
-                // (n / RPI * LOADERS + w) * RPI + n % RPI, and its lane n % 32 looks it up
-                constexpr int CH = DIM / 8, RPI = 32 / CH, TURNS = (BM / RPI + LOADERS - 1) / LOADERS;
-                static_assert(TURNS * RPI <= 64, "two rows a lane");
-                uint32_t rows[2] = {}, oks[2] = {}, bads[2] = {};
-                // pages are asked for a tile ahead
-                Walk ahead = at;
-                int ahead_tile = 0;  // of the piece
-                int pages[2] = {};
-                auto row_in_tile = [&](int h) {
-                    const int n = 32 * h + lane, r = (n / RPI * LOADERS + w) * RPI + n % RPI;
-                    return n < TURNS * RPI && r < BM ? r : -1;
-                };
-                auto by_tma = [&](const Walk& of, int tile) { return a.box > 0 && of.of.keys - tile * BM >= BM; };
-                int box_page = 0, box_asked = 0;
-                auto ask = [&]() {
-                    if (ahead.left <= 0)
-                        return;
-                    const int tile = ahead.tile + ahead_tile;
-                    if (by_tma(ahead, tile)) {
-                        box_asked = page_of(ahead, tile * BM + lane % (BM / a.box) * a.box);
-                        return;
-                    }
+            // A copy instruction takes RPI rows, the warps by turns; number n of a warp's rows is row
+            // (n / RPI * LOADERS + w) * RPI + n % RPI, and its lane n % 32 looks it up, pages a tile ahead.
+            constexpr int CH = DIM * (INT8 ? 1 : 2) / 16, RPI = 32 / CH, TURNS = (BM / RPI + LOADERS - 1) / LOADERS;
+            static_assert(TURNS * RPI <= 64, "two rows a lane");
+            uint32_t rows[2] = {}, oks[2] = {}, bads[2] = {};
+            Walk ahead = at;
+            int ahead_tile = 0;  // of the piece
+            int pages[2] = {}, box_page = 0, box_asked = 0;
+            auto row_in_tile = [&](int h) {
+                const int n = 32 * h + lane, r = (n / RPI * LOADERS + w) * RPI + n % RPI;
+                return n < TURNS * RPI && r < BM ? r : -1;
+            };
+            auto by_tma = [&](const Walk& of, int tile) { return !INT8 && a.box > 0 && of.of.keys - tile * BM >= BM; };
+            auto ask = [&]() {
+                if (ahead.left <= 0)
+                    return;
+                const int tile = ahead.tile + ahead_tile;
+                if (by_tma(ahead, tile)) {
+                    box_asked = page_of(ahead, tile * BM + lane % (BM / a.box) * a.box);
+                    return;
+                }
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
+                for (int h = 0; h < 2; ++h)
+                    if (row_in_tile(h) >= 0)
+                        pages[h] = page_of(ahead, tile * BM + row_in_tile(h));
+            };
+            auto look_up = [&](int tile) {
+                box_page = box_asked;
+                if (!by_tma(at, tile)) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        bool there = false, bad = false;
+                        rows[h] = 0;
                         if (row_in_tile(h) >= 0)
-                            pages[h] = page_of(ahead, tile * BM + row_in_tile(h));
-                };
-                auto look_up = [&](int tile) {
-                    box_page = box_asked;
-                    if (!by_tma(at, tile)) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            bool ok = false, bad = false;
-                            rows[h] = 0;
-                            if (row_in_tile(h) >= 0)
-                                rows[h] = row_of(at, tile * BM + row_in_tile(h), pages[h], &ok, &bad);
-                            oks[h] = __ballot_sync(FULL, ok), bads[h] = __ballot_sync(FULL, bad);
-                        }
-                        if ((bads[0] | bads[1]) && lane == 0)
-                            atomicOr(err, kErrIndex);
+                            rows[h] = row_of(at, tile * BM + row_in_tile(h), pages[h], &there, &bad);
+                        oks[h] = __ballot_sync(FULL, there), bads[h] = __ballot_sync(FULL, bad);
                     }
-                    if (++ahead_tile == ahead.count()) {
-                        ahead_tile = 0;
-                        ahead.next(work);
-                    }
-                    ask();
-                };
+                    if ((bads[0] | bads[1]) && lane == 0)
+                        atomicOr(err, kErrIndex);
+                }
+                if (++ahead_tile == ahead.count()) {
+                    ahead_tile = 0;
+                    ahead.next(work);
+                }
                 ask();
+            };
+            ask();
+            if constexpr (!INT8) {
+                // groups of copies in flight, and the barriers that wait for them (the oldest first)
+                constexpr int FLIGHT = 2;
+                uint64_t* pending[FLIGHT + 1] = {};
+                int in_flight = 0;
+                auto all_landed = [&]() {
+                    cp_async_wait<0>();
+#pragma unroll
+                    for (int i = 0; i < FLIGHT; ++i)
+                        if (i < in_flight)
+                            landed(pending[i]);
+                    in_flight = 0;
+                };
+                auto sent = [&](uint64_t* bar) {
+                    cp_async_commit();
+#pragma unroll
+                    for (int i = 0; i <= FLIGHT; ++i)
+                        pending[i] = i == in_flight ? bar : pending[i];
+                    if (++in_flight > FLIGHT) {
+                        cp_async_wait<FLIGHT>();
+                        landed(pending[0]);
+#pragma unroll
+                        for (int i = 0; i < FLIGHT; ++i)
+                            pending[i] = pending[i + 1];
+                        --in_flight;
+                    }
+                };
+                // (what has been sent must not wait for what is to come)
+                auto wait = [&](uint64_t* bar, uint32_t parity) {
+                    if (__all_sync(FULL, mbar_try_wait(bar, parity)))
+                        return true;
+                    all_landed();
+                    return wait_all(bar, parity);
+                };
                 // A tile whose keys are all there comes by TMA, a lane of the first warp for each box of rows of one page
                 // and 64 values; one on a page out of range gets NaN for K and zeros for V.
                 const int box = a.box, boxes = box > 0 ? BM / box * (DIM / 64) : 0;
@@ -569,142 +577,120 @@ __global__ void __launch_bounds__(THREADS, 1)
                 };
                 for (; ok && at.left > 0; at.next(work)) {
                     const int count = at.count();
-                    ok = load_q(0);
-                    look_up(at.tile);
-                    ok = ok && load_unit(true, at.tile);
-                    if (ok && seqs(1) > 0)
-                        ok = load_q(1);
                     for (int j = 0; ok && j < count; ++j) {
-                        ok = load_unit(false, at.tile + j);
-                        if (ok && j + 1 < count) {
-                            look_up(at.tile + j + 1);
-                            ok = load_unit(true, at.tile + j + 1);
-                        }
+                        look_up(at.tile + j);
+                        ok = load_unit(true, at.tile + j) && load_unit(false, at.tile + j);
                     }
                 }
                 all_landed();
             } else {
-                // half tiles of raw codes through a ring, each widened by the thread that copied it
-                constexpr int CH = DIM / 16, RPI = 32 / CH, ROWS = C::RAW_ROWS;
-                constexpr int TURNS = (ROWS / RPI + LOADERS - 1) / LOADERS;
-                static_assert(TURNS * RPI <= 32, "a row a lane");
-                // copies run ahead of the widening by up to RAWS - 1 halves, over the pieces' ends too
-                Walk ahead = at;
-                int ahead_half = 0;  // of the piece: 4 j + (0, 1: K; 2, 3: V)
-                uint32_t copies = 0, widened = 0, k_tiles_ahead = 0;
-                uint32_t bads[C::RAWS] = {};
+                // The raw codes of a tile land in the first half of its own place in the ring, their scales behind
+                // them; from there they go through registers, each thread's own copies, when all warps have
+                // read theirs.
+                constexpr uint32_t SCALES_AT = BM * DIM;
+                const uint32_t units = 2 * (uint32_t)at.left;  // K, V, K, V, ..
+                uint32_t copies = 0, widened = 0;
+                int j = 0;  // tile of the piece that the next copies are of
                 auto copy = [&]() {
-                    if (ahead.left > 0) {
-                        const int raw = copies % C::RAWS;
-                        const bool is_k = (ahead_half & 2) == 0;
-                        const int first = (ahead.tile + ahead_half / 4) * BM + (ahead_half & 1) * ROWS;
-                        const int n = lane, r = (n / RPI * LOADERS + w) * RPI + n % RPI;
-                        bool ok = false, bad = false;
-                        uint32_t row = 0;
-                        if (n < TURNS * RPI && r < ROWS)
-                            row = row_of(ahead, first + r, page_of(ahead, first + r), &ok, &bad);
-                        const uint32_t oks = __ballot_sync(FULL, ok), bad_rows = __ballot_sync(FULL, bad);
-#pragma unroll
-                        for (int i = 0; i < C::RAWS; ++i)
-                            bads[i] = i == raw ? bad_rows : bads[i];
-                        if (bad_rows && lane == 0)
-                            atomicOr(err, kErrIndex);
-                        const uint8_t* base = static_cast<const uint8_t*>(is_k ? cache.k : cache.v) + lane % CH * 16;
-                        const float* scales = is_k ? cache.k_scale : cache.v_scale;
-                        const uint32_t dst = smem_u32(s_raw) + raw * C::RAW_BYTES;
-#pragma unroll
-                        for (int i = 0; i < TURNS; ++i) {
-                            const int rr = (i * LOADERS + w) * RPI + lane / CH, nn = i * RPI + lane / CH;
-                            const uint32_t from = __shfl_sync(FULL, row, nn);
-                            if (rr < ROWS)
-                                cp_async16(dst + rr * DIM + lane % CH * 16, base + (uint64_t)from * DIM, (oks >> nn) & 1u);
-                        }
-                        if (n < TURNS * RPI && r < ROWS)
-                            cp_async_small<4>(smem_u32(s_rscale + raw * ROWS + r), scales + row, ok);
-                        ++copies;
-                        ahead_half++;
-                        if (ahead_half == 4 * ahead.count()) {
-                            ahead_half = 0;
-                            ahead.next(work);
-                        }
-                    }
-                    cp_async_commit();
-                };
-                // the next half, into rows half * ROWS .. of the tile at dst
-                auto widen = [&](uint32_t dst, int half, bool is_k, float* kscale) {
-                    cp_async_wait<C::RAWS - 2>();
-                    __syncwarp();  // scales come from other lanes' copies
-                    const int raw = widened % C::RAWS;
-                    uint32_t bad_rows = 0;
-#pragma unroll
-                    for (int i = 0; i < C::RAWS; ++i)
-                        bad_rows = i == raw ? bads[i] : bad_rows;
-                    ++widened;
-#pragma unroll 1
+                    const bool is_k = (copies & 1u) == 0;
+                    if (is_k)
+                        look_up(at.tile + j);
+                    const uint32_t dst = smem_u32(s_ring) + copies % UNITS * C::TILE_BYTES;
+                    const uint8_t* base = static_cast<const uint8_t*>(is_k ? cache.k : cache.v) + lane % CH * 16;
+#pragma unroll 2
                     for (int i = 0; i < TURNS; ++i) {
-                        const int r = (i * LOADERS + w) * RPI + lane / CH, c = lane % CH;
-                        if (r >= ROWS)
-                            break;
-                        const bool bad = (bad_rows >> (i * RPI + lane / CH)) & 1u;
-                        const uint4 codes = lds128(smem_u32(s_raw) + raw * C::RAW_BYTES + r * DIM + c * 16);
-                        const float scale = s_rscale[raw * ROWS + r];
-                        const uint32_t word[4] = {codes.x ^ 0x80808080u, codes.y ^ 0x80808080u, codes.z ^ 0x80808080u,
-                                                  codes.w ^ 0x80808080u};
-                        uint32_t out[8];
-                        const float f = is_k ? 1.0f : scale;
+                        const int r = (i * LOADERS + w) * RPI + lane / CH, n = i * RPI + lane / CH, h = i * RPI / 32;
+                        const uint32_t row = __shfl_sync(FULL, h ? rows[1] : rows[0], n % 32);
+                        if (r < BM)
+                            cp_async16(dst + r * DIM + lane % CH * 16, base + (uint64_t)row * DIM,
+                                       ((h ? oks[1] : oks[0]) >> (n % 32)) & 1u);
+                    }
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            out[k] = E::pack2(code_value(word[k / 2], 2 * (k & 1)) * f, code_value(word[k / 2], 2 * (k & 1) + 1) * f);
-                        const int row = half * ROWS + r;
-                        sts128(dst + chunk_at(row, 2 * c), make_uint4(out[0], out[1], out[2], out[3]));
-                        sts128(dst + chunk_at(row, 2 * c + 1), make_uint4(out[4], out[5], out[6], out[7]));
-                        if (is_k && c == 0)
-                            kscale[row] = bad ? NAN : scale;
+                    for (int h = 0; h < 2; ++h)
+                        if (row_in_tile(h) >= 0) {
+                            const uint32_t to = dst + SCALES_AT + row_in_tile(h) * 4;
+                            if ((bads[h] >> lane) & 1u)  // on a page out of range: NaN
+                                asm volatile("st.shared.u32 [%0], %1;" ::"r"(to), "r"(0x7fffffffu) : "memory");
+                            else
+                                cp_async_small<4>(to, (is_k ? cache.k_scale : cache.v_scale) + rows[h], (oks[h] >> lane) & 1u);
+                        }
+                    cp_async_commit();
+                    ++copies;
+                    if (!is_k && ++j == at.count()) {
+                        j = 0;
+                        at.next(work);
+                    }
+                };
+                auto widen = [&]() {
+                    const bool is_k = (widened & 1u) == 0;
+                    const int slot = widened % UNITS;
+                    switch (copies - widened - 1) {  // copies under way that came after this one's
+                    case 0: cp_async_wait<0>(); break;
+                    case 1: cp_async_wait<1>(); break;
+                    case 2: cp_async_wait<2>(); break;
+                    default: cp_async_wait<3>(); break;
+                    }
+                    __syncwarp();  // scales come from other lanes' copies
+                    const uint32_t dst = smem_u32(s_ring) + slot * C::TILE_BYTES;
+                    float* kscale = s_kscale + (widened / 2) % C::SCALES * BM;
+                    uint4 codes[TURNS];
+                    float scales[TURNS];
+#pragma unroll
+                    for (int i = 0; i < TURNS; ++i) {
+                        const int r = min((i * LOADERS + w) * RPI + lane / CH, BM - 1);
+                        codes[i] = lds128(dst + r * DIM + lane % CH * 16);
+                        scales[i] = __uint_as_float(lds32(dst + SCALES_AT + r * 4));
                     }
                     __syncwarp();
-                    copy();
-                };
-                auto load_unit = [&](bool is_k) {
-                    const int slot = uses % UNITS;
-                    if (!wait(&empty[slot], (uses / UNITS + 1) & 1u))
+                    if (lane == 0)
+                        mbar_arrive(raw_read);
+                    if (!wait_all(raw_read, widened & 1u))
                         return false;
-                    ++uses;
-                    const uint32_t dst = smem_u32(s_ring) + slot * C::TILE_BYTES;
-                    float* kscale = s_kscale + k_tiles_ahead % C::SCALES * BM;
-                    k_tiles_ahead += is_k ? 1 : 0;
-                    widen(dst, 0, is_k, kscale);
-                    widen(dst, 1, is_k, kscale);
+#pragma unroll
+                    for (int i = 0; i < TURNS; ++i) {
+                        const int r = (i * LOADERS + w) * RPI + lane / CH, c = lane % CH;
+                        const uint32_t word[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+                        uint32_t out[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            out[k] = code_pair<E>(word[k / 2], k & 1);
+                            if (!is_k) {
+                                const float2 v = f2_mul_rn(E::to2(out[k]), make_float2(scales[i], scales[i]));
+                                out[k] = E::pack2(v.x, v.y);
+                            }
+                        }
+                        if (r < BM) {
+                            sts128(dst + chunk_at(r, 2 * c), make_uint4(out[0], out[1], out[2], out[3]));
+                            sts128(dst + chunk_at(r, 2 * c + 1), make_uint4(out[4], out[5], out[6], out[7]));
+                            if (is_k && c == 0)
+                                kscale[r] = scales[i];
+                        }
+                    }
                     landed(&full[slot]);
+                    ++widened;
                     return true;
                 };
-                ok = load_q(0);
-                bool first_q = true;
-#pragma unroll
-                for (int i = 0; i < C::RAWS - 1; ++i)
-                    copy();
-                for (; ok && at.left > 0; at.next(work)) {
-                    const int count = at.count();
-                    if (!first_q)
-                        ok = load_q(0);
-                    first_q = false;
-                    ok = ok && load_unit(true);
-                    if (ok && seqs(1) > 0)
-                        ok = load_q(1);
-                    for (int j = 0; ok && j < count; ++j) {
-                        ok = load_unit(false);
-                        if (ok && j + 1 < count)
-                            ok = load_unit(true);
+                while (ok && widened < units) {
+                    // copies as far ahead as there is room
+                    while (ok && copies < units && copies - widened < (uint32_t)min(UNITS, 4)) {
+                        uint64_t* bar = &empty[copies % UNITS];
+                        const uint32_t parity = (copies / UNITS + 1) & 1u;
+                        if (!__all_sync(FULL, mbar_test_wait(bar, parity))) {
+                            if (copies > widened)
+                                break;
+                            ok = wait_all(bar, parity);
+                            if (!ok)
+                                break;
+                        }
+                        copy();
                     }
+                    ok = ok && widen();
                 }
                 cp_async_wait<0>();
             }
-            if (!ok && w == 0 && lane == 0) {  // aborting: every issued copy lands before shared memory is released
-                for (int t = 0; t < 2; ++t)
-                    if (q_uses[t] > 0)
-                        wait_out(&q_full[t], (q_uses[t] - 1) & 1u, err, kErrWaitPrefix, TIMEOUT_NS);
-                for (uint32_t i = INT8 ? uses : uses > UNITS ? uses - UNITS : 0; i < uses; ++i)
+            if (!INT8 && !ok && w == 0 && lane == 0)  // aborting: every issued copy lands before shared memory is released
+                for (uint32_t i = uses > UNITS ? uses - UNITS : 0; i < uses; ++i)
                     wait_out(&full[i % UNITS], (i / UNITS) & 1u, err, kErrWaitPrefix, TIMEOUT_NS);
-            }
             __syncwarp();
         }
     } else {
