@@ -161,6 +161,35 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t codes, int i)
     }
 }
 
+// Pairs of codes times a scale, rounded once.  bf16: the scale as the sum of two, code * low added to the exact
+// product with high (2^-17 of a unit off at most); fp16, which such a low part may leave: in fp32.
+template <class E>
+struct Scaled {
+    float scale;
+    __device__ __forceinline__ Scaled(float s) : scale(s) {}
+    __device__ __forceinline__ uint32_t operator()(uint32_t pair) const
+    {
+        const float2 v = f2_mul_rn(E::to2(pair), make_float2(scale, scale));
+        return E::pack2(v.x, v.y);
+    }
+};
+template <>
+struct Scaled<Bf16> {
+    __nv_bfloat162 high, low;
+    __device__ __forceinline__ Scaled(float s)
+    {
+        const __nv_bfloat16 h = __float2bfloat16_rn(s);
+        high = __bfloat162bfloat162(h);
+        low = __bfloat162bfloat162(__float2bfloat16_rn(s - __bfloat162float(h)));
+    }
+    __device__ __forceinline__ uint32_t operator()(uint32_t pair) const
+    {
+        const __nv_bfloat162 c = *reinterpret_cast<const __nv_bfloat162*>(&pair);
+        const __nv_bfloat162 v = __hfma2(c, high, __hmul2_rn(c, low));
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+};
+
 template <class E, int DIM, bool INT8>
 __global__ void __launch_bounds__(THREADS, 1)
     prefix_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -176,18 +205,17 @@ __global__ void __launch_bounds__(THREADS, 1)
     float* s_kscale = reinterpret_cast<float*>(s_ring + UNITS * C::TILE_BYTES);  // int8: [SCALES][BM]
     uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(s_kscale) + C::SCALE_BYTES);
     uint64_t* q_full = bars;             // [2]
-    uint64_t* raw_read = bars + 2;       // int8: the raw codes of a tile are in registers
-    uint64_t* s_full = bars + 4;         // [2] S_t is complete (and every product before it)
-    uint64_t* p_half = bars + 6;         // [2] P_t is for its first keys, O_t may be added to
-    uint64_t* p_full = bars + 8;         // [2] P_t is written
-    uint64_t* o_full = bars + 10;        // [2] O_t is final
-    uint64_t* drain = bars + 12;
-    uint64_t* full = bars + 13;          // [UNITS]
+    uint64_t* s_full = bars + 2;         // [2] S_t is complete (and every product before it)
+    uint64_t* p_half = bars + 4;         // [2] P_t is for its first keys, O_t may be added to
+    uint64_t* p_full = bars + 6;         // [2] P_t is written
+    uint64_t* o_full = bars + 8;         // [2] O_t is final
+    uint64_t* drain = bars + 10;
+    uint64_t* full = bars + 11;          // [UNITS]
     uint64_t* empty = full + UNITS;      // [UNITS]
     int64_t* s_start = reinterpret_cast<int64_t*>(empty + UNITS);  // where the block begins
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_start + 5);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    static_assert((13 + 2 * UNITS + 5) * 8 + 8 <= C::STATE, "barriers");
+    static_assert((11 + 2 * UNITS + 5) * 8 + 8 <= C::STATE, "barriers");
 
     const int warp = __shfl_sync(FULL, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (warp == 0 && lane == 0) {
@@ -198,7 +226,6 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(&p_full[t], 4);
             mbar_init(&o_full[t], 1);
         }
-        mbar_init(raw_read, LOADERS);
         mbar_init(drain, 1);
         for (int s = 0; s < UNITS; ++s) {
             mbar_init(&full[s], LOADERS);
@@ -222,10 +249,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     const PrefixWork& work = a.work;
     if (warp == 1) {
         // this block's range of tiles
-        const bool bad = work.shared.bad_groups(a.p.batch);
-        int64_t total = 0, units = 0, t_before = 0, u_before = 0, prefix = 0, t0 = 0, left = 0;
+        int64_t total = 0, t_before = 0, u_before = 0, prefix = 0, t0 = 0, left = 0;
+        const bool bad = work.survey(a.p.batch, &total);
         if (!bad) {
-            work.before(work.shared.count, &total, &units);
             const int64_t blocks = min((int64_t)gridDim.x, total);
             if (blockIdx.x < blocks) {
                 t0 = blockIdx.x * total / blocks;
@@ -584,11 +610,17 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 all_landed();
             } else {
-                // The raw codes of a tile land in the first half of its own place in the ring, their scales behind
-                // them; from there they go through registers, each thread's own copies, when all warps have
-                // read theirs.
-                constexpr uint32_t SCALES_AT = BM * DIM;
+                // The raw codes of a row land where its own last values will be (the second box's row, or with heads of
+                // 64 the first half of its row), its scale where its first ones will: so a row is widened in
+                // place, by the lanes that copied it.
+                constexpr uint32_t RAW_AT = DIM == 128 ? C::BOX_BYTES : 0, SCALE_AT = DIM == 128 ? 0 : 64;
                 const uint32_t units = 2 * (uint32_t)at.left;  // K, V, K, V, ..
+                // Lanes of 8 rows' halves at once: chunk c of a row is lane's bits 0, 1 (and 3 with heads of 128), its row among
+                // the instruction's the others, and raw chunks of odd rows lie the other half first: reads and writes
+                // of 8 lanes spread over all banks.
+                auto raw_chunk = [](int r, int c) { return CH == 8 ? c ^ ((r & 1) << 2) : c; };
+                const int my_chunk = CH == 8 ? (lane & 3) | ((lane >> 1) & 4) : lane & 3;
+                const int my_sub = CH == 8 ? ((lane >> 2) & 1) | ((lane >> 3) & 2) : lane >> 2;
                 uint32_t copies = 0, widened = 0;
                 int j = 0;  // tile of the piece that the next copies are of
                 auto copy = [&]() {
@@ -602,13 +634,13 @@ __global__ void __launch_bounds__(THREADS, 1)
                         const int r = (i * LOADERS + w) * RPI + lane / CH, n = i * RPI + lane / CH, h = i * RPI / 32;
                         const uint32_t row = __shfl_sync(FULL, h ? rows[1] : rows[0], n % 32);
                         if (r < BM)
-                            cp_async16(dst + r * DIM + lane % CH * 16, base + (uint64_t)row * DIM,
+                            cp_async16(dst + RAW_AT + r * 128 + raw_chunk(r, lane % CH) * 16, base + (uint64_t)row * DIM,
                                        ((h ? oks[1] : oks[0]) >> (n % 32)) & 1u);
                     }
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
                         if (row_in_tile(h) >= 0) {
-                            const uint32_t to = dst + SCALES_AT + row_in_tile(h) * 4;
+                            const uint32_t to = dst + SCALE_AT + row_in_tile(h) * 128;
                             if ((bads[h] >> lane) & 1u)  // on a page out of range: NaN
                                 asm volatile("st.shared.u32 [%0], %1;" ::"r"(to), "r"(0x7fffffffu) : "memory");
                             else
@@ -630,45 +662,45 @@ __global__ void __launch_bounds__(THREADS, 1)
                     case 2: cp_async_wait<2>(); break;
                     default: cp_async_wait<3>(); break;
                     }
-                    __syncwarp();  // scales come from other lanes' copies
+                    __syncwarp();  // codes and scales come from other lanes' copies too
                     const uint32_t dst = smem_u32(s_ring) + slot * C::TILE_BYTES;
                     float* kscale = s_kscale + (widened / 2) % C::SCALES * BM;
-                    uint4 codes[TURNS];
-                    float scales[TURNS];
+                    constexpr int BATCH = 4;
 #pragma unroll
-                    for (int i = 0; i < TURNS; ++i) {
-                        const int r = min((i * LOADERS + w) * RPI + lane / CH, BM - 1);
-                        codes[i] = lds128(dst + r * DIM + lane % CH * 16);
-                        scales[i] = __uint_as_float(lds32(dst + SCALES_AT + r * 4));
-                    }
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(raw_read);
-                    if (!wait_all(raw_read, widened & 1u))
-                        return false;
+                    for (int i0 = 0; i0 < TURNS; i0 += BATCH) {
+                        uint4 codes[BATCH];
+                        float scale[BATCH];
 #pragma unroll
-                    for (int i = 0; i < TURNS; ++i) {
-                        const int r = (i * LOADERS + w) * RPI + lane / CH, c = lane % CH;
-                        const uint32_t word[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
-                        uint32_t out[8];
+                        for (int i = i0; i < i0 + BATCH && i < TURNS; ++i) {
+                            const int r = min((i * LOADERS + w) * RPI + my_sub, BM - 1);
+                            codes[i - i0] = lds128(dst + RAW_AT + r * 128 + raw_chunk(r, my_chunk) * 16);
+                            scale[i - i0] = __uint_as_float(lds32(dst + SCALE_AT + r * 128));
+                        }
+                        __syncwarp();
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            out[k] = code_pair<E>(word[k / 2], k & 1);
-                            if (!is_k) {
-                                const float2 v = f2_mul_rn(E::to2(out[k]), make_float2(scales[i], scales[i]));
-                                out[k] = E::pack2(v.x, v.y);
+                        for (int i = i0; i < i0 + BATCH && i < TURNS; ++i) {
+                            const int r = (i * LOADERS + w) * RPI + my_sub;
+                            const uint4 q = codes[i - i0];
+                            const uint32_t word[4] = {q.x, q.y, q.z, q.w};
+                            uint32_t out[8];
+                            const Scaled<E> by(scale[i - i0]);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                out[k] = code_pair<E>(word[k / 2], k & 1);
+                                if (!is_k)
+                                    out[k] = by(out[k]);
+                            }
+                            if (r < BM) {
+                                sts128(dst + chunk_at(r, 2 * my_chunk), make_uint4(out[0], out[1], out[2], out[3]));
+                                sts128(dst + chunk_at(r, 2 * my_chunk + 1), make_uint4(out[4], out[5], out[6], out[7]));
+                                if (is_k && my_chunk == 0)
+                                    kscale[r] = scale[i - i0];
                             }
                         }
-                        if (r < BM) {
-                            sts128(dst + chunk_at(r, 2 * c), make_uint4(out[0], out[1], out[2], out[3]));
-                            sts128(dst + chunk_at(r, 2 * c + 1), make_uint4(out[4], out[5], out[6], out[7]));
-                            if (is_k && c == 0)
-                                kscale[r] = scales[i];
-                        }
+                        __syncwarp();
                     }
                     landed(&full[slot]);
                     ++widened;
-                    return true;
                 };
                 while (ok && widened < units) {
                     // copies as far ahead as there is room
@@ -684,7 +716,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
                         copy();
                     }
-                    ok = ok && widen();
+                    if (ok)
+                        widen();
                 }
                 cp_async_wait<0>();
             }
@@ -704,21 +737,30 @@ __global__ void __launch_bounds__(THREADS, 1)
         const float c = a.c;
         uint32_t phase = 0, o_phase = 0, k_tiles = 0;
         bool ok = true;  // once a wait has given up, the remaining rows become NaN
-        for (; at.left > 0; at.next(work)) {
-            const int count = at.count();
+        // The first time round the steps below run without a tile, for the instruction cache's sake, while
+        // the first tile is on its way: what they find is let go.  (Its first pass over a tile took 5 us, the
+        // next 0.7.)
+        bool dry = true;
+        for (; at.left > 0;) {
+            const int count = dry ? 1 : at.count();
             const int rows = seqs(t) * group;
             if (rows == 0) {
-                k_tiles += count;
+                k_tiles += dry ? 0 : count;
+                if (!dry)
+                    at.next(work);
+                dry = false;
                 continue;
             }
             float m = -INFINITY;  // what the row's sums are relative to, in units of scores
             float l = 0.0f;
-            for (int j = 0; ok && j < count; ++j, ++k_tiles) {
-                ok = mbar_wait(&s_full[t], phase, abort_flag, err, kErrWaitPrefix, TIMEOUT_NS);
-                ok = __all_sync(FULL, ok);
-                if (!ok)
-                    break;
-                phase ^= 1u;
+            for (int j = 0; ok && j < count; ++j, k_tiles += dry ? 0 : 1) {
+                if (!dry) {
+                    ok = mbar_wait(&s_full[t], phase, abort_flag, err, kErrWaitPrefix, TIMEOUT_NS);
+                    ok = __all_sync(FULL, ok);
+                    if (!ok)
+                        break;
+                    phase ^= 1u;
+                }
                 tc_fence_after();
                 const int keys = at.of.keys - (at.tile + j) * BM;  // of this tile and after it
                 uint32_t sr[4][32];
@@ -799,16 +841,17 @@ __global__ void __launch_bounds__(THREADS, 1)
                             sum = f2_add_rn(sum, x);
                             packed[i - from.value][n] = E::pack2(x.x, x.y);
                         }
+                    // (a dry pass leaves its weights where nothing is yet: O)
 #pragma unroll
                     for (int i = from.value; i < to.value; ++i)
-                        tmem_st_32x32b_x16(s_addr + 16 * i, packed[i - from.value]);
+                        tmem_st_32x32b_x16((dry ? o_addr : s_addr) + 16 * i, packed[i - from.value]);
                 };
                 if constexpr (FIRST > 0) {
                     part(std::integral_constant<int, 0>(), std::integral_constant<int, FIRST>());
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0)
+                    if (lane == 0 && !dry)
                         mbar_arrive(&p_half[t]);
                 }
                 part(std::integral_constant<int, FIRST>(), std::integral_constant<int, 4>());
@@ -816,9 +859,13 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0)
+                if (lane == 0 && !dry)
                     mbar_arrive(&p_full[t]);
                 __syncwarp();
+            }
+            if (dry) {
+                dry = false;
+                continue;
             }
             // ---- the piece
             if (ok) {
@@ -843,6 +890,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             // O is read: the piece's last hand-over of P was before that, so the next one's first, which lets O be
             // written again, says so too
             tc_fence_before();
+            at.next(work);
         }
     }
     tc_fence_before();

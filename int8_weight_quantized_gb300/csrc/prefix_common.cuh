@@ -53,6 +53,23 @@ struct PrefixWork {
         }
         *tiles = t, *units_ = u;
     }
+    // by a whole warp: key tiles of all prefixes; true: the groups' bounds descend or leave 0 .. batch
+    __device__ __forceinline__ bool survey(int64_t batch, int64_t* tiles) const
+    {
+        int64_t t = 0;
+        bool bad = false;
+        for (int64_t i = threadIdx.x & 31; i < shared.count; i += 32) {
+            const int64_t lo = __ldg(shared.cu + i), hi = __ldg(shared.cu + i + 1);
+            bad |= lo < 0 || hi < lo || hi > batch;
+            const Of w = of(i);
+            t += units(w) * w.tiles;
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1)
+            t += __shfl_xor_sync(0xffffffffu, t, o);
+        *tiles = t;
+        return __any_sync(0xffffffffu, bad);
+    }
     // by a whole warp: the prefix that holds key tile `t` of all, and the tiles and units before it
     __device__ __forceinline__ int64_t holds(int64_t t, int64_t* tiles, int64_t* units_) const
     {
