@@ -1109,10 +1109,18 @@ constexpr size_t align256(size_t n)
     return (n + 255) / 256 * 256;
 }
 
-// Whether the shared part is computed for whole groups: where there are rows enough to a prefix.
-bool in_pieces(int64_t batch, int group, int64_t prefixes, int64_t max_prefix_len)
+// Whether the shared part is computed for whole groups, three launches, or each sequence walks its prefix's
+// keys and its own, two: by how many values of keys the latter reads at most (the tables say).  Measured (GB300,
+// heads of 128, 32 on 8, 64 own tokens; groups, each for itself): 4 sequences behind 512 tokens (16 heads on 4 of
+// 64, 0.5 M values) 14.2 us, 11.0; 16 behind 1024 (17 M) 15.3, 19.4; 4 behind 8192 (34 M) 25.3, 26.0; 16
+// behind 4096 (67 M) 21.3, 38.2; 64 behind 1024 (67 M) 23.1, 49.4; 256 behind 512 52, 165; 4 each behind 16
+// prefixes of 256 to 4096 tokens 56, 86.
+constexpr int64_t kSharedValues = 12 << 20;
+bool in_pieces(int64_t batch, int group, int kv_heads, int dim, int64_t prefixes, int64_t max_prefix_len)
 {
-    return group <= 128 && batch * group >= 16 * prefixes && max_prefix_len >= 256;
+    // (by division: the product could overflow)
+    return group <= kPrefixKeys && batch >= 2 * prefixes && max_prefix_len > 0 &&
+           batch * kv_heads * dim >= (kSharedValues + max_prefix_len - 1) / max_prefix_len;
 }
 
 size_t pieces_bytes(int64_t batch, int group, int kv_heads, int dim, int64_t prefixes)
@@ -1126,7 +1134,7 @@ size_t pieces_bytes(int64_t batch, int group, int kv_heads, int dim, int64_t pre
 size_t prefix_attention_workspace(int64_t batch, int group, int kv_heads, int dim, int64_t prefixes, int64_t max_prefix_len,
                                   int64_t max_len)
 {
-    if (!in_pieces(batch, group, prefixes, max_prefix_len))
+    if (!in_pieces(batch, group, kv_heads, dim, prefixes, max_prefix_len))
         return paged_attention_workspace(group, dim, max_prefix_len + max_len);
     return pieces_bytes(batch, group, kv_heads, dim, prefixes) + align256(paged_attention_workspace(group, dim, max_len)) +
            (size_t)batch * group * kv_heads * (dim + 2) * sizeof(float);
@@ -1134,13 +1142,15 @@ size_t prefix_attention_workspace(int64_t batch, int group, int kv_heads, int di
 
 int prefix_attention_launches(const PagedAttention& p)
 {
-    return in_pieces(p.batch, p.q_heads / p.cache.heads, p.shared.count, p.shared.max_len) ? 3 : paged_attention_launches(p);
+    return in_pieces(p.batch, p.q_heads / p.cache.heads, p.cache.heads, p.cache.dim, p.shared.count, p.shared.max_len)
+               ? 3
+               : paged_attention_launches(p);
 }
 
 cudaError_t launch_prefix_attention(PagedAttention p, const DeviceInfo& dev, cudaStream_t s, std::string* why)
 {
     const int group = p.q_heads / p.cache.heads;
-    if (!in_pieces(p.batch, group, p.shared.count, p.shared.max_len))
+    if (!in_pieces(p.batch, group, p.cache.heads, p.cache.dim, p.shared.count, p.shared.max_len))
         return launch_paged_attention(p, dev, s);
     char* ws = static_cast<char*>(p.workspace);
     p.pieces = reinterpret_cast<float*>(ws);

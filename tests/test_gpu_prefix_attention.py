@@ -13,9 +13,10 @@ DEV = "cuda"
 BF, F16 = torch.bfloat16, torch.float16
 
 
-def make(plens, cu, lens, hq, hkv, d, page, dtype, int8, seed, q_std=1.5, extra=1):
-    """A shuffled pool; every row that nobody owns is NaN (16-bit) or has a NaN scale.  Tables have `extra`
-    pages more than the longest needs, naming a page of NaN rows."""
+def make(plens, cu, lens, hq, hkv, d, page, dtype, int8, seed, q_std=1.5, wide=False):
+    """A shuffled pool; every row that nobody owns is NaN (16-bit) or has a NaN scale.  Tables have a page more
+    than the longest needs, naming one of NaN rows; with `wide` the prefixes' has so many that the call computes
+    the shared part for whole groups, whatever the lengths (it goes by the table's width)."""
     g = torch.Generator(device=DEV)
     g.manual_seed(seed)
     owners = list(plens) + list(lens)
@@ -35,7 +36,10 @@ def make(plens, cu, lens, hq, hkv, d, page, dtype, int8, seed, q_std=1.5, extra=
     owned = torch.zeros((pages, page), dtype=torch.bool, device=DEV)
     at = 0
     for part in (list(plens), list(lens)):
-        table = torch.full((len(part), max([1] + [-(-n // page) for n in part]) + extra), spare, dtype=torch.int32, device=DEV)
+        width = max([1] + [-(-n // page) for n in part]) + 1
+        if wide and not tables:
+            width = max(width, -(-(12 << 20) // (len(lens) * hkv * d * page)))
+        table = torch.full((len(part), width), spare, dtype=torch.int32, device=DEV)
         for i, n in enumerate(part):
             mine = pool[at:at + -(-n // page)]
             at += len(mine)
@@ -112,14 +116,23 @@ CASES = [
     ([1500, 400], [0, 9, 30], [i * 3 for i in range(30)], 40, 2, 64, 100),  # of 20
     ([4097], [0, 140], [1 + i % 3 for i in range(140)], 8, 8, 128, 128),   # of 1, pages of a tile
     ([513], [0, 3], [1, 600, 20], 3, 3, 64, 1),                          # pages of one row
+    ([260, 3, 129], [0, 5, 5, 9], [2] * 9, 64, 1, 128, 8),               # 64 heads to one
 ]
 
 
+def in_groups(s):
+    ck.ck_profile_begin(with_events=False)
+    call(s)
+    return ck.ck_profile_end()["attention"][1] == 3
+
+
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("int8", [False, True])
 @pytest.mark.parametrize("dtype", [BF, F16])
 @pytest.mark.parametrize("plens,cu,lens,hq,hkv,d,page", CASES)
-def test_against_the_definition(plens, cu, lens, hq, hkv, d, page, dtype, int8):
-    s = make(plens, cu, lens, hq, hkv, d, page, dtype, int8, seed=sum(plens) + d)
+def test_against_the_definition(plens, cu, lens, hq, hkv, d, page, dtype, int8, wide):
+    s = make(plens, cu, lens, hq, hkv, d, page, dtype, int8, seed=sum(plens) + d, wide=wide)
+    assert in_groups(s) or not wide or len(lens) < 2 * len(plens)
     out, lse = call(s, return_lse=True)
     check(s, out, lse)
     assert ck.ck_device_error() == 0
@@ -138,7 +151,7 @@ def test_a_long_prefix_and_many_sequences(int8):
 def test_equals_attention_over_one_table(batch, int8):
     """Behind a prefix of whole pages, a block table that names its pages first says the same."""
     lens = [1 + i * 11 % 50 for i in range(batch)]
-    s = make([640], [0, batch], lens, 8, 2, 128, 32, BF, int8, seed=batch)
+    s = make([640], [0, batch], lens, 8, 2, 128, 32, BF, int8, seed=batch, wide=batch > 3)
     both = torch.cat([s["ptable"][:, :20].expand(batch, 20), s["table"]], 1).contiguous()
     want, want_lse = ck.ck_paged_attention(s["q"], s["cache"], both, s["lens"] + 640, return_lse=True)
     out, lse = call(s, return_lse=True)
@@ -149,7 +162,7 @@ def test_equals_attention_over_one_table(batch, int8):
 
 def test_sharp_scores_scale_and_strides():
     lens = [30, 4, 0] + [5] * 40
-    s = make([900], [0, 43], lens, 8, 2, 128, 16, F16, False, seed=5, q_std=12.0)
+    s = make([900], [0, 43], lens, 8, 2, 128, 16, F16, False, seed=5, q_std=12.0, wide=True)
     wide = torch.zeros((43, 8 * 128 + 64), dtype=F16, device=DEV)
     wide[:, :1024] = s["q"].reshape(43, -1)
     view = dict(s, q=wide[:, :1024].view(43, 8, 128))
@@ -160,7 +173,7 @@ def test_sharp_scores_scale_and_strides():
 
 @pytest.mark.parametrize("batch", [2, 40])
 def test_infinities_and_nan_stay_with_who_sees_them(batch):
-    s = make([300, 400], [0, batch, 2 * batch], [5] * (2 * batch), 4, 2, 64, 16, BF, False, seed=9)
+    s = make([300, 400], [0, batch, 2 * batch], [5] * (2 * batch), 4, 2, 64, 16, BF, False, seed=9, wide=batch > 2)
     want, want_lse = call(s, return_lse=True)
     s["cache"].v[s["ptable"][1, 3].long(), 0, 2, 5] = float("inf")  # of the second prefix's rows of head 0
     s["cache"].k[s["table"][0, 0].long(), 1, 1] = float("nan")      # of the first sequence's own keys, head 1
@@ -173,9 +186,10 @@ def test_infinities_and_nan_stay_with_who_sees_them(batch):
     assert out[0, 2:].isnan().all() and lse[0, 2:].isnan().all()
 
 
-def test_scores_of_minus_infinity():
+@pytest.mark.parametrize("wide", [False, True])
+def test_scores_of_minus_infinity(wide):
     """A prefix without weight leaves the rest as it is; rows with nothing but such scores are NaN."""
-    s = make([200], [0, 36], [3] * 35 + [0], 4, 2, 64, 16, BF, False, seed=10)
+    s = make([200], [0, 36], [3] * 35 + [0], 4, 2, 64, 16, BF, False, seed=10, wide=wide)
     s["q"].abs_()
     clean = ck.ck_paged_attention(s["q"], s["cache"], s["table"], s["lens"])
     rows = torch.arange(200, device=DEV)
@@ -189,7 +203,8 @@ def test_scores_of_minus_infinity():
 @pytest.mark.parametrize("batch", [2, 40])
 def test_lengths_bounds_and_pages_out_of_range(batch, int8):
     lens = [5] * (2 * batch)
-    base = make([300, 200], [0, batch, 2 * batch], lens, 4, 2, 64, 16, BF, int8, seed=11)
+    base = make([300, 200], [0, batch, 2 * batch], lens, 4, 2, 64, 16, BF, int8, seed=11, wide=batch > 2)
+    assert in_groups(base) == (batch > 2)
     want = call(base)
     assert ck.ck_device_error() == 0
 
@@ -218,6 +233,7 @@ def test_lengths_bounds_and_pages_out_of_range(batch, int8):
 
 def test_given_outputs_streams_and_graphs():
     s = make([2000], [0, 50], [i % 40 for i in range(50)], 8, 2, 128, 16, BF, False, seed=12)
+    assert in_groups(s)
     want, want_lse = call(s, return_lse=True)
     out, lse = torch.empty_like(want), torch.empty_like(want_lse)
     side = torch.cuda.Stream()
@@ -253,9 +269,12 @@ def test_more_rows_than_the_cache_has_bytes_for_in_32_bits():
     at = torch.tensor([pages - 1, 3, pages - 2, 2 ** 15, 1, pages - 3], device=DEV)
     for t in (cache.k, cache.v):
         t[at] = torch.randn((6, hkv, page, d), device=DEV).to(BF)
-    s = dict(q=torch.randn((40, 8, d), device=DEV).to(BF), cache=cache, ptable=at[:4][None].to(torch.int32).contiguous(),
+    ptable = torch.zeros((1, 10), dtype=torch.int32, device=DEV)  # (so wide that the groups are computed as such)
+    ptable[0, :4] = at[:4].to(torch.int32)
+    s = dict(q=torch.randn((40, 8, d), device=DEV).to(BF), cache=cache, ptable=ptable,
              plens=torch.tensor([250], dtype=torch.int32, device=DEV), cu=torch.tensor([0, 40], dtype=torch.int32, device=DEV),
              table=at[4:].to(torch.int32).repeat(40, 1).contiguous(), lens=torch.full((40,), 100, dtype=torch.int32, device=DEV))
+    assert in_groups(s)
     out, lse = call(s, return_lse=True)
     check(s, out, lse, only=[0, 17, 39])
 
