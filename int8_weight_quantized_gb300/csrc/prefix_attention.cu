@@ -17,11 +17,11 @@
 //   warps 4-11  softmax, a warpgroup for each query tile, one thread per row, as in attention.cu: the
 //               weights go back over S as the 16-bit operand P of the second product, the row's
 //               reference trails its maximum by up to 2^8.
-// int8 rows: codes are exact in bf16 and fp16; k's scale multiplies the fp32 score, v's the code, rounded
-// once to the queries' type.
+// int8 rows: codes are exact in bf16 and fp16; k's scale multiplies the fp32 score, v's the fp32 weight.
 //
-// Rounding to fewer bits: each weight once, to the queries' type (and the values of int8 rows); scores,
-// sums, maxima and O are fp32.
+// Rounding to fewer bits: each weight once, to the queries' type; over int8 rows its product with the value
+// scale, to bf16, or to a sum of two of these (16 bits) where the queries are fp16.  Scores, sums, maxima
+// and O are fp32.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -57,11 +57,12 @@ template <int DIM, bool INT8>
 struct Cfg {
     static constexpr uint32_t BOX_BYTES = BM * 128;             // 128 rows of 64 values
     static constexpr uint32_t TILE_BYTES = DIM / 64 * BOX_BYTES;  // a Q, K or V tile
-    static constexpr int UNITS = DIM == 128 ? 5 : 10;             // ring of K_0, V_0, K_1, V_1, ..
-    // Key tiles whose scales are kept: while a softmax warp reads those of tile j, V_j is in the ring, so that
-    // K's of up to UNITS / 2 further tiles are.
+    static constexpr int UNITS = DIM == 128 ? (INT8 ? 4 : 5) : 10;  // ring of K_0, V_0, K_1, V_1, ..
+    // Key tiles whose scales are kept: those of tile m come with K_m, for which the place of unit 2 m - UNITS
+    // has to be free, by when the weights of tile m - UNITS / 2 - 1 have been used.
     static constexpr int SCALES = UNITS / 2 + 1;
-    static constexpr size_t SCALE_BYTES = INT8 ? SCALES * BM * 4 : 0;
+    static constexpr size_t SCALE_BYTES = INT8 ? 2 * SCALES * BM * 4 : 0;
+    static_assert(UNITS % 2 == 0 || !INT8, "scales");
     static constexpr size_t STATE = 512;
     static constexpr size_t SMEM = 1024 + (2 + UNITS) * (size_t)TILE_BYTES + SCALE_BYTES + STATE;
     static_assert(SMEM <= 232448, "shared memory budget");
@@ -161,35 +162,6 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t codes, int i)
     }
 }
 
-// Pairs of codes times a scale, rounded once.  bf16: the scale as the sum of two, code * low added to the exact
-// product with high (2^-17 of a unit off at most); fp16, which such a low part may leave: in fp32.
-template <class E>
-struct Scaled {
-    float scale;
-    __device__ __forceinline__ Scaled(float s) : scale(s) {}
-    __device__ __forceinline__ uint32_t operator()(uint32_t pair) const
-    {
-        const float2 v = f2_mul_rn(E::to2(pair), make_float2(scale, scale));
-        return E::pack2(v.x, v.y);
-    }
-};
-template <>
-struct Scaled<Bf16> {
-    __nv_bfloat162 high, low;
-    __device__ __forceinline__ Scaled(float s)
-    {
-        const __nv_bfloat16 h = __float2bfloat16_rn(s);
-        high = __bfloat162bfloat162(h);
-        low = __bfloat162bfloat162(__float2bfloat16_rn(s - __bfloat162float(h)));
-    }
-    __device__ __forceinline__ uint32_t operator()(uint32_t pair) const
-    {
-        const __nv_bfloat162 c = *reinterpret_cast<const __nv_bfloat162*>(&pair);
-        const __nv_bfloat162 v = __hfma2(c, high, __hmul2_rn(c, low));
-        return *reinterpret_cast<const uint32_t*>(&v);
-    }
-};
-
 template <class E, int DIM, bool INT8>
 __global__ void __launch_bounds__(THREADS, 1)
     prefix_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -197,12 +169,17 @@ __global__ void __launch_bounds__(THREADS, 1)
 {
     using C = Cfg<DIM, INT8>;
     using T = typename E::T;
+    // The second product's type.  int8: codes are exact in bf16, and a weight times its value's scale is in its
+    // range whatever the scale; with fp16 queries, whose 11 bits a bf16 weight would not have, as a sum of two.
+    using PV = typename std::conditional<INT8, Bf16, E>::type;
+    constexpr bool TWO = INT8 && std::is_same<E, Fp16>::value;
     constexpr int UNITS = C::UNITS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* s_q = smem;
     uint8_t* s_ring = s_q + 2 * C::TILE_BYTES;
-    float* s_kscale = reinterpret_cast<float*>(s_ring + UNITS * C::TILE_BYTES);  // int8: [SCALES][BM]
+    float* s_kscale = reinterpret_cast<float*>(s_ring + UNITS * C::TILE_BYTES);  // int8: [SCALES][BM] of K, of V
+    float* s_vscale = s_kscale + (INT8 ? C::SCALES * BM : 0);
     uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(s_kscale) + C::SCALE_BYTES);
     uint64_t* q_full = bars;             // [2]
     uint64_t* s_full = bars + 2;         // [2] S_t is complete (and every product before it)
@@ -309,7 +286,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (warp == 0) {
             // -------------------------------------------------------------- products
             const uint32_t idesc_s = idesc_of<E>(BM, false) | (a.negate ? 1u << 13 : 0u);
-            constexpr uint32_t idesc_o = idesc_of<E>(DIM, true);
+            constexpr uint32_t idesc_o = idesc_of<PV>(DIM, true);
             const uint64_t q_desc = desc_kmajor_sw128(smem_u32(s_q));
             const uint64_t k_desc = desc_kmajor_sw128(smem_u32(s_ring));
             const uint64_t v_desc = desc_nmajor_sw128(smem_u32(s_ring), C::BOX_BYTES);
@@ -328,6 +305,10 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                 for (int k = from.value / 16; k < keys.value / 16; ++k)
                     mma_ts(tmem + 2 * BM + t * DIM, tmem + t * BM + k * 8, y + k * (16 * 128 >> 4), idesc_o, k > 0 || started);
+                if (TWO)
+#pragma unroll
+                    for (int k = from.value / 16; k < keys.value / 16; ++k)
+                        mma_ts(tmem + 2 * BM + t * DIM, tmem + t * BM + BM / 2 + k * 8, y + k * (16 * 128 >> 4), idesc_o, 1);
             };
             // Q_t of a walk's piece, once the scores from the one before are computed
             auto load_q = [&](const Walk& of, int t) {
@@ -611,9 +592,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 all_landed();
             } else {
                 // The raw codes of a row land where its own last values will be (the second box's row, or with heads of
-                // 64 the first half of its row), its scale where its first ones will: so a row is widened in
-                // place, by the lanes that copied it.
-                constexpr uint32_t RAW_AT = DIM == 128 ? C::BOX_BYTES : 0, SCALE_AT = DIM == 128 ? 0 : 64;
+                // 64 the first half of its row), so that it is widened in place, by the lanes that copied it; scales go
+                // to the softmax.
+                constexpr uint32_t RAW_AT = DIM == 128 ? C::BOX_BYTES : 0;
                 const uint32_t units = 2 * (uint32_t)at.left;  // K, V, K, V, ..
                 // Lanes of 8 rows' halves at once: chunk c of a row is lane's bits 0, 1 (and 3 with heads of 128), its row among
                 // the instruction's the others, and raw chunks of odd rows lie the other half first: reads and writes
@@ -637,15 +618,20 @@ __global__ void __launch_bounds__(THREADS, 1)
                             cp_async16(dst + RAW_AT + r * 128 + raw_chunk(r, lane % CH) * 16, base + (uint64_t)row * DIM,
                                        ((h ? oks[1] : oks[0]) >> (n % 32)) & 1u);
                     }
+                    if (is_k) {
+                        const uint32_t at_tile = copies / 2 % C::SCALES * BM;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        if (row_in_tile(h) >= 0) {
-                            const uint32_t to = dst + SCALE_AT + row_in_tile(h) * 128;
-                            if ((bads[h] >> lane) & 1u)  // on a page out of range: NaN
-                                asm volatile("st.shared.u32 [%0], %1;" ::"r"(to), "r"(0x7fffffffu) : "memory");
-                            else
-                                cp_async_small<4>(to, (is_k ? cache.k_scale : cache.v_scale) + rows[h], (oks[h] >> lane) & 1u);
-                        }
+                        for (int h = 0; h < 2; ++h)
+                            if (row_in_tile(h) >= 0) {
+                                const uint32_t at_row = (at_tile + row_in_tile(h)) * 4;
+                                const bool there = (oks[h] >> lane) & 1u;
+                                if ((bads[h] >> lane) & 1u)  // on a page out of range: NaN
+                                    s_kscale[at_tile + row_in_tile(h)] = NAN;
+                                else
+                                    cp_async_small<4>(smem_u32(s_kscale) + at_row, cache.k_scale + rows[h], there);
+                                cp_async_small<4>(smem_u32(s_vscale) + at_row, cache.v_scale + rows[h], there);
+                            }
+                    }
                     cp_async_commit();
                     ++copies;
                     if (!is_k && ++j == at.count()) {
@@ -654,7 +640,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                 };
                 auto widen = [&]() {
-                    const bool is_k = (widened & 1u) == 0;
+                    [[maybe_unused]] const bool is_k = (widened & 1u) == 0;
                     const int slot = widened % UNITS;
                     switch (copies - widened - 1) {  // copies under way that came after this one's
                     case 0: cp_async_wait<0>(); break;
@@ -662,43 +648,39 @@ __global__ void __launch_bounds__(THREADS, 1)
                     case 2: cp_async_wait<2>(); break;
                     default: cp_async_wait<3>(); break;
                     }
-                    __syncwarp();  // codes and scales come from other lanes' copies too
+                    __syncwarp();  // codes come from other lanes' copies too
                     const uint32_t dst = smem_u32(s_ring) + slot * C::TILE_BYTES;
-                    float* kscale = s_kscale + (widened / 2) % C::SCALES * BM;
-                    constexpr int BATCH = 4;
+                    auto rows_as = [&](auto type) {
+                        using X = decltype(type);
+                        constexpr int BATCH = 4;
 #pragma unroll
-                    for (int i0 = 0; i0 < TURNS; i0 += BATCH) {
-                        uint4 codes[BATCH];
-                        float scale[BATCH];
+                        for (int i0 = 0; i0 < TURNS; i0 += BATCH) {
+                            uint4 codes[BATCH];
 #pragma unroll
-                        for (int i = i0; i < i0 + BATCH && i < TURNS; ++i) {
-                            const int r = min((i * LOADERS + w) * RPI + my_sub, BM - 1);
-                            codes[i - i0] = lds128(dst + RAW_AT + r * 128 + raw_chunk(r, my_chunk) * 16);
-                            scale[i - i0] = __uint_as_float(lds32(dst + SCALE_AT + r * 128));
-                        }
-                        __syncwarp();
-#pragma unroll
-                        for (int i = i0; i < i0 + BATCH && i < TURNS; ++i) {
-                            const int r = (i * LOADERS + w) * RPI + my_sub;
-                            const uint4 q = codes[i - i0];
-                            const uint32_t word[4] = {q.x, q.y, q.z, q.w};
-                            uint32_t out[8];
-                            const Scaled<E> by(scale[i - i0]);
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                out[k] = code_pair<E>(word[k / 2], k & 1);
-                                if (!is_k)
-                                    out[k] = by(out[k]);
+                            for (int i = i0; i < i0 + BATCH && i < TURNS; ++i) {
+                                const int r = min((i * LOADERS + w) * RPI + my_sub, BM - 1);
+                                codes[i - i0] = lds128(dst + RAW_AT + r * 128 + raw_chunk(r, my_chunk) * 16);
                             }
-                            if (r < BM) {
-                                sts128(dst + chunk_at(r, 2 * my_chunk), make_uint4(out[0], out[1], out[2], out[3]));
-                                sts128(dst + chunk_at(r, 2 * my_chunk + 1), make_uint4(out[4], out[5], out[6], out[7]));
-                                if (is_k && my_chunk == 0)
-                                    kscale[r] = scale[i - i0];
+                            __syncwarp();
+#pragma unroll
+                            for (int i = i0; i < i0 + BATCH && i < TURNS; ++i) {
+                                const int r = (i * LOADERS + w) * RPI + my_sub;
+                                const uint4 q = codes[i - i0];
+                                if (r < BM) {
+                                    sts128(dst + chunk_at(r, 2 * my_chunk), make_uint4(code_pair<X>(q.x, 0), code_pair<X>(q.x, 1),
+                                                                                       code_pair<X>(q.y, 0), code_pair<X>(q.y, 1)));
+                                    sts128(dst + chunk_at(r, 2 * my_chunk + 1),
+                                           make_uint4(code_pair<X>(q.z, 0), code_pair<X>(q.z, 1), code_pair<X>(q.w, 0),
+                                                      code_pair<X>(q.w, 1)));
+                                }
                             }
+                            __syncwarp();
                         }
-                        __syncwarp();
-                    }
+                    };
+                    if (std::is_same<E, PV>::value || is_k)
+                        rows_as(E());
+                    else
+                        rows_as(PV());
                     landed(&full[slot]);
                     ++widened;
                 };
@@ -828,8 +810,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const float2 c2 = make_float2(c, c), mc2 = make_float2(mc, mc);
                 float2 sum = make_float2(0.0f, 0.0f);
                 constexpr int FIRST = FIRST_KEYS<DIM> / 32;
+                const uint32_t vscales = smem_u32(s_vscale + (INT8 ? k_tiles % C::SCALES * BM : 0));
                 auto part = [&](auto from, auto to) {
                     uint32_t packed[to.value - from.value][16];
+                    [[maybe_unused]] uint32_t rest[TWO ? to.value - from.value : 1][16];
 #pragma unroll
                     for (int i = from.value; i < to.value; ++i)
 #pragma unroll
@@ -839,12 +823,23 @@ __global__ void __launch_bounds__(THREADS, 1)
                             x.x = fast_exp2(x.x);
                             x.y = fast_exp2(x.y);
                             sum = f2_add_rn(sum, x);
-                            packed[i - from.value][n] = E::pack2(x.x, x.y);
+                            if constexpr (INT8) {
+                                const uint2 f = lds64(vscales + (32 * i + 2 * n) * 4);
+                                x = f2_mul_rn(x, make_float2(__uint_as_float(f.x), __uint_as_float(f.y)));
+                            }
+                            packed[i - from.value][n] = PV::pack2(x.x, x.y);
+                            if constexpr (TWO) {
+                                const float2 high = PV::to2(packed[i - from.value][n]);
+                                rest[i - from.value][n] = PV::pack2(x.x - high.x, x.y - high.y);
+                            }
                         }
                     // (a dry pass leaves its weights where nothing is yet: O)
 #pragma unroll
-                    for (int i = from.value; i < to.value; ++i)
+                    for (int i = from.value; i < to.value; ++i) {
                         tmem_st_32x32b_x16((dry ? o_addr : s_addr) + 16 * i, packed[i - from.value]);
+                        if constexpr (TWO)
+                            tmem_st_32x32b_x16(dry ? o_addr + 16 * i : s_addr + BM / 2 + 16 * i, rest[i - from.value]);
+                    }
                 };
                 if constexpr (FIRST > 0) {
                     part(std::integral_constant<int, 0>(), std::integral_constant<int, FIRST>());

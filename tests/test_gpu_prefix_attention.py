@@ -1,7 +1,7 @@
 """Attention of one new token behind shared prefixes, against the 64-bit definition over the prefix's
-keys and the sequence's own (transformer_ref.attend derives the bound; values of int8 rows may be
-rounded once to the queries' type before the second product, one more unit of theirs; one rounding
-of the output on top)."""
+keys and the sequence's own (transformer_ref.attend derives the bound: each weight, over int8 rows its
+product with the value scale, is rounded once, to the queries' type or better; one rounding of the
+output on top)."""
 import pytest
 import torch
 
@@ -81,8 +81,7 @@ def check(s, out, lse, scale=None, only=None):
     int8 = cache.k.dtype == torch.int8
     scale = d ** -0.5 if scale is None else scale
     cu, plens = s["cu"].tolist(), s["plens"].tolist()
-    # int8 rows: weights in fp16 (16-bit keys of a short call) or in the queries' type, values rounded once
-    p_unit = ref.unit(dtype) * (2 if int8 else 1)
+    p_unit = ref.unit(dtype)
     p_least = max(ref.least(dtype), ref.least(F16)) if int8 else ref.least(dtype)
     for b, n in enumerate(s["lens"].tolist()):
         if only is not None and b not in only:
