@@ -375,6 +375,20 @@ bool make_map_2d(CUtensorMap* map, const void* base, int64_t rows, int64_t K, in
     return make_box_map(map, base, 2, dims, strides, box, f16, why);
 }
 
+// [M, N] outputs as boxes of 128 rows of 128 bytes.
+bool make_out_map(CUtensorMap* map, const void* base, int64_t M, int64_t N, int out, std::string* why)
+{
+    const int size = out == CK_OUT_F32 ? 4 : 2;
+    const cuuint64_t dims[2] = {(cuuint64_t)N, (cuuint64_t)M};
+    const cuuint64_t strides[1] = {(cuuint64_t)N * size};
+    const cuuint32_t box[2] = {(cuuint32_t)(128 / size), TILE};
+    return make_box_map(map, base, 2, dims, strides, box,
+                        out == CK_OUT_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                        : out == CK_OUT_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                            : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                        why);
+}
+
 // ---- 8 neighbouring outputs of a lane
 template <int OUT>
 struct Eight;
@@ -583,6 +597,347 @@ __global__ void __launch_bounds__(THREADS, 2) expand_kernel(const AdapterLinear 
     griddep_launch_dependents();
 }
 
+// ---- many rows: a block takes 128 rows and some boxes of 128 bytes of their outputs
+//   warp 0       copies the residual's boxes and each adapter's part of B by TMA;
+//   warp 1       issues the products, one lane: h B_i^T of a box, for one adapter after the other;
+//   warps 2 - 5  add h up, round it and leave it as the products' first operand; then a thread a row: what
+//                the product of its adapter adds to its row of a box, in shared memory, from where the box
+//                goes out by TMA.
+constexpr int MOST_ADAPTERS = TILE;  // of a tile
+constexpr int BOX_STAGES = 2, B_STAGES = 2, SUMS = 2;
+
+template <int OUT>
+struct GrowCfg {
+    static constexpr int W = OUT == CK_OUT_F32 ? 32 : 64;  // columns of a box
+    // boxes of the residual, of B, of h; kb: boxes of 64 of the rank
+    static constexpr size_t smem(int kb) { return 1024 + BOX_STAGES * X_BYTES + (size_t)kb * (B_STAGES * W * 128 + X_BYTES); }
+};
+
+template <class E, int OUT>
+__global__ void __launch_bounds__(MANY_THREADS)
+    expand_many_kernel(const __grid_constant__ CUtensorMap tmR, const __grid_constant__ CUtensorMap tmB,
+                       const __grid_constant__ CUtensorMap tmY, const AdapterLinear p, int boxes, int splits, unsigned int* err)
+{
+    constexpr int W = GrowCfg<OUT>::W;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint32_t key[TILE];
+    __shared__ uint32_t list[MOST_ADAPTERS];
+    __shared__ float factors[TILE];
+    __shared__ uint64_t bars[2 * BOX_STAGES + 2 * B_STAGES + 2 * SUMS + 3];
+    __shared__ int found[4];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int aborted;
+    const int kb = (p.rank + 63) / 64;  // boxes of 64 of the rank
+    uint8_t* s_box = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* s_h = s_box + BOX_STAGES * X_BYTES;
+    uint8_t* s_b = s_h + kb * X_BYTES;
+    uint64_t *box_full = bars, *box_empty = box_full + BOX_STAGES, *b_full = box_empty + BOX_STAGES, *b_empty = b_full + B_STAGES,
+             *done = b_empty + B_STAGES, *taken = done + SUMS, *h_full = taken + SUMS, *box_ready = h_full + 1, *drain = box_ready + 1;
+    volatile int* abort_flag = &aborted;
+    const int warp = __shfl_sync(FULL, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    constexpr uint32_t TMEM = SUMS * W < 32 ? 32 : SUMS * W;
+    if (warp == 0 && lane == 0) {
+        for (int i = 0; i < BOX_STAGES; ++i) {
+            mbar_init(&box_full[i], 1);
+            mbar_init(&box_empty[i], 1);
+        }
+        for (int i = 0; i < B_STAGES; ++i) {
+            mbar_init(&b_full[i], 1);
+            mbar_init(&b_empty[i], 1);
+        }
+        for (int i = 0; i < SUMS; ++i) {
+            mbar_init(&done[i], 1);
+            mbar_init(&taken[i], 4);
+        }
+        mbar_init(h_full, 4);
+        mbar_init(box_ready, 4);
+        mbar_init(drain, 1);
+        aborted = 0;
+        fence_mbar_init();
+        fence_proxy_async_smem();
+        tma_prefetch_desc(&tmR);
+        tma_prefetch_desc(&tmB);
+        tma_prefetch_desc(&tmY);
+    }
+    if (warp == 1) {
+        tmem_alloc(&tmem_slot, TMEM);
+        tmem_relinquish();
+    }
+    __syncwarp();
+    // (the first kernel lets this one begin when its blocks have seen the work before them complete: only h is
+    // waited for)
+    const int64_t all_boxes = (p.N + W - 1) / W, chunks = (all_boxes + boxes - 1) / boxes;
+    const int64_t first = blockIdx.x / chunks * TILE, box0 = blockIdx.x % chunks * boxes;
+    const int count_boxes = (int)min(all_boxes - box0, (int64_t)boxes);
+    const int m = threadIdx.x;
+    uint32_t mine = (uint32_t)p.adapters;
+    if (m < TILE) {
+        if (first + m < p.M) {
+            const int32_t i = __ldg(p.index + first + m);
+            mine = i < 0 ? (uint32_t)p.adapters : (int64_t)i < p.adapters ? (uint32_t)i : (uint32_t)p.adapters + 1u;
+        }
+        key[m] = mine;
+    }
+    const bool out_of_range = mine > p.adapters;
+    __syncthreads();
+    bool leads = m < TILE && mine < p.adapters;
+    for (int n = 0; leads && n < m; ++n)
+        leads = key[n] != mine;
+    const uint32_t leaders = __ballot_sync(FULL, leads);
+    if (lane == 0 && m < TILE)
+        found[warp] = __popc(leaders);
+    tc_fence_before();
+    const bool any_bad = __syncthreads_or(out_of_range);
+    tc_fence_after();
+    int count = 0, before = 0;
+    for (int w = 0; w < 4; ++w) {
+        before += w < warp ? found[w] : 0;
+        count += found[w];
+    }
+    if (leads)
+        list[before + __popc(leaders & ((1u << lane) - 1u))] = mine;
+    __syncthreads();
+    const uint32_t tmem = __shfl_sync(FULL, tmem_slot, 0);
+    const bool residual = p.residual != nullptr;
+    const bool idle = count == 0 && !any_bad && p.residual == p.y;  // in place, without adapters
+
+    if (idle) {
+        // the rows stay as they are
+    } else if (warp == 0) {
+        if (lane == 0) {
+            int boxes_sent = 0, parts_sent = 0;
+            auto wait = [&](uint64_t* bar, uint32_t parity) {
+                return mbar_wait(bar, parity, abort_flag, err, kErrWaitAdapter, TIMEOUT_NS);
+            };
+            bool ok = true;
+            for (int i = 0; ok && i < count_boxes; ++i) {
+                if (residual) {
+                    const int s = i % BOX_STAGES;
+                    ok = wait(&box_empty[s], (uint32_t)(i / BOX_STAGES + 1) & 1u);
+                    if (!ok)
+                        break;
+                    mbar_arrive_expect_tx(&box_full[s], X_BYTES);
+                    tma_load_2d(s_box + s * X_BYTES, &tmR, &box_full[s], (int32_t)(box0 + i) * W, (int32_t)first);
+                    ++boxes_sent;
+                }
+                for (int n = 0; n < count; ++n) {
+                    const int s = parts_sent % B_STAGES;
+                    ok = wait(&b_empty[s], (uint32_t)(parts_sent / B_STAGES + 1) & 1u);
+                    if (!ok)
+                        break;
+                    mbar_arrive_expect_tx(&b_full[s], (uint32_t)(kb * W * 128));
+                    for (int k = 0; k < kb; ++k)
+                        tma_load_3d(s_b + (s * kb + k) * W * 128, &tmB, &b_full[s], 64 * k, (int32_t)(box0 + i) * W,
+                                    (int32_t)list[n]);
+                    ++parts_sent;
+                }
+            }
+            if (!ok) {  // aborting: every issued copy lands before shared memory is released
+                for (int i = max(boxes_sent - BOX_STAGES, 0); i < boxes_sent; ++i)
+                    wait_out(&box_full[i % BOX_STAGES], (uint32_t)(i / BOX_STAGES) & 1u, err, kErrWaitAdapter, TIMEOUT_NS);
+                for (int i = max(parts_sent - B_STAGES, 0); i < parts_sent; ++i)
+                    wait_out(&b_full[i % B_STAGES], (uint32_t)(i / B_STAGES) & 1u, err, kErrWaitAdapter, TIMEOUT_NS);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        const uint32_t idesc = idesc_of<E>(W, false);
+        const uint64_t h_desc = desc_kmajor_sw128(smem_u32(s_h)), b_desc = desc_kmajor_sw128(smem_u32(s_b));
+        const bool leader = elect_one();
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            const bool ok = mbar_wait(bar, parity, abort_flag, err, kErrWaitAdapter, TIMEOUT_NS);
+            return __all_sync(FULL, ok) != 0;
+        };
+        const int uses = count_boxes * count, steps = (p.rank + 15) / 16;
+        bool ok = uses == 0 || wait(h_full, 0);
+        for (int use = 0; ok && use < uses; ++use) {
+            const int s = use % B_STAGES, d = use % SUMS;
+            ok = wait(&taken[d], (uint32_t)(use / SUMS + 1) & 1u) && wait(&b_full[s], (uint32_t)(use / B_STAGES) & 1u);
+            if (!ok)
+                break;
+            tc_fence_after();
+            if (leader) {
+                for (int k = 0; k < steps; ++k)
+                    mma_ss(tmem + d * W, h_desc + (uint64_t)(k / 4) * (X_BYTES >> 4) + (k % 4) * 2,
+                           b_desc + (uint64_t)(s * kb + k / 4) * (W * 128 >> 4) + (k % 4) * 2, idesc, k > 0);
+                mma_commit(&b_empty[s]);
+                mma_commit(&done[d]);
+            }
+            __syncwarp();
+        }
+        // every product must be complete before tensor and shared memory are released
+        if (leader) {
+            mma_commit(drain);
+            wait_out(drain, 0, err, kErrWaitAdapter, TIMEOUT_NS);
+        }
+        __syncwarp();
+    } else {
+        const int quarter = warp & 3, row = quarter * 32 + lane;
+        // ---- h: 8 values a lane, a row to as many lanes as it takes (a power of two, of one warp's rows)
+        int lanes = 1;
+        while (lanes * 8 < p.rank)
+            lanes *= 2;
+        const int c = lane % lanes * 8;
+        griddep_wait();
+        for (int r = quarter * 32 + lane / lanes; r < quarter * 32 + 32; r += 32 / lanes) {
+            const uint32_t adapter = key[r];
+            const bool in = adapter < p.adapters && c < p.rank;
+            float v[8] = {};
+            const float* src = static_cast<const float*>(p.workspace) + (first + r) * p.rank + c;
+            if (in)
+#pragma unroll 4
+                for (int n = 0; n < splits; ++n) {
+                    const float4* part = reinterpret_cast<const float4*>(src + (int64_t)n * p.M * p.rank);
+                    const float4 lo = __ldcg(part), hi = __ldcg(part + 1);
+                    v[0] += lo.x, v[1] += lo.y, v[2] += lo.z, v[3] += lo.w;
+                    v[4] += hi.x, v[5] += hi.y, v[6] += hi.z, v[7] += hi.w;
+                }
+            float down = 1.0f, factor = adapter < p.adapters && p.scaling ? __ldg(p.scaling + adapter) : 1.0f;
+            if (std::is_same<E, Fp16>::value) {
+                float top = 0.0f;
+#pragma unroll
+                for (int n = 0; n < 8; ++n)
+                    top = fmaxf(top, fabsf(v[n]));
+                for (int o = 1; o < lanes; o *= 2)
+                    top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
+                const int e = top > 0.0f && top < INFINITY ? max(ilogbf(top), -126) : 0;
+                down = ldexpf(1.0f, -e);  // (both powers are floats for these e)
+                factor *= ldexpf(1.0f, e);
+            }
+            // (beyond the rank, up to the products' last step of 16: zeros)
+            if (c < (p.rank + 15) / 16 * 16) {
+                uint8_t* dst = s_h + (c / 64) * X_BYTES + r * 128 + (((c / 8 & 7) ^ (r & 7)) << 4);
+                *reinterpret_cast<uint4*>(dst) =
+                    make_uint4(E::pack2(v[0] * down, v[1] * down), E::pack2(v[2] * down, v[3] * down),
+                               E::pack2(v[4] * down, v[5] * down), E::pack2(v[6] * down, v[7] * down));
+            }
+            if (c == 0)
+                factors[r] = adapter > p.adapters ? NAN : factor;
+        }
+        if (lanes * 8 < (p.rank + 15) / 16 * 16 && lane < 32)  // a rank of 8: one lane a row
+            *reinterpret_cast<uint4*>(s_h + row * 128 + ((1 ^ (row & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(h_full);
+        // ---- boxes
+        const uint32_t own = key[row];
+        const float factor = factors[row];
+        bool ok = true;
+        int use = 0, unsure = 0;
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            const bool yes = ok && mbar_wait(bar, parity, abort_flag, err, kErrWaitAdapter, TIMEOUT_NS);
+            return __all_sync(FULL, yes) != 0;
+        };
+        // 16 bytes of the thread's row in a box
+        auto piece = [&](int s, int i) { return reinterpret_cast<uint4*>(s_box + s * X_BYTES + row * 128 + ((i ^ (row & 7)) << 4)); };
+        for (int i = 0; i < count_boxes; ++i) {
+            const int s = i % BOX_STAGES;
+            if (residual) {
+                if (i > 0 && warp == 2 && lane == 0) {  // the place of the box before is free for the next load
+                    bulk_wait_group_read<0>();
+                    mbar_arrive(&box_empty[(i - 1) % BOX_STAGES]);
+                }
+                __syncwarp();
+                ok = wait(&box_full[s], (uint32_t)(i / BOX_STAGES) & 1u);
+            } else {
+                // (this box's place is free once the stores before it have been read)
+                if (warp == 2 && lane == 0)
+                    bulk_wait_group_read<BOX_STAGES - 1>();
+                __syncwarp();
+                if (warp == 2 && lane == 0)
+                    mbar_arrive(&box_full[s]);
+                ok = wait(&box_full[s], (uint32_t)(i / BOX_STAGES) & 1u);
+#pragma unroll
+                for (int n = 0; n < 8; ++n)
+                    *piece(s, n) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            if (own > p.adapters || !ok)
+#pragma unroll
+                for (int n = 0; n < 8; ++n)
+                    *piece(s, n) = OUT == CK_OUT_F32 ? make_uint4(0x7fffffffu, 0x7fffffffu, 0x7fffffffu, 0x7fffffffu)
+                                                     : make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+            for (int n = 0; n < count; ++n, ++use) {
+                const int d = use % SUMS;
+                ok = wait(&done[d], (uint32_t)(use / SUMS) & 1u);
+                tc_fence_after();
+                const bool add = ok && own == list[n];
+#pragma unroll
+                for (int w = 0; w < W; w += 32) {
+                    uint32_t v[32];
+                    if (ok) {
+                        tmem_ld_32x32b_x32(tmem + ((uint32_t)(quarter * 32) << 16) + d * W + w, v);
+                        tmem_wait_ld();
+                    }
+                    if (add) {
+                        constexpr int PER = OUT == CK_OUT_F32 ? 4 : 8;  // values of 16 bytes
+#pragma unroll
+                        for (int q = 0; q < 32 / PER; ++q) {
+                            uint4* at = piece(s, w / PER + q);
+                            uint4 y = *at;
+                            if constexpr (OUT == CK_OUT_F32) {
+                                y.x = __float_as_uint(__uint_as_float(y.x) + __uint_as_float(v[4 * q]) * factor);
+                                y.y = __float_as_uint(__uint_as_float(y.y) + __uint_as_float(v[4 * q + 1]) * factor);
+                                y.z = __float_as_uint(__uint_as_float(y.z) + __uint_as_float(v[4 * q + 2]) * factor);
+                                y.w = __float_as_uint(__uint_as_float(y.w) + __uint_as_float(v[4 * q + 3]) * factor);
+                            } else {
+                                using O = typename std::conditional<OUT == CK_OUT_F16, Fp16, Bf16>::type;
+                                uint32_t* word = &y.x;
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    const float2 f = O::to2(word[k]);
+                                    word[k] = O::pack2(f.x + __uint_as_float(v[8 * q + 2 * k]) * factor,
+                                                       f.y + __uint_as_float(v[8 * q + 2 * k + 1]) * factor);
+                                }
+                            }
+                            *at = y;
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (ok && lane == 0)
+                    mbar_arrive(&taken[d]);
+                __syncwarp();
+            }
+            // the box, once all four warps have left their rows
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(box_ready);
+            if (warp == 2) {
+                const bool all = mbar_wait(box_ready, (uint32_t)i & 1u, abort_flag, err, kErrWaitAdapter, TIMEOUT_NS);
+                if (lane == 0 && all) {
+                    tma_store_2d(&tmY, s_box + s * X_BYTES, (int32_t)(box0 + i) * W, (int32_t)first);
+                    bulk_commit_group();
+                }
+                __syncwarp();
+            }
+            unsure = ok ? i : unsure;
+        }
+        if (warp == 2 && lane == 0)
+            bulk_wait_group<0>();
+        __syncwarp();
+        if (!ok && first + row < p.M) {  // a wait gave up: NaN in what may not have gone out
+            const int64_t end = min((box0 + count_boxes) * W, p.N);
+            for (int64_t n = (box0 + unsure) * W; n < end; ++n) {
+                const int64_t at = (first + row) * p.N + n;
+                if (OUT == CK_OUT_F32)
+                    static_cast<float*>(p.y)[at] = NAN;
+                else
+                    static_cast<uint16_t*>(p.y)[at] = 0x7fff;
+            }
+        }
+    }
+    griddep_launch_dependents();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, TMEM);
+    }
+}
+
 // Parts of K.  Few rows: enough steps for a block's warps; many: blocks that fill the rounds of two to
 // an SM well, a part at least 4 boxes of 64.
 constexpr int64_t kSlots = 304;
@@ -684,10 +1039,53 @@ cudaError_t launch_adapter_linear(const AdapterLinear& p, const DeviceInfo& dev,
             return by_rank(std::integral_constant<int, 1>());
         return p.rank <= 64 ? by_rank(std::integral_constant<int, 2>()) : by_rank(std::integral_constant<int, 4>());
     };
+    auto grow_many = [&](auto type, auto out) {
+        using E = decltype(type);
+        constexpr int OUT = decltype(out)::value;
+        using C = GrowCfg<OUT>;
+        constexpr auto kernel = expand_many_kernel<E, OUT>;
+        static ContextCache<int> cache;
+        int done = 0;
+        const cudaError_t r = cache.get(&done, [&](int* d) {
+            *d = 1;
+            return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::smem(2));
+        });
+        if (r != cudaSuccess)
+            return r;
+        const int kb = (p.rank + 63) / 64;
+        // boxes of a block, by the rounds of the blocks that fit at once, each as long as its boxes and a fixed
+        // cost of about 5
+        const int64_t all = (p.N + C::W - 1) / C::W, slots = (int64_t)dev.sm_count * (kb == 1 ? 3 : 2);
+        int64_t boxes = 1;
+        double best = INFINITY;
+        for (int64_t n = 1; n <= 64 && n <= all; ++n) {
+            const double cost = (double)((tiles * ((all + n - 1) / n) + slots - 1) / slots) * ((double)n + 5.0);
+            if (cost < best)
+                best = cost, boxes = n;
+        }
+        CUtensorMap res, b, y;
+        const cuuint64_t b_dims[3] = {(cuuint64_t)p.rank, (cuuint64_t)p.N, (cuuint64_t)std::max<int64_t>(p.adapters, 1)};
+        const cuuint64_t b_strides[2] = {(cuuint64_t)p.rank * 2, (cuuint64_t)p.rank * p.N * 2};
+        const cuuint32_t b_box[3] = {64, C::W, 1};
+        if (!make_out_map(&y, p.y, p.M, p.N, OUT, why))
+            return cudaErrorInvalidValue;
+        res = b = y;  // where there is none no block copies any
+        if ((p.residual && !make_out_map(&res, p.residual, p.M, p.N, OUT, why)) ||
+            (p.adapters > 0 && !make_box_map(&b, p.b, 3, b_dims, b_strides, b_box, p.f16, why)))
+            return cudaErrorInvalidValue;
+        return launch_pdl(kernel, dim3((unsigned)(tiles * ((all + boxes - 1) / boxes))), dim3(MANY_THREADS), C::smem(kb), s, res, b,
+                          y, p, (int)boxes, splits, err);
+    };
     auto run = [&](auto type) {
         const cudaError_t r = shrink(type);
         if (r != cudaSuccess)
             return r;
+        if (!few) {
+            if (p.out_dtype == CK_OUT_F32)
+                return grow_many(type, std::integral_constant<int, CK_OUT_F32>());
+            return p.out_dtype == CK_OUT_F16 ? grow_many(type, std::integral_constant<int, CK_OUT_F16>())
+                                             : grow_many(type, std::integral_constant<int, CK_OUT_BF16>());
+        }
         if (p.out_dtype == CK_OUT_F32)
             return grow(type, std::integral_constant<int, CK_OUT_F32>());
         return p.out_dtype == CK_OUT_F16 ? grow(type, std::integral_constant<int, CK_OUT_F16>())

@@ -177,9 +177,9 @@ inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
     return fn;
 }
 
-// A tensor of 16-bit values, the first dimension dense, copied as boxes with 128-byte swizzling.
+// A tensor, the first dimension dense, copied as boxes with 128-byte swizzling.
 inline bool make_box_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
-                         const cuuint32_t* box, bool f16, std::string* why)
+                         const cuuint32_t* box, CUtensorMapDataType type, std::string* why)
 {
     auto fn = encode_fn();
     if (!fn) {
@@ -187,13 +187,20 @@ inline bool make_box_map(CUtensorMap* map, const void* base, int rank, const cuu
         return false;
     }
     const cuuint32_t estr[3] = {1, 1, 1};
-    const CUresult r = fn(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank,
+    const CUresult r = fn(map, type, (cuuint32_t)rank,
                           const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
         *why = "cuTensorMapEncodeTiled failed (" + std::to_string((int)r) + ")";
     return r == CUDA_SUCCESS;
+}
+
+inline bool make_box_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                         const cuuint32_t* box, bool f16, std::string* why)
+{
+    return make_box_map(map, base, rank, dims, strides, box,
+                        f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, why);
 }
 
 }  // namespace ck
