@@ -941,7 +941,10 @@ __global__ void __launch_bounds__(MANY_THREADS)
 // Parts of K.  Few rows: enough steps for a block's warps; many: blocks that fill the rounds of two to
 // an SM well, a part at least 4 boxes of 64.
 constexpr int64_t kSlots = 304;
-int splits_of(int64_t M, int64_t K)
+// The second product on the fifth-generation tensor core from this many outputs on.  (Rank 64, 4 adapters in
+// runs, K 4096: 4000 x 4096 43 us, 55 the other way; 1000 x 16384 54, 59; 2000 x 4096 48, 42; 4000 x 1024 35, 31.)
+constexpr int64_t kManyOutputs = 12 << 20;
+int splits_of(int64_t M, int64_t K, int rank)
 {
     if (M <= kFewRows)
         return (int)std::min<int64_t>(8, std::max<int64_t>(1, K / 512));
@@ -949,8 +952,10 @@ int splits_of(int64_t M, int64_t K)
     int best = 1;
     double least = INFINITY;
     for (int s = 1; s <= 16 && (s == 1 || boxes / s >= 4); ++s) {
-        // rounds of blocks, each as long as its boxes and a fixed cost of about 6
-        const double cost = (double)((tiles * s + kSlots - 1) / kSlots) * ((double)((boxes + s - 1) / s) + 6.0);
+        // rounds of blocks, each as long as its boxes and a fixed cost of about 6; and each part is one more that
+        // the second kernel's blocks add up
+        const double cost = (double)((tiles * s + kSlots - 1) / kSlots) * ((double)((boxes + s - 1) / s) + 6.0) +
+                            s * (0.4 + rank / 32.0);
         if (cost < 0.98 * least)
             least = cost, best = s;
     }
@@ -961,7 +966,7 @@ int splits_of(int64_t M, int64_t K)
 
 size_t adapter_workspace(int64_t M, int64_t, int64_t K, int rank)
 {
-    return (size_t)splits_of(M, K) * M * rank * sizeof(float);
+    return (size_t)splits_of(M, K, rank) * M * rank * sizeof(float);
 }
 
 cudaError_t launch_adapter_linear(const AdapterLinear& p, const DeviceInfo& dev, cudaStream_t s, std::string* why)
@@ -971,7 +976,7 @@ cudaError_t launch_adapter_linear(const AdapterLinear& p, const DeviceInfo& dev,
     if (e != cudaSuccess)
         return e;
     const bool few = p.M <= kFewRows;
-    const int splits = splits_of(p.M, p.K);
+    const int splits = splits_of(p.M, p.K, p.rank);
     const int tile = few ? (int)p.M : TILE;
     const int64_t tiles = (p.M + tile - 1) / tile;
     // columns of a block, by the rounds of two blocks to an SM, each as long as its columns and a fixed cost
@@ -1080,7 +1085,7 @@ cudaError_t launch_adapter_linear(const AdapterLinear& p, const DeviceInfo& dev,
         const cudaError_t r = shrink(type);
         if (r != cudaSuccess)
             return r;
-        if (!few) {
+        if (p.M > kFewRows && p.M * p.N >= kManyOutputs) {
             if (p.out_dtype == CK_OUT_F32)
                 return grow_many(type, std::integral_constant<int, CK_OUT_F32>());
             return p.out_dtype == CK_OUT_F16 ? grow_many(type, std::integral_constant<int, CK_OUT_F16>())

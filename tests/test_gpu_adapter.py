@@ -90,6 +90,33 @@ def test_residual_and_output_types(M, out_dtype):
         ref.assert_within(ck.ck_adapter_linear(x, a, b, index, out_dtype=out_dtype), want, tol, "no scaling")
 
 
+@pytest.mark.parametrize("out_dtype", [BF, F16, F32])
+@pytest.mark.parametrize("dtype", [BF, F16])
+@pytest.mark.parametrize("M,N,K,rank,adapters,order", [
+    (3100, 4104, 16, 8, 3, "runs"), (3333, 4104, 528, 24, 2, "mixed"), (12300, 1032, 64, 128, 4, "runs"),
+    (1600, 8008, 272, 72, 9, "runs"), (1573736, 8, 16, 16, 5, "runs"), (400, 31464, 48, 64, 30, "mixed"),
+])
+def test_many_outputs(M, N, K, rank, adapters, order, dtype, out_dtype):
+    """From some millions of outputs on the second product is another kernel's."""
+    x, a, b, index, scaling = make(M, N, K, rank, adapters, dtype, M, order)
+    want, tol = expected(x, a, b, index, scaling, None, out_dtype)
+    y = ck.ck_adapter_linear(x, a, b, index, scaling=scaling, out_dtype=out_dtype)
+    ref.assert_within(y, want, tol, "y")
+    assert (y[index < 0] == 0).all()
+    del want, tol
+    residual = torch.randn((M, N), device=DEV).to(out_dtype)
+    want, tol = expected(x, a, b, index, scaling, residual, out_dtype)
+    y = ck.ck_adapter_linear(x, a, b, index, scaling=scaling, residual=residual)
+    ref.assert_within(y, want, tol, "with residual")
+    assert torch.equal(y[index < 0], residual[index < 0])
+    index[M // 2] = adapters  # out of range
+    ck.ck_adapter_linear(x, a, b, index, scaling=scaling, residual=residual, y=residual)
+    assert ck.ck_device_error() == 128
+    assert residual[M // 2].isnan().all()
+    y[M // 2] = residual[M // 2]
+    assert torch.equal(residual.nan_to_num(7.0), y.nan_to_num(7.0))
+
+
 @pytest.mark.parametrize("M", [4, 300])
 def test_low_rank_values_beyond_the_types_range(M):
     """x A^T far above fp16's largest number (and far below its smallest), B and scaling that bring it back."""
