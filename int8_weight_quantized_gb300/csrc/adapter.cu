@@ -44,7 +44,7 @@ constexpr uint64_t TIMEOUT_NS = 2000000000ull;
 
 // The rows of a tile by adapter, in groups of up to 16.
 struct Groups {
-    uint32_t key[kFewRows];            // adapter of each row; `adapters`: none, above: out of range
+    alignas(16) uint32_t key[kFewRows];  // adapter of each row; `adapters`: none, above: out of range
     int16_t row[kFewRows];             // rows in order of their adapters
     int16_t begin[kFewRows + 1];       // of each group, in `row`
     int count;
@@ -66,10 +66,15 @@ __device__ __forceinline__ void make_groups(Groups& g, const int32_t* index, int
     int at = m, of_mine = m;  // place in order, and among the rows of its own adapter
     if (!same && m < rows) {
         at = of_mine = 0;
-        for (int n = 0; n < rows; ++n) {
-            const uint32_t k = g.key[n];
-            at += k < key || (k == key && n < m);
-            of_mine += k == key && n < m;
+        for (int n0 = 0; n0 < rows; n0 += 4) {
+            const uint4 four = *reinterpret_cast<const uint4*>(g.key + n0);
+            const uint32_t k[4] = {four.x, four.y, four.z, four.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool same_before = k[i] == key && n0 + i < m;
+                at += (k[i] < key && n0 + i < rows) || same_before;
+                of_mine += same_before;
+            }
         }
     }
     // which places begin a group
@@ -938,6 +943,13 @@ __global__ void __launch_bounds__(MANY_THREADS)
     }
 }
 
+// The most groups that few rows make: a full one for every 16, one that is not for every adapter, for rows without
+// and for those out of range.
+int64_t most_groups(int64_t M, int64_t adapters)
+{
+    return std::min(M, M / 16 + std::min(adapters, M) + 2);
+}
+
 // Parts of K.  Few rows: enough steps for a block's warps; many: blocks that fill the rounds of two to
 // an SM well, a part at least 4 boxes of 64.
 constexpr int64_t kSlots = 304;
@@ -947,7 +959,7 @@ constexpr int64_t kManyOutputs = 12 << 20;
 int splits_of(int64_t M, int64_t K, int rank)
 {
     if (M <= kFewRows)
-        return (int)std::min<int64_t>(8, std::max<int64_t>(1, K / 512));
+        return (int)std::min<int64_t>(M <= 64 ? 8 : 4, std::max<int64_t>(1, K / 512));
     const int64_t tiles = (M + TILE - 1) / TILE, boxes = (K + 63) / 64;
     int best = 1;
     double least = INFINITY;
@@ -1012,8 +1024,8 @@ cudaError_t launch_adapter_linear(const AdapterLinear& p, const DeviceInfo& dev,
                               p, splits, err);
         }
         auto by_rank = [&](auto rt) {
-            return launch_pdl(shrink_few_kernel<E, decltype(rt)::value>, dim3((unsigned)(p.M * splits)), dim3(THREADS), 0, s, p,
-                              splits, err);
+            const unsigned blocks = (unsigned)(most_groups(p.M, p.adapters) * splits);
+            return launch_pdl(shrink_few_kernel<E, decltype(rt)::value>, dim3(blocks), dim3(THREADS), 0, s, p, splits, err);
         };
         if (p.rank <= 8)
             return by_rank(std::integral_constant<int, 1>());
