@@ -41,7 +41,9 @@ namespace {
 constexpr int WARPS = 4;
 constexpr int THREADS = WARPS * 32;
 constexpr int BLOCKS = 32 / WARPS;       // of an SM
-constexpr int DEPTH = 1;                 // 32-byte loads of a lane ahead of its work
+// 32-byte loads of a lane ahead of its work (two: 4096 rows of 64000 117.5 us, 117; 48 of 131071 in pieces 21.2, 21.3;
+// 4096 of fp32 167, 181)
+constexpr int DEPTH = 1;
 constexpr int64_t kLeastPiece = 2048;    // logits
 constexpr int64_t kPieces = 152 * 4;     // as many pieces as blocks fit at once
 constexpr uint32_t FULL = 0xffffffffu;
@@ -637,8 +639,8 @@ cudaError_t launch_token_logprobs(const TokenLogprobs& p, const DeviceInfo&, cud
     auto run = [&](auto type, auto top) {
         constexpr int TYPE = decltype(type)::value;
         constexpr bool TOP = decltype(top)::value;
-        cudaError_t r = launch_pdl(piece_kernel<TYPE, TOP>, dim3((unsigned)(p.rows * pieces)), dim3(THREADS), 0, s, p, pieces,
-                                   piece, err);
+        const dim3 blocks((unsigned)(p.rows * pieces));
+        cudaError_t r = launch_pdl(piece_kernel<TYPE, TOP>, blocks, dim3(THREADS), 0, s, p, pieces, piece, err);
         if (r == cudaSuccess && pieces > 1)
             r = launch_pdl(join_kernel<TYPE, TOP>, dim3((unsigned)p.rows), dim3(THREADS), 0, s, p, pieces, err);
         return r;

@@ -238,7 +238,8 @@ fp32 log probabilities `top` and int32 `index` [rows, top] of the likeliest toke
 def ck_token_logprobs(logits, tokens=None, top=0, scale=1.0, out=None, ws=None, stream=None):
     """Log probabilities of tokens int32 [rows] (negative: none, 0) under softmax(scale * logits), logits
     [rows, vocab] (bf16, fp16 or fp32; rows may be strided), with each row's entropy, log of the
-    softmax's sum and `top` likeliest tokens.  Returns a TokenLogprobs, `out` itself where it is given."""
+    softmax's sum and `top` likeliest tokens.  Returns a TokenLogprobs, `out` itself where it is given (new ones
+    share one allocation)."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return ck_token_logprobs(logits, tokens, top, scale, out, ws)
