@@ -13,7 +13,7 @@
 //               the order O_0 += P_0 V_j, S_0 = Q_0 K_{j+1}, O_1 += P_1 V_j, S_1 = Q_1 K_{j+1};
 //   warps 1-3   copies: rows of pages of a multiple of 8 by TMA; rows of other pages, and those of a prefix's
 //               last tile, by 16-byte asynchronous copies into the same swizzled layout; int8 rows as raw
-//               codes into their place in the ring, from where they are widened in place;
+//               codes through a small ring, each lane widening what it copied itself;
 //   warps 4-11  softmax, a warpgroup for each query tile, one thread per row, as in attention.cu: the
 //               weights go back over S as the 16-bit operand P of the second product, the row's
 //               reference trails its maximum by up to 2^8.
@@ -58,13 +58,15 @@ struct Cfg {
     static constexpr uint32_t BOX_BYTES = BM * 128;             // 128 rows of 64 values
     static constexpr uint32_t TILE_BYTES = DIM / 64 * BOX_BYTES;  // a Q, K or V tile
     static constexpr int UNITS = DIM == 128 ? (INT8 ? 4 : 5) : 10;  // ring of K_0, V_0, K_1, V_1, ..
-    // Key tiles whose scales are kept: those of tile m come with K_m, for which the place of unit 2 m - UNITS
-    // has to be free, by when the weights of tile m - UNITS / 2 - 1 have been used.
-    static constexpr int SCALES = UNITS / 2 + 1;
+    // int8: raw codes on their way, of each copying warp: batches of 4 instructions of 512 bytes
+    static constexpr int BATCH = 4, BATCHES = 4;
+    static constexpr size_t RAW_BYTES = INT8 ? (size_t)LOADERS * BATCHES * BATCH * 512 : 0;
+    // Key tiles whose scales are kept: those of tile m come with K_m's codes, at most a tile before K_m has a place
+    // in the ring, for which that of unit 2 m - UNITS has to be free.
+    static constexpr int SCALES = UNITS / 2 + 2;
     static constexpr size_t SCALE_BYTES = INT8 ? 2 * SCALES * BM * 4 : 0;
-    static_assert(UNITS % 2 == 0 || !INT8, "scales");
     static constexpr size_t STATE = 512;
-    static constexpr size_t SMEM = 1024 + (2 + UNITS) * (size_t)TILE_BYTES + SCALE_BYTES + STATE;
+    static constexpr size_t SMEM = 1024 + (2 + UNITS) * (size_t)TILE_BYTES + RAW_BYTES + SCALE_BYTES + STATE;
     static_assert(SMEM <= 232448, "shared memory budget");
 };
 
@@ -178,7 +180,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* s_q = smem;
     uint8_t* s_ring = s_q + 2 * C::TILE_BYTES;
-    float* s_kscale = reinterpret_cast<float*>(s_ring + UNITS * C::TILE_BYTES);  // int8: [SCALES][BM] of K, of V
+    uint8_t* s_raw = s_ring + UNITS * C::TILE_BYTES;                             // int8
+    float* s_kscale = reinterpret_cast<float*>(s_raw + C::RAW_BYTES);            // [SCALES][BM] of K, of V
     float* s_vscale = s_kscale + (INT8 ? C::SCALES * BM : 0);
     uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(s_kscale) + C::SCALE_BYTES);
     uint64_t* q_full = bars;             // [2]
@@ -187,12 +190,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint64_t* p_full = bars + 6;         // [2] P_t is written
     uint64_t* o_full = bars + 8;         // [2] O_t is final
     uint64_t* drain = bars + 10;
-    uint64_t* full = bars + 11;          // [UNITS]
+    uint64_t* start = bars + 11;         // s_start is there
+    uint64_t* full = bars + 12;          // [UNITS]
     uint64_t* empty = full + UNITS;      // [UNITS]
     int64_t* s_start = reinterpret_cast<int64_t*>(empty + UNITS);  // where the block begins
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_start + 5);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    static_assert((11 + 2 * UNITS + 5) * 8 + 8 <= C::STATE, "barriers");
+    static_assert((12 + 2 * UNITS + 5) * 8 + 8 <= C::STATE, "barriers");
 
     const int warp = __shfl_sync(FULL, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (warp == 0 && lane == 0) {
@@ -204,6 +208,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(&o_full[t], 1);
         }
         mbar_init(drain, 1);
+        mbar_init(start, 1);
         for (int s = 0; s < UNITS; ++s) {
             mbar_init(&full[s], LOADERS);
             mbar_init(&empty[s], 1);
@@ -221,62 +226,68 @@ __global__ void __launch_bounds__(THREADS, 1)
         tmem_relinquish();
     }
     __syncwarp();
-    griddep_wait();
-    griddep_launch_dependents();
-    const PrefixWork& work = a.work;
-    if (warp == 1) {
-        // this block's range of tiles
-        int64_t total = 0, t_before = 0, u_before = 0, prefix = 0, t0 = 0, left = 0;
-        const bool bad = work.survey(a.p.batch, &total);
-        if (!bad) {
-            const int64_t blocks = min((int64_t)gridDim.x, total);
-            if (blockIdx.x < blocks) {
-                t0 = blockIdx.x * total / blocks;
-                left = (blockIdx.x + 1) * total / blocks - t0;
-                prefix = work.holds(t0, &t_before, &u_before);
-            }
-        }
-        if (lane == 0) {
-            s_start[0] = left, s_start[1] = prefix, s_start[2] = t0 - t_before, s_start[3] = u_before;
-            if (bad)
-                atomicOr(err, kErrIndex);
-        }
-    } else if (warp == 2 && blockIdx.x == 0) {
-        // lengths out of range (the last kernel gives NaN for them)
-        bool bad = false;
-        for (int64_t i = lane; i < work.shared.count; i += 32) {
-            const int64_t n = __ldg(work.shared.lens + i);
-            bad |= n < 0 || n > work.shared.max_len;
-        }
-        if (bad)
-            atomicOr(err, kErrIndex);
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(FULL, *tmem_slot, 0);
+    const PrefixWork& work = a.work;
+    // Where the block begins, by whole warps, once the work before this kernel is complete.
     Walk at;
-    at.left = s_start[0];
-    const bool any = at.left > 0;
-    if (any) {
-        at.prefix = s_start[1];
-        at.open(work);
-        const int64_t in_prefix = s_start[2], unit = in_prefix / at.of.tiles;
-        at.tile = (int)(in_prefix - unit * at.of.tiles);
-        at.unit = s_start[3] + unit;
-        at.head = (int)(unit / at.of.pairs);
-        at.pair = (int)(unit - (int64_t)at.head * at.of.pairs);
-    }
+    auto begin = [&]() {
+        griddep_wait();
+        griddep_launch_dependents();
+        const bool ok = mbar_wait(start, 0, abort_flag, err, kErrWaitPrefix, TIMEOUT_NS);
+        at.left = __all_sync(FULL, ok) ? s_start[0] : 0;
+        if (at.left > 0) {
+            at.prefix = s_start[1];
+            at.open(work);
+            const int64_t in_prefix = s_start[2], unit = in_prefix / at.of.tiles;
+            at.tile = (int)(in_prefix - unit * at.of.tiles);
+            at.unit = s_start[3] + unit;
+            at.head = (int)(unit / at.of.pairs);
+            at.pair = (int)(unit - (int64_t)at.head * at.of.pairs);
+        }
+    };
     const int per_tile = work.per_tile, group = a.group;
     // sequences of query tile t of a walk's piece
     auto seqs_of = [&](const Walk& of, int t) { return max(0, min(per_tile, of.of.seqs - (2 * of.pair + t) * per_tile)); };
     auto seqs = [&](int t) { return seqs_of(at, t); };
     const KvCache& cache = a.p.cache;
 
-    if (!any) {
-        // nothing to do (fewer tiles than blocks)
-    } else if (warp < 4) {
+    if (warp < 4) {
         setmaxnreg_dec<REGS_LOAD>();
+        if (warp == 1) {
+            // this block's range of tiles
+            griddep_wait();
+            int64_t total = 0, t_before = 0, u_before = 0, prefix = 0, t0 = 0, left = 0;
+            const bool bad = work.survey(a.p.batch, &total);
+            if (!bad) {
+                const int64_t blocks = min((int64_t)gridDim.x, total);
+                if (blockIdx.x < blocks) {
+                    t0 = blockIdx.x * total / blocks;
+                    left = (blockIdx.x + 1) * total / blocks - t0;
+                    prefix = work.holds(t0, &t_before, &u_before);
+                }
+            }
+            if (lane == 0) {
+                s_start[0] = left, s_start[1] = prefix, s_start[2] = t0 - t_before, s_start[3] = u_before;
+                if (bad)
+                    atomicOr(err, kErrIndex);
+                mbar_arrive(start);
+            }
+            __syncwarp();
+        } else if (warp == 2 && blockIdx.x == 0) {
+            // lengths out of range (the last kernel gives NaN for them)
+            griddep_wait();
+            bool bad = false;
+            for (int64_t i = lane; i < work.shared.count; i += 32) {
+                const int64_t n = __ldg(work.shared.lens + i);
+                bad |= n < 0 || n > work.shared.max_len;
+            }
+            if (bad)
+                atomicOr(err, kErrIndex);
+        }
+        begin();
         auto wait_all = [&](uint64_t* bar, uint32_t parity) {
             if (__all_sync(FULL, mbar_try_wait(bar, parity)))
                 return true;
@@ -591,115 +602,95 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 all_landed();
             } else {
-                // The raw codes of a row land where its own last values will be (the second box's row, or with heads of
-                // 64 the first half of its row), so that it is widened in place, by the lanes that copied it; scales go
-                // to the softmax.
-                constexpr uint32_t RAW_AT = DIM == 128 ? C::BOX_BYTES : 0;
-                const uint32_t units = 2 * (uint32_t)at.left;  // K, V, K, V, ..
-                // Lanes of 8 rows' halves at once: chunk c of a row is lane's bits 0, 1 (and 3 with heads of 128), its row among
-                // the instruction's the others, and raw chunks of odd rows lie the other half first: reads and writes
-                // of 8 lanes spread over all banks.
-                auto raw_chunk = [](int r, int c) { return CH == 8 ? c ^ ((r & 1) << 2) : c; };
+                // Raw codes go through a small ring of each warp's own, 16 bytes of an instruction to the lane that
+                // copied them; what is widened needs a place in the ring of tiles, what is copied does not.
+                // Chunk c of a row is lane's bits 0, 1 (and 3 with heads of 128), its row among the instruction's the
+                // others: the writes of 8 lanes spread over all banks.
+                constexpr int BATCH = C::BATCH, SUBS = (TURNS + BATCH - 1) / BATCH;
                 const int my_chunk = CH == 8 ? (lane & 3) | ((lane >> 1) & 4) : lane & 3;
                 const int my_sub = CH == 8 ? ((lane >> 2) & 1) | ((lane >> 3) & 2) : lane >> 2;
-                uint32_t copies = 0, widened = 0;
-                int j = 0;  // tile of the piece that the next copies are of
+                const uint32_t raw = smem_u32(s_raw) + w * (C::BATCHES * BATCH * 512) + lane * 16;
+                const uint32_t batches = 2 * (uint32_t)at.left * SUBS;  // K, V, K, V, ..
+                uint32_t copied = 0, widened = 0;
+                int j = 0, sub = 0;  // of the piece's tiles, of a unit's batches: where the next copies are
+                bool is_k = true;
                 auto copy = [&]() {
-                    const bool is_k = (copies & 1u) == 0;
-                    if (is_k)
-                        look_up(at.tile + j);
-                    const uint32_t dst = smem_u32(s_ring) + copies % UNITS * C::TILE_BYTES;
-                    const uint8_t* base = static_cast<const uint8_t*>(is_k ? cache.k : cache.v) + lane % CH * 16;
-#pragma unroll 2
-                    for (int i = 0; i < TURNS; ++i) {
-                        const int r = (i * LOADERS + w) * RPI + lane / CH, n = i * RPI + lane / CH, h = i * RPI / 32;
-                        const uint32_t row = __shfl_sync(FULL, h ? rows[1] : rows[0], n % 32);
-                        if (r < BM)
-                            cp_async16(dst + RAW_AT + r * 128 + raw_chunk(r, lane % CH) * 16, base + (uint64_t)row * DIM,
-                                       ((h ? oks[1] : oks[0]) >> (n % 32)) & 1u);
-                    }
-                    if (is_k) {
-                        const uint32_t at_tile = copies / 2 % C::SCALES * BM;
+                    if (copied < batches) {
+                        if (is_k && sub == 0) {
+                            look_up(at.tile + j);
+                            const uint32_t at_tile = copied / (2 * SUBS) % C::SCALES * BM;
 #pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            if (row_in_tile(h) >= 0) {
-                                const uint32_t at_row = (at_tile + row_in_tile(h)) * 4;
-                                const bool there = (oks[h] >> lane) & 1u;
-                                if ((bads[h] >> lane) & 1u)  // on a page out of range: NaN
-                                    s_kscale[at_tile + row_in_tile(h)] = NAN;
-                                else
-                                    cp_async_small<4>(smem_u32(s_kscale) + at_row, cache.k_scale + rows[h], there);
-                                cp_async_small<4>(smem_u32(s_vscale) + at_row, cache.v_scale + rows[h], there);
+                            for (int h = 0; h < 2; ++h)
+                                if (row_in_tile(h) >= 0) {
+                                    const uint32_t at_row = (at_tile + row_in_tile(h)) * 4;
+                                    const bool there = (oks[h] >> lane) & 1u;
+                                    if ((bads[h] >> lane) & 1u)  // on a page out of range: NaN
+                                        s_kscale[at_tile + row_in_tile(h)] = NAN;
+                                    else
+                                        cp_async_small<4>(smem_u32(s_kscale) + at_row, cache.k_scale + rows[h], there);
+                                    cp_async_small<4>(smem_u32(s_vscale) + at_row, cache.v_scale + rows[h], there);
+                                }
+                        }
+                        const uint32_t dst = raw + copied % C::BATCHES * (BATCH * 512);
+                        const uint8_t* base = static_cast<const uint8_t*>(is_k ? cache.k : cache.v) + my_chunk * 16;
+#pragma unroll
+                        for (int n = 0; n < BATCH; ++n) {
+                            const int i = sub * BATCH + n, number = i * RPI + my_sub;
+                            const uint32_t row0 = __shfl_sync(FULL, rows[0], number % 32), row1 = __shfl_sync(FULL, rows[1], number % 32);
+                            const bool there = number < 64 && (((number < 32 ? oks[0] : oks[1]) >> (number % 32)) & 1u);
+                            if (i < TURNS)
+                                cp_async16(dst + n * 512, base + (uint64_t)(number < 32 ? row0 : row1) * DIM, there);
+                        }
+                        ++copied;
+                        if (++sub == SUBS) {
+                            sub = 0;
+                            is_k = !is_k;
+                            if (is_k && ++j == at.count()) {
+                                j = 0;
+                                at.next(work);
                             }
+                        }
                     }
                     cp_async_commit();
-                    ++copies;
-                    if (!is_k && ++j == at.count()) {
-                        j = 0;
-                        at.next(work);
-                    }
                 };
-                auto widen = [&]() {
-                    [[maybe_unused]] const bool is_k = (widened & 1u) == 0;
-                    const int slot = widened % UNITS;
-                    switch (copies - widened - 1) {  // copies under way that came after this one's
-                    case 0: cp_async_wait<0>(); break;
-                    case 1: cp_async_wait<1>(); break;
-                    case 2: cp_async_wait<2>(); break;
-                    default: cp_async_wait<3>(); break;
-                    }
-                    __syncwarp();  // codes come from other lanes' copies too
-                    const uint32_t dst = smem_u32(s_ring) + slot * C::TILE_BYTES;
-                    auto rows_as = [&](auto type) {
-                        using X = decltype(type);
-                        constexpr int BATCH = 4;
+                auto widen = [&](auto type, uint32_t dst, int i0) {  // a batch, from instruction i0 of the tile on
+                    using X = decltype(type);
+                    cp_async_wait<C::BATCHES - 2>();
+                    const uint32_t from = raw + widened % C::BATCHES * (BATCH * 512);
+                    uint4 codes[BATCH];
 #pragma unroll
-                        for (int i0 = 0; i0 < TURNS; i0 += BATCH) {
-                            uint4 codes[BATCH];
+                    for (int n = 0; n < BATCH; ++n)
+                        codes[n] = lds128(from + n * 512);
 #pragma unroll
-                            for (int i = i0; i < i0 + BATCH && i < TURNS; ++i) {
-                                const int r = min((i * LOADERS + w) * RPI + my_sub, BM - 1);
-                                codes[i - i0] = lds128(dst + RAW_AT + r * 128 + raw_chunk(r, my_chunk) * 16);
-                            }
-                            __syncwarp();
-#pragma unroll
-                            for (int i = i0; i < i0 + BATCH && i < TURNS; ++i) {
-                                const int r = (i * LOADERS + w) * RPI + my_sub;
-                                const uint4 q = codes[i - i0];
-                                if (r < BM) {
-                                    sts128(dst + chunk_at(r, 2 * my_chunk), make_uint4(code_pair<X>(q.x, 0), code_pair<X>(q.x, 1),
-                                                                                       code_pair<X>(q.y, 0), code_pair<X>(q.y, 1)));
-                                    sts128(dst + chunk_at(r, 2 * my_chunk + 1),
-                                           make_uint4(code_pair<X>(q.z, 0), code_pair<X>(q.z, 1), code_pair<X>(q.w, 0),
-                                                      code_pair<X>(q.w, 1)));
-                                }
-                            }
-                            __syncwarp();
+                    for (int n = 0; n < BATCH; ++n) {
+                        const int i = i0 + n, r = (i * LOADERS + w) * RPI + my_sub;
+                        const uint4 q = codes[n];
+                        if (i < TURNS && r < BM) {
+                            sts128(dst + chunk_at(r, 2 * my_chunk), make_uint4(code_pair<X>(q.x, 0), code_pair<X>(q.x, 1),
+                                                                               code_pair<X>(q.y, 0), code_pair<X>(q.y, 1)));
+                            sts128(dst + chunk_at(r, 2 * my_chunk + 1), make_uint4(code_pair<X>(q.z, 0), code_pair<X>(q.z, 1),
+                                                                                   code_pair<X>(q.w, 0), code_pair<X>(q.w, 1)));
                         }
-                    };
-                    if (std::is_same<E, PV>::value || is_k)
-                        rows_as(E());
-                    else
-                        rows_as(PV());
-                    landed(&full[slot]);
+                    }
                     ++widened;
+                    copy();
                 };
-                while (ok && widened < units) {
-                    // copies as far ahead as there is room
-                    while (ok && copies < units && copies - widened < (uint32_t)min(UNITS, 4)) {
-                        uint64_t* bar = &empty[copies % UNITS];
-                        const uint32_t parity = (copies / UNITS + 1) & 1u;
-                        if (!__all_sync(FULL, mbar_test_wait(bar, parity))) {
-                            if (copies > widened)
-                                break;
-                            ok = wait_all(bar, parity);
-                            if (!ok)
-                                break;
-                        }
-                        copy();
-                    }
-                    if (ok)
-                        widen();
+#pragma unroll
+                for (int i = 0; i < C::BATCHES - 1; ++i)
+                    copy();
+                for (; ok && widened < batches; ++uses) {
+                    const int slot = uses % UNITS;
+                    ok = wait_all(&empty[slot], (uses / UNITS + 1) & 1u);
+                    if (!ok)
+                        break;
+                    const uint32_t dst = smem_u32(s_ring) + slot * C::TILE_BYTES;
+#pragma unroll 1
+                    for (int i0 = 0; i0 < SUBS * BATCH; i0 += BATCH)
+                        if (std::is_same<E, PV>::value || (uses & 1u) == 0)
+                            widen(E(), dst, i0);
+                        else
+                            widen(PV(), dst, i0);
+                    landed(&full[slot]);
                 }
                 cp_async_wait<0>();
             }
@@ -719,18 +710,18 @@ __global__ void __launch_bounds__(THREADS, 1)
         const float c = a.c;
         uint32_t phase = 0, o_phase = 0, k_tiles = 0;
         bool ok = true;  // once a wait has given up, the remaining rows become NaN
-        // The first time round the steps below run without a tile, for the instruction cache's sake, while
-        // the first tile is on its way: what they find is let go.  (Its first pass over a tile took 5 us, the
-        // next 0.7.)
+        // The first time round the steps below run without a tile, for the instruction cache's sake, while the
+        // work before this kernel ends and the first tile is on its way: what they find is let go.  (Its first
+        // pass over a tile took 5 us, the next 0.7.)
         bool dry = true;
-        for (; at.left > 0;) {
+        for (;;) {
+            if (!dry && at.left <= 0)
+                break;
             const int count = dry ? 1 : at.count();
-            const int rows = seqs(t) * group;
+            const int rows = dry ? 1 : seqs(t) * group;
             if (rows == 0) {
-                k_tiles += dry ? 0 : count;
-                if (!dry)
-                    at.next(work);
-                dry = false;
+                k_tiles += count;
+                at.next(work);
                 continue;
             }
             float m = -INFINITY;  // what the row's sums are relative to, in units of scores
@@ -744,7 +735,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     phase ^= 1u;
                 }
                 tc_fence_after();
-                const int keys = at.of.keys - (at.tile + j) * BM;  // of this tile and after it
+                const int keys = dry ? BM : at.of.keys - (at.tile + j) * BM;  // of this tile and after it
                 uint32_t sr[4][32];
                 float tops[4];
 #pragma unroll
@@ -860,6 +851,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             if (dry) {
                 dry = false;
+                begin();
                 continue;
             }
             // ---- the piece
