@@ -607,6 +607,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 // Chunk c of a row is lane's bits 0, 1 (and 3 with heads of 128), its row among the instruction's the
                 // others: the writes of 8 lanes spread over all banks.
                 constexpr int BATCH = C::BATCH, SUBS = (TURNS + BATCH - 1) / BATCH;
+                static_assert(32 % (BATCH * RPI) == 0, "a batch's rows are looked up by one register");
                 const int my_chunk = CH == 8 ? (lane & 3) | ((lane >> 1) & 4) : lane & 3;
                 const int my_sub = CH == 8 ? ((lane >> 2) & 1) | ((lane >> 3) & 2) : lane >> 2;
                 const uint32_t raw = smem_u32(s_raw) + w * (C::BATCHES * BATCH * 512) + lane * 16;
@@ -633,14 +634,19 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
                         const uint32_t dst = raw + copied % C::BATCHES * (BATCH * 512);
                         const uint8_t* base = static_cast<const uint8_t*>(is_k ? cache.k : cache.v) + my_chunk * 16;
+                        uint32_t row[BATCH];
+                        uint32_t there = 0;
 #pragma unroll
-                        for (int n = 0; n < BATCH; ++n) {
-                            const int i = sub * BATCH + n, number = i * RPI + my_sub;
-                            const uint32_t row0 = __shfl_sync(FULL, rows[0], number % 32), row1 = __shfl_sync(FULL, rows[1], number % 32);
-                            const bool there = number < 64 && (((number < 32 ? oks[0] : oks[1]) >> (number % 32)) & 1u);
-                            if (i < TURNS)
-                                cp_async16(dst + n * 512, base + (uint64_t)(number < 32 ? row0 : row1) * DIM, there);
+                        for (int n = 0; n < BATCH; ++n) {  // (number / 32 is the same for a batch)
+                            const int number = (sub * BATCH + n) * RPI + my_sub;
+                            const bool second = sub * BATCH * RPI >= 32;
+                            row[n] = __shfl_sync(FULL, second ? rows[1] : rows[0], number % 32);
+                            there |= (((second ? oks[1] : oks[0]) >> (number % 32)) & 1u) << n;
                         }
+#pragma unroll
+                        for (int n = 0; n < BATCH; ++n)
+                            if (sub * BATCH + n < TURNS)
+                                cp_async16(dst + n * 512, base + (uint64_t)row[n] * DIM, (there >> n) & 1u);
                         ++copied;
                         if (++sub == SUBS) {
                             sub = 0;
