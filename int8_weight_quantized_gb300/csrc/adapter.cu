@@ -628,7 +628,7 @@ __global__ void __launch_bounds__(MANY_THREADS)
     __shared__ uint32_t key[TILE];
     __shared__ uint32_t list[MOST_ADAPTERS];
     __shared__ float factors[TILE];
-    __shared__ uint64_t bars[2 * BOX_STAGES + 2 * B_STAGES + 2 * SUMS + 3];
+    __shared__ uint64_t bars[3 * BOX_STAGES + 2 * B_STAGES + 2 * SUMS + 2];
     __shared__ int found[4];
     __shared__ uint32_t tmem_slot;
     __shared__ int aborted;
@@ -637,7 +637,7 @@ __global__ void __launch_bounds__(MANY_THREADS)
     uint8_t* s_h = s_box + BOX_STAGES * X_BYTES;
     uint8_t* s_b = s_h + kb * X_BYTES;
     uint64_t *box_full = bars, *box_empty = box_full + BOX_STAGES, *b_full = box_empty + BOX_STAGES, *b_empty = b_full + B_STAGES,
-             *done = b_empty + B_STAGES, *taken = done + SUMS, *h_full = taken + SUMS, *box_ready = h_full + 1, *drain = box_ready + 1;
+             *done = b_empty + B_STAGES, *taken = done + SUMS, *h_full = taken + SUMS, *drain = h_full + 1, *box_ready = drain + 1;
     volatile int* abort_flag = &aborted;
     const int warp = __shfl_sync(FULL, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     constexpr uint32_t TMEM = SUMS * W < 32 ? 32 : SUMS * W;
@@ -645,6 +645,7 @@ __global__ void __launch_bounds__(MANY_THREADS)
         for (int i = 0; i < BOX_STAGES; ++i) {
             mbar_init(&box_full[i], 1);
             mbar_init(&box_empty[i], 1);
+            mbar_init(&box_ready[i], 4);
         }
         for (int i = 0; i < B_STAGES; ++i) {
             mbar_init(&b_full[i], 1);
@@ -655,7 +656,6 @@ __global__ void __launch_bounds__(MANY_THREADS)
             mbar_init(&taken[i], 4);
         }
         mbar_init(h_full, 4);
-        mbar_init(box_ready, 4);
         mbar_init(drain, 1);
         aborted = 0;
         fence_mbar_init();
@@ -905,13 +905,15 @@ __global__ void __launch_bounds__(MANY_THREADS)
                     mbar_arrive(&taken[d]);
                 __syncwarp();
             }
-            // the box, once all four warps have left their rows
+            // The box, once all four warps have left their rows.  (A barrier of each place: a warp that is ahead arrives
+            // for the next box, and meets this place's again only after its box has gone out.)
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(box_ready);
+                mbar_arrive(&box_ready[s]);
             if (warp == 2) {
-                const bool all = mbar_wait(box_ready, (uint32_t)i & 1u, abort_flag, err, kErrWaitAdapter, TIMEOUT_NS);
+                const bool all = mbar_wait(&box_ready[s], (uint32_t)(i / BOX_STAGES) & 1u, abort_flag, err, kErrWaitAdapter,
+                                           TIMEOUT_NS);
                 if (lane == 0 && all) {
                     tma_store_2d(&tmY, s_box + s * X_BYTES, (int32_t)(box0 + i) * W, (int32_t)first);
                     bulk_commit_group();
