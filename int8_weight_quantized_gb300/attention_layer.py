@@ -5,7 +5,8 @@ by one.
 
 Prompt: INT8 QKV projection, norm and rotation into the paged cache, attention over the prompt,
 INT8 output projection with the residual.  Each further token: the same with 4-bit projections
-and attention over the cache.  Random weights and activations; prints the time of each part and
+and attention over the cache.  A prompt's next chunk (`resume`): the same over the cached tokens read
+back, with low-rank adapters beside the QKV projection where there are some.  Random weights and activations; prints the time of each part and
 how far the last token's attention over the cache is from the same token's over the whole
 sequence at once.
 """
@@ -68,6 +69,26 @@ class AttentionLayer:
         a = ck.ck_attention(q, k, v, cu.to(torch.int32), window=self.window, sinks=self.sinks)
         w8, w_scale, _, _ = self.projections["out"]
         return ck.ck_int8_linear(a.view(x.shape[0], -1), w8, w_scale, residual=x)
+
+    def resume(self, x, lengths, cached, adapters=None):
+        """The next chunk of prompts whose first `cached` tokens (a list) are in the cache: x [tokens, hidden] bf16, `lengths`
+        tokens of each -> y [tokens, hidden].  adapters: (a, b, index, scaling) of the QKV projection, index one for each
+        token."""
+        w8, w_scale, _, _ = self.projections["qkv"]
+        qkv = ck.ck_int8_linear(x, w8, w_scale)
+        if adapters is not None:
+            a, b, index, scaling = adapters
+            ck.ck_adapter_linear(x, a, b, index, scaling=scaling, residual=qkv, y=qkv)
+        n, before = torch.tensor(lengths, device=x.device), torch.tensor(cached, device=x.device)
+        cu_q = torch.cat([n.new_zeros(1), n.cumsum(0)])
+        cu_k = torch.cat([n.new_zeros(1), (n + before).cumsum(0)]).to(torch.int32)
+        sequence = torch.repeat_interleave(torch.arange(len(lengths), device=x.device), n)
+        positions = torch.arange(x.shape[0], device=x.device) - cu_q[sequence] + before[sequence]
+        q, _ = self.rotate(qkv, sequence, positions, False)
+        k, v = ck.ck_cache_read(self.cache, self.block_table[:len(lengths)], cu_k, sum(lengths) + sum(cached), dtype=q.dtype)
+        o = ck.ck_attention(q, k, v, cu_q.to(torch.int32), cu_k, window=self.window, sinks=self.sinks)
+        w8, w_scale, _, _ = self.projections["out"]
+        return ck.ck_int8_linear(o.view(x.shape[0], -1), w8, w_scale, residual=x)
 
     def step(self, x, lengths):
         """x [batch, hidden] bf16, one new token of each sequence; lengths [batch] (int64) cached

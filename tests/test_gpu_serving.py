@@ -1,0 +1,146 @@
+"""The operators for many requests of one model as they are used together: requests with adapters of
+their own behind a shared prompt, its keys and values stored once."""
+import pytest
+import torch
+
+import int8_weight_quantized_gb300 as ck
+from int8_weight_quantized_gb300.attention_layer import AttentionLayer
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF = torch.bfloat16
+
+
+@pytest.mark.parametrize("cache", [BF, torch.int8])
+def test_a_prompt_in_two_chunks(cache):
+    """The second chunk over the first one's cached tokens, and the whole prompt at once."""
+    layers = [AttentionLayer(256, 4, 2, 64, 400, batch=2, page_size=16, cache_dtype=cache, seed=1) for _ in range(2)]
+    g = torch.Generator(device=DEV)
+    g.manual_seed(2)
+    lengths, first = [300, 170], [130, 33]
+    parts = [torch.randn((n, 256), generator=g, device=DEV).to(BF) for n in lengths]
+    whole = layers[0].prompt(torch.cat(parts), lengths)
+    layers[1].prompt(torch.cat([p[:n] for p, n in zip(parts, first)]), first)
+    rest = [n - m for n, m in zip(lengths, first)]
+    y = layers[1].resume(torch.cat([p[m:] for p, m in zip(parts, first)]), rest, first)
+    want = torch.cat([whole[first[0]:300], whole[300 + first[1]:]])
+    # (16-bit rows come back as they went in: the same keys in the same tiles but for the chunk's own start)
+    off = (y.float() - want.float()).norm() / want.float().norm()
+    assert off < (4e-3 if cache == BF else 2e-2)
+
+
+@pytest.mark.parametrize("kind", [BF, torch.int8])
+@pytest.mark.parametrize("batch", [3, 48])
+def test_requests_with_adapters_behind_a_shared_prompt(batch, kind):
+    hidden, hq, hkv, d, page, prefix, vocab = 256, 8, 2, 64, 16, 1600, 4096
+    g = torch.Generator(device=DEV)
+    g.manual_seed(batch)
+
+    def rand(*shape, std=1.0):
+        return torch.randn(shape, generator=g, device=DEV) * std
+
+    width = (hq + 2 * hkv) * d
+    W = rand(width, hidden, std=hidden ** -0.5)
+    scale = W.abs().amax(1) / 127
+    w8 = (W / scale[:, None]).round().to(torch.int8)
+    w4, w4_scale = ck.ck_int4_prepare_weight(W)
+    head8 = (rand(vocab, hq * d, std=30)).round().clamp(-127, 127).to(torch.int8)
+    head_scale = torch.full((vocab,), (hq * d) ** -0.5 / 8, device=DEV)
+    a, b = rand(5, 16, hidden, std=hidden ** -0.5).to(BF), rand(5, width, 16, std=0.1).to(BF)
+    scaling = torch.rand(5, generator=g, device=DEV)
+    index = torch.arange(batch, device=DEV, dtype=torch.int32) % 6 - 1  # one in six without an adapter
+    table = ck.rope_table(prefix + 64, d)
+    pages = prefix // page + 2 * batch
+    cache = ck.KVCache.empty(pages, page, hkv, d, dtype=kind)
+    pool = torch.randperm(pages, generator=g, device=DEV).to(torch.int32)
+    ptable, own = pool[:prefix // page][None].contiguous(), pool[prefix // page:].view(batch, 2).contiguous()
+    both = torch.cat([ptable.expand(batch, -1), own], 1).contiguous()
+
+    def slots(t, sequence, j):
+        return t[sequence, j // page].long() * page + j % page
+
+    # the shared prompt, once
+    x = rand(prefix, hidden).to(BF)
+    j = torch.arange(prefix, device=DEV)
+    ck.ck_qk_norm_rope(ck.ck_int8_linear(x, w8, scale), j.to(torch.int32), table, hq, hkv, cache=cache,
+                       slots=slots(ptable, torch.zeros_like(j), j))
+    plens = torch.tensor([prefix], dtype=torch.int32, device=DEV)
+    cu = torch.tensor([0, batch], dtype=torch.int32, device=DEV)
+    everyone = torch.arange(batch, device=DEV)
+    outs, queries = [], []
+    for step in range(20):
+        x = rand(batch, hidden).to(BF)
+        qkv = ck.ck_int4_linear(x, w4, w4_scale)
+        plain = qkv.clone()
+        ck.ck_adapter_linear(x, a, b, index, scaling=scaling, residual=qkv, y=qkv)
+        assert torch.equal(qkv[index < 0], plain[index < 0]) and not torch.equal(qkv, plain)
+        at = torch.full((batch,), step, device=DEV)
+        q, _ = ck.ck_qk_norm_rope(qkv, (at + prefix).to(torch.int32), table, hq, hkv, cache=cache,
+                                  slots=slots(own, everyone, at))
+        lens = (at + 1).to(torch.int32)
+        out, lse = ck.ck_prefix_attention(q, cache, ptable, plens, cu, own, lens, return_lse=True)
+        # the same keys through one table
+        want, want_lse = ck.ck_paged_attention(q, cache, both, lens + prefix, return_lse=True)
+        assert (out.float() - want.float()).abs().max() <= 6 * 2.0 ** -8 * want.float().abs().max()
+        assert (lse - want_lse).abs().max() <= 1e-4 * (1 + want_lse.abs().max())
+        outs.append(out)
+        queries.append(q)
+    # the last token of each request over its keys read back
+    cu_k = (torch.arange(batch + 1, device=DEV) * (prefix + 20)).to(torch.int32)
+    k, v = ck.ck_cache_read(cache, both, cu_k, batch * (prefix + 20), dtype=BF)
+    want = ck.ck_attention(queries[-1], k, v, torch.arange(batch + 1, device=DEV, dtype=torch.int32), cu_k)
+    # (int8 rows rounded to bf16 there: 2^-9 of each value on average less)
+    assert (outs[-1].float() - want.float()).abs().max() <= 10 * 2.0 ** -8 * want.float().abs().max()
+    # what the requests would say next
+    logits = ck.ck_int8_linear(outs[-1].view(batch, -1), head8, head_scale, out_dtype=torch.float32)
+    best = ck.ck_token_logprobs(logits, top=4)
+    said = best.index[:, 0].contiguous()
+    r = ck.ck_token_logprobs(logits, said, top=4)
+    assert torch.equal(r.logprob, r.top[:, 0])
+    p = torch.log_softmax(logits.double(), -1)
+    assert (r.logprob.double() - p.gather(1, said.long()[:, None])[:, 0]).abs().max() < 1e-5
+    assert (r.entropy.double() + (p.exp() * p).sum(-1)).abs().max() < 1e-4
+    assert torch.equal(said, logits.argmax(-1).to(torch.int32))
+    assert ck.ck_device_error() == 0
+
+
+def test_a_step_in_a_graph_beside_a_stream():
+    """The four operators of a step captured together and replayed on new inputs, while another stream runs the
+    same on its own; both equal calls one by one."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(3)
+    batch, hq, hkv, d, page, prefix = 40, 8, 2, 128, 16, 2048
+    pages = prefix // page + 2 * batch
+    cache = ck.KVCache(*[torch.randn((pages, hkv, page, d), generator=g, device=DEV).to(BF) for _ in range(2)])
+    table = torch.randperm(pages, generator=g, device=DEV).to(torch.int32)
+    ptable, own = table[:prefix // page][None].contiguous(), table[prefix // page:].view(batch, 2).contiguous()
+    plens = torch.tensor([prefix - 5], dtype=torch.int32, device=DEV)
+    cu = torch.tensor([0, batch], dtype=torch.int32, device=DEV)
+    lens = (torch.arange(batch, device=DEV) % 32 + 1).to(torch.int32)
+    a = (torch.randn((3, 16, hq * d), generator=g, device=DEV) * 0.05).to(BF)
+    b = (torch.randn((3, 512, 16), generator=g, device=DEV)).to(BF)
+    index = (torch.arange(batch, device=DEV) % 3).to(torch.int32)
+    cu_k = (torch.arange(batch + 1, device=DEV) * 20).to(torch.int32)
+
+    def step(q):
+        out, lse = ck.ck_prefix_attention(q, cache, ptable, plens, cu, own, lens, return_lse=True)
+        y = ck.ck_adapter_linear(out.view(batch, -1), a, b, index, out_dtype=torch.float32)
+        return [out, lse, y, *ck.ck_token_logprobs(y, index, top=3), *ck.ck_cache_read(cache, own, cu_k, batch * 20)]
+
+    qs = [torch.randn((batch, hq, d), generator=g, device=DEV).to(BF) for _ in range(3)]
+    want = [step(q) for q in qs]
+    q = qs[0].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step(q)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for i in (1, 2, 0):
+        q.copy_(qs[i])
+        graph.replay()
+        with torch.cuda.stream(side):
+            other = step(qs[(i + 1) % 3])
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(captured, want[i]))
+        assert all(torch.equal(x, y) for x, y in zip(other, want[(i + 1) % 3]))
+    assert ck.ck_device_error() == 0
