@@ -348,8 +348,8 @@ int ck_paged_attention(const void *q, int64_t q_stride, const ck_kv_cache_t *cac
  *   cu_prefix:   int32 [num_prefixes + 1], ascending: sequences cu[i] .. cu[i + 1] - 1 stand behind
  *                prefix i, those before cu[0] and from cu[num_prefixes] on behind none.  Bounds that
  *                descend or leave 0 .. batch: every output is NaN.
- *   block_table, seq_lens: each sequence's own tokens (its new one is the last of them), which need
- *                not begin on a page of their own length: token t of these is at page T[t / page_size].
+ *   block_table, seq_lens: each sequence's own tokens, the new one the last of them; token t of these is in
+ *                page block_table[b, t / page_size], whatever the prefix's length.
  * The rest as for ck_paged_attention; no window.  A sequence without any key gives zeros (lse -inf).
  * workspace: ck_prefix_attention_workspace_size(batch, q_heads, kv_heads, head_dim, num_prefixes,
  *              max_prefix_blocks * page_size, max_blocks * page_size) bytes. */
@@ -426,7 +426,9 @@ int ck_int4_linear(const void *x, const uint32_t *w4, const void *w_scale, const
  *   scaling:  fp32 [num_adapters] or NULL (1).
  *   residual: [M,N] of out_dtype, the shared projection's output, or NULL (0); may be y.
  *   y:        [M,N] of out_dtype (a ck_dtype_t), written.
- * K a multiple of 16, N of 8, rank of 8 up to 128, M up to 16777216.  Sums are fp32.
+ * K a multiple of 16, N and rank of 8, rank up to 128, M up to 16777216, num_adapters * rank below 2^31.  Sums
+ * are fp32; x A_i^T is rounded to dtype once.  Rows of one adapter are best beside one another where there are
+ * more than 256: a tile of 128 rows passes by once for each of its adapters.
  * workspace: ck_adapter_linear_workspace_size(M, N, K, rank) bytes; its content does not matter. */
 size_t ck_adapter_linear_workspace_size(int64_t M, int64_t N, int64_t K, int64_t rank);
 int ck_adapter_linear(const void *x, const void *a, const void *b, const int32_t *index, const float *scaling,
@@ -454,9 +456,10 @@ int ck_token_logprobs(const void *logits, int64_t stride, const int32_t *tokens,
  * the library counts the kernels it enqueues from the calling host thread, by kind
  * (0 = activation quantize, 1 = int8 -> bf16 operand widening, 2 = GEMM with fused
  * epilogue, 3 = norm and rotation, 4 = attention, 5 = 4-bit linear, 6 = low-rank
- * adapters, 7 = log probabilities, 8 = cache rows read back).  With with_events != 0 it also brackets each launch with two CUDA events on
- * the kernel's own stream (the kernels are unchanged, but the events separate
- * consecutive kernels, so launch overlap between them is lost while timing).
+ * adapters, 7 = log probabilities, 8 = cache rows read back).  With with_events != 0 it
+ * also brackets each launch with two CUDA events on the kernel's own stream (the kernels
+ * are unchanged, but the events separate consecutive kernels, so launch overlap between
+ * them is lost while timing).
  * ck_profile_end() waits for the events and fills, for each kind k < nkinds,
  * ms[k] = summed device milliseconds (0 without events) and launches[k] = number of
  * kernel launches.  Both arrays are host memory owned by the caller. */

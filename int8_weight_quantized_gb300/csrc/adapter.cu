@@ -12,12 +12,21 @@
 //     a step is the same permutation on both sides), and add their sums up in shared memory.
 //   many rows: a block takes 128 rows and a part of K on the fifth-generation tensor core, x and A by TMA
 //     through a ring, h in tensor memory; once for every adapter that some of its rows have.
-//   the second product: a warp takes a group and 32 columns at a time; columns are dealt to the
-//     instruction's tiles so that a lane holds 8 neighbouring ones, and residual and y pass in 16 bytes.
+//   the second product, few outputs: a warp takes a group and 32 columns at a time; columns are dealt to
+//     the instruction's tiles so that a lane holds 8 neighbouring ones, and residual and y pass in 16 bytes.
+//   many outputs: a block takes 128 rows and some boxes of columns on the fifth-generation tensor core, the
+//     boxes in and out by TMA; once for every adapter that some of its rows have.
 //
-// Rounding to fewer bits: h once, to the type of B, as the matrix instruction takes it; in fp16 relative
-// to the power of two of the row's largest value, so that it neither overflows nor vanishes where the
-// result does not.
+// Measured (GB300, bf16): 1 row of 4096 x 4096, rank 16, 7.6 to 8.5 us, two launches and their latencies; 48
+// rows of 24 mixed adapters, 28672 x 5376, rank 32, 23.4 us (54 MB of A, B, residual and y, 2.3 TB/s: two launches
+// of a few steps each, latency); 256 rows of 32 adapters, 4096 x 4096, 20; 8000 rows of 4096 x
+// 4096, rank 16 to 64, 50 to 58 us, 3.3 to 3.9 TB/s of x, residual and y (the first product 21 us, 3.1 TB/s, the
+// second 40 us, 3.3 TB/s); 4000 rows 43.  1000 rows of 32 adapters in any order 83 us: rows of one adapter are
+// best beside one another, a tile of 128 rows passes by once for each of its adapters.
+//
+// Rounding to fewer bits: h, to the type of B, as the matrix instruction takes it: once where the outputs have
+// 16 bits, as a sum of two fp16 (22 bits) or three bf16 (24) where they have 32; in fp16 relative to the power
+// of two of the row's largest value, so that it neither overflows nor vanishes where the result does not.
 #include <algorithm>
 #include <cmath>
 #include <string>
@@ -183,7 +192,8 @@ __global__ void __launch_bounds__(THREADS) shrink_few_kernel(const AdapterLinear
 //   warp 0       copies 128 x 64 of x and rank x 64 of A by TMA through the ring;
 //   warp 1       issues the products, one lane; the sums of two adapters have room in tensor memory;
 //   warps 2 - 5  leave the rows of a finished adapter.
-// Measured (GB300): see expand_kernel.
+// Bound: x from HBM; what it reaches less (8000 x 4096: 21 us, 3.1 TB/s) is the 64 bytes of A that come with each
+// 128 of x at rank 64, and blocks that begin and end together (two rounds of two to an SM).
 constexpr int MANY_THREADS = 192;
 constexpr uint32_t X_BYTES = TILE * 128;
 constexpr uint32_t RING_BYTES = 96 * 1024;  // of two blocks on an SM
@@ -446,20 +456,50 @@ struct Eight<CK_OUT_F16> : Eight16<Fp16> {
     static __device__ __forceinline__ Eight load(const void* base, int64_t i) { return {{read(base, i)}}; }
 };
 
+// How many numbers of 16 bits a value of h is the sum of.
+template <class E, int OUT>
+constexpr int PARTS = OUT != CK_OUT_F32 ? 1 : std::is_same<E, Fp16>::value ? 2 : 3;
+
+// Eight values as PARTS words of 16 bits each, the largest part first; put(n, word) takes part n.
+template <class E, int P, class Put>
+__device__ __forceinline__ void in_parts(float (&v)[8], float factor, Put put)
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v[i] *= factor;
+#pragma unroll
+    for (int n = 0; n < P; ++n) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w[i] = E::pack2(v[2 * i], v[2 * i + 1]);
+            if (n + 1 < P) {
+                const float2 f = E::to2(w[i]);
+                // (what is infinite or NaN is so in its first part, and the others 0)
+                v[2 * i] = fabsf(f.x) < INFINITY ? v[2 * i] - f.x : 0.0f;
+                v[2 * i + 1] = fabsf(f.y) < INFINITY ? v[2 * i + 1] - f.y : 0.0f;
+            }
+        }
+        put(n, make_uint4(w[0], w[1], w[2], w[3]));
+    }
+}
+
 // Items are a tile's (group, 32 columns of the block's); a warp takes a run of them, the residual of the
-// next one on its way while it works on one.  h is added up and rounded once for the block, into shared
+// next one on its way while it works on one.  h is added up and rounded for the block, into shared
 // memory; rows are padded so that 8 of them spread over the banks.
 constexpr int kPad = 8;
-__host__ __device__ constexpr int h_bytes(int tile, int rank)
+__host__ __device__ constexpr int h_bytes(int tile, int rank)  // of a part
 {
     return tile * (rank + kPad) * 2;
 }
 
 template <class E, int OUT, int KT>  // KT: steps of 32 of the rank
-__global__ void __launch_bounds__(THREADS, 2) expand_kernel(const AdapterLinear p, int tile, int chunk, int splits)
+__global__ void __launch_bounds__(THREADS, KT * PARTS<E, OUT> >= 8 ? 1 : 2)
+    expand_kernel(const AdapterLinear p, int tile, int chunk, int splits)
 {
     using T = typename E::T;
-    extern __shared__ __align__(16) uint8_t h_smem[];  // [tile][rank + kPad] of T
+    constexpr int P = PARTS<E, OUT>;
+    extern __shared__ __align__(16) uint8_t h_smem[];  // [P][tile][rank + kPad] of T
     __shared__ Groups groups;
     __shared__ float factors[kFewRows];
     const int64_t chunks = (p.N + chunk - 1) / chunk;
@@ -511,9 +551,9 @@ __global__ void __launch_bounds__(THREADS, 2) expand_kernel(const AdapterLinear 
                 factor *= ldexpf(1.0f, e);
             }
             if (in)
-                *reinterpret_cast<uint4*>(h_smem + m * ld + c * 2) =
-                    make_uint4(E::pack2(v[0] * down, v[1] * down), E::pack2(v[2] * down, v[3] * down),
-                               E::pack2(v[4] * down, v[5] * down), E::pack2(v[6] * down, v[7] * down));
+                in_parts<E, P>(v, down, [&](int n, uint4 w) {
+                    *reinterpret_cast<uint4*>(h_smem + (n * tile + m) * ld + c * 2) = w;
+                });
             if (c == 0 && m < rows)
                 factors[m] = factor;
         }
@@ -537,7 +577,7 @@ __global__ void __launch_bounds__(THREADS, 2) expand_kernel(const AdapterLinear 
         bool there[2];
         int64_t at[2];  // of the lane's outputs of step 0
         float factor[2];
-        uint32_t h[KT][2][4];
+        uint32_t h[P][KT][2][4];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             there[r] = g + 8 * r < count;
@@ -545,12 +585,14 @@ __global__ void __launch_bounds__(THREADS, 2) expand_kernel(const AdapterLinear 
             at[r] = (first + m) * p.N + n_first + 8 * t;
             factor[r] = adapter > p.adapters ? NAN : factors[m];
 #pragma unroll
-            for (int k = 0; k < KT; ++k) {
-                uint4 w = make_uint4(0u, 0u, 0u, 0u);
-                if (there[r] && !none && 32 * k + 8 * t < p.rank)
-                    w = *reinterpret_cast<const uint4*>(h_smem + m * ld + (32 * k + 8 * t) * 2);
-                h[k][0][r] = w.x, h[k][0][2 + r] = w.y, h[k][1][r] = w.z, h[k][1][2 + r] = w.w;
-            }
+            for (int n = 0; n < P; ++n)
+#pragma unroll
+                for (int k = 0; k < KT; ++k) {
+                    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                    if (there[r] && !none && 32 * k + 8 * t < p.rank)
+                        w = *reinterpret_cast<const uint4*>(h_smem + (n * tile + m) * ld + (32 * k + 8 * t) * 2);
+                    h[n][k][0][r] = w.x, h[n][k][0][2 + r] = w.y, h[n][k][1][r] = w.z, h[n][k][1][2 + r] = w.w;
+                }
         }
         const T* b = static_cast<const T*>(p.b) + (none ? 0 : ((int64_t)adapter * p.N + n_first) * p.rank) + 8 * t;
         Eight<OUT> next[2] = {};
@@ -579,10 +621,12 @@ __global__ void __launch_bounds__(THREADS, 2) expand_kernel(const AdapterLinear 
                                     : make_uint4(0u, 0u, 0u, 0u);
                     }
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        mma_16816<E>(acc[j], h[k][0], bv[j].x, bv[j].y);
-                        mma_16816<E>(acc[j], h[k][1], bv[j].z, bv[j].w);
-                    }
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int n = P - 1; n >= 0; --n) {
+                            mma_16816<E>(acc[j], h[n][k][0], bv[j].x, bv[j].y);
+                            mma_16816<E>(acc[j], h[n][k][1], bv[j].z, bv[j].w);
+                        }
                 }
             }
 #pragma unroll
@@ -608,14 +652,21 @@ __global__ void __launch_bounds__(THREADS, 2) expand_kernel(const AdapterLinear 
 //   warps 2 - 5  add h up, round it and leave it as the products' first operand; then a thread a row: what
 //                the product of its adapter adds to its row of a box, in shared memory, from where the box
 //                goes out by TMA.
+// Bound: the residual and y, 8000 x 4096 40 us, 3.3 TB/s; a third place for boxes costs the third block of an SM
+// (69 us for the whole call against 58).
 constexpr int MOST_ADAPTERS = TILE;  // of a tile
 constexpr int BOX_STAGES = 2, B_STAGES = 2, SUMS = 2;
 
-template <int OUT>
+template <class E, int OUT>
 struct GrowCfg {
     static constexpr int W = OUT == CK_OUT_F32 ? 32 : 64;  // columns of a box
     // boxes of the residual, of B, of h; kb: boxes of 64 of the rank
-    static constexpr size_t smem(int kb) { return 1024 + BOX_STAGES * X_BYTES + (size_t)kb * (B_STAGES * W * 128 + X_BYTES); }
+    static constexpr size_t smem(int kb)
+    {
+        return 1024 + BOX_STAGES * X_BYTES + (size_t)kb * (B_STAGES * W * 128 + PARTS<E, OUT> * X_BYTES);
+    }
+    // blocks that an SM has room for (some 4 KB each are not counted)
+    static constexpr int64_t blocks(int kb) { return std::min<int64_t>(3, 220 * 1024 / (int64_t)smem(kb)); }
 };
 
 template <class E, int OUT>
@@ -623,7 +674,7 @@ __global__ void __launch_bounds__(MANY_THREADS)
     expand_many_kernel(const __grid_constant__ CUtensorMap tmR, const __grid_constant__ CUtensorMap tmB,
                        const __grid_constant__ CUtensorMap tmY, const AdapterLinear p, int boxes, int splits, unsigned int* err)
 {
-    constexpr int W = GrowCfg<OUT>::W;
+    constexpr int W = GrowCfg<E, OUT>::W, P = PARTS<E, OUT>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint32_t key[TILE];
     __shared__ uint32_t list[MOST_ADAPTERS];
@@ -635,7 +686,7 @@ __global__ void __launch_bounds__(MANY_THREADS)
     const int kb = (p.rank + 63) / 64;  // boxes of 64 of the rank
     uint8_t* s_box = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* s_h = s_box + BOX_STAGES * X_BYTES;
-    uint8_t* s_b = s_h + kb * X_BYTES;
+    uint8_t* s_b = s_h + P * kb * X_BYTES;
     uint64_t *box_full = bars, *box_empty = box_full + BOX_STAGES, *b_full = box_empty + BOX_STAGES, *b_empty = b_full + B_STAGES,
              *done = b_empty + B_STAGES, *taken = done + SUMS, *h_full = taken + SUMS, *drain = h_full + 1, *box_ready = drain + 1;
     volatile int* abort_flag = &aborted;
@@ -707,7 +758,7 @@ __global__ void __launch_bounds__(MANY_THREADS)
     const bool idle = count == 0 && !any_bad && p.residual == p.y;  // in place, without adapters
 
     if (idle) {
-        // the rows stay as they are
+        griddep_wait();  // the rows stay as they are; but this kernel ends after the one before it
     } else if (warp == 0) {
         if (lane == 0) {
             int boxes_sent = 0, parts_sent = 0;
@@ -762,9 +813,10 @@ __global__ void __launch_bounds__(MANY_THREADS)
                 break;
             tc_fence_after();
             if (leader) {
-                for (int k = 0; k < steps; ++k)
-                    mma_ss(tmem + d * W, h_desc + (uint64_t)(k / 4) * (X_BYTES >> 4) + (k % 4) * 2,
-                           b_desc + (uint64_t)(s * kb + k / 4) * (W * 128 >> 4) + (k % 4) * 2, idesc, k > 0);
+                for (int n = P - 1; n >= 0; --n)  // (the smallest part first)
+                    for (int k = 0; k < steps; ++k)
+                        mma_ss(tmem + d * W, h_desc + (uint64_t)(n * kb + k / 4) * (X_BYTES >> 4) + (k % 4) * 2,
+                               b_desc + (uint64_t)(s * kb + k / 4) * (W * 128 >> 4) + (k % 4) * 2, idesc, k > 0 || n + 1 < P);
                 mma_commit(&b_empty[s]);
                 mma_commit(&done[d]);
             }
@@ -812,15 +864,14 @@ __global__ void __launch_bounds__(MANY_THREADS)
             // (beyond the rank, up to the products' last step of 16: zeros)
             if (c < (p.rank + 15) / 16 * 16) {
                 uint8_t* dst = s_h + (c / 64) * X_BYTES + r * 128 + (((c / 8 & 7) ^ (r & 7)) << 4);
-                *reinterpret_cast<uint4*>(dst) =
-                    make_uint4(E::pack2(v[0] * down, v[1] * down), E::pack2(v[2] * down, v[3] * down),
-                               E::pack2(v[4] * down, v[5] * down), E::pack2(v[6] * down, v[7] * down));
+                in_parts<E, P>(v, down, [&](int n, uint4 w) { *reinterpret_cast<uint4*>(dst + n * kb * X_BYTES) = w; });
             }
             if (c == 0)
                 factors[r] = adapter > p.adapters ? NAN : factor;
         }
-        if (lanes * 8 < (p.rank + 15) / 16 * 16 && lane < 32)  // a rank of 8: one lane a row
-            *reinterpret_cast<uint4*>(s_h + row * 128 + ((1 ^ (row & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+        if (lanes * 8 < (p.rank + 15) / 16 * 16)  // a rank of 8: one lane a row
+            for (int n = 0; n < P; ++n)
+                *reinterpret_cast<uint4*>(s_h + n * kb * X_BYTES + row * 128 + ((1 ^ (row & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0)
@@ -1039,7 +1090,7 @@ cudaError_t launch_adapter_linear(const AdapterLinear& p, const DeviceInfo& dev,
     };
     auto grow = [&](auto type, auto out) {
         using E = decltype(type);
-        constexpr int OUT = decltype(out)::value;
+        constexpr int OUT = decltype(out)::value, P = PARTS<E, OUT>;
         auto by_rank = [&](auto kt) {
             constexpr auto kernel = expand_kernel<E, OUT, decltype(kt)::value>;
             static ContextCache<int> cache;
@@ -1047,11 +1098,11 @@ cudaError_t launch_adapter_linear(const AdapterLinear& p, const DeviceInfo& dev,
             const cudaError_t r = cache.get(&done, [&](int* d) {
                 *d = 1;
                 return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                            h_bytes(kFewRows, 32 * decltype(kt)::value));
+                                            P * h_bytes(kFewRows, 32 * decltype(kt)::value));
             });
             if (r != cudaSuccess)
                 return r;
-            return launch_pdl(kernel, dim3(expand), dim3(THREADS), (size_t)h_bytes(tile, p.rank), s, p, tile, (int)chunk,
+            return launch_pdl(kernel, dim3(expand), dim3(THREADS), (size_t)P * h_bytes(tile, p.rank), s, p, tile, (int)chunk,
                               splits);
         };
         if (p.rank <= 32)
@@ -1061,7 +1112,7 @@ cudaError_t launch_adapter_linear(const AdapterLinear& p, const DeviceInfo& dev,
     auto grow_many = [&](auto type, auto out) {
         using E = decltype(type);
         constexpr int OUT = decltype(out)::value;
-        using C = GrowCfg<OUT>;
+        using C = GrowCfg<E, OUT>;
         constexpr auto kernel = expand_many_kernel<E, OUT>;
         static ContextCache<int> cache;
         int done = 0;
@@ -1074,7 +1125,7 @@ cudaError_t launch_adapter_linear(const AdapterLinear& p, const DeviceInfo& dev,
         const int kb = (p.rank + 63) / 64;
         // boxes of a block, by the rounds of the blocks that fit at once, each as long as its boxes and a fixed
         // cost of about 5
-        const int64_t all = (p.N + C::W - 1) / C::W, slots = (int64_t)dev.sm_count * (kb == 1 ? 3 : 2);
+        const int64_t all = (p.N + C::W - 1) / C::W, slots = dev.sm_count * C::blocks(kb);
         int64_t boxes = 1;
         double best = INFINITY;
         for (int64_t n = 1; n <= 64 && n <= all; ++n) {

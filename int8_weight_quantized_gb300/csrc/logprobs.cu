@@ -13,6 +13,11 @@
 // together with what else is seldom.  Pieces of a row are joined by a second launch, always in the
 // same order.
 //
+// Measured (GB300): 4096 rows of 64000 bf16 logits, the best one 117 us, 4.5 TB/s, 66% of a copy's bandwidth
+// (normal logits: none 95, one 122, 5 149, 32 203); fp32, one 166 us, 6.3 TB/s, 93%; 48 rows of 131071, 21.2; one
+// row of 32000, 10.5 (two launches, and the host's part of them).  16-bit logits are bound by
+// instructions: widening, maximum, exponential and two sums of each.
+//
 // Sums.  Terms above 1/4 (of the largest's 1) and the others have sums of their own, so that a sharp
 // row's small rest, which is its entropy and the log probability of its likeliest token, does not lose
 // its bits to the 1: log s = log1p((a - 1) + b).  With terms above 1/4 other than the 1 the rest is
@@ -45,7 +50,9 @@ constexpr int BLOCKS = 32 / WARPS;       // of an SM
 // 4096 of fp32 167, 181)
 constexpr int DEPTH = 1;
 constexpr int64_t kLeastPiece = 2048;    // logits
-constexpr int64_t kPieces = 152 * 4;     // as many pieces as blocks fit at once
+// Pieces of all rows together, half as many as blocks fit at once: 48 rows of 131071 21.2 us, twice as many 24 (each
+// warms up its bar and its maximum, and is joined).
+constexpr int64_t kPieces = 152 * 4;
 constexpr uint32_t FULL = 0xffffffffu;
 constexpr float kNone = -160.0f;         // 2^-160 is 0 in fp32
 // Beside a maximum of at most kFew in size, logits below kFloor add nothing (scale is 1e-6 or more): raised

@@ -1,10 +1,11 @@
 """Low-rank adapters of many requests at once, against the 64-bit definition.
 
 Bound of row m with adapter i, all sums in fp32: each low-rank value h_r is a K-term sum, off by
-(K + 8) 2^-24 sum_k |x a|, and rounded once to the type of x (relative to the row's largest value where
-that type is fp16, so that nothing overflows: 2^-25 of it at least); the product with B adds
-(rank + 8) 2^-24 of its terms; scaling and residual two more roundings of fp32; then one rounding to
-the output type."""
+(K + 8) 2^-24 sum_k |x a|, and rounded to the type of x (relative to the row's largest value where
+that type is fp16, so that nothing overflows: 2^-25 of it at least), once, or where the output has 32 bits to a
+sum of two fp16 (2^-11 of what 2^-11 is left) or three bf16 (2^-24 in the same way); the product with B adds
+(rank + 8) 2^-24 of its terms for each of these; scaling and residual two more roundings of fp32; then one
+rounding to the output type."""
 import pytest
 import torch
 
@@ -33,6 +34,7 @@ def expected(x, a, b, index, scaling, residual, out_dtype):
     M, N, K, rank = x.shape[0], b.shape[1], x.shape[1], a.shape[1]
     y = torch.zeros((M, N), dtype=torch.float64, device=DEV)
     tol = torch.zeros_like(y)
+    parts = 1 if out_dtype != F32 else 2 if x.dtype == F16 else 3
     for i in range(a.shape[0]):
         rows = (index == i).nonzero()[:, 0]
         if not rows.numel():
@@ -40,11 +42,11 @@ def expected(x, a, b, index, scaling, residual, out_dtype):
         xs, aa, bb = x[rows].double(), a[i].double(), b[i].double()
         h = xs @ aa.t()
         off = (K + 8) * ref.U32 * (xs.abs() @ aa.abs().t())
-        off = off + (h.abs() + off) * ref.unit(x.dtype) + 2.0 ** -25 * (h.abs() + off).amax(1, keepdim=True)
+        off = off + (h.abs() + off) * ref.unit(x.dtype) ** parts + 2.0 ** -25 * (h.abs() + off).amax(1, keepdim=True)
         s = 1.0 if scaling is None else scaling[i].double()
         y[rows] = h @ bb.t() * s
         mag = (h.abs() + off) @ bb.abs().t() * s
-        tol[rows] = off @ bb.abs().t() * s + (rank + 8) * ref.U32 * mag
+        tol[rows] = off @ bb.abs().t() * s + parts * (rank + 8) * ref.U32 * mag
     if residual is not None:
         y = y + residual.double()
         tol = tol + 2 * ref.U32 * (residual.double().abs() + y.abs())
@@ -70,6 +72,19 @@ def test_against_the_definition(M, N, K, rank, adapters, order, dtype):
     assert (y[index < 0] == 0).all()
     assert ck.ck_device_error() == 0
     assert torch.equal(y, ck.ck_adapter_linear(x, a, b, index, scaling=scaling))
+
+
+@pytest.mark.parametrize("dtype", [BF, F16])
+@pytest.mark.parametrize("M,N,K,rank", [(1, 264, 512, 128), (40, 520, 272, 24), (256, 136, 512, 64), (300, 520, 512, 8), (2100, 6032, 512, 128)])
+def test_32_bit_outputs_keep_32_bit_sums(M, N, K, rank, dtype):
+    """In the 2-norm.  Each addition of 16 products onto a sum is off by 2^-23 of it at most (by cutting off), and
+    sums on the way are no larger than the last in the mean: K / 16 for h, rank / 16 and as many for each part of h
+    for y, scaling and h's parts with them.  (h in 16 bits: 2^-13 and more.)"""
+    x, a, b, index, scaling = make(M, N, K, rank, 3, dtype, 5, order="runs")
+    y = ck.ck_adapter_linear(x, a, b, index, scaling=scaling, out_dtype=F32)
+    want = expected(x, a, b, index, scaling, None, F32)[0]
+    off = float((y.double() - want).norm() / want.norm())
+    assert off <= (K / 16 + 3 * (rank / 16 + 1) + 8) * 2.0 ** -23, off
 
 
 @pytest.mark.parametrize("out_dtype", [BF, F16, F32])
