@@ -21,13 +21,13 @@
 //
 // Measured (GB300, heads of 128, 32 on 8, the whole call with the own keys and the join): 256 sequences behind 32768
 // tokens 155 us, 0.88 PFLOP/s, 47% of the measured rate, 1.7 to 2.0 us a key tile of 128 with two query tiles (the
-// softmax of 256 rows; attention.cu needs 1.6); the same in int8 rows 285, 4.7 to 5 a key tile (three warps widen
+// softmax of 256 rows; attention.cu needs 1.6); the same in int8 rows 303, 5 to 5.3 a key tile (three warps widen
 // the codes); 64 sequences behind 8192 tokens 46 us, of which this kernel is 20 to 23: 3.4 key tiles a block, 6.5 to
 // the first one's scores, 2 to leave the sums.
 //
 // Rounding to fewer bits: each weight once, to the queries' type; over int8 rows its product with the value
-// scale, to bf16, or to a sum of two of these (16 bits) where the queries are fp16.  Scores, sums, maxima
-// and O are fp32.
+// scale, to a sum of two bf16 (16 bits), which costs 2 to 6% there, where the products wait for widened codes,
+// and leaves the output's own rounding as the error.  Scores, sums, maxima and O are fp32.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -178,9 +178,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     using C = Cfg<DIM, INT8>;
     using T = typename E::T;
     // The second product's type.  int8: codes are exact in bf16, and a weight times its value's scale is in its
-    // range whatever the scale; with fp16 queries, whose 11 bits a bf16 weight would not have, as a sum of two.
+    // range whatever the scale; as a sum of two, for bits.
     using PV = typename std::conditional<INT8, Bf16, E>::type;
-    constexpr bool TWO = INT8 && std::is_same<E, Fp16>::value;
+    constexpr bool TWO = INT8;
     constexpr int UNITS = C::UNITS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
