@@ -18,7 +18,7 @@
 //     boxes in and out by TMA; once for every adapter that some of its rows have.
 //
 // Measured (GB300, bf16): 1 row of 4096 x 4096, rank 16, 7.6 to 8.5 us, two launches and their latencies; 48
-// rows of 24 mixed adapters, 28672 x 5376, rank 32, 23.4 us (54 MB of A, B, residual and y, 2.3 TB/s: two launches
+// rows of 24 mixed adapters, 28672 x 5376, rank 32, 22.0 us (54 MB of A, B, residual and y, 2.4 TB/s: two launches
 // of a few steps each, latency); 256 rows of 32 adapters, 4096 x 4096, 20; 8000 rows of 4096 x
 // 4096, rank 16 to 64, 50 to 58 us, 3.3 to 3.9 TB/s of x, residual and y (the first product 21 us, 3.1 TB/s, the
 // second 40 us, 3.3 TB/s); 4000 rows 43.  1000 rows of 32 adapters in any order 83 us: rows of one adapter are
@@ -565,83 +565,116 @@ __global__ void __launch_bounds__(THREADS, KT * PARTS<E, OUT> >= 8 ? 1 : 2)
     const int items = groups.count * steps;
     const int i0 = warp * items / WARPS, i1 = (warp + 1) * items / WARPS;
     const bool in_place = p.residual == p.y;
-    int step = i0 % steps;
-    for (int i = i0, group = i0 / steps; i < i1; ++group, step = 0) {
-        const int last = min(steps, step + (i1 - i));  // of this group's steps
-        i += last - step;
-        const int begin = groups.begin[group], count = groups.begin[group + 1] - begin;
-        const uint32_t adapter = groups.key[groups.row[begin]];
-        if (adapter == p.adapters && in_place)
-            continue;
-        const bool none = adapter >= p.adapters;
+    // a group's: its adapter, the lane's rows and its outputs of step 0
+    struct Group {
+        uint32_t adapter;
         bool there[2];
-        int64_t at[2];  // of the lane's outputs of step 0
-        float factor[2];
-        uint32_t h[P][KT][2][4];
+        int row[2];
+        int64_t at[2];
+    };
+    auto open = [&](int group) {
+        Group x;
+        const int begin = groups.begin[group], count = groups.begin[group + 1] - begin;
+        x.adapter = groups.key[groups.row[begin]];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            there[r] = g + 8 * r < count;
-            const int m = there[r] ? groups.row[begin + g + 8 * r] : 0;
-            at[r] = (first + m) * p.N + n_first + 8 * t;
-            factor[r] = adapter > p.adapters ? NAN : factors[m];
-#pragma unroll
-            for (int n = 0; n < P; ++n)
-#pragma unroll
-                for (int k = 0; k < KT; ++k) {
-                    uint4 w = make_uint4(0u, 0u, 0u, 0u);
-                    if (there[r] && !none && 32 * k + 8 * t < p.rank)
-                        w = *reinterpret_cast<const uint4*>(h_smem + (n * tile + m) * ld + (32 * k + 8 * t) * 2);
-                    h[n][k][0][r] = w.x, h[n][k][0][2 + r] = w.y, h[n][k][1][r] = w.z, h[n][k][1][2 + r] = w.w;
-                }
+            x.there[r] = g + 8 * r < count;
+            x.row[r] = x.there[r] ? groups.row[begin + g + 8 * r] : 0;
+            x.at[r] = (first + x.row[r]) * p.N + n_first + 8 * t;
         }
-        const T* b = static_cast<const T*>(p.b) + (none ? 0 : ((int64_t)adapter * p.N + n_first) * p.rank) + 8 * t;
-        Eight<OUT> next[2] = {};
-        auto fetch = [&](int s) {
+        return x;
+    };
+    // what comes from memory for an item, asked for while the one before it is worked on: outputs to add to and, at
+    // a rank up to 32, the columns of B (48 rows of 24 adapters, 28672 x 5376, B asked for when needed: 23.4 us, now 22.0)
+    constexpr bool B_AHEAD = KT == 1;
+    Eight<OUT> next[2] = {};
+    uint4 next_b[4] = {};
+    auto column = [&](const Group& x, int step, int j, int k) {
+        const int col = 32 * step + 8 * (g >> 1) + 2 * j + (g & 1);
+        const T* b = static_cast<const T*>(p.b) + ((int64_t)x.adapter * p.N + n_first) * p.rank + 8 * t;
+        return col < columns && 32 * k + 8 * t < p.rank ? __ldg(reinterpret_cast<const uint4*>(b + col * p.rank + 32 * k))
+                                                        : make_uint4(0u, 0u, 0u, 0u);
+    };
+    auto fetch = [&](const Group& x, int step) {
+        if (p.residual && !(x.adapter == p.adapters && in_place)) {
 #pragma unroll
             for (int r = 0; r < 2; ++r)
-                if (there[r] && 32 * s + 8 * t < columns)
-                    next[r] = Eight<OUT>::load(p.residual, at[r] + 32 * s);
-        };
-        if (p.residual)
-            fetch(step);
-        for (; step < last; ++step) {
-            Eight<OUT> y[2] = {next[0], next[1]};
-            if (p.residual && step + 1 < last)
-                fetch(step + 1);
-            float acc[4][4] = {};
-            if (!none) {
+                if (x.there[r] && 32 * step + 8 * t < columns)
+                    next[r] = Eight<OUT>::load(p.residual, x.at[r] + 32 * step);
+        }
+        if (B_AHEAD && x.adapter < p.adapters)
 #pragma unroll
-                for (int k = 0; k < KT; ++k) {
-                    uint4 bv[4];
+            for (int j = 0; j < 4; ++j)
+                next_b[j] = column(x, step, j, 0);
+    };
+    int group = i0 / steps, step = i0 - group * steps;
+    Group here{}, ahead{};
+    float factor[2] = {};
+    uint32_t h[P][KT][2][4] = {};
+    if (i0 < i1) {
+        ahead = open(group);
+        fetch(ahead, step);
+    }
+    bool opens = true;  // the item begins a group, or the warp's run
+    for (int i = i0; i < i1; ++i) {
+        if (opens) {
+            here = ahead;
+            const bool none = here.adapter >= p.adapters;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int col = 32 * step + 8 * (g >> 1) + 2 * j + (g & 1);
-                        bv[j] = col < columns && 32 * k + 8 * t < p.rank
-                                    ? __ldg(reinterpret_cast<const uint4*>(b + col * p.rank + 32 * k))
-                                    : make_uint4(0u, 0u, 0u, 0u);
+            for (int r = 0; r < 2; ++r) {
+                factor[r] = here.adapter > p.adapters ? NAN : factors[here.row[r]];
+#pragma unroll
+                for (int n = 0; n < P; ++n)
+#pragma unroll
+                    for (int k = 0; k < KT; ++k) {
+                        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                        if (here.there[r] && !none && 32 * k + 8 * t < p.rank)
+                            w = *reinterpret_cast<const uint4*>(h_smem + (n * tile + here.row[r]) * ld + (32 * k + 8 * t) * 2);
+                        h[n][k][0][r] = w.x, h[n][k][0][2 + r] = w.y, h[n][k][1][r] = w.z, h[n][k][1][2 + r] = w.w;
                     }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-#pragma unroll
-                        for (int n = P - 1; n >= 0; --n) {
-                            mma_16816<E>(acc[j], h[n][k][0], bv[j].x, bv[j].y);
-                            mma_16816<E>(acc[j], h[n][k][1], bv[j].z, bv[j].w);
-                        }
-                }
             }
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-                if (there[r] && 32 * step + 8 * t < columns) {
-                    if (adapter != p.adapters) {
-                        const float d[8] = {acc[0][2 * r] * factor[r], acc[0][2 * r + 1] * factor[r], acc[1][2 * r] * factor[r],
-                                            acc[1][2 * r + 1] * factor[r], acc[2][2 * r] * factor[r],
-                                            acc[2][2 * r + 1] * factor[r], acc[3][2 * r] * factor[r],
-                                            acc[3][2 * r + 1] * factor[r]};
-                        y[r].add(d);  // (an index out of range: 0 * NaN)
-                    }
-                    y[r].store(p.y, at[r] + 32 * step);
-                }
         }
+        const int at_step = step;
+        Eight<OUT> y[2] = {next[0], next[1]};
+        uint4 first_b[4] = {next_b[0], next_b[1], next_b[2], next_b[3]};
+        opens = ++step == steps;
+        if (opens)
+            step = 0, ++group;
+        if (i + 1 < i1) {
+            if (opens)
+                ahead = open(group);
+            fetch(ahead, step);
+        }
+        if (here.adapter == p.adapters && in_place)
+            continue;
+        float acc[4][4] = {};
+        if (here.adapter < p.adapters) {
+#pragma unroll
+            for (int k = 0; k < KT; ++k) {
+                uint4 bv[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    bv[j] = B_AHEAD ? first_b[j] : column(here, at_step, j, k);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int n = P - 1; n >= 0; --n) {
+                        mma_16816<E>(acc[j], h[n][k][0], bv[j].x, bv[j].y);
+                        mma_16816<E>(acc[j], h[n][k][1], bv[j].z, bv[j].w);
+                    }
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+            if (here.there[r] && 32 * at_step + 8 * t < columns) {
+                if (here.adapter != p.adapters) {
+                    const float d[8] = {acc[0][2 * r] * factor[r], acc[0][2 * r + 1] * factor[r], acc[1][2 * r] * factor[r],
+                                        acc[1][2 * r + 1] * factor[r], acc[2][2 * r] * factor[r], acc[2][2 * r + 1] * factor[r],
+                                        acc[3][2 * r] * factor[r], acc[3][2 * r + 1] * factor[r]};
+                    y[r].add(d);  // (an index out of range: 0 * NaN)
+                }
+                y[r].store(p.y, here.at[r] + 32 * at_step);
+            }
     }
     griddep_launch_dependents();
 }
@@ -1007,7 +1040,8 @@ int64_t most_groups(int64_t M, int64_t adapters)
 // an SM well, a part at least 4 boxes of 64.
 constexpr int64_t kSlots = 304;
 // The second product on the fifth-generation tensor core from this many outputs on.  (Rank 64, 4 adapters in
-// runs, K 4096: 4000 x 4096 43 us, 55 the other way; 1000 x 16384 54, 59; 2000 x 4096 48, 42; 4000 x 1024 35, 31.)
+// runs, K 4096: 4000 x 4096 43 us, 55 the other way; 1000 x 16384 54, 59; 2000 x 4096 48, 42; 4000 x 1024 35, 31; with
+// 32-bit outputs 8000 x 4096 96, 154; at rank 128 157, 176.)
 constexpr int64_t kManyOutputs = 12 << 20;
 int splits_of(int64_t M, int64_t K, int rank)
 {
