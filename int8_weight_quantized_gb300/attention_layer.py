@@ -5,10 +5,10 @@ by one.
 
 Prompt: INT8 QKV projection, norm and rotation into the paged cache, attention over the prompt,
 INT8 output projection with the residual.  Each further token: the same with 4-bit projections
-and attention over the cache.  A prompt's next chunk (`resume`): the same over the cached tokens read
-back, with low-rank adapters beside the QKV projection where there are some.  Random weights and activations; prints the time of each part and
-how far the last token's attention over the cache is from the same token's over the whole
-sequence at once.
+and attention over the cache.  A prompt's next chunk (`resume`): the same as for a prompt, over the
+cached tokens read back, with low-rank adapters beside the QKV projection where there are some.
+Random weights and activations; prints the time of each part and how far the last token's
+attention over the cache is from the same token's over the whole sequence at once.
 """
 import argparse
 

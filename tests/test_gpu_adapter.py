@@ -75,7 +75,8 @@ def test_against_the_definition(M, N, K, rank, adapters, order, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F16])
-@pytest.mark.parametrize("M,N,K,rank", [(1, 264, 512, 128), (40, 520, 272, 24), (256, 136, 512, 64), (300, 520, 512, 8), (2100, 6032, 512, 128)])
+@pytest.mark.parametrize("M,N,K,rank", [(1, 264, 512, 128), (40, 520, 272, 24), (256, 136, 512, 64), (256, 1032, 272, 128),
+                                        (300, 520, 512, 8), (300, 136, 272, 128), (2100, 6032, 512, 128), (2100, 6032, 272, 8)])
 def test_32_bit_outputs_keep_32_bit_sums(M, N, K, rank, dtype):
     """In the 2-norm.  Each addition of 16 products onto a sum is off by 2^-23 of it at most (by cutting off), and
     sums on the way are no larger than the last in the mean: K / 16 for h, rank / 16 and as many for each part of h
